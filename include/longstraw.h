@@ -21,6 +21,12 @@
  *                          held in host memory
  *   ls_mla_replay_bwd      its backward: dq, and the gradient of the response's own
  *                          latent rows (the prompt rows are stopgrad)
+ *   ls_qk_norm_rope_*      the stage between a layer's projections and its attention:
+ *                          query / key norms with rotary positions, forward, backward,
+ *                          and fused with the write into pages
+ *   ls_extend_pages        pages and slots of a group's growing responses
+ *   ls_decode_attn         the rollout's decode step: every member's newest tokens over
+ *                          the shared captured prompt and its own paged response
  *
  * Conventions shared by every call
  *   - Memory: every pointer argument is DEVICE memory on the current CUDA device unless
@@ -35,7 +41,9 @@
  *   - Alignment: every device pointer must be 16-byte aligned, except the per-token
  *     arrays of the loss and scoring calls (targets, logp_old, ref_logp, logp_out,
  *     lse_out, kl_out), which need 4 bytes, so that a member's slice of a token-major
- *     buffer can be passed whatever its token offset.
+ *     buffer can be passed whatever its token offset, and the index arrays of the
+ *     query / key stage and of the decode step (4 bytes, inv_freq 8, unless said
+ *     otherwise there).
  *   - Errors: arguments are checked on the host first; on failure the call returns
  *     LS_ERR_INVALID_ARG / LS_ERR_UNSUPPORTED / LS_ERR_WORKSPACE and launches
  *     nothing.  A failed launch returns LS_ERR_CUDA.  Conditions only the device can
@@ -406,6 +414,162 @@ ls_status ls_mla_replay_bwd(const ls_latent_cache* cache, const void* q, const v
                             const void* o, const float* lse, const void* d_o, int R, int H,
                             float softmax_scale, int num_splits, float* dq, float* dlat,
                             void* workspace, size_t workspace_bytes, ls_stream_t stream);
+
+/* ---------------------------------------------------------------- query / key stage
+ * What a layer does to its projections before attention: the RMS norm of every query and
+ * key head and the rotary positions, in one pass, at the layouts the projections have
+ * and the replay calls want.  The pages' model norms its query and key heads; they give
+ * no formula, so the common one is taken.  For a head x of 128 values at token t:
+ *   r = 1 / sqrt(mean_i x_i^2 + eps),   u_i = x_i r (w_offset + w_i),
+ *   y = u, with each pair (a, b) of its first rot_dim values turned by the pair's angle
+ *       p inv_freq[j]: (a cos - b sin, b cos + a sin), p = positions[pair_axis[j]][t].
+ * Everything is computed in fp32 and rounded to bf16 once; the angle is exact to 2^-32 of
+ * a turn at position 4,194,304 whatever its size (64-bit fixed-point turns).  A row takes
+ * only its own values: a non-finite one reaches no other row.
+ *
+ * ls_qkv_view: rows of 128 values at q + t q_stride[0] + h q_stride[1] elements (k and v
+ * alike), so that a packed projection's slices need no copy.  Strides are multiples of 8
+ * elements; rows of an output may not overlap.  An output may be the input itself (the
+ * same pointers and strides), otherwise the two may not overlap.
+ * ls_qk_norm: weights [128] of type w_dtype, or NULL for ones; w_offset is 1 for weights
+ * that are stored around zero.  A NULL ls_qk_norm* leaves the norm out (y = the turned x).
+ * ls_rotary: rot_dim a multiple of 16 up to 128 (0, or a NULL ls_rotary*: no rotation);
+ * inv_freq fp64 [rot_dim / 2] (finite), radians per position; pair_axis int32 [rot_dim / 2]
+ * gives the axis of each pair (time, height, width, ... of image and video tokens), NULL
+ * with one axis; pairs are (j, j + rot_dim / 2), or (2 j, 2 j + 1) when interleaved.
+ * positions int32 [axes][T], any sign.  An axis outside [0, axes) sets
+ * LS_ERR_DEVICE_CHECK and is taken as axis 0. */
+typedef struct {
+  void* q;
+  void* k;
+  void* v;
+  int64_t q_stride[2]; /* token, head (elements) */
+  int64_t k_stride[2];
+  int64_t v_stride[2];
+} ls_qkv_view;
+
+typedef struct {
+  const void* wq;
+  const void* wk;
+  ls_dtype w_dtype;
+  float w_offset;
+  float eps; /* > 0 */
+} ls_qk_norm;
+
+typedef struct {
+  const double* inv_freq;
+  const int32_t* pair_axis;
+  int32_t rot_dim;
+  int32_t axes; /* 1 to 8 */
+  int32_t interleaved;
+} ls_rotary;
+
+/* The K and V pages of one layer, as in ls_kv_cache:
+ * bf16 [num_pages][num_kv_heads][page_size][128]. */
+typedef struct {
+  void* k_pool;
+  void* v_pool;
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+} ls_page_pool;
+
+/* Forward: out.q, out.k from x.q, x.k; v (when x.v is given) is copied to out.v.  All bf16.
+ * T == 0 is a no-op. */
+ls_status ls_qk_norm_rope_fwd(const ls_qkv_view* x, int64_t T, int Hq, int Hkv,
+                              const ls_qk_norm* norm, const ls_rotary* rotary,
+                              const int32_t* positions, const ls_qkv_view* out,
+                              ls_stream_t stream);
+
+/* The forward with keys and values written into pages instead (a chunk of the prompt on
+ * its way into the cache, or the new tokens of a decode step): token t's key and value
+ * heads go to slot slots[t] = page * page_size + offset; out.q as above (out.k, out.v are
+ * not used).  slots[t] < 0 marks a padding token: nothing of it is written.  A slot
+ * outside the pool sets LS_ERR_DEVICE_CHECK and writes no key or value.  Two tokens may
+ * not share a slot (either may stay). */
+ls_status ls_qk_norm_rope_append(const ls_page_pool* pool, const ls_qkv_view* x, int64_t T,
+                                 int Hq, const ls_qk_norm* norm, const ls_rotary* rotary,
+                                 const int32_t* positions, const int32_t* slots,
+                                 const ls_qkv_view* q_out, ls_stream_t stream);
+
+/* Backward.  x: the forward's inputs (x.v is not read; without a norm nothing of x is).
+ * dy: gradients of its outputs, of type dy_dtype (the replay backward's dq, dk_resp and
+ * dv_resp are fp32); dx: bf16 gradients of its inputs, dx.v (when dy.v is given) the
+ * rounded dy.v.  dwq, dwk: fp32 [128] weight gradients, each or both NULL when not wanted;
+ * accumulate != 0 adds into them.  With g = dy turned back, xh = x r, h = g (w_offset + w):
+ *   dx = r (h - xh mean_i(h_i xh_i)),   dw_i = sum over tokens and heads of g_i xh_i.
+ * dw is summed in a fixed order (fp32 within a block, 64 bits across blocks).  dx may be x
+ * itself (same pointers and strides).  workspace: the query's bytes, needed for dwq or dwk
+ * only.  T == 0 leaves dx alone and gives (or adds) zero weight gradients. */
+ls_status ls_qk_norm_rope_bwd_workspace(int64_t T, size_t* bytes);
+ls_status ls_qk_norm_rope_bwd(const ls_qkv_view* x, int64_t T, int Hq, int Hkv,
+                              const ls_qk_norm* norm, const ls_rotary* rotary,
+                              const int32_t* positions, const ls_qkv_view* dy,
+                              ls_dtype dy_dtype, int accumulate, const ls_qkv_view* dx,
+                              float* dwq, float* dwk, void* workspace, size_t workspace_bytes,
+                              ls_stream_t stream);
+
+/* ---------------------------------------------------------------- growing responses
+ * ls_extend_pages: make room for new tokens of `members` sequences whose pages come from
+ * one pool, and say where they go; lengths and counts stay on the device, so a captured
+ * graph can run it step after step.  Member m holds lens[m] tokens in the pages of row m
+ * of block_table (int32 [members][max_blocks], logical -> physical page) and receives
+ * add[m] more.  The pages still missing, ceil((len + add) / page_size) -
+ * ceil(len / page_size), are taken in member order from free_list[*used], free_list[*used
+ * + 1], ... and entered into the table; other entries are left as they are.
+ *   slots      int32 [capacity]: page * page_size + offset of every new token, members one
+ *              after the other; -1 behind the last token
+ *   positions  int32 [axes][capacity] or NULL: pos0 + index within the response (the
+ *              same on every axis), 0 behind the last token
+ *   lens_out   int32 [members]: lens + add;  used_out int32 [1]: *used + pages taken.
+ *              Each may be the input itself (in place), otherwise they may not overlap.
+ * A member out of use has lens[m] < 0 and add[m] == 0 and is passed over.  All or nothing:
+ * when an add is negative, a member out of use grows, a row of the table is full, the
+ * free list ends or the tokens exceed capacity, LS_ERR_DEVICE_CHECK is recorded, every
+ * slot is -1, every position 0, and lens_out and used_out repeat the inputs.  A page id
+ * outside [0, num_pages) sets LS_ERR_DEVICE_CHECK and gives slot -1.  members <= 1024;
+ * page_size a power of two in [16, 4096]; slots and positions 16-byte aligned, the other
+ * arrays 4-byte. */
+ls_status ls_extend_pages(int32_t* block_table, int members, int max_blocks, int page_size,
+                          int num_pages, const int32_t* lens, const int32_t* add,
+                          const int32_t* free_list, int num_free, const int32_t* used, int pos0,
+                          int axes, int64_t capacity, int32_t* slots, int32_t* positions,
+                          int32_t* lens_out, int32_t* used_out, ls_stream_t stream);
+
+/* The responses of a group in their own pages: member m's key j lies in page
+ * block_table[m][j / page_size] of `pool`; lens int32 [members] on the device, negative
+ * for a member out of use.  Entries behind a member's length are not read. */
+typedef struct {
+  ls_page_pool pool;
+  const int32_t* block_table; /* int32 [members][max_blocks] */
+  const int32_t* lens;
+  int32_t members;
+  int32_t max_blocks;
+} ls_resp_cache;
+
+/* ls_decode_attn: attention of a decode step: the n newest tokens of every member (their
+ * keys and values already in its pages, as the last n of its lens[m]) over the shared
+ * captured prompt and the member's own response:
+ *   s_j = softmax_scale <q_{m,i,h}, k_j>, j over all P prompt positions and the member's
+ *         response keys j <= lens[m] - n + i (none when that is negative)
+ *   lse = log sum_j exp(s_j) (natural log),  o = sum_j exp(s_j - lse) v_j
+ * Each prompt K/V tile is read once for all members.  q, o: bf16 [members][n][Hq][128];
+ * lse: fp32 [members][n][Hq].  A token that sees no key at all (P == 0 and an empty
+ * response) gets o = 0 and lse = -inf; the rows of a member out of use are not written.
+ * A member's result takes its own queries and keys and the prompt only.  Values must be
+ * finite where a row may not look (a later new token's value times zero weight); what
+ * lies behind a sequence's end in its last page may be anything.  A length past
+ * max_blocks * page_size is cut there and sets LS_ERR_DEVICE_CHECK, as does a page id
+ * outside its pool (its keys and values count as zeros).  n * Hq / num_kv_heads <= 128,
+ * members <= 1024, and at most one row tile (floor(128 / g) tokens, g = Hq / num_kv_heads)
+ * per SM, else LS_ERR_UNSUPPORTED.  Two launches; the lengths may change between replays
+ * of a captured graph, the pointers and P may not.  members == 0 is a no-op. */
+ls_status ls_decode_attn_workspace(const ls_kv_cache* cache, const ls_resp_cache* resp, int n,
+                                   int Hq, size_t* bytes);
+ls_status ls_decode_attn(const ls_kv_cache* cache, const ls_resp_cache* resp, const void* q,
+                         int n, int Hq, float softmax_scale, void* o, float* lse,
+                         void* workspace, size_t workspace_bytes, ls_stream_t stream);
 
 /* ---------------------------------------------------------------- checks
  * ls_validate_page_table: enqueue a check that every entry of the page table covering

@@ -31,6 +31,8 @@ EXPORTED = (
     "ls_replay_attn_bwd_ragged_workspace", "ls_replay_attn_bwd_ragged",
     "ls_capture_latent", "ls_mla_replay_fwd_workspace", "ls_mla_replay_fwd",
     "ls_mla_replay_bwd_workspace", "ls_mla_replay_bwd",
+    "ls_qk_norm_rope_fwd", "ls_qk_norm_rope_append", "ls_qk_norm_rope_bwd_workspace",
+    "ls_qk_norm_rope_bwd", "ls_extend_pages", "ls_decode_attn_workspace", "ls_decode_attn",
 )
 
 
@@ -46,6 +48,41 @@ class ls_latent_cache(C.Structure):
     _fields_ = [
         ("pool", C.c_void_p), ("page_table", C.c_void_p), ("num_pages", C.c_int32),
         ("num_logical_pages", C.c_int32), ("page_size", C.c_int32), ("num_tokens", C.c_int64),
+    ]
+
+
+class ls_qkv_view(C.Structure):
+    _fields_ = [
+        ("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("q_stride", C.c_int64 * 2),
+        ("k_stride", C.c_int64 * 2), ("v_stride", C.c_int64 * 2),
+    ]
+
+
+class ls_qk_norm(C.Structure):
+    _fields_ = [
+        ("wq", C.c_void_p), ("wk", C.c_void_p), ("w_dtype", C.c_int32), ("w_offset", C.c_float),
+        ("eps", C.c_float),
+    ]
+
+
+class ls_rotary(C.Structure):
+    _fields_ = [
+        ("inv_freq", C.c_void_p), ("pair_axis", C.c_void_p), ("rot_dim", C.c_int32),
+        ("axes", C.c_int32), ("interleaved", C.c_int32),
+    ]
+
+
+class ls_page_pool(C.Structure):
+    _fields_ = [
+        ("k_pool", C.c_void_p), ("v_pool", C.c_void_p), ("num_pages", C.c_int32),
+        ("page_size", C.c_int32), ("num_kv_heads", C.c_int32), ("head_dim", C.c_int32),
+    ]
+
+
+class ls_resp_cache(C.Structure):
+    _fields_ = [
+        ("pool", ls_page_pool), ("block_table", C.c_void_p), ("lens", C.c_void_p),
+        ("members", C.c_int32), ("max_blocks", C.c_int32),
     ]
 
 
@@ -108,6 +145,20 @@ def lib() -> C.CDLL:
             "ls_gdn_replay_bwd": [P, P, P, P, P, P, P, i32, i32, f32, i32, P, P, P, P, P, P, sz,
                                   P],
         }
+        view, norm, rot = C.POINTER(ls_qkv_view), C.POINTER(ls_qk_norm), C.POINTER(ls_rotary)
+        rcache = C.POINTER(ls_resp_cache)
+        sig.update({
+            "ls_qk_norm_rope_fwd": [view, i64, i32, i32, norm, rot, P, view, P],
+            "ls_qk_norm_rope_append": [C.POINTER(ls_page_pool), view, i64, i32, norm, rot, P, P,
+                                       view, P],
+            "ls_qk_norm_rope_bwd_workspace": [i64, szp],
+            "ls_qk_norm_rope_bwd": [view, i64, i32, i32, norm, rot, P, view, i32, i32, view, P, P,
+                                    P, sz, P],
+            "ls_extend_pages": [P, i32, i32, i32, i32, P, P, P, i32, P, i32, i32, i64, P, P, P, P,
+                                P],
+            "ls_decode_attn_workspace": [cache, rcache, i32, i32, szp],
+            "ls_decode_attn": [cache, rcache, P, i32, i32, f32, P, P, P, sz, P],
+        })
         for name, args in sig.items():
             f = getattr(l, name)
             f.argtypes = args
@@ -331,3 +382,54 @@ def ls_replay_attn_bwd_ragged(cache: ls_kv_cache, q: int, k_resp: int, v_resp: i
         lib().ls_replay_attn_bwd_ragged(C.byref(cache), q, k_resp, v_resp, o, lse, d_o, arr, n,
                                         Hq, softmax_scale, num_splits, accumulate, dq, dk_resp,
                                         dv_resp, workspace, workspace_bytes, stream))
+
+
+def ls_qk_norm_rope_fwd(x: ls_qkv_view, T: int, Hq: int, Hkv: int, norm: ls_qk_norm | None,
+                        rotary: ls_rotary | None, positions: int | None, out: ls_qkv_view,
+                        stream: int = 0) -> None:
+    _ok("ls_qk_norm_rope_fwd",
+        lib().ls_qk_norm_rope_fwd(x, T, Hq, Hkv, norm, rotary, positions, out, stream))
+
+
+def ls_qk_norm_rope_append(pool: ls_page_pool, x: ls_qkv_view, T: int, Hq: int,
+                           norm: ls_qk_norm | None, rotary: ls_rotary | None,
+                           positions: int | None, slots: int, q_out: ls_qkv_view,
+                           stream: int = 0) -> None:
+    _ok("ls_qk_norm_rope_append",
+        lib().ls_qk_norm_rope_append(pool, x, T, Hq, norm, rotary, positions, slots, q_out, stream))
+
+
+def ls_qk_norm_rope_bwd_workspace(T: int) -> int:
+    return _size("ls_qk_norm_rope_bwd_workspace", T)
+
+
+def ls_qk_norm_rope_bwd(x: ls_qkv_view | None, T: int, Hq: int, Hkv: int, norm: ls_qk_norm | None,
+                        rotary: ls_rotary | None, positions: int | None, dy: ls_qkv_view,
+                        dy_dtype: int, accumulate: int, dx: ls_qkv_view, dwq: int | None,
+                        dwk: int | None, workspace: int | None, workspace_bytes: int,
+                        stream: int = 0) -> None:
+    _ok("ls_qk_norm_rope_bwd",
+        lib().ls_qk_norm_rope_bwd(x, T, Hq, Hkv, norm, rotary, positions, dy, dy_dtype, accumulate,
+                                  dx, dwq, dwk, workspace, workspace_bytes, stream))
+
+
+def ls_extend_pages(block_table: int, members: int, max_blocks: int, page_size: int, num_pages: int,
+                    lens: int, add: int, free_list: int, num_free: int, used: int, pos0: int,
+                    axes: int, capacity: int, slots: int, positions: int | None, lens_out: int,
+                    used_out: int, stream: int = 0) -> None:
+    _ok("ls_extend_pages",
+        lib().ls_extend_pages(block_table, members, max_blocks, page_size, num_pages, lens, add,
+                              free_list, num_free, used, pos0, axes, capacity, slots, positions,
+                              lens_out, used_out, stream))
+
+
+def ls_decode_attn_workspace(cache: ls_kv_cache, resp: ls_resp_cache, n: int, Hq: int) -> int:
+    return _size("ls_decode_attn_workspace", C.byref(cache), C.byref(resp), n, Hq)
+
+
+def ls_decode_attn(cache: ls_kv_cache, resp: ls_resp_cache, q: int, n: int, Hq: int,
+                   softmax_scale: float, o: int, lse: int, workspace: int, workspace_bytes: int,
+                   stream: int = 0) -> None:
+    _ok("ls_decode_attn",
+        lib().ls_decode_attn(C.byref(cache), C.byref(resp), q, n, Hq, softmax_scale, o, lse,
+                             workspace, workspace_bytes, stream))

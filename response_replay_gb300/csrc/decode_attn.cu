@@ -1,0 +1,788 @@
+// decode_attn.cu -- decode attention of a group whose members share one captured prompt.
+//
+// Each member has n new tokens (one, or a few) whose keys and values are the last n of
+// its response pages.  For token i of member m with len keys in its pages, query head h,
+// KV head h / g:
+//   s_j = scale <q, k_j> over the P prompt positions and the member's response keys
+//         j <= len - n + i;   lse = log sum_j exp(s_j);   o = sum_j exp(s_j - lse) v_j
+//
+// Work.  A row tile is up to 128 rows (token, head of the group) that share a KV head:
+// all members' tokens against the prompt's keys (each prompt K/V tile serves every
+// member), one member's tokens against its own keys.  The prompt's tiles (128 keys, KV
+// head by KV head) followed by the responses' tiles (member by member, KV head by KV
+// head) form one sequence that is cut evenly over the grid, so a CTA holds a few
+// segments, each a run of tiles of one row tile and one key source; a segment leaves a
+// partial (o, lse) and decode_combine merges a row's partials by log-sum-exp.  With more
+// rows than one tile (rts row tiles) the prompt part is cut over `cols` columns of rts
+// CTAs: a column's CTAs walk the same prompt tiles at the same time, one row tile each, so
+// a tile is read from HBM once and from L2 after that.  The response lengths stay on the
+// device (a captured graph follows them): every CTA sums them when it starts.
+//
+// CTA (one per SM, 12 warps):
+//   warp 0      TMA producer: Q of a segment (two buffers), then its K and V tiles page by
+//               page into a 5-stage ring.
+//   warps 1, 2  MMA issuers: the segment's even and odd tiles.  S_t = Q K^T into tensor
+//               memory, O_t += P_t V with P_t read from tensor memory; the two tile
+//               sequences are independent, so one's MMAs run under the other's softmax.
+//   warp 3      clears the V rows behind a sequence's end (stale page contents, even NaN,
+//               would survive a zero weight) before the tile is handed over.
+//   warps 4-7   softmax of the even tiles, warps 8-11 of the odd ones, one row a thread;
+//               warps whose rows are all padding only keep the barriers going.
+// Tensor memory (512 columns): S_0 [0,128) S_1 [128,256) O_0 [256,384) O_1 [384,512).
+#include <math.h>
+
+#include "ls_device.cuh"
+#include "ls_internal.h"
+#include "ls_tmap.h"
+#include "ls_umma.cuh"
+
+namespace {
+
+using namespace umma;
+
+constexpr int kD = 128;
+constexpr int kTile = 128;
+constexpr int kStages = 5;
+constexpr int kThreads = 384;
+// 168 registers a thread at launch (64,512); warpgroup 0 drops to 96, the two softmax
+// warpgroups rise to 200: 128 x 96 + 256 x 200 = 63,488.
+constexpr int kRegsLaunch = 168, kRegsControl = 96, kRegsSoftmax = 200;
+static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
+constexpr uint32_t kTileBytes = kTile * kD * 2;
+constexpr uint32_t kHalfBytes = kTileBytes / 2;
+constexpr uint32_t kOffQ = 0;  // two buffers
+constexpr uint32_t kOffRing = 2 * kTileBytes;
+constexpr uint32_t kOffBar = kOffRing + kStages * kTileBytes;
+constexpr uint32_t kSmemBytes = kOffBar + 512 + 1024;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleLog2 = 8.0f;
+
+enum {
+  B_KV_FULL = 0,
+  B_KV_EMPTY = B_KV_FULL + kStages,
+  B_AUX = B_KV_EMPTY + kStages,  // a ragged V tile has landed, its tail not yet cleared
+  B_Q_FULL = B_AUX + kStages,    // 2
+  B_Q_EMPTY = B_Q_FULL + 2,      // 2
+  B_S_FULL = B_Q_EMPTY + 2,      // 2
+  B_P_FULL = B_S_FULL + 2,       // 4: tile sequence t, key half hf at 2 t + hf
+  B_O_DONE = B_P_FULL + 4,       // 2
+  B_DONE = B_O_DONE + 2,         // 2
+  B_COUNT = B_DONE + 2
+};
+constexpr uint32_t kOffVars = kOffBar + B_COUNT * 8;
+static_assert(B_COUNT * 8 + 32 <= 512, "barrier area");
+
+struct TmapSet {
+  CUtensorMap q, kp, vp, kr, vr;
+};
+
+__device__ __forceinline__ uint32_t bar_addr(uint32_t base, int i) { return base + kOffBar + 8 * i; }
+
+// A member's response keys: none for a member out of use (negative length); a length
+// past its row of the block table is cut (and reported by the main kernel).
+__device__ __forceinline__ int32_t clamp_len(const LsDecodeArgs& a, int32_t len) {
+  const long long room = (long long)a.max_blocks << a.r_ps_log2;
+  if (len < 0) return 0;
+  return len < room ? len : (int32_t)room;
+}
+__device__ __forceinline__ int32_t tiles_of(int32_t len) {
+  return (int32_t)(((long long)len + kTile - 1) / kTile);
+}
+
+// The cut of the tile sequence.  Weights: a prompt tile occupies the rts CTAs of a column,
+// a response tile one of them, so the sequence weighs rts tp + tr in CTA tiles.
+struct Cut {
+  int32_t tp, rts, cols;
+  long long w;
+  __device__ __forceinline__ Cut(const LsDecodeArgs& a, int32_t resp_tiles)
+      : tp(a.nt * a.hkv), rts(a.rts), cols(a.cols), w((long long)rts * tp + resp_tiles) {}
+  __device__ __forceinline__ void prompt(int32_t col, int32_t* b, int32_t* e) const {
+    *b = bound(col);
+    *e = bound(col + 1);
+  }
+  __device__ __forceinline__ void resp(int32_t col, int32_t rt, int32_t* b, int32_t* e) const {
+    const int32_t lo = rbound(col);
+    const long long n = rbound(col + 1) - lo;
+    *b = lo + (int32_t)(n * rt / rts);
+    *e = lo + (int32_t)(n * (rt + 1) / rts);
+  }
+
+ private:
+  __device__ __forceinline__ int32_t bound(int32_t col) const {
+    const long long p = (w * col / cols + rts - 1) / rts;
+    return p < tp ? (int32_t)p : tp;
+  }
+  __device__ __forceinline__ int32_t rbound(int32_t col) const {
+    const long long r = w * col / cols - (long long)rts * tp;
+    return r > 0 ? (int32_t)r : 0;
+  }
+};
+
+// One segment: `count` tiles from key `key0` of one source; rows of one row tile.
+struct Seg {
+  bool resp;
+  int32_t kvh, m;       // KV head; member (responses)
+  int32_t item;         // KV head (prompt) or m * hkv + kvh
+  int32_t key0, count;
+  int32_t len;          // keys of the source
+};
+
+struct Walk {
+  const LsDecodeArgs& a;
+  int32_t p, p_end, r, r_end;
+  int32_t m, off;       // member and tile within its hkv x nt tiles
+  __device__ __forceinline__ Walk(const LsDecodeArgs& a_, const volatile int32_t* start, int32_t p0,
+                                  int32_t p1, int32_t r0, int32_t r1)
+      : a(a_), p(p0), p_end(p1), r(r0), r_end(r1), m(start[0]), off(start[1]) {}
+  __device__ __forceinline__ bool next(Seg* s) {
+    if (p < p_end) {
+      const int32_t h = p / a.nt, first = p - h * a.nt;
+      s->resp = false;
+      s->kvh = s->item = h;
+      s->m = 0;
+      s->len = (int32_t)a.P;
+      s->key0 = first * kTile;
+      s->count = min(p_end - p, a.nt - first);
+      p += s->count;
+      return true;
+    }
+    if (r >= r_end) return false;
+    int32_t len = 0, nt = 0;
+    for (; m < a.M; ++m, off = 0) {
+      len = clamp_len(a, __ldg(a.lens + m));
+      nt = tiles_of(len);
+      if (off < nt * a.hkv) break;
+    }
+    if (m >= a.M) return false;  // only when lengths changed under the kernel
+    const int32_t h = off / nt, first = off - h * nt;
+    s->resp = true;
+    s->kvh = h;
+    s->m = m;
+    s->item = m * a.hkv + h;
+    s->len = len;
+    s->key0 = first * kTile;
+    s->count = min(r_end - r, nt - first);
+    r += s->count;
+    off += s->count;
+    return true;
+  }
+};
+
+// Rows of a partial: prompt partials first, then the responses'.  (item + CTA in walk
+// order) numbers a CTA's segments uniquely: from one segment to the next of the whole
+// sequence the item, the CTA or both grow.
+__device__ __forceinline__ int64_t prompt_row0(const LsDecodeArgs& a, int32_t h, int32_t col,
+                                               int32_t rt, int t) {
+  return ((((int64_t)h + col) * a.rts + rt) * 2 + t) * kTile;
+}
+__device__ __forceinline__ int64_t resp_row0(const LsDecodeArgs& a, int64_t prompt_rows,
+                                             int32_t item, int32_t cta, int t) {
+  return prompt_rows + (((int64_t)item + cta) * 2 + t) * (a.n * a.g);
+}
+__host__ __device__ __forceinline__ int64_t prompt_rows_of(const LsDecodeArgs& a) {
+  return a.nt > 0 ? ((int64_t)a.hkv + a.cols) * a.rts * 2 * kTile : 0;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsDecodeArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + kOffVars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffVars + 4);
+  volatile int32_t* start = reinterpret_cast<volatile int32_t*>(smem + kOffVars + 8);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int32_t cta = blockIdx.x, col = cta / a.rts, rt = cta - col * a.rts;
+
+  // ---- response tiles before each member, summed by the whole CTA (scratch: the ring,
+  // which no copy has touched yet)
+  int32_t p0, p1, r0, r1;
+  {
+    int32_t* wsum = reinterpret_cast<int32_t*>(smem + kOffRing);
+    const int per = (a.M + kThreads - 1) / kThreads;
+    int32_t mine = 0;
+    for (int i = 0; i < per; ++i) {
+      const int m = tid * per + i;
+      if (m < a.M) {
+        const int32_t len = __ldg(a.lens + m);
+        const int32_t cl = clamp_len(a, len);
+        if (len > cl && cta == 0) ls_report(a.err, LS_DEVERR_CHECK);
+        mine += tiles_of(cl);
+      }
+    }
+    int32_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 31) wsum[warp] = sum;
+    if (tid == 0) start[0] = start[1] = 0;
+    __syncthreads();
+    int32_t before = 0, total = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+      const int32_t v = wsum[i];
+      if (i < warp) before += v;
+      total += v;
+    }
+    const Cut cut(a, total * a.hkv);
+    cut.prompt(col, &p0, &p1);
+    cut.resp(col, rt, &r0, &r1);
+    // the member whose tiles hold r0
+    int32_t pre = before + sum - mine;
+    if (r0 < r1 && pre * a.hkv <= r0 && r0 < (pre + mine) * a.hkv) {
+      for (int i = 0; i < per; ++i) {
+        const int m = tid * per + i;
+        const int32_t nt = tiles_of(clamp_len(a, __ldg(a.lens + m)));
+        if (r0 < (pre + nt) * a.hkv) {
+          start[0] = m;
+          start[1] = r0 - pre * a.hkv;
+          break;
+        }
+        pre += nt;
+      }
+    }
+    if (p0 >= p1 && r0 >= r1) return;  // uniform: no tiles for this CTA
+  }
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar_addr(sbase, B_KV_FULL + i), 1);
+      mbar_init(bar_addr(sbase, B_KV_EMPTY + i), 1);
+      mbar_init(bar_addr(sbase, B_AUX + i), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar_addr(sbase, B_Q_FULL + t), 1);
+      mbar_init(bar_addr(sbase, B_Q_EMPTY + t), 2);
+      mbar_init(bar_addr(sbase, B_S_FULL + t), 1);
+      mbar_init(bar_addr(sbase, B_P_FULL + 2 * t), kTile);
+      mbar_init(bar_addr(sbase, B_P_FULL + 2 * t + 1), kTile);
+      mbar_init(bar_addr(sbase, B_O_DONE + t), 1);
+      mbar_init(bar_addr(sbase, B_DONE + t), 1);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), 512);
+    tmem_relinquish();
+  }
+  {
+    // a Q box holds tpt tokens x g heads; the tile's other rows are never loaded
+    const int used = a.tpt * a.g;
+    if (used < kTile) {
+      const int per_half = (kTile - used) * 8;
+      for (int i = tid; i < 4 * per_half; i += kThreads) {
+        const int part = i / per_half, c = i % per_half;
+        *reinterpret_cast<uint4*>(smem + kOffQ + part * kHalfBytes + used * 128 + c * 16) =
+            make_uint4(0, 0, 0, 0);
+      }
+    }
+    fence_proxy_async_smem();  // also the scratch above, before TMA writes the ring
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto fail = [&](void) {
+    ls_report(a.err, LS_DEVERR_TIMEOUT);
+    *abort_flag = 1;
+  };
+  Walk walk(a, start, p0, p1, r0, r1);
+  Seg s;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    if (warp == 0) {
+      // ---------------------------------------------------------- TMA producer
+      if (lane == 0) {
+        tma_prefetch_desc(&tm.q);
+        tma_prefetch_desc(&tm.kp);
+        tma_prefetch_desc(&tm.vp);
+        tma_prefetch_desc(&tm.kr);
+        tma_prefetch_desc(&tm.vr);
+        uint32_t seg = 0, fills = 0;
+        RingPos<kStages> ring;
+        bool ok = true;
+        while (ok && walk.next(&s)) {
+          const int b = seg & 1;
+          if (seg >= 2 && !mbar_wait(bar_addr(sbase, B_Q_EMPTY + b), ((seg >> 1) - 1) & 1)) {
+            fail();
+            break;
+          }
+          const uint32_t qb = bar_addr(sbase, B_Q_FULL + b);
+          mbar_expect_tx(qb, 2u * 128u * (uint32_t)(a.g * a.tpt));
+          const int32_t tok0 = s.resp ? s.m * a.n : rt * a.tpt;
+          for (int hf = 0; hf < 2; ++hf)
+            tma_load_3d(sbase + kOffQ + b * kTileBytes + hf * kHalfBytes, &tm.q, hf * 64,
+                        s.kvh * a.g, tok0, qb);
+          ++seg;
+          const int ps_log2 = s.resp ? a.r_ps_log2 : a.ps_log2;
+          const int32_t ps = 1 << ps_log2;
+          const int32_t box_rows = ps < kTile ? ps : kTile;
+          const int32_t pages = s.resp ? a.r_num_pages : a.num_pages;
+          const int32_t pool_rows = pages * a.hkv * ps;
+          const int32_t* table = s.resp ? a.blocks + (int64_t)s.m * a.max_blocks : a.page_table;
+          for (int32_t j = 0; ok && j < s.count; ++j) {
+            const int32_t key0 = s.key0 + j * kTile, left = s.len - key0;  // keys from key0 on
+            for (int kv = 0; kv < 2 && ok; ++kv) {
+              if (!mbar_wait(bar_addr(sbase, B_KV_EMPTY + ring.stage), ring.phase ^ 1)) {
+                fail();
+                ok = false;
+                break;
+              }
+              if (*abort_flag) {
+                ok = false;
+                break;
+              }
+              const bool ragged_v = kv == 1 && left < kTile;
+              const uint32_t fb = bar_addr(sbase, (ragged_v ? B_AUX : B_KV_FULL) + ring.stage);
+              const uint32_t dst = sbase + kOffRing + ring.stage * kTileBytes;
+              const void* map = s.resp ? (kv ? (const void*)&tm.vr : (const void*)&tm.kr)
+                                       : (kv ? (const void*)&tm.vp : (const void*)&tm.kp);
+              mbar_expect_tx(fb, kTileBytes);
+              for (int x = 0; x < kTile / box_rows; ++x) {
+                int32_t y = pool_rows;  // out of bounds: zero fill
+                if (x * box_rows < left) {
+                  const int32_t pos = key0 + x * box_rows;
+                  const int32_t phys = __ldg(table + (pos >> ps_log2));
+                  if ((uint32_t)phys < (uint32_t)pages)
+                    y = (phys * a.hkv + s.kvh) * ps + (pos & (ps - 1));
+                  else
+                    ls_report(a.err, LS_DEVERR_CHECK);
+                }
+                for (int hf = 0; hf < 2; ++hf)
+                  tma_load_2d(dst + hf * kHalfBytes + x * box_rows * 128, map, hf * 64, y, fb);
+              }
+              ring.advance();
+              ++fills;
+            }
+          }
+        }
+        // Do not leave while loads into this CTA's shared memory may still be in flight.
+        for (uint32_t i = fills > kStages ? fills - kStages : 0; i < fills; ++i)
+          mbar_wait(bar_addr(sbase, B_KV_FULL + i % kStages), (i / kStages) & 1);
+        for (uint32_t i = seg > 2 ? seg - 2 : 0; i < seg; ++i)
+          mbar_wait(bar_addr(sbase, B_Q_FULL + (i & 1)), (i >> 1) & 1);
+      }
+    } else if (warp == 3) {
+      // ---------------------------------------------------------- V tails
+      uint32_t ring = 1, aux_phase = 0;  // ring slot of the tile's V; a phase bit per stage
+      bool ok = true;
+      while (ok && walk.next(&s)) {
+        for (int32_t j = 0; ok && j < s.count; ++j, ring += 2) {
+          const int32_t left = s.len - (s.key0 + j * kTile);
+          if (left >= kTile) continue;
+          const uint32_t st = ring % kStages;
+          ok = mbar_wait(bar_addr(sbase, B_AUX + st), (aux_phase >> st) & 1);
+          if (!ok) {
+            fail();
+            break;
+          }
+          aux_phase ^= 1u << st;
+          uint8_t* vb = smem + kOffRing + st * kTileBytes;
+          for (int i = left * 8 + lane; i < kTile * 8; i += 32) {
+            *reinterpret_cast<uint4*>(vb + i * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(vb + kHalfBytes + i * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_addr(sbase, B_KV_FULL + st));
+        }
+      }
+    } else {
+      // ---------------------------------------------------------- MMA issuers
+      if (lane == 0) {
+        const int t = warp - 1;
+        const uint32_t idS = idesc_bf16_f32(kTile, kTile, false);
+        const uint32_t idPV = idesc_bf16_f32(kTile, kD, true);
+        const uint32_t dk_base = sdesc_lo(sbase + kOffRing, 16);
+        const uint32_t dv_base = sdesc_lo(sbase + kOffRing, kHalfBytes);
+        const uint32_t d_s = tmem + t * kTile, d_o = tmem + 256 + t * kTile;
+        auto issue_s = [&](uint32_t dq, uint32_t kstage) {
+          const uint32_t b0 = dk_base + ((kstage * kTileBytes) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
+            mma_ss_lo(d_s, dq + off, b0 + off, idS, kk > 0);
+          }
+        };
+        auto issue_pv_half = [&](uint32_t vstage, int hf, bool accumulate) {
+          const uint32_t b0 = dv_base + ((vstage * kTileBytes) >> 4);
+#pragma unroll
+          for (int k4 = 0; k4 < 4; ++k4) {
+            const int kk = 4 * hf + k4;
+            mma_ts_lo(d_o, d_s + kk * 8, b0 + ((kk * 2048) >> 4), idPV,
+                      (accumulate || kk > 0) ? 1u : 0u);
+          }
+        };
+        uint32_t seg = 0, base = 0, kc = 0;  // segments, ring slots before the segment, own tiles
+        bool ok = true;
+        while (ok && walk.next(&s)) {
+          const int b = seg & 1;
+          if (!mbar_wait(bar_addr(sbase, B_Q_FULL + b), (seg >> 1) & 1)) { fail(); break; }
+          ++seg;
+          if (s.count <= t) {  // no tile of this segment is this issuer's
+            mbar_arrive(bar_addr(sbase, B_Q_EMPTY + b));
+            base += 2 * s.count;
+            continue;
+          }
+          const uint32_t dq = sdesc_lo(sbase + kOffQ + b * kTileBytes, 16);
+          // S of own tile j: its K is ring slot base + 2 j
+          auto s_tile = [&](int32_t j) {
+            const uint32_t slot = base + 2 * j, st = slot % kStages;
+            if (!mbar_wait(bar_addr(sbase, B_KV_FULL + st), (slot / kStages) & 1)) return false;
+            tc_fence_after();
+            issue_s(dq, st);
+            mma_commit(bar_addr(sbase, B_S_FULL + t));
+            mma_commit(bar_addr(sbase, B_KV_EMPTY + st));
+            if (j + 2 >= s.count) mma_commit(bar_addr(sbase, B_Q_EMPTY + b));
+            return true;
+          };
+          ok = s_tile(t);
+          for (int32_t j = t; ok && j < s.count; j += 2) {
+            const uint32_t slot = base + 2 * j + 1, st = slot % kStages;
+            ok = mbar_wait(bar_addr(sbase, B_KV_FULL + st), (slot / kStages) & 1) &&
+                 mbar_wait(bar_addr(sbase, B_P_FULL + 2 * t), kc & 1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv_half(st, 0, j > t);
+            ok = mbar_wait(bar_addr(sbase, B_P_FULL + 2 * t + 1), kc & 1);
+            if (!ok) break;
+            ++kc;
+            tc_fence_after();
+            issue_pv_half(st, 1, true);
+            if (j + 2 >= s.count) mma_commit(bar_addr(sbase, B_O_DONE + t));
+            mma_commit(bar_addr(sbase, B_KV_EMPTY + st));
+            // after P V in issue order: the next S overwrites P
+            if (j + 2 < s.count) ok = s_tile(j + 2);
+            if (*abort_flag) ok = false;
+          }
+          if (!ok) fail();
+          base += 2 * s.count;
+        }
+        // every MMA this thread issued has finished before tensor memory is released
+        mma_commit(bar_addr(sbase, B_DONE + t));
+        mbar_wait(bar_addr(sbase, B_DONE + t), 0);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // ------------------------------------------------------------ softmax warpgroups
+    const int t = (warp - 4) >> 2;
+    const int quad = warp & 3;
+    const int row = quad * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t s_col = tmem + lane_off + t * kTile;
+    const uint32_t o_col = tmem + lane_off + 256 + t * kTile;
+    const float c = a.scale_log2;
+    const int64_t prompt_rows = prompt_rows_of(a);
+    uint32_t kc = 0, oc = 0;
+    bool ok = true;
+    while (ok && walk.next(&s)) {
+      if (s.count <= t) continue;
+      // rows of the segment, and the first key this row does not see
+      int32_t rows, end = s.len;
+      if (s.resp) {
+        rows = a.n * a.g;
+        end = min(end, end - a.n + 1 + row / a.g);
+      } else {
+        rows = min(a.M * a.n - rt * a.tpt, a.tpt) * a.g;
+      }
+      const bool idle = quad * 32 >= rows;  // the whole warp is padding
+      float m = -INFINITY, l = 0.f, lcomp = 0.f;
+      for (int32_t j = t; j < s.count; j += 2) {
+        if (!mbar_wait(bar_addr(sbase, B_S_FULL + t), kc & 1)) { fail(); ok = false; break; }
+        ++kc;
+        if (idle) {  // P keeps what S left: rows of D depend on their own rows of A only
+          mbar_arrive(bar_addr(sbase, B_P_FULL + 2 * t));
+          mbar_arrive(bar_addr(sbase, B_P_FULL + 2 * t + 1));
+          continue;
+        }
+        tc_fence_after();
+        uint32_t sr[128];
+        tmem_ld32(s_col + 0, sr);
+        tmem_ld32(s_col + 32, sr + 32);
+        tmem_ld32(s_col + 64, sr + 64);
+        tmem_ld32(s_col + 96, sr + 96);
+        tmem_wait_ld();
+        reg_fence32(sr);
+        reg_fence32(sr + 32);
+        reg_fence32(sr + 64);
+        reg_fence32(sr + 96);
+        const int32_t lim = end - (s.key0 + j * kTile);
+        if (lim < kTile) {  // the source's ragged end, the causal end
+#pragma unroll
+          for (int e = 0; e < 128; ++e)
+            if (e >= lim) sr[e] = __float_as_uint(-INFINITY);
+        }
+        float mx8[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(__uint_as_float(sr[k]), __uint_as_float(sr[k + 8]));
+#pragma unroll
+        for (int e = 16; e < 128; e += 16)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mx8[k] = fmax3(mx8[k], __uint_as_float(sr[e + k]), __uint_as_float(sr[e + 8 + k]));
+        const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
+                               fmaxf(mx8[6], mx8[7]));
+        const float mt = mx * c;
+        bool rescale = false;
+        float alpha = 1.f;
+        if (j == t) {
+          m = mt;
+        } else if (mt > m + kRescaleLog2) {
+          alpha = fast_exp2(m - mt);
+          m = mt;
+          l *= alpha;
+          lcomp *= alpha;
+          rescale = true;
+        }
+        const float msub = (m == -INFINITY) ? 0.f : m;
+        if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < 128; c0 += 32) {
+            uint32_t ov[32];
+            tmem_ld32(o_col + c0, ov);
+            tmem_wait_ld();
+            reg_fence32(ov);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+            tmem_st32(o_col + c0, ov);
+          }
+        }
+        const float2 c2 = make_float2(c, c), nm2 = make_float2(-msub, -msub);
+        float2 ls4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                         make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int jj = 0; jj < 32; ++jj) {
+            const int e = half * 32 + jj;
+            float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])),
+                                  c2, nm2);
+            x.x = fast_exp2(x.x);
+            x.y = fast_exp2(x.y);
+            ls4[jj & 3] = __fadd2_rn(ls4[jj & 3], x);
+            // weights in [0, 2^8] enter the product as bf16, as in the replay forward:
+            // their roundings are independent, so o's error is that of one bf16 rounding
+            pk[jj] = pack_bf16(x.x, x.y);
+          }
+          tmem_st32(s_col + half * 32, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar_addr(sbase, B_P_FULL + 2 * t + half));
+        }
+        const float2 lsa = __fadd2_rn(__fadd2_rn(ls4[0], ls4[1]), __fadd2_rn(ls4[2], ls4[3]));
+        const float ls = lsa.x + lsa.y;
+        const float tsum = l + ls;
+        lcomp += (l - tsum) + ls;
+        l = tsum;
+      }
+      if (!ok) break;
+      if (!mbar_wait(bar_addr(sbase, B_O_DONE + t), oc & 1)) { fail(); break; }
+      ++oc;
+      if (!idle) {
+        tc_fence_after();
+        const float lt = l + lcomp;
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;  // a row that sees no key here
+        const int64_t prow =
+            (s.resp ? resp_row0(a, prompt_rows, s.item, cta, t) : prompt_row0(a, s.item, col, rt, t)) +
+            row;
+        float* po = a.part_o + prow * kD;
+#pragma unroll 1
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          uint32_t ov[32];
+          tmem_ld32(o_col + c0, ov);
+          tmem_wait_ld();
+          reg_fence32(ov);
+          if (row < rows) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4*>(po + c0 + i) =
+                  make_float4(__uint_as_float(ov[i]) * inv, __uint_as_float(ov[i + 1]) * inv,
+                              __uint_as_float(ov[i + 2]) * inv, __uint_as_float(ov[i + 3]) * inv);
+          }
+        }
+        if (row < rows) a.part_lse[prow] = lt == 0.f ? -INFINITY : m + log2f(lt);
+        tc_fence_before();
+      }
+      if (*abort_flag) break;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Merge a row's partials: lse = log2 sum 2^lse_k, o = sum 2^(lse_k - lse) o_k, in the
+// order of the sequence's cut.  Block = (member, KV head, group of kCombineRows rows); the
+// block lists the partials of its (member, KV head) once, then each warp takes rows.
+constexpr int kCombineThreads = 256;
+constexpr int kCombineRows = kCombineThreads / 32;
+constexpr int kMaxParts = 1024;
+
+__global__ void __launch_bounds__(kCombineThreads) decode_combine(const LsDecodeArgs a) {
+  __shared__ int64_t rows0[kMaxParts];
+  __shared__ int32_t wsum[kCombineThreads / 32], wpre[kCombineThreads / 32];
+  __shared__ int32_t wcnt[kCombineThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int m = blockIdx.x / a.hkv, kvh = blockIdx.x - m * a.hkv;
+  const int32_t len = __ldg(a.lens + m);
+  if (len < 0) return;  // a member out of use: its rows stay as they were
+  const int32_t nt = tiles_of(clamp_len(a, len));
+  int32_t tot = 0, pre = 0;
+  for (int i = tid; i < a.M; i += kCombineThreads) {
+    const int32_t x = tiles_of(clamp_len(a, __ldg(a.lens + i)));
+    tot += x;
+    if (i < m) pre += x;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    tot += __shfl_xor_sync(0xffffffffu, tot, o);
+    pre += __shfl_xor_sync(0xffffffffu, pre, o);
+  }
+  if (lane == 0) {
+    wsum[warp] = tot;
+    wpre[warp] = pre;
+  }
+  __syncthreads();
+  tot = pre = 0;
+#pragma unroll
+  for (int i = 0; i < kCombineThreads / 32; ++i) {
+    tot += wsum[i];
+    pre += wpre[i];
+  }
+  const Cut cut(a, tot * a.hkv);
+  const int32_t pb = kvh * a.nt, pe = pb + a.nt;
+  const int32_t rb = pre * a.hkv + kvh * nt, re = rb + nt;
+  const int64_t prompt_rows = prompt_rows_of(a);
+  const int ctas = a.cols * a.rts;
+  // a row tile's rows: token m n + i is row (token - rt tpt) g + head of the group.  The
+  // n tokens of a member may straddle two row tiles, so a row looks its own up below; the
+  // list holds column numbers for the prompt and base rows for the response.
+  int count = 0, prompts = 0;
+  for (int part = 0; part < 2; ++part) {
+    const int n_c = part == 0 ? a.cols : ctas;
+    for (int c0 = 0; c0 < n_c; c0 += kCombineThreads) {
+      const int c = c0 + tid;
+      int halves = 0;
+      if (c < n_c) {
+        int32_t b, e, ob, oe;
+        if (part == 0) {
+          cut.prompt(c, &b, &e);
+          ob = b > pb ? b : pb;
+          oe = e < pe ? e : pe;
+        } else {
+          cut.resp(c / a.rts, c % a.rts, &b, &e);
+          ob = b > rb ? b : rb;
+          oe = e < re ? e : re;
+        }
+        halves = oe - ob >= 2 ? 2 : (oe > ob ? 1 : 0);
+      }
+      // ordered append: inclusive sum over the block
+      int sum = halves;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      if (lane == 31) wcnt[warp] = sum;
+      __syncthreads();
+      int at = count + sum - halves, all = 0;
+#pragma unroll
+      for (int i = 0; i < kCombineThreads / 32; ++i) {
+        if (i < warp) at += wcnt[i];
+        all += wcnt[i];
+      }
+      for (int t = 0; t < halves; ++t)
+        rows0[at + t] = part == 0 ? prompt_row0(a, kvh, c, 0, t)
+                                  : resp_row0(a, prompt_rows, m * a.hkv + kvh, c, t);
+      count += all;
+      __syncthreads();
+    }
+    if (part == 0) prompts = count;
+  }
+  const int r = blockIdx.y * kCombineRows + warp;  // row of the member: token, head
+  if (r >= a.n * a.g) return;
+  const int32_t token = m * a.n + r / a.g, rt = token / a.tpt;
+  const int64_t prompt_off =
+      (int64_t)rt * 2 * kTile + (int64_t)(token - rt * a.tpt) * a.g + r % a.g;
+  auto part_row = [&](int k) { return rows0[k] + (k < prompts ? prompt_off : r); };
+  float mx = -INFINITY;
+  for (int k = lane; k < count; k += 32) mx = fmaxf(mx, a.part_lse[part_row(k)]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float msub = mx == -INFINITY ? 0.f : mx;
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < count; k0 += 32) {
+    const int k = k0 + lane;
+    const int64_t mine = k < count ? part_row(k) : 0;
+    const float w = k < count ? exp2f(a.part_lse[mine] - msub) : 0.f;
+    const int n = count - k0 < 32 ? count - k0 : 32;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const int64_t ri = __shfl_sync(0xffffffffu, mine, i);
+      const float4 v = *(reinterpret_cast<const float4*>(a.part_o + ri * kD) + lane);
+      sum += wi;
+      acc.x = fmaf(wi, v.x, acc.x);
+      acc.y = fmaf(wi, v.y, acc.y);
+      acc.z = fmaf(wi, v.z, acc.z);
+      acc.w = fmaf(wi, v.w, acc.w);
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key at all: o = 0, lse = -inf
+  const int64_t orow = (int64_t)token * a.hq + kvh * a.g + r % a.g;
+  uint2 w;
+  w.x = pack_bf16(acc.x * inv, acc.y * inv);
+  w.y = pack_bf16(acc.z * inv, acc.w * inv);
+  *(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + orow * kD) + lane) = w;
+  if (lane == 0) a.lse[orow] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+}
+
+}  // namespace
+
+int ls_decode_row_tile() { return kTile; }
+int64_t ls_decode_prompt_rows(const LsDecodeArgs& a) { return prompt_rows_of(a); }
+int64_t ls_decode_resp_rows(const LsDecodeArgs& a) {
+  return ((int64_t)a.M * a.hkv + (int64_t)a.cols * a.rts) * 2 * a.n * a.g;
+}
+
+cudaError_t ls_launch_decode_attn(const LsDecodeArgs& a, cudaStream_t st) {
+  TmapSet tm;
+  {
+    const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)a.hq, (uint64_t)a.M * a.n};
+    const uint64_t strides[2] = {(uint64_t)kD * 2, (uint64_t)a.hq * kD * 2};
+    const uint32_t box[3] = {64, (uint32_t)a.g, (uint32_t)a.tpt};
+    if (!ls_make_tmap_bf16(&tm.q, a.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  for (int src = 0; src < 2; ++src) {
+    const int ps = 1 << (src ? a.r_ps_log2 : a.ps_log2);
+    const uint64_t dims[2] = {(uint64_t)kD, (uint64_t)(src ? a.r_num_pages : a.num_pages) * a.hkv * ps};
+    const uint64_t strides[1] = {(uint64_t)kD * 2};
+    const uint32_t box[2] = {64, (uint32_t)(ps < kTile ? ps : kTile)};
+    if (!ls_make_tmap_bf16(src ? &tm.kr : &tm.kp, src ? a.rk_pool : a.k_pool, 2, dims, strides, box) ||
+        !ls_make_tmap_bf16(src ? &tm.vr : &tm.vp, src ? a.rv_pool : a.v_pool, 2, dims, strides, box))
+      return cudaErrorInvalidValue;
+  }
+  cudaError_t e = cudaFuncSetAttribute(decode_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kSmemBytes);
+  if (e != cudaSuccess) return e;
+  decode_attn_kernel<<<a.cols * a.rts, kThreads, kSmemBytes, st>>>(tm, a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  ls_note_launch();
+  decode_combine<<<dim3((unsigned)(a.M * a.hkv), (unsigned)((a.n * a.g + kCombineRows - 1) / kCombineRows)),
+                   kCombineThreads, 0, st>>>(a);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) ls_note_launch();
+  return e;
+}

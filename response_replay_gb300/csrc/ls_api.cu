@@ -906,3 +906,312 @@ ls_status ls_last_device_error(ls_stream_t stream) {
 }
 
 }  // extern "C"
+
+// ---- query/key norm and rotary stage, pages of growing responses, decode attention
+
+namespace {
+
+bool view_ok(const void* p, const int64_t* stride, bool need) {
+  if (!p) return !need;
+  return aligned16(p) && stride[0] >= 0 && stride[1] >= 0 && !(stride[0] & 7) && !(stride[1] & 7);
+}
+
+// Row addresses of a view; false when a required pointer is missing or a stride or address
+// is not whole 16-byte units (8 elements; of 4 bytes, 32-byte units, hold them too).
+bool rows_of(const ls_qkv_view* v, bool need_kv, bool need_v, LsRows* r) {
+  if (!v) return false;
+  if (!view_ok(v->q, v->q_stride, true) || !view_ok(v->k, v->k_stride, need_kv) ||
+      !view_ok(v->v, v->v_stride, need_v))
+    return false;
+  r->p[0] = v->q;
+  r->p[1] = v->k;
+  r->p[2] = v->v;
+  const int64_t* s[3] = {v->q_stride, v->k_stride, v->v_stride};
+  for (int i = 0; i < 3; ++i) {
+    r->ts[i] = s[i][0];
+    r->hs[i] = s[i][1];
+  }
+  return true;
+}
+
+ls_status norm_rope_args(int64_t T, int Hq, int Hkv, const ls_qk_norm* norm, const ls_rotary* rot,
+                         const int32_t* positions, LsNormRopeArgs* a) {
+  if (T < 0 || Hq <= 0 || Hkv <= 0) return LS_ERR_INVALID_ARG;
+  if (T > INT32_MAX || Hq > 65536 || Hkv > 65536) return LS_ERR_UNSUPPORTED;
+  *a = LsNormRopeArgs{};
+  a->T = T;
+  a->hq = Hq;
+  a->hkv = Hkv;
+  a->axes = 1;
+  if (norm) {
+    if (!isfinite(norm->eps) || !(norm->eps > 0.f) || !isfinite(norm->w_offset))
+      return LS_ERR_INVALID_ARG;
+    if (norm->w_dtype != LS_BF16 && norm->w_dtype != LS_FP32) return LS_ERR_INVALID_ARG;
+    if (!aligned16(norm->wq) || !aligned16(norm->wk)) return LS_ERR_INVALID_ARG;
+    a->norm = 1;
+    a->w[0] = norm->wq;
+    a->w[1] = norm->wk;
+    a->w_bf16 = norm->w_dtype == LS_BF16;
+    a->w_offset = norm->w_offset;
+    a->eps = norm->eps;
+  }
+  if (rot && rot->rot_dim != 0) {
+    if (rot->rot_dim < 0 || rot->rot_dim > kHeadDim) return LS_ERR_INVALID_ARG;
+    if (rot->rot_dim & 15) return LS_ERR_UNSUPPORTED;
+    if (rot->axes < 1 || (rot->axes > 1 && !rot->pair_axis)) return LS_ERR_INVALID_ARG;
+    if (rot->axes > 8) return LS_ERR_UNSUPPORTED;
+    if (!rot->inv_freq || (reinterpret_cast<uintptr_t>(rot->inv_freq) & 7) ||
+        !aligned4(rot->pair_axis))
+      return LS_ERR_INVALID_ARG;
+    if (T > 0 && (!positions || !aligned4(positions))) return LS_ERR_INVALID_ARG;
+    a->half = rot->rot_dim / 2;
+    a->axes = rot->axes;
+    a->inv_freq = rot->inv_freq;
+    a->pair_axis = rot->pair_axis;
+    a->interleaved = rot->interleaved != 0;
+    a->pos = positions;
+  }
+  return LS_OK;
+}
+
+ls_status check_pool(const ls_page_pool* c) {
+  if (!c) return LS_ERR_INVALID_ARG;
+  if (c->head_dim != kHeadDim) return LS_ERR_UNSUPPORTED;
+  const int l = ilog2_exact(c->page_size);
+  if (l < 4 || l > 12) return LS_ERR_UNSUPPORTED;
+  if (c->num_kv_heads <= 0 || c->num_pages <= 0) return LS_ERR_INVALID_ARG;
+  if ((int64_t)c->num_pages * c->num_kv_heads * c->page_size >= (1ll << 31)) return LS_ERR_UNSUPPORTED;
+  if (!c->k_pool || !c->v_pool || !aligned16(c->k_pool) || !aligned16(c->v_pool))
+    return LS_ERR_INVALID_ARG;
+  return LS_OK;
+}
+
+struct DecodeWs {
+  size_t part_o, part_lse, total;
+};
+
+// Geometry and workspace of a decode call (device pointers of q and the outputs aside).
+ls_status decode_args(const ls_kv_cache* c, const ls_resp_cache* r, int n, int Hq, LsDecodeArgs* a,
+                      DecodeWs* w) {
+  ls_status s = check_cache(c);
+  if (s != LS_OK) return s;
+  if (!r) return LS_ERR_INVALID_ARG;
+  if ((s = check_pool(&r->pool)) != LS_OK) return s;
+  if (r->pool.num_kv_heads != c->num_kv_heads) return LS_ERR_INVALID_ARG;
+  if (r->members < 0 || r->max_blocks < 0 || n < 1 || Hq <= 0 || Hq % c->num_kv_heads)
+    return LS_ERR_INVALID_ARG;
+  if (r->members > 1024 || (int64_t)r->max_blocks * r->pool.page_size >= (1ll << 31) - 128 ||
+      (int64_t)r->members * r->max_blocks >= (1ll << 31))
+    return LS_ERR_UNSUPPORTED;
+  if (r->members > 0 && (!r->lens || !aligned4(r->lens) ||
+                         (r->max_blocks > 0 && (!r->block_table || !aligned4(r->block_table)))))
+    return LS_ERR_INVALID_ARG;
+  // tile and key counts are 32-bit numbers
+  if (c->num_tokens >= (1ll << 31) - 128 ||
+      ((int64_t)r->max_blocks * r->pool.page_size / 128 + 1) * r->members * c->num_kv_heads >= (1ll << 31) ||
+      (c->num_tokens / 128 + 1) * c->num_kv_heads >= (1ll << 31))
+    return LS_ERR_UNSUPPORTED;
+  *a = LsDecodeArgs{};
+  a->g = Hq / c->num_kv_heads;
+  const int tile = ls_decode_row_tile();
+  if ((int64_t)n * a->g > tile) return LS_ERR_UNSUPPORTED;
+  DevInfo d;
+  if ((s = dev_info(&d)) != LS_OK) return s;
+  a->k_pool = c->k_pool;
+  a->v_pool = c->v_pool;
+  a->page_table = c->page_table;
+  a->num_pages = c->num_pages;
+  a->ps_log2 = ilog2_exact(c->page_size);
+  a->P = c->num_tokens;
+  a->rk_pool = r->pool.k_pool;
+  a->rv_pool = r->pool.v_pool;
+  a->blocks = r->block_table;
+  a->lens = r->lens;
+  a->r_num_pages = r->pool.num_pages;
+  a->r_ps_log2 = ilog2_exact(r->pool.page_size);
+  a->max_blocks = r->max_blocks;
+  a->M = r->members;
+  a->n = n;
+  a->hq = Hq;
+  a->hkv = c->num_kv_heads;
+  a->tpt = tile / a->g;
+  a->nt = (int32_t)((c->num_tokens + tile - 1) / tile);
+  const int ctas = d.sms < 256 ? d.sms : 256;
+  a->rts = r->members > 0 ? (r->members * n + a->tpt - 1) / a->tpt : 1;
+  if (a->rts > ctas) return LS_ERR_UNSUPPORTED;
+  a->cols = ctas / a->rts;
+  a->err = d.err;
+  const size_t rows = (size_t)(ls_decode_prompt_rows(*a) + ls_decode_resp_rows(*a));
+  w->part_o = 0;
+  w->part_lse = align256(rows * kHeadDim * 4);
+  w->total = align256(w->part_lse + rows * 4);
+  return LS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ls_status ls_qk_norm_rope_fwd(const ls_qkv_view* x, int64_t T, int Hq, int Hkv,
+                              const ls_qk_norm* norm, const ls_rotary* rotary,
+                              const int32_t* positions, const ls_qkv_view* out, ls_stream_t stream) {
+  LsNormRopeArgs a;
+  ls_status s = norm_rope_args(T, Hq, Hkv, norm, rotary, positions, &a);
+  if (s != LS_OK) return s;
+  if (T == 0) return LS_OK;
+  LsRows rx, ry;
+  if (!rows_of(x, true, false, &rx) || !rows_of(out, true, rx.p[2] != nullptr, &ry))
+    return LS_ERR_INVALID_ARG;
+  DevInfo d;
+  if ((s = dev_info(&d)) != LS_OK) return s;
+  a.err = d.err;
+  return from_cuda(ls_launch_norm_rope_fwd(a, rx, ry, nullptr, d.sms, (cudaStream_t)stream));
+}
+
+ls_status ls_qk_norm_rope_append(const ls_page_pool* pool, const ls_qkv_view* x, int64_t T, int Hq,
+                                 const ls_qk_norm* norm, const ls_rotary* rotary,
+                                 const int32_t* positions, const int32_t* slots,
+                                 const ls_qkv_view* q_out, ls_stream_t stream) {
+  ls_status s = check_pool(pool);
+  if (s != LS_OK) return s;
+  LsNormRopeArgs a;
+  s = norm_rope_args(T, Hq, pool->num_kv_heads, norm, rotary, positions, &a);
+  if (s != LS_OK) return s;
+  if (T == 0) return LS_OK;
+  LsRows rx, ry;
+  if (!rows_of(x, true, true, &rx) || !rows_of(q_out, false, false, &ry)) return LS_ERR_INVALID_ARG;
+  if (!slots || !aligned4(slots)) return LS_ERR_INVALID_ARG;
+  DevInfo d;
+  if ((s = dev_info(&d)) != LS_OK) return s;
+  a.err = d.err;
+  LsPoolDst dst;
+  dst.k_pool = pool->k_pool;
+  dst.v_pool = pool->v_pool;
+  dst.slots = slots;
+  dst.num_pages = pool->num_pages;
+  dst.ps_log2 = ilog2_exact(pool->page_size);
+  return from_cuda(ls_launch_norm_rope_fwd(a, rx, ry, &dst, d.sms, (cudaStream_t)stream));
+}
+
+ls_status ls_qk_norm_rope_bwd_workspace(int64_t T, size_t* bytes) {
+  if (!bytes || T < 0) return LS_ERR_INVALID_ARG;
+  if (T > INT32_MAX) return LS_ERR_UNSUPPORTED;
+  DevInfo d;
+  const ls_status s = dev_info(&d);
+  if (s != LS_OK) return s;
+  *bytes = (size_t)ls_norm_rope_bwd_ctas(T, d.sms) * 2 * kHeadDim * 4;
+  return LS_OK;
+}
+
+ls_status ls_qk_norm_rope_bwd(const ls_qkv_view* x, int64_t T, int Hq, int Hkv,
+                              const ls_qk_norm* norm, const ls_rotary* rotary,
+                              const int32_t* positions, const ls_qkv_view* dy, ls_dtype dy_dtype,
+                              int accumulate, const ls_qkv_view* dx, float* dwq, float* dwk,
+                              void* workspace, size_t workspace_bytes, ls_stream_t stream) {
+  LsNormRopeArgs a;
+  ls_status s = norm_rope_args(T, Hq, Hkv, norm, rotary, positions, &a);
+  if (s != LS_OK) return s;
+  if (dy_dtype != LS_BF16 && dy_dtype != LS_FP32) return LS_ERR_INVALID_ARG;
+  if ((dwq || dwk) && !norm) return LS_ERR_INVALID_ARG;
+  if (!aligned16(dwq) || !aligned16(dwk)) return LS_ERR_INVALID_ARG;
+  LsRows rx{}, ry{}, rd{};
+  if (T > 0) {
+    // without a norm the inputs are not read
+    if (norm && !rows_of(x, true, false, &rx)) return LS_ERR_INVALID_ARG;
+    if (!rows_of(dy, true, false, &ry) || !rows_of(dx, true, ry.p[2] != nullptr, &rd))
+      return LS_ERR_INVALID_ARG;
+  }
+  DevInfo d;
+  if ((s = dev_info(&d)) != LS_OK) return s;
+  a.err = d.err;
+  if (dwq || dwk) {
+    const size_t need = (size_t)ls_norm_rope_bwd_ctas(T, d.sms) * 2 * kHeadDim * 4;
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+      return LS_ERR_WORKSPACE;
+  } else if (T == 0) {
+    return LS_OK;
+  }
+  return from_cuda(ls_launch_norm_rope_bwd(a, rx, ry, dy_dtype == LS_BF16, rd, dwq, dwk, accumulate,
+                                           static_cast<float*>(workspace), d.sms,
+                                           (cudaStream_t)stream));
+}
+
+ls_status ls_extend_pages(int32_t* block_table, int members, int max_blocks, int page_size,
+                          int num_pages, const int32_t* lens, const int32_t* add,
+                          const int32_t* free_list, int num_free, const int32_t* used, int pos0,
+                          int axes, int64_t capacity, int32_t* slots, int32_t* positions,
+                          int32_t* lens_out, int32_t* used_out, ls_stream_t stream) {
+  if (members < 0 || max_blocks < 0 || num_pages < 0 || num_free < 0 || pos0 < 0 || axes < 1 ||
+      capacity < 0)
+    return LS_ERR_INVALID_ARG;
+  const int l = ilog2_exact(page_size);
+  if (l < 4 || l > 12 || members > 1024 || axes > 8) return LS_ERR_UNSUPPORTED;
+  if ((int64_t)members * max_blocks >= (1ll << 31) || (int64_t)num_pages * page_size >= (1ll << 31) ||
+      (int64_t)max_blocks * page_size + pos0 >= (1ll << 31) || capacity >= (1ll << 31))
+    return LS_ERR_UNSUPPORTED;
+  const void* ptrs[] = {lens, add, used, lens_out, used_out};
+  for (const void* p : ptrs)
+    if (!p || !aligned4(p)) return LS_ERR_INVALID_ARG;
+  if ((max_blocks > 0 && (!block_table || !aligned4(block_table))) ||
+      (num_free > 0 && (!free_list || !aligned4(free_list))) ||
+      (capacity > 0 && (!slots || !aligned16(slots))) || !aligned16(positions))
+    return LS_ERR_INVALID_ARG;
+  if (members == 0 && capacity == 0) return LS_OK;
+  DevInfo d;
+  const ls_status s = dev_info(&d);
+  if (s != LS_OK) return s;
+  LsExtendArgs a;
+  a.table = block_table;
+  a.lens = lens;
+  a.add = add;
+  a.free_list = free_list;
+  a.used = used;
+  a.lens_out = lens_out;
+  a.used_out = used_out;
+  a.slots = slots;
+  a.pos = positions;
+  a.members = members;
+  a.max_blocks = max_blocks;
+  a.num_free = num_free;
+  a.num_pages = num_pages;
+  a.ps_log2 = l;
+  a.axes = axes;
+  a.pos0 = pos0;
+  a.capacity = capacity;
+  a.err = d.err;
+  return from_cuda(ls_launch_extend_pages(a, d.sms, (cudaStream_t)stream));
+}
+
+ls_status ls_decode_attn_workspace(const ls_kv_cache* cache, const ls_resp_cache* resp, int n,
+                                   int Hq, size_t* bytes) {
+  if (!bytes) return LS_ERR_INVALID_ARG;
+  LsDecodeArgs a;
+  DecodeWs w;
+  const ls_status s = decode_args(cache, resp, n, Hq, &a, &w);
+  if (s == LS_OK) *bytes = w.total;
+  return s;
+}
+
+ls_status ls_decode_attn(const ls_kv_cache* cache, const ls_resp_cache* resp, const void* q, int n,
+                         int Hq, float softmax_scale, void* o, float* lse, void* workspace,
+                         size_t workspace_bytes, ls_stream_t stream) {
+  if (!isfinite(softmax_scale) || !(softmax_scale > 0.f)) return LS_ERR_INVALID_ARG;
+  LsDecodeArgs a;
+  DecodeWs w;
+  const ls_status s = decode_args(cache, resp, n, Hq, &a, &w);
+  if (s != LS_OK) return s;
+  if (a.M == 0) return LS_OK;
+  const void* ptrs[] = {q, o, lse};
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return LS_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < w.total || !aligned16(workspace)) return LS_ERR_WORKSPACE;
+  a.q = q;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.o = o;
+  a.lse = lse;
+  a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.part_o);
+  a.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.part_lse);
+  return from_cuda(ls_launch_decode_attn(a, (cudaStream_t)stream));
+}
+
+}  // extern "C"

@@ -209,3 +209,84 @@ int ls_mla_bwd_unit_rows();
 int ls_mla_bwd_part_cols();
 int ls_mla_bwd_dlat_ctas(int32_t R, int32_t H, int sms);
 cudaError_t ls_launch_mla_bwd(const LsMlaBwdArgs& a, const LsSched& sc, int sms, cudaStream_t st);
+
+// Query/key norm and rotary stage (qk_norm_rope.cu).  Rows are heads of 128 bf16 values;
+// tensor i (0 queries, 1 keys, 2 values) has its rows at base + t * ts + h * hs elements.
+struct LsRows {
+  const void* p[3];   // values may be NULL
+  int64_t ts[3], hs[3];
+};
+struct LsNormRopeArgs {
+  int64_t T;
+  int32_t hq, hkv;
+  int32_t norm;              // 0: rotation only
+  const void* w[2];          // norm weights of queries and keys, or NULL (ones)
+  int32_t w_bf16;
+  float w_offset, eps;
+  const int32_t* pos;        // [axes][T]
+  const double* inv_freq;    // [half], radians per position
+  const int32_t* pair_axis;  // [half] or NULL (axis 0)
+  int32_t axes, half, interleaved;
+  uint32_t* err;
+};
+struct LsPoolDst {           // append: keys and values go to pages by slot
+  void* k_pool;
+  void* v_pool;
+  const int32_t* slots;
+  int32_t num_pages, ps_log2;
+};
+cudaError_t ls_launch_norm_rope_fwd(const LsNormRopeArgs& a, const LsRows& x, const LsRows& y,
+                                    const LsPoolDst* dst, int sms, cudaStream_t st);
+int ls_norm_rope_bwd_ctas(int64_t T, int sms);
+// dy: gradients of the outputs (bf16 or fp32 rows); dw: fp32 [128] each or NULL; part:
+// [ctas][2][128] fp32.
+cudaError_t ls_launch_norm_rope_bwd(const LsNormRopeArgs& a, const LsRows& x, const LsRows& dy,
+                                    int dy_bf16, const LsRows& dx, float* dwq, float* dwk,
+                                    int accumulate, float* part, int sms, cudaStream_t st);
+
+// Pages and slots of growing sequences (pages.cu).
+struct LsExtendArgs {
+  int32_t* table;            // [members][max_blocks]
+  const int32_t* lens;
+  const int32_t* add;
+  const int32_t* free_list;
+  const int32_t* used;
+  int32_t* lens_out;
+  int32_t* used_out;
+  int32_t* slots;            // [capacity]
+  int32_t* pos;              // [axes][capacity] or NULL
+  int32_t members, max_blocks, num_free, num_pages, ps_log2, axes, pos0;
+  int64_t capacity;
+  uint32_t* err;
+};
+cudaError_t ls_launch_extend_pages(const LsExtendArgs& a, int sms, cudaStream_t st);
+
+// Decode attention of a group over a shared prompt (decode_attn.cu).
+struct LsDecodeArgs {
+  const void* k_pool;        // prompt pages
+  const void* v_pool;
+  const int32_t* page_table;
+  int32_t num_pages, ps_log2;
+  int64_t P;
+  const void* rk_pool;       // response pages
+  const void* rv_pool;
+  const int32_t* blocks;     // [members][max_blocks]
+  const int32_t* lens;       // [members]
+  int32_t r_num_pages, r_ps_log2, max_blocks;
+  int32_t M, n, hq, hkv, g;
+  int32_t tpt;               // tokens per row tile: floor(128 / g)
+  int32_t rts, cols;         // row tiles; columns of rts CTAs each
+  int32_t nt;                // prompt tiles of one KV head
+  const void* q;             // bf16 [M][n][hq][128]
+  float scale_log2;
+  void* o;
+  float* lse;
+  float* part_o;             // [prompt slots][2][128][128], [response slots][2][n g][128]
+  float* part_lse;           // same without the last dimension (log2 domain)
+  uint32_t* err;
+};
+int ls_decode_row_tile();
+// Rows of partial results: slots x 2 halves x rows.
+int64_t ls_decode_prompt_rows(const LsDecodeArgs& a);
+int64_t ls_decode_resp_rows(const LsDecodeArgs& a);
+cudaError_t ls_launch_decode_attn(const LsDecodeArgs& a, cudaStream_t st);

@@ -431,3 +431,376 @@ def mla_replay_bwd(cache: LatentCache, q: torch.Tensor, lat_resp: torch.Tensor, 
                         dq.data_ptr(), dlat.data_ptr(), ws.data_ptr(), ws.numel(),
                         _stream(stream))
     return dq, dlat
+
+
+# ---------------------------------------------------------------- query / key stage
+
+def _on(device: torch.device, *tensors) -> None:
+    """The kernels run on the current CUDA device: every tensor has to live there."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}")
+
+
+def _head_rows(t: torch.Tensor, name: str, dtypes, shape=None):
+    """A [T][H][128] tensor whose heads are dense rows (token and head strides are free)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != HEAD_DIM or (shape is not None and tuple(t.shape) != shape):
+        want = shape or ("T", "H", HEAD_DIM)
+        raise ValueError(f"{name}: expected shape {want}, got {tuple(t.shape)}")
+    if t.numel() and (t.stride(2) != 1 or t.stride(0) % 8 or t.stride(1) % 8):
+        raise ValueError(f"{name}: heads must be contiguous, at strides of whole 8 elements")
+
+
+def _no_overlap(t: torch.Tensor, name: str):
+    """Rows of an output written at the same time must be distinct memory."""
+    T, H, _ = t.shape
+    st, sh = t.stride(0), t.stride(1)
+    if H > 1 and sh < HEAD_DIM or T > 1 and st < HEAD_DIM:
+        raise ValueError(f"{name}: rows overlap")
+    if T > 1 and H > 1 and st < (H - 1) * sh + HEAD_DIM and sh < (T - 1) * st + HEAD_DIM:
+        raise ValueError(f"{name}: rows overlap")
+
+
+def _view(q, k=None, v=None) -> B.ls_qkv_view:
+    s = B.ls_qkv_view()
+    s.q = q.data_ptr()
+    s.q_stride[0], s.q_stride[1] = q.stride(0), q.stride(1)
+    if k is not None:
+        s.k = k.data_ptr()
+        s.k_stride[0], s.k_stride[1] = k.stride(0), k.stride(1)
+    if v is not None:
+        s.v = v.data_ptr()
+        s.v_stride[0], s.v_stride[1] = v.stride(0), v.stride(1)
+    return s
+
+
+class Rotary:
+    """Rotary positions of a layer (ls_rotary): inv_freq fp64 [rot_dim / 2], radians per
+    position; with more than one axis, pair_axis int32 [rot_dim / 2] gives each pair's.
+    Pairs are (j, j + rot_dim / 2), or (2 j, 2 j + 1) when interleaved."""
+
+    def __init__(self, inv_freq: torch.Tensor, pair_axis: torch.Tensor | None = None, axes: int = 1,
+                 interleaved: bool = False):
+        _check(inv_freq, "inv_freq", torch.float64)
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must have one dimension")
+        if pair_axis is not None:
+            _check(pair_axis, "pair_axis", torch.int32, inv_freq.shape)
+            if pair_axis.device != inv_freq.device:
+                raise ValueError("pair_axis and inv_freq must be on one device")
+        elif axes > 1:
+            raise ValueError("pair_axis is required with more than one axis")
+        self.inv_freq, self.pair_axis, self.axes = inv_freq, pair_axis, axes
+        self.rot_dim, self.interleaved = 2 * inv_freq.numel(), interleaved
+        self.struct = B.ls_rotary(inv_freq.data_ptr(),
+                                  pair_axis.data_ptr() if pair_axis is not None else None,
+                                  self.rot_dim, axes, int(interleaved))
+
+    @classmethod
+    def from_base(cls, base: float, rot_dim: int, device, **kw) -> "Rotary":
+        """inv_freq[j] = base^(-2 j / rot_dim)."""
+        j = torch.arange(rot_dim // 2, dtype=torch.float64)
+        return cls((float(base) ** (-2.0 * j / rot_dim)).to(device), **kw)
+
+
+def _norm_rope_args(q, k, positions, rotary, wq, wk, norm, eps, weight_offset):
+    """Checks shared by the calls of the stage; returns (T, Hq, Hkv, norm struct, rotary
+    struct, positions address)."""
+    T, hq, _ = q.shape
+    hkv = k.shape[1]
+    ns = None
+    if norm:
+        dt = None
+        for w, n in ((wq, "wq"), (wk, "wk")):
+            if w is not None:
+                if w.dtype not in (torch.float32, torch.bfloat16) or w.dtype != (dt or w.dtype):
+                    raise ValueError("wq and wk must both be fp32 or both bf16")
+                dt = w.dtype
+                _check(w, n, dt, (HEAD_DIM,))
+        ns = B.ls_qk_norm(wq.data_ptr() if wq is not None else None,
+                          wk.data_ptr() if wk is not None else None,
+                          B.LS_BF16 if dt == torch.bfloat16 else B.LS_FP32, weight_offset, eps)
+    elif wq is not None or wk is not None:
+        raise ValueError("norm weights without a norm")
+    _on(q.device, k, wq, wk, positions, rotary.inv_freq if rotary is not None else None)
+    pp = None
+    if rotary is not None:
+        if positions is None:
+            raise ValueError("positions are required with rotary")
+        if positions.dim() == 1 and rotary.axes == 1:
+            positions = positions[None]
+        _check(positions, "positions", torch.int32, (rotary.axes, T))
+        pp = positions.data_ptr()
+    return T, hq, hkv, ns, rotary.struct if rotary is not None else None, pp
+
+
+_BF16 = (torch.bfloat16,)
+
+
+def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None,
+                     positions: torch.Tensor | None, rotary: Rotary | None,
+                     wq: torch.Tensor | None = None, wk: torch.Tensor | None = None,
+                     norm: bool = True, eps: float = 1e-6, weight_offset: float = 0.0,
+                     q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                     v_out: torch.Tensor | None = None, stream=None):
+    """Norm of every query and key head and rotary positions in one pass: q [T][Hq][128],
+    k / v [T][Hkv][128] bf16, any token and head strides (slices of a packed projection),
+    positions int32 [axes][T].  Returns (q_out, k_out, v_out); the outputs are dense
+    unless given (an output may be its input), v is copied into the replay's layout."""
+    _head_rows(q, "q", _BF16)
+    _head_rows(k, "k", _BF16, (q.shape[0], k.shape[1], HEAD_DIM))
+    T, hq, hkv, ns, rs, pp = _norm_rope_args(q, k, positions, rotary, wq, wk, norm, eps,
+                                             weight_offset)
+    if v is not None:
+        _head_rows(v, "v", _BF16, (T, hkv, HEAD_DIM))
+    elif v_out is not None:
+        raise ValueError("v_out without v")
+    outs = []
+    for x, o, n in ((q, q_out, "q_out"), (k, k_out, "k_out"), (v, v_out, "v_out")):
+        if x is None:
+            outs.append(None)
+            continue
+        if o is None:
+            o = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        else:
+            _head_rows(o, n, _BF16, tuple(x.shape))
+            _no_overlap(o, n)
+        outs.append(o)
+    _on(q.device, v, *outs)
+    B.ls_qk_norm_rope_fwd(_view(q, k, v), T, hq, hkv, ns, rs, pp, _view(*outs), _stream(stream))
+    return tuple(outs)
+
+
+def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor | None,
+                     rotary: Rotary | None, dq: torch.Tensor, dk: torch.Tensor,
+                     dv: torch.Tensor | None = None, wq: torch.Tensor | None = None,
+                     wk: torch.Tensor | None = None, norm: bool = True, eps: float = 1e-6,
+                     weight_offset: float = 0.0, dx_q: torch.Tensor | None = None,
+                     dx_k: torch.Tensor | None = None, dx_v: torch.Tensor | None = None,
+                     dwq: torch.Tensor | None = None, dwk: torch.Tensor | None = None,
+                     accumulate: bool = False, stream=None):
+    """Backward of qk_norm_rope_fwd: q, k its inputs; dq, dk, dv the gradients of its
+    outputs (all fp32, as the replay backward gives them, or all bf16).  Returns (dx_q,
+    dx_k, dx_v, dwq, dwk): bf16 gradients of the inputs (dense unless given, e.g. as
+    slices of the packed projection's gradient) and fp32 [128] weight gradients, which
+    accumulate adds into; a weight gradient is returned for each weight given."""
+    _head_rows(q, "q", _BF16)
+    _head_rows(k, "k", _BF16, (q.shape[0], k.shape[1], HEAD_DIM))
+    T, hq, hkv, ns, rs, pp = _norm_rope_args(q, k, positions, rotary, wq, wk, norm, eps,
+                                             weight_offset)
+    dt = (dq.dtype,)
+    if dq.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("dq must be fp32 or bf16")
+    _head_rows(dq, "dq", dt, tuple(q.shape))
+    _head_rows(dk, "dk", dt, tuple(k.shape))
+    if dv is not None:
+        _head_rows(dv, "dv", dt, tuple(k.shape))
+    elif dx_v is not None:
+        raise ValueError("dx_v without dv")
+    dev = q.device
+    outs = []
+    for g, o, n in ((dq, dx_q, "dx_q"), (dk, dx_k, "dx_k"), (dv, dx_v, "dx_v")):
+        if g is None:
+            outs.append(None)
+            continue
+        if o is None:
+            o = torch.empty(g.shape, dtype=torch.bfloat16, device=dev)
+        else:
+            _head_rows(o, n, _BF16, tuple(g.shape))
+            _no_overlap(o, n)
+        outs.append(o)
+    if not norm and (dwq is not None or dwk is not None):
+        raise ValueError("weight gradients without a norm")
+    if accumulate and ((wq is not None and dwq is None) or (wk is not None and dwk is None)):
+        raise ValueError("accumulate needs the weight gradients to add into")
+    if wq is not None and dwq is None:
+        dwq = torch.empty(HEAD_DIM, dtype=torch.float32, device=dev)
+    if wk is not None and dwk is None:
+        dwk = torch.empty(HEAD_DIM, dtype=torch.float32, device=dev)
+    for w, n in ((dwq, "dwq"), (dwk, "dwk")):
+        if w is not None:
+            _check(w, n, torch.float32, (HEAD_DIM,))
+    _on(dev, dq, dk, dv, dwq, dwk, *outs)
+    ws, nbytes = None, 0
+    if dwq is not None or dwk is not None:
+        ws = workspace(B.ls_qk_norm_rope_bwd_workspace(T), dev, "qk_norm")
+        nbytes = ws.numel()
+    B.ls_qk_norm_rope_bwd(_view(q, k), T, hq, hkv, ns, rs, pp, _view(dq, dk, dv),
+                          B.LS_FP32 if dq.dtype == torch.float32 else B.LS_BF16, int(accumulate),
+                          _view(*outs), dwq.data_ptr() if dwq is not None else None,
+                          dwk.data_ptr() if dwk is not None else None,
+                          ws.data_ptr() if ws is not None else None, nbytes, _stream(stream))
+    return (*outs, dwq, dwk)
+
+
+class PagePool:
+    """K / V pages of one layer (ls_page_pool): bf16 [num_pages][Hkv][page_size][128]."""
+
+    def __init__(self, k_pool: torch.Tensor, v_pool: torch.Tensor):
+        if k_pool.dim() != 4:
+            raise ValueError("k_pool must be [num_pages][Hkv][page_size][128]")
+        n, hkv, ps, _ = k_pool.shape
+        _check_pool(k_pool, "k_pool", (n, hkv, ps, HEAD_DIM))
+        _check_pool(v_pool, "v_pool", (n, hkv, ps, HEAD_DIM))
+        self.k_pool, self.v_pool = k_pool, v_pool
+        self.num_pages, self.num_kv_heads, self.page_size = n, hkv, ps
+        self.struct = B.ls_page_pool(k_pool.data_ptr(), v_pool.data_ptr(), n, ps, hkv, HEAD_DIM)
+
+    @classmethod
+    def empty(cls, num_pages: int, num_kv_heads: int, page_size: int, device) -> "PagePool":
+        shape = (num_pages, num_kv_heads, page_size, HEAD_DIM)
+        return cls(torch.empty(shape, dtype=torch.bfloat16, device=device),
+                   torch.empty(shape, dtype=torch.bfloat16, device=device))
+
+    @classmethod
+    def of(cls, cache: PagedKVCache) -> "PagePool":
+        """The pools of a prompt cache, to append a chunk of the prompt to by slot."""
+        return cls(cache.k_pool, cache.v_pool)
+
+
+def qk_norm_rope_append(pool: PagePool, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                        slots: torch.Tensor, positions: torch.Tensor | None, rotary: Rotary | None,
+                        wq: torch.Tensor | None = None, wk: torch.Tensor | None = None,
+                        norm: bool = True, eps: float = 1e-6, weight_offset: float = 0.0,
+                        q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """qk_norm_rope_fwd with keys and values written into `pool` at slots[t] = page *
+    page_size + offset (int32 [T]; negative: a padding token, nothing of it is written).
+    Returns q_out."""
+    _head_rows(q, "q", _BF16)
+    _head_rows(k, "k", _BF16, (q.shape[0], pool.num_kv_heads, HEAD_DIM))
+    _head_rows(v, "v", _BF16, tuple(k.shape))
+    T, hq, _, ns, rs, pp = _norm_rope_args(q, k, positions, rotary, wq, wk, norm, eps,
+                                           weight_offset)
+    _check(slots, "slots", torch.int32, (T,))
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    else:
+        _head_rows(q_out, "q_out", _BF16, tuple(q.shape))
+        _no_overlap(q_out, "q_out")
+    _on(q.device, v, slots, q_out, *(p for p in (pool.k_pool, pool.v_pool) if p.is_cuda))
+    B.ls_qk_norm_rope_append(pool.struct, _view(q, k, v), T, hq, ns, rs, pp, slots.data_ptr(),
+                             _view(q_out), _stream(stream))
+    return q_out
+
+
+# ---------------------------------------------------------------- decode step
+
+class PageAllocator:
+    """Pages of a group's growing responses (ls_extend_pages): block_table int32
+    [members][max_blocks], lens int32 [members] (negative: out of use), free_list int32
+    [num_free] and used int32 [1], all on the GPU.  One allocator serves every layer's
+    pools: the token -> page map is the same in each."""
+
+    def __init__(self, block_table: torch.Tensor, lens: torch.Tensor, free_list: torch.Tensor,
+                 used: torch.Tensor, page_size: int, num_pages: int | None = None):
+        _check(block_table, "block_table", torch.int32)
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [members][max_blocks]")
+        _check(lens, "lens", torch.int32, block_table.shape[:1])
+        _check(free_list, "free_list", torch.int32, (free_list.numel(),))
+        _check(used, "used", torch.int32, (1,))
+        for t in (lens, free_list, used):
+            if t.device != block_table.device:
+                raise ValueError("the allocator's tensors must be on one device")
+        self.block_table, self.lens, self.free_list, self.used = block_table, lens, free_list, used
+        self.page_size = page_size
+        self.num_pages = free_list.numel() if num_pages is None else num_pages
+
+    @classmethod
+    def empty(cls, members: int, max_blocks: int, num_pages: int, page_size: int,
+              device) -> "PageAllocator":
+        """No tokens yet, every page of the pool free."""
+        z = dict(dtype=torch.int32, device=device)
+        return cls(torch.zeros((members, max_blocks), **z), torch.zeros(members, **z),
+                   torch.arange(num_pages, **z), torch.zeros(1, **z), page_size)
+
+    @property
+    def members(self) -> int:
+        return self.block_table.shape[0]
+
+    @property
+    def device(self):
+        return self.block_table.device
+
+
+def extend_pages(alloc: PageAllocator, add: torch.Tensor, pos0: int, slots: torch.Tensor,
+                 positions: torch.Tensor | None = None, lens_out: torch.Tensor | None = None,
+                 used_out: torch.Tensor | None = None, stream=None) -> None:
+    """Room for add[m] more tokens of every member: fills slots int32 [capacity] (-1 behind
+    the last token) and positions int32 [axes][capacity] (pos0 + index within the
+    response), enters new pages into the table and advances alloc.lens and alloc.used (or
+    writes them to lens_out / used_out).  See ls_extend_pages for what is refused."""
+    M, nb = alloc.block_table.shape
+    _check(add, "add", torch.int32, (M,))
+    _check(slots, "slots", torch.int32, (slots.numel(),))
+    cap = slots.numel()
+    axes = 1
+    if positions is not None:
+        if positions.dim() != 2:
+            raise ValueError("positions must be [axes][capacity]")
+        axes = positions.shape[0]
+        _check(positions, "positions", torch.int32, (axes, cap))
+    lens_out = alloc.lens if lens_out is None else lens_out
+    used_out = alloc.used if used_out is None else used_out
+    _check(lens_out, "lens_out", torch.int32, (M,))
+    _check(used_out, "used_out", torch.int32, (1,))
+    _on(alloc.device, add, slots, positions, lens_out, used_out)
+    B.ls_extend_pages(alloc.block_table.data_ptr(), M, nb, alloc.page_size, alloc.num_pages,
+                      alloc.lens.data_ptr(), add.data_ptr(), alloc.free_list.data_ptr(),
+                      alloc.free_list.numel(), alloc.used.data_ptr(), pos0, axes, cap,
+                      slots.data_ptr(), positions.data_ptr() if positions is not None else None,
+                      lens_out.data_ptr(), used_out.data_ptr(), _stream(stream))
+
+
+class ResponseCache:
+    """One layer's view of a group's responses (ls_resp_cache): its page pool under the
+    members' block table and lengths (an allocator's, shared by all layers)."""
+
+    def __init__(self, pool: PagePool, block_table: torch.Tensor, lens: torch.Tensor):
+        _check(block_table, "block_table", torch.int32)
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [members][max_blocks]")
+        _check(lens, "lens", torch.int32, block_table.shape[:1])
+        if lens.device != block_table.device:
+            raise ValueError("block_table and lens must be on one device")
+        self.pool, self.block_table, self.lens = pool, block_table, lens
+        self.struct = B.ls_resp_cache(pool.struct, block_table.data_ptr(), lens.data_ptr(),
+                                      block_table.shape[0], block_table.shape[1])
+
+    @classmethod
+    def of(cls, pool: PagePool, alloc: PageAllocator) -> "ResponseCache":
+        if pool.page_size != alloc.page_size or pool.num_pages < alloc.num_pages:
+            raise ValueError("the pool does not hold the allocator's pages")
+        return cls(pool, alloc.block_table, alloc.lens)
+
+    @property
+    def members(self) -> int:
+        return self.block_table.shape[0]
+
+
+def decode_attn(cache: PagedKVCache, resp: ResponseCache, q: torch.Tensor, softmax_scale: float,
+                o: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None):
+    """Attention of a decode step: q [members][n][Hq][128], the n newest tokens of every
+    member (already appended to its pages), over the shared prompt and the member's own
+    response.  Returns (o, lse)."""
+    M, n, hq, _ = q.shape
+    _check(q, "q", torch.bfloat16, (resp.members, n, hq, HEAD_DIM))
+    if o is None:
+        o = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((M, n, hq), dtype=torch.float32, device=q.device)
+    _check(o, "o", torch.bfloat16, q.shape)
+    _check(lse, "lse", torch.float32, (M, n, hq))
+    _on(q.device, cache.page_table, resp.block_table, o, lse)
+    nbytes = B.ls_decode_attn_workspace(cache.struct, resp.struct, n, hq)
+    ws = workspace(nbytes, q.device, "decode")
+    B.ls_decode_attn(cache.struct, resp.struct, q.data_ptr(), n, hq, softmax_scale, o.data_ptr(),
+                     lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    return o, lse
