@@ -58,8 +58,13 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;
 
 enum {
-  B_KV_FULL = 0,
-  B_KV_EMPTY = B_KV_FULL + kStages,
+  // A stage is filled for the issuer of its tile's parity t, who may reach it before the
+  // other issuer's earlier fill of the same stage has landed (loads finish in any order):
+  // one barrier for both would show that issuer a phase that is not its own.  So each
+  // stage has a FULL barrier per issuer (at kStages t + stage), and each issuer counts the
+  // phases of its own fills.
+  B_KV_FULL = 0,                 // 2 kStages
+  B_KV_EMPTY = B_KV_FULL + 2 * kStages,
   B_AUX = B_KV_EMPTY + kStages,  // a ragged V tile has landed, its tail not yet cleared
   B_Q_FULL = B_AUX + kStages,    // 2
   B_Q_EMPTY = B_Q_FULL + 2,      // 2
@@ -250,6 +255,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bar_addr(sbase, B_KV_FULL + i), 1);
+      mbar_init(bar_addr(sbase, B_KV_FULL + kStages + i), 1);
       mbar_init(bar_addr(sbase, B_KV_EMPTY + i), 1);
       mbar_init(bar_addr(sbase, B_AUX + i), 1);
     }
@@ -304,7 +310,8 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
         tma_prefetch_desc(&tm.vp);
         tma_prefetch_desc(&tm.kr);
         tma_prefetch_desc(&tm.vr);
-        uint32_t seg = 0, fills = 0;
+        // per FULL barrier: parity of its next fill; per stage: issuer of its last one
+        uint32_t seg = 0, full_phase = 0, last_t = 0, filled = 0;
         RingPos<kStages> ring;
         bool ok = true;
         while (ok && walk.next(&s)) {
@@ -339,7 +346,9 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
                 break;
               }
               const bool ragged_v = kv == 1 && left < kTile;
-              const uint32_t fb = bar_addr(sbase, (ragged_v ? B_AUX : B_KV_FULL) + ring.stage);
+              const uint32_t t = j & 1, full = kStages * t + ring.stage;
+              const uint32_t fb =
+                  bar_addr(sbase, ragged_v ? B_AUX + ring.stage : B_KV_FULL + full);
               const uint32_t dst = sbase + kOffRing + ring.stage * kTileBytes;
               const void* map = s.resp ? (kv ? (const void*)&tm.vr : (const void*)&tm.kr)
                                        : (kv ? (const void*)&tm.vp : (const void*)&tm.kp);
@@ -357,14 +366,19 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
                 for (int hf = 0; hf < 2; ++hf)
                   tma_load_2d(dst + hf * kHalfBytes + x * box_rows * 128, map, hf * 64, y, fb);
               }
+              full_phase ^= 1u << full;
+              last_t = (last_t & ~(1u << ring.stage)) | (t << ring.stage);
+              filled |= 1u << ring.stage;
               ring.advance();
-              ++fills;
             }
           }
         }
         // Do not leave while loads into this CTA's shared memory may still be in flight.
-        for (uint32_t i = fills > kStages ? fills - kStages : 0; i < fills; ++i)
-          mbar_wait(bar_addr(sbase, B_KV_FULL + i % kStages), (i / kStages) & 1);
+        for (uint32_t st = 0; st < kStages; ++st) {
+          const uint32_t full = kStages * ((last_t >> st) & 1) + st;
+          if ((filled >> st) & 1)
+            mbar_wait(bar_addr(sbase, B_KV_FULL + full), ((full_phase >> full) & 1) ^ 1);
+        }
         for (uint32_t i = seg > 2 ? seg - 2 : 0; i < seg; ++i)
           mbar_wait(bar_addr(sbase, B_Q_FULL + (i & 1)), (i >> 1) & 1);
       }
@@ -390,7 +404,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar_addr(sbase, B_KV_FULL + st));
+          if (lane == 0) mbar_arrive(bar_addr(sbase, B_KV_FULL + kStages * (j & 1) + st));
         }
       }
     } else {
@@ -420,6 +434,12 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
           }
         };
         uint32_t seg = 0, base = 0, kc = 0;  // segments, ring slots before the segment, own tiles
+        uint32_t full_phase = 0;             // per stage: parity of this issuer's next fill
+        auto wait_full = [&](uint32_t st) {
+          const bool w = mbar_wait(bar_addr(sbase, B_KV_FULL + kStages * t + st), (full_phase >> st) & 1);
+          full_phase ^= 1u << st;
+          return w;
+        };
         bool ok = true;
         while (ok && walk.next(&s)) {
           const int b = seg & 1;
@@ -434,7 +454,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
           // S of own tile j: its K is ring slot base + 2 j
           auto s_tile = [&](int32_t j) {
             const uint32_t slot = base + 2 * j, st = slot % kStages;
-            if (!mbar_wait(bar_addr(sbase, B_KV_FULL + st), (slot / kStages) & 1)) return false;
+            if (!wait_full(st)) return false;
             tc_fence_after();
             issue_s(dq, st);
             mma_commit(bar_addr(sbase, B_S_FULL + t));
@@ -445,8 +465,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
           ok = s_tile(t);
           for (int32_t j = t; ok && j < s.count; j += 2) {
             const uint32_t slot = base + 2 * j + 1, st = slot % kStages;
-            ok = mbar_wait(bar_addr(sbase, B_KV_FULL + st), (slot / kStages) & 1) &&
-                 mbar_wait(bar_addr(sbase, B_P_FULL + 2 * t), kc & 1);
+            ok = wait_full(st) && mbar_wait(bar_addr(sbase, B_P_FULL + 2 * t), kc & 1);
             if (!ok) break;
             tc_fence_after();
             issue_pv_half(st, 0, j > t);

@@ -86,6 +86,27 @@ CASES = [
 ]
 
 
+# Many tiles to a CTA: long segments, in which the ring of tiles goes round many times and
+# loads land out of order; several segments of several tiles each.
+LONG = [
+    (200003, [5000, 37, 1, 2600], 6, 1, 1, 64, 64),
+    (0, [40000, 129, 30001], 6, 2, 1, 64, 16),
+    (70000, [300 + 100 * i for i in range(44)], 12, 2, 1, 16, 256),
+    (128000, [513, 30000], 8, 8, 2, 256, 32),
+]
+
+
+@pytest.mark.parametrize("P,lens,hq,hkv,n,ps,rps", LONG)
+def test_long_segments(cuda, P, lens, hq, hkv, n, ps, rps):
+    g = Group(cuda, P, lens, hq, hkv, n, ps, rps, seed=P + hq)
+    o, lse = g.run()
+    g.check(o, lse)
+    for _ in range(50):  # the same bits whatever order the loads land in
+        o2, lse2 = api.decode_attn(g.cache, g.resp, g.q, SCALE)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert B.ls_last_device_error(0) == B.LS_OK
+
+
 @pytest.mark.parametrize("P,lens,hq,hkv,n,ps,rps", CASES)
 def test_decode(cuda, P, lens, hq, hkv, n, ps, rps):
     g = Group(cuda, P, lens, hq, hkv, n, ps, rps, seed=P + hq)
