@@ -562,8 +562,8 @@ typedef struct {
  * lies behind a sequence's end in its last page may be anything.  A length past
  * max_blocks * page_size is cut there and sets LS_ERR_DEVICE_CHECK, as does a page id
  * outside its pool (its keys and values count as zeros).  n * Hq / num_kv_heads <= 128,
- * members <= 1024, and at most one row tile (floor(128 / g) tokens, g = Hq / num_kv_heads)
- * per SM, else LS_ERR_UNSUPPORTED.  Two launches; the lengths may change between replays
+ * members <= 1024, and members * n * Hq / num_kv_heads rows of at most 128 per SM, else
+ * LS_ERR_UNSUPPORTED.  Two launches; the lengths may change between replays
  * of a captured graph, the pointers and P may not.  members == 0 is a no-op. */
 ls_status ls_decode_attn_workspace(const ls_kv_cache* cache, const ls_resp_cache* resp, int n,
                                    int Hq, size_t* bytes);

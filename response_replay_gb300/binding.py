@@ -53,8 +53,10 @@ class ls_latent_cache(C.Structure):
 
 class ls_qkv_view(C.Structure):
     _fields_ = [
-        ("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("q_stride", C.c_int64 * 2),
-        ("k_stride", C.c_int64 * 2), ("v_stride", C.c_int64 * 2),
+        ("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p),
+        # token and head strides (elements) of q, k, v
+        ("q_ts", C.c_int64), ("q_hs", C.c_int64), ("k_ts", C.c_int64), ("k_hs", C.c_int64),
+        ("v_ts", C.c_int64), ("v_hs", C.c_int64),
     ]
 
 
@@ -431,5 +433,5 @@ def ls_decode_attn(cache: ls_kv_cache, resp: ls_resp_cache, q: int, n: int, Hq: 
                    softmax_scale: float, o: int, lse: int, workspace: int, workspace_bytes: int,
                    stream: int = 0) -> None:
     _ok("ls_decode_attn",
-        lib().ls_decode_attn(C.byref(cache), C.byref(resp), q, n, Hq, softmax_scale, o, lse,
+        lib().ls_decode_attn(cache, resp, q, n, Hq, softmax_scale, o, lse,
                              workspace, workspace_bytes, stream))

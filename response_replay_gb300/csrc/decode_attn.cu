@@ -19,13 +19,13 @@
 // device (a captured graph follows them): every CTA sums them when it starts.
 //
 // CTA (one per SM, 12 warps):
-//   warp 0      TMA producer: Q of a segment (two buffers), then its K and V tiles page by
-//               page into a 5-stage ring.
+//   warp 0      TMA producer: the segments' K and V tiles, page by page, into a 5-stage ring.
 //   warps 1, 2  MMA issuers: the segment's even and odd tiles.  S_t = Q K^T into tensor
 //               memory, O_t += P_t V with P_t read from tensor memory; the two tile
 //               sequences are independent, so one's MMAs run under the other's softmax.
-//   warp 3      clears the V rows behind a sequence's end (stale page contents, even NaN,
-//               would survive a zero weight) before the tile is handed over.
+//   warp 3      loads the segments' Q (two buffers), and clears the V rows behind a
+//               sequence's end (stale page contents, even NaN, would survive a zero weight)
+//               before such a tile is handed over.
 //   warps 4-7   softmax of the even tiles, warps 8-11 of the odd ones, one row a thread;
 //               warps whose rows are all padding only keep the barriers going.
 // Tensor memory (512 columns): S_0 [0,128) S_1 [128,256) O_0 [256,384) O_1 [384,512).
@@ -78,8 +78,15 @@ constexpr uint32_t kOffVars = kOffBar + B_COUNT * 8;
 static_assert(B_COUNT * 8 + 32 <= 512, "barrier area");
 
 struct TmapSet {
-  CUtensorMap q, kp, vp, kr, vr;
+  CUtensorMap kp, vp, kr, vr;
 };
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
 
 __device__ __forceinline__ uint32_t bar_addr(uint32_t base, int i) { return base + kOffBar + 8 * i; }
 
@@ -139,6 +146,7 @@ struct Walk {
   __device__ __forceinline__ Walk(const LsDecodeArgs& a_, const volatile int32_t* start, int32_t p0,
                                   int32_t p1, int32_t r0, int32_t r1)
       : a(a_), p(p0), p_end(p1), r(r0), r_end(r1), m(start[0]), off(start[1]) {}
+  __device__ __forceinline__ bool done() const { return p >= p_end && r >= r_end; }
   __device__ __forceinline__ bool next(Seg* s) {
     if (p < p_end) {
       const int32_t h = p / a.nt, first = p - h * a.nt;
@@ -172,6 +180,12 @@ struct Walk {
     return true;
   }
 };
+
+// Query rows of a segment: row r of row tile rt is row rt x 128 + r of all (token, head of
+// the group) pairs against the prompt, row r of the member's own against a response.
+__device__ __forceinline__ int32_t seg_rows(const LsDecodeArgs& a, const Seg& s, int32_t rt) {
+  return s.resp ? a.n * a.g : min(a.M * a.n * a.g - rt * kTile, kTile);
+}
 
 // Rows of a partial: prompt partials first, then the responses'.  (item + CTA in walk
 // order) numbers a CTA's segments uniquely: from one segment to the next of the whole
@@ -275,19 +289,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), 512);
     tmem_relinquish();
   }
-  {
-    // a Q box holds tpt tokens x g heads; the tile's other rows are never loaded
-    const int used = a.tpt * a.g;
-    if (used < kTile) {
-      const int per_half = (kTile - used) * 8;
-      for (int i = tid; i < 4 * per_half; i += kThreads) {
-        const int part = i / per_half, c = i % per_half;
-        *reinterpret_cast<uint4*>(smem + kOffQ + part * kHalfBytes + used * 128 + c * 16) =
-            make_uint4(0, 0, 0, 0);
-      }
-    }
-    fence_proxy_async_smem();  // also the scratch above, before TMA writes the ring
-  }
+  fence_proxy_async_smem();  // the scratch above, before TMA writes the ring
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -305,28 +307,15 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     if (warp == 0) {
       // ---------------------------------------------------------- TMA producer
       if (lane == 0) {
-        tma_prefetch_desc(&tm.q);
         tma_prefetch_desc(&tm.kp);
         tma_prefetch_desc(&tm.vp);
         tma_prefetch_desc(&tm.kr);
         tma_prefetch_desc(&tm.vr);
         // per FULL barrier: parity of its next fill; per stage: issuer of its last one
-        uint32_t seg = 0, full_phase = 0, last_t = 0, filled = 0;
+        uint32_t full_phase = 0, last_t = 0, filled = 0;
         RingPos<kStages> ring;
         bool ok = true;
         while (ok && walk.next(&s)) {
-          const int b = seg & 1;
-          if (seg >= 2 && !mbar_wait(bar_addr(sbase, B_Q_EMPTY + b), ((seg >> 1) - 1) & 1)) {
-            fail();
-            break;
-          }
-          const uint32_t qb = bar_addr(sbase, B_Q_FULL + b);
-          mbar_expect_tx(qb, 2u * 128u * (uint32_t)(a.g * a.tpt));
-          const int32_t tok0 = s.resp ? s.m * a.n : rt * a.tpt;
-          for (int hf = 0; hf < 2; ++hf)
-            tma_load_3d(sbase + kOffQ + b * kTileBytes + hf * kHalfBytes, &tm.q, hf * 64,
-                        s.kvh * a.g, tok0, qb);
-          ++seg;
           const int ps_log2 = s.resp ? a.r_ps_log2 : a.ps_log2;
           const int32_t ps = 1 << ps_log2;
           const int32_t box_rows = ps < kTile ? ps : kTile;
@@ -379,23 +368,46 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
           if ((filled >> st) & 1)
             mbar_wait(bar_addr(sbase, B_KV_FULL + full), ((full_phase >> full) & 1) ^ 1);
         }
-        for (uint32_t i = seg > 2 ? seg - 2 : 0; i < seg; ++i)
-          mbar_wait(bar_addr(sbase, B_Q_FULL + (i & 1)), (i >> 1) & 1);
       }
     } else if (warp == 3) {
-      // ---------------------------------------------------------- V tails
-      uint32_t ring = 1, aux_phase = 0;  // ring slot of the tile's V; a phase bit per stage
+      // ---------------------------------------------------------- Q, V tails
+      // Q of segment s goes to buffer s & 1 in the operand layout (128-byte swizzle: chunk c
+      // of row r lies at chunk c ^ (r & 7)), row by row, so that a row tile may begin inside
+      // a token.  Rows behind the segment's keep what the buffer held: a row of S, P and O
+      // depends on its own row of Q only, and theirs are not written out.
+      Walk ahead = walk;
+      Seg sq;
+      uint32_t loaded = 0;
+      auto load_q = [&]() {  // the next segment's Q, if there is one
+        if (!ahead.next(&sq)) return;
+        const uint32_t buf = sbase + kOffQ + (loaded & 1) * kTileBytes;
+        const int rows = seg_rows(a, sq, rt);
+        const int32_t row0 = sq.resp ? sq.m * a.n * a.g : rt * kTile;
+        int32_t token = (row0 + (lane >> 4)) / a.g, head = (row0 + (lane >> 4)) - token * a.g;
+        const int c = lane & 15;
+        for (int r = lane >> 4; r < rows; r += 2) {
+          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
+                                     ((int64_t)token * a.hq + sq.kvh * a.g + head) * kD + c * 8;
+          cp_async16(buf + (c >> 3) * kHalfBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4), src);
+          for (head += 2; head >= a.g; head -= a.g) ++token;
+        }
+        cp_async_wait_all();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_addr(sbase, B_Q_FULL + (loaded & 1)));
+        ++loaded;
+      };
+      load_q();
+      load_q();
+      uint32_t seg = 0, ring = 1, aux_phase = 0;  // ring slot of the tile's V; a phase bit per stage
       bool ok = true;
-      while (ok && walk.next(&s)) {
+      for (; ok && walk.next(&s); ++seg) {
         for (int32_t j = 0; ok && j < s.count; ++j, ring += 2) {
           const int32_t left = s.len - (s.key0 + j * kTile);
           if (left >= kTile) continue;
           const uint32_t st = ring % kStages;
           ok = mbar_wait(bar_addr(sbase, B_AUX + st), (aux_phase >> st) & 1);
-          if (!ok) {
-            fail();
-            break;
-          }
+          if (!ok) break;
           aux_phase ^= 1u << st;
           uint8_t* vb = smem + kOffRing + st * kTileBytes;
           for (int i = left * 8 + lane; i < kTile * 8; i += 32) {
@@ -406,7 +418,13 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_addr(sbase, B_KV_FULL + kStages * (j & 1) + st));
         }
+        // segment s + 2 reuses this one's Q buffer, once its last S is done
+        if (ok && loaded == seg + 2 && !ahead.done()) {
+          ok = mbar_wait(bar_addr(sbase, B_Q_EMPTY + (seg & 1)), (seg >> 1) & 1);
+          if (ok) load_q();
+        }
       }
+      if (!ok) fail();
     } else {
       // ---------------------------------------------------------- MMA issuers
       if (lane == 0) {
@@ -504,13 +522,8 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     while (ok && walk.next(&s)) {
       if (s.count <= t) continue;
       // rows of the segment, and the first key this row does not see
-      int32_t rows, end = s.len;
-      if (s.resp) {
-        rows = a.n * a.g;
-        end = min(end, end - a.n + 1 + row / a.g);
-      } else {
-        rows = min(a.M * a.n - rt * a.tpt, a.tpt) * a.g;
-      }
+      const int32_t rows = seg_rows(a, s, rt);
+      const int32_t end = s.resp ? min(s.len, s.len - a.n + 1 + row / a.g) : s.len;
       const bool idle = quad * 32 >= rows;  // the whole warp is padding
       float m = -INFINITY, l = 0.f, lcomp = 0.f;
       for (int32_t j = t; j < s.count; j += 2) {
@@ -684,9 +697,8 @@ __global__ void __launch_bounds__(kCombineThreads) decode_combine(const LsDecode
   const int32_t rb = pre * a.hkv + kvh * nt, re = rb + nt;
   const int64_t prompt_rows = prompt_rows_of(a);
   const int ctas = a.cols * a.rts;
-  // a row tile's rows: token m n + i is row (token - rt tpt) g + head of the group.  The
-  // n tokens of a member may straddle two row tiles, so a row looks its own up below; the
-  // list holds column numbers for the prompt and base rows for the response.
+  // a member's rows may straddle two row tiles: the list holds row 0 of row tile 0 for the
+  // prompt's partials, and a row adds its own place below
   int count = 0, prompts = 0;
   for (int part = 0; part < 2; ++part) {
     const int n_c = part == 0 ? a.cols : ctas;
@@ -731,9 +743,8 @@ __global__ void __launch_bounds__(kCombineThreads) decode_combine(const LsDecode
   }
   const int r = blockIdx.y * kCombineRows + warp;  // row of the member: token, head
   if (r >= a.n * a.g) return;
-  const int32_t token = m * a.n + r / a.g, rt = token / a.tpt;
-  const int64_t prompt_off =
-      (int64_t)rt * 2 * kTile + (int64_t)(token - rt * a.tpt) * a.g + r % a.g;
+  const int32_t token = m * a.n + r / a.g, grow = m * a.n * a.g + r;
+  const int64_t prompt_off = (int64_t)(grow / kTile) * 2 * kTile + grow % kTile;
   auto part_row = [&](int k) { return rows0[k] + (k < prompts ? prompt_off : r); };
   float mx = -INFINITY;
   for (int k = lane; k < count; k += 32) mx = fmaxf(mx, a.part_lse[part_row(k)]);
@@ -778,12 +789,6 @@ int64_t ls_decode_resp_rows(const LsDecodeArgs& a) {
 
 cudaError_t ls_launch_decode_attn(const LsDecodeArgs& a, cudaStream_t st) {
   TmapSet tm;
-  {
-    const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)a.hq, (uint64_t)a.M * a.n};
-    const uint64_t strides[2] = {(uint64_t)kD * 2, (uint64_t)a.hq * kD * 2};
-    const uint32_t box[3] = {64, (uint32_t)a.g, (uint32_t)a.tpt};
-    if (!ls_make_tmap_bf16(&tm.q, a.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
-  }
   for (int src = 0; src < 2; ++src) {
     const int ps = 1 << (src ? a.r_ps_log2 : a.ps_log2);
     const uint64_t dims[2] = {(uint64_t)kD, (uint64_t)(src ? a.r_num_pages : a.num_pages) * a.hkv * ps};

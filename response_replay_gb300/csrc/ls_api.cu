@@ -1034,10 +1034,9 @@ ls_status decode_args(const ls_kv_cache* c, const ls_resp_cache* r, int n, int H
   a->n = n;
   a->hq = Hq;
   a->hkv = c->num_kv_heads;
-  a->tpt = tile / a->g;
   a->nt = (int32_t)((c->num_tokens + tile - 1) / tile);
   const int ctas = d.sms < 256 ? d.sms : 256;
-  a->rts = r->members > 0 ? (r->members * n + a->tpt - 1) / a->tpt : 1;
+  a->rts = r->members > 0 ? (r->members * n * a->g + tile - 1) / tile : 1;
   if (a->rts > ctas) return LS_ERR_UNSUPPORTED;
   a->cols = ctas / a->rts;
   a->err = d.err;

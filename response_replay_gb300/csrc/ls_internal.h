@@ -274,8 +274,7 @@ struct LsDecodeArgs {
   const int32_t* lens;       // [members]
   int32_t r_num_pages, r_ps_log2, max_blocks;
   int32_t M, n, hq, hkv, g;
-  int32_t tpt;               // tokens per row tile: floor(128 / g)
-  int32_t rts, cols;         // row tiles; columns of rts CTAs each
+  int32_t rts, cols;         // row tiles of 128 (token, head) rows; columns of rts CTAs each
   int32_t nt;                // prompt tiles of one KV head
   const void* q;             // bf16 [M][n][hq][128]
   float scale_log2;

@@ -33,6 +33,22 @@ def _check(t: torch.Tensor, name: str, dtype, shape=None):
 _workspaces: dict = {}
 
 
+_retired: list = []
+
+
+def _call_workspace(nbytes: int, like: torch.Tensor, key: str, stream: int) -> torch.Tensor:
+    """A workspace of the calls on one stream (calls on different streams may overlap).
+    One that was outgrown is kept: a captured graph may still use it."""
+    k = (like.get_device(), key, stream)
+    ws = _workspaces.get(k)
+    if ws is None or ws.numel() < nbytes:
+        if ws is not None:
+            _retired.append(ws)
+        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=like.device)
+        _workspaces[k] = ws
+    return ws
+
+
 def workspace(nbytes: int, device: torch.device, key: str = "default") -> torch.Tensor:
     """A reusable uint8 workspace of at least nbytes on `device` (grown on demand).
     Calls that share a key must not overlap on the GPU."""
@@ -434,32 +450,55 @@ def mla_replay_bwd(cache: LatentCache, q: torch.Tensor, lat_resp: torch.Tensor, 
 
 
 # ---------------------------------------------------------------- query / key stage
+#
+# These calls are a few microseconds of GPU work at decode sizes, so their argument checks
+# are kept to one pass over each tensor's attributes.
 
-def _on(device: torch.device, *tensors) -> None:
-    """The kernels run on the current CUDA device: every tensor has to live there."""
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {device}, but the current device is "
+def _dev_stream(dev: int, stream) -> int:
+    """The stream of a call on CUDA device `dev`, which has to be the current one (the
+    kernels run there)."""
+    if dev < 0:
+        raise ValueError("the tensors must be CUDA tensors")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _head_rows(t: torch.Tensor, name: str, dtypes, shape=None):
-    """A [T][H][128] tensor whose heads are dense rows (token and head strides are free)."""
-    if not t.is_cuda:
+def _refuse(t: torch.Tensor, name: str, dtype, shape, dev: int):
+    if t.get_device() < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != HEAD_DIM or (shape is not None and tuple(t.shape) != shape):
-        want = shape or ("T", "H", HEAD_DIM)
-        raise ValueError(f"{name}: expected shape {want}, got {tuple(t.shape)}")
-    if t.numel() and (t.stride(2) != 1 or t.stride(0) % 8 or t.stride(1) % 8):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, others on cuda:{dev}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _dense(t: torch.Tensor, name: str, dtype, shape, dev: int) -> int:
+    """Address of a contiguous tensor of the given type, shape and device."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _refuse(t, name, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, dtype, shape, dev: int):
+    """(address, token stride, head stride) of a [T][H][128] tensor whose heads are dense
+    rows; token and head strides are free, in whole 16-byte units."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _refuse(t, name, dtype, shape, dev)
+    ts, hs, es = t.stride()
+    if (es != 1 or (ts | hs) & 7) and t.numel():
         raise ValueError(f"{name}: heads must be contiguous, at strides of whole 8 elements")
+    return t.data_ptr(), ts, hs
 
 
 def _no_overlap(t: torch.Tensor, name: str):
-    """Rows of an output written at the same time must be distinct memory."""
+    """Rows of an output, written at the same time, must be distinct memory."""
     T, H, _ = t.shape
     st, sh = t.stride(0), t.stride(1)
     if H > 1 and sh < HEAD_DIM or T > 1 and st < HEAD_DIM:
@@ -468,17 +507,21 @@ def _no_overlap(t: torch.Tensor, name: str):
         raise ValueError(f"{name}: rows overlap")
 
 
-def _view(q, k=None, v=None) -> B.ls_qkv_view:
-    s = B.ls_qkv_view()
-    s.q = q.data_ptr()
-    s.q_stride[0], s.q_stride[1] = q.stride(0), q.stride(1)
-    if k is not None:
-        s.k = k.data_ptr()
-        s.k_stride[0], s.k_stride[1] = k.stride(0), k.stride(1)
-    if v is not None:
-        s.v = v.data_ptr()
-        s.v_stride[0], s.v_stride[1] = v.stride(0), v.stride(1)
-    return s
+def _out_rows(t, like: torch.Tensor, name: str, shape, dev: int):
+    """An output of the stage: allocated dense, or the caller's rows."""
+    if t is None:
+        t = torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+        return t, (t.data_ptr(), shape[1] * HEAD_DIM, HEAD_DIM)
+    r = _rows(t, name, torch.bfloat16, shape, dev)
+    _no_overlap(t, name)
+    return t, r
+
+
+_NO_ROWS = (None, 0, 0)
+
+
+def _view(q, k=_NO_ROWS, v=_NO_ROWS) -> B.ls_qkv_view:
+    return B.ls_qkv_view(q[0], k[0], v[0], q[1], q[2], k[1], k[2], v[1], v[2])
 
 
 class Rotary:
@@ -499,6 +542,7 @@ class Rotary:
             raise ValueError("pair_axis is required with more than one axis")
         self.inv_freq, self.pair_axis, self.axes = inv_freq, pair_axis, axes
         self.rot_dim, self.interleaved = 2 * inv_freq.numel(), interleaved
+        self.device_index = inv_freq.get_device()
         self.struct = B.ls_rotary(inv_freq.data_ptr(),
                                   pair_axis.data_ptr() if pair_axis is not None else None,
                                   self.rot_dim, axes, int(interleaved))
@@ -510,38 +554,35 @@ class Rotary:
         return cls((float(base) ** (-2.0 * j / rot_dim)).to(device), **kw)
 
 
-def _norm_rope_args(q, k, positions, rotary, wq, wk, norm, eps, weight_offset):
-    """Checks shared by the calls of the stage; returns (T, Hq, Hkv, norm struct, rotary
-    struct, positions address)."""
+def _stage_args(q, k, positions, rotary, wq, wk, norm, eps, weight_offset):
+    """Checks shared by the calls of the stage; returns (device, T, Hq, Hkv, q rows, k rows,
+    norm struct, rotary struct, positions address)."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [T][H][128]")
+    dev = q.get_device()
     T, hq, _ = q.shape
     hkv = k.shape[1]
+    qr = _rows(q, "q", torch.bfloat16, (T, hq, HEAD_DIM), dev)
+    kr = _rows(k, "k", torch.bfloat16, (T, hkv, HEAD_DIM), dev)
     ns = None
     if norm:
-        dt = None
-        for w, n in ((wq, "wq"), (wk, "wk")):
-            if w is not None:
-                if w.dtype not in (torch.float32, torch.bfloat16) or w.dtype != (dt or w.dtype):
-                    raise ValueError("wq and wk must both be fp32 or both bf16")
-                dt = w.dtype
-                _check(w, n, dt, (HEAD_DIM,))
-        ns = B.ls_qk_norm(wq.data_ptr() if wq is not None else None,
-                          wk.data_ptr() if wk is not None else None,
-                          B.LS_BF16 if dt == torch.bfloat16 else B.LS_FP32, weight_offset, eps)
+        dt = torch.float32 if wq is None and wk is None else (wk if wq is None else wq).dtype
+        if dt is not torch.float32 and dt is not torch.bfloat16:
+            raise ValueError("wq and wk must both be fp32 or both bf16")
+        ns = B.ls_qk_norm(_dense(wq, "wq", dt, (HEAD_DIM,), dev) if wq is not None else None,
+                          _dense(wk, "wk", dt, (HEAD_DIM,), dev) if wk is not None else None,
+                          B.LS_FP32 if dt is torch.float32 else B.LS_BF16, weight_offset, eps)
     elif wq is not None or wk is not None:
         raise ValueError("norm weights without a norm")
-    _on(q.device, k, wq, wk, positions, rotary.inv_freq if rotary is not None else None)
-    pp = None
-    if rotary is not None:
-        if positions is None:
-            raise ValueError("positions are required with rotary")
-        if positions.dim() == 1 and rotary.axes == 1:
-            positions = positions[None]
-        _check(positions, "positions", torch.int32, (rotary.axes, T))
-        pp = positions.data_ptr()
-    return T, hq, hkv, ns, rotary.struct if rotary is not None else None, pp
-
-
-_BF16 = (torch.bfloat16,)
+    if rotary is None:
+        return dev, T, hq, hkv, qr, kr, ns, None, None
+    if positions is None:
+        raise ValueError("positions are required with rotary")
+    if rotary.device_index != dev:
+        raise ValueError("the rotary frequencies are on another device")
+    shape = (T,) if rotary.axes == 1 and positions.dim() == 1 else (rotary.axes, T)
+    return (dev, T, hq, hkv, qr, kr, ns, rotary.struct,
+            _dense(positions, "positions", torch.int32, shape, dev))
 
 
 def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None,
@@ -554,28 +595,20 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None,
     k / v [T][Hkv][128] bf16, any token and head strides (slices of a packed projection),
     positions int32 [axes][T].  Returns (q_out, k_out, v_out); the outputs are dense
     unless given (an output may be its input), v is copied into the replay's layout."""
-    _head_rows(q, "q", _BF16)
-    _head_rows(k, "k", _BF16, (q.shape[0], k.shape[1], HEAD_DIM))
-    T, hq, hkv, ns, rs, pp = _norm_rope_args(q, k, positions, rotary, wq, wk, norm, eps,
-                                             weight_offset)
+    dev, T, hq, hkv, qr, kr, ns, rs, pp = _stage_args(q, k, positions, rotary, wq, wk, norm, eps,
+                                                      weight_offset)
+    st = _dev_stream(dev, stream)
+    qs, ks = (T, hq, HEAD_DIM), (T, hkv, HEAD_DIM)
+    vr = vo = _NO_ROWS
     if v is not None:
-        _head_rows(v, "v", _BF16, (T, hkv, HEAD_DIM))
+        vr = _rows(v, "v", torch.bfloat16, ks, dev)
+        v_out, vo = _out_rows(v_out, q, "v_out", ks, dev)
     elif v_out is not None:
         raise ValueError("v_out without v")
-    outs = []
-    for x, o, n in ((q, q_out, "q_out"), (k, k_out, "k_out"), (v, v_out, "v_out")):
-        if x is None:
-            outs.append(None)
-            continue
-        if o is None:
-            o = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-        else:
-            _head_rows(o, n, _BF16, tuple(x.shape))
-            _no_overlap(o, n)
-        outs.append(o)
-    _on(q.device, v, *outs)
-    B.ls_qk_norm_rope_fwd(_view(q, k, v), T, hq, hkv, ns, rs, pp, _view(*outs), _stream(stream))
-    return tuple(outs)
+    q_out, qo = _out_rows(q_out, q, "q_out", qs, dev)
+    k_out, ko = _out_rows(k_out, q, "k_out", ks, dev)
+    B.ls_qk_norm_rope_fwd(_view(qr, kr, vr), T, hq, hkv, ns, rs, pp, _view(qo, ko, vo), st)
+    return q_out, k_out, v_out
 
 
 def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor | None,
@@ -591,53 +624,42 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor |
     dx_k, dx_v, dwq, dwk): bf16 gradients of the inputs (dense unless given, e.g. as
     slices of the packed projection's gradient) and fp32 [128] weight gradients, which
     accumulate adds into; a weight gradient is returned for each weight given."""
-    _head_rows(q, "q", _BF16)
-    _head_rows(k, "k", _BF16, (q.shape[0], k.shape[1], HEAD_DIM))
-    T, hq, hkv, ns, rs, pp = _norm_rope_args(q, k, positions, rotary, wq, wk, norm, eps,
-                                             weight_offset)
-    dt = (dq.dtype,)
-    if dq.dtype not in (torch.float32, torch.bfloat16):
+    dev, T, hq, hkv, qr, kr, ns, rs, pp = _stage_args(q, k, positions, rotary, wq, wk, norm, eps,
+                                                      weight_offset)
+    st = _dev_stream(dev, stream)
+    dt = dq.dtype
+    if dt is not torch.float32 and dt is not torch.bfloat16:
         raise ValueError("dq must be fp32 or bf16")
-    _head_rows(dq, "dq", dt, tuple(q.shape))
-    _head_rows(dk, "dk", dt, tuple(k.shape))
+    qs, ks = (T, hq, HEAD_DIM), (T, hkv, HEAD_DIM)
+    gq, gk, gv, ov = _rows(dq, "dq", dt, qs, dev), _rows(dk, "dk", dt, ks, dev), _NO_ROWS, _NO_ROWS
     if dv is not None:
-        _head_rows(dv, "dv", dt, tuple(k.shape))
+        gv = _rows(dv, "dv", dt, ks, dev)
+        dx_v, ov = _out_rows(dx_v, q, "dx_v", ks, dev)
     elif dx_v is not None:
         raise ValueError("dx_v without dv")
-    dev = q.device
-    outs = []
-    for g, o, n in ((dq, dx_q, "dx_q"), (dk, dx_k, "dx_k"), (dv, dx_v, "dx_v")):
-        if g is None:
-            outs.append(None)
-            continue
-        if o is None:
-            o = torch.empty(g.shape, dtype=torch.bfloat16, device=dev)
-        else:
-            _head_rows(o, n, _BF16, tuple(g.shape))
-            _no_overlap(o, n)
-        outs.append(o)
+    dx_q, oq = _out_rows(dx_q, q, "dx_q", qs, dev)
+    dx_k, ok = _out_rows(dx_k, q, "dx_k", ks, dev)
     if not norm and (dwq is not None or dwk is not None):
         raise ValueError("weight gradients without a norm")
     if accumulate and ((wq is not None and dwq is None) or (wk is not None and dwk is None)):
         raise ValueError("accumulate needs the weight gradients to add into")
     if wq is not None and dwq is None:
-        dwq = torch.empty(HEAD_DIM, dtype=torch.float32, device=dev)
+        dwq = torch.empty(HEAD_DIM, dtype=torch.float32, device=q.device)
     if wk is not None and dwk is None:
-        dwk = torch.empty(HEAD_DIM, dtype=torch.float32, device=dev)
-    for w, n in ((dwq, "dwq"), (dwk, "dwk")):
-        if w is not None:
-            _check(w, n, torch.float32, (HEAD_DIM,))
-    _on(dev, dq, dk, dv, dwq, dwk, *outs)
-    ws, nbytes = None, 0
-    if dwq is not None or dwk is not None:
-        ws = workspace(B.ls_qk_norm_rope_bwd_workspace(T), dev, "qk_norm")
-        nbytes = ws.numel()
-    B.ls_qk_norm_rope_bwd(_view(q, k), T, hq, hkv, ns, rs, pp, _view(dq, dk, dv),
-                          B.LS_FP32 if dq.dtype == torch.float32 else B.LS_BF16, int(accumulate),
-                          _view(*outs), dwq.data_ptr() if dwq is not None else None,
-                          dwk.data_ptr() if dwk is not None else None,
-                          ws.data_ptr() if ws is not None else None, nbytes, _stream(stream))
-    return (*outs, dwq, dwk)
+        dwk = torch.empty(HEAD_DIM, dtype=torch.float32, device=q.device)
+    pq = pk = ws = None
+    nbytes = 0
+    if dwq is not None:
+        pq = _dense(dwq, "dwq", torch.float32, (HEAD_DIM,), dev)
+    if dwk is not None:
+        pk = _dense(dwk, "dwk", torch.float32, (HEAD_DIM,), dev)
+    if pq is not None or pk is not None:
+        buf = _call_workspace(B.ls_qk_norm_rope_bwd_workspace(T), q, "qk_norm", st)
+        ws, nbytes = buf.data_ptr(), buf.numel()
+    B.ls_qk_norm_rope_bwd(_view(qr, kr), T, hq, hkv, ns, rs, pp, _view(gq, gk, gv),
+                          B.LS_FP32 if dt is torch.float32 else B.LS_BF16, int(accumulate),
+                          _view(oq, ok, ov), pq, pk, ws, nbytes, st)
+    return dx_q, dx_k, dx_v, dwq, dwk
 
 
 class PagePool:
@@ -651,6 +673,8 @@ class PagePool:
         _check_pool(v_pool, "v_pool", (n, hkv, ps, HEAD_DIM))
         self.k_pool, self.v_pool = k_pool, v_pool
         self.num_pages, self.num_kv_heads, self.page_size = n, hkv, ps
+        # -1: pinned host memory, read and written there from any device
+        self.device_indices = {k_pool.get_device(), v_pool.get_device()} - {-1}
         self.struct = B.ls_page_pool(k_pool.data_ptr(), v_pool.data_ptr(), n, ps, hkv, HEAD_DIM)
 
     @classmethod
@@ -673,20 +697,15 @@ def qk_norm_rope_append(pool: PagePool, q: torch.Tensor, k: torch.Tensor, v: tor
     """qk_norm_rope_fwd with keys and values written into `pool` at slots[t] = page *
     page_size + offset (int32 [T]; negative: a padding token, nothing of it is written).
     Returns q_out."""
-    _head_rows(q, "q", _BF16)
-    _head_rows(k, "k", _BF16, (q.shape[0], pool.num_kv_heads, HEAD_DIM))
-    _head_rows(v, "v", _BF16, tuple(k.shape))
-    T, hq, _, ns, rs, pp = _norm_rope_args(q, k, positions, rotary, wq, wk, norm, eps,
-                                           weight_offset)
-    _check(slots, "slots", torch.int32, (T,))
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    else:
-        _head_rows(q_out, "q_out", _BF16, tuple(q.shape))
-        _no_overlap(q_out, "q_out")
-    _on(q.device, v, slots, q_out, *(p for p in (pool.k_pool, pool.v_pool) if p.is_cuda))
-    B.ls_qk_norm_rope_append(pool.struct, _view(q, k, v), T, hq, ns, rs, pp, slots.data_ptr(),
-                             _view(q_out), _stream(stream))
+    dev, T, hq, hkv, qr, kr, ns, rs, pp = _stage_args(q, k, positions, rotary, wq, wk, norm, eps,
+                                                      weight_offset)
+    st = _dev_stream(dev, stream)
+    if hkv != pool.num_kv_heads or pool.device_indices - {dev}:
+        raise ValueError("the pool has other key heads or is on another device")
+    vr = _rows(v, "v", torch.bfloat16, (T, hkv, HEAD_DIM), dev)
+    sp = _dense(slots, "slots", torch.int32, (T,), dev)
+    q_out, qo = _out_rows(q_out, q, "q_out", (T, hq, HEAD_DIM), dev)
+    B.ls_qk_norm_rope_append(pool.struct, _view(qr, kr, vr), T, hq, ns, rs, pp, sp, _view(qo), st)
     return q_out
 
 
@@ -711,7 +730,10 @@ class PageAllocator:
                 raise ValueError("the allocator's tensors must be on one device")
         self.block_table, self.lens, self.free_list, self.used = block_table, lens, free_list, used
         self.page_size = page_size
-        self.num_pages = free_list.numel() if num_pages is None else num_pages
+        self.members, self.max_blocks = block_table.shape
+        self.num_free = free_list.numel()
+        self.num_pages = self.num_free if num_pages is None else num_pages
+        self.device_index = block_table.get_device()
 
     @classmethod
     def empty(cls, members: int, max_blocks: int, num_pages: int, page_size: int,
@@ -721,14 +743,6 @@ class PageAllocator:
         return cls(torch.zeros((members, max_blocks), **z), torch.zeros(members, **z),
                    torch.arange(num_pages, **z), torch.zeros(1, **z), page_size)
 
-    @property
-    def members(self) -> int:
-        return self.block_table.shape[0]
-
-    @property
-    def device(self):
-        return self.block_table.device
-
 
 def extend_pages(alloc: PageAllocator, add: torch.Tensor, pos0: int, slots: torch.Tensor,
                  positions: torch.Tensor | None = None, lens_out: torch.Tensor | None = None,
@@ -737,26 +751,20 @@ def extend_pages(alloc: PageAllocator, add: torch.Tensor, pos0: int, slots: torc
     the last token) and positions int32 [axes][capacity] (pos0 + index within the
     response), enters new pages into the table and advances alloc.lens and alloc.used (or
     writes them to lens_out / used_out).  See ls_extend_pages for what is refused."""
-    M, nb = alloc.block_table.shape
-    _check(add, "add", torch.int32, (M,))
-    _check(slots, "slots", torch.int32, (slots.numel(),))
-    cap = slots.numel()
-    axes = 1
+    M, dev, i32 = alloc.members, alloc.device_index, torch.int32
+    st = _dev_stream(dev, stream)
+    cap = slots.shape[0] if slots.dim() == 1 else -1
+    sp = _dense(slots, "slots", i32, (cap,), dev)
+    axes, pp = 1, None
     if positions is not None:
-        if positions.dim() != 2:
-            raise ValueError("positions must be [axes][capacity]")
-        axes = positions.shape[0]
-        _check(positions, "positions", torch.int32, (axes, cap))
-    lens_out = alloc.lens if lens_out is None else lens_out
-    used_out = alloc.used if used_out is None else used_out
-    _check(lens_out, "lens_out", torch.int32, (M,))
-    _check(used_out, "used_out", torch.int32, (1,))
-    _on(alloc.device, add, slots, positions, lens_out, used_out)
-    B.ls_extend_pages(alloc.block_table.data_ptr(), M, nb, alloc.page_size, alloc.num_pages,
-                      alloc.lens.data_ptr(), add.data_ptr(), alloc.free_list.data_ptr(),
-                      alloc.free_list.numel(), alloc.used.data_ptr(), pos0, axes, cap,
-                      slots.data_ptr(), positions.data_ptr() if positions is not None else None,
-                      lens_out.data_ptr(), used_out.data_ptr(), _stream(stream))
+        axes = positions.shape[0] if positions.dim() == 2 else -1
+        pp = _dense(positions, "positions", i32, (axes, cap), dev)
+    lens, used = alloc.lens.data_ptr(), alloc.used.data_ptr()
+    B.ls_extend_pages(alloc.block_table.data_ptr(), M, alloc.max_blocks, alloc.page_size,
+                      alloc.num_pages, lens, _dense(add, "add", i32, (M,), dev),
+                      alloc.free_list.data_ptr(), alloc.num_free, used, pos0, axes, cap, sp, pp,
+                      lens if lens_out is None else _dense(lens_out, "lens_out", i32, (M,), dev),
+                      used if used_out is None else _dense(used_out, "used_out", i32, (1,), dev), st)
 
 
 class ResponseCache:
@@ -771,6 +779,10 @@ class ResponseCache:
         if lens.device != block_table.device:
             raise ValueError("block_table and lens must be on one device")
         self.pool, self.block_table, self.lens = pool, block_table, lens
+        self.members = block_table.shape[0]
+        self.device_index = block_table.get_device()
+        if pool.device_indices - {self.device_index}:
+            raise ValueError("the pool is on another device")
         self.struct = B.ls_resp_cache(pool.struct, block_table.data_ptr(), lens.data_ptr(),
                                       block_table.shape[0], block_table.shape[1])
 
@@ -780,27 +792,34 @@ class ResponseCache:
             raise ValueError("the pool does not hold the allocator's pages")
         return cls(pool, alloc.block_table, alloc.lens)
 
-    @property
-    def members(self) -> int:
-        return self.block_table.shape[0]
-
 
 def decode_attn(cache: PagedKVCache, resp: ResponseCache, q: torch.Tensor, softmax_scale: float,
                 o: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None):
     """Attention of a decode step: q [members][n][Hq][128], the n newest tokens of every
     member (already appended to its pages), over the shared prompt and the member's own
     response.  Returns (o, lse)."""
-    M, n, hq, _ = q.shape
-    _check(q, "q", torch.bfloat16, (resp.members, n, hq, HEAD_DIM))
+    if q.dim() != 4:
+        raise ValueError("q must be [members][n][Hq][128]")
+    _, n, hq, _ = shape = q.shape
+    M, dev = resp.members, resp.device_index
+    st = _dev_stream(dev, stream)
+    if cache.page_table.get_device() != dev:
+        raise ValueError("the prompt's page table is on another device")
+    qp = _dense(q, "q", torch.bfloat16, (M, n, hq, HEAD_DIM), dev)
     if o is None:
-        o = torch.empty_like(q)
+        o = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
     if lse is None:
         lse = torch.empty((M, n, hq), dtype=torch.float32, device=q.device)
-    _check(o, "o", torch.bfloat16, q.shape)
-    _check(lse, "lse", torch.float32, (M, n, hq))
-    _on(q.device, cache.page_table, resp.block_table, o, lse)
-    nbytes = B.ls_decode_attn_workspace(cache.struct, resp.struct, n, hq)
-    ws = workspace(nbytes, q.device, "decode")
-    B.ls_decode_attn(cache.struct, resp.struct, q.data_ptr(), n, hq, softmax_scale, o.data_ptr(),
-                     lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    op = _dense(o, "o", torch.bfloat16, shape, dev)
+    lp = _dense(lse, "lse", torch.float32, (M, n, hq), dev)
+    ws = _call_workspace(0, q, "decode", st)
+    args = (cache.struct, resp.struct, qp, n, hq, softmax_scale, op, lp)
+    try:
+        B.ls_decode_attn(*args, ws.data_ptr(), ws.numel(), st)
+    except B.LongstrawError as e:  # nothing was launched: the workspace has to grow
+        if e.status != B.LS_ERR_WORKSPACE:
+            raise
+        ws = _call_workspace(B.ls_decode_attn_workspace(cache.struct, resp.struct, n, hq), q,
+                             "decode", st)
+        B.ls_decode_attn(*args, ws.data_ptr(), ws.numel(), st)
     return o, lse

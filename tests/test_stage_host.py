@@ -24,12 +24,8 @@ def lib():
 
 
 def view(**kw):
-    v = B.ls_qkv_view(q=A, k=A, v=A)
-    for n in ("q_stride", "k_stride", "v_stride"):
-        getattr(v, n)[0], getattr(v, n)[1] = kw.pop(n, (4096, 128))
-    for n, x in kw.items():
-        setattr(v, n, x)
-    return v
+    s = {f"{n}_{d}": x for n in "qkv" for d, x in zip(("ts", "hs"), kw.pop(f"{n}_stride", (4096, 128)))}
+    return B.ls_qkv_view(**{**dict(q=A, k=A, v=A), **s, **kw})
 
 
 def norm(**kw):
