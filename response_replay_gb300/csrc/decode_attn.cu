@@ -214,6 +214,8 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int32_t cta = blockIdx.x, col = cta / a.rts, rt = cta - col * a.rts;
 
+  // the combine may be launched: its blocks wait for this grid before they read from it
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // ---- response tiles before each member, summed by the whole CTA (scratch: the ring,
   // which no copy has touched yet)
   int32_t p0, p1, r0, r1;
@@ -520,9 +522,15 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     uint32_t kc = 0, oc = 0;
     bool ok = true;
     while (ok && walk.next(&s)) {
-      if (s.count <= t) continue;
-      // rows of the segment, and the first key this row does not see
       const int32_t rows = seg_rows(a, s, rt);
+      const int64_t prow =
+          (s.resp ? resp_row0(a, prompt_rows, s.item, cta, t) : prompt_row0(a, s.item, col, rt, t)) +
+          row;
+      if (s.count <= t) {  // a segment of one tile: the odd half says so
+        if (row < rows) a.part_lse[prow] = -INFINITY;
+        continue;
+      }
+      // the first key this row does not see
       const int32_t end = s.resp ? min(s.len, s.len - a.n + 1 + row / a.g) : s.len;
       const bool idle = quad * 32 >= rows;  // the whole warp is padding
       float m = -INFINITY, l = 0.f, lcomp = 0.f;
@@ -622,9 +630,6 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
         tc_fence_after();
         const float lt = l + lcomp;
         const float inv = lt == 0.f ? 0.f : 1.f / lt;  // a row that sees no key here
-        const int64_t prow =
-            (s.resp ? resp_row0(a, prompt_rows, s.item, cta, t) : prompt_row0(a, s.item, col, rt, t)) +
-            row;
         float* po = a.part_o + prow * kD;
 #pragma unroll 1
         for (int c0 = 0; c0 < 128; c0 += 32) {
@@ -654,19 +659,27 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
   }
 }
 
-// Merge a row's partials: lse = log2 sum 2^lse_k, o = sum 2^(lse_k - lse) o_k, in the
-// order of the sequence's cut.  Block = (member, KV head, group of kCombineRows rows); the
-// block lists the partials of its (member, KV head) once, then each warp takes rows.
+// Merge a row's partials: lse = log2 sum 2^lse_k, o = sum 2^(lse_k - lse) o_k, in a fixed
+// order.  A block per row (the 76 partials of a row of a 2,097,152-token prompt are read by
+// eight warps at once: one warp a row took 36 us for 192 rows).  The row's partials lie
+// in the columns and CTAs whose parts of the sequence meet the row's keys; a thread looks
+// at one column and one CTA.  That much needs only the lengths, so the launch overlaps the
+// main kernel's end and waits for it then.
 constexpr int kCombineThreads = 256;
-constexpr int kCombineRows = kCombineThreads / 32;
-constexpr int kMaxParts = 1024;
+constexpr int kCombineWarps = kCombineThreads / 32;
+constexpr int kMaxParts = 1024;  // 2 halves of 256 columns and 256 CTAs at most
 
-__global__ void __launch_bounds__(kCombineThreads) decode_combine(const LsDecodeArgs a) {
-  __shared__ int64_t rows0[kMaxParts];
-  __shared__ int32_t wsum[kCombineThreads / 32], wpre[kCombineThreads / 32];
-  __shared__ int32_t wcnt[kCombineThreads / 32];
+__global__ void __launch_bounds__(kCombineThreads)
+decode_combine(const __grid_constant__ LsDecodeArgs a) {
+  __shared__ float wt[kMaxParts];
+  __shared__ float4 acc[kCombineWarps][32];
+  __shared__ int32_t sums[2][kCombineWarps];
+  __shared__ float red[kCombineWarps];
+  __shared__ uint16_t from[2][kCombineThreads];  // columns, CTAs with partials of the row
+  __shared__ int32_t counts[2][kCombineWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int m = blockIdx.x / a.hkv, kvh = blockIdx.x - m * a.hkv;
+  const int32_t token = blockIdx.x / a.hq, head = blockIdx.x - token * a.hq;
+  const int32_t m = token / a.n, kvh = head / a.g;
   const int32_t len = __ldg(a.lens + m);
   if (len < 0) return;  // a member out of use: its rows stay as they were
   const int32_t nt = tiles_of(clamp_len(a, len));
@@ -676,107 +689,106 @@ __global__ void __launch_bounds__(kCombineThreads) decode_combine(const LsDecode
     tot += x;
     if (i < m) pre += x;
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    tot += __shfl_xor_sync(0xffffffffu, tot, o);
-    pre += __shfl_xor_sync(0xffffffffu, pre, o);
-  }
+  tot = __reduce_add_sync(0xffffffffu, tot);
+  pre = __reduce_add_sync(0xffffffffu, pre);
   if (lane == 0) {
-    wsum[warp] = tot;
-    wpre[warp] = pre;
+    sums[0][warp] = tot;
+    sums[1][warp] = pre;
   }
   __syncthreads();
   tot = pre = 0;
 #pragma unroll
-  for (int i = 0; i < kCombineThreads / 32; ++i) {
-    tot += wsum[i];
-    pre += wpre[i];
+  for (int i = 0; i < kCombineWarps; ++i) {
+    tot += sums[0][i];
+    pre += sums[1][i];
   }
   const Cut cut(a, tot * a.hkv);
-  const int32_t pb = kvh * a.nt, pe = pb + a.nt;
-  const int32_t rb = pre * a.hkv + kvh * nt, re = rb + nt;
-  const int64_t prompt_rows = prompt_rows_of(a);
-  const int ctas = a.cols * a.rts;
-  // a member's rows may straddle two row tiles: the list holds row 0 of row tile 0 for the
-  // prompt's partials, and a row adds its own place below
-  int count = 0, prompts = 0;
-  for (int part = 0; part < 2; ++part) {
-    const int n_c = part == 0 ? a.cols : ctas;
-    for (int c0 = 0; c0 < n_c; c0 += kCombineThreads) {
-      const int c = c0 + tid;
-      int halves = 0;
-      if (c < n_c) {
-        int32_t b, e, ob, oe;
-        if (part == 0) {
-          cut.prompt(c, &b, &e);
-          ob = b > pb ? b : pb;
-          oe = e < pe ? e : pe;
-        } else {
-          cut.resp(c / a.rts, c % a.rts, &b, &e);
-          ob = b > rb ? b : rb;
-          oe = e < re ? e : re;
-        }
-        halves = oe - ob >= 2 ? 2 : (oe > ob ? 1 : 0);
-      }
-      // ordered append: inclusive sum over the block
-      int sum = halves;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += v;
-      }
-      if (lane == 31) wcnt[warp] = sum;
-      __syncthreads();
-      int at = count + sum - halves, all = 0;
-#pragma unroll
-      for (int i = 0; i < kCombineThreads / 32; ++i) {
-        if (i < warp) at += wcnt[i];
-        all += wcnt[i];
-      }
-      for (int t = 0; t < halves; ++t)
-        rows0[at + t] = part == 0 ? prompt_row0(a, kvh, c, 0, t)
-                                  : resp_row0(a, prompt_rows, m * a.hkv + kvh, c, t);
-      count += all;
-      __syncthreads();
+  bool hit[2] = {false, false};
+  {
+    const int32_t pb = kvh * a.nt, rb = pre * a.hkv + kvh * nt;
+    int32_t b, e;
+    if (tid < a.cols) {
+      cut.prompt(tid, &b, &e);
+      hit[0] = max(b, pb) < min(e, pb + a.nt);
     }
-    if (part == 0) prompts = count;
+    if (tid < a.cols * a.rts) {
+      cut.resp(tid / a.rts, tid % a.rts, &b, &e);
+      hit[1] = max(b, rb) < min(e, rb + nt);
+    }
   }
-  const int r = blockIdx.y * kCombineRows + warp;  // row of the member: token, head
-  if (r >= a.n * a.g) return;
-  const int32_t token = m * a.n + r / a.g, grow = m * a.n * a.g + r;
-  const int64_t prompt_off = (int64_t)(grow / kTile) * 2 * kTile + grow % kTile;
-  auto part_row = [&](int k) { return rows0[k] + (k < prompts ? prompt_off : r); };
+  uint32_t in_warp[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    in_warp[i] = __ballot_sync(0xffffffffu, hit[i]);
+    if (lane == 0) counts[i][warp] = __popc(in_warp[i]);
+  }
+  __syncthreads();
+  int32_t all[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    int32_t at = __popc(in_warp[i] & ((1u << lane) - 1));
+#pragma unroll
+    for (int v = 0; v < kCombineWarps; ++v) {
+      if (v < warp) at += counts[i][v];
+      all[i] += counts[i][v];
+    }
+    if (hit[i]) from[i][at] = (uint16_t)tid;
+  }
+  __syncthreads();
+  const int32_t np = 2 * all[0], count = np + 2 * all[1];
+  // row of all rows (token, head of the group) against the prompt; row of the member's own
+  const int32_t grow = token * a.g + head % a.g, mrow = grow - m * a.n * a.g;
+  const int64_t prompt0 = prompt_row0(a, kvh, 0, grow / kTile, 0) + grow % kTile;
+  const int64_t resp0 = resp_row0(a, prompt_rows_of(a), m * a.hkv + kvh, 0, 0) + mrow;
+  auto part_row = [&](int k) {
+    if (k < np) return prompt0 + ((int64_t)from[0][k >> 1] * a.rts * 2 + (k & 1)) * kTile;
+    k -= np;
+    return resp0 + ((int64_t)from[1][k >> 1] * 2 + (k & 1)) * (a.n * a.g);
+  };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float mx = -INFINITY;
-  for (int k = lane; k < count; k += 32) mx = fmaxf(mx, a.part_lse[part_row(k)]);
+  for (int k = tid; k < count; k += kCombineThreads) {
+    const float v = __ldcg(a.part_lse + part_row(k));
+    wt[k] = v;
+    mx = fmaxf(mx, v);
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (lane == 0) red[warp] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kCombineWarps; ++i) mx = fmaxf(mx, red[i]);
   const float msub = mx == -INFINITY ? 0.f : mx;
   float sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 < count; k0 += 32) {
-    const int k = k0 + lane;
-    const int64_t mine = k < count ? part_row(k) : 0;
-    const float w = k < count ? exp2f(a.part_lse[mine] - msub) : 0.f;
-    const int n = count - k0 < 32 ? count - k0 : 32;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const int64_t ri = __shfl_sync(0xffffffffu, mine, i);
-      const float4 v = *(reinterpret_cast<const float4*>(a.part_o + ri * kD) + lane);
-      sum += wi;
-      acc.x = fmaf(wi, v.x, acc.x);
-      acc.y = fmaf(wi, v.y, acc.y);
-      acc.z = fmaf(wi, v.z, acc.z);
-      acc.w = fmaf(wi, v.w, acc.w);
-    }
+  for (int k = warp; k < count; k += kCombineWarps) {
+    const float w = exp2f(wt[k] - msub);
+    // a half that had no tile left no o
+    const float4 v = w == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                              : __ldcg(reinterpret_cast<const float4*>(a.part_o + part_row(k) * kD) + lane);
+    sum += w;
+    s.x = fmaf(w, v.x, s.x);
+    s.y = fmaf(w, v.y, s.y);
+    s.z = fmaf(w, v.z, s.z);
+    s.w = fmaf(w, v.w, s.w);
+  }
+  acc[warp][lane] = s;
+  __syncthreads();  // red has been read
+  if (lane == 0) red[warp] = sum;
+  __syncthreads();
+  if (tid >= kD) return;
+  sum = 0.f;
+  float o = 0.f;
+#pragma unroll
+  for (int i = 0; i < kCombineWarps; ++i) {
+    sum += red[i];
+    o += reinterpret_cast<const float*>(acc[i])[tid];
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key at all: o = 0, lse = -inf
-  const int64_t orow = (int64_t)token * a.hq + kvh * a.g + r % a.g;
-  uint2 w;
-  w.x = pack_bf16(acc.x * inv, acc.y * inv);
-  w.y = pack_bf16(acc.z * inv, acc.w * inv);
-  *(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + orow * kD) + lane) = w;
-  if (lane == 0) a.lse[orow] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+  const int64_t row = (int64_t)token * a.hq + head;
+  static_cast<__nv_bfloat16*>(a.o)[row * kD + tid] = __float2bfloat16_rn(o * inv);
+  if (tid == 0) a.lse[row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
 }  // namespace
@@ -804,9 +816,16 @@ cudaError_t ls_launch_decode_attn(const LsDecodeArgs& a, cudaStream_t st) {
   decode_attn_kernel<<<a.cols * a.rts, kThreads, kSmemBytes, st>>>(tm, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   ls_note_launch();
-  decode_combine<<<dim3((unsigned)(a.M * a.hkv), (unsigned)((a.n * a.g + kCombineRows - 1) / kCombineRows)),
-                   kCombineThreads, 0, st>>>(a);
-  e = cudaGetLastError();
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.M * a.n * a.hq));
+  cfg.blockDim = dim3(kCombineThreads);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, decode_combine, a);
   if (e == cudaSuccess) ls_note_launch();
   return e;
 }
