@@ -19,13 +19,16 @@
 // device (a captured graph follows them): every CTA sums them when it starts.
 //
 // CTA (one per SM, 12 warps):
-//   warp 0      TMA producer: the segments' K and V tiles, page by page, into a 5-stage ring.
+//   warps 0, 3  TMA producers of the segments' K and V tiles, page by page, each into a ring
+//               of 3 tiles (one thread for both was the bound with several row tiles: about
+//               2,000 clocks a tile); warp 3 also loads the segments' Q, and clears the V rows
+//               behind a sequence's end (stale page contents, even NaN, would survive a zero
+//               weight) before such a tile is handed over.
 //   warps 1, 2  MMA issuers: the segment's even and odd tiles.  S_t = Q K^T into tensor
 //               memory, O_t += P_t V with P_t read from tensor memory; the two tile
-//               sequences are independent, so one's MMAs run under the other's softmax.
-//   warp 3      loads the segments' Q (two buffers), and clears the V rows behind a
-//               sequence's end (stale page contents, even NaN, would survive a zero weight)
-//               before such a tile is handed over.
+//               sequences are independent, so one's MMAs can run under the other's softmax
+//               (left alone they tend to fall into step; made to take turns they cost more
+//               between segments than it gave: 280 against 267 us at 64 members).
 //   warps 4-7   softmax of the even tiles, warps 8-11 of the odd ones, one row a thread;
 //               warps whose rows are all padding only keep the barriers going.
 // Tensor memory (512 columns): S_0 [0,128) S_1 [128,256) O_0 [256,384) O_1 [384,512).
@@ -42,18 +45,23 @@ using namespace umma;
 
 constexpr int kD = 128;
 constexpr int kTile = 128;
-constexpr int kStages = 5;
+constexpr int kStages = 6;
 constexpr int kThreads = 384;
-// 168 registers a thread at launch (64,512); warpgroup 0 drops to 96, the two softmax
-// warpgroups rise to 200: 128 x 96 + 256 x 200 = 63,488.
-constexpr int kRegsLaunch = 168, kRegsControl = 96, kRegsSoftmax = 200;
+// 168 registers a thread at launch (64,512); warpgroup 0 drops to 112, the two softmax
+// warpgroups rise to 192: 128 x 112 + 256 x 192 = 63,488.
+constexpr int kRegsLaunch = 168, kRegsControl = 112, kRegsSoftmax = 192;
 static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
 constexpr uint32_t kTileBytes = kTile * kD * 2;
 constexpr uint32_t kHalfBytes = kTileBytes / 2;
-constexpr uint32_t kOffQ = 0;  // two buffers
-constexpr uint32_t kOffRing = 2 * kTileBytes;
+constexpr uint32_t kOffQ = 0;
+constexpr uint32_t kOffRing = kTileBytes;
+// A segment of up to 64 query rows takes half of the Q tile, by turns, so that the next
+// segment's rows can be there before the last one is done.  Its MMAs still read 128 rows,
+// the other half's or the ring's bytes among them: rows that nothing looks at.
+constexpr int kHalfRows = kTile / 2;
 constexpr uint32_t kOffBar = kOffRing + kStages * kTileBytes;
 constexpr uint32_t kSmemBytes = kOffBar + 512 + 1024;
+constexpr int kMaxBoxes = kTile / 16;  // a tile's pages at the smallest page size
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;
 
@@ -86,6 +94,23 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// 16 consecutive 32-bit columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void reg_fence16(uint32_t* r) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
 
 __device__ __forceinline__ uint32_t bar_addr(uint32_t base, int i) { return base + kOffBar + 8 * i; }
@@ -146,7 +171,6 @@ struct Walk {
   __device__ __forceinline__ Walk(const LsDecodeArgs& a_, const volatile int32_t* start, int32_t p0,
                                   int32_t p1, int32_t r0, int32_t r1)
       : a(a_), p(p0), p_end(p1), r(r0), r_end(r1), m(start[0]), off(start[1]) {}
-  __device__ __forceinline__ bool done() const { return p >= p_end && r >= r_end; }
   __device__ __forceinline__ bool next(Seg* s) {
     if (p < p_end) {
       const int32_t h = p / a.nt, first = p - h * a.nt;
@@ -186,6 +210,67 @@ struct Walk {
 __device__ __forceinline__ int32_t seg_rows(const LsDecodeArgs& a, const Seg& s, int32_t rt) {
   return s.resp ? a.n * a.g : min(a.M * a.n * a.g - rt * kTile, kTile);
 }
+
+__device__ __forceinline__ bool whole_q(const LsDecodeArgs& a, const Seg& s, int32_t rt) {
+  return seg_rows(a, s, rt) > kHalfRows;
+}
+__device__ __forceinline__ uint32_t q_offset(bool whole, uint32_t seg) {
+  return kOffQ + (whole ? 0u : (seg & 1) * kHalfRows * 128u);
+}
+
+// The loads of one ring (K or V) of a CTA, issued by one thread.  A tile's pages are looked
+// up while the last tile's loads are under way.  Whole-tile boxes (pages of 128 rows and
+// more) come with both 64-dim halves in one copy; smaller pages take two copies a page.
+struct Loader {
+  const void* map;              // of the segment's source
+  const int32_t* table;
+  int32_t len, key0, boxes, box_rows, ps_log2, pages, hkv, kvh, pool_rows;
+  int32_t page[kMaxBoxes];
+
+  __device__ __forceinline__ void open(const LsDecodeArgs& a, const Seg& s, const void* prompt_map,
+                                       const void* resp_map) {
+    map = s.resp ? resp_map : prompt_map;
+    table = s.resp ? a.blocks + (int64_t)s.m * a.max_blocks : a.page_table;
+    ps_log2 = s.resp ? a.r_ps_log2 : a.ps_log2;
+    pages = s.resp ? a.r_num_pages : a.num_pages;
+    box_rows = min(1 << ps_log2, kTile);
+    boxes = kTile / box_rows;
+    pool_rows = (pages * a.hkv) << ps_log2;
+    hkv = a.hkv;
+    kvh = s.kvh;
+    len = s.len;
+    key0 = s.key0;
+    look_up();
+  }
+  __device__ __forceinline__ void look_up() {
+#pragma unroll
+    for (int x = 0; x < kMaxBoxes; ++x)
+      if (x < boxes && key0 + x * box_rows < len) page[x] = __ldg(table + ((key0 + x * box_rows) >> ps_log2));
+  }
+  // one tile to `dst`, counted on barrier `bar`; then the next tile's pages
+  __device__ __forceinline__ void load(uint32_t dst, uint32_t bar, bool more, uint32_t* err) {
+    mbar_expect_tx(bar, kTileBytes);
+#pragma unroll
+    for (int x = 0; x < kMaxBoxes; ++x) {
+      if (x >= boxes) break;
+      int32_t y = pool_rows;  // out of bounds: zero fill
+      if (key0 + x * box_rows < len) {
+        if ((uint32_t)page[x] < (uint32_t)pages)
+          y = ((page[x] * hkv + kvh) << ps_log2) + ((key0 + x * box_rows) & ((1 << ps_log2) - 1));
+        else
+          ls_report(err, LS_DEVERR_CHECK);
+      }
+      if (boxes == 1) {
+        tma_load_3d(dst, map, 0, y, 0, bar);
+      } else {
+        tma_load_2d(dst + x * box_rows * 128, map, 0, y, bar);
+        tma_load_2d(dst + kHalfBytes + x * box_rows * 128, map, 64, y, bar);
+      }
+    }
+    key0 += kTile;
+    if (more) look_up();
+  }
+};
 
 // Rows of a partial: prompt partials first, then the responses'.  (item + CTA in walk
 // order) numbers a CTA's segments uniquely: from one segment to the next of the whole
@@ -301,89 +386,66 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     ls_report(a.err, LS_DEVERR_TIMEOUT);
     *abort_flag = 1;
   };
+  // The loading warps do not leave while loads into this CTA's shared memory may still be
+  // in flight: they wait for the last fill of each of their stages.
+  auto drain = [&](uint32_t filled, uint32_t last_t, uint32_t full_phase) {
+    for (uint32_t st = 0; st < kStages; ++st) {
+      const uint32_t full = kStages * ((last_t >> st) & 1) + st;
+      if ((filled >> st) & 1)
+        mbar_wait(bar_addr(sbase, B_KV_FULL + full), ((full_phase >> full) & 1) ^ 1);
+    }
+  };
   Walk walk(a, start, p0, p1, r0, r1);
   Seg s;
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
     if (warp == 0) {
-      // ---------------------------------------------------------- TMA producer
+      // ---------------------------------------------------------- K loads
       if (lane == 0) {
         tma_prefetch_desc(&tm.kp);
-        tma_prefetch_desc(&tm.vp);
         tma_prefetch_desc(&tm.kr);
-        tma_prefetch_desc(&tm.vr);
         // per FULL barrier: parity of its next fill; per stage: issuer of its last one
         uint32_t full_phase = 0, last_t = 0, filled = 0;
-        RingPos<kStages> ring;
+        RingPos<kStages / 2> ring;
+        Loader ld;
         bool ok = true;
         while (ok && walk.next(&s)) {
-          const int ps_log2 = s.resp ? a.r_ps_log2 : a.ps_log2;
-          const int32_t ps = 1 << ps_log2;
-          const int32_t box_rows = ps < kTile ? ps : kTile;
-          const int32_t pages = s.resp ? a.r_num_pages : a.num_pages;
-          const int32_t pool_rows = pages * a.hkv * ps;
-          const int32_t* table = s.resp ? a.blocks + (int64_t)s.m * a.max_blocks : a.page_table;
-          for (int32_t j = 0; ok && j < s.count; ++j) {
-            const int32_t key0 = s.key0 + j * kTile, left = s.len - key0;  // keys from key0 on
-            for (int kv = 0; kv < 2 && ok; ++kv) {
-              if (!mbar_wait(bar_addr(sbase, B_KV_EMPTY + ring.stage), ring.phase ^ 1)) {
-                fail();
-                ok = false;
-                break;
-              }
-              if (*abort_flag) {
-                ok = false;
-                break;
-              }
-              const bool ragged_v = kv == 1 && left < kTile;
-              const uint32_t t = j & 1, full = kStages * t + ring.stage;
-              const uint32_t fb =
-                  bar_addr(sbase, ragged_v ? B_AUX + ring.stage : B_KV_FULL + full);
-              const uint32_t dst = sbase + kOffRing + ring.stage * kTileBytes;
-              const void* map = s.resp ? (kv ? (const void*)&tm.vr : (const void*)&tm.kr)
-                                       : (kv ? (const void*)&tm.vp : (const void*)&tm.kp);
-              mbar_expect_tx(fb, kTileBytes);
-              for (int x = 0; x < kTile / box_rows; ++x) {
-                int32_t y = pool_rows;  // out of bounds: zero fill
-                if (x * box_rows < left) {
-                  const int32_t pos = key0 + x * box_rows;
-                  const int32_t phys = __ldg(table + (pos >> ps_log2));
-                  if ((uint32_t)phys < (uint32_t)pages)
-                    y = (phys * a.hkv + s.kvh) * ps + (pos & (ps - 1));
-                  else
-                    ls_report(a.err, LS_DEVERR_CHECK);
-                }
-                for (int hf = 0; hf < 2; ++hf)
-                  tma_load_2d(dst + hf * kHalfBytes + x * box_rows * 128, map, hf * 64, y, fb);
-              }
-              full_phase ^= 1u << full;
-              last_t = (last_t & ~(1u << ring.stage)) | (t << ring.stage);
-              filled |= 1u << ring.stage;
-              ring.advance();
+          ld.open(a, s, &tm.kp, &tm.kr);
+          for (int32_t j = 0; j < s.count; ++j) {
+            const uint32_t st = 2 * ring.stage, t = j & 1, full = kStages * t + st;
+            const uint32_t empty = bar_addr(sbase, B_KV_EMPTY + st);
+            ok = (mbar_try_wait(empty, ring.phase ^ 1) || mbar_wait(empty, ring.phase ^ 1)) && !*abort_flag;
+            if (!ok) {
+              fail();
+              break;
             }
+            ld.load(sbase + kOffRing + st * kTileBytes, bar_addr(sbase, B_KV_FULL + full),
+                    j + 1 < s.count, a.err);
+            full_phase ^= 1u << full;
+            last_t = (last_t & ~(1u << st)) | (t << st);
+            filled |= 1u << st;
+            ring.advance();
           }
         }
-        // Do not leave while loads into this CTA's shared memory may still be in flight.
-        for (uint32_t st = 0; st < kStages; ++st) {
-          const uint32_t full = kStages * ((last_t >> st) & 1) + st;
-          if ((filled >> st) & 1)
-            mbar_wait(bar_addr(sbase, B_KV_FULL + full), ((full_phase >> full) & 1) ^ 1);
-        }
+        drain(filled, last_t, full_phase);
       }
     } else if (warp == 3) {
-      // ---------------------------------------------------------- Q, V tails
-      // Q of segment s goes to buffer s & 1 in the operand layout (128-byte swizzle: chunk c
-      // of row r lies at chunk c ^ (r & 7)), row by row, so that a row tile may begin inside
-      // a token.  Rows behind the segment's keep what the buffer held: a row of S, P and O
-      // depends on its own row of Q only, and theirs are not written out.
-      Walk ahead = walk;
-      Seg sq;
-      uint32_t loaded = 0;
-      auto load_q = [&]() {  // the next segment's Q, if there is one
-        if (!ahead.next(&sq)) return;
-        const uint32_t buf = sbase + kOffQ + (loaded & 1) * kTileBytes;
+      // ---------------------------------------------------------- Q, V loads, V tails
+      // Q goes into the operand layout (128-byte swizzle: chunk c of row r lies at chunk
+      // c ^ (r & 7)), row by row, so that a row tile may begin inside a token.  Rows behind
+      // the segment's keep what was there: a row of S, P and O depends on its own row of Q
+      // only, and theirs are not written out.
+      if (lane == 0) {
+        tma_prefetch_desc(&tm.vp);
+        tma_prefetch_desc(&tm.vr);
+      }
+      uint32_t full_phase = 0, last_t = 0, filled = 0, aux_phase = 0, seg = 0;
+      RingPos<kStages / 2> ring;
+      Loader ld;
+      auto load_q = [&](const Seg& sq, uint32_t n_seg) {
         const int rows = seg_rows(a, sq, rt);
+        const uint32_t buf = sbase + q_offset(whole_q(a, sq, rt), n_seg);
         const int32_t row0 = sq.resp ? sq.m * a.n * a.g : rt * kTile;
         int32_t token = (row0 + (lane >> 4)) / a.g, head = (row0 + (lane >> 4)) - token * a.g;
         const int c = lane & 15;
@@ -396,18 +458,42 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
         cp_async_wait_all();
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_addr(sbase, B_Q_FULL + (loaded & 1)));
-        ++loaded;
+        if (lane == 0) mbar_arrive(bar_addr(sbase, B_Q_FULL + (n_seg & 1)));
       };
-      load_q();
-      load_q();
-      uint32_t seg = 0, ring = 1, aux_phase = 0;  // ring slot of the tile's V; a phase bit per stage
-      bool ok = true;
-      for (; ok && walk.next(&s); ++seg) {
-        for (int32_t j = 0; ok && j < s.count; ++j, ring += 2) {
-          const int32_t left = s.len - (s.key0 + j * kTile);
-          if (left >= kTile) continue;
-          const uint32_t st = ring % kStages;
+      bool ok = true, have = walk.next(&s);
+      if (have) load_q(s, 0);
+      for (; ok && have; ++seg) {
+        if (lane == 0) ld.open(a, s, &tm.vp, &tm.vr);
+        uint32_t st = 0, full = 0;
+        for (int32_t j = 0; j < s.count; ++j) {
+          st = 2 * ring.stage + 1;
+          full = kStages * (j & 1) + st;
+          const uint32_t empty = bar_addr(sbase, B_KV_EMPTY + st);
+          ok = (mbar_try_wait(empty, ring.phase ^ 1) || mbar_wait(empty, ring.phase ^ 1)) && !*abort_flag;
+          if (!ok) break;
+          if (lane == 0)
+            ld.load(sbase + kOffRing + st * kTileBytes,
+                    bar_addr(sbase, s.len - (s.key0 + j * kTile) < kTile ? B_AUX + st : B_KV_FULL + full),
+                    j + 1 < s.count, a.err);
+          full_phase ^= 1u << full;
+          last_t = (last_t & ~(1u << st)) | ((j & 1) << st);
+          filled |= 1u << st;
+          ring.advance();
+        }
+        if (!ok) break;
+        const int32_t left = s.len - (s.key0 + (s.count - 1) * kTile);
+        const bool whole = whole_q(a, s, rt);
+        have = walk.next(&s);
+        if (have) {
+          // the next segment's Q: its half of the tile is the segment before's, and a whole
+          // tile also waits for this one's last S
+          if (seg > 0) ok = mbar_wait(bar_addr(sbase, B_Q_EMPTY + ((seg - 1) & 1)), ((seg - 1) >> 1) & 1);
+          if (ok && (whole || whole_q(a, s, rt)))
+            ok = mbar_wait(bar_addr(sbase, B_Q_EMPTY + (seg & 1)), (seg >> 1) & 1);
+          if (!ok) break;
+          load_q(s, seg + 1);
+        }
+        if (left < kTile) {  // the segment's last tile passes its source's end
           ok = mbar_wait(bar_addr(sbase, B_AUX + st), (aux_phase >> st) & 1);
           if (!ok) break;
           aux_phase ^= 1u << st;
@@ -418,15 +504,11 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar_addr(sbase, B_KV_FULL + kStages * (j & 1) + st));
-        }
-        // segment s + 2 reuses this one's Q buffer, once its last S is done
-        if (ok && loaded == seg + 2 && !ahead.done()) {
-          ok = mbar_wait(bar_addr(sbase, B_Q_EMPTY + (seg & 1)), (seg >> 1) & 1);
-          if (ok) load_q();
+          if (lane == 0) mbar_arrive(bar_addr(sbase, B_KV_FULL + full));
         }
       }
       if (!ok) fail();
+      drain(filled, last_t, full_phase);
     } else {
       // ---------------------------------------------------------- MMA issuers
       if (lane == 0) {
@@ -470,7 +552,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
             base += 2 * s.count;
             continue;
           }
-          const uint32_t dq = sdesc_lo(sbase + kOffQ + b * kTileBytes, 16);
+          const uint32_t dq = sdesc_lo(sbase + q_offset(whole_q(a, s, rt), seg - 1), 16);
           // S of own tile j: its K is ring slot base + 2 j
           auto s_tile = [&](int32_t j) {
             const uint32_t slot = base + 2 * j, st = slot % kStages;
@@ -500,8 +582,8 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
             if (j + 2 < s.count) ok = s_tile(j + 2);
             if (*abort_flag) ok = false;
           }
-          if (!ok) fail();
           base += 2 * s.count;
+          if (!ok) fail();
         }
         // every MMA this thread issued has finished before tensor memory is released
         mma_commit(bar_addr(sbase, B_DONE + t));
@@ -522,19 +604,23 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     uint32_t kc = 0, oc = 0;
     bool ok = true;
     while (ok && walk.next(&s)) {
+      // (the row of scores takes 128 registers: what the loop keeps beside it is counted)
       const int32_t rows = seg_rows(a, s, rt);
-      const int64_t prow =
-          (s.resp ? resp_row0(a, prompt_rows, s.item, cta, t) : prompt_row0(a, s.item, col, rt, t)) +
-          row;
+      const bool idle = quad * 32 >= rows;  // the whole warp is padding
+      const int32_t prow =                  // this row's partial, or -1
+          row >= rows ? -1
+                      : (int32_t)(s.resp ? resp_row0(a, prompt_rows, s.item, cta, t)
+                                         : prompt_row0(a, s.item, col, rt, t)) + row;
       if (s.count <= t) {  // a segment of one tile: the odd half says so
-        if (row < rows) a.part_lse[prow] = -INFINITY;
+        if (prow >= 0) a.part_lse[prow] = -INFINITY;
         continue;
       }
-      // the first key this row does not see
-      const int32_t end = s.resp ? min(s.len, s.len - a.n + 1 + row / a.g) : s.len;
-      const bool idle = quad * 32 >= rows;  // the whole warp is padding
+      // keys of the tile from its first one on that this row sees
+      int32_t lim = (s.resp ? min(s.len, s.len - a.n + 1 + row / a.g) : s.len) - s.key0 - t * kTile;
+      int32_t todo = (s.count - t + 1) >> 1;
+      bool first = true;
       float m = -INFINITY, l = 0.f, lcomp = 0.f;
-      for (int32_t j = t; j < s.count; j += 2) {
+      for (; todo > 0; --todo, lim -= 2 * kTile) {
         if (!mbar_wait(bar_addr(sbase, B_S_FULL + t), kc & 1)) { fail(); ok = false; break; }
         ++kc;
         if (idle) {  // P keeps what S left: rows of D depend on their own rows of A only
@@ -543,37 +629,48 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
           continue;
         }
         tc_fence_after();
-        uint32_t sr[128];
+        // The second half of the row is read twice (for the maximum, and again for its
+        // weights): the whole row in registers spilled, and with this kernel's shared memory
+        // spilled registers come back from L2.
+        uint32_t sr[64], tr[32];
         tmem_ld32(s_col + 0, sr);
         tmem_ld32(s_col + 32, sr + 32);
-        tmem_ld32(s_col + 64, sr + 64);
-        tmem_ld32(s_col + 96, sr + 96);
+        tmem_ld32(s_col + 64, tr);
         tmem_wait_ld();
         reg_fence32(sr);
         reg_fence32(sr + 32);
-        reg_fence32(sr + 64);
-        reg_fence32(sr + 96);
-        const int32_t lim = end - (s.key0 + j * kTile);
-        if (lim < kTile) {  // the source's ragged end, the causal end
+        reg_fence32(tr);
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto mask = [&](uint32_t* v, int n, int e0) {  // the source's ragged end, the causal end
+          if (lim < kTile) {
 #pragma unroll
-          for (int e = 0; e < 128; ++e)
-            if (e >= lim) sr[e] = __float_as_uint(-INFINITY);
-        }
-        float mx8[8];
+            for (int e = 0; e < n; ++e)
+              if (e0 + e >= lim) v[e] = __float_as_uint(-INFINITY);
+          }
+        };
+        auto row_max = [&](const uint32_t* v, int n) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(__uint_as_float(sr[k]), __uint_as_float(sr[k + 8]));
+          for (int e = 0; e < n; e += 8)
 #pragma unroll
-        for (int e = 16; e < 128; e += 16)
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mx8[k] = fmax3(mx8[k], __uint_as_float(sr[e + k]), __uint_as_float(sr[e + 8 + k]));
-        const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
-                               fmaxf(mx8[6], mx8[7]));
+            for (int k = 0; k < 4; ++k)
+              mx4[k] = fmax3(mx4[k], __uint_as_float(v[e + k]), __uint_as_float(v[e + 4 + k]));
+        };
+        mask(tr, 32, 64);
+        row_max(tr, 32);
+        tmem_ld32(s_col + 96, tr);
+        mask(sr, 64, 0);
+        row_max(sr, 64);
+        tmem_wait_ld();
+        reg_fence32(tr);
+        mask(tr, 32, 96);
+        row_max(tr, 32);
+        const float mx = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]);
         const float mt = mx * c;
         bool rescale = false;
         float alpha = 1.f;
-        if (j == t) {
+        if (first) {
           m = mt;
+          first = false;
         } else if (mt > m + kRescaleLog2) {
           alpha = fast_exp2(m - mt);
           m = mt;
@@ -584,14 +681,14 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
         const float msub = (m == -INFINITY) ? 0.f : m;
         if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
-          for (int c0 = 0; c0 < 128; c0 += 32) {
-            uint32_t ov[32];
-            tmem_ld32(o_col + c0, ov);
+          for (int c0 = 0; c0 < 128; c0 += 16) {
+            uint32_t ov[16];
+            tmem_ld16(o_col + c0, ov);
             tmem_wait_ld();
-            reg_fence32(ov);
+            reg_fence16(ov);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-            tmem_st32(o_col + c0, ov);
+            for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+            tmem_st16(o_col + c0, ov);
           }
         }
         const float2 c2 = make_float2(c, c), nm2 = make_float2(-msub, -msub);
@@ -599,20 +696,30 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
                          make_float2(0.f, 0.f)};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int jj = 0; jj < 32; ++jj) {
-            const int e = half * 32 + jj;
-            float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])),
-                                  c2, nm2);
-            x.x = fast_exp2(x.x);
-            x.y = fast_exp2(x.y);
-            ls4[jj & 3] = __fadd2_rn(ls4[jj & 3], x);
-            // weights in [0, 2^8] enter the product as bf16, as in the replay forward:
-            // their roundings are independent, so o's error is that of one bf16 rounding
-            pk[jj] = pack_bf16(x.x, x.y);
+          if (half == 1) {
+            tmem_ld32(s_col + 64, sr);
+            tmem_ld32(s_col + 96, sr + 32);
+            tmem_wait_ld();
+            reg_fence32(sr);
+            reg_fence32(sr + 32);
+            mask(sr, 64, 64);
           }
-          tmem_st32(s_col + half * 32, pk);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int jj = 0; jj < 16; ++jj) {
+              const int e = 32 * q + 2 * jj;
+              float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), c2, nm2);
+              x.x = fast_exp2(x.x);
+              x.y = fast_exp2(x.y);
+              ls4[jj & 3] = __fadd2_rn(ls4[jj & 3], x);
+              // weights in [0, 2^8] enter the product as bf16, as in the replay forward:
+              // their roundings are independent, so o's error is that of one bf16 rounding
+              pk[jj] = pack_bf16(x.x, x.y);
+            }
+            tmem_st16(s_col + half * 32 + 16 * q, pk);
+          }
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(bar_addr(sbase, B_P_FULL + 2 * t + half));
@@ -630,22 +737,22 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
         tc_fence_after();
         const float lt = l + lcomp;
         const float inv = lt == 0.f ? 0.f : 1.f / lt;  // a row that sees no key here
-        float* po = a.part_o + prow * kD;
+        float* po = a.part_o + (int64_t)prow * kD;
 #pragma unroll 1
-        for (int c0 = 0; c0 < 128; c0 += 32) {
-          uint32_t ov[32];
-          tmem_ld32(o_col + c0, ov);
+        for (int c0 = 0; c0 < 128; c0 += 16) {
+          uint32_t ov[16];
+          tmem_ld16(o_col + c0, ov);
           tmem_wait_ld();
-          reg_fence32(ov);
-          if (row < rows) {
+          reg_fence16(ov);
+          if (prow >= 0) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
+            for (int i = 0; i < 16; i += 4)
               *reinterpret_cast<float4*>(po + c0 + i) =
                   make_float4(__uint_as_float(ov[i]) * inv, __uint_as_float(ov[i + 1]) * inv,
                               __uint_as_float(ov[i + 2]) * inv, __uint_as_float(ov[i + 3]) * inv);
           }
         }
-        if (row < rows) a.part_lse[prow] = lt == 0.f ? -INFINITY : m + log2f(lt);
+        if (prow >= 0) a.part_lse[prow] = lt == 0.f ? -INFINITY : m + log2f(lt);
         tc_fence_before();
       }
       if (*abort_flag) break;
@@ -802,12 +909,16 @@ int64_t ls_decode_resp_rows(const LsDecodeArgs& a) {
 cudaError_t ls_launch_decode_attn(const LsDecodeArgs& a, cudaStream_t st) {
   TmapSet tm;
   for (int src = 0; src < 2; ++src) {
+    // rows of 256 bytes; a whole-tile box takes both halves of its rows, half by half
     const int ps = 1 << (src ? a.r_ps_log2 : a.ps_log2);
-    const uint64_t dims[2] = {(uint64_t)kD, (uint64_t)(src ? a.r_num_pages : a.num_pages) * a.hkv * ps};
-    const uint64_t strides[1] = {(uint64_t)kD * 2};
-    const uint32_t box[2] = {64, (uint32_t)(ps < kTile ? ps : kTile)};
-    if (!ls_make_tmap_bf16(src ? &tm.kr : &tm.kp, src ? a.rk_pool : a.k_pool, 2, dims, strides, box) ||
-        !ls_make_tmap_bf16(src ? &tm.vr : &tm.vp, src ? a.rv_pool : a.v_pool, 2, dims, strides, box))
+    const uint64_t rows = (uint64_t)(src ? a.r_num_pages : a.num_pages) * a.hkv * ps;
+    const bool whole = ps >= kTile;
+    const uint64_t dims[3] = {whole ? 64u : (uint64_t)kD, rows, 2};
+    const uint64_t strides[2] = {(uint64_t)kD * 2, (uint64_t)kD};
+    const uint32_t box[3] = {64, (uint32_t)(ps < kTile ? ps : kTile), 2};
+    const int rank = whole ? 3 : 2;
+    if (!ls_make_tmap_bf16(src ? &tm.kr : &tm.kp, src ? a.rk_pool : a.k_pool, rank, dims, strides, box) ||
+        !ls_make_tmap_bf16(src ? &tm.vr : &tm.vp, src ? a.rv_pool : a.v_pool, rank, dims, strides, box))
       return cudaErrorInvalidValue;
   }
   cudaError_t e = cudaFuncSetAttribute(decode_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

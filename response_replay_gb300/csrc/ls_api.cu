@@ -1041,6 +1041,7 @@ ls_status decode_args(const ls_kv_cache* c, const ls_resp_cache* r, int n, int H
   a->cols = ctas / a->rts;
   a->err = d.err;
   const size_t rows = (size_t)(ls_decode_prompt_rows(*a) + ls_decode_resp_rows(*a));
+  if (rows >= (1ull << 31)) return LS_ERR_UNSUPPORTED;
   w->part_o = 0;
   w->part_lse = align256(rows * kHeadDim * 4);
   w->total = align256(w->part_lse + rows * 4);

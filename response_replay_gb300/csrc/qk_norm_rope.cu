@@ -265,6 +265,7 @@ norm_rope_fwd_kernel(const __grid_constant__ LsNormRopeArgs a, const __grid_cons
   const bool active = l < a.half / 4;  // the lane's values are rotated
 
   Walk<kFwdRows> w;  // one batch ahead
+  w.begin(a, sp, blockIdx.x * kWarps + (threadIdx.x >> 5));
   const uint4* src = nullptr;
   int64_t shs = 0;
   auto load = [&](int to) {
@@ -283,7 +284,6 @@ norm_rope_fwd_kernel(const __grid_constant__ LsNormRopeArgs a, const __grid_cons
     cp_async_commit();
   };
 
-  w.begin(a, sp, blockIdx.x * kWarps + (threadIdx.x >> 5));
   load(0);
   load_const(a, cst);
   Positions pos;
@@ -433,6 +433,7 @@ norm_rope_bwd_kernel(const __grid_constant__ LsNormRopeArgs a, const __grid_cons
   const bool active = l < a.half / 4;
 
   Walk<kBwdRows> w;  // one batch ahead
+  w.begin(a, sp, blockIdx.x * kWarps + (threadIdx.x >> 5));
   const uint4 *xs = nullptr, *gs = nullptr;
   int64_t xhs = 0, ghs = 0;
   auto load = [&](int to) {
@@ -462,7 +463,6 @@ norm_rope_bwd_kernel(const __grid_constant__ LsNormRopeArgs a, const __grid_cons
     cp_async_commit();
   };
 
-  w.begin(a, sp, blockIdx.x * kWarps + (threadIdx.x >> 5));
   load(0);
   load_const(a, cst);
   for (int i = threadIdx.x; i < 2 * kGroups * kD; i += kThreads) red[i] = 0.f;
