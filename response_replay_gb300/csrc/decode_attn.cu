@@ -19,19 +19,23 @@
 // device (a captured graph follows them): every CTA sums them when it starts.
 //
 // CTA (one per SM, 12 warps):
-//   warps 0, 3  TMA producers of the segments' K and V tiles, page by page, each into a ring
-//               of 3 tiles (one thread for both was the bound with several row tiles: about
-//               2,000 clocks a tile); warp 3 also loads the segments' Q, and clears the V rows
-//               behind a sequence's end (stale page contents, even NaN, would survive a zero
-//               weight) before such a tile is handed over.
-//   warps 1, 2  MMA issuers: the segment's even and odd tiles.  S_t = Q K^T into tensor
-//               memory, O_t += P_t V with P_t read from tensor memory; the two tile
-//               sequences are independent, so one's MMAs can run under the other's softmax
-//               (left alone they tend to fall into step; made to take turns they cost more
-//               between segments than it gave: 280 against 267 us at 64 members).
-//   warps 4-7   softmax of the even tiles, warps 8-11 of the odd ones, one row a thread;
-//               warps whose rows are all padding only keep the barriers going.
-// Tensor memory (512 columns): S_0 [0,128) S_1 [128,256) O_0 [256,384) O_1 [384,512).
+//   warp 0      TMA producer of the segments' K tiles, page by page, into a ring of 3.
+//   warp 1      issues S = Q K^T into one of two S buffers, a tile ahead of the softmax.
+//   warp 2      issues O_t += P_t V over the two halves t of a tile's keys, P_t read from
+//               tensor memory.  (One thread for both kinds of MMA, and one for both kinds of
+//               load, were each the bound with several row tiles: about 2,000 clocks a tile
+//               where the tensor core needs 1,024.)
+//   warp 3      TMA producer of V; loads the segments' Q; clears the V rows behind a
+//               sequence's end (stale page contents, even NaN, would survive a zero weight)
+//               before such a tile is handed over.
+//   warps 4-7   softmax of a tile's keys 0-63, warps 8-11 of its keys 64-127, one row a
+//               thread.  Each half keeps its own running maximum, sum and O, as if it were a
+//               sequence of its own, so the two threads of a row need nothing of each other;
+//               the combine merges them like any partials.  (One warpgroup a tile, by turns,
+//               took 267 us where this takes 261 at 64 members, and spilled registers.)
+//               Warps whose rows are all padding only keep the barriers going.
+// Tensor memory (512 columns): S_0 [0,128) S_1 [128,256) O_0 [256,384) O_1 [384,512); P_t
+// overlays the first 32 of its 64 columns of S.
 #include <math.h>
 
 #include "ls_device.cuh"
@@ -45,41 +49,36 @@ using namespace umma;
 
 constexpr int kD = 128;
 constexpr int kTile = 128;
-constexpr int kStages = 6;
+constexpr int kRing = 3;  // K tiles, and V tiles, in shared memory
 constexpr int kThreads = 384;
-// 168 registers a thread at launch (64,512); warpgroup 0 drops to 112, the two softmax
-// warpgroups rise to 192: 128 x 112 + 256 x 192 = 63,488.
-constexpr int kRegsLaunch = 168, kRegsControl = 112, kRegsSoftmax = 192;
-static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
 constexpr uint32_t kTileBytes = kTile * kD * 2;
 constexpr uint32_t kHalfBytes = kTileBytes / 2;
 constexpr uint32_t kOffQ = 0;
-constexpr uint32_t kOffRing = kTileBytes;
+constexpr uint32_t kOffK = kTileBytes;
+constexpr uint32_t kOffV = kOffK + kRing * kTileBytes;
 // A segment of up to 64 query rows takes half of the Q tile, by turns, so that the next
 // segment's rows can be there before the last one is done.  Its MMAs still read 128 rows,
 // the other half's or the ring's bytes among them: rows that nothing looks at.
 constexpr int kHalfRows = kTile / 2;
-constexpr uint32_t kOffBar = kOffRing + kStages * kTileBytes;
+constexpr uint32_t kOffBar = kOffV + kRing * kTileBytes;
 constexpr uint32_t kSmemBytes = kOffBar + 512 + 1024;
 constexpr int kMaxBoxes = kTile / 16;  // a tile's pages at the smallest page size
+constexpr int kHalfKeys = kTile / 2;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;
 
 enum {
-  // A stage is filled for the issuer of its tile's parity t, who may reach it before the
-  // other issuer's earlier fill of the same stage has landed (loads finish in any order):
-  // one barrier for both would show that issuer a phase that is not its own.  So each
-  // stage has a FULL barrier per issuer (at kStages t + stage), and each issuer counts the
-  // phases of its own fills.
-  B_KV_FULL = 0,                 // 2 kStages
-  B_KV_EMPTY = B_KV_FULL + 2 * kStages,
-  B_AUX = B_KV_EMPTY + kStages,  // a ragged V tile has landed, its tail not yet cleared
-  B_Q_FULL = B_AUX + kStages,    // 2
+  B_K_FULL = 0,
+  B_K_EMPTY = B_K_FULL + kRing,
+  B_V_FULL = B_K_EMPTY + kRing,
+  B_V_EMPTY = B_V_FULL + kRing,  // P V of the tile is done
+  B_AUX = B_V_EMPTY + kRing,     // a ragged V tile has landed, its tail not yet cleared
+  B_Q_FULL = B_AUX + kRing,      // 2
   B_Q_EMPTY = B_Q_FULL + 2,      // 2
-  B_S_FULL = B_Q_EMPTY + 2,      // 2
-  B_P_FULL = B_S_FULL + 2,       // 4: tile sequence t, key half hf at 2 t + hf
-  B_O_DONE = B_P_FULL + 4,       // 2
-  B_DONE = B_O_DONE + 2,         // 2
+  B_S_FULL = B_Q_EMPTY + 2,      // 2: S buffers
+  B_P_FULL = B_S_FULL + 2,       // 4: buffer b, key half t at 2 b + t
+  B_O_DONE = B_P_FULL + 4,
+  B_DONE,                        // 2: the S and the P V issuer
   B_COUNT = B_DONE + 2
 };
 constexpr uint32_t kOffVars = kOffBar + B_COUNT * 8;
@@ -89,28 +88,16 @@ struct TmapSet {
   CUtensorMap kp, vp, kr, vr;
 };
 
+// A bounded wait that asks once without the suspend: most of the issuing warps' waits find
+// their phase complete.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
+  return mbar_try_wait(bar, parity) || mbar_wait(bar, parity);
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
-}
-
-// 16 consecutive 32-bit columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void reg_fence16(uint32_t* r) {
-  asm volatile(""
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
 
 __device__ __forceinline__ uint32_t bar_addr(uint32_t base, int i) { return base + kOffBar + 8 * i; }
@@ -305,7 +292,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
   // which no copy has touched yet)
   int32_t p0, p1, r0, r1;
   {
-    int32_t* wsum = reinterpret_cast<int32_t*>(smem + kOffRing);
+    int32_t* wsum = reinterpret_cast<int32_t*>(smem + kOffK);
     const int per = (a.M + kThreads - 1) / kThreads;
     int32_t mine = 0;
     for (int i = 0; i < per; ++i) {
@@ -354,21 +341,17 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
   }
 
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(bar_addr(sbase, B_KV_FULL + i), 1);
-      mbar_init(bar_addr(sbase, B_KV_FULL + kStages + i), 1);
-      mbar_init(bar_addr(sbase, B_KV_EMPTY + i), 1);
-      mbar_init(bar_addr(sbase, B_AUX + i), 1);
+    for (int i = 0; i < B_Q_FULL; ++i) mbar_init(bar_addr(sbase, i), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_addr(sbase, B_Q_FULL + i), 1);
+      mbar_init(bar_addr(sbase, B_Q_EMPTY + i), 1);
+      mbar_init(bar_addr(sbase, B_S_FULL + i), 1);
+      mbar_init(bar_addr(sbase, B_P_FULL + 2 * i), kTile);
+      mbar_init(bar_addr(sbase, B_P_FULL + 2 * i + 1), kTile);
     }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(bar_addr(sbase, B_Q_FULL + t), 1);
-      mbar_init(bar_addr(sbase, B_Q_EMPTY + t), 2);
-      mbar_init(bar_addr(sbase, B_S_FULL + t), 1);
-      mbar_init(bar_addr(sbase, B_P_FULL + 2 * t), kTile);
-      mbar_init(bar_addr(sbase, B_P_FULL + 2 * t + 1), kTile);
-      mbar_init(bar_addr(sbase, B_O_DONE + t), 1);
-      mbar_init(bar_addr(sbase, B_DONE + t), 1);
-    }
+    mbar_init(bar_addr(sbase, B_O_DONE), 1);
+    mbar_init(bar_addr(sbase, B_DONE), 1);
+    mbar_init(bar_addr(sbase, B_DONE + 1), 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -386,291 +369,229 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     ls_report(a.err, LS_DEVERR_TIMEOUT);
     *abort_flag = 1;
   };
-  // The loading warps do not leave while loads into this CTA's shared memory may still be
-  // in flight: they wait for the last fill of each of their stages.
-  auto drain = [&](uint32_t filled, uint32_t last_t, uint32_t full_phase) {
-    for (uint32_t st = 0; st < kStages; ++st) {
-      const uint32_t full = kStages * ((last_t >> st) & 1) + st;
-      if ((filled >> st) & 1)
-        mbar_wait(bar_addr(sbase, B_KV_FULL + full), ((full_phase >> full) & 1) ^ 1);
-    }
-  };
   Walk walk(a, start, p0, p1, r0, r1);
   Seg s;
 
-  if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
-    if (warp == 0) {
-      // ---------------------------------------------------------- K loads
-      if (lane == 0) {
-        tma_prefetch_desc(&tm.kp);
-        tma_prefetch_desc(&tm.kr);
-        // per FULL barrier: parity of its next fill; per stage: issuer of its last one
-        uint32_t full_phase = 0, last_t = 0, filled = 0;
-        RingPos<kStages / 2> ring;
-        Loader ld;
-        bool ok = true;
-        while (ok && walk.next(&s)) {
-          ld.open(a, s, &tm.kp, &tm.kr);
-          for (int32_t j = 0; j < s.count; ++j) {
-            const uint32_t st = 2 * ring.stage, t = j & 1, full = kStages * t + st;
-            const uint32_t empty = bar_addr(sbase, B_KV_EMPTY + st);
-            ok = (mbar_try_wait(empty, ring.phase ^ 1) || mbar_wait(empty, ring.phase ^ 1)) && !*abort_flag;
-            if (!ok) {
-              fail();
-              break;
-            }
-            ld.load(sbase + kOffRing + st * kTileBytes, bar_addr(sbase, B_KV_FULL + full),
-                    j + 1 < s.count, a.err);
-            full_phase ^= 1u << full;
-            last_t = (last_t & ~(1u << st)) | (t << st);
-            filled |= 1u << st;
-            ring.advance();
-          }
-        }
-        drain(filled, last_t, full_phase);
-      }
-    } else if (warp == 3) {
-      // ---------------------------------------------------------- Q, V loads, V tails
-      // Q goes into the operand layout (128-byte swizzle: chunk c of row r lies at chunk
-      // c ^ (r & 7)), row by row, so that a row tile may begin inside a token.  Rows behind
-      // the segment's keep what was there: a row of S, P and O depends on its own row of Q
-      // only, and theirs are not written out.
-      if (lane == 0) {
-        tma_prefetch_desc(&tm.vp);
-        tma_prefetch_desc(&tm.vr);
-      }
-      uint32_t full_phase = 0, last_t = 0, filled = 0, aux_phase = 0, seg = 0;
-      RingPos<kStages / 2> ring;
+  if (warp == 0) {
+    // ------------------------------------------------------------ K loads
+    if (lane == 0) {
+      tma_prefetch_desc(&tm.kp);
+      tma_prefetch_desc(&tm.kr);
+      RingPos<kRing> ring;
+      uint32_t fills = 0;
       Loader ld;
-      auto load_q = [&](const Seg& sq, uint32_t n_seg) {
-        const int rows = seg_rows(a, sq, rt);
-        const uint32_t buf = sbase + q_offset(whole_q(a, sq, rt), n_seg);
-        const int32_t row0 = sq.resp ? sq.m * a.n * a.g : rt * kTile;
-        int32_t token = (row0 + (lane >> 4)) / a.g, head = (row0 + (lane >> 4)) - token * a.g;
-        const int c = lane & 15;
-        for (int r = lane >> 4; r < rows; r += 2) {
-          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
-                                     ((int64_t)token * a.hq + sq.kvh * a.g + head) * kD + c * 8;
-          cp_async16(buf + (c >> 3) * kHalfBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4), src);
-          for (head += 2; head >= a.g; head -= a.g) ++token;
+      bool ok = true;
+      while (ok && walk.next(&s)) {
+        ld.open(a, s, &tm.kp, &tm.kr);
+        for (int32_t j = 0; j < s.count; ++j) {
+          ok = wait_bar(bar_addr(sbase, B_K_EMPTY + ring.stage), ring.phase ^ 1) && !*abort_flag;
+          if (!ok) {
+            fail();
+            break;
+          }
+          ld.load(sbase + kOffK + ring.stage * kTileBytes, bar_addr(sbase, B_K_FULL + ring.stage),
+                  j + 1 < s.count, a.err);
+          ring.advance();
+          ++fills;
         }
-        cp_async_wait_all();
+      }
+      // Do not leave while loads into this CTA's shared memory may still be in flight.
+      for (uint32_t i = fills > kRing ? fills - kRing : 0; i < fills; ++i)
+        mbar_wait(bar_addr(sbase, B_K_FULL + i % kRing), (i / kRing) & 1);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ Q, V loads, V tails
+    // Q goes into the operand layout (128-byte swizzle: chunk c of row r lies at chunk
+    // c ^ (r & 7)), row by row, so that a row tile may begin inside a token.  Rows behind
+    // the segment's keep what was there: a row of S, P and O depends on its own row of Q
+    // only, and theirs are not written out.
+    if (lane == 0) {
+      tma_prefetch_desc(&tm.vp);
+      tma_prefetch_desc(&tm.vr);
+    }
+    RingPos<kRing> ring;
+    uint32_t fills = 0, aux_phase = 0, seg = 0;
+    Loader ld;
+    auto load_q = [&](uint32_t n_seg) {
+      const int rows = seg_rows(a, s, rt);
+      const uint32_t buf = sbase + q_offset(whole_q(a, s, rt), n_seg);
+      const int32_t row0 = s.resp ? s.m * a.n * a.g : rt * kTile;
+      int32_t token = (row0 + (lane >> 4)) / a.g, head = (row0 + (lane >> 4)) - token * a.g;
+      const int c = lane & 15;
+      for (int r = lane >> 4; r < rows; r += 2) {
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
+                                   ((int64_t)token * a.hq + s.kvh * a.g + head) * kD + c * 8;
+        cp_async16(buf + (c >> 3) * kHalfBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4), src);
+        for (head += 2; head >= a.g; head -= a.g) ++token;
+      }
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_addr(sbase, B_Q_FULL + (n_seg & 1)));
+    };
+    bool ok = true, have = walk.next(&s);
+    if (have) load_q(0);
+    for (; ok && have; ++seg) {
+      if (lane == 0) ld.open(a, s, &tm.vp, &tm.vr);
+      uint32_t st = 0;
+      for (int32_t j = 0; j < s.count; ++j) {
+        st = ring.stage;
+        ok = wait_bar(bar_addr(sbase, B_V_EMPTY + st), ring.phase ^ 1) && !*abort_flag;
+        if (!ok) break;
+        if (lane == 0) {
+          const bool ragged = s.len - (s.key0 + j * kTile) < kTile;
+          ld.load(sbase + kOffV + st * kTileBytes, bar_addr(sbase, (ragged ? B_AUX : B_V_FULL) + st),
+                  j + 1 < s.count, a.err);
+        }
+        ring.advance();
+        ++fills;
+      }
+      if (!ok) break;
+      const int32_t left = s.len - (s.key0 + (s.count - 1) * kTile);
+      const bool whole = whole_q(a, s, rt);
+      have = walk.next(&s);
+      if (have) {
+        // the next segment's Q: its half of the Q tile was the segment before's, and a whole
+        // tile also waits for this one's last S
+        if (seg > 0) ok = wait_bar(bar_addr(sbase, B_Q_EMPTY + ((seg - 1) & 1)), ((seg - 1) >> 1) & 1);
+        if (ok && (whole || whole_q(a, s, rt)))
+          ok = wait_bar(bar_addr(sbase, B_Q_EMPTY + (seg & 1)), (seg >> 1) & 1);
+        if (!ok) break;
+        load_q(seg + 1);
+      }
+      if (left < kTile) {  // the segment's last tile passes its source's end
+        ok = wait_bar(bar_addr(sbase, B_AUX + st), (aux_phase >> st) & 1);
+        if (!ok) break;
+        aux_phase ^= 1u << st;
+        uint8_t* vb = smem + kOffV + st * kTileBytes;
+        for (int i = left * 8 + lane; i < kTile * 8; i += 32) {
+          *reinterpret_cast<uint4*>(vb + i * 16) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(vb + kHalfBytes + i * 16) = make_uint4(0, 0, 0, 0);
+        }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_addr(sbase, B_Q_FULL + (n_seg & 1)));
-      };
-      bool ok = true, have = walk.next(&s);
-      if (have) load_q(s, 0);
-      for (; ok && have; ++seg) {
-        if (lane == 0) ld.open(a, s, &tm.vp, &tm.vr);
-        uint32_t st = 0, full = 0;
-        for (int32_t j = 0; j < s.count; ++j) {
-          st = 2 * ring.stage + 1;
-          full = kStages * (j & 1) + st;
-          const uint32_t empty = bar_addr(sbase, B_KV_EMPTY + st);
-          ok = (mbar_try_wait(empty, ring.phase ^ 1) || mbar_wait(empty, ring.phase ^ 1)) && !*abort_flag;
-          if (!ok) break;
-          if (lane == 0)
-            ld.load(sbase + kOffRing + st * kTileBytes,
-                    bar_addr(sbase, s.len - (s.key0 + j * kTile) < kTile ? B_AUX + st : B_KV_FULL + full),
-                    j + 1 < s.count, a.err);
-          full_phase ^= 1u << full;
-          last_t = (last_t & ~(1u << st)) | ((j & 1) << st);
-          filled |= 1u << st;
-          ring.advance();
-        }
-        if (!ok) break;
-        const int32_t left = s.len - (s.key0 + (s.count - 1) * kTile);
-        const bool whole = whole_q(a, s, rt);
-        have = walk.next(&s);
-        if (have) {
-          // the next segment's Q: its half of the tile is the segment before's, and a whole
-          // tile also waits for this one's last S
-          if (seg > 0) ok = mbar_wait(bar_addr(sbase, B_Q_EMPTY + ((seg - 1) & 1)), ((seg - 1) >> 1) & 1);
-          if (ok && (whole || whole_q(a, s, rt)))
-            ok = mbar_wait(bar_addr(sbase, B_Q_EMPTY + (seg & 1)), (seg >> 1) & 1);
-          if (!ok) break;
-          load_q(s, seg + 1);
-        }
-        if (left < kTile) {  // the segment's last tile passes its source's end
-          ok = mbar_wait(bar_addr(sbase, B_AUX + st), (aux_phase >> st) & 1);
-          if (!ok) break;
-          aux_phase ^= 1u << st;
-          uint8_t* vb = smem + kOffRing + st * kTileBytes;
-          for (int i = left * 8 + lane; i < kTile * 8; i += 32) {
-            *reinterpret_cast<uint4*>(vb + i * 16) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(vb + kHalfBytes + i * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_addr(sbase, B_KV_FULL + full));
-        }
+        if (lane == 0) mbar_arrive(bar_addr(sbase, B_V_FULL + st));
       }
-      if (!ok) fail();
-      drain(filled, last_t, full_phase);
-    } else {
-      // ---------------------------------------------------------- MMA issuers
-      if (lane == 0) {
-        const int t = warp - 1;
-        const uint32_t idS = idesc_bf16_f32(kTile, kTile, false);
-        const uint32_t idPV = idesc_bf16_f32(kTile, kD, true);
-        const uint32_t dk_base = sdesc_lo(sbase + kOffRing, 16);
-        const uint32_t dv_base = sdesc_lo(sbase + kOffRing, kHalfBytes);
-        const uint32_t d_s = tmem + t * kTile, d_o = tmem + 256 + t * kTile;
-        auto issue_s = [&](uint32_t dq, uint32_t kstage) {
-          const uint32_t b0 = dk_base + ((kstage * kTileBytes) >> 4);
+    }
+    if (!ok) fail();
+    for (uint32_t i = fills > kRing ? fills - kRing : 0; i < fills; ++i)
+      mbar_wait(bar_addr(sbase, B_V_FULL + i % kRing), (i / kRing) & 1);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ S = Q K^T
+    if (lane == 0) {
+      const uint32_t idS = idesc_bf16_f32(kTile, kTile, false);
+      const uint32_t dk = sdesc_lo(sbase + kOffK, 16);
+      RingPos<kRing> ring;
+      uint32_t n = 0, seg = 0;  // tiles, segments
+      bool ok = true;
+      for (; ok && walk.next(&s); ++seg) {
+        ok = wait_bar(bar_addr(sbase, B_Q_FULL + (seg & 1)), (seg >> 1) & 1);
+        const uint32_t dq = sdesc_lo(sbase + q_offset(whole_q(a, s, rt), seg), 16);
+        for (int32_t j = 0; ok && j < s.count; ++j, ++n) {
+          ok = wait_bar(bar_addr(sbase, B_K_FULL + ring.stage), ring.phase);
+          // the buffer's last weights have been multiplied: the V of tile n - 2 is done with
+          if (ok && n >= 2) ok = wait_bar(bar_addr(sbase, B_V_EMPTY + (n - 2) % kRing), ((n - 2) / kRing) & 1);
+          if (!ok || *abort_flag) break;
+          tc_fence_after();
+          const uint32_t b0 = dk + ((ring.stage * kTileBytes) >> 4), d_s = tmem + (n & 1) * kTile;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
             mma_ss_lo(d_s, dq + off, b0 + off, idS, kk > 0);
           }
-        };
-        auto issue_pv_half = [&](uint32_t vstage, int hf, bool accumulate) {
-          const uint32_t b0 = dv_base + ((vstage * kTileBytes) >> 4);
-#pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4) {
-            const int kk = 4 * hf + k4;
-            mma_ts_lo(d_o, d_s + kk * 8, b0 + ((kk * 2048) >> 4), idPV,
-                      (accumulate || kk > 0) ? 1u : 0u);
-          }
-        };
-        uint32_t seg = 0, base = 0, kc = 0;  // segments, ring slots before the segment, own tiles
-        uint32_t full_phase = 0;             // per stage: parity of this issuer's next fill
-        auto wait_full = [&](uint32_t st) {
-          const bool w = mbar_wait(bar_addr(sbase, B_KV_FULL + kStages * t + st), (full_phase >> st) & 1);
-          full_phase ^= 1u << st;
-          return w;
-        };
-        bool ok = true;
-        while (ok && walk.next(&s)) {
-          const int b = seg & 1;
-          if (!mbar_wait(bar_addr(sbase, B_Q_FULL + b), (seg >> 1) & 1)) { fail(); break; }
-          ++seg;
-          if (s.count <= t) {  // no tile of this segment is this issuer's
-            mbar_arrive(bar_addr(sbase, B_Q_EMPTY + b));
-            base += 2 * s.count;
-            continue;
-          }
-          const uint32_t dq = sdesc_lo(sbase + q_offset(whole_q(a, s, rt), seg - 1), 16);
-          // S of own tile j: its K is ring slot base + 2 j
-          auto s_tile = [&](int32_t j) {
-            const uint32_t slot = base + 2 * j, st = slot % kStages;
-            if (!wait_full(st)) return false;
-            tc_fence_after();
-            issue_s(dq, st);
-            mma_commit(bar_addr(sbase, B_S_FULL + t));
-            mma_commit(bar_addr(sbase, B_KV_EMPTY + st));
-            if (j + 2 >= s.count) mma_commit(bar_addr(sbase, B_Q_EMPTY + b));
-            return true;
-          };
-          ok = s_tile(t);
-          for (int32_t j = t; ok && j < s.count; j += 2) {
-            const uint32_t slot = base + 2 * j + 1, st = slot % kStages;
-            ok = wait_full(st) && mbar_wait(bar_addr(sbase, B_P_FULL + 2 * t), kc & 1);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv_half(st, 0, j > t);
-            ok = mbar_wait(bar_addr(sbase, B_P_FULL + 2 * t + 1), kc & 1);
-            if (!ok) break;
-            ++kc;
-            tc_fence_after();
-            issue_pv_half(st, 1, true);
-            if (j + 2 >= s.count) mma_commit(bar_addr(sbase, B_O_DONE + t));
-            mma_commit(bar_addr(sbase, B_KV_EMPTY + st));
-            // after P V in issue order: the next S overwrites P
-            if (j + 2 < s.count) ok = s_tile(j + 2);
-            if (*abort_flag) ok = false;
-          }
-          base += 2 * s.count;
-          if (!ok) fail();
+          mma_commit(bar_addr(sbase, B_S_FULL + (n & 1)));
+          mma_commit(bar_addr(sbase, B_K_EMPTY + ring.stage));
+          if (j + 1 == s.count) mma_commit(bar_addr(sbase, B_Q_EMPTY + (seg & 1)));
+          ring.advance();
         }
-        // every MMA this thread issued has finished before tensor memory is released
-        mma_commit(bar_addr(sbase, B_DONE + t));
-        mbar_wait(bar_addr(sbase, B_DONE + t), 0);
       }
+      if (!ok) fail();
+      // every MMA this thread issued has finished before tensor memory is released
+      mma_commit(bar_addr(sbase, B_DONE));
+      mbar_wait(bar_addr(sbase, B_DONE), 0);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ O_t += P_t V
+    if (lane == 0) {
+      const uint32_t idPV = idesc_bf16_f32(kTile, kD, true);
+      const uint32_t dv = sdesc_lo(sbase + kOffV, kHalfBytes);
+      RingPos<kRing> ring;
+      uint32_t n = 0;
+      bool ok = true;
+      while (ok && walk.next(&s)) {
+        for (int32_t j = 0; ok && j < s.count; ++j, ++n) {
+          const uint32_t buf = n & 1, d_s = tmem + buf * kTile;
+          const uint32_t b0 = dv + ((ring.stage * kTileBytes) >> 4);
+          ok = wait_bar(bar_addr(sbase, B_V_FULL + ring.stage), ring.phase);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            ok = ok && wait_bar(bar_addr(sbase, B_P_FULL + 2 * buf + t), (n >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k4 = 0; k4 < 4; ++k4)
+              mma_ts_lo(tmem + 256 + t * kTile, d_s + t * kHalfKeys + k4 * 8,
+                        b0 + (((4 * t + k4) * 2048) >> 4), idPV, (j > 0 || k4 > 0) ? 1u : 0u);
+          }
+          if (!ok || *abort_flag) break;
+          if (j + 1 == s.count) mma_commit(bar_addr(sbase, B_O_DONE));
+          mma_commit(bar_addr(sbase, B_V_EMPTY + ring.stage));
+          ring.advance();
+        }
+      }
+      if (!ok) fail();
+      mma_commit(bar_addr(sbase, B_DONE + 1));
+      mbar_wait(bar_addr(sbase, B_DONE + 1), 0);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ------------------------------------------------------------ softmax warpgroups
-    const int t = (warp - 4) >> 2;
+    const int t = (warp - 4) >> 2;  // half of a tile's keys
     const int quad = warp & 3;
     const int row = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t s_col = tmem + lane_off + t * kTile;
     const uint32_t o_col = tmem + lane_off + 256 + t * kTile;
     const float c = a.scale_log2;
     const int64_t prompt_rows = prompt_rows_of(a);
-    uint32_t kc = 0, oc = 0;
+    uint32_t n = 0, oc = 0;
     bool ok = true;
     while (ok && walk.next(&s)) {
-      // (the row of scores takes 128 registers: what the loop keeps beside it is counted)
       const int32_t rows = seg_rows(a, s, rt);
       const bool idle = quad * 32 >= rows;  // the whole warp is padding
-      const int32_t prow =                  // this row's partial, or -1
-          row >= rows ? -1
-                      : (int32_t)(s.resp ? resp_row0(a, prompt_rows, s.item, cta, t)
-                                         : prompt_row0(a, s.item, col, rt, t)) + row;
-      if (s.count <= t) {  // a segment of one tile: the odd half says so
-        if (prow >= 0) a.part_lse[prow] = -INFINITY;
-        continue;
-      }
-      // keys of the tile from its first one on that this row sees
-      int32_t lim = (s.resp ? min(s.len, s.len - a.n + 1 + row / a.g) : s.len) - s.key0 - t * kTile;
-      int32_t todo = (s.count - t + 1) >> 1;
-      bool first = true;
+      // keys of the half tile from its first one on that this row sees
+      int32_t lim = (s.resp ? min(s.len, s.len - a.n + 1 + row / a.g) : s.len) - s.key0 - t * kHalfKeys;
       float m = -INFINITY, l = 0.f, lcomp = 0.f;
-      for (; todo > 0; --todo, lim -= 2 * kTile) {
-        if (!mbar_wait(bar_addr(sbase, B_S_FULL + t), kc & 1)) { fail(); ok = false; break; }
-        ++kc;
+      for (int32_t j = 0; j < s.count; ++j, ++n, lim -= kTile) {
+        const uint32_t buf = n & 1, s_col = tmem + lane_off + buf * kTile + t * kHalfKeys;
+        if (!wait_bar(bar_addr(sbase, B_S_FULL + buf), (n >> 1) & 1)) { fail(); ok = false; break; }
         if (idle) {  // P keeps what S left: rows of D depend on their own rows of A only
-          mbar_arrive(bar_addr(sbase, B_P_FULL + 2 * t));
-          mbar_arrive(bar_addr(sbase, B_P_FULL + 2 * t + 1));
+          mbar_arrive(bar_addr(sbase, B_P_FULL + 2 * buf + t));
           continue;
         }
         tc_fence_after();
-        // The second half of the row is read twice (for the maximum, and again for its
-        // weights): the whole row in registers spilled, and with this kernel's shared memory
-        // spilled registers come back from L2.
-        uint32_t sr[64], tr[32];
-        tmem_ld32(s_col + 0, sr);
+        uint32_t sr[64];
+        tmem_ld32(s_col, sr);
         tmem_ld32(s_col + 32, sr + 32);
-        tmem_ld32(s_col + 64, tr);
         tmem_wait_ld();
         reg_fence32(sr);
         reg_fence32(sr + 32);
-        reg_fence32(tr);
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto mask = [&](uint32_t* v, int n, int e0) {  // the source's ragged end, the causal end
-          if (lim < kTile) {
+        if (lim < kHalfKeys) {  // the source's ragged end, the causal end
 #pragma unroll
-            for (int e = 0; e < n; ++e)
-              if (e0 + e >= lim) v[e] = __float_as_uint(-INFINITY);
-          }
-        };
-        auto row_max = [&](const uint32_t* v, int n) {
+          for (int e = 0; e < 64; ++e)
+            if (e >= lim) sr[e] = __float_as_uint(-INFINITY);
+        }
+        float mx4[4];
 #pragma unroll
-          for (int e = 0; e < n; e += 8)
+        for (int k = 0; k < 4; ++k) mx4[k] = fmaxf(__uint_as_float(sr[k]), __uint_as_float(sr[k + 4]));
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mx4[k] = fmax3(mx4[k], __uint_as_float(v[e + k]), __uint_as_float(v[e + 4 + k]));
-        };
-        mask(tr, 32, 64);
-        row_max(tr, 32);
-        tmem_ld32(s_col + 96, tr);
-        mask(sr, 64, 0);
-        row_max(sr, 64);
-        tmem_wait_ld();
-        reg_fence32(tr);
-        mask(tr, 32, 96);
-        row_max(tr, 32);
-        const float mx = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]);
-        const float mt = mx * c;
+        for (int e = 8; e < 64; e += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx4[k] = fmax3(mx4[k], __uint_as_float(sr[e + k]), __uint_as_float(sr[e + 4 + k]));
+        const float mt = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]) * c;
         bool rescale = false;
         float alpha = 1.f;
-        if (first) {
+        if (j == 0) {
           m = mt;
-          first = false;
         } else if (mt > m + kRescaleLog2) {
           alpha = fast_exp2(m - mt);
           m = mt;
@@ -680,50 +601,43 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
         }
         const float msub = (m == -INFINITY) ? 0.f : m;
         if (__any_sync(0xffffffffu, rescale)) {
+          // P V of the tile before may still be adding to O
+          if (!mbar_wait(bar_addr(sbase, B_V_EMPTY + (n - 1) % kRing), ((n - 1) / kRing) & 1)) {
+            fail();
+            ok = false;
+            break;
+          }
+          tc_fence_after();
 #pragma unroll 1
-          for (int c0 = 0; c0 < 128; c0 += 16) {
-            uint32_t ov[16];
-            tmem_ld16(o_col + c0, ov);
+          for (int c0 = 0; c0 < 128; c0 += 32) {
+            uint32_t ov[32];
+            tmem_ld32(o_col + c0, ov);
             tmem_wait_ld();
-            reg_fence16(ov);
+            reg_fence32(ov);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-            tmem_st16(o_col + c0, ov);
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+            tmem_st32(o_col + c0, ov);
           }
         }
         const float2 c2 = make_float2(c, c), nm2 = make_float2(-msub, -msub);
         float2 ls4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                          make_float2(0.f, 0.f)};
+        uint32_t pk[32];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (half == 1) {
-            tmem_ld32(s_col + 64, sr);
-            tmem_ld32(s_col + 96, sr + 32);
-            tmem_wait_ld();
-            reg_fence32(sr);
-            reg_fence32(sr + 32);
-            mask(sr, 64, 64);
-          }
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int jj = 0; jj < 16; ++jj) {
-              const int e = 32 * q + 2 * jj;
-              float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), c2, nm2);
-              x.x = fast_exp2(x.x);
-              x.y = fast_exp2(x.y);
-              ls4[jj & 3] = __fadd2_rn(ls4[jj & 3], x);
-              // weights in [0, 2^8] enter the product as bf16, as in the replay forward:
-              // their roundings are independent, so o's error is that of one bf16 rounding
-              pk[jj] = pack_bf16(x.x, x.y);
-            }
-            tmem_st16(s_col + half * 32 + 16 * q, pk);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(bar_addr(sbase, B_P_FULL + 2 * t + half));
+        for (int jj = 0; jj < 32; ++jj) {
+          float2 x = __ffma2_rn(
+              make_float2(__uint_as_float(sr[2 * jj]), __uint_as_float(sr[2 * jj + 1])), c2, nm2);
+          x.x = fast_exp2(x.x);
+          x.y = fast_exp2(x.y);
+          ls4[jj & 3] = __fadd2_rn(ls4[jj & 3], x);
+          // weights in [0, 2^8] enter the product as bf16, as in the replay forward: their
+          // roundings are independent, so o's error is that of one bf16 rounding
+          pk[jj] = pack_bf16(x.x, x.y);
         }
+        tmem_st32(s_col, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar_addr(sbase, B_P_FULL + 2 * buf + t));
         const float2 lsa = __fadd2_rn(__fadd2_rn(ls4[0], ls4[1]), __fadd2_rn(ls4[2], ls4[3]));
         const float ls = lsa.x + lsa.y;
         const float tsum = l + ls;
@@ -731,28 +645,31 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
         l = tsum;
       }
       if (!ok) break;
-      if (!mbar_wait(bar_addr(sbase, B_O_DONE + t), oc & 1)) { fail(); break; }
+      if (!mbar_wait(bar_addr(sbase, B_O_DONE), oc & 1)) { fail(); break; }
       ++oc;
       if (!idle) {
         tc_fence_after();
         const float lt = l + lcomp;
         const float inv = lt == 0.f ? 0.f : 1.f / lt;  // a row that sees no key here
-        float* po = a.part_o + (int64_t)prow * kD;
+        const int64_t prow =
+            (s.resp ? resp_row0(a, prompt_rows, s.item, cta, t) : prompt_row0(a, s.item, col, rt, t)) +
+            row;
+        float* po = a.part_o + prow * kD;
 #pragma unroll 1
-        for (int c0 = 0; c0 < 128; c0 += 16) {
-          uint32_t ov[16];
-          tmem_ld16(o_col + c0, ov);
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          uint32_t ov[32];
+          tmem_ld32(o_col + c0, ov);
           tmem_wait_ld();
-          reg_fence16(ov);
-          if (prow >= 0) {
+          reg_fence32(ov);
+          if (row < rows) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 4)
+            for (int i = 0; i < 32; i += 4)
               *reinterpret_cast<float4*>(po + c0 + i) =
                   make_float4(__uint_as_float(ov[i]) * inv, __uint_as_float(ov[i + 1]) * inv,
                               __uint_as_float(ov[i + 2]) * inv, __uint_as_float(ov[i + 3]) * inv);
           }
         }
-        if (prow >= 0) a.part_lse[prow] = lt == 0.f ? -INFINITY : m + log2f(lt);
+        if (row < rows) a.part_lse[prow] = lt == 0.f ? -INFINITY : m + log2f(lt);
         tc_fence_before();
       }
       if (*abort_flag) break;
@@ -871,7 +788,7 @@ decode_combine(const __grid_constant__ LsDecodeArgs a) {
 #pragma unroll 4
   for (int k = warp; k < count; k += kCombineWarps) {
     const float w = exp2f(wt[k] - msub);
-    // a half that had no tile left no o
+    // a half that saw no key adds nothing
     const float4 v = w == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
                               : __ldcg(reinterpret_cast<const float4*>(a.part_o + part_row(k) * kD) + lane);
     sum += w;

@@ -431,6 +431,8 @@ norm_rope_bwd_kernel(const __grid_constant__ LsNormRopeArgs a, const __grid_cons
   float2* tab = cst.tab[grp];
   const int partner = partner_of(a, l);
   const bool active = l < a.half / 4;
+  // the sum of the partials may be launched: its blocks wait for this grid
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   Walk<kBwdRows> w;  // one batch ahead
   w.begin(a, sp, blockIdx.x * kWarps + (threadIdx.x >> 5));
@@ -585,10 +587,11 @@ __device__ __forceinline__ float sum32(float v) {
 // dw[c] (+)= sum over blocks of part[block][c], in a fixed order: 128 chains of blocks,
 // then the chains.  256 columns (queries, keys), 32 a block, 4 a thread.
 constexpr int kDwCols = 32, kDwChains = 128;
-__global__ void __launch_bounds__(1024) norm_rope_dw(const float* __restrict__ part, int blocks,
+__global__ void __launch_bounds__(1024) norm_rope_dw(const float* part, int blocks,
                                                      float* dwq, float* dwk, int accumulate) {
   __shared__ float red[kDwChains][kDwCols + 1];
   const int c = threadIdx.x & 7, chain = threadIdx.x >> 3;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are written
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int b = chain; b < blocks; b += kDwChains) {
@@ -671,8 +674,16 @@ cudaError_t ls_launch_norm_rope_bwd(const LsNormRopeArgs& a, const LsRows& x, co
     ls_note_launch();
   }
   if (dw) {
-    norm_rope_dw<<<2 * kD / kDwCols, 1024, 0, st>>>(part, ctas, dwq, dwk, accumulate);
-    e = cudaGetLastError();
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * kD / kDwCols);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = ctas > 0 ? 1 : 0;  // only behind the kernel above, which lets it start early
+    e = cudaLaunchKernelEx(&cfg, norm_rope_dw, (const float*)part, ctas, dwq, dwk, accumulate);
     if (e == cudaSuccess) ls_note_launch();
   }
   return e;
