@@ -23,6 +23,8 @@ takes its dQ / dK / dV.  This module holds the part that needs no weights:
   GB300 node), streamed into a two-slot page cache in GPU memory one layer ahead of the
   replay that reads them (explainer, same section, GLM bullet: the prompt's pages held in
   CPU memory); ``StreamedLatentLayers`` does the same for latent (MLA-style) pages.
+- ``LayeredResponses``: the rollout's side of the same prompt: the growing responses of a
+  group in L layers' pages under one block table, and their decode steps.
 
 Every step of the computation is a call of the replay backward in the CUDA library.
 """
@@ -65,6 +67,54 @@ class LayeredKVCache:
     def capture(self, layer: int, k: torch.Tensor, v: torch.Tensor, start_pos: int = 0,
                 stream=None) -> None:
         self.layers[layer].capture(k, v, start_pos, stream)
+
+
+class LayeredResponses:
+    """The growing responses of a group in the pages of every layer.  The token -> page map
+    is the same in each, so one allocator (``alloc``) serves all; layer l's pools are slice
+    l of one allocation, ``layers[l]`` its ResponseCache.  A decode step is one ``extend``
+    and then, layer by layer, ``append`` (norm, rotary positions, K and V into the pages)
+    and ``attend`` (over the layer's captured prompt and the members' own responses); it
+    can be captured as one CUDA graph."""
+
+    def __init__(self, prompt, num_kv_heads: int, members: int, max_tokens: int,
+                 num_pages: int, page_size: int, device, capacity: int | None = None,
+                 axes: int = 1):
+        """prompt: the captured prompt's layers (LayeredKVCache, or anything whose [l] is a
+        PagedKVCache); max_tokens: longest response; capacity: most new tokens of a step
+        (default: one a member); axes: rows of positions, one an axis of the rotary."""
+        self.prompt = prompt
+        blocks = (max_tokens + page_size - 1) // page_size
+        self.alloc = api.PageAllocator.empty(members, blocks, num_pages, page_size, device)
+        shape = (len(prompt), num_pages, num_kv_heads, page_size, api.HEAD_DIM)
+        self.k_pools = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        self.v_pools = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        self.pools = [api.PagePool(k, v) for k, v in zip(self.k_pools, self.v_pools)]
+        self.layers = [api.ResponseCache.of(pool, self.alloc) for pool in self.pools]
+        n = members if capacity is None else capacity
+        self.slots = torch.empty(n, dtype=torch.int32, device=device)
+        self.positions = torch.empty((axes, n), dtype=torch.int32, device=device)
+
+    def __len__(self) -> int:
+        return len(self.layers)
+
+    def extend(self, add: torch.Tensor, stream=None) -> None:
+        """Room for add[m] new tokens of every member, behind the prompt."""
+        api.extend_pages(self.alloc, add, self.prompt[0].num_tokens, self.slots, self.positions,
+                         stream=stream)
+
+    def append(self, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rotary,
+               wq=None, wk=None, stream=None, **kw) -> torch.Tensor:
+        """The new tokens' projections (in the order of ``slots``) into layer's pages; the
+        normed and rotated queries."""
+        return api.qk_norm_rope_append(self.pools[layer], q, k, v, self.slots, self.positions,
+                                       rotary, wq, wk, stream=stream, **kw)
+
+    def attend(self, layer: int, q: torch.Tensor, softmax_scale: float, o=None, lse=None,
+               stream=None):
+        """q [members][n][Hq][128]: the n newest tokens of every member; returns (o, lse)."""
+        return api.decode_attn(self.prompt[layer], self.layers[layer], q, softmax_scale, o, lse,
+                               stream)
 
 
 class KVGradPages:

@@ -264,3 +264,50 @@ def test_decode_loop(cuda, graph):
         ro, rl = api.replay_fwd(cache, q, k, v, SCALE, 2)
         assert (ro.float() - got[m].float()).abs().max() <= 2 ** -7 * got[m].float().abs().max()
         assert (rl - gl[m]).abs().max() <= 1e-5
+
+
+def test_layered_responses(cuda):
+    """Two layers under one allocator, ragged first tokens, then decode steps: every layer's
+    output of a member's newest token is that of the replay of its whole response."""
+    from response_replay_gb300 import layers as L
+    P, M, hq, hkv, ps, nl = 200, 3, 6, 2, 16, 2
+    gen = torch.Generator(device=cuda)
+    gen.manual_seed(5)
+
+    def normal(*s):
+        return torch.randn(*s, generator=gen, device=cuda).to(torch.bfloat16)
+
+    table = torch.tensor([3, 0, 2, 1], dtype=torch.int32, device=cuda)
+    prompt = L.LayeredKVCache(nl, 5, table, 64, hkv, P, fill=float("nan"))
+    for l in range(nl):
+        prompt.capture(l, normal(P, hkv, 128), normal(P, hkv, 128))
+    r = L.LayeredResponses(prompt, hkv, M, 64, 12, ps, cuda, capacity=60)
+    r.k_pools.fill_(float("nan"))
+    r.v_pools.fill_(float("nan"))
+    rot = api.Rotary.from_base(1e6, 128, cuda)
+    w = torch.rand(128, generator=gen, device=cuda) + 0.5
+    adds = [[17, 0, 33], [1, 1, 1], [1, 1, 1]]
+    xs = [[normal(sum(a[m] for a in adds), hq + 2 * hkv, 128) for m in range(M)] for _ in range(nl)]
+    done = [0] * M
+    for add in adds:
+        r.extend(torch.tensor(add, dtype=torch.int32, device=cuda))
+        n = sum(add)
+        for l in range(nl):
+            x = torch.zeros(60, hq + 2 * hkv, 128, dtype=torch.bfloat16, device=cuda)
+            x[:n] = torch.cat([xs[l][m][done[m]:done[m] + add[m]] for m in range(M)])
+            q = r.append(l, x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], rot, w, w)
+            last = torch.tensor([sum(add[:m + 1]) - 1 for m in range(M)], device=cuda).clamp(min=0)
+            o, lse = r.attend(l, q[last].view(M, 1, hq, 128), SCALE)
+            for m in range(M):
+                R = done[m] + add[m]
+                if add[m] == 0:
+                    continue
+                pos = torch.arange(P, P + R, dtype=torch.int32, device=cuda)
+                xm = xs[l][m][:R]
+                rq, rk, rv = api.qk_norm_rope_fwd(xm[:, :hq], xm[:, hq:hq + hkv], xm[:, hq + hkv:],
+                                                  pos, rot, w, w)
+                ro, rl = api.replay_fwd(prompt[l], rq, rk, rv, SCALE, 2)
+                assert (ro[R - 1].float() - o[m, 0].float()).abs().max() <= 2 ** -7 * ro.float().abs().max()
+                assert (rl[R - 1] - lse[m, 0]).abs().max() <= 1e-5
+        done = [d + a for d, a in zip(done, add)]
+    assert r.alloc.lens.tolist() == done and B.ls_last_device_error(0) == B.LS_OK
