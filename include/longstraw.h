@@ -453,7 +453,7 @@ typedef struct {
   const void* wk;
   ls_dtype w_dtype;
   float w_offset;
-  float eps; /* > 0 */
+  float eps; /* > 0, a normal number */
 } ls_qk_norm;
 
 typedef struct {
@@ -499,7 +499,7 @@ ls_status ls_qk_norm_rope_append(const ls_page_pool* pool, const ls_qkv_view* x,
  * rounded dy.v.  dwq, dwk: fp32 [128] weight gradients, each or both NULL when not wanted;
  * accumulate != 0 adds into them.  With g = dy turned back, xh = x r, h = g (w_offset + w):
  *   dx = r (h - xh mean_i(h_i xh_i)),   dw_i = sum over tokens and heads of g_i xh_i.
- * dw is summed in a fixed order (fp32 within a block, 64 bits across blocks).  dx may be x
+ * dw is summed in fp32 in a fixed order (by rows of a block, then by blocks).  dx may be x
  * itself (same pointers and strides).  workspace: the query's bytes, needed for dwq or dwk
  * only.  T == 0 leaves dx alone and gives (or adds) zero weight gradients. */
 ls_status ls_qk_norm_rope_bwd_workspace(int64_t T, size_t* bytes);
@@ -523,7 +523,8 @@ ls_status ls_qk_norm_rope_bwd(const ls_qkv_view* x, int64_t T, int Hq, int Hkv,
  *   positions  int32 [axes][capacity] or NULL: pos0 + index within the response (the
  *              same on every axis), 0 behind the last token
  *   lens_out   int32 [members]: lens + add;  used_out int32 [1]: *used + pages taken.
- *              Each may be the input itself (in place), otherwise they may not overlap.
+ *              Each may be the input itself (in place), and lens_out may be add.
+ *              Other arrays may not overlap.
  * A member out of use has lens[m] < 0 and add[m] == 0 and is passed over.  All or nothing:
  * when an add is negative, a member out of use grows, a row of the table is full, the
  * free list ends or the tokens exceed capacity, LS_ERR_DEVICE_CHECK is recorded, every

@@ -944,7 +944,7 @@ ls_status norm_rope_args(int64_t T, int Hq, int Hkv, const ls_qk_norm* norm, con
   a->hkv = Hkv;
   a->axes = 1;
   if (norm) {
-    if (!isfinite(norm->eps) || !(norm->eps > 0.f) || !isfinite(norm->w_offset))
+    if (!isfinite(norm->eps) || !(norm->eps >= 1.17549435e-38f) || !isfinite(norm->w_offset))
       return LS_ERR_INVALID_ARG;
     if (norm->w_dtype != LS_BF16 && norm->w_dtype != LS_FP32) return LS_ERR_INVALID_ARG;
     if (!aligned16(norm->wq) || !aligned16(norm->wk)) return LS_ERR_INVALID_ARG;
@@ -1149,14 +1149,14 @@ ls_status ls_extend_pages(int32_t* block_table, int members, int max_blocks, int
   if ((int64_t)members * max_blocks >= (1ll << 31) || (int64_t)num_pages * page_size >= (1ll << 31) ||
       (int64_t)max_blocks * page_size + pos0 >= (1ll << 31) || capacity >= (1ll << 31))
     return LS_ERR_UNSUPPORTED;
-  const void* ptrs[] = {lens, add, used, lens_out, used_out};
-  for (const void* p : ptrs)
-    if (!p || !aligned4(p)) return LS_ERR_INVALID_ARG;
-  if ((max_blocks > 0 && (!block_table || !aligned4(block_table))) ||
+  const void* ptrs[] = {used, used_out, lens, add, lens_out};
+  for (int i = 0; i < 5; ++i)  // without members there are no counts
+    if ((!ptrs[i] && (i < 2 || members > 0)) || !aligned4(ptrs[i])) return LS_ERR_INVALID_ARG;
+  if ((members > 0 && max_blocks > 0 && (!block_table || !aligned4(block_table))) ||
       (num_free > 0 && (!free_list || !aligned4(free_list))) ||
       (capacity > 0 && (!slots || !aligned16(slots))) || !aligned16(positions))
     return LS_ERR_INVALID_ARG;
-  if (members == 0 && capacity == 0) return LS_OK;
+  if (members == 0 && capacity == 0 && used_out == used) return LS_OK;
   DevInfo d;
   const ls_status s = dev_info(&d);
   if (s != LS_OK) return s;

@@ -11,7 +11,7 @@
 // tokens and of the new table entries, so one launch serves any length.  The lengths and
 // the count of used pages are read by every block; they are written by the only block of
 // a small call, by block 0 when they go to buffers of their own, and by a second launch
-// when a large call updates them in place.
+// when a large call writes them over what it reads.
 #include "ls_device.cuh"
 #include "ls_internal.h"
 
@@ -192,7 +192,11 @@ cudaError_t ls_launch_extend_pages(const LsExtendArgs& a, int sms, cudaStream_t 
   int64_t blocks = (a.capacity + kChunk - 1) / kChunk;
   if (blocks < 1) blocks = 1;
   if (blocks > sms) blocks = sms;
-  const bool in_place = a.lens_out == a.lens || a.used_out == a.used;
+  auto meets = [](const int32_t* p, int64_t n, const int32_t* q, int64_t m) { return p < q + m && q < p + n; };
+  bool in_place = false;
+  const struct { const int32_t* p; int64_t n; } in[] = {{a.lens, a.members}, {a.add, a.members}, {a.used, 1}};
+  for (const auto& i : in)
+    in_place = in_place || meets(a.lens_out, a.members, i.p, i.n) || meets(a.used_out, 1, i.p, i.n);
   const bool one = blocks == 1 || !in_place;
   extend_pages_kernel<<<(unsigned)blocks, kThreads, 0, st>>>(a, 1, one ? 1 : 0);
   cudaError_t e = cudaGetLastError();

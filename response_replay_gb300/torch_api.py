@@ -36,17 +36,28 @@ _workspaces: dict = {}
 _retired: list = []
 
 
-def _call_workspace(nbytes: int, like: torch.Tensor, key: str, stream: int) -> torch.Tensor:
-    """A workspace of the calls on one stream (calls on different streams may overlap).
-    One that was outgrown is kept: a captured graph may still use it."""
+def _with_workspace(call, args: tuple, size, like: torch.Tensor, key: str, stream: int) -> None:
+    """call(*args, workspace, its bytes, stream) with the workspace of the calls of one kind
+    on the current stream (calls on different streams may overlap).  It grows when the call
+    says that it is too small, which it does before it launches anything; one that was
+    outgrown is kept, in case a graph that was captured without torch still uses it.  A call
+    captured into a graph takes one from the graph's own memory: two graphs captured on
+    one stream may be replayed on two."""
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(max(size(), 256), dtype=torch.uint8, device=like.device)
+        return call(*args, ws.data_ptr(), ws.numel(), stream)
     k = (like.get_device(), key, stream)
     ws = _workspaces.get(k)
-    if ws is None or ws.numel() < nbytes:
-        if ws is not None:
-            _retired.append(ws)
-        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=like.device)
-        _workspaces[k] = ws
-    return ws
+    if ws is not None:
+        try:
+            return call(*args, ws.data_ptr(), ws.numel(), stream)
+        except B.LongstrawError as e:
+            if e.status != B.LS_ERR_WORKSPACE:
+                raise
+        _retired.append(ws)
+    ws = torch.empty(max(size(), 256), dtype=torch.uint8, device=like.device)
+    _workspaces[k] = ws
+    call(*args, ws.data_ptr(), ws.numel(), stream)
 
 
 def workspace(nbytes: int, device: torch.device, key: str = "default") -> torch.Tensor:
@@ -452,19 +463,25 @@ def mla_replay_bwd(cache: LatentCache, q: torch.Tensor, lat_resp: torch.Tensor, 
 # ---------------------------------------------------------------- query / key stage
 #
 # These calls are a few microseconds of GPU work at decode sizes, so their argument checks
-# are kept to one pass over each tensor's attributes.
+# are kept to one pass over each tensor's attributes.  With a stream given, a call does
+# what it does with that stream as the current one: what it allocates belongs to it.
 
-def _dev_stream(dev: int, stream) -> int:
-    """The stream of a call on CUDA device `dev`, which has to be the current one (the
+def _as_current(stream):
+    if isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    h = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(h) if h > 1 else torch.cuda.default_stream())
+
+
+def _dev_stream(dev: int) -> int:
+    """The current stream of CUDA device `dev`, which has to be the current one (the
     kernels run there)."""
     if dev < 0:
         raise ValueError("the tensors must be CUDA tensors")
     if dev != torch.cuda.current_device():
         raise ValueError(f"tensors on cuda:{dev}, but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _refuse(t: torch.Tensor, name: str, dtype, shape, dev: int):
@@ -595,9 +612,13 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None,
     k / v [T][Hkv][128] bf16, any token and head strides (slices of a packed projection),
     positions int32 [axes][T].  Returns (q_out, k_out, v_out); the outputs are dense
     unless given (an output may be its input), v is copied into the replay's layout."""
+    if stream is not None:
+        with _as_current(stream):
+            return qk_norm_rope_fwd(q, k, v, positions, rotary, wq, wk, norm, eps, weight_offset,
+                                    q_out, k_out, v_out)
     dev, T, hq, hkv, qr, kr, ns, rs, pp = _stage_args(q, k, positions, rotary, wq, wk, norm, eps,
                                                       weight_offset)
-    st = _dev_stream(dev, stream)
+    st = _dev_stream(dev)
     qs, ks = (T, hq, HEAD_DIM), (T, hkv, HEAD_DIM)
     vr = vo = _NO_ROWS
     if v is not None:
@@ -624,9 +645,13 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor |
     dx_k, dx_v, dwq, dwk): bf16 gradients of the inputs (dense unless given, e.g. as
     slices of the packed projection's gradient) and fp32 [128] weight gradients, which
     accumulate adds into; a weight gradient is returned for each weight given."""
+    if stream is not None:
+        with _as_current(stream):
+            return qk_norm_rope_bwd(q, k, positions, rotary, dq, dk, dv, wq, wk, norm, eps,
+                                    weight_offset, dx_q, dx_k, dx_v, dwq, dwk, accumulate)
     dev, T, hq, hkv, qr, kr, ns, rs, pp = _stage_args(q, k, positions, rotary, wq, wk, norm, eps,
                                                       weight_offset)
-    st = _dev_stream(dev, stream)
+    st = _dev_stream(dev)
     dt = dq.dtype
     if dt is not torch.float32 and dt is not torch.bfloat16:
         raise ValueError("dq must be fp32 or bf16")
@@ -647,18 +672,16 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor |
         dwq = torch.empty(HEAD_DIM, dtype=torch.float32, device=q.device)
     if wk is not None and dwk is None:
         dwk = torch.empty(HEAD_DIM, dtype=torch.float32, device=q.device)
-    pq = pk = ws = None
-    nbytes = 0
+    pq = pk = None
     if dwq is not None:
         pq = _dense(dwq, "dwq", torch.float32, (HEAD_DIM,), dev)
     if dwk is not None:
         pk = _dense(dwk, "dwk", torch.float32, (HEAD_DIM,), dev)
-    if pq is not None or pk is not None:
-        buf = _call_workspace(B.ls_qk_norm_rope_bwd_workspace(T), q, "qk_norm", st)
-        ws, nbytes = buf.data_ptr(), buf.numel()
-    B.ls_qk_norm_rope_bwd(_view(qr, kr), T, hq, hkv, ns, rs, pp, _view(gq, gk, gv),
-                          B.LS_FP32 if dt is torch.float32 else B.LS_BF16, int(accumulate),
-                          _view(oq, ok, ov), pq, pk, ws, nbytes, st)
+    _with_workspace(B.ls_qk_norm_rope_bwd,
+                    (_view(qr, kr), T, hq, hkv, ns, rs, pp, _view(gq, gk, gv),
+                     B.LS_FP32 if dt is torch.float32 else B.LS_BF16, int(accumulate),
+                     _view(oq, ok, ov), pq, pk),
+                    lambda: B.ls_qk_norm_rope_bwd_workspace(T), q, "qk_norm", st)
     return dx_q, dx_k, dx_v, dwq, dwk
 
 
@@ -697,9 +720,13 @@ def qk_norm_rope_append(pool: PagePool, q: torch.Tensor, k: torch.Tensor, v: tor
     """qk_norm_rope_fwd with keys and values written into `pool` at slots[t] = page *
     page_size + offset (int32 [T]; negative: a padding token, nothing of it is written).
     Returns q_out."""
+    if stream is not None:
+        with _as_current(stream):
+            return qk_norm_rope_append(pool, q, k, v, slots, positions, rotary, wq, wk, norm, eps,
+                                       weight_offset, q_out)
     dev, T, hq, hkv, qr, kr, ns, rs, pp = _stage_args(q, k, positions, rotary, wq, wk, norm, eps,
                                                       weight_offset)
-    st = _dev_stream(dev, stream)
+    st = _dev_stream(dev)
     if hkv != pool.num_kv_heads or pool.device_indices - {dev}:
         raise ValueError("the pool has other key heads or is on another device")
     vr = _rows(v, "v", torch.bfloat16, (T, hkv, HEAD_DIM), dev)
@@ -751,8 +778,11 @@ def extend_pages(alloc: PageAllocator, add: torch.Tensor, pos0: int, slots: torc
     the last token) and positions int32 [axes][capacity] (pos0 + index within the
     response), enters new pages into the table and advances alloc.lens and alloc.used (or
     writes them to lens_out / used_out).  See ls_extend_pages for what is refused."""
+    if stream is not None:
+        with _as_current(stream):
+            return extend_pages(alloc, add, pos0, slots, positions, lens_out, used_out)
     M, dev, i32 = alloc.members, alloc.device_index, torch.int32
-    st = _dev_stream(dev, stream)
+    st = _dev_stream(dev)
     cap = slots.shape[0] if slots.dim() == 1 else -1
     sp = _dense(slots, "slots", i32, (cap,), dev)
     axes, pp = 1, None
@@ -798,13 +828,17 @@ def decode_attn(cache: PagedKVCache, resp: ResponseCache, q: torch.Tensor, softm
     """Attention of a decode step: q [members][n][Hq][128], the n newest tokens of every
     member (already appended to its pages), over the shared prompt and the member's own
     response.  Returns (o, lse)."""
+    if stream is not None:
+        with _as_current(stream):
+            return decode_attn(cache, resp, q, softmax_scale, o, lse)
     if q.dim() != 4:
         raise ValueError("q must be [members][n][Hq][128]")
     _, n, hq, _ = shape = q.shape
     M, dev = resp.members, resp.device_index
-    st = _dev_stream(dev, stream)
-    if cache.page_table.get_device() != dev:
-        raise ValueError("the prompt's page table is on another device")
+    st = _dev_stream(dev)
+    if (cache.page_table.get_device() != dev or cache.k_pool.get_device() not in (-1, dev)
+            or cache.v_pool.get_device() not in (-1, dev)):
+        raise ValueError("the prompt's pages are on another device")
     qp = _dense(q, "q", torch.bfloat16, (M, n, hq, HEAD_DIM), dev)
     if o is None:
         o = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
@@ -812,14 +846,7 @@ def decode_attn(cache: PagedKVCache, resp: ResponseCache, q: torch.Tensor, softm
         lse = torch.empty((M, n, hq), dtype=torch.float32, device=q.device)
     op = _dense(o, "o", torch.bfloat16, shape, dev)
     lp = _dense(lse, "lse", torch.float32, (M, n, hq), dev)
-    ws = _call_workspace(0, q, "decode", st)
-    args = (cache.struct, resp.struct, qp, n, hq, softmax_scale, op, lp)
-    try:
-        B.ls_decode_attn(*args, ws.data_ptr(), ws.numel(), st)
-    except B.LongstrawError as e:  # nothing was launched: the workspace has to grow
-        if e.status != B.LS_ERR_WORKSPACE:
-            raise
-        ws = _call_workspace(B.ls_decode_attn_workspace(cache.struct, resp.struct, n, hq), q,
-                             "decode", st)
-        B.ls_decode_attn(*args, ws.data_ptr(), ws.numel(), st)
+    _with_workspace(B.ls_decode_attn, (cache.struct, resp.struct, qp, n, hq, softmax_scale, op, lp),
+                    lambda: B.ls_decode_attn_workspace(cache.struct, resp.struct, n, hq), q,
+                    "decode", st)
     return o, lse

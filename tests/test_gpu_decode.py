@@ -311,3 +311,60 @@ def test_layered_responses(cuda):
                 assert (rl[R - 1] - lse[m, 0]).abs().max() <= 1e-5
         done = [d + a for d, a in zip(done, add)]
     assert r.alloc.lens.tolist() == done and B.ls_last_device_error(0) == B.LS_OK
+
+
+def test_two_graphs_of_one_stream_at_once(cuda):
+    """Decode steps captured on one stream and replayed on two: each has its workspace."""
+    st, other = torch.cuda.Stream(), torch.cuda.Stream()
+    runs = []
+    for seed in (30, 31):
+        g = Group(cuda, 60000, [500, 90, 1], 12, 2, seed=seed)
+        want = g.run()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            got = api.decode_attn(g.cache, g.resp, g.q, SCALE)
+        runs.append((graph, got, want, g))
+    for _ in range(30):
+        for (graph, *_), on in zip(runs, (st, other)):
+            with torch.cuda.stream(on):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, got, want, _ in runs:
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert B.ls_last_device_error(0) == B.LS_OK
+
+
+def test_shared_pages_and_responses_in_host_memory(cuda):
+    """Two members over the same response pages; pages appended to and read in pinned host
+    memory; pages further than 2^32 elements into a pool."""
+    g = Group(cuda, 300, [70, 70, 5], 8, 2, rps=16, seed=32)
+    g.resp.block_table[1] = g.resp.block_table[0]
+    g.kr[1], g.vr[1], g.q[1] = g.kr[0], g.vr[0], g.q[0]
+    o, lse = g.run()
+    g.check(o, lse)
+    assert torch.equal(o[0], o[1]) and torch.equal(lse[0], lse[1])
+
+    n = 5
+    slots = torch.tensor([3, 2, 17, 40, -1], dtype=torch.int32, device=cuda)
+    x = torch.randn(n, 3, 128, device=cuda).to(torch.bfloat16)
+    args = (x[:, :1].expand(n, 4, 128), x[:, 1:2], x[:, 2:], slots, None, None)
+    dev = api.PagePool.empty(3, 1, 16, cuda)
+    dev.k_pool.zero_(), dev.v_pool.zero_()
+    host = api.PagePool(*(torch.zeros(3, 1, 16, 128, dtype=torch.bfloat16, pin_memory=True) for _ in "kv"))
+    for pool in (dev, host):
+        q = api.qk_norm_rope_append(pool, *args)
+    torch.cuda.synchronize()
+    assert torch.equal(host.k_pool, dev.k_pool.cpu()) and torch.equal(host.v_pool, dev.v_pool.cpu())
+    cache = api.PagedKVCache(1, torch.zeros(1, dtype=torch.int32, device=cuda), 16, 1, 0)
+    table = torch.tensor([[0, 1, 2], [2, 0, 1]], dtype=torch.int32, device=cuda)
+    lens = torch.tensor([48, 20], dtype=torch.int32, device=cuda)
+    out = [api.decode_attn(cache, api.ResponseCache(pool, table, lens), q[:2].view(2, 1, 4, 128), SCALE)
+           for pool in (dev, host)]
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+
+    far = 2 ** 21
+    big = api.PagePool.empty(far + 3, 1, 16, cuda)
+    big.k_pool[far:], big.v_pool[far:] = dev.k_pool, dev.v_pool
+    got = api.decode_attn(cache, api.ResponseCache(big, table + far, lens), q[:2].view(2, 1, 4, 128), SCALE)
+    assert torch.equal(out[0][0], got[0]) and torch.equal(out[0][1], got[1])
+    assert B.ls_last_device_error(0) == B.LS_OK

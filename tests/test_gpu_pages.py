@@ -144,3 +144,17 @@ def test_steps_in_a_graph(cuda):
     assert pos.tolist() == [[46, 46, 46, 0]] and all(s[3] == -1 for s in seen)
     flat = [x for s in seen for x in s[:3]]
     assert len(set(flat)) == 120 and B.ls_last_device_error(0) == B.LS_OK
+
+
+def test_no_members_and_lengths_over_the_counts(cuda):
+    """Nothing to extend still fills the outputs; lens_out may lie over add."""
+    Case(cuda, [], [], 16, capacity=0).check(False)
+    Case(cuda, [], [], 16, capacity=9).check(False)
+    lens, add = list(range(64)), [90 + i for i in range(64)]  # several blocks
+    c, ref = Case(cuda, lens, add, 16), Case(cuda, lens, add, 16)
+    api.extend_pages(ref.alloc, ref.add, 3, ref.slots, ref.pos)
+    used = torch.empty_like(c.alloc.used)
+    api.extend_pages(c.alloc, c.add, 3, c.slots, c.pos, lens_out=c.add, used_out=used)
+    assert torch.equal(c.slots, ref.slots) and torch.equal(c.pos, ref.pos)
+    assert torch.equal(c.add, ref.alloc.lens) and torch.equal(used, ref.alloc.used)
+    assert c.alloc.lens.tolist() == lens and B.ls_last_device_error(0) == B.LS_OK

@@ -323,3 +323,74 @@ def test_other_stream_and_graph(cuda):
     for t, w in zip((q, k, dxq, dxk, dwq, dwk), got):
         assert torch.equal(t, w)
     ok()
+
+
+def test_two_graphs_of_one_stream_at_once(cuda):
+    """Backward passes captured on one stream and replayed on two: each has its workspace."""
+    st, other = torch.cuda.Stream(), torch.cuda.Stream()
+    runs = []
+    for seed in (3, 4):
+        s = Stage(cuda, 9000, 8, 2, 128, seed=seed)
+        dy = [torch.randn(9000, h, 128, device=cuda, generator=gen(seed, cuda)) for h in (8, 2)]
+        args = (s.q, s.k, s.pos, s.rot, dy[0], dy[1])
+        want = api.qk_norm_rope_bwd(*args, wq=s.wq, wk=s.wk)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            got = api.qk_norm_rope_bwd(*args, wq=s.wq, wk=s.wk)
+        runs.append((g, got, want, (s, dy)))  # a graph needs its inputs alive
+    for _ in range(20):
+        for (g, got, _, _), on in zip(runs, (st, other)):
+            with torch.cuda.stream(on):
+                g.replay()
+    torch.cuda.synchronize()
+    for _, got, want, _ in runs:
+        for i in (0, 1, 3, 4):
+            assert torch.equal(got[i], want[i])
+    ok()
+
+
+def test_a_given_stream_owns_what_the_call_allocates(cuda):
+    """Memory that the current stream has freed but still uses is not handed to a call on
+    another stream."""
+    s = Stage(cuda, 300, 8, 2, 128, seed=5)
+    want = api.qk_norm_rope_fwd(s.q, s.k, s.v, s.pos, s.rot, s.wq, s.wk)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for given in (st, st.cuda_stream):
+        freed = torch.empty_like(want[0])
+        at = freed.data_ptr()
+        del freed
+        got = api.qk_norm_rope_fwd(s.q, s.k, s.v, s.pos, s.rot, s.wq, s.wk, stream=given)
+        assert got[0].data_ptr() != at
+        st.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+    ok()
+
+
+def test_offsets_past_32_bits(cuda):
+    """Rows further than 2^32 elements into their tensors and pages."""
+    T, far = 3, 2 ** 31 + 2 ** 20
+    s = Stage(cuda, T, 2, 1, 128, seed=6)
+    big = torch.empty(2 * far + 1024, dtype=torch.bfloat16, device=cuda)
+    q = big.as_strided((T, 2, 128), (far, 128, 1))
+    k = big.as_strided((T, 1, 128), (far, 128, 1), 256)
+    q.copy_(s.q)
+    k.copy_(s.k)
+    want = api.qk_norm_rope_fwd(s.q, s.k, None, s.pos, s.rot, s.wq, s.wk)
+    got = api.qk_norm_rope_fwd(q, k, None, s.pos, s.rot, s.wq, s.wk)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    dy = [torch.randn(T, h, 128, device=cuda) for h in (2, 1)]
+    want_b = api.qk_norm_rope_bwd(s.q, s.k, s.pos, s.rot, dy[0], dy[1], wq=s.wq, wk=s.wk)
+    got_b = api.qk_norm_rope_bwd(q, k, s.pos, s.rot, dy[0], dy[1], wq=s.wq, wk=s.wk, dx_q=q, dx_k=k)
+    for x, y in zip(got_b, want_b):
+        assert (x is None and y is None) or torch.equal(x, y)
+    del big, q, k, got_b
+    n = 2 ** 21 + 8  # pages of 16 rows of one head: 2^32 elements and some
+    pool = api.PagePool.empty(n, 1, 16, cuda)
+    slots = torch.tensor([n * 16 - 1, 5, n * 16 - 100], dtype=torch.int32, device=cuda)
+    api.qk_norm_rope_append(pool, s.q, s.k, s.v, slots, s.pos, s.rot, s.wq, s.wk)
+    at = slots.long()
+    assert torch.equal(pool.k_pool[at // 16, 0, at % 16], want[1][:, 0])
+    assert torch.equal(pool.v_pool[at // 16, 0, at % 16], s.v[:, 0])
+    ok()

@@ -46,6 +46,7 @@ BAD_COMMON = [
     (dict(T=2 ** 31), B.LS_ERR_UNSUPPORTED),
     (dict(Hq=0), B.LS_ERR_INVALID_ARG),
     (dict(norm=norm(eps=0.0)), B.LS_ERR_INVALID_ARG),
+    (dict(norm=norm(eps=1e-39)), B.LS_ERR_INVALID_ARG),
     (dict(norm=norm(eps=float("nan"))), B.LS_ERR_INVALID_ARG),
     (dict(norm=norm(w_offset=float("inf"))), B.LS_ERR_INVALID_ARG),
     (dict(norm=norm(w_dtype=7)), B.LS_ERR_INVALID_ARG),
