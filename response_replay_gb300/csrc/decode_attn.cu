@@ -64,6 +64,7 @@ constexpr uint32_t kOffBar = kOffV + kRing * kTileBytes;
 constexpr uint32_t kSmemBytes = kOffBar + 512 + 1024;
 constexpr int kMaxBoxes = kTile / 16;  // a tile's pages at the smallest page size
 constexpr int kHalfKeys = kTile / 2;
+constexpr int kSegTiles = 3;  // a segment's beginning and end take a CTA as long as so many tiles
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;
 
@@ -112,14 +113,21 @@ __device__ __forceinline__ int32_t clamp_len(const LsDecodeArgs& a, int32_t len)
 __device__ __forceinline__ int32_t tiles_of(int32_t len) {
   return (int32_t)(((long long)len + kTile - 1) / kTile);
 }
+// Units of the cut: the keys of one source under one KV head weigh their tiles and, in front
+// of them, kSegTiles more.  (With tiles alone a CTA got up to 85 responses of one tile each
+// at 64 members of a few tokens over 262,139: 317 us, with 1 more 247, with 2 180, with 3
+// 178, with 5 190; at 8 members 142, 110, 97, 97, 97.)
+__device__ __forceinline__ int32_t units_of(int32_t tiles) {
+  return tiles > 0 ? tiles + kSegTiles : 0;
+}
 
-// The cut of the tile sequence.  Weights: a prompt tile occupies the rts CTAs of a column,
-// a response tile one of them, so the sequence weighs rts tp + tr in CTA tiles.
+// The cut of the sequence.  A unit of the prompt occupies the rts CTAs of a column, a unit of
+// a response one of them, so the sequence weighs rts tp + (responses' units).
 struct Cut {
   int32_t tp, rts, cols;
   long long w;
-  __device__ __forceinline__ Cut(const LsDecodeArgs& a, int32_t resp_tiles)
-      : tp(a.nt * a.hkv), rts(a.rts), cols(a.cols), w((long long)rts * tp + resp_tiles) {}
+  __device__ __forceinline__ Cut(const LsDecodeArgs& a, int32_t resp_units)
+      : tp(units_of(a.nt) * a.hkv), rts(a.rts), cols(a.cols), w((long long)rts * tp + resp_units) {}
   __device__ __forceinline__ void prompt(int32_t col, int32_t* b, int32_t* e) const {
     *b = bound(col);
     *e = bound(col + 1);
@@ -154,41 +162,51 @@ struct Seg {
 struct Walk {
   const LsDecodeArgs& a;
   int32_t p, p_end, r, r_end;
-  int32_t m, off;       // member and tile within its hkv x nt tiles
+  int32_t m, off;       // member and unit within its KV heads' units
   __device__ __forceinline__ Walk(const LsDecodeArgs& a_, const volatile int32_t* start, int32_t p0,
                                   int32_t p1, int32_t r0, int32_t r1)
       : a(a_), p(p0), p_end(p1), r(r0), r_end(r1), m(start[0]), off(start[1]) {}
   __device__ __forceinline__ bool next(Seg* s) {
-    if (p < p_end) {
-      const int32_t h = p / a.nt, first = p - h * a.nt;
+    while (p < p_end) {
+      const int32_t nu = units_of(a.nt), h = p / nu, x = p - h * nu, step = min(p_end - p, nu - x);
+      p += step;
+      if (!tiles(s, x, step)) continue;
       s->resp = false;
       s->kvh = s->item = h;
       s->m = 0;
       s->len = (int32_t)a.P;
-      s->key0 = first * kTile;
-      s->count = min(p_end - p, a.nt - first);
-      p += s->count;
       return true;
     }
-    if (r >= r_end) return false;
-    int32_t len = 0, nt = 0;
-    for (; m < a.M; ++m, off = 0) {
-      len = clamp_len(a, __ldg(a.lens + m));
-      nt = tiles_of(len);
-      if (off < nt * a.hkv) break;
+    while (r < r_end) {
+      int32_t len = 0, nt = 0, nu = 0;
+      for (; m < a.M; ++m, off = 0) {
+        len = clamp_len(a, __ldg(a.lens + m));
+        nt = tiles_of(len);
+        nu = units_of(nt);
+        if (off < nu * a.hkv) break;
+      }
+      if (m >= a.M) return false;  // only when lengths changed under the kernel
+      const int32_t h = off / nu, x = off - h * nu, step = min(r_end - r, nu - x);
+      r += step;
+      off += step;
+      if (!tiles(s, x, step)) continue;
+      s->resp = true;
+      s->kvh = h;
+      s->m = m;
+      s->item = m * a.hkv + h;
+      s->len = len;
+      return true;
     }
-    if (m >= a.M) return false;  // only when lengths changed under the kernel
-    const int32_t h = off / nt, first = off - h * nt;
-    s->resp = true;
-    s->kvh = h;
-    s->m = m;
-    s->item = m * a.hkv + h;
-    s->len = len;
+    return false;
+  }
+
+ private:
+  // the tiles among units x .. x + step - 1 of a source; none: they are another CTA's
+  __device__ __forceinline__ static bool tiles(Seg* s, int32_t x, int32_t step) {
+    const int32_t first = max(x - kSegTiles, 0);
     s->key0 = first * kTile;
-    s->count = min(r_end - r, nt - first);
-    r += s->count;
-    off += s->count;
-    return true;
+    s->count = x + step - kSegTiles - first;
+    return s->count > 0;
   }
 };
 
@@ -261,14 +279,24 @@ struct Loader {
 
 // Rows of a partial: prompt partials first, then the responses'.  (item + CTA in walk
 // order) numbers a CTA's segments uniquely: from one segment to the next of the whole
-// sequence the item, the CTA or both grow.
+// sequence the item, the CTA or both grow.  Eight rows lie together, four values of each in
+// turn: a warp of the main kernel, which has a row a lane, writes whole 128-byte lines, and a
+// warp of the combine reads the rows of one KV head's group with whole sectors.  (Row by row,
+// a warp's stores met 32 lines each: 128 rows took more than 4 us to write, and the same cut
+// 262 us where this takes 232 at 64 members.)
+__host__ __device__ __forceinline__ int32_t resp_rows_of(const LsDecodeArgs& a) {
+  return (a.n * a.g + 7) & ~7;
+}
 __device__ __forceinline__ int64_t prompt_row0(const LsDecodeArgs& a, int32_t h, int32_t col,
                                                int32_t rt, int t) {
   return ((((int64_t)h + col) * a.rts + rt) * 2 + t) * kTile;
 }
 __device__ __forceinline__ int64_t resp_row0(const LsDecodeArgs& a, int64_t prompt_rows,
                                              int32_t item, int32_t cta, int t) {
-  return prompt_rows + (((int64_t)item + cta) * 2 + t) * (a.n * a.g);
+  return prompt_rows + (((int64_t)item + cta) * 2 + t) * resp_rows_of(a);
+}
+__device__ __forceinline__ float* part_at(const LsDecodeArgs& a, int64_t row) {
+  return a.part_o + (row >> 3) * (8 * kD) + (row & 7) * 4;  // values 4 c .. 4 c + 3 at 32 c
 }
 __host__ __device__ __forceinline__ int64_t prompt_rows_of(const LsDecodeArgs& a) {
   return a.nt > 0 ? ((int64_t)a.hkv + a.cols) * a.rts * 2 * kTile : 0;
@@ -288,7 +316,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
 
   // the combine may be launched: its blocks wait for this grid before they read from it
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // ---- response tiles before each member, summed by the whole CTA (scratch: the ring,
+  // ---- units of the responses before each member, summed by the whole CTA (scratch: the ring,
   // which no copy has touched yet)
   int32_t p0, p1, r0, r1;
   {
@@ -301,7 +329,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
         const int32_t len = __ldg(a.lens + m);
         const int32_t cl = clamp_len(a, len);
         if (len > cl && cta == 0) ls_report(a.err, LS_DEVERR_CHECK);
-        mine += tiles_of(cl);
+        mine += units_of(tiles_of(cl));
       }
     }
     int32_t sum = mine;
@@ -323,18 +351,18 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     const Cut cut(a, total * a.hkv);
     cut.prompt(col, &p0, &p1);
     cut.resp(col, rt, &r0, &r1);
-    // the member whose tiles hold r0
+    // the member whose units hold r0
     int32_t pre = before + sum - mine;
     if (r0 < r1 && pre * a.hkv <= r0 && r0 < (pre + mine) * a.hkv) {
       for (int i = 0; i < per; ++i) {
         const int m = tid * per + i;
-        const int32_t nt = tiles_of(clamp_len(a, __ldg(a.lens + m)));
-        if (r0 < (pre + nt) * a.hkv) {
+        const int32_t nu = units_of(tiles_of(clamp_len(a, __ldg(a.lens + m))));
+        if (r0 < (pre + nu) * a.hkv) {
           start[0] = m;
           start[1] = r0 - pre * a.hkv;
           break;
         }
-        pre += nt;
+        pre += nu;
       }
     }
     if (p0 >= p1 && r0 >= r1) return;  // uniform: no tiles for this CTA
@@ -412,7 +440,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     RingPos<kRing> ring;
     uint32_t fills = 0, aux_phase = 0, seg = 0;
     Loader ld;
-    auto load_q = [&](uint32_t n_seg) {
+    auto start_q = [&](uint32_t n_seg) {
       const int rows = seg_rows(a, s, rt);
       const uint32_t buf = sbase + q_offset(whole_q(a, s, rt), n_seg);
       const int32_t row0 = s.resp ? s.m * a.n * a.g : rt * kTile;
@@ -424,13 +452,15 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
         cp_async16(buf + (c >> 3) * kHalfBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4), src);
         for (head += 2; head >= a.g; head -= a.g) ++token;
       }
+    };
+    auto finish_q = [&](uint32_t n_seg) {
       cp_async_wait_all();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_addr(sbase, B_Q_FULL + (n_seg & 1)));
     };
     bool ok = true, have = walk.next(&s);
-    if (have) load_q(0);
+    if (have) start_q(0);
     for (; ok && have; ++seg) {
       if (lane == 0) ld.open(a, s, &tm.vp, &tm.vr);
       uint32_t st = 0;
@@ -443,6 +473,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
           ld.load(sbase + kOffV + st * kTileBytes, bar_addr(sbase, (ragged ? B_AUX : B_V_FULL) + st),
                   j + 1 < s.count, a.err);
         }
+        if (fills == 0) finish_q(0);
         ring.advance();
         ++fills;
       }
@@ -457,7 +488,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
         if (ok && (whole || whole_q(a, s, rt)))
           ok = wait_bar(bar_addr(sbase, B_Q_EMPTY + (seg & 1)), (seg >> 1) & 1);
         if (!ok) break;
-        load_q(seg + 1);
+        start_q(seg + 1);
       }
       if (left < kTile) {  // the segment's last tile passes its source's end
         ok = wait_bar(bar_addr(sbase, B_AUX + st), (aux_phase >> st) & 1);
@@ -472,8 +503,10 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_addr(sbase, B_V_FULL + st));
       }
+      if (have) finish_q(seg + 1);  // its rows came meanwhile
     }
     if (!ok) fail();
+    cp_async_wait_all();
     for (uint32_t i = fills > kRing ? fills - kRing : 0; i < fills; ++i)
       mbar_wait(bar_addr(sbase, B_V_FULL + i % kRing), (i / kRing) & 1);
   } else if (warp == 1) {
@@ -654,7 +687,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
         const int64_t prow =
             (s.resp ? resp_row0(a, prompt_rows, s.item, cta, t) : prompt_row0(a, s.item, col, rt, t)) +
             row;
-        float* po = a.part_o + prow * kD;
+        float* po = part_at(a, prow);
 #pragma unroll 1
         for (int c0 = 0; c0 < 128; c0 += 32) {
           uint32_t ov[32];
@@ -664,7 +697,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
           if (row < rows) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(po + c0 + i) =
+              *reinterpret_cast<float4*>(po + (c0 + i) * 8) =
                   make_float4(__uint_as_float(ov[i]) * inv, __uint_as_float(ov[i + 1]) * inv,
                               __uint_as_float(ov[i + 2]) * inv, __uint_as_float(ov[i + 3]) * inv);
           }
@@ -684,32 +717,33 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
 }
 
 // Merge a row's partials: lse = log2 sum 2^lse_k, o = sum 2^(lse_k - lse) o_k, in a fixed
-// order.  A block per row (the 76 partials of a row of a 2,097,152-token prompt are read by
-// eight warps at once: one warp a row took 36 us for 192 rows).  The row's partials lie
-// in the columns and CTAs whose parts of the sequence meet the row's keys; a thread looks
-// at one column and one CTA.  That much needs only the lengths, so the launch overlaps the
-// main kernel's end and waits for it then.
+// order.  A block takes up to eight heads of one token and KV head, whose partials lie in the
+// same columns and CTAs, and 32 of their 128 values; a lane has the values of one head.  Its
+// eight warps take the partials by turns (at 2,097,152 tokens and 4 KV heads there are 76
+// columns' worth), four at a time with a running maximum, so that nothing waits for the
+// maximum of all; then the warps' sums are merged.  Which columns and CTAs meet the keys, a
+// thread looks at one of each, needs only the lengths, so the launch overlaps the main
+// kernel's end and waits for it then.
 constexpr int kCombineThreads = 256;
 constexpr int kCombineWarps = kCombineThreads / 32;
-constexpr int kMaxParts = 1024;  // 2 halves of 256 columns and 256 CTAs at most
 
 __global__ void __launch_bounds__(kCombineThreads)
 decode_combine(const __grid_constant__ LsDecodeArgs a) {
-  __shared__ float wt[kMaxParts];
-  __shared__ float4 acc[kCombineWarps][32];
+  __shared__ __align__(16) float acc[kCombineWarps][2][32][4];
   __shared__ int32_t sums[2][kCombineWarps];
-  __shared__ float red[kCombineWarps];
-  __shared__ uint16_t from[2][kCombineThreads];  // columns, CTAs with partials of the row
+  __shared__ float red[2][kCombineWarps][8];     // maximum, sum; by warp and head
+  __shared__ uint16_t from[2][kCombineThreads];  // columns, CTAs with partials of the rows
   __shared__ int32_t counts[2][kCombineWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int32_t token = blockIdx.x / a.hq, head = blockIdx.x - token * a.hq;
-  const int32_t m = token / a.n, kvh = head / a.g;
+  const int32_t octets = (a.g + 7) >> 3, group = (blockIdx.x >> 2) / octets;
+  const int32_t head0 = 8 * ((blockIdx.x >> 2) - group * octets), col0 = 32 * (blockIdx.x & 3);
+  const int32_t token = group / a.hkv, kvh = group - token * a.hkv, m = token / a.n;
   const int32_t len = __ldg(a.lens + m);
   if (len < 0) return;  // a member out of use: its rows stay as they were
   const int32_t nt = tiles_of(clamp_len(a, len));
   int32_t tot = 0, pre = 0;
   for (int i = tid; i < a.M; i += kCombineThreads) {
-    const int32_t x = tiles_of(clamp_len(a, __ldg(a.lens + i)));
+    const int32_t x = units_of(tiles_of(clamp_len(a, __ldg(a.lens + i))));
     tot += x;
     if (i < m) pre += x;
   }
@@ -729,7 +763,7 @@ decode_combine(const __grid_constant__ LsDecodeArgs a) {
   const Cut cut(a, tot * a.hkv);
   bool hit[2] = {false, false};
   {
-    const int32_t pb = kvh * a.nt, rb = pre * a.hkv + kvh * nt;
+    const int32_t pb = kvh * units_of(a.nt) + kSegTiles, rb = pre * a.hkv + kvh * units_of(nt) + kSegTiles;
     int32_t b, e;
     if (tid < a.cols) {
       cut.prompt(tid, &b, &e);
@@ -760,67 +794,93 @@ decode_combine(const __grid_constant__ LsDecodeArgs a) {
   }
   __syncthreads();
   const int32_t np = 2 * all[0], count = np + 2 * all[1];
-  // row of all rows (token, head of the group) against the prompt; row of the member's own
-  const int32_t grow = token * a.g + head % a.g, mrow = grow - m * a.n * a.g;
+  // a lane's head (behind the last one: that one again): row of all rows (token, head of the
+  // group) against the prompt, row of the member's own
+  const int32_t grow = token * a.g + min(head0 + (lane & 7), a.g - 1), mrow = grow - m * a.n * a.g;
   const int64_t prompt0 = prompt_row0(a, kvh, 0, grow / kTile, 0) + grow % kTile;
   const int64_t resp0 = resp_row0(a, prompt_rows_of(a), m * a.hkv + kvh, 0, 0) + mrow;
+  const int32_t resp_rows = resp_rows_of(a);
   auto part_row = [&](int k) {
     if (k < np) return prompt0 + ((int64_t)from[0][k >> 1] * a.rts * 2 + (k & 1)) * kTile;
     k -= np;
-    return resp0 + ((int64_t)from[1][k >> 1] * 2 + (k & 1)) * (a.n * a.g);
+    return resp0 + ((int64_t)from[1][k >> 1] * 2 + (k & 1)) * resp_rows;
   };
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  float mx = -INFINITY;
-  for (int k = tid; k < count; k += kCombineThreads) {
-    const float v = __ldcg(a.part_lse + part_row(k));
-    wt[k] = v;
-    mx = fmaxf(mx, v);
-  }
+  constexpr int kBatch = 4;
+  float mx = -INFINITY, sum = 0.f;
+  float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int k0 = warp; k0 < count; k0 += kBatch * kCombineWarps) {
+    float l[kBatch], top = mx;
+    float4 v[kBatch][2];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (lane == 0) red[warp] = mx;
-  __syncthreads();
+    for (int i = 0; i < kBatch; ++i) {
+      const int k = k0 + i * kCombineWarps;
+      l[i] = -INFINITY;
+      if (k < count) {
+        const int64_t row = part_row(k);
+        const float* p = part_at(a, row) + (col0 / 4 + (lane >> 3)) * 32;
+        l[i] = __ldcg(a.part_lse + row);
+        v[i][0] = __ldcg(reinterpret_cast<const float4*>(p));
+        v[i][1] = __ldcg(reinterpret_cast<const float4*>(p + 128));
+      }
+    }
 #pragma unroll
-  for (int i = 0; i < kCombineWarps; ++i) mx = fmaxf(mx, red[i]);
-  const float msub = mx == -INFINITY ? 0.f : mx;
-  float sum = 0.f;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = warp; k < count; k += kCombineWarps) {
-    const float w = exp2f(wt[k] - msub);
-    // a half that saw no key adds nothing
-    const float4 v = w == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                              : __ldcg(reinterpret_cast<const float4*>(a.part_o + part_row(k) * kD) + lane);
-    sum += w;
-    s.x = fmaf(w, v.x, s.x);
-    s.y = fmaf(w, v.y, s.y);
-    s.z = fmaf(w, v.z, s.z);
-    s.w = fmaf(w, v.w, s.w);
+    for (int i = 0; i < kBatch; ++i) top = fmaxf(top, l[i]);
+    const float sub = top == -INFINITY ? 0.f : top, keep = exp2f(mx - sub);
+    mx = top;
+    sum *= keep;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      s[h] = make_float4(s[h].x * keep, s[h].y * keep, s[h].z * keep, s[h].w * keep);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float w = exp2f(l[i] - sub);
+      sum += w;
+      if (l[i] == -INFINITY) continue;  // a half that saw no key adds nothing
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        s[h].x = fmaf(w, v[i][h].x, s[h].x);
+        s[h].y = fmaf(w, v[i][h].y, s[h].y);
+        s[h].z = fmaf(w, v[i][h].z, s[h].z);
+        s[h].w = fmaf(w, v[i][h].w, s[h].w);
+      }
+    }
   }
-  acc[warp][lane] = s;
-  __syncthreads();  // red has been read
-  if (lane == 0) red[warp] = sum;
+  *reinterpret_cast<float4*>(acc[warp][0][lane]) = s[0];
+  *reinterpret_cast<float4*>(acc[warp][1][lane]) = s[1];
+  if (lane < 8) {
+    red[0][warp][lane] = mx;
+    red[1][warp][lane] = sum;
+  }
   __syncthreads();
-  if (tid >= kD) return;
+  // a thread a value: four values of eight heads a warp
+  const int h = lane & 7, e = lane >> 3;
+  if (head0 + h >= a.g) return;
+  mx = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kCombineWarps; ++i) mx = fmaxf(mx, red[0][i][h]);
+  const float sub = mx == -INFINITY ? 0.f : mx;
   sum = 0.f;
   float o = 0.f;
 #pragma unroll
   for (int i = 0; i < kCombineWarps; ++i) {
-    sum += red[i];
-    o += reinterpret_cast<const float*>(acc[i])[tid];
+    const float w = exp2f(red[0][i][h] - sub);
+    sum = fmaf(w, red[1][i][h], sum);
+    o = fmaf(w, acc[i][warp >> 2][(warp & 3) * 8 + h][e], o);
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key at all: o = 0, lse = -inf
-  const int64_t row = (int64_t)token * a.hq + head;
-  static_cast<__nv_bfloat16*>(a.o)[row * kD + tid] = __float2bfloat16_rn(o * inv);
-  if (tid == 0) a.lse[row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+  const int64_t row = (int64_t)token * a.hq + kvh * a.g + head0 + h;
+  static_cast<__nv_bfloat16*>(a.o)[row * kD + col0 + warp * 4 + e] = __float2bfloat16_rn(o * inv);
+  if (warp == 0 && e == 0 && col0 == 0) a.lse[row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
 }  // namespace
 
 int ls_decode_row_tile() { return kTile; }
+int ls_decode_seg_tiles() { return kSegTiles; }
 int64_t ls_decode_prompt_rows(const LsDecodeArgs& a) { return prompt_rows_of(a); }
 int64_t ls_decode_resp_rows(const LsDecodeArgs& a) {
-  return ((int64_t)a.M * a.hkv + (int64_t)a.cols * a.rts) * 2 * a.n * a.g;
+  return ((int64_t)a.M * a.hkv + (int64_t)a.cols * a.rts) * 2 * resp_rows_of(a);
 }
 
 cudaError_t ls_launch_decode_attn(const LsDecodeArgs& a, cudaStream_t st) {
@@ -848,7 +908,7 @@ cudaError_t ls_launch_decode_attn(const LsDecodeArgs& a, cudaStream_t st) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.M * a.n * a.hq));
+  cfg.gridDim = dim3((unsigned)(a.M * a.n * a.hkv * ((a.g + 7) / 8) * 4));
   cfg.blockDim = dim3(kCombineThreads);
   cfg.stream = st;
   cfg.attrs = &attr;

@@ -1006,10 +1006,11 @@ ls_status decode_args(const ls_kv_cache* c, const ls_resp_cache* r, int n, int H
   if (r->members > 0 && (!r->lens || !aligned4(r->lens) ||
                          (r->max_blocks > 0 && (!r->block_table || !aligned4(r->block_table)))))
     return LS_ERR_INVALID_ARG;
-  // tile and key counts are 32-bit numbers
+  // tile, unit and key counts are 32-bit numbers
   if (c->num_tokens >= (1ll << 31) - 128 ||
-      ((int64_t)r->max_blocks * r->pool.page_size / 128 + 1) * r->members * c->num_kv_heads >= (1ll << 31) ||
-      (c->num_tokens / 128 + 1) * c->num_kv_heads >= (1ll << 31))
+      ((int64_t)r->max_blocks * r->pool.page_size / 128 + 1 + ls_decode_seg_tiles()) * r->members *
+              c->num_kv_heads >= (1ll << 31) ||
+      (c->num_tokens / 128 + 1 + ls_decode_seg_tiles()) * c->num_kv_heads >= (1ll << 31))
     return LS_ERR_UNSUPPORTED;
   *a = LsDecodeArgs{};
   a->g = Hq / c->num_kv_heads;

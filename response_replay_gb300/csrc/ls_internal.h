@@ -285,6 +285,7 @@ struct LsDecodeArgs {
   uint32_t* err;
 };
 int ls_decode_row_tile();
+int ls_decode_seg_tiles();  // tiles' worth of time that a segment of a response takes besides
 // Rows of partial results: slots x 2 halves x rows.
 int64_t ls_decode_prompt_rows(const LsDecodeArgs& a);
 int64_t ls_decode_resp_rows(const LsDecodeArgs& a);
