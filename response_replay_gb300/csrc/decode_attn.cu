@@ -18,6 +18,14 @@
 // a tile is read from HBM once and from L2 after that.  The response lengths stay on the
 // device (a captured graph follows them): every CTA sums them when it starts.
 //
+// What bounds it.  A key and value row of 512 bytes meets at most 128 query rows, so the
+// reads are the floor up to about 100 rows and the tensor core (1,024 clocks a tile) from
+// there on.  Measured with 24 query and 4 KV heads, against the copy's 6,783 GB/s: 8 members
+// over 2,097,152 tokens 628 us, the whole of it; 64 members with up to 8,192 tokens of their
+// own over 262,139 tokens 238 us, 69%: there a tile takes 1,800 clocks, one after the other
+// through a softmax warp (scores loaded, maximum, exponentials, weights stored and handed
+// over); 2 members over 4,096 tokens (8 and 2 heads) 12 us, the latency of two launches.
+//
 // CTA (one per SM, 12 warps):
 //   warp 0      TMA producer of the segments' K tiles, page by page, into a ring of 3.
 //   warp 1      issues S = Q K^T into one of two S buffers, a tile ahead of the softmax.
@@ -31,8 +39,9 @@
 //   warps 4-7   softmax of a tile's keys 0-63, warps 8-11 of its keys 64-127, one row a
 //               thread.  Each half keeps its own running maximum, sum and O, as if it were a
 //               sequence of its own, so the two threads of a row need nothing of each other;
-//               the combine merges them like any partials.  (One warpgroup a tile, by turns,
-//               took 267 us where this takes 261 at 64 members, and spilled registers.)
+//               the combine merges them like any partials.  (At 64 members one warpgroup a
+//               tile, by turns, took 267 us where this took 261, and spilled registers; the
+//               next tile's scores loaded early took ten registers more and 272 us for 246.)
 //               Warps whose rows are all padding only keep the barriers going.
 // Tensor memory (512 columns): S_0 [0,128) S_1 [128,256) O_0 [256,384) O_1 [384,512); P_t
 // overlays the first 32 of its 64 columns of S.
@@ -116,7 +125,7 @@ __device__ __forceinline__ int32_t tiles_of(int32_t len) {
 // Units of the cut: the keys of one source under one KV head weigh their tiles and, in front
 // of them, kSegTiles more.  (With tiles alone a CTA got up to 85 responses of one tile each
 // at 64 members of a few tokens over 262,139: 317 us, with 1 more 247, with 2 180, with 3
-// 178, with 5 190; at 8 members 142, 110, 97, 97, 97.)
+// 176, with 5 190; at 8 members 142, 110, 97, 96, 97.)
 __device__ __forceinline__ int32_t units_of(int32_t tiles) {
   return tiles > 0 ? tiles + kSegTiles : 0;
 }
@@ -282,8 +291,9 @@ struct Loader {
 // sequence the item, the CTA or both grow.  Eight rows lie together, four values of each in
 // turn: a warp of the main kernel, which has a row a lane, writes whole 128-byte lines, and a
 // warp of the combine reads the rows of one KV head's group with whole sectors.  (Row by row,
-// a warp's stores met 32 lines each: 128 rows took more than 4 us to write, and the same cut
-// 262 us where this takes 232 at 64 members.)
+// a warp's stores met 32 lines each and 128 rows took more than 4 us to write: 64 responses
+// of up to 8,192 tokens took 123 us where this takes 103.  Transposed by shuffles instead,
+// the group of 64 members below took 259 us for 246.)
 __host__ __device__ __forceinline__ int32_t resp_rows_of(const LsDecodeArgs& a) {
   return (a.n * a.g + 7) & ~7;
 }

@@ -12,6 +12,10 @@
 // the count of used pages are read by every block; they are written by the only block of
 // a small call, by block 0 when they go to buffers of their own, and by a second launch
 // when a large call writes them over what it reads.
+//
+// It is bound by a launch and one dependent chain (lengths, two scans, a search, a page, a
+// slot): one token for each of 8 members 4.0 us, 282,000 tokens for 64 members 5.2 us, of
+// which the 2.2 MB of slots and positions are 0.3 us at the copy's rate.
 #include "ls_device.cuh"
 #include "ls_internal.h"
 
