@@ -19,32 +19,34 @@
 // device (a captured graph follows them): every CTA sums them when it starts.
 //
 // What bounds it.  A key and value row of 512 bytes meets at most 128 query rows, so the
-// reads are the floor up to about 100 rows and the tensor core (1,024 clocks a tile) from
-// there on.  Measured with 24 query and 4 KV heads, against the copy's 6,783 GB/s: 8 members
-// over 2,097,152 tokens 628 us, the whole of it; 64 members with up to 8,192 tokens of their
-// own over 262,139 tokens 238 us, 69%: there a tile takes 1,800 clocks, one after the other
-// through a softmax warp (scores loaded, maximum, exponentials, weights stored and handed
-// over); 2 members over 4,096 tokens (8 and 2 heads) 12 us, the latency of two launches.
+// reads are the floor up to about 100 rows and the tensor core (1,024 clocks a tile, and
+// 1,250 for the shared memory that feeds it) from there on.  Measured with 24 query and 4 KV
+// heads, against the copy's 6,783 GB/s: 8 members over 2,097,152 tokens 625 us, the whole of
+// it; 64 members with up to 8,192 tokens of their own over 262,139 tokens 243 us, 67%: there a
+// tile takes 1,650 clocks, one after the other through a softmax warp (scores loaded, maximum,
+// exchange, exponentials, weights stored and handed over); 2 members over 4,096 tokens (8 and 2
+// heads) 11.5 us, the latency of two launches.
 //
 // CTA (one per SM, 12 warps):
 //   warp 0      TMA producer of the segments' K tiles, page by page, into a ring of 3.
-//   warp 1      issues S = Q K^T into one of two S buffers, a tile ahead of the softmax.
-//   warp 2      issues O_t += P_t V over the two halves t of a tile's keys, P_t read from
-//               tensor memory.  (One thread for both kinds of MMA, and one for both kinds of
-//               load, were each the bound with several row tiles: about 2,000 clocks a tile
-//               where the tensor core needs 1,024.)
+//   warp 1      issues S = Q K^T into one of two S buffers, as soon as the softmax has the
+//               scores before the last ones in registers.
+//   warp 2      issues O += P V, P read from one of two buffers in tensor memory.
+//               (One thread for both kinds of MMA, and one for both kinds of load, were each
+//               the bound with several row tiles: about 2,000 clocks a tile.)
 //   warp 3      TMA producer of V; loads the segments' Q; clears the V rows behind a
 //               sequence's end (stale page contents, even NaN, would survive a zero weight)
 //               before such a tile is handed over.
 //   warps 4-7   softmax of a tile's keys 0-63, warps 8-11 of its keys 64-127, one row a
-//               thread.  Each half keeps its own running maximum, sum and O, as if it were a
-//               sequence of its own, so the two threads of a row need nothing of each other;
-//               the combine merges them like any partials.  (At 64 members one warpgroup a
-//               tile, by turns, took 267 us where this took 261, and spilled registers; the
-//               next tile's scores loaded early took ten registers more and 272 us for 246.)
+//               thread.  The two threads of a row exchange their maxima through shared memory
+//               and go by the larger; each rescales and writes out half of the row's O.
+//               (As two sequences with an O each, P in the place of S, nothing is exchanged
+//               but the next S waits for P V: 5 to 7% slower at 8 to 42 members of a few
+//               tokens, 1% faster at 64 with long responses.  One warpgroup a tile, by turns,
+//               was slower and spilled registers; the next tile's scores loaded before the
+//               weights are stored were slower both ways.)
 //               Warps whose rows are all padding only keep the barriers going.
-// Tensor memory (512 columns): S_0 [0,128) S_1 [128,256) O_0 [256,384) O_1 [384,512); P_t
-// overlays the first 32 of its 64 columns of S.
+// Tensor memory (512 columns): S_0 [0,128) S_1 [128,256) O [256,384) P_0 [384,448) P_1 [448,512).
 #include <math.h>
 
 #include "ls_device.cuh"
@@ -60,6 +62,7 @@ constexpr int kD = 128;
 constexpr int kTile = 128;
 constexpr int kRing = 3;  // K tiles, and V tiles, in shared memory
 constexpr int kThreads = 384;
+constexpr int kSoftmaxThreads = 256;
 constexpr uint32_t kTileBytes = kTile * kD * 2;
 constexpr uint32_t kHalfBytes = kTileBytes / 2;
 constexpr uint32_t kOffQ = 0;
@@ -70,9 +73,11 @@ constexpr uint32_t kOffV = kOffK + kRing * kTileBytes;
 // the other half's or the ring's bytes among them: rows that nothing looks at.
 constexpr int kHalfRows = kTile / 2;
 constexpr uint32_t kOffBar = kOffV + kRing * kTileBytes;
-constexpr uint32_t kSmemBytes = kOffBar + 512 + 1024;
+constexpr uint32_t kOffMax = kOffBar + 512;       // [2][2][128] fp32: buffer, key half, row
+constexpr uint32_t kSmemBytes = kOffMax + 2 * 2 * kTile * 4;
 constexpr int kMaxBoxes = kTile / 16;  // a tile's pages at the smallest page size
 constexpr int kHalfKeys = kTile / 2;
+constexpr uint32_t kColO = 2 * kTile, kColP = 3 * kTile;  // tensor memory behind the S buffers
 constexpr int kSegTiles = 3;  // a segment's beginning and end take a CTA as long as so many tiles
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;
@@ -86,8 +91,10 @@ enum {
   B_Q_FULL = B_AUX + kRing,      // 2
   B_Q_EMPTY = B_Q_FULL + 2,      // 2
   B_S_FULL = B_Q_EMPTY + 2,      // 2: S buffers
-  B_P_FULL = B_S_FULL + 2,       // 4: buffer b, key half t at 2 b + t
-  B_O_DONE = B_P_FULL + 4,
+  B_S_EMPTY = B_S_FULL + 2,      // 2: the scores are in registers
+  B_P_FULL = B_S_EMPTY + 2,      // 2: P buffers
+  B_PAIR = B_P_FULL + 2,         // 4: the two warps of 32 rows have shown their numbers
+  B_O_DONE = B_PAIR + 4,
   B_DONE,                        // 2: the S and the P V issuer
   B_COUNT = B_DONE + 2
 };
@@ -125,7 +132,8 @@ __device__ __forceinline__ int32_t tiles_of(int32_t len) {
 // Units of the cut: the keys of one source under one KV head weigh their tiles and, in front
 // of them, kSegTiles more.  (With tiles alone a CTA got up to 85 responses of one tile each
 // at 64 members of a few tokens over 262,139: 317 us, with 1 more 247, with 2 180, with 3
-// 176, with 5 190; at 8 members 142, 110, 97, 96, 97.)
+// 176, with 5 190; at 8 members 142, 110, 97, 96, 97.  Each kind cut by itself, so that every
+// CTA has its share of both, took 183 us for 169 there and 241 for 243 with long responses.)
 __device__ __forceinline__ int32_t units_of(int32_t tiles) {
   return tiles > 0 ? tiles + kSegTiles : 0;
 }
@@ -298,26 +306,29 @@ __host__ __device__ __forceinline__ int32_t resp_rows_of(const LsDecodeArgs& a) 
   return (a.n * a.g + 7) & ~7;
 }
 __device__ __forceinline__ int64_t prompt_row0(const LsDecodeArgs& a, int32_t h, int32_t col,
-                                               int32_t rt, int t) {
-  return ((((int64_t)h + col) * a.rts + rt) * 2 + t) * kTile;
+                                               int32_t rt) {
+  return (((int64_t)h + col) * a.rts + rt) * kTile;
 }
 __device__ __forceinline__ int64_t resp_row0(const LsDecodeArgs& a, int64_t prompt_rows,
-                                             int32_t item, int32_t cta, int t) {
-  return prompt_rows + (((int64_t)item + cta) * 2 + t) * resp_rows_of(a);
+                                             int32_t item, int32_t cta) {
+  return prompt_rows + ((int64_t)item + cta) * resp_rows_of(a);
 }
 __device__ __forceinline__ float* part_at(const LsDecodeArgs& a, int64_t row) {
   return a.part_o + (row >> 3) * (8 * kD) + (row & 7) * 4;  // values 4 c .. 4 c + 3 at 32 c
 }
 __host__ __device__ __forceinline__ int64_t prompt_rows_of(const LsDecodeArgs& a) {
-  return a.nt > 0 ? ((int64_t)a.hkv + a.cols) * a.rts * 2 * kTile : 0;
+  return a.nt > 0 ? ((int64_t)a.hkv + a.cols) * a.rts * kTile : 0;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
 decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsDecodeArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* smem = smem_raw;
   const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023) {  // the swizzled tiles' alignment, which the declaration asks for
+    if (threadIdx.x == 0) ls_report(a.err, LS_DEVERR_CHECK);
+    return;
+  }
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + kOffVars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffVars + 4);
   volatile int32_t* start = reinterpret_cast<volatile int32_t*>(smem + kOffVars + 8);
@@ -384,9 +395,10 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
       mbar_init(bar_addr(sbase, B_Q_FULL + i), 1);
       mbar_init(bar_addr(sbase, B_Q_EMPTY + i), 1);
       mbar_init(bar_addr(sbase, B_S_FULL + i), 1);
-      mbar_init(bar_addr(sbase, B_P_FULL + 2 * i), kTile);
-      mbar_init(bar_addr(sbase, B_P_FULL + 2 * i + 1), kTile);
+      mbar_init(bar_addr(sbase, B_S_EMPTY + i), kSoftmaxThreads);
+      mbar_init(bar_addr(sbase, B_P_FULL + i), kSoftmaxThreads);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(bar_addr(sbase, B_PAIR + i), kSoftmaxThreads / 4);
     mbar_init(bar_addr(sbase, B_O_DONE), 1);
     mbar_init(bar_addr(sbase, B_DONE), 1);
     mbar_init(bar_addr(sbase, B_DONE + 1), 1);
@@ -532,8 +544,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
         const uint32_t dq = sdesc_lo(sbase + q_offset(whole_q(a, s, rt), seg), 16);
         for (int32_t j = 0; ok && j < s.count; ++j, ++n) {
           ok = wait_bar(bar_addr(sbase, B_K_FULL + ring.stage), ring.phase);
-          // the buffer's last weights have been multiplied: the V of tile n - 2 is done with
-          if (ok && n >= 2) ok = wait_bar(bar_addr(sbase, B_V_EMPTY + (n - 2) % kRing), ((n - 2) / kRing) & 1);
+          if (ok && n >= 2) ok = wait_bar(bar_addr(sbase, B_S_EMPTY + (n & 1)), ((n - 2) >> 1) & 1);
           if (!ok || *abort_flag) break;
           tc_fence_after();
           const uint32_t b0 = dk + ((ring.stage * kTileBytes) >> 4), d_s = tmem + (n & 1) * kTile;
@@ -554,7 +565,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
       mbar_wait(bar_addr(sbase, B_DONE), 0);
     }
   } else if (warp == 2) {
-    // ------------------------------------------------------------ O_t += P_t V
+    // ------------------------------------------------------------ O += P V
     if (lane == 0) {
       const uint32_t idPV = idesc_bf16_f32(kTile, kD, true);
       const uint32_t dv = sdesc_lo(sbase + kOffV, kHalfBytes);
@@ -563,20 +574,16 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
       bool ok = true;
       while (ok && walk.next(&s)) {
         for (int32_t j = 0; ok && j < s.count; ++j, ++n) {
-          const uint32_t buf = n & 1, d_s = tmem + buf * kTile;
+          const uint32_t buf = n & 1, p_col = tmem + kColP + buf * kHalfKeys;
           const uint32_t b0 = dv + ((ring.stage * kTileBytes) >> 4);
-          ok = wait_bar(bar_addr(sbase, B_V_FULL + ring.stage), ring.phase);
+          ok = wait_bar(bar_addr(sbase, B_V_FULL + ring.stage), ring.phase) &&
+               wait_bar(bar_addr(sbase, B_P_FULL + buf), (n >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            ok = ok && wait_bar(bar_addr(sbase, B_P_FULL + 2 * buf + t), (n >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4)
-              mma_ts_lo(tmem + 256 + t * kTile, d_s + t * kHalfKeys + k4 * 8,
-                        b0 + (((4 * t + k4) * 2048) >> 4), idPV, (j > 0 || k4 > 0) ? 1u : 0u);
-          }
-          if (!ok || *abort_flag) break;
+          for (int k = 0; k < 8; ++k)
+            mma_ts_lo(tmem + kColO, p_col + k * 8, b0 + ((k * 2048) >> 4), idPV, (j > 0 || k > 0) ? 1u : 0u);
+          if (*abort_flag) break;
           if (j + 1 == s.count) mma_commit(bar_addr(sbase, B_O_DONE));
           mma_commit(bar_addr(sbase, B_V_EMPTY + ring.stage));
           ring.advance();
@@ -592,10 +599,21 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     const int quad = warp & 3;
     const int row = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t o_col = tmem + lane_off + 256 + t * kTile;
+    const uint32_t o_col = tmem + lane_off + kColO + t * kHalfKeys;  // this thread's half of O
     const float c = a.scale_log2;
     const int64_t prompt_rows = prompt_rows_of(a);
-    uint32_t n = 0, oc = 0;
+    volatile float* left = reinterpret_cast<volatile float*>(smem + kOffMax);
+    uint32_t n = 0, oc = 0, pair = 0;
+    RingPos<kRing> pv;  // of tile n - 2
+    // the two threads of a row show each other a number, through slot `slot`
+    auto exchange = [&](uint32_t slot, float x, float* other) {
+      left[(slot * 2 + t) * kTile + row] = x;
+      mbar_arrive(bar_addr(sbase, B_PAIR + quad));
+      const bool met = wait_bar(bar_addr(sbase, B_PAIR + quad), pair & 1);
+      ++pair;
+      *other = left[(slot * 2 + 1 - t) * kTile + row];
+      return met;
+    };
     bool ok = true;
     while (ok && walk.next(&s)) {
       const int32_t rows = seg_rows(a, s, rt);
@@ -605,9 +623,16 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
       float m = -INFINITY, l = 0.f, lcomp = 0.f;
       for (int32_t j = 0; j < s.count; ++j, ++n, lim -= kTile) {
         const uint32_t buf = n & 1, s_col = tmem + lane_off + buf * kTile + t * kHalfKeys;
-        if (!wait_bar(bar_addr(sbase, B_S_FULL + buf), (n >> 1) & 1)) { fail(); ok = false; break; }
-        if (idle) {  // P keeps what S left: rows of D depend on their own rows of A only
-          mbar_arrive(bar_addr(sbase, B_P_FULL + 2 * buf + t));
+        ok = wait_bar(bar_addr(sbase, B_S_FULL + buf), (n >> 1) & 1);
+        if (!ok) break;
+        const uint32_t free_bar = bar_addr(sbase, B_V_EMPTY + pv.stage), free_phase = pv.phase;
+        if (n >= 2) pv.advance();
+        if (idle) {  // P keeps what was there: rows of D depend on their own rows of A only
+          mbar_arrive(bar_addr(sbase, B_S_EMPTY + buf));
+          // or the arrivals of two tiles would count for one
+          ok = n < 2 || wait_bar(free_bar, free_phase);
+          if (!ok) break;
+          mbar_arrive(bar_addr(sbase, B_P_FULL + buf));
           continue;
         }
         tc_fence_after();
@@ -617,6 +642,8 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
         tmem_wait_ld();
         reg_fence32(sr);
         reg_fence32(sr + 32);
+        tc_fence_before();
+        mbar_arrive(bar_addr(sbase, B_S_EMPTY + buf));
         if (lim < kHalfKeys) {  // the source's ragged end, the causal end
 #pragma unroll
           for (int e = 0; e < 64; ++e)
@@ -630,7 +657,14 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mx4[k] = fmax3(mx4[k], __uint_as_float(sr[e + k]), __uint_as_float(sr[e + 4 + k]));
-        const float mt = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]) * c;
+        float mt = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]) * c;
+        float other;
+        ok = exchange(buf, mt, &other);
+        if (!ok) break;
+        mt = fmaxf(mt, other);
+        // the P buffer's last weights have been multiplied, most likely: asked here, needed
+        // when the next ones are there
+        const bool freed = n < 2 || mbar_try_wait(free_bar, free_phase);
         bool rescale = false;
         float alpha = 1.f;
         if (j == 0) {
@@ -645,14 +679,11 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
         const float msub = (m == -INFINITY) ? 0.f : m;
         if (__any_sync(0xffffffffu, rescale)) {
           // P V of the tile before may still be adding to O
-          if (!mbar_wait(bar_addr(sbase, B_V_EMPTY + (n - 1) % kRing), ((n - 1) / kRing) & 1)) {
-            fail();
-            ok = false;
-            break;
-          }
+          ok = mbar_wait(bar_addr(sbase, B_V_EMPTY + (n - 1) % kRing), ((n - 1) / kRing) & 1);
+          if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
-          for (int c0 = 0; c0 < 128; c0 += 32) {
+          for (int c0 = 0; c0 < kHalfKeys; c0 += 32) {
             uint32_t ov[32];
             tmem_ld32(o_col + c0, ov);
             tmem_wait_ld();
@@ -677,29 +708,36 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
           // roundings are independent, so o's error is that of one bf16 rounding
           pk[jj] = pack_bf16(x.x, x.y);
         }
-        tmem_st32(s_col, pk);
+        if (!__all_sync(0xffffffffu, freed)) {
+          ok = mbar_wait(free_bar, free_phase);
+          if (!ok) break;
+        }
+        tc_fence_after();
+        tmem_st32(tmem + lane_off + kColP + buf * kHalfKeys + t * (kHalfKeys / 2), pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar_addr(sbase, B_P_FULL + 2 * buf + t));
+        mbar_arrive(bar_addr(sbase, B_P_FULL + buf));
         const float2 lsa = __fadd2_rn(__fadd2_rn(ls4[0], ls4[1]), __fadd2_rn(ls4[2], ls4[3]));
         const float ls = lsa.x + lsa.y;
         const float tsum = l + ls;
         lcomp += (l - tsum) + ls;
         l = tsum;
       }
+      ok = ok && mbar_wait(bar_addr(sbase, B_O_DONE), oc & 1);
       if (!ok) break;
-      if (!mbar_wait(bar_addr(sbase, B_O_DONE), oc & 1)) { fail(); break; }
       ++oc;
       if (!idle) {
+        float lt = l + lcomp, lo;
+        ok = exchange((n - 1) & 1, lt, &lo);  // that slot's maxima have long been read
+        if (!ok) break;
+        lt = t ? lo + lt : lt + lo;
         tc_fence_after();
-        const float lt = l + lcomp;
         const float inv = lt == 0.f ? 0.f : 1.f / lt;  // a row that sees no key here
         const int64_t prow =
-            (s.resp ? resp_row0(a, prompt_rows, s.item, cta, t) : prompt_row0(a, s.item, col, rt, t)) +
-            row;
-        float* po = part_at(a, prow);
+            (s.resp ? resp_row0(a, prompt_rows, s.item, cta) : prompt_row0(a, s.item, col, rt)) + row;
+        float* po = part_at(a, prow) + t * kHalfKeys * 8;
 #pragma unroll 1
-        for (int c0 = 0; c0 < 128; c0 += 32) {
+        for (int c0 = 0; c0 < kHalfKeys; c0 += 32) {
           uint32_t ov[32];
           tmem_ld32(o_col + c0, ov);
           tmem_wait_ld();
@@ -712,11 +750,12 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
                               __uint_as_float(ov[i + 2]) * inv, __uint_as_float(ov[i + 3]) * inv);
           }
         }
-        if (row < rows) a.part_lse[prow] = lt == 0.f ? -INFINITY : m + log2f(lt);
+        if (row < rows && t == 0) a.part_lse[prow] = lt == 0.f ? -INFINITY : m + log2f(lt);
         tc_fence_before();
       }
       if (*abort_flag) break;
     }
+    if (!ok) fail();
   }
   tc_fence_before();
   __syncthreads();
@@ -803,17 +842,16 @@ decode_combine(const __grid_constant__ LsDecodeArgs a) {
     if (hit[i]) from[i][at] = (uint16_t)tid;
   }
   __syncthreads();
-  const int32_t np = 2 * all[0], count = np + 2 * all[1];
+  const int32_t np = all[0], count = np + all[1];
   // a lane's head (behind the last one: that one again): row of all rows (token, head of the
   // group) against the prompt, row of the member's own
   const int32_t grow = token * a.g + min(head0 + (lane & 7), a.g - 1), mrow = grow - m * a.n * a.g;
-  const int64_t prompt0 = prompt_row0(a, kvh, 0, grow / kTile, 0) + grow % kTile;
-  const int64_t resp0 = resp_row0(a, prompt_rows_of(a), m * a.hkv + kvh, 0, 0) + mrow;
+  const int64_t prompt0 = prompt_row0(a, kvh, 0, grow / kTile) + grow % kTile;
+  const int64_t resp0 = resp_row0(a, prompt_rows_of(a), m * a.hkv + kvh, 0) + mrow;
   const int32_t resp_rows = resp_rows_of(a);
   auto part_row = [&](int k) {
-    if (k < np) return prompt0 + ((int64_t)from[0][k >> 1] * a.rts * 2 + (k & 1)) * kTile;
-    k -= np;
-    return resp0 + ((int64_t)from[1][k >> 1] * 2 + (k & 1)) * resp_rows;
+    if (k < np) return prompt0 + (int64_t)from[0][k] * a.rts * kTile;
+    return resp0 + (int64_t)from[1][k - np] * resp_rows;
   };
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int kBatch = 4;
@@ -846,7 +884,7 @@ decode_combine(const __grid_constant__ LsDecodeArgs a) {
     for (int i = 0; i < kBatch; ++i) {
       const float w = exp2f(l[i] - sub);
       sum += w;
-      if (l[i] == -INFINITY) continue;  // a half that saw no key adds nothing
+      if (l[i] == -INFINITY) continue;  // a part that saw no key adds nothing
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         s[h].x = fmaf(w, v[i][h].x, s[h].x);
@@ -890,7 +928,7 @@ int ls_decode_row_tile() { return kTile; }
 int ls_decode_seg_tiles() { return kSegTiles; }
 int64_t ls_decode_prompt_rows(const LsDecodeArgs& a) { return prompt_rows_of(a); }
 int64_t ls_decode_resp_rows(const LsDecodeArgs& a) {
-  return ((int64_t)a.M * a.hkv + (int64_t)a.cols * a.rts) * 2 * resp_rows_of(a);
+  return ((int64_t)a.M * a.hkv + (int64_t)a.cols * a.rts) * resp_rows_of(a);
 }
 
 cudaError_t ls_launch_decode_attn(const LsDecodeArgs& a, cudaStream_t st) {

@@ -280,13 +280,13 @@ struct LsDecodeArgs {
   float scale_log2;
   void* o;
   float* lse;
-  float* part_o;             // [prompt slots][2][128][128], [response slots][2][n g][128]
+  float* part_o;             // [prompt slots][128][128], [response slots][n g, to 8][128], 8 rows together
   float* part_lse;           // same without the last dimension (log2 domain)
   uint32_t* err;
 };
 int ls_decode_row_tile();
 int ls_decode_seg_tiles();  // tiles' worth of time that a segment of a response takes besides
-// Rows of partial results: slots x 2 halves x rows.
+// Rows of partial results: slots x rows.
 int64_t ls_decode_prompt_rows(const LsDecodeArgs& a);
 int64_t ls_decode_resp_rows(const LsDecodeArgs& a);
 cudaError_t ls_launch_decode_attn(const LsDecodeArgs& a, cudaStream_t st);
