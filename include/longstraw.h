@@ -524,7 +524,8 @@ ls_status ls_qk_norm_rope_bwd(const ls_qkv_view* x, int64_t T, int Hq, int Hkv,
  *              same on every axis), 0 behind the last token
  *   lens_out   int32 [members]: lens + add;  used_out int32 [1]: *used + pages taken.
  *              Each may be the input itself (in place), and lens_out may be add.
- *              Other arrays may not overlap.
+ *              Other arrays may not overlap.  Without members lens, add and lens_out may be
+ *              NULL.
  * A member out of use has lens[m] < 0 and add[m] == 0 and is passed over.  All or nothing:
  * when an add is negative, a member out of use grows, a row of the table is full, the
  * free list ends or the tokens exceed capacity, LS_ERR_DEVICE_CHECK is recorded, every
