@@ -788,7 +788,13 @@ decode_combine(const __grid_constant__ LsDecodeArgs a) {
   const int32_t head0 = 8 * ((blockIdx.x >> 2) - group * octets), col0 = 32 * (blockIdx.x & 3);
   const int32_t token = group / a.hkv, kvh = group - token * a.hkv, m = token / a.n;
   const int32_t len = __ldg(a.lens + m);
-  if (len < 0) return;  // a member out of use: its rows stay as they were
+  if (len < 0) {
+    // A member out of use: its rows stay as they were.  Its blocks wait all the same: the
+    // stream goes on when this grid ends, and with every member out of use nothing else
+    // would hold it back until the main kernel has ended.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int32_t nt = tiles_of(clamp_len(a, len));
   int32_t tot = 0, pre = 0;
   for (int i = tid; i < a.M; i += kCombineThreads) {

@@ -1,0 +1,31 @@
+"""GPU tests of decode calls as a group's life brings them: every member out of use, calls
+from several host threads, captures that torch does not make, members that end at different
+times; and of every V tile's way into the output."""
+import pytest
+import torch
+
+from response_replay_gb300 import binding as B
+from response_replay_gb300 import torch_api as api
+from test_gpu_decode import SCALE, Group
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("P,members", [(300000, 8), (5000, 70)])
+def test_every_member_out_of_use(cuda, P, members):
+    """A finished group's call writes nothing, and what follows it on the stream (lengths
+    written anew, a live call with the same workspace) finds it done."""
+    g = Group(cuda, P, [40 + 3 * i for i in range(members)], 12, 2, seed=50)
+    live = g.lens.clone()
+    want = [x.clone() for x in g.run()]
+    gone = torch.full_like(live, -1)
+    o, lse = torch.full_like(want[0], 5.0), torch.full_like(want[1], 6.0)
+    got = [torch.empty_like(x) for x in want]
+    for _ in range(20):
+        g.lens.copy_(gone)
+        api.decode_attn(g.cache, g.resp, g.q, SCALE, o=o, lse=lse)
+        g.lens.copy_(live)
+        api.decode_attn(g.cache, g.resp, g.q, SCALE, o=got[0], lse=got[1])
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert bool((o == 5.0).all()) and bool((lse == 6.0).all())
+    assert B.ls_last_device_error(0) == B.LS_OK
