@@ -6,6 +6,8 @@ with torch, check shapes and dtypes, and pass raw pointers to the binding.
 """
 from __future__ import annotations
 
+import threading
+
 import torch
 
 from . import binding as B
@@ -36,28 +38,45 @@ _workspaces: dict = {}
 _retired: list = []
 
 
+class _StreamWorkspace:
+    """The workspace of the calls of one kind on one stream, and the lock of its users."""
+
+    __slots__ = ("lock", "buf")
+
+    def __init__(self):
+        self.lock, self.buf = threading.Lock(), None
+
+
+_stream_workspaces: dict = {}
+
+
 def _with_workspace(call, args: tuple, size, like: torch.Tensor, key: str, stream: int) -> None:
     """call(*args, workspace, its bytes, stream) with the workspace of the calls of one kind
-    on the current stream (calls on different streams may overlap).  It grows when the call
-    says that it is too small, which it does before it launches anything; one that was
-    outgrown is kept, in case a graph that was captured without torch still uses it.  A call
-    captured into a graph takes one from the graph's own memory: two graphs captured on
-    one stream may be replayed on two."""
+    on the current stream (calls on different streams may overlap).  A call launches kernels
+    that talk through it, and other host threads run while it does, so it holds the
+    workspace's lock: two threads' calls on one stream go in whole, one behind the other.  It
+    grows when the call says that it is too small, which it does before it launches anything;
+    one that was outgrown is kept, in case a graph that was captured without torch still uses
+    it.  A call captured into a graph takes one from the graph's own memory: two graphs
+    captured on one stream may be replayed on two."""
     if torch.cuda.is_current_stream_capturing():
         ws = torch.empty(max(size(), 256), dtype=torch.uint8, device=like.device)
         return call(*args, ws.data_ptr(), ws.numel(), stream)
     k = (like.get_device(), key, stream)
-    ws = _workspaces.get(k)
-    if ws is not None:
-        try:
-            return call(*args, ws.data_ptr(), ws.numel(), stream)
-        except B.LongstrawError as e:
-            if e.status != B.LS_ERR_WORKSPACE:
-                raise
-        _retired.append(ws)
-    ws = torch.empty(max(size(), 256), dtype=torch.uint8, device=like.device)
-    _workspaces[k] = ws
-    call(*args, ws.data_ptr(), ws.numel(), stream)
+    entry = _stream_workspaces.get(k)
+    if entry is None:
+        entry = _stream_workspaces.setdefault(k, _StreamWorkspace())
+    with entry.lock:
+        ws = entry.buf
+        if ws is not None:
+            try:
+                return call(*args, ws.data_ptr(), ws.numel(), stream)
+            except B.LongstrawError as e:
+                if e.status != B.LS_ERR_WORKSPACE:
+                    raise
+            _retired.append(ws)
+        entry.buf = ws = torch.empty(max(size(), 256), dtype=torch.uint8, device=like.device)
+        call(*args, ws.data_ptr(), ws.numel(), stream)
 
 
 def workspace(nbytes: int, device: torch.device, key: str = "default") -> torch.Tensor:

@@ -7,6 +7,7 @@ import torch
 from response_replay_gb300 import binding as B
 from response_replay_gb300 import torch_api as api
 from test_gpu_decode import SCALE, Group
+from test_stage_calls import run_threads
 
 pytestmark = pytest.mark.gpu
 
@@ -28,4 +29,34 @@ def test_every_member_out_of_use(cuda, P, members):
         api.decode_attn(g.cache, g.resp, g.q, SCALE, o=got[0], lse=got[1])
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert bool((o == 5.0).all()) and bool((lse == 6.0).all())
+    assert B.ls_last_device_error(0) == B.LS_OK
+
+
+def test_two_host_threads_on_one_stream(cuda):
+    """Decode calls and backward calls from two threads, each with inputs of its own: every
+    call gives the bits that it gives alone."""
+    runs = []
+    for seed, (P, lens) in enumerate([(30000, [500, 90, 1]), (9000, [7, 1300, 64])]):
+        g = Group(cuda, P, lens, 12, 2, seed=60 + seed)
+        gen = torch.Generator(device=cuda)
+        gen.manual_seed(seed)
+        x = torch.randn(300 + 100 * seed, 8, 128, generator=gen, device=cuda).to(torch.bfloat16)
+        dy = torch.randn(x.shape, generator=gen, device=cuda)
+        w = torch.rand(128, generator=gen, device=cuda) + 0.5
+
+        def work(g=g, x=x, dy=dy, w=w):
+            o, lse = api.decode_attn(g.cache, g.resp, g.q, SCALE)
+            return [o, lse, *api.qk_norm_rope_bwd(x[:, :6], x[:, 6:], None, None, dy[:, :6], dy[:, 6:],
+                                                  wq=w, wk=w)]
+
+        runs.append((work, [t.clone() for t in work() if t is not None]))
+    torch.cuda.synchronize()
+
+    def body(i):
+        work, want = runs[i]
+        for _ in range(100):
+            got = [t for t in work() if t is not None]
+            assert all(torch.equal(a, b) for a, b in zip(got, want, strict=True))
+
+    run_threads(2, body)
     assert B.ls_last_device_error(0) == B.LS_OK

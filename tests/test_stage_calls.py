@@ -2,8 +2,13 @@
 order of dependent launches, workspaces, and the values that the smoke run compares with."""
 import os
 import re
+import threading
 
 import pytest
+import torch
+
+from response_replay_gb300 import binding as B
+from response_replay_gb300 import torch_api as api
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                     "response_replay_gb300", "csrc")
@@ -23,3 +28,65 @@ def test_dependent_grids_wait_before_every_exit(name):
         before = k[:k.rindex(WAIT)]
         for m in re.finditer(r"\breturn;", before):
             assert WAIT in before[before.rindex("{", 0, m.start()):m.start()], before[m.start() - 80:m.end()]
+
+
+@pytest.fixture
+def host_calls(monkeypatch):
+    """_with_workspace on host tensors: run(call, bytes, stream) for a fake of a C call."""
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(api, "_stream_workspaces", {}, raising=False)
+    monkeypatch.setattr(api, "_workspaces", {})
+    like = torch.empty(0)
+
+    def run(call, nbytes, stream=1):
+        def checked(ws, have, st):
+            if have < nbytes:
+                raise B.LongstrawError("call", B.LS_ERR_WORKSPACE)
+            call(ws)
+        return api._with_workspace(checked, (), lambda: nbytes, like, "kind", stream)
+
+    return run
+
+
+def run_threads(n, body):
+    errors = []
+
+    def guarded(i):
+        try:
+            body(i)
+        except BaseException as e:  # noqa: BLE001 - reported by the test's thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=guarded, args=(i,)) for i in range(n)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+
+
+def test_one_workspace_serves_one_call_at_a_time(host_calls):
+    """Two threads on one stream: a call's launches are not mixed with another's, whether
+    they find the workspace, make it or outgrow it."""
+    inside, clash, seen = [], [], []
+
+    def body(i):
+        def call(ws):
+            seen.append(ws)
+            if ws in inside:
+                clash.append(ws)
+            inside.append(ws)
+            pause.wait(0.002)
+            inside.remove(ws)
+
+        for step in range(20):
+            host_calls(call, 256 * (1 + (step * 7 + i) % (step + 1)))
+
+    pause = threading.Event()
+    run_threads(4, body)
+    assert len(seen) == 80 and not clash
+
+
+def test_calls_on_two_streams_do_not_wait_for_each_other(host_calls):
+    both = threading.Barrier(2)
+    run_threads(2, lambda i: host_calls(lambda ws: both.wait(10), 1000, stream=7 + i))
