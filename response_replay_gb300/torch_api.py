@@ -35,9 +35,6 @@ def _check(t: torch.Tensor, name: str, dtype, shape=None):
 _workspaces: dict = {}
 
 
-_retired: list = []
-
-
 class _StreamWorkspace:
     """The workspace of the calls of one kind on one stream, and the lock of its users."""
 
@@ -48,6 +45,15 @@ class _StreamWorkspace:
 
 
 _stream_workspaces: dict = {}
+_captured_workspaces: list = []  # of captures that torch does not know of
+
+
+def _graph_memory(t: torch.Tensor) -> bool:
+    """Whether t lies in a pool of its own (that of the torch.cuda.CUDAGraph being
+    captured), which outlives t, or in the memory that all tensors share."""
+    p = t.data_ptr()
+    return any(s["address"] <= p < s["address"] + s["total_size"] and tuple(s["segment_pool_id"]) != (0, 0)
+               for s in torch.cuda.memory_snapshot())
 
 
 def _with_workspace(call, args: tuple, size, like: torch.Tensor, key: str, stream: int) -> None:
@@ -55,12 +61,15 @@ def _with_workspace(call, args: tuple, size, like: torch.Tensor, key: str, strea
     on the current stream (calls on different streams may overlap).  A call launches kernels
     that talk through it, and other host threads run while it does, so it holds the
     workspace's lock: two threads' calls on one stream go in whole, one behind the other.  It
-    grows when the call says that it is too small, which it does before it launches anything;
-    one that was outgrown is kept, in case a graph that was captured without torch still uses
-    it.  A call captured into a graph takes one from the graph's own memory: two graphs
-    captured on one stream may be replayed on two."""
+    grows when the call says that it is too small, which it does before it launches anything.
+    A captured call takes one of its own (two graphs captured on one stream may be replayed
+    on two): from the graph's memory, or, in a capture that torch does not make, from all
+    tensors' memory, where it stays taken as long as the process lives, as nothing says when
+    such a graph's last replay has been."""
     if torch.cuda.is_current_stream_capturing():
         ws = torch.empty(max(size(), 256), dtype=torch.uint8, device=like.device)
+        if not _graph_memory(ws):
+            _captured_workspaces.append(ws)
         return call(*args, ws.data_ptr(), ws.numel(), stream)
     k = (like.get_device(), key, stream)
     entry = _stream_workspaces.get(k)
@@ -74,7 +83,6 @@ def _with_workspace(call, args: tuple, size, like: torch.Tensor, key: str, strea
             except B.LongstrawError as e:
                 if e.status != B.LS_ERR_WORKSPACE:
                     raise
-            _retired.append(ws)
         entry.buf = ws = torch.empty(max(size(), 256), dtype=torch.uint8, device=like.device)
         call(*args, ws.data_ptr(), ws.numel(), stream)
 

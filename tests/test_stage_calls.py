@@ -3,6 +3,7 @@ order of dependent launches, workspaces, and the values that the smoke run compa
 import os
 import re
 import threading
+import weakref
 
 import pytest
 import torch
@@ -90,3 +91,41 @@ def test_one_workspace_serves_one_call_at_a_time(host_calls):
 def test_calls_on_two_streams_do_not_wait_for_each_other(host_calls):
     both = threading.Barrier(2)
     run_threads(2, lambda i: host_calls(lambda ws: both.wait(10), 1000, stream=7 + i))
+
+
+@pytest.mark.parametrize("pool,kept", [((0, 0), True), ((3, 0), False), ((0, 9), False)])
+def test_a_captured_workspace_lives_as_long_as_its_graph(monkeypatch, pool, kept):
+    """Within torch's capture the graph's own memory pool holds on to the workspace; in a
+    capture of another library the memory would go to the next tensor, under every replay's
+    writes, so it stays taken."""
+    made, empty = [], torch.empty
+
+    def recorded(*a, **kw):
+        t = empty(*a, **kw)
+        made.append(weakref.ref(t))
+        return t
+
+    segments = [{"address": 0, "total_size": 16, "segment_pool_id": (5, 0)},
+                {"address": 16, "total_size": 2 ** 63, "segment_pool_id": pool}]
+    like = empty(0)
+    monkeypatch.setattr(torch, "empty", recorded)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    monkeypatch.setattr(torch.cuda, "memory_snapshot", lambda *a: segments)
+    monkeypatch.setattr(api, "_captured_workspaces", [], raising=False)
+    for _ in range(2):
+        api._with_workspace(lambda *a: None, (), lambda: 1000, like, "kind", 1)
+    assert [r() is not None for r in made] == [kept, kept]
+
+
+def test_an_outgrown_workspace_is_given_back(monkeypatch, host_calls):
+    made, empty = [], torch.empty
+
+    def recorded(*a, **kw):
+        t = empty(*a, **kw)
+        made.append(weakref.ref(t))
+        return t
+
+    monkeypatch.setattr(torch, "empty", recorded)
+    for nbytes in (1000, 2000, 1500, 3000):
+        host_calls(lambda ws: None, nbytes)
+    assert [r() is not None for r in made] == [False, False, True]
