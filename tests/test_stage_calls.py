@@ -8,6 +8,8 @@ import weakref
 import pytest
 import torch
 
+import __graft_entry__ as entry
+import qk_oracle as qo
 from response_replay_gb300 import binding as B
 from response_replay_gb300 import torch_api as api
 
@@ -129,3 +131,31 @@ def test_an_outgrown_workspace_is_given_back(monkeypatch, host_calls):
     for nbytes in (1000, 2000, 1500, 3000):
         host_calls(lambda ws: None, nbytes)
     assert [r() is not None for r in made] == [False, False, True]
+
+
+def test_smoke_weight_gradient():
+    """The smoke run's value is that of the tests' 64-bit backward, and its limit takes what
+    fp32 gives for any inputs and refuses a gradient that lacks a row."""
+    T, H, lim = 40, 4, 2.0 ** -16
+    f = 1e6 ** (-torch.arange(32, dtype=torch.float64) / 32)
+    pos = torch.arange(700, 700 + T, dtype=torch.int32)
+    for seed in range(50):
+        gen = torch.Generator().manual_seed(seed)
+        x = torch.randn(T, H, 128, generator=gen).to(torch.bfloat16)
+        dy = torch.randn(T, H, 128, generator=gen)
+        want, size = entry.norm_weight_gradient(x, dy, pos, f, 1e-6)
+        ref = qo.bwd(qo.f64(x), qo.f64(dy), 1.0, 0.0, 1e-6, pos[None].numpy(), f.numpy(), None, False)[2]
+        assert abs(want.numpy() - ref).max() <= 1e-12 * float(size.max())
+
+        def error(dw):
+            return float(((dw.double() - want).abs() / size).max())
+
+        r = torch.rsqrt(x.float().square().mean(-1, keepdim=True) + 1e-6)
+        a = (pos.double()[:, None] * f)[:, None]
+        c, s = a.cos().float(), a.sin().float()
+        g = torch.cat([dy[..., :32] * c + dy[..., 32:64] * s, dy[..., 32:64] * c - dy[..., :32] * s,
+                       dy[..., 64:]], -1)
+        terms = g * (x.float() * r)
+        assert error(terms.sum((0, 1))) <= lim
+        terms[seed % T, seed % H] = 0
+        assert error(terms.sum((0, 1))) > lim
