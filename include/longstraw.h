@@ -24,7 +24,8 @@
  *   ls_qk_norm_rope_*      the stage between a layer's projections and its attention:
  *                          query / key norms with rotary positions, forward, backward,
  *                          and fused with the write into pages
- *   ls_extend_pages        pages and slots of a group's growing responses
+ *   ls_extend_pages        pages and slots of a group's growing responses, packed or
+ *                          (_by_member) in every member's own rows
  *   ls_decode_attn         the rollout's decode step: every member's newest tokens over
  *                          the shared captured prompt and its own paged response
  *
@@ -538,6 +539,19 @@ ls_status ls_extend_pages(int32_t* block_table, int members, int max_blocks, int
                           const int32_t* free_list, int num_free, const int32_t* used, int pos0,
                           int axes, int64_t capacity, int32_t* slots, int32_t* positions,
                           int32_t* lens_out, int32_t* used_out, ls_stream_t stream);
+
+/* The same for a step that has `rows` rows of every member, whoever adds how many (members
+ * that have ended add none): slots is int32 [members][rows], positions [axes][members][rows],
+ * and member m's add[m] new tokens are the last of its rows; slot -1 and position 0 before
+ * them.  So row r of member m is its (rows - r)-th newest token, as ls_decode_attn with
+ * n = rows takes it.  An add above rows is refused like the others.  (Packed, a member that
+ * adds nothing moves every later member's tokens up.) */
+ls_status ls_extend_pages_by_member(int32_t* block_table, int members, int max_blocks,
+                                    int page_size, int num_pages, const int32_t* lens,
+                                    const int32_t* add, const int32_t* free_list, int num_free,
+                                    const int32_t* used, int pos0, int axes, int rows,
+                                    int32_t* slots, int32_t* positions, int32_t* lens_out,
+                                    int32_t* used_out, ls_stream_t stream);
 
 /* The responses of a group in their own pages: member m's key j lies in page
  * block_table[m][j / page_size] of `pool`; lens int32 [members] on the device, negative

@@ -11,8 +11,8 @@ loudly if it has not been built.
 from . import binding  # noqa: F401
 from .binding import (  # noqa: F401
     ls_capture_kv, ls_decode_attn, ls_decode_attn_workspace, ls_extend_pages,
-    ls_qk_norm_rope_append, ls_qk_norm_rope_bwd, ls_qk_norm_rope_bwd_workspace,
-    ls_qk_norm_rope_fwd, ls_grpo_loss_fwd_bwd, ls_grpo_workspace, ls_last_device_error,
+    ls_extend_pages_by_member, ls_qk_norm_rope_append, ls_qk_norm_rope_bwd,
+    ls_qk_norm_rope_bwd_workspace, ls_qk_norm_rope_fwd, ls_grpo_loss_fwd_bwd, ls_grpo_workspace, ls_last_device_error,
     ls_replay_attn_bwd, ls_replay_attn_bwd_workspace, ls_replay_attn_fwd,
     ls_replay_attn_fwd_workspace, ls_validate_page_table, ls_validate_page_table_workspace,
     LongstrawError,

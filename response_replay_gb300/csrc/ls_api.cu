@@ -1137,11 +1137,14 @@ ls_status ls_qk_norm_rope_bwd(const ls_qkv_view* x, int64_t T, int Hq, int Hkv,
                                            (cudaStream_t)stream));
 }
 
-ls_status ls_extend_pages(int32_t* block_table, int members, int max_blocks, int page_size,
-                          int num_pages, const int32_t* lens, const int32_t* add,
-                          const int32_t* free_list, int num_free, const int32_t* used, int pos0,
-                          int axes, int64_t capacity, int32_t* slots, int32_t* positions,
-                          int32_t* lens_out, int32_t* used_out, ls_stream_t stream) {
+namespace {
+
+// rows: 0, or the rows of every member, capacity then members * rows
+ls_status extend_pages(int32_t* block_table, int members, int max_blocks, int page_size,
+                       int num_pages, const int32_t* lens, const int32_t* add,
+                       const int32_t* free_list, int num_free, const int32_t* used, int pos0,
+                       int axes, int rows, int64_t capacity, int32_t* slots, int32_t* positions,
+                       int32_t* lens_out, int32_t* used_out, ls_stream_t stream) {
   if (members < 0 || max_blocks < 0 || num_pages < 0 || num_free < 0 || pos0 < 0 || axes < 1 ||
       capacity < 0)
     return LS_ERR_INVALID_ARG;
@@ -1178,9 +1181,34 @@ ls_status ls_extend_pages(int32_t* block_table, int members, int max_blocks, int
   a.ps_log2 = l;
   a.axes = axes;
   a.pos0 = pos0;
+  a.rows = rows;
   a.capacity = capacity;
   a.err = d.err;
   return from_cuda(ls_launch_extend_pages(a, d.sms, (cudaStream_t)stream));
+}
+
+}  // namespace
+
+ls_status ls_extend_pages(int32_t* block_table, int members, int max_blocks, int page_size,
+                          int num_pages, const int32_t* lens, const int32_t* add,
+                          const int32_t* free_list, int num_free, const int32_t* used, int pos0,
+                          int axes, int64_t capacity, int32_t* slots, int32_t* positions,
+                          int32_t* lens_out, int32_t* used_out, ls_stream_t stream) {
+  return extend_pages(block_table, members, max_blocks, page_size, num_pages, lens, add, free_list,
+                      num_free, used, pos0, axes, 0, capacity, slots, positions, lens_out, used_out,
+                      stream);
+}
+
+ls_status ls_extend_pages_by_member(int32_t* block_table, int members, int max_blocks, int page_size,
+                                    int num_pages, const int32_t* lens, const int32_t* add,
+                                    const int32_t* free_list, int num_free, const int32_t* used,
+                                    int pos0, int axes, int rows, int32_t* slots, int32_t* positions,
+                                    int32_t* lens_out, int32_t* used_out, ls_stream_t stream) {
+  if (rows < 1) return LS_ERR_INVALID_ARG;
+  const int64_t capacity = members > 0 ? (int64_t)members * rows : 0;
+  return extend_pages(block_table, members, max_blocks, page_size, num_pages, lens, add, free_list,
+                      num_free, used, pos0, axes, rows, capacity, slots, positions, lens_out,
+                      used_out, stream);
 }
 
 ls_status ls_decode_attn_workspace(const ls_kv_cache* cache, const ls_resp_cache* resp, int n,

@@ -256,6 +256,7 @@ struct LsExtendArgs {
   int32_t* slots;            // [capacity]
   int32_t* pos;              // [axes][capacity] or NULL
   int32_t members, max_blocks, num_free, num_pages, ps_log2, axes, pos0;
+  int32_t rows;              // of every member (its tokens the last ones), 0: members packed
   int64_t capacity;
   uint32_t* err;
 };

@@ -5,6 +5,8 @@
 // ceil((len + add) / ps); the missing ones are taken from the free list in member order
 // (an exclusive sum over the members gives each its first), entered into the table, and
 // token i of the member gets slot table[i / ps] * ps + i % ps and position pos0 + i.
+// The new tokens stand packed, member after member, or each member's as the last of its own
+// `rows` rows, which is where a step of fixed rows has them whoever adds how many.
 //
 // Nothing here depends on another block: every block sums the members' counts itself
 // (at most 1,024 members, one per thread; 8 KB from L2) and then fills its share of the
@@ -94,7 +96,8 @@ __global__ void __launch_bounds__(kThreads) extend_pages_kernel(const LsExtendAr
     add = __ldg(a.add + tid);
     const long long room = (long long)a.max_blocks << a.ps_log2;
     // a member out of use (negative length) may not grow
-    good = add >= 0 && (len >= 0 || add == 0) && (long long)(len < 0 ? 0 : len) + add <= room;
+    good = add >= 0 && (len >= 0 || add == 0) && (long long)(len < 0 ? 0 : len) + add <= room &&
+           (a.rows == 0 || add <= a.rows);
     if (good && len >= 0) {
       have = (int)(((long long)len + ps - 1) >> a.ps_log2);
       need = (int)(((long long)len + add + ps - 1) >> a.ps_log2);
@@ -125,13 +128,20 @@ __global__ void __launch_bounds__(kThreads) extend_pages_kernel(const LsExtendAr
       int32_t slot[kPerThread], pos[kPerThread];
       int m = -1;
       long long begin = 0, end = 0;
+      // packed, the tokens end at `total`; with rows every one belongs to a member
+      const long long stop = a.rows ? a.capacity : total;
 #pragma unroll
       for (int e = 0; e < kPerThread; ++e) {
         slot[e] = -1;
         pos[e] = 0;
         const long long t = i + e;
-        if (!ok || t >= total) continue;
-        if (m < 0) {  // first member whose tokens end behind t
+        if (!ok || t >= stop) continue;
+        if (a.rows) {
+          m = (int)(t / a.rows);
+          end = (long long)(m + 1) * a.rows;
+          begin = end - (p.tok_end[m] - (m ? p.tok_end[m - 1] : 0));
+          if (t < begin) continue;
+        } else if (m < 0) {  // first member whose tokens end behind t
           int lo = 0, hi = a.members - 1;
           while (lo < hi) {
             const int mid = (lo + hi) >> 1;

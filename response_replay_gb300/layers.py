@@ -75,14 +75,27 @@ class LayeredResponses:
     l of one allocation, ``layers[l]`` its ResponseCache.  A decode step is one ``extend``
     and then, layer by layer, ``append`` (norm, rotary positions, K and V into the pages)
     and ``attend`` (over the layer's captured prompt and the members' own responses); it
-    can be captured as one CUDA graph."""
+    can be captured as one CUDA graph.
+
+    The rows of a step's projections are packed, member after member, so that a member that
+    adds nothing moves the later ones up, or, with member_rows, every member has that many rows
+    and its new tokens are the last of them.  A loop whose members end at different times
+    takes member_rows and sets an ended member's add to 0: its rows of ``attend`` hold nothing
+    of use then, and the others' stay where they are."""
 
     def __init__(self, prompt, num_kv_heads: int, members: int, max_tokens: int,
                  num_pages: int, page_size: int, device, capacity: int | None = None,
-                 axes: int = 1):
+                 axes: int = 1, member_rows: int | None = None):
         """prompt: the captured prompt's layers (LayeredKVCache, or anything whose [l] is a
         PagedKVCache); max_tokens: longest response; capacity: most new tokens of a step
-        (default: one a member); axes: rows of positions, one an axis of the rotary."""
+        (default: one a member); axes: rows of positions, one an axis of the rotary;
+        member_rows: rows of every member in a step (capacity is then members *
+        member_rows)."""
+        if member_rows is not None:
+            if member_rows < 1 or capacity not in (None, members * member_rows):
+                raise ValueError("member_rows is at least 1, and capacity members * member_rows")
+            capacity = members * member_rows
+        self.member_rows = member_rows
         self.prompt = prompt
         blocks = (max_tokens + page_size - 1) // page_size
         self.alloc = api.PageAllocator.empty(members, blocks, num_pages, page_size, device)
@@ -101,12 +114,12 @@ class LayeredResponses:
     def extend(self, add: torch.Tensor, stream=None) -> None:
         """Room for add[m] new tokens of every member, behind the prompt."""
         api.extend_pages(self.alloc, add, self.prompt[0].num_tokens, self.slots, self.positions,
-                         stream=stream)
+                         stream=stream, member_rows=self.member_rows)
 
     def append(self, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rotary,
                wq=None, wk=None, stream=None, **kw) -> torch.Tensor:
-        """The new tokens' projections (in the order of ``slots``) into layer's pages; the
-        normed and rotated queries."""
+        """The new tokens' projections (in the order of ``slots``; rows of slot -1 may hold
+        anything) into layer's pages; the normed and rotated queries."""
         return api.qk_norm_rope_append(self.pools[layer], q, k, v, self.slots, self.positions,
                                        rotary, wq, wk, stream=stream, **kw)
 

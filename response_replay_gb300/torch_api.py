@@ -800,28 +800,38 @@ class PageAllocator:
 
 def extend_pages(alloc: PageAllocator, add: torch.Tensor, pos0: int, slots: torch.Tensor,
                  positions: torch.Tensor | None = None, lens_out: torch.Tensor | None = None,
-                 used_out: torch.Tensor | None = None, stream=None) -> None:
+                 used_out: torch.Tensor | None = None, stream=None,
+                 member_rows: int | None = None) -> None:
     """Room for add[m] more tokens of every member: fills slots int32 [capacity] (-1 behind
     the last token) and positions int32 [axes][capacity] (pos0 + index within the
     response), enters new pages into the table and advances alloc.lens and alloc.used (or
-    writes them to lens_out / used_out).  See ls_extend_pages for what is refused."""
+    writes them to lens_out / used_out).  See ls_extend_pages for what is refused.
+
+    The tokens are packed, member after member; with member_rows given, capacity is members *
+    member_rows and a member's tokens are the last of its own rows (-1 before them), the order
+    in which decode_attn takes queries [members][member_rows] while some members add none."""
     if stream is not None:
         with _as_current(stream):
-            return extend_pages(alloc, add, pos0, slots, positions, lens_out, used_out)
+            return extend_pages(alloc, add, pos0, slots, positions, lens_out, used_out,
+                                member_rows=member_rows)
     M, dev, i32 = alloc.members, alloc.device_index, torch.int32
     st = _dev_stream(dev)
     cap = slots.shape[0] if slots.dim() == 1 else -1
+    if member_rows is not None and (member_rows < 1 or cap != M * member_rows):
+        raise ValueError(f"slots must be [{M} members * member_rows], member_rows at least 1")
     sp = _dense(slots, "slots", i32, (cap,), dev)
     axes, pp = 1, None
     if positions is not None:
         axes = positions.shape[0] if positions.dim() == 2 else -1
         pp = _dense(positions, "positions", i32, (axes, cap), dev)
     lens, used = alloc.lens.data_ptr(), alloc.used.data_ptr()
-    B.ls_extend_pages(alloc.block_table.data_ptr(), M, alloc.max_blocks, alloc.page_size,
-                      alloc.num_pages, lens, _dense(add, "add", i32, (M,), dev),
-                      alloc.free_list.data_ptr(), alloc.num_free, used, pos0, axes, cap, sp, pp,
-                      lens if lens_out is None else _dense(lens_out, "lens_out", i32, (M,), dev),
-                      used if used_out is None else _dense(used_out, "used_out", i32, (1,), dev), st)
+    call, room = ((B.ls_extend_pages, cap) if member_rows is None
+                  else (B.ls_extend_pages_by_member, member_rows))
+    call(alloc.block_table.data_ptr(), M, alloc.max_blocks, alloc.page_size,
+         alloc.num_pages, lens, _dense(add, "add", i32, (M,), dev),
+         alloc.free_list.data_ptr(), alloc.num_free, used, pos0, axes, room, sp, pp,
+         lens if lens_out is None else _dense(lens_out, "lens_out", i32, (M,), dev),
+         used if used_out is None else _dense(used_out, "used_out", i32, (1,), dev), st)
 
 
 class ResponseCache:

@@ -3,10 +3,13 @@ from several host threads, captures that torch does not make, members that end a
 times; and of every V tile's way into the output."""
 import ctypes as C
 
+import numpy as np
 import pytest
 import torch
 
+import qk_oracle as qo
 from response_replay_gb300 import binding as B
+from response_replay_gb300 import layers as L
 from response_replay_gb300 import torch_api as api
 from test_gpu_decode import SCALE, Group
 from test_stage_calls import run_threads
@@ -126,3 +129,133 @@ def test_workspaces_of_torch_graphs_stay_in_their_pools(cuda):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want, strict=True))
     assert len(api._captured_workspaces) == kept
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("lens,add,rows,ps", [
+    ([15, 16, 0, 31, -1], [1, 0, 1, 1, 0], 1, 16),
+    ([15, 16, 0, 31, -1, 7], [3, 0, 1, 2, 0, 5], 5, 16),
+    ([i % 50 for i in range(1024)], [i % 8 for i in range(1024)], 7, 16),       # several blocks
+    ([0, 300, 5], [4001, 0, 6000], 6000, 256),
+    ([3, 4], [1, 3], 2, 16),                                                    # more than its rows
+    ([3, -1], [1, 1], 2, 16),                                                   # out of use
+])
+def test_extend_by_member(cuda, lens, add, rows, ps, in_place):
+    """Pages, lengths and slots are those of the packed call, every member's in its rows."""
+    M, spare = len(lens), 3
+    have = [-(-x // ps) if x > 0 else 0 for x in lens]
+    blocks = max(-(-(max(x, 0) + a) // ps) for x, a in zip(lens, add)) + 1
+    free = np.random.default_rng(M).permutation(M * blocks + spare)
+    table, used = np.full((M, blocks), -7), 0
+    for m, h in enumerate(have):
+        table[m, :h] = free[used:used + h]
+        used += h
+
+    def i32(x):
+        return torch.tensor(np.asarray(x), dtype=torch.int32, device=cuda)
+
+    a = api.PageAllocator(i32(table), i32(lens), i32(free), i32([used]), ps)
+    slots = torch.full((M * rows,), 99, dtype=torch.int32, device=cuda)
+    pos = torch.full((2, M * rows), 99, dtype=torch.int32, device=cuda)
+    lo, uo = (None, None) if in_place else (torch.empty_like(a.lens), torch.empty_like(a.used))
+    api.extend_pages(a, i32(add), 1000, slots, pos, lens_out=lo, used_out=uo, member_rows=rows)
+    lo, uo = (a.lens, a.used) if in_place else (lo, uo)
+    ref = qo.extend(table, lens, add, free, used, ps, 1000, 2, sum(add))
+    if ref is None or max(add) > rows:
+        assert B.ls_last_device_error(0) == B.LS_ERR_DEVICE_CHECK
+        assert bool((slots == -1).all()) and bool((pos == 0).all())
+        assert lo.tolist() == lens and int(uo) == used and a.block_table.tolist() == table.tolist()
+        return
+    assert B.ls_last_device_error(0) == B.LS_OK
+    want_slots, want_pos, t = np.full((M, rows), -1), np.zeros((2, M, rows), int), 0
+    for m, n in enumerate(add):
+        want_slots[m, rows - n:] = ref[0][t:t + n]
+        want_pos[:, m, rows - n:] = ref[1][:, t:t + n]
+        t += n
+    np.testing.assert_array_equal(slots.cpu().numpy(), want_slots.ravel())
+    np.testing.assert_array_equal(pos.cpu().numpy(), want_pos.reshape(2, -1))
+    np.testing.assert_array_equal(a.block_table.cpu().numpy(), ref[2])
+    np.testing.assert_array_equal(lo.cpu().numpy(), ref[3])
+    assert int(uo) == ref[4]
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("rows", [1, 3])
+def test_loop_whose_members_end_at_different_times(cuda, graph, rows):
+    """Steps of fixed rows, eager and as one captured graph, in which members end, pause and
+    add up to `rows` tokens: every token's output is that of its response's replay."""
+    P, M, hq, hkv, ps = 200, 4, 6, 2, 16
+    gen = torch.Generator(device=cuda)
+    gen.manual_seed(80 + rows)
+
+    def normal(*s):
+        return torch.randn(*s, generator=gen, device=cuda).to(torch.bfloat16)
+
+    table = torch.tensor([3, 0, 2, 1], dtype=torch.int32, device=cuda)
+    prompt = L.LayeredKVCache(1, 5, table, 64, hkv, P, fill=float("nan"))
+    prompt.capture(0, normal(P, hkv, 128), normal(P, hkv, 128))
+    r = L.LayeredResponses(prompt, hkv, M, 64, 16, ps, cuda, member_rows=rows)
+    r.k_pools.fill_(float("nan"))
+    r.v_pools.fill_(float("nan"))
+    rot = api.Rotary.from_base(1e6, 128, cuda)
+    w = torch.rand(128, generator=gen, device=cuda) + 0.5
+    rng = np.random.default_rng(rows)
+    last = [20, 5, 0, 13]  # step after which a member adds nothing
+    adds = [[int(rng.integers(0 if rows > 1 else 1, rows + 1)) if t < last[m] else 0 for m in range(M)]
+            for t in range(20)]
+    total = [sum(a[m] for a in adds) for m in range(M)]
+    x = [normal(max(n, 1), hq + 2 * hkv, 128) for n in total]
+    cur = torch.empty(M, rows, hq + 2 * hkv, 128, dtype=torch.bfloat16, device=cuda)
+    add = torch.zeros(M, dtype=torch.int32, device=cuda)
+    o = torch.empty(M, rows, hq, 128, dtype=torch.bfloat16, device=cuda)
+    lse = torch.empty(M, rows, hq, device=cuda)
+
+    def step():
+        r.extend(add)
+        f = cur.view(M * rows, hq + 2 * hkv, 128)
+        q = r.append(0, f[:, :hq], f[:, hq:hq + hkv], f[:, hq + hkv:], rot, w, w)
+        r.attend(0, q.view(M, rows, hq, 128), SCALE, o=o, lse=lse)
+
+    run = step
+    if graph:
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            step()  # adds nothing yet
+        st.synchronize()
+        captured = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(captured, stream=st):
+            step()
+        run = captured.replay
+    got, got_lse, done = [[] for _ in x], [[] for _ in x], [0] * M
+    for a in adds:
+        cur.fill_(float("nan"))  # rows without a token hold anything
+        for m, n in enumerate(a):
+            cur[m, rows - n:] = x[m][done[m]:done[m] + n]
+            done[m] += n
+        add.copy_(torch.tensor(a, dtype=torch.int32))
+        run()
+        for m, n in enumerate(a):
+            got[m].append(o[m, rows - n:].clone())
+            got_lse[m].append(lse[m, rows - n:].clone())
+    assert r.alloc.lens.tolist() == total and B.ls_last_device_error(0) == B.LS_OK
+    for m, n in enumerate(total):
+        if n == 0:
+            continue
+        pos = torch.arange(P, P + n, dtype=torch.int32, device=cuda)
+        q, k, v = api.qk_norm_rope_fwd(x[m][:, :hq], x[m][:, hq:hq + hkv], x[m][:, hq + hkv:], pos, rot, w, w)
+        ro, rl = api.replay_fwd(prompt[0], q, k, v, SCALE, 2)
+        od, ld = torch.cat(got[m]), torch.cat(got_lse[m])
+        assert (ro.float() - od.float()).abs().max() <= 2 ** -7 * ro.float().abs().max()
+        assert (rl - ld).abs().max() <= 1e-5
+
+
+def test_member_rows_refused(cuda):
+    a = api.PageAllocator.empty(3, 4, 12, 16, cuda)
+    add = torch.ones(3, dtype=torch.int32, device=cuda)
+    for n, rows in ((4, 1), (3, 2), (0, 0), (3, -1)):
+        with pytest.raises(ValueError, match="member_rows"):
+            api.extend_pages(a, add, 0, torch.empty(n, dtype=torch.int32, device=cuda), member_rows=rows)
+    with pytest.raises(ValueError, match="member_rows"):
+        L.LayeredResponses([None], 2, 3, 64, 12, 16, cuda, capacity=5, member_rows=2)
+    assert a.lens.tolist() == [0, 0, 0]

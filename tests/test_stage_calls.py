@@ -159,3 +159,22 @@ def test_smoke_weight_gradient():
         assert error(terms.sum((0, 1))) <= lim
         terms[seed % T, seed % H] = 0
         assert error(terms.sum((0, 1))) > lim
+
+
+def test_extend_by_member_refuses():
+    if not os.path.exists(B.LIB_PATH):
+        from response_replay_gb300 import build
+        build.build()
+    lib, A = B.lib(), 1 << 20
+    base = dict(table=A, members=4, max_blocks=8, ps=64, pages=100, lens=A, add=A, free=A, nfree=50,
+                used=A, pos0=0, axes=1, rows=2, slots=A, pos=A, lo=A, uo=A)
+    for kw, want in [
+        (dict(rows=0), B.LS_ERR_INVALID_ARG), (dict(rows=-3), B.LS_ERR_INVALID_ARG),
+        (dict(members=-1), B.LS_ERR_INVALID_ARG), (dict(members=1025), B.LS_ERR_UNSUPPORTED),
+        (dict(rows=2 ** 29), B.LS_ERR_UNSUPPORTED), (dict(members=1024, rows=2 ** 30), B.LS_ERR_UNSUPPORTED),
+        (dict(ps=8), B.LS_ERR_UNSUPPORTED), (dict(slots=None), B.LS_ERR_INVALID_ARG),
+        (dict(slots=A + 4), B.LS_ERR_INVALID_ARG), (dict(pos=A + 8), B.LS_ERR_INVALID_ARG),
+        (dict(lens=None), B.LS_ERR_INVALID_ARG), (dict(axes=0), B.LS_ERR_INVALID_ARG),
+    ]:
+        assert lib.ls_extend_pages_by_member(*{**base, **kw}.values(), None) == want, kw
+    assert lib.ls_extend_pages_by_member(*{**base, "members": 0}.values(), None) == B.LS_OK
