@@ -259,3 +259,45 @@ def test_member_rows_refused(cuda):
     with pytest.raises(ValueError, match="member_rows"):
         L.LayeredResponses([None], 2, 3, 64, 12, 16, cuda, capacity=5, member_rows=2)
     assert a.lens.tolist() == [0, 0, 0]
+
+
+# long segments of one and several row tiles, one and several KV heads; small and large pages
+TILES = [
+    (200003, [5000, 37, 1, 2600], 6, 1, 1, 64, 64),
+    (0, [40000, 129, 30001], 6, 2, 1, 64, 16),
+    (70000, [300 + 100 * i for i in range(44)], 12, 2, 1, 16, 256),
+    (128000, [513, 30000], 8, 8, 2, 256, 32),
+    (16389, [700, 2000], 16, 8, 2, 16, 16),
+]
+
+
+@pytest.mark.parametrize("mod", [128, 101])
+@pytest.mark.parametrize("P,lens,hq,hkv,n,ps,rps", TILES)
+def test_every_v_tile_shows(cuda, P, lens, hq, hkv, n, ps, rps, mod):
+    """Nearly even weights, and values that are one in a single dimension, another for every
+    tile of 128 keys until `mod` of them have gone by: a tile that is left out, taken twice or
+    taken from another place of the ring moves o by more than its bound allows, twice over."""
+    g = Group(cuda, P, lens, hq, hkv, n, ps, rps, seed=P + mod, sharp=0.03)
+
+    def coded(keys, first):
+        d = (first + torch.arange(keys, device=cuda) // 128)[:, None] + 17 * torch.arange(hkv, device=cuda)
+        return torch.nn.functional.one_hot(d % mod, 128).to(torch.bfloat16)
+
+    before = -(-P // 128)  # a response's tiles are numbered behind the prompt's
+    g.vp = coded(P, 0)
+    if P:
+        g.cache.capture(g.kp, g.vp)
+    for m, x in enumerate(lens):
+        g.vr[m] = coded(x, before + 3 * m)
+        t = torch.arange(x, device=cuda)
+        g.resp.pool.v_pool[g.resp.block_table[m, t // rps].long(), :, t % rps] = g.vr[m]
+    o, lse = g.run()
+    # what half a tile brings into its dimension at the least, against that dimension's bound
+    _, ob, _, _ = qo.decode(qo.f64(g.q), qo.f64(g.kp), qo.f64(g.vp), [qo.f64(x) for x in g.kr],
+                            [qo.f64(x) for x in g.vr], lens, SCALE)
+    for m, x in enumerate(lens):
+        qh = g.q[m].double().view(n, hkv, hq // hkv, 128).permute(1, 0, 2, 3).flatten(1, 2)
+        s = SCALE * max(float((qh @ k.double().permute(1, 2, 0)).abs().max())
+                        for k in (g.kp, g.kr[m]) if len(k))
+        assert 64 / (P + x) * np.exp(-2 * s) > 2 * ob[m].max(), m
+    g.check(o, lse)
