@@ -424,9 +424,11 @@ ls_status ls_mla_replay_bwd(const ls_latent_cache* cache, const void* q, const v
  *   r = 1 / sqrt(mean_i x_i^2 + eps),   u_i = x_i r (w_offset + w_i),
  *   y = u, with each pair (a, b) of its first rot_dim values turned by the pair's angle
  *       p inv_freq[j]: (a cos - b sin, b cos + a sin), p = positions[pair_axis[j]][t].
- * Everything is computed in fp32 and rounded to bf16 once; the angle is exact to 2^-32 of
- * a turn at position 4,194,304 whatever its size (64-bit fixed-point turns).  A row takes
- * only its own values: a non-finite one reaches no other row.
+ * Everything is computed in fp32 and rounded to bf16 once.  The angle's part of a turn is
+ * a 64-bit fixed-point number, off by at most 2^-54 of a turn per position (2^-32 at position
+ * 4,194,304) for frequencies up to 2 pi however many turns it passes; it is rounded to fp32,
+ * by at most 2^-26 of a turn, where its cosine and sine are taken.  A row takes only its own
+ * values: a non-finite one reaches no other row.
  *
  * ls_qkv_view: rows of 128 values at q + t q_stride[0] + h q_stride[1] elements (k and v
  * alike), so that a packed projection's slices need no copy.  Strides are multiples of 8

@@ -14,8 +14,10 @@
 // bits would lose the angle (at position 4,194,304 one fp32 step is 0.25 rad for the
 // fastest pair).  A pair's turns per position (inv_freq / 2 pi, its fractional part) are
 // taken as a 64-bit fixed-point fraction, so that position x fraction modulo 2^64 is the
-// angle's fraction of a turn exactly; its top 32 bits go through sincospif.  The error
-// left is that of the fraction (2^-54 of a turn per position: 2^-32 at 4,194,304).
+// angle's fraction of a turn exactly.  The error until there is that of the fraction (2^-54
+// of a turn per position for frequencies up to 2 pi: 2^-32 at 4,194,304).  Its top 32 bits,
+// as an fp32 number of half turns in [-1, 1) (a rounding of up to 2^-26 of a turn, which is
+// what the angle is off by), go through sincospif.
 #include "ls_device.cuh"
 #include "ls_internal.h"
 

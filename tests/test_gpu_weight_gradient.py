@@ -1,5 +1,7 @@
 """The stage's weight gradients within a bound of the walk that sums them, close enough to see
-any one row that is lost or taken twice."""
+any one row that is lost or taken twice; and the angles, which they show in 32 bits."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -63,3 +65,29 @@ def test_no_row_is_lost(cuda, T, hq, hkv, rot, axes, inter, with_v, dtype):
         assert seen == 1 or (terms.shape[0] * terms.shape[1] > 200000 and seen > 0.9), seen
         err = np.abs(qo.f64(out[3 + i]) - dw) / bound
         assert err.max() <= 1, (i, err.max())
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_the_angle_in_32_bits(cuda, inter):
+    """One token of one head, all ones, whose gradient is one in the first value of every pair:
+    its weight gradient is (cos, -sin).  The angle is off by the fp32 rounding of its part of a
+    turn, 2^-26, and 2^-54 a position; cosine and sine by 2 half steps each, the products, the
+    sum and xh by another three."""
+    half = 64
+    freq = torch.tensor([1e7 ** (-j / half) for j in range(half)], dtype=torch.float64, device=cuda)
+    rot = api.Rotary(freq, interleaved=inter)
+    x = torch.ones(1, 1, 128, dtype=torch.bfloat16, device=cuda)
+    first = np.arange(0, 128, 2) if inter else np.arange(half)
+    second = first + (1 if inter else half)
+    dy = torch.zeros(1, 1, 128, device=cuda)
+    dy[0, 0, first] = 1.0
+    w = torch.ones(128, device=cuda)
+    for p in [0, 1, -1, 1000, 131071, 2097152, 4194304, *np.random.default_rng(1).integers(0, 4194304, 40)]:
+        pos = torch.tensor([int(p)], dtype=torch.int32, device=cuda)
+        dw = qo.f64(api.qk_norm_rope_bwd(x, x, pos, rot, dy, dy, wq=w, wk=w, eps=2e-38)[3])
+        turns = [math.fmod(int(p) * f, 2 * math.pi) for f in freq.tolist()]
+        # p f of a 64-bit product is off by 2^-53 of its size
+        bound = 2 * math.pi * (2.0 ** -26 + abs(int(p)) * 2.0 ** -54) + abs(int(p)) * 2.0 ** -53 + 5 * qo.U32
+        assert np.abs(dw[first] - np.cos(turns)).max() <= bound, p
+        assert np.abs(dw[second] + np.sin(turns)).max() <= bound, p
+    ok()
