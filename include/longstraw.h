@@ -456,7 +456,7 @@ typedef struct {
   const void* wk;
   ls_dtype w_dtype;
   float w_offset;
-  float eps; /* > 0, a normal number */
+  float eps; /* > 0, a normal number, at most 3e38 */
 } ls_qk_norm;
 
 typedef struct {

@@ -944,7 +944,8 @@ ls_status norm_rope_args(int64_t T, int Hq, int Hkv, const ls_qk_norm* norm, con
   a->hkv = Hkv;
   a->axes = 1;
   if (norm) {
-    if (!isfinite(norm->eps) || !(norm->eps >= 1.17549435e-38f) || !isfinite(norm->w_offset))
+    // a normal number that leaves room for the mean beside it
+    if (!(norm->eps >= 1.17549435e-38f && norm->eps <= 3e38f) || !isfinite(norm->w_offset))
       return LS_ERR_INVALID_ARG;
     if (norm->w_dtype != LS_BF16 && norm->w_dtype != LS_FP32) return LS_ERR_INVALID_ARG;
     if (!aligned16(norm->wq) || !aligned16(norm->wk)) return LS_ERR_INVALID_ARG;

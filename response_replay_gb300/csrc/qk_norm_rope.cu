@@ -215,8 +215,16 @@ __device__ __forceinline__ float dot8(const float2* x, const float2* y) {
 }
 
 // bf16 values reach 3e38, whose squares do not fit fp32: the values of such a row are
-// scaled by 2^-80 and summed again.  (eps is nothing beside them.)
+// scaled by 2^-80 and summed again, and eps with their squares.
 constexpr float kDown = 8.271806125530277e-25f;
+__device__ __forceinline__ float rsqrt_ftz(float x) {  // x is a normal number here
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rsqrt_down(float ss, float eps) {
+  return rsqrt_ftz(fmaf(ss, 1.f / kD, eps * kDown * kDown));
+}
 __device__ __forceinline__ void scale8(float2* x, float f) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] = __fmul2_rn(x[i], both(f));
@@ -243,12 +251,6 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ float rsqrt_ftz(float x) {  // x is a normal number here
-  float y;
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // Forward.  It reads and writes every row once and is bound by that: 32,768 tokens of 24
@@ -377,7 +379,7 @@ norm_rope_fwd_kernel(const __grid_constant__ LsNormRopeArgs a, const __grid_cons
             scale8(u, big ? kDown : 1.f);
             if (!kInter) scale8(o, big ? kDown : 1.f);
             ss = sum16(dot8(u, u));
-            if (big) r = rsqrt_ftz(ss * (1.f / kD));
+            if (big) r = rsqrt_down(ss, a.eps);
           }
         }
         if (kInter) {
@@ -561,7 +563,7 @@ norm_rope_bwd_kernel(const __grid_constant__ LsNormRopeArgs a, const __grid_cons
             ss = sum16(dot8(u, u));
             hx = sum16(dot8(h, u));
             if (big) {
-              r = rsqrt_ftz(ss * (1.f / kD));
+              r = rsqrt_down(ss, a.eps);
               r_dx = r * kDown;
             }
           }

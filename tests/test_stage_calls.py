@@ -178,3 +178,12 @@ def test_extend_by_member_refuses():
     ]:
         assert lib.ls_extend_pages_by_member(*{**base, **kw}.values(), None) == want, kw
     assert lib.ls_extend_pages_by_member(*{**base, "members": 0}.values(), None) == B.LS_OK
+
+
+@pytest.mark.parametrize("eps", [3.1e38, float("inf"), float("nan"), 0.0, 1e-39, -1.0])
+def test_eps_refused(eps):
+    """3e38 and the largest mean of squares that fit fp32 have a sum in fp32."""
+    lib, A = B.lib(), 1 << 20
+    view = B.ls_qkv_view(A, A, A, *(4096, 128) * 3)
+    norm = B.ls_qk_norm(A, A, B.LS_FP32, 0.0, eps)
+    assert lib.ls_qk_norm_rope_fwd(view, 4, 8, 4, norm, None, None, view, None) == B.LS_ERR_INVALID_ARG
