@@ -557,22 +557,28 @@ norm_rope_bwd_kernel(const __grid_constant__ LsNormRopeArgs a, const __grid_cons
           for (int e = 0; e < 4; ++e) h[e] = __fmul2_rn(g[e], wt[e]);
           float ss = sum16(dot8(u, u)), hx = sum16(dot8(h, u));
           float r = rsqrt_ftz(fmaf(ss, 1.f / kD, a.eps)), r_dx = r;
-          if (__any_sync(0xffffffffu, ss > kOverflow)) {
+          // a sum has passed fp32 (that of h and u, too, where neither's squares do)
+          const bool over = !(ss + fabsf(hx) <= kOverflow);
+          hx *= r;  // from here on the sum of h xh
+          if (__any_sync(0xffffffffu, over)) {
             const bool big = ss > kOverflow;
             scale8(u, big ? kDown : 1.f);
             ss = sum16(dot8(u, u));
-            hx = sum16(dot8(h, u));
             if (big) {
               r = rsqrt_down(ss, a.eps);
               r_dx = r * kDown;
             }
+            scale8(u, r);
+            const float sum = sum16(dot8(h, u));
+            if (over) hx = sum;  // the warp's other row keeps its bits
+            r = 1.f;
           }
           scale8(u, r);
           if (live) {  // else the ring holds something older
 #pragma unroll
             for (int e = 0; e < 4; ++e) dw[e] = __ffma2_rn(g[e], u[e], dw[e]);
           }
-          const float2 nm = both(-hx * r * (1.f / kD));
+          const float2 nm = both(-hx * (1.f / kD));  // the mean of h xh
 #pragma unroll
           for (int e = 0; e < 4; ++e) g[e] = __fmul2_rn(__ffma2_rn(nm, u[e], h[e]), both(r_dx));
         }
