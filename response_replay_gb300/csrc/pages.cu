@@ -80,7 +80,10 @@ __device__ __forceinline__ int32_t page_of(const LsExtendArgs& a, const Plan& p,
   return __ldg(a.free_list + p.used0 + before + b - p.have[m]);
 }
 
-// fill: slots, positions and table entries; commit: lens_out and used_out.
+// fill: slots, positions and table entries; commit: lens_out and used_out.  kRows: every
+// member has rows of its own (a template, as a test of it for every token made the packed
+// call 0.3 us longer).
+template <bool kRows>
 __global__ void __launch_bounds__(kThreads) extend_pages_kernel(const LsExtendArgs a, int fill,
                                                                 int commit) {
   __shared__ Plan p;
@@ -97,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) extend_pages_kernel(const LsExtendAr
     const long long room = (long long)a.max_blocks << a.ps_log2;
     // a member out of use (negative length) may not grow
     good = add >= 0 && (len >= 0 || add == 0) && (long long)(len < 0 ? 0 : len) + add <= room &&
-           (a.rows == 0 || add <= a.rows);
+           (!kRows || add <= a.rows);
     if (good && len >= 0) {
       have = (int)(((long long)len + ps - 1) >> a.ps_log2);
       need = (int)(((long long)len + add + ps - 1) >> a.ps_log2);
@@ -129,14 +132,14 @@ __global__ void __launch_bounds__(kThreads) extend_pages_kernel(const LsExtendAr
       int m = -1;
       long long begin = 0, end = 0;
       // packed, the tokens end at `total`; with rows every one belongs to a member
-      const long long stop = a.rows ? a.capacity : total;
+      const long long stop = kRows ? a.capacity : total;
 #pragma unroll
       for (int e = 0; e < kPerThread; ++e) {
         slot[e] = -1;
         pos[e] = 0;
         const long long t = i + e;
         if (!ok || t >= stop) continue;
-        if (a.rows) {
+        if (kRows) {
           m = (int)(t / a.rows);
           end = (long long)(m + 1) * a.rows;
           begin = end - (p.tok_end[m] - (m ? p.tok_end[m - 1] : 0));
@@ -212,12 +215,13 @@ cudaError_t ls_launch_extend_pages(const LsExtendArgs& a, int sms, cudaStream_t 
   for (const auto& i : in)
     in_place = in_place || meets(a.lens_out, a.members, i.p, i.n) || meets(a.used_out, 1, i.p, i.n);
   const bool one = blocks == 1 || !in_place;
-  extend_pages_kernel<<<(unsigned)blocks, kThreads, 0, st>>>(a, 1, one ? 1 : 0);
+  const auto kernel = a.rows ? extend_pages_kernel<true> : extend_pages_kernel<false>;
+  kernel<<<(unsigned)blocks, kThreads, 0, st>>>(a, 1, one ? 1 : 0);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   ls_note_launch();
   if (!one) {
-    extend_pages_kernel<<<1, kThreads, 0, st>>>(a, 0, 1);
+    kernel<<<1, kThreads, 0, st>>>(a, 0, 1);
     e = cudaGetLastError();
     if (e == cudaSuccess) ls_note_launch();
   }
