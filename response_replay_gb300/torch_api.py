@@ -49,11 +49,19 @@ _captured_workspaces: list = []  # of captures that torch does not know of
 
 
 def _graph_memory(t: torch.Tensor) -> bool:
-    """Whether t lies in a pool of its own (that of the torch.cuda.CUDAGraph being
-    captured), which outlives t, or in the memory that all tensors share."""
+    """Whether t, made during a capture, lies in memory that is the graph's: in a pool of its
+    own (that of the torch.cuda.CUDAGraph being captured), not in the one that all tensors
+    share; or from the stream-ordered allocator, whose allocations and releases are captured
+    themselves.  An allocator that does not say counts as shared."""
+    if torch.cuda.get_allocator_backend() == "cudaMallocAsync":
+        return True
+    try:
+        segments = torch.cuda.memory_snapshot()
+    except RuntimeError:
+        return False
     p = t.data_ptr()
     return any(s["address"] <= p < s["address"] + s["total_size"] and tuple(s["segment_pool_id"]) != (0, 0)
-               for s in torch.cuda.memory_snapshot())
+               for s in segments)
 
 
 def _with_workspace(call, args: tuple, size, like: torch.Tensor, key: str, stream: int) -> None:

@@ -2,6 +2,9 @@
 from several host threads, captures that torch does not make, members that end at different
 times; and of every V tile's way into the output."""
 import ctypes as C
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -301,3 +304,37 @@ def test_every_v_tile_shows(cuda, P, lens, hq, hkv, n, ps, rps, mod):
                         for k in (g.kp, g.kr[m]) if len(k))
         assert 64 / (P + x) * np.exp(-2 * s) > 2 * ob[m].max(), m
     g.check(o, lse)
+
+
+ASYNC = """
+import sys
+sys.path[:0] = {paths!r}
+import torch
+from response_replay_gb300 import binding as B, torch_api as api
+from test_gpu_decode import SCALE, Group
+assert torch.cuda.get_allocator_backend() == "cudaMallocAsync"
+g = Group(torch.device("cuda:0"), 3000, [50, 9], 12, 2, seed=71)
+want = [t.clone() for t in g.run()]
+graph = torch.cuda.CUDAGraph()
+outs = [torch.empty_like(t) for t in want]
+with torch.cuda.graph(graph):
+    for _ in range(3):
+        api.decode_attn(g.cache, g.resp, g.q, SCALE, o=outs[0], lse=outs[1])
+for _ in range(3):
+    for t in outs:
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want, strict=True))
+assert B.ls_last_device_error(0) == B.LS_OK and not api._captured_workspaces
+"""
+
+
+def test_captured_with_the_stream_ordered_allocator(cuda):
+    """A process whose allocator is cudaMallocAsync: captured calls and their replays."""
+    tests = os.path.dirname(os.path.abspath(__file__))
+    env = {**os.environ, "PYTORCH_CUDA_ALLOC_CONF": "backend:cudaMallocAsync",
+           "PYTORCH_ALLOC_CONF": "backend:cudaMallocAsync"}
+    r = subprocess.run([sys.executable, "-c", ASYNC.format(paths=[os.path.dirname(tests), tests])], env=env,
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]

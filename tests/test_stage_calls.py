@@ -112,6 +112,7 @@ def test_a_captured_workspace_lives_as_long_as_its_graph(monkeypatch, pool, kept
     like = empty(0)
     monkeypatch.setattr(torch, "empty", recorded)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    monkeypatch.setattr(torch.cuda, "get_allocator_backend", lambda: "native")
     monkeypatch.setattr(torch.cuda, "memory_snapshot", lambda *a: segments)
     monkeypatch.setattr(api, "_captured_workspaces", [], raising=False)
     for _ in range(2):
@@ -187,3 +188,15 @@ def test_eps_refused(eps):
     view = B.ls_qkv_view(A, A, A, *(4096, 128) * 3)
     norm = B.ls_qk_norm(A, A, B.LS_FP32, 0.0, eps)
     assert lib.ls_qk_norm_rope_fwd(view, 4, 8, 4, norm, None, None, view, None) == B.LS_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("backend,graph", [("cudaMallocAsync", True), ("pluggable", False)])
+def test_captured_workspaces_of_other_allocators(monkeypatch, backend, graph):
+    """The stream-ordered allocator's memory is the graph's; one that keeps no record of its
+    segments is taken not to have pools."""
+    def none(*a):
+        raise RuntimeError("no snapshot")
+
+    monkeypatch.setattr(torch.cuda, "get_allocator_backend", lambda: backend)
+    monkeypatch.setattr(torch.cuda, "memory_snapshot", none)
+    assert api._graph_memory(torch.empty(1)) is graph
