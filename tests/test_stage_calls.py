@@ -200,3 +200,9 @@ def test_captured_workspaces_of_other_allocators(monkeypatch, backend, graph):
     monkeypatch.setattr(torch.cuda, "get_allocator_backend", lambda: backend)
     monkeypatch.setattr(torch.cuda, "memory_snapshot", none)
     assert api._graph_memory(torch.empty(1)) is graph
+
+
+@pytest.mark.parametrize("pos0", [-1, 2 ** 31, 2 ** 32 + 7])
+def test_positions_past_an_int_are_refused(pos0):
+    with pytest.raises(ValueError, match="pos0"):
+        api.extend_pages(None, None, pos0, None)
