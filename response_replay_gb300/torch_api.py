@@ -822,7 +822,7 @@ def extend_pages(alloc: PageAllocator, add: torch.Tensor, pos0: int, slots: torc
         with _as_current(stream):
             return extend_pages(alloc, add, pos0, slots, positions, lens_out, used_out,
                                 member_rows=member_rows)
-    if not 0 <= pos0 < 2 ** 31:  # a C int takes any other's low bits
+    if not -2 ** 31 <= pos0 < 2 ** 31:  # a C int would take its low bits
         raise ValueError(f"pos0 must be a position, got {pos0}")
     M, dev, i32 = alloc.members, alloc.device_index, torch.int32
     st = _dev_stream(dev)

@@ -202,7 +202,7 @@ def test_captured_workspaces_of_other_allocators(monkeypatch, backend, graph):
     assert api._graph_memory(torch.empty(1)) is graph
 
 
-@pytest.mark.parametrize("pos0", [-1, 2 ** 31, 2 ** 32 + 7])
+@pytest.mark.parametrize("pos0", [-2 ** 31 - 1, 2 ** 31, 2 ** 32 + 7])
 def test_positions_past_an_int_are_refused(pos0):
     with pytest.raises(ValueError, match="pos0"):
         api.extend_pages(None, None, pos0, None)
