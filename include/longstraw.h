@@ -419,8 +419,9 @@ ls_status ls_mla_replay_bwd(const ls_latent_cache* cache, const void* q, const v
 /* ---------------------------------------------------------------- query / key stage
  * What a layer does to its projections before attention: the RMS norm of every query and
  * key head and the rotary positions, in one pass, at the layouts the projections have
- * and the replay calls want.  The pages' model norms its query and key heads; they give
- * no formula, so the common one is taken.  For a head x of 128 values at token t:
+ * and the replay calls want.  The pages begin at queries and keys as attention takes them and
+ * say nothing of this stage, so the common formula is taken.  For a head x of 128 values at
+ * token t:
  *   r = 1 / sqrt(mean_i x_i^2 + eps),   u_i = x_i r (w_offset + w_i),
  *   y = u, with each pair (a, b) of its first rot_dim values turned by the pair's angle
  *       p inv_freq[j]: (a cos - b sin, b cos + a sin), p = positions[pair_axis[j]][t].
@@ -434,8 +435,8 @@ ls_status ls_mla_replay_bwd(const ls_latent_cache* cache, const void* q, const v
  * alike), so that a packed projection's slices need no copy.  Strides are multiples of 8
  * elements; rows of an output may not overlap.  An output may be the input itself (the
  * same pointers and strides), otherwise the two may not overlap.
- * ls_qk_norm: weights [128] of type w_dtype, or NULL for ones; w_offset is 1 for weights
- * that are stored around zero.  A NULL ls_qk_norm* leaves the norm out (y = the turned x).
+ * ls_qk_norm: weights [128] of type w_dtype, or NULL for none (u_i = x_i r whatever
+ * w_offset is); w_offset is 1 for weights that are stored around zero.  A NULL ls_qk_norm* leaves the norm out (y = the turned x).
  * ls_rotary: rot_dim a multiple of 16 up to 128 (0, or a NULL ls_rotary*: no rotation);
  * inv_freq fp64 [rot_dim / 2] (finite), radians per position; pair_axis int32 [rot_dim / 2]
  * gives the axis of each pair (time, height, width, ... of image and video tokens), NULL

@@ -409,10 +409,11 @@ norm_rope_fwd_kernel(const __grid_constant__ LsNormRopeArgs a, const __grid_cons
 // token, then into its half-warp's place in shared memory; a block leaves one partial per
 // weight, which norm_rope_dw sums in block order.
 // 4,096 tokens of 24 / 4 / 4 heads with fp32 gradients take 36 us with the sum (54% of the
-// copy's rate), 20,011 tokens of 12 / 2 / 2 with bf16 47 us (74%): a row takes about 210
-// instructions a warp and two reductions over 16 lanes, which 16 warps an SM do not hide.
-// Two rows a batch: 36 and 48 us, four 39 and 47; three blocks an SM spill registers (81 and
-// 76 us).
+// copy's rate), 20,011 tokens of 12 / 2 / 2 with bf16 48 us (73%): a row takes about 210
+// instructions a warp and two reductions over 16 lanes, a vote between them and the next row,
+// so a warp has one row's chain under way, which 16 warps an SM do not hide (63% of the
+// issue slots).  Two rows a batch: 36 and 48 us where three took 35 and 47, four 39 and 47;
+// three blocks an SM spill registers (81 and 76 us).
 constexpr int kBwdRows = 3, kBwdCtas = 2;
 template <bool kBf16> constexpr int bwd_units() { return kBf16 ? 2 : 3; }  // 16 bytes each
 
