@@ -41,7 +41,7 @@ class _StreamWorkspace:
     __slots__ = ("lock", "buf")
 
     def __init__(self):
-        self.lock, self.buf = threading.Lock(), None
+        self.lock, self.buf = threading.RLock(), None  # a finalizer may call
 
 
 _stream_workspaces: dict = {}

@@ -206,3 +206,17 @@ def test_captured_workspaces_of_other_allocators(monkeypatch, backend, graph):
 def test_positions_past_an_int_are_refused(pos0):
     with pytest.raises(ValueError, match="pos0"):
         api.extend_pages(None, None, pos0, None)
+
+
+def test_a_call_within_a_call_does_not_wait_for_itself(host_calls):
+    """A finalizer or a signal handler that calls while the same thread is between a call's
+    lookup and its launch."""
+    done = []
+
+    def body(i):
+        host_calls(lambda ws: host_calls(lambda inner: done.append(inner), 5000), 1000)
+
+    t = threading.Thread(target=body, args=(0,), daemon=True)
+    t.start()
+    t.join(10)
+    assert not t.is_alive() and len(done) == 1
