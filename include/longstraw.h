@@ -28,6 +28,14 @@
  *                          (_by_member) in every member's own rows
  *   ls_decode_attn         the rollout's decode step: every member's newest tokens over
  *                          the shared captured prompt and its own paged response
+ *   ls_draft_tree, ls_decode_attn_tree, ls_accept_draft, ls_compact_rows
+ *                          the decode step over a tree of drafted tokens a member: its plan,
+ *                          its attention, the accepted path, and that path's keys and values
+ *                          moved together
+ *   ls_trim_pages, ls_fork_pages, ls_copy_pages
+ *                          pages given back, and shared by branches of a response
+ *   ls_token_logp_*        log probabilities of given tokens, entropies and top alternatives
+ *                          of vocabulary rows, and their backward
  *
  * Conventions shared by every call
  *   - Memory: every pointer argument is DEVICE memory on the current CUDA device unless
@@ -589,6 +597,148 @@ ls_status ls_decode_attn_workspace(const ls_kv_cache* cache, const ls_resp_cache
 ls_status ls_decode_attn(const ls_kv_cache* cache, const ls_resp_cache* resp, const void* q,
                          int n, int Hq, float softmax_scale, void* o, float* lse,
                          void* workspace, size_t workspace_bytes, ls_stream_t stream);
+
+/* ---------------------------------------------------------------- drafted trees
+ * A decode step over drafted tokens: every member's draft is a tree of tokens that the policy
+ * looks at in one pass; of it the path that the policy itself chooses is kept.  (The pages
+ * describe no rollout; this is the decode step above for several continuations at once.)
+ *
+ * A step has n rows a member (1 to 128), and the last drafted[m] of them are its draft; drafted
+ * NULL: all n.  The rows before are padding.  lens[m] counts the draft, whose keys are the
+ * member's last ones: row r's is key lens[m] - n + r, and keys before lens[m] - drafted[m] are
+ * the context.  (ls_extend_pages_by_member with rows = n and add = drafted gives these slots.)
+ * parents int32 [members][n]: row r's node continues node parents[m][r], an earlier row of the
+ * draft, or -1: the context.  Another value sets LS_ERR_DEVICE_CHECK and is taken as -1, as does
+ * a drafted[m] outside 0 .. min(n, lens[m]), which is cut.  A member out of use (lens[m] < 0)
+ * has no draft.  members <= 1024.
+ *
+ * ls_draft_tree: the plan of a step, once for all layers.
+ *   visible    int32 [members][n][ceil(n / 32)]: bit j of row r (bit j % 32 of word j / 32) is
+ *              set when r sees row j: itself and its ancestors.  0 in padding rows
+ *   positions  int32 [axes][members][n] or NULL: pos0 + context + depth (a node behind the
+ *              context has depth 0), the same on every axis; 0 in padding rows */
+ls_status ls_draft_tree(const int32_t* parents, const int32_t* lens, const int32_t* drafted,
+                        int members, int n, int pos0, int axes, int32_t* visible,
+                        int32_t* positions, ls_stream_t stream);
+
+/* ls_decode_attn_tree: ls_decode_attn for trees.  Row r of member m sees all P prompt
+ * positions, the member's context, and of its draft the rows whose bits are set in
+ * visible[m][r] (any bits, not only a tree's; bits of padding rows and behind n count for
+ * nothing).  q, o, lse as there; padding rows of o and lse are not written, nor are those of a
+ * member out of use; a row that sees no key gets o = 0 and lse = -inf.  resp->lens counts the
+ * drafts.  n <= 128, Hq / num_kv_heads <= 128, and members * n * Hq / num_kv_heads rows of at
+ * most 128 per SM, else LS_ERR_UNSUPPORTED.  Values must be finite where a row may not look
+ * within the draft.  The rest as ls_decode_attn. */
+ls_status ls_decode_attn_tree_workspace(const ls_kv_cache* cache, const ls_resp_cache* resp, int n,
+                                        int Hq, size_t* bytes);
+ls_status ls_decode_attn_tree(const ls_kv_cache* cache, const ls_resp_cache* resp, const void* q,
+                              int n, int Hq, const int32_t* visible, const int32_t* drafted,
+                              float softmax_scale, void* o, float* lse, void* workspace,
+                              size_t workspace_bytes, ls_stream_t stream);
+
+/* ls_accept_draft: which nodes the policy keeps.  tokens int32 [members][n]: the drafted tokens;
+ * chosen int32 [members][n]: the policy's own token behind each row (sampled or the most likely
+ * one: the caller's).  The draft's first row is always kept (its token is the one chosen in the
+ * step before); then, from a kept row, its child whose token is the one chosen there (the first
+ * such row; negative tokens match nothing), and so on.  Other rows with parent -1 are not kept.
+ *   rows    int32 [members][n]: the kept rows, ascending; -1 behind them
+ *   count   int32 [members]: how many;  ends int32 [members]: context + count (a negative
+ *           length as it is)
+ *   follow  int32 [members]: the token chosen behind the last kept row; -1 without a draft */
+ls_status ls_accept_draft(const int32_t* parents, const int32_t* tokens, const int32_t* chosen,
+                          const int32_t* lens, const int32_t* drafted, int members, int n,
+                          int32_t* rows, int32_t* count, int32_t* follow, int32_t* ends,
+                          ls_stream_t stream);
+
+/* ls_compact_rows: in the pages of every layer, the key and value of rows[m][i] become the
+ * i-th of those behind member m's context.  Layer l's pools begin l * layer_stride values (a
+ * multiple of 8, at least a pool's size) behind pool's.  rows, count as from ls_accept_draft
+ * (rows ascending within the draft; a count or row that is not sets LS_ERR_DEVICE_CHECK and moves
+ * nothing of the member, as does a length past the table; a page id outside the pool sets it and
+ * moves nothing of the row).  Lengths are not changed: ls_trim_pages to `ends` follows.  No two
+ * members may hold a page of their drafts together. */
+ls_status ls_compact_rows(const ls_page_pool* pool, int layers, int64_t layer_stride,
+                          const int32_t* block_table, int max_blocks, const int32_t* lens,
+                          const int32_t* drafted, int members, int n, const int32_t* rows,
+                          const int32_t* count, ls_stream_t stream);
+
+/* ---------------------------------------------------------------- pages given back and shared
+ * Beside ls_extend_pages, on the same arrays.  shared int32 [num_pages]: how many members hold
+ * a page besides the first (0 for pages that ls_extend_pages gives out).
+ *
+ * ls_trim_pages: member m keeps its first new_lens[m] <= lens[m] tokens; new_lens[m] < 0 puts
+ * it out of use (lens -1).  Pages behind the new end lose m as an owner, and those without one
+ * left go back: they become free_list[used - freed .. used), in member and block order, and
+ * used falls by their number.  The table's entries stay as they are.  shared NULL: no page has
+ * a second owner.  lens_out and used_out may be the inputs themselves (lens_out also new_lens).
+ * All or nothing: when a new length passes the old one (a member out of use has a negative
+ * one), a length its row of the table, a page id the pool, a page is given back more often than
+ * it is held, more pages than are in use, or a member would end inside a page that others
+ * still hold (it would write there next; branch it with ls_fork_pages instead),
+ * LS_ERR_DEVICE_CHECK is recorded, lens_out and used_out repeat the inputs, and nothing else
+ * changes. */
+ls_status ls_trim_pages(const int32_t* block_table, int members, int max_blocks, int page_size,
+                        int num_pages, const int32_t* lens, const int32_t* new_lens,
+                        int32_t* free_list, int num_free, const int32_t* used, int32_t* shared,
+                        int32_t* lens_out, int32_t* used_out, ls_stream_t stream);
+
+/* ls_fork_pages: member m with src[m] >= 0 becomes a branch of member src[m]: its first keep[m]
+ * tokens (keep NULL: all).  m is out of use or holds no tokens, src[m] is in use and no branch
+ * of this call.  Whole pages are shared; for a partial last one m takes a page of its own, in
+ * member order from free_list[*used] on, into which its rows are to be copied, in every layer:
+ *   copies  int32 [3][members]: from page, to page, rows; (-1, -1, 0) where there is none.
+ *           The three rows are ls_copy_pages' from, to and rows
+ * All or nothing, as ls_trim_pages; copies then says that there is none.  src[m] < 0: m stays
+ * as it is.  lens_out and used_out may be the inputs themselves. */
+ls_status ls_fork_pages(int32_t* block_table, int members, int max_blocks, int page_size,
+                        int num_pages, const int32_t* lens, const int32_t* src, const int32_t* keep,
+                        const int32_t* free_list, int num_free, const int32_t* used,
+                        int32_t* shared, int32_t* copies, int32_t* lens_out, int32_t* used_out,
+                        ls_stream_t stream);
+
+/* ls_copy_pages: the first rows[i] rows (rows NULL: all) of every KV head of page from[i] to
+ * page to[i], keys and values, in every layer (as in ls_compact_rows), for i < count.  Bit copy.
+ * from[i] and to[i] both negative: nothing.  Another id outside the pool, or rows[i] outside
+ * [0, page_size], sets LS_ERR_DEVICE_CHECK and copies nothing of the pair.  A page that is
+ * written may appear only once. */
+ls_status ls_copy_pages(const ls_page_pool* pool, int layers, int64_t layer_stride, int count,
+                        const int32_t* from, const int32_t* to, const int32_t* rows,
+                        ls_stream_t stream);
+
+/* ---------------------------------------------------------------- token statistics
+ * What rollouts log and objectives are made of, beside the fused loss above.  For a row of
+ * logits z, temperature tau (1e-6 to 1e6) and target y:
+ *   lse = log sum_v exp(z_v / tau),  logp = z_y / tau - lse,  p_v = exp(z_v / tau - lse),
+ *   entropy = -sum_v p_v log p_v,
+ *   alternatives: the top (0 to 32, <= V) largest z_v / tau - lse with their ids, equal ones by
+ *   the lowest id first.
+ * logits: T rows of V values of type dtype, row_stride >= V values apart (a padded vocabulary's
+ * rows need no copy; values behind V are not read), aligned to their own size.  targets int32
+ * [T]: -1 marks a padding row, whose outputs are 0 and ids -1 and whose logits are not read;
+ * another one outside [0, V) sets LS_ERR_DEVICE_CHECK and gives logp = NaN.  Outputs fp32 [T],
+ * each or NULL: logp (needs targets), lse, entropy; targets NULL: no row is padding.  top_logp
+ * fp32 and top_ids int32 [T][top] (4-byte aligned, as every array here).  A logit of -inf (or
+ * the type's lowest value) has probability 0; a row with a NaN or +inf, or without a finite
+ * logit, has NaN numbers, and its ids are of V or -1.
+ *
+ * Backward, with upstream d_logp [T], d_entropy [T] (each or NULL) and d_top [T][top] (top 0:
+ * none) and G = d_logp + sum_j d_top_j:
+ *   dlogits_v = (d_logp 1[v = y] + sum_j d_top_j 1[v = top_ids_j]
+ *                - p_v (G + d_entropy (log p_v + entropy))) / tau
+ * of type dtype, rows d_row_stride >= V apart (values behind V are left alone); zeros in padding
+ * rows.  It may be the logits themselves (same pointer and stride), otherwise the two may not
+ * overlap.  lse and entropy (needed with d_entropy) are the forward's, top_ids any ids.  A target
+ * or id outside [0, V) sets LS_ERR_DEVICE_CHECK and makes its row NaN. */
+ls_status ls_token_logp_fwd_workspace(ls_dtype dtype, int64_t T, int V, int top, size_t* bytes);
+ls_status ls_token_logp_fwd(const void* logits, ls_dtype dtype, int64_t T, int V, int64_t row_stride,
+                            const int32_t* targets, float temperature, int top, float* logp,
+                            float* lse, float* entropy, float* top_logp, int32_t* top_ids,
+                            void* workspace, size_t workspace_bytes, ls_stream_t stream);
+ls_status ls_token_logp_bwd(const void* logits, ls_dtype dtype, int64_t T, int V, int64_t row_stride,
+                            const int32_t* targets, float temperature, const float* lse,
+                            const float* entropy, int top, const int32_t* top_ids,
+                            const float* d_logp, const float* d_entropy, const float* d_top,
+                            void* dlogits, int64_t d_row_stride, ls_stream_t stream);
 
 /* ---------------------------------------------------------------- checks
  * ls_validate_page_table: enqueue a check that every entry of the page table covering

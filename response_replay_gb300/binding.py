@@ -33,7 +33,9 @@ EXPORTED = (
     "ls_mla_replay_bwd_workspace", "ls_mla_replay_bwd",
     "ls_qk_norm_rope_fwd", "ls_qk_norm_rope_append", "ls_qk_norm_rope_bwd_workspace",
     "ls_qk_norm_rope_bwd", "ls_extend_pages", "ls_extend_pages_by_member", "ls_decode_attn_workspace",
-    "ls_decode_attn",
+    "ls_decode_attn", "ls_decode_attn_tree_workspace", "ls_decode_attn_tree", "ls_draft_tree",
+    "ls_accept_draft", "ls_compact_rows", "ls_copy_pages", "ls_trim_pages", "ls_fork_pages",
+    "ls_token_logp_fwd_workspace", "ls_token_logp_fwd", "ls_token_logp_bwd",
 )
 
 
@@ -163,6 +165,17 @@ def lib() -> C.CDLL:
                                           P, P, P],
             "ls_decode_attn_workspace": [cache, rcache, i32, i32, szp],
             "ls_decode_attn": [cache, rcache, P, i32, i32, f32, P, P, P, sz, P],
+            "ls_decode_attn_tree_workspace": [cache, rcache, i32, i32, szp],
+            "ls_decode_attn_tree": [cache, rcache, P, i32, i32, P, P, f32, P, P, P, sz, P],
+            "ls_draft_tree": [P, P, P, i32, i32, i32, i32, P, P, P],
+            "ls_accept_draft": [P, P, P, P, P, i32, i32, P, P, P, P, P],
+            "ls_compact_rows": [C.POINTER(ls_page_pool), i32, i64, P, i32, P, P, i32, i32, P, P, P],
+            "ls_copy_pages": [C.POINTER(ls_page_pool), i32, i64, i32, P, P, P, P],
+            "ls_trim_pages": [P, i32, i32, i32, i32, P, P, P, i32, P, P, P, P, P],
+            "ls_fork_pages": [P, i32, i32, i32, i32, P, P, P, P, i32, P, P, P, P, P, P],
+            "ls_token_logp_fwd_workspace": [i32, i64, i32, i32, szp],
+            "ls_token_logp_fwd": [P, i32, i64, i32, i64, P, f32, i32, P, P, P, P, P, P, sz, P],
+            "ls_token_logp_bwd": [P, i32, i64, i32, i64, P, f32, P, P, i32, P, P, P, P, P, i64, P],
         })
         for name, args in sig.items():
             f = getattr(l, name)
@@ -449,3 +462,83 @@ def ls_decode_attn(cache: ls_kv_cache, resp: ls_resp_cache, q: int, n: int, Hq: 
     _ok("ls_decode_attn",
         lib().ls_decode_attn(cache, resp, q, n, Hq, softmax_scale, o, lse,
                              workspace, workspace_bytes, stream))
+
+
+def ls_decode_attn_tree_workspace(cache: ls_kv_cache, resp: ls_resp_cache, n: int, Hq: int) -> int:
+    return _size("ls_decode_attn_tree_workspace", C.byref(cache), C.byref(resp), n, Hq)
+
+
+def ls_decode_attn_tree(cache: ls_kv_cache, resp: ls_resp_cache, q: int, n: int, Hq: int,
+                        visible: int, drafted: int | None, softmax_scale: float, o: int, lse: int,
+                        workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _ok("ls_decode_attn_tree",
+        lib().ls_decode_attn_tree(cache, resp, q, n, Hq, visible, drafted, softmax_scale, o, lse,
+                                  workspace, workspace_bytes, stream))
+
+
+def ls_draft_tree(parents: int, lens: int, drafted: int | None, members: int, n: int, pos0: int,
+                  axes: int, visible: int, positions: int | None, stream: int = 0) -> None:
+    _ok("ls_draft_tree",
+        lib().ls_draft_tree(parents, lens, drafted, members, n, pos0, axes, visible, positions,
+                            stream))
+
+
+def ls_accept_draft(parents: int, tokens: int, chosen: int, lens: int, drafted: int | None,
+                    members: int, n: int, rows: int, count: int, follow: int, ends: int,
+                    stream: int = 0) -> None:
+    _ok("ls_accept_draft",
+        lib().ls_accept_draft(parents, tokens, chosen, lens, drafted, members, n, rows, count,
+                              follow, ends, stream))
+
+
+def ls_compact_rows(pool: ls_page_pool, layers: int, layer_stride: int, block_table: int,
+                    max_blocks: int, lens: int, drafted: int | None, members: int, n: int, rows: int,
+                    count: int, stream: int = 0) -> None:
+    _ok("ls_compact_rows",
+        lib().ls_compact_rows(pool, layers, layer_stride, block_table, max_blocks, lens, drafted,
+                              members, n, rows, count, stream))
+
+
+def ls_copy_pages(pool: ls_page_pool, layers: int, layer_stride: int, count: int, from_: int, to: int,
+                  rows: int | None, stream: int = 0) -> None:
+    _ok("ls_copy_pages",
+        lib().ls_copy_pages(pool, layers, layer_stride, count, from_, to, rows, stream))
+
+
+def ls_trim_pages(block_table: int, members: int, max_blocks: int, page_size: int, num_pages: int,
+                  lens: int, new_lens: int, free_list: int, num_free: int, used: int,
+                  shared: int | None, lens_out: int, used_out: int, stream: int = 0) -> None:
+    _ok("ls_trim_pages",
+        lib().ls_trim_pages(block_table, members, max_blocks, page_size, num_pages, lens, new_lens,
+                            free_list, num_free, used, shared, lens_out, used_out, stream))
+
+
+def ls_fork_pages(block_table: int, members: int, max_blocks: int, page_size: int, num_pages: int,
+                  lens: int, src: int, keep: int | None, free_list: int, num_free: int, used: int,
+                  shared: int, copies: int, lens_out: int, used_out: int, stream: int = 0) -> None:
+    _ok("ls_fork_pages",
+        lib().ls_fork_pages(block_table, members, max_blocks, page_size, num_pages, lens, src, keep,
+                            free_list, num_free, used, shared, copies, lens_out, used_out, stream))
+
+
+def ls_token_logp_fwd_workspace(dtype: int, T: int, V: int, top: int) -> int:
+    return _size("ls_token_logp_fwd_workspace", dtype, T, V, top)
+
+
+def ls_token_logp_fwd(logits: int, dtype: int, T: int, V: int, row_stride: int, targets: int | None,
+                      temperature: float, top: int, logp: int | None, lse: int | None,
+                      entropy: int | None, top_logp: int | None, top_ids: int | None,
+                      workspace: int | None, workspace_bytes: int, stream: int = 0) -> None:
+    _ok("ls_token_logp_fwd",
+        lib().ls_token_logp_fwd(logits, dtype, T, V, row_stride, targets, temperature, top, logp, lse,
+                                entropy, top_logp, top_ids, workspace, workspace_bytes, stream))
+
+
+def ls_token_logp_bwd(logits: int, dtype: int, T: int, V: int, row_stride: int, targets: int | None,
+                      temperature: float, lse: int, entropy: int | None, top: int,
+                      top_ids: int | None, d_logp: int | None, d_entropy: int | None,
+                      d_top: int | None, dlogits: int, d_row_stride: int, stream: int = 0) -> None:
+    _ok("ls_token_logp_bwd",
+        lib().ls_token_logp_bwd(logits, dtype, T, V, row_stride, targets, temperature, lse, entropy,
+                                top, top_ids, d_logp, d_entropy, d_top, dlogits, d_row_stride,
+                                stream))

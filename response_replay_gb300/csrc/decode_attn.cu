@@ -60,6 +60,7 @@ using namespace umma;
 
 constexpr int kD = 128;
 constexpr int kTile = 128;
+constexpr int kTreeTokens = 128;
 constexpr int kRing = 3;  // K tiles, and V tiles, in shared memory
 constexpr int kThreads = 384;
 constexpr int kSoftmaxThreads = 256;
@@ -126,6 +127,29 @@ __device__ __forceinline__ int32_t clamp_len(const LsDecodeArgs& a, int32_t len)
   if (len < 0) return 0;
   return len < room ? len : (int32_t)room;
 }
+// Row groups of the responses: a member's rows, or with a tree the rows of up to a.tpt of its
+// tokens (as many whole tokens as fit a row tile), group by group; a group walks the member's
+// keys like a member of its own.
+template <bool kTree>
+__device__ __forceinline__ int32_t groups_of(const LsDecodeArgs& a) {
+  return kTree ? a.M * a.rtm : a.M;
+}
+template <bool kTree>
+__device__ __forceinline__ int32_t member_of(const LsDecodeArgs& a, int32_t group) {
+  return kTree ? group / a.rtm : group;
+}
+// Drafted tokens of a member, the last of its n.
+__device__ __forceinline__ int32_t drafted_of(const LsDecodeArgs& a, int32_t m) {
+  return a.drafted ? min(max(__ldg(a.drafted + m), 0), a.n) : a.n;
+}
+// Keys that a row group meets: none when all of its tokens are padding.
+template <bool kTree>
+__device__ __forceinline__ int32_t group_len(const LsDecodeArgs& a, int32_t group) {
+  const int32_t m = member_of<kTree>(a, group);
+  const int32_t len = clamp_len(a, __ldg(a.lens + m));
+  if (!kTree) return len;
+  return (group - m * a.rtm + 1) * a.tpt <= a.n - drafted_of(a, m) ? 0 : len;
+}
 __device__ __forceinline__ int32_t tiles_of(int32_t len) {
   return (int32_t)(((long long)len + kTile - 1) / kTile);
 }
@@ -170,16 +194,17 @@ struct Cut {
 // One segment: `count` tiles from key `key0` of one source; rows of one row tile.
 struct Seg {
   bool resp;
-  int32_t kvh, m;       // KV head; member (responses)
+  int32_t kvh, m;       // KV head; row group (responses)
   int32_t item;         // KV head (prompt) or m * hkv + kvh
   int32_t key0, count;
   int32_t len;          // keys of the source
 };
 
+template <bool kTree>
 struct Walk {
   const LsDecodeArgs& a;
   int32_t p, p_end, r, r_end;
-  int32_t m, off;       // member and unit within its KV heads' units
+  int32_t m, off;       // row group and unit within its KV heads' units
   __device__ __forceinline__ Walk(const LsDecodeArgs& a_, const volatile int32_t* start, int32_t p0,
                                   int32_t p1, int32_t r0, int32_t r1)
       : a(a_), p(p0), p_end(p1), r(r0), r_end(r1), m(start[0]), off(start[1]) {}
@@ -196,13 +221,13 @@ struct Walk {
     }
     while (r < r_end) {
       int32_t len = 0, nt = 0, nu = 0;
-      for (; m < a.M; ++m, off = 0) {
-        len = clamp_len(a, __ldg(a.lens + m));
+      for (; m < groups_of<kTree>(a); ++m, off = 0) {
+        len = group_len<kTree>(a, m);
         nt = tiles_of(len);
         nu = units_of(nt);
         if (off < nu * a.hkv) break;
       }
-      if (m >= a.M) return false;  // only when lengths changed under the kernel
+      if (m >= groups_of<kTree>(a)) return false;  // only when lengths changed under the kernel
       const int32_t h = off / nu, x = off - h * nu, step = min(r_end - r, nu - x);
       r += step;
       off += step;
@@ -228,13 +253,21 @@ struct Walk {
 };
 
 // Query rows of a segment: row r of row tile rt is row rt x 128 + r of all (token, head of
-// the group) pairs against the prompt, row r of the member's own against a response.
+// the group) pairs against the prompt, row r of the row group's own against a response.
+// seg_token: the first token of a response segment's rows, among its member's.
+template <bool kTree>
+__device__ __forceinline__ int32_t seg_token(const LsDecodeArgs& a, const Seg& s) {
+  return kTree ? (s.m - member_of<kTree>(a, s.m) * a.rtm) * a.tpt : 0;
+}
+template <bool kTree>
 __device__ __forceinline__ int32_t seg_rows(const LsDecodeArgs& a, const Seg& s, int32_t rt) {
-  return s.resp ? a.n * a.g : min(a.M * a.n * a.g - rt * kTile, kTile);
+  if (!s.resp) return min(a.M * a.n * a.g - rt * kTile, kTile);
+  return kTree ? min(a.n - seg_token<kTree>(a, s), a.tpt) * a.g : a.n * a.g;
 }
 
+template <bool kTree>
 __device__ __forceinline__ bool whole_q(const LsDecodeArgs& a, const Seg& s, int32_t rt) {
-  return seg_rows(a, s, rt) > kHalfRows;
+  return seg_rows<kTree>(a, s, rt) > kHalfRows;
 }
 __device__ __forceinline__ uint32_t q_offset(bool whole, uint32_t seg) {
   return kOffQ + (whole ? 0u : (seg & 1) * kHalfRows * 128u);
@@ -249,10 +282,11 @@ struct Loader {
   int32_t len, key0, boxes, box_rows, ps_log2, pages, hkv, kvh, pool_rows;
   int32_t page[kMaxBoxes];
 
+  template <bool kTree>
   __device__ __forceinline__ void open(const LsDecodeArgs& a, const Seg& s, const void* prompt_map,
                                        const void* resp_map) {
     map = s.resp ? resp_map : prompt_map;
-    table = s.resp ? a.blocks + (int64_t)s.m * a.max_blocks : a.page_table;
+    table = s.resp ? a.blocks + (int64_t)member_of<kTree>(a, s.m) * a.max_blocks : a.page_table;
     ps_log2 = s.resp ? a.r_ps_log2 : a.ps_log2;
     pages = s.resp ? a.r_num_pages : a.num_pages;
     box_rows = min(1 << ps_log2, kTile);
@@ -303,7 +337,7 @@ struct Loader {
 // of up to 8,192 tokens took 123 us where this takes 103.  Transposed by shuffles instead,
 // the group of 64 members below took 259 us for 246.)
 __host__ __device__ __forceinline__ int32_t resp_rows_of(const LsDecodeArgs& a) {
-  return (a.n * a.g + 7) & ~7;
+  return (a.tpt * a.g + 7) & ~7;
 }
 __device__ __forceinline__ int64_t prompt_row0(const LsDecodeArgs& a, int32_t h, int32_t col,
                                                int32_t rt) {
@@ -320,6 +354,24 @@ __host__ __device__ __forceinline__ int64_t prompt_rows_of(const LsDecodeArgs& a
   return a.nt > 0 ? ((int64_t)a.hkv + a.cols) * a.rts * kTile : 0;
 }
 
+// What a row of a tree may see of the 64 keys from key kb on: the member's context (the keys
+// before its drafted ones), and of the drafted ones those of its bits.  d: kb counted from the
+// key of the member's first row; pad: rows before the first drafted one.
+__device__ __forceinline__ uint64_t tree_window(const LsDecodeArgs& a, const uint32_t* bits, int32_t d,
+                                                int32_t pad) {
+  auto words = [&](int32_t at) {  // bits 32 at .. 32 at + 31 of the row
+    const int32_t lo = pad - 32 * at, hi = a.n - 32 * at;
+    uint32_t x = at >= 0 && at < a.words ? __ldg(bits + at) : 0u;
+    if (hi < 32) x &= hi > 0 ? (1u << hi) - 1 : 0u;
+    if (lo > 0) x |= lo < 32 ? (1u << lo) - 1 : 0xffffffffu;
+    return x;
+  };
+  const int32_t at = d >> 5, sh = d & 31;
+  const uint32_t w0 = words(at), w1 = words(at + 1), w2 = words(at + 2);
+  return (uint64_t)__funnelshift_r(w0, w1, sh) | (uint64_t)__funnelshift_r(w1, w2, sh) << 32;
+}
+
+template <bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsDecodeArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -342,15 +394,22 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
   int32_t p0, p1, r0, r1;
   {
     int32_t* wsum = reinterpret_cast<int32_t*>(smem + kOffK);
-    const int per = (a.M + kThreads - 1) / kThreads;
+    const int32_t groups = groups_of<kTree>(a);
+    const int per = (groups + kThreads - 1) / kThreads;
     int32_t mine = 0;
     for (int i = 0; i < per; ++i) {
       const int m = tid * per + i;
-      if (m < a.M) {
-        const int32_t len = __ldg(a.lens + m);
-        const int32_t cl = clamp_len(a, len);
-        if (len > cl && cta == 0) ls_report(a.err, LS_DEVERR_CHECK);
-        mine += units_of(tiles_of(cl));
+      if (m < groups) {
+        if (cta == 0) {
+          const int32_t member = member_of<kTree>(a, m), len = __ldg(a.lens + member);
+          bool bad = len > clamp_len(a, len);
+          if (kTree && a.drafted && len >= 0) {
+            const int32_t c = __ldg(a.drafted + member);
+            bad = bad || c < 0 || c > a.n || c > len;
+          }
+          if (bad) ls_report(a.err, LS_DEVERR_CHECK);
+        }
+        mine += units_of(tiles_of(group_len<kTree>(a, m)));
       }
     }
     int32_t sum = mine;
@@ -377,7 +436,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     if (r0 < r1 && pre * a.hkv <= r0 && r0 < (pre + mine) * a.hkv) {
       for (int i = 0; i < per; ++i) {
         const int m = tid * per + i;
-        const int32_t nu = units_of(tiles_of(clamp_len(a, __ldg(a.lens + m))));
+        const int32_t nu = units_of(tiles_of(group_len<kTree>(a, m)));
         if (r0 < (pre + nu) * a.hkv) {
           start[0] = m;
           start[1] = r0 - pre * a.hkv;
@@ -419,7 +478,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     ls_report(a.err, LS_DEVERR_TIMEOUT);
     *abort_flag = 1;
   };
-  Walk walk(a, start, p0, p1, r0, r1);
+  Walk<kTree> walk(a, start, p0, p1, r0, r1);
   Seg s;
 
   if (warp == 0) {
@@ -432,7 +491,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
       Loader ld;
       bool ok = true;
       while (ok && walk.next(&s)) {
-        ld.open(a, s, &tm.kp, &tm.kr);
+        ld.open<kTree>(a, s, &tm.kp, &tm.kr);
         for (int32_t j = 0; j < s.count; ++j) {
           ok = wait_bar(bar_addr(sbase, B_K_EMPTY + ring.stage), ring.phase ^ 1) && !*abort_flag;
           if (!ok) {
@@ -463,9 +522,10 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     uint32_t fills = 0, aux_phase = 0, seg = 0;
     Loader ld;
     auto start_q = [&](uint32_t n_seg) {
-      const int rows = seg_rows(a, s, rt);
-      const uint32_t buf = sbase + q_offset(whole_q(a, s, rt), n_seg);
-      const int32_t row0 = s.resp ? s.m * a.n * a.g : rt * kTile;
+      const int rows = seg_rows<kTree>(a, s, rt);
+      const uint32_t buf = sbase + q_offset(whole_q<kTree>(a, s, rt), n_seg);
+      const int32_t row0 = s.resp ? (member_of<kTree>(a, s.m) * a.n + seg_token<kTree>(a, s)) * a.g
+                                  : rt * kTile;
       int32_t token = (row0 + (lane >> 4)) / a.g, head = (row0 + (lane >> 4)) - token * a.g;
       const int c = lane & 15;
       for (int r = lane >> 4; r < rows; r += 2) {
@@ -484,7 +544,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     bool ok = true, have = walk.next(&s);
     if (have) start_q(0);
     for (; ok && have; ++seg) {
-      if (lane == 0) ld.open(a, s, &tm.vp, &tm.vr);
+      if (lane == 0) ld.open<kTree>(a, s, &tm.vp, &tm.vr);
       uint32_t st = 0;
       for (int32_t j = 0; j < s.count; ++j) {
         st = ring.stage;
@@ -501,13 +561,13 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
       }
       if (!ok) break;
       const int32_t left = s.len - (s.key0 + (s.count - 1) * kTile);
-      const bool whole = whole_q(a, s, rt);
+      const bool whole = whole_q<kTree>(a, s, rt);
       have = walk.next(&s);
       if (have) {
         // the next segment's Q: its half of the Q tile was the segment before's, and a whole
         // tile also waits for this one's last S
         if (seg > 0) ok = wait_bar(bar_addr(sbase, B_Q_EMPTY + ((seg - 1) & 1)), ((seg - 1) >> 1) & 1);
-        if (ok && (whole || whole_q(a, s, rt)))
+        if (ok && (whole || whole_q<kTree>(a, s, rt)))
           ok = wait_bar(bar_addr(sbase, B_Q_EMPTY + (seg & 1)), (seg >> 1) & 1);
         if (!ok) break;
         start_q(seg + 1);
@@ -541,7 +601,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
       bool ok = true;
       for (; ok && walk.next(&s); ++seg) {
         ok = wait_bar(bar_addr(sbase, B_Q_FULL + (seg & 1)), (seg >> 1) & 1);
-        const uint32_t dq = sdesc_lo(sbase + q_offset(whole_q(a, s, rt), seg), 16);
+        const uint32_t dq = sdesc_lo(sbase + q_offset(whole_q<kTree>(a, s, rt), seg), 16);
         for (int32_t j = 0; ok && j < s.count; ++j, ++n) {
           ok = wait_bar(bar_addr(sbase, B_K_FULL + ring.stage), ring.phase);
           if (ok && n >= 2) ok = wait_bar(bar_addr(sbase, B_S_EMPTY + (n & 1)), ((n - 2) >> 1) & 1);
@@ -616,10 +676,20 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     };
     bool ok = true;
     while (ok && walk.next(&s)) {
-      const int32_t rows = seg_rows(a, s, rt);
+      const int32_t rows = seg_rows<kTree>(a, s, rt);
       const bool idle = quad * 32 >= rows;  // the whole warp is padding
       // keys of the half tile from its first one on that this row sees
-      int32_t lim = (s.resp ? min(s.len, s.len - a.n + 1 + row / a.g) : s.len) - s.key0 - t * kHalfKeys;
+      int32_t lim = (s.resp && !kTree ? min(s.len, s.len - a.n + 1 + row / a.g) : s.len) - s.key0 -
+                    t * kHalfKeys;
+      // of a tree's response: lim counts the member's context, which every row sees
+      int32_t pad = 0;
+      const uint32_t* bits = nullptr;
+      if (kTree && s.resp) {
+        const int32_t member = member_of<kTree>(a, s.m);
+        pad = a.n - drafted_of(a, member);
+        lim -= a.n - pad;
+        bits = a.visible + ((int64_t)member * a.n + min(seg_token<kTree>(a, s) + row / a.g, a.n - 1)) * a.words;
+      }
       float m = -INFINITY, l = 0.f, lcomp = 0.f;
       for (int32_t j = 0; j < s.count; ++j, ++n, lim -= kTile) {
         const uint32_t buf = n & 1, s_col = tmem + lane_off + buf * kTile + t * kHalfKeys;
@@ -644,7 +714,14 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
         reg_fence32(sr + 32);
         tc_fence_before();
         mbar_arrive(bar_addr(sbase, B_S_EMPTY + buf));
-        if (lim < kHalfKeys) {  // the source's ragged end, the causal end
+        if (kTree && s.resp) {
+          if (lim < kHalfKeys) {  // drafted keys among these
+            const uint64_t see = tree_window(a, bits, pad - lim, pad);
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              if (!((uint32_t)(see >> (e & 32)) & (1u << (e & 31)))) sr[e] = __float_as_uint(-INFINITY);
+          }
+        } else if (lim < kHalfKeys) {  // the source's ragged end, the causal end
 #pragma unroll
           for (int e = 0; e < 64; ++e)
             if (e >= lim) sr[e] = __float_as_uint(-INFINITY);
@@ -776,6 +853,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
 constexpr int kCombineThreads = 256;
 constexpr int kCombineWarps = kCombineThreads / 32;
 
+template <bool kTree>
 __global__ void __launch_bounds__(kCombineThreads)
 decode_combine(const __grid_constant__ LsDecodeArgs a) {
   __shared__ __align__(16) float acc[kCombineWarps][2][32][4];
@@ -787,20 +865,21 @@ decode_combine(const __grid_constant__ LsDecodeArgs a) {
   const int32_t octets = (a.g + 7) >> 3, group = (blockIdx.x >> 2) / octets;
   const int32_t head0 = 8 * ((blockIdx.x >> 2) - group * octets), col0 = 32 * (blockIdx.x & 3);
   const int32_t token = group / a.hkv, kvh = group - token * a.hkv, m = token / a.n;
-  const int32_t len = __ldg(a.lens + m);
-  if (len < 0) {
-    // A member out of use: its rows stay as they were.  Its blocks wait all the same: the
+  const int32_t len = __ldg(a.lens + m), at = token - m * a.n;  // token of the member
+  if (len < 0 || (kTree && at < a.n - drafted_of(a, m))) {
+    // A member out of use, or a token that is padding: its rows stay as they were.  Its blocks wait all the same: the
     // stream goes on when this grid ends, and with every member out of use nothing else
     // would hold it back until the main kernel has ended.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
   const int32_t nt = tiles_of(clamp_len(a, len));
+  const int32_t own = kTree ? m * a.rtm + at / a.tpt : m;  // the token's row group
   int32_t tot = 0, pre = 0;
-  for (int i = tid; i < a.M; i += kCombineThreads) {
-    const int32_t x = units_of(tiles_of(clamp_len(a, __ldg(a.lens + i))));
+  for (int i = tid; i < groups_of<kTree>(a); i += kCombineThreads) {
+    const int32_t x = units_of(tiles_of(group_len<kTree>(a, i)));
     tot += x;
-    if (i < m) pre += x;
+    if (i < own) pre += x;
   }
   tot = __reduce_add_sync(0xffffffffu, tot);
   pre = __reduce_add_sync(0xffffffffu, pre);
@@ -851,9 +930,10 @@ decode_combine(const __grid_constant__ LsDecodeArgs a) {
   const int32_t np = all[0], count = np + all[1];
   // a lane's head (behind the last one: that one again): row of all rows (token, head of the
   // group) against the prompt, row of the member's own
-  const int32_t grow = token * a.g + min(head0 + (lane & 7), a.g - 1), mrow = grow - m * a.n * a.g;
+  const int32_t grow = token * a.g + min(head0 + (lane & 7), a.g - 1);
+  const int32_t mrow = grow - (m * a.n + (kTree ? (own - m * a.rtm) * a.tpt : 0)) * a.g;
   const int64_t prompt0 = prompt_row0(a, kvh, 0, grow / kTile) + grow % kTile;
-  const int64_t resp0 = resp_row0(a, prompt_rows_of(a), m * a.hkv + kvh, 0) + mrow;
+  const int64_t resp0 = resp_row0(a, prompt_rows_of(a), own * a.hkv + kvh, 0) + mrow;
   const int32_t resp_rows = resp_rows_of(a);
   auto part_row = [&](int k) {
     if (k < np) return prompt0 + (int64_t)from[0][k] * a.rts * kTile;
@@ -931,13 +1011,17 @@ decode_combine(const __grid_constant__ LsDecodeArgs a) {
 }  // namespace
 
 int ls_decode_row_tile() { return kTile; }
+int ls_decode_tree_tokens() { return kTreeTokens; }
 int ls_decode_seg_tiles() { return kSegTiles; }
 int64_t ls_decode_prompt_rows(const LsDecodeArgs& a) { return prompt_rows_of(a); }
 int64_t ls_decode_resp_rows(const LsDecodeArgs& a) {
-  return ((int64_t)a.M * a.hkv + (int64_t)a.cols * a.rts) * resp_rows_of(a);
+  return ((int64_t)a.M * a.rtm * a.hkv + (int64_t)a.cols * a.rts) * resp_rows_of(a);
 }
 
-cudaError_t ls_launch_decode_attn(const LsDecodeArgs& a, cudaStream_t st) {
+namespace {
+
+template <bool kTree>
+cudaError_t launch(const LsDecodeArgs& a, cudaStream_t st) {
   TmapSet tm;
   for (int src = 0; src < 2; ++src) {
     // rows of 256 bytes; a whole-tile box takes both halves of its rows, half by half
@@ -952,10 +1036,10 @@ cudaError_t ls_launch_decode_attn(const LsDecodeArgs& a, cudaStream_t st) {
         !ls_make_tmap_bf16(src ? &tm.vr : &tm.vp, src ? a.rv_pool : a.v_pool, rank, dims, strides, box))
       return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(decode_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(decode_attn_kernel<kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kSmemBytes);
   if (e != cudaSuccess) return e;
-  decode_attn_kernel<<<a.cols * a.rts, kThreads, kSmemBytes, st>>>(tm, a);
+  decode_attn_kernel<kTree><<<a.cols * a.rts, kThreads, kSmemBytes, st>>>(tm, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   ls_note_launch();
   cudaLaunchAttribute attr;
@@ -967,7 +1051,13 @@ cudaError_t ls_launch_decode_attn(const LsDecodeArgs& a, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, decode_combine, a);
+  e = cudaLaunchKernelEx(&cfg, decode_combine<kTree>, a);
   if (e == cudaSuccess) ls_note_launch();
   return e;
+}
+
+}  // namespace
+
+cudaError_t ls_launch_decode_attn(const LsDecodeArgs& a, cudaStream_t st) {
+  return a.visible ? launch<true>(a, st) : launch<false>(a, st);
 }

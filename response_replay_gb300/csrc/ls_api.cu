@@ -991,9 +991,10 @@ struct DecodeWs {
   size_t part_o, part_lse, total;
 };
 
-// Geometry and workspace of a decode call (device pointers of q and the outputs aside).
-ls_status decode_args(const ls_kv_cache* c, const ls_resp_cache* r, int n, int Hq, LsDecodeArgs* a,
-                      DecodeWs* w) {
+// Geometry and workspace of a decode call (device pointers of q and the outputs aside).  With
+// a tree a member's rows may take several row tiles, of whole tokens each.
+ls_status decode_args(const ls_kv_cache* c, const ls_resp_cache* r, int n, int Hq, bool tree,
+                      LsDecodeArgs* a, DecodeWs* w) {
   ls_status s = check_cache(c);
   if (s != LS_OK) return s;
   if (!r) return LS_ERR_INVALID_ARG;
@@ -1007,16 +1008,21 @@ ls_status decode_args(const ls_kv_cache* c, const ls_resp_cache* r, int n, int H
   if (r->members > 0 && (!r->lens || !aligned4(r->lens) ||
                          (r->max_blocks > 0 && (!r->block_table || !aligned4(r->block_table)))))
     return LS_ERR_INVALID_ARG;
+  const int tile = ls_decode_row_tile();
+  const int g = Hq / c->num_kv_heads;
+  if (tree ? n > ls_decode_tree_tokens() || g > tile : (int64_t)n * g > tile) return LS_ERR_UNSUPPORTED;
+  const int tpt = tree && n > tile / g ? tile / g : n, rtm = (n + tpt - 1) / tpt;
   // tile, unit and key counts are 32-bit numbers
   if (c->num_tokens >= (1ll << 31) - 128 ||
       ((int64_t)r->max_blocks * r->pool.page_size / 128 + 1 + ls_decode_seg_tiles()) * r->members *
-              c->num_kv_heads >= (1ll << 31) ||
+              rtm * c->num_kv_heads >= (1ll << 31) ||
       (c->num_tokens / 128 + 1 + ls_decode_seg_tiles()) * c->num_kv_heads >= (1ll << 31))
     return LS_ERR_UNSUPPORTED;
   *a = LsDecodeArgs{};
-  a->g = Hq / c->num_kv_heads;
-  const int tile = ls_decode_row_tile();
-  if ((int64_t)n * a->g > tile) return LS_ERR_UNSUPPORTED;
+  a->g = g;
+  a->tpt = tpt;
+  a->rtm = rtm;
+  a->words = (n + 31) / 32;
   DevInfo d;
   if ((s = dev_info(&d)) != LS_OK) return s;
   a->k_pool = c->k_pool;
@@ -1038,8 +1044,9 @@ ls_status decode_args(const ls_kv_cache* c, const ls_resp_cache* r, int n, int H
   a->hkv = c->num_kv_heads;
   a->nt = (int32_t)((c->num_tokens + tile - 1) / tile);
   const int ctas = d.sms < 256 ? d.sms : 256;
-  a->rts = r->members > 0 ? (r->members * n * a->g + tile - 1) / tile : 1;
-  if (a->rts > ctas) return LS_ERR_UNSUPPORTED;
+  const int64_t rts = r->members > 0 ? ((int64_t)r->members * n * a->g + tile - 1) / tile : 1;
+  if (rts > ctas) return LS_ERR_UNSUPPORTED;
+  a->rts = (int32_t)rts;
   a->cols = ctas / a->rts;
   a->err = d.err;
   const size_t rows = (size_t)(ls_decode_prompt_rows(*a) + ls_decode_resp_rows(*a));
@@ -1217,20 +1224,26 @@ ls_status ls_decode_attn_workspace(const ls_kv_cache* cache, const ls_resp_cache
   if (!bytes) return LS_ERR_INVALID_ARG;
   LsDecodeArgs a;
   DecodeWs w;
-  const ls_status s = decode_args(cache, resp, n, Hq, &a, &w);
+  const ls_status s = decode_args(cache, resp, n, Hq, false, &a, &w);
   if (s == LS_OK) *bytes = w.total;
   return s;
 }
 
-ls_status ls_decode_attn(const ls_kv_cache* cache, const ls_resp_cache* resp, const void* q, int n,
-                         int Hq, float softmax_scale, void* o, float* lse, void* workspace,
-                         size_t workspace_bytes, ls_stream_t stream) {
+namespace {
+
+ls_status decode_attn(const ls_kv_cache* cache, const ls_resp_cache* resp, const void* q, int n,
+                      int Hq, bool tree, const int32_t* visible, const int32_t* drafted,
+                      float softmax_scale, void* o, float* lse, void* workspace,
+                      size_t workspace_bytes, ls_stream_t stream) {
   if (!isfinite(softmax_scale) || !(softmax_scale > 0.f)) return LS_ERR_INVALID_ARG;
   LsDecodeArgs a;
   DecodeWs w;
-  const ls_status s = decode_args(cache, resp, n, Hq, &a, &w);
+  const ls_status s = decode_args(cache, resp, n, Hq, tree, &a, &w);
   if (s != LS_OK) return s;
   if (a.M == 0) return LS_OK;
+  if (tree && (!visible || !aligned4(visible) || !aligned4(drafted))) return LS_ERR_INVALID_ARG;
+  a.visible = reinterpret_cast<const uint32_t*>(visible);
+  a.drafted = drafted;
   const void* ptrs[] = {q, o, lse};
   for (const void* p : ptrs)
     if (!p || !aligned16(p)) return LS_ERR_INVALID_ARG;
@@ -1242,6 +1255,321 @@ ls_status ls_decode_attn(const ls_kv_cache* cache, const ls_resp_cache* resp, co
   a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.part_o);
   a.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.part_lse);
   return from_cuda(ls_launch_decode_attn(a, (cudaStream_t)stream));
+}
+
+}  // namespace
+
+ls_status ls_decode_attn(const ls_kv_cache* cache, const ls_resp_cache* resp, const void* q, int n,
+                         int Hq, float softmax_scale, void* o, float* lse, void* workspace,
+                         size_t workspace_bytes, ls_stream_t stream) {
+  return decode_attn(cache, resp, q, n, Hq, false, nullptr, nullptr, softmax_scale, o, lse, workspace,
+                     workspace_bytes, stream);
+}
+
+ls_status ls_decode_attn_tree_workspace(const ls_kv_cache* cache, const ls_resp_cache* resp, int n,
+                                        int Hq, size_t* bytes) {
+  if (!bytes) return LS_ERR_INVALID_ARG;
+  LsDecodeArgs a;
+  DecodeWs w;
+  const ls_status s = decode_args(cache, resp, n, Hq, true, &a, &w);
+  if (s == LS_OK) *bytes = w.total;
+  return s;
+}
+
+ls_status ls_decode_attn_tree(const ls_kv_cache* cache, const ls_resp_cache* resp, const void* q,
+                              int n, int Hq, const int32_t* visible, const int32_t* drafted,
+                              float softmax_scale, void* o, float* lse, void* workspace,
+                              size_t workspace_bytes, ls_stream_t stream) {
+  return decode_attn(cache, resp, q, n, Hq, true, visible, drafted, softmax_scale, o, lse, workspace,
+                     workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- token statistics
+
+namespace {
+
+// Checks shared by the forward and the backward.
+ls_status token_logp_args(const void* logits, ls_dtype dtype, int64_t T, int V, int64_t ld, int top,
+                          float temperature) {
+  if (dtype != LS_BF16 && dtype != LS_FP32) return LS_ERR_INVALID_ARG;
+  if (T < 0 || V <= 0 || ld < V || top < 0 || top > V) return LS_ERR_INVALID_ARG;
+  if (!(temperature >= 1e-6f) || !(temperature <= 1e6f)) return LS_ERR_INVALID_ARG;
+  if (top > 32 || V > (1 << 30) || T >= (1ll << 31)) return LS_ERR_UNSUPPORTED;
+  const uintptr_t size = dtype == LS_BF16 ? 2 : 4;
+  if (T > 0 && (!logits || (reinterpret_cast<uintptr_t>(logits) & (size - 1)))) return LS_ERR_INVALID_ARG;
+  return LS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ls_status ls_token_logp_fwd_workspace(ls_dtype dtype, int64_t T, int V, int top, size_t* bytes) {
+  if (!bytes) return LS_ERR_INVALID_ARG;
+  ls_status s = token_logp_args(reinterpret_cast<const void*>(16), dtype, T, V, V, top, 1.f);
+  if (s != LS_OK) return s;
+  DevInfo d;
+  if ((s = dev_info(&d)) != LS_OK) return s;
+  *bytes = ls_token_logp_ws_bytes(T, ls_token_logp_parts(dtype == LS_BF16, T, V, top, d.sms));
+  return LS_OK;
+}
+
+ls_status ls_token_logp_fwd(const void* logits, ls_dtype dtype, int64_t T, int V, int64_t row_stride,
+                            const int32_t* targets, float temperature, int top, float* logp,
+                            float* lse, float* entropy, float* top_logp, int32_t* top_ids,
+                            void* workspace, size_t workspace_bytes, ls_stream_t stream) {
+  ls_status s = token_logp_args(logits, dtype, T, V, row_stride, top, temperature);
+  if (s != LS_OK) return s;
+  if (T == 0) return LS_OK;
+  const void* ptrs[] = {targets, logp, lse, entropy, top_logp, top_ids};
+  for (const void* p : ptrs)
+    if (!aligned4(p)) return LS_ERR_INVALID_ARG;
+  if ((logp && !targets) || (top > 0 && (!top_logp || !top_ids))) return LS_ERR_INVALID_ARG;
+  DevInfo d;
+  if ((s = dev_info(&d)) != LS_OK) return s;
+  const int parts = ls_token_logp_parts(dtype == LS_BF16, T, V, top, d.sms);
+  if (T * parts >= (1ll << 31)) return LS_ERR_UNSUPPORTED;
+  const size_t need = ls_token_logp_ws_bytes(T, parts);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return LS_ERR_WORKSPACE;
+  LsTokenLogpArgs a;
+  a.logits = logits;
+  a.is_bf16 = dtype == LS_BF16;
+  a.T = T;
+  a.ld = row_stride;
+  a.V = V;
+  a.targets = targets;
+  a.temperature = temperature;
+  a.top = top;
+  a.logp = logp;
+  a.lse = lse;
+  a.entropy = entropy;
+  a.top_logp = top_logp;
+  a.top_ids = top_ids;
+  a.workspace = workspace;
+  a.err = d.err;
+  return from_cuda(ls_launch_token_logp_fwd(a, parts, (cudaStream_t)stream));
+}
+
+ls_status ls_token_logp_bwd(const void* logits, ls_dtype dtype, int64_t T, int V, int64_t row_stride,
+                            const int32_t* targets, float temperature, const float* lse,
+                            const float* entropy, int top, const int32_t* top_ids,
+                            const float* d_logp, const float* d_entropy, const float* d_top,
+                            void* dlogits, int64_t d_row_stride, ls_stream_t stream) {
+  ls_status s = token_logp_args(logits, dtype, T, V, row_stride, top, temperature);
+  if (s != LS_OK) return s;
+  if (d_row_stride < V) return LS_ERR_INVALID_ARG;
+  if (T == 0) return LS_OK;
+  const uintptr_t size = dtype == LS_BF16 ? 2 : 4;
+  if (!dlogits || (reinterpret_cast<uintptr_t>(dlogits) & (size - 1))) return LS_ERR_INVALID_ARG;
+  const void* ptrs[] = {targets, lse, entropy, top_ids, d_logp, d_entropy, d_top};
+  for (const void* p : ptrs)
+    if (!aligned4(p)) return LS_ERR_INVALID_ARG;
+  if (!lse || (d_logp && !targets) || (d_entropy && !entropy) || (top > 0 && (!top_ids || !d_top)))
+    return LS_ERR_INVALID_ARG;
+  // in place the rows have to be the same ones
+  if (dlogits == logits && d_row_stride != row_stride && T > 1) return LS_ERR_INVALID_ARG;
+  DevInfo d;
+  if ((s = dev_info(&d)) != LS_OK) return s;
+  LsTokenLogpBwdArgs a;
+  a.logits = logits;
+  a.dlogits = dlogits;
+  a.is_bf16 = dtype == LS_BF16;
+  a.T = T;
+  a.ld = row_stride;
+  a.dld = d_row_stride;
+  a.V = V;
+  a.targets = targets;
+  a.temperature = temperature;
+  a.top = top;
+  a.top_ids = top_ids;
+  a.lse = lse;
+  a.entropy = entropy;
+  a.d_logp = d_logp;
+  a.d_entropy = d_entropy;
+  a.d_top = d_top;
+  a.err = d.err;
+  if (T * ls_token_logp_bwd_parts(a, d.sms) >= (1ll << 31)) return LS_ERR_UNSUPPORTED;
+  return from_cuda(ls_launch_token_logp_bwd(a, d.sms, (cudaStream_t)stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- drafts and branches
+
+namespace {
+
+ls_status draft_args(const int32_t* lens, const int32_t* drafted, int members, int n, LsDraftArgs* a) {
+  if (members < 0 || n < 1) return LS_ERR_INVALID_ARG;
+  if (members > 1024 || n > ls_decode_tree_tokens()) return LS_ERR_UNSUPPORTED;
+  if ((members > 0 && !lens) || !aligned4(lens) || !aligned4(drafted)) return LS_ERR_INVALID_ARG;
+  a->parents = nullptr;
+  a->lens = lens;
+  a->drafted = drafted;
+  a->members = members;
+  a->n = n;
+  a->err = nullptr;
+  return LS_OK;
+}
+
+ls_status layer_pools(const ls_page_pool* pool, int layers, int64_t stride, LsLayerPools* p) {
+  const ls_status s = check_pool(pool);
+  if (s != LS_OK) return s;
+  const int64_t size = (int64_t)pool->num_pages * pool->num_kv_heads * pool->page_size * kHeadDim;
+  if (layers < 1 || stride < 0 || (stride & 7) || (layers > 1 && stride < size)) return LS_ERR_INVALID_ARG;
+  if (layers > 65535) return LS_ERR_UNSUPPORTED;
+  p->k_pool = pool->k_pool;
+  p->v_pool = pool->v_pool;
+  p->stride = stride;
+  p->layers = layers;
+  p->num_pages = pool->num_pages;
+  p->ps_log2 = ilog2_exact(pool->page_size);
+  p->hkv = pool->num_kv_heads;
+  return LS_OK;
+}
+
+ls_status share_args(int32_t* table, int members, int max_blocks, int page_size, int num_pages,
+                     const int32_t* lens, int32_t* free_list, int num_free, const int32_t* used,
+                     int32_t* shared, int32_t* lens_out, int32_t* used_out, LsShareArgs* a) {
+  if (members < 0 || max_blocks < 0 || num_pages < 0 || num_free < 0) return LS_ERR_INVALID_ARG;
+  const int l = ilog2_exact(page_size);
+  if (l < 4 || l > 12 || members > 1024 || (int64_t)members * max_blocks > (1 << 30) ||
+      (int64_t)num_pages * page_size >= (1ll << 31) || (int64_t)max_blocks * page_size >= (1ll << 31))
+    return LS_ERR_UNSUPPORTED;
+  const void* ptrs[] = {used, used_out, lens, lens_out};
+  for (int i = 0; i < 4; ++i)
+    if ((!ptrs[i] && (i < 2 || members > 0)) || !aligned4(ptrs[i])) return LS_ERR_INVALID_ARG;
+  if ((members > 0 && max_blocks > 0 && (!table || !aligned4(table))) ||
+      (num_free > 0 && (!free_list || !aligned4(free_list))) || !aligned4(shared))
+    return LS_ERR_INVALID_ARG;
+  DevInfo d;
+  const ls_status s = dev_info(&d);
+  if (s != LS_OK) return s;
+  a->table = table;
+  a->lens = lens;
+  a->free_list = free_list;
+  a->used = used;
+  a->shared = shared;
+  a->lens_out = lens_out;
+  a->used_out = used_out;
+  a->members = members;
+  a->max_blocks = max_blocks;
+  a->num_free = num_free;
+  a->num_pages = num_pages;
+  a->ps_log2 = l;
+  a->err = d.err;
+  return LS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ls_status ls_draft_tree(const int32_t* parents, const int32_t* lens, const int32_t* drafted,
+                        int members, int n, int pos0, int axes, int32_t* visible,
+                        int32_t* positions, ls_stream_t stream) {
+  LsDraftArgs a;
+  ls_status s = draft_args(lens, drafted, members, n, &a);
+  if (s != LS_OK) return s;
+  if (pos0 < 0 || axes < 1) return LS_ERR_INVALID_ARG;
+  if (axes > 8) return LS_ERR_UNSUPPORTED;
+  if (members == 0) return LS_OK;
+  if (!parents || !aligned4(parents) || !visible || !aligned4(visible) || !aligned4(positions))
+    return LS_ERR_INVALID_ARG;
+  DevInfo d;
+  if ((s = dev_info(&d)) != LS_OK) return s;
+  a.parents = parents;
+  a.err = d.err;
+  return from_cuda(ls_launch_draft_tree(a, visible, positions, axes, pos0, (cudaStream_t)stream));
+}
+
+ls_status ls_accept_draft(const int32_t* parents, const int32_t* tokens, const int32_t* chosen,
+                          const int32_t* lens, const int32_t* drafted, int members, int n,
+                          int32_t* rows, int32_t* count, int32_t* follow, int32_t* ends,
+                          ls_stream_t stream) {
+  LsDraftArgs a;
+  ls_status s = draft_args(lens, drafted, members, n, &a);
+  if (s != LS_OK) return s;
+  if (members == 0) return LS_OK;
+  const void* ptrs[] = {parents, tokens, chosen, rows, count, follow, ends};
+  for (const void* p : ptrs)
+    if (!p || !aligned4(p)) return LS_ERR_INVALID_ARG;
+  DevInfo d;
+  if ((s = dev_info(&d)) != LS_OK) return s;
+  a.parents = parents;
+  a.err = d.err;
+  return from_cuda(ls_launch_accept_draft(a, tokens, chosen, rows, count, follow, ends,
+                                          (cudaStream_t)stream));
+}
+
+ls_status ls_compact_rows(const ls_page_pool* pool, int layers, int64_t layer_stride,
+                          const int32_t* block_table, int max_blocks, const int32_t* lens,
+                          const int32_t* drafted, int members, int n, const int32_t* rows,
+                          const int32_t* count, ls_stream_t stream) {
+  LsLayerPools p;
+  ls_status s = layer_pools(pool, layers, layer_stride, &p);
+  if (s != LS_OK) return s;
+  LsDraftArgs a;
+  if ((s = draft_args(lens, drafted, members, n, &a)) != LS_OK) return s;
+  if (max_blocks < 0) return LS_ERR_INVALID_ARG;
+  if ((int64_t)members * max_blocks >= (1ll << 31) || (int64_t)max_blocks * pool->page_size >= (1ll << 31) ||
+      (int64_t)members * layers * p.hkv >= (1ll << 31))
+    return LS_ERR_UNSUPPORTED;
+  if (members == 0) return LS_OK;
+  if ((max_blocks > 0 && !block_table) || !rows || !count || !aligned4(block_table) || !aligned4(rows) ||
+      !aligned4(count))
+    return LS_ERR_INVALID_ARG;
+  DevInfo d;
+  if ((s = dev_info(&d)) != LS_OK) return s;
+  a.err = d.err;
+  return from_cuda(ls_launch_compact_rows(p, block_table, max_blocks, a, rows, count, (cudaStream_t)stream));
+}
+
+ls_status ls_copy_pages(const ls_page_pool* pool, int layers, int64_t layer_stride, int count,
+                        const int32_t* from, const int32_t* to, const int32_t* rows,
+                        ls_stream_t stream) {
+  LsLayerPools p;
+  ls_status s = layer_pools(pool, layers, layer_stride, &p);
+  if (s != LS_OK) return s;
+  if (count < 0) return LS_ERR_INVALID_ARG;
+  if ((int64_t)count * layers * p.hkv * 2 >= (1ll << 31)) return LS_ERR_UNSUPPORTED;
+  if (count == 0) return LS_OK;
+  if (!from || !to || !aligned4(from) || !aligned4(to) || !aligned4(rows)) return LS_ERR_INVALID_ARG;
+  DevInfo d;
+  if ((s = dev_info(&d)) != LS_OK) return s;
+  return from_cuda(ls_launch_copy_pages(p, count, from, to, rows, d.err, (cudaStream_t)stream));
+}
+
+ls_status ls_trim_pages(const int32_t* block_table, int members, int max_blocks, int page_size,
+                        int num_pages, const int32_t* lens, const int32_t* new_lens,
+                        int32_t* free_list, int num_free, const int32_t* used, int32_t* shared,
+                        int32_t* lens_out, int32_t* used_out, ls_stream_t stream) {
+  if ((members > 0 && !new_lens) || !aligned4(new_lens)) return LS_ERR_INVALID_ARG;
+  LsShareArgs a;
+  const ls_status s = share_args(const_cast<int32_t*>(block_table), members, max_blocks, page_size,
+                                 num_pages, lens, free_list, num_free, used, shared, lens_out,
+                                 used_out, &a);
+  if (s != LS_OK) return s;
+  if (members == 0 && used_out == used) return LS_OK;
+  return from_cuda(ls_launch_trim_pages(a, new_lens, (cudaStream_t)stream));
+}
+
+ls_status ls_fork_pages(int32_t* block_table, int members, int max_blocks, int page_size,
+                        int num_pages, const int32_t* lens, const int32_t* src, const int32_t* keep,
+                        const int32_t* free_list, int num_free, const int32_t* used,
+                        int32_t* shared, int32_t* copies, int32_t* lens_out, int32_t* used_out,
+                        ls_stream_t stream) {
+  if ((members > 0 && (!src || !shared || !copies)) || !aligned4(src) || !aligned4(keep) ||
+      !aligned4(copies))
+    return LS_ERR_INVALID_ARG;
+  LsShareArgs a;
+  const ls_status s = share_args(block_table, members, max_blocks, page_size, num_pages, lens,
+                                 const_cast<int32_t*>(free_list), num_free, used, shared, lens_out,
+                                 used_out, &a);
+  if (s != LS_OK) return s;
+  if (members == 0 && used_out == used) return LS_OK;
+  return from_cuda(ls_launch_fork_pages(a, src, keep, copies, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -275,6 +275,10 @@ struct LsDecodeArgs {
   const int32_t* lens;       // [members]
   int32_t r_num_pages, r_ps_log2, max_blocks;
   int32_t M, n, hq, hkv, g;
+  const uint32_t* visible;   // trees: [M][n][words] rows that a row sees, NULL: the newest tokens in a line
+  const int32_t* drafted;    // trees: [M] drafted tokens, or NULL (n)
+  int32_t words;             // 32-bit words of a row of `visible`
+  int32_t tpt, rtm;          // tokens of a row group and row groups of a member (n and 1 without a tree)
   int32_t rts, cols;         // row tiles of 128 (token, head) rows; columns of rts CTAs each
   int32_t nt;                // prompt tiles of one KV head
   const void* q;             // bf16 [M][n][hq][128]
@@ -286,8 +290,93 @@ struct LsDecodeArgs {
   uint32_t* err;
 };
 int ls_decode_row_tile();
+int ls_decode_tree_tokens();  // most tokens of a member with a tree
 int ls_decode_seg_tiles();  // tiles' worth of time that a segment of a response takes besides
 // Rows of partial results: slots x rows.
 int64_t ls_decode_prompt_rows(const LsDecodeArgs& a);
 int64_t ls_decode_resp_rows(const LsDecodeArgs& a);
 cudaError_t ls_launch_decode_attn(const LsDecodeArgs& a, cudaStream_t st);
+
+// Log probabilities of given tokens, entropies, top alternatives (token_logp.cu).
+struct LsTokenLogpArgs {
+  const void* logits;        // [T] rows of V values, ld apart
+  int32_t is_bf16;
+  int64_t T, ld;
+  int32_t V;
+  const int32_t* targets;    // [T] or NULL; -1: a padding row
+  float temperature;
+  int32_t top;               // alternatives, 0 to 32
+  float* logp;               // [T] each, or NULL
+  float* lse;
+  float* entropy;
+  float* top_logp;           // [T][top]
+  int32_t* top_ids;
+  void* workspace;           // parts' results, 16-byte aligned
+  uint32_t* err;
+};
+struct LsTokenLogpBwdArgs {
+  const void* logits;
+  void* dlogits;
+  int32_t is_bf16;
+  int64_t T, ld, dld;
+  int32_t V;
+  const int32_t* targets;
+  float temperature;
+  int32_t top;
+  const int32_t* top_ids;
+  const float* lse;
+  const float* entropy;
+  const float* d_logp;
+  const float* d_entropy;
+  const float* d_top;
+  uint32_t* err;
+};
+int ls_token_logp_parts(bool is_bf16, int64_t T, int V, int top, int sms);
+size_t ls_token_logp_ws_bytes(int64_t T, int parts);
+cudaError_t ls_launch_token_logp_fwd(const LsTokenLogpArgs& a, int parts, cudaStream_t st);
+int64_t ls_token_logp_bwd_parts(const LsTokenLogpBwdArgs& a, int sms);
+cudaError_t ls_launch_token_logp_bwd(const LsTokenLogpBwdArgs& a, int sms, cudaStream_t st);
+
+// Drafted trees (drafts.cu).  Row r of member m is one of its n rows; its `drafted` nodes are
+// the last of them, parents earlier rows of its own or -1.
+struct LsDraftArgs {
+  const int32_t* parents;    // [members][n]
+  const int32_t* lens;       // [members], drafted tokens included
+  const int32_t* drafted;    // [members] or NULL (n)
+  int32_t members, n;
+  uint32_t* err;
+};
+cudaError_t ls_launch_draft_tree(const LsDraftArgs& a, int32_t* visible, int32_t* positions,
+                                 int32_t axes, int32_t pos0, cudaStream_t st);
+cudaError_t ls_launch_accept_draft(const LsDraftArgs& a, const int32_t* tokens,
+                                   const int32_t* chosen, int32_t* rows, int32_t* count,
+                                   int32_t* follow, int32_t* ends, cudaStream_t st);
+// Pages of one or several layers, layer l's pools l * stride values behind the first's.
+struct LsLayerPools {
+  void* k_pool;
+  void* v_pool;
+  int64_t stride;
+  int32_t layers, num_pages, ps_log2, hkv;
+};
+cudaError_t ls_launch_compact_rows(const LsLayerPools& p, const int32_t* table, int32_t max_blocks,
+                                   const LsDraftArgs& a, const int32_t* rows, const int32_t* count,
+                                   cudaStream_t st);
+cudaError_t ls_launch_copy_pages(const LsLayerPools& p, int32_t count, const int32_t* from,
+                                 const int32_t* to, const int32_t* rows, uint32_t* err,
+                                 cudaStream_t st);
+
+// Pages given back and shared (pages.cu).
+struct LsShareArgs {
+  int32_t* table;            // [members][max_blocks]
+  const int32_t* lens;
+  int32_t* free_list;
+  const int32_t* used;
+  int32_t* shared;           // [num_pages] owners besides the first, or NULL
+  int32_t* lens_out;
+  int32_t* used_out;
+  int32_t members, max_blocks, num_free, num_pages, ps_log2;
+  uint32_t* err;
+};
+cudaError_t ls_launch_trim_pages(const LsShareArgs& a, const int32_t* new_lens, cudaStream_t st);
+cudaError_t ls_launch_fork_pages(const LsShareArgs& a, const int32_t* src, const int32_t* keep,
+                                 int32_t* copies, cudaStream_t st);

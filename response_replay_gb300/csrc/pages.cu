@@ -15,9 +15,11 @@
 // a small call, by block 0 when they go to buffers of their own, and by a second launch
 // when a large call writes them over what it reads.
 //
-// It is bound by a launch and one dependent chain (lengths, two scans, a search, a page, a
+// extend_pages is bound by a launch and one dependent chain (lengths, two scans, a search, a page, a
 // slot): one token for each of 8 members 4.0 us, 282,000 tokens for 64 members 5.2 us, of
 // which the 2.2 MB of slots and positions are 0.3 us at the copy's rate.
+//
+// Below: pages given back at the end of sequences, and shared by branches of a sequence.
 #include "ls_device.cuh"
 #include "ls_internal.h"
 
@@ -203,7 +205,263 @@ __global__ void __launch_bounds__(kThreads) extend_pages_kernel(const LsExtendAr
   }
 }
 
+// ---------------------------------------------------------------- pages given back
+//
+// Member m keeps its first new_len tokens; the pages behind them lose it as an owner.  A page
+// that no owner is left of goes back to the free list, which is a stack: the freed pages, in
+// member and block order, become its entries [used - freed, used).
+//
+// shared[page] counts a page's owners besides the first, so a page that extend_pages has just
+// taken is at its right count, 0.  A call may drop several owners of a page at once; which of
+// its entries stands for the page in the free list must not depend on who came first.  So the
+// drops are counted into shared (integer atomics: the sum is the same in any order), a page
+// that lost all its owners ends at -1, and among its entries the first one is found by a
+// maximum over INT_MIN + (entries - place), kept in shared as well until the end.
+//
+// One block: the counts of all entries have to meet before the first is written.  A decode
+// step's drafts free about a page a member; 8,192 entries take eight rounds of each phase.
+
+struct Drops {
+  int end[kThreads];   // entries up to and including the member
+  int need[kThreads];  // its first dropped block
+};
+
+__global__ void __launch_bounds__(kThreads) trim_pages_kernel(const LsShareArgs a,
+                                                              const int32_t* __restrict__ new_lens) {
+  __shared__ Drops d;
+  __shared__ long long wt[32];
+  __shared__ int wp[32];
+  __shared__ int batch[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ps = 1 << a.ps_log2, used0 = *a.used;
+  int len = -1, keep = -1, have = 0, need = 0;
+  bool good = true;
+  if (tid < a.members) {
+    len = a.lens[tid];
+    keep = new_lens[tid];
+    good = len < 0 ? keep < 0 : keep <= len && len <= ((long long)a.max_blocks << a.ps_log2);
+    if (good) {
+      have = len > 0 ? (int)(((long long)len + ps - 1) >> a.ps_log2) : 0;
+      need = keep > 0 ? (int)(((long long)keep + ps - 1) >> a.ps_log2) : 0;
+    }
+  }
+  long long tok = 0;
+  int drops = have - need;
+  block_scan(&tok, &drops, wt, wp);
+  d.end[tid] = drops;
+  d.need[tid] = need;
+  good = __syncthreads_and(good) && used0 >= 0 && used0 <= a.num_free;
+  const int total = d.end[kThreads - 1];
+  auto page_at = [&](int j) {  // the page of entry j
+    int lo = 0, hi = a.members - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (d.end[mid] > j) hi = mid; else lo = mid + 1;
+    }
+    return a.table[(int64_t)lo * a.max_blocks + d.need[lo] + j - (lo ? d.end[lo - 1] : 0)];
+  };
+  auto in_pool = [&](int page) { return (uint32_t)page < (uint32_t)a.num_pages; };
+  int freed = total;
+  if (good) {
+    bool fine = true;
+    for (int j = tid; j < total; j += kThreads) {
+      const int page = page_at(j);
+      if (!in_pool(page)) fine = false;
+      else if (a.shared) atomicSub(a.shared + page, 1);
+    }
+    good = __syncthreads_and(fine);
+    bool undo = !good;
+    if (a.shared && good) {
+      fine = true;
+      int n = 0;
+      for (int j = tid; j < total; j += kThreads)
+        if (__ldcg(a.shared + page_at(j)) < -1) fine = false;  // more owners dropped than it had
+      // a member cut inside a page that others still read would write there next
+      if (keep > 0 && keep < len && (keep & (ps - 1))) {
+        const int page = a.table[(int64_t)tid * a.max_blocks + (keep >> a.ps_log2)];
+        if (in_pool(page) && __ldcg(a.shared + page) > 0) fine = false;
+      }
+      good = __syncthreads_and(fine);
+      undo = !good;
+      if (good) {
+        for (int j = tid; j < total; j += kThreads) {
+          int32_t* c = a.shared + page_at(j);
+          if (__ldcg(c) < 0) __stcg(c, INT32_MIN);  // every entry of the page writes the same
+        }
+        __syncthreads();
+        for (int j = tid; j < total; j += kThreads) {
+          int32_t* c = a.shared + page_at(j);
+          if (__ldcg(c) < 0) atomicMax(c, INT32_MIN + (total - j));
+        }
+        __syncthreads();
+        for (int j = tid; j < total; j += kThreads)
+          n += __ldcg(a.shared + page_at(j)) == INT32_MIN + (total - j);
+        int sum = n;
+        tok = 0;
+        __syncthreads();
+        block_scan(&tok, &sum, wt, wp);
+        freed = wp[31];
+        if (freed > used0) {  // pages that were never taken: the counts before the drops again
+          good = false;
+          undo = true;
+          for (int j = tid; j < total; j += kThreads) {
+            int32_t* c = a.shared + page_at(j);
+            if (__ldcg(c) < 0) __stcg(c, -1);
+          }
+          __syncthreads();
+        }
+      }
+    } else if (good && freed > used0) {
+      good = false;
+    }
+    if (undo && a.shared)
+      for (int j = tid; j < total; j += kThreads) {
+        const int page = page_at(j);
+        if (in_pool(page)) atomicAdd(a.shared + page, 1);
+      }
+  }
+  if (good) {
+    int before = used0 - freed;
+    for (int j0 = 0; j0 < total; j0 += kThreads) {
+      const int j = j0 + tid, page = j < total ? page_at(j) : -1;
+      const bool mine = j < total && (!a.shared || __ldcg(a.shared + page) == INT32_MIN + (total - j));
+      const uint32_t mask = __ballot_sync(0xffffffffu, mine);
+      if (lane == 0) batch[warp] = __popc(mask);
+      __syncthreads();
+      int at = before;
+#pragma unroll
+      for (int w = 0; w < 32; ++w) {
+        if (w < warp) at += batch[w];
+        before += batch[w];
+      }
+      if (mine) a.free_list[at + __popc(mask & ((1u << lane) - 1))] = page;
+      __syncthreads();
+    }
+    if (a.shared) {
+      for (int j = tid; j < total; j += kThreads) {
+        int32_t* c = a.shared + page_at(j);
+        if (__ldcg(c) < 0) __stcg(c, 0);
+      }
+    }
+  }
+  if (tid < a.members) a.lens_out[tid] = !good || len < 0 ? len : max(keep, -1);
+  if (tid == 0) {
+    *a.used_out = good ? used0 - freed : used0;
+    if (!good) ls_report(a.err, LS_DEVERR_CHECK);
+  }
+}
+
+// ---------------------------------------------------------------- pages shared
+//
+// Member m, out of use or empty, becomes a branch of member src[m]'s first keep[m] tokens: the
+// whole pages are shared, the rows of a partial last one are to be copied to a page of its own
+// (from the free list, in member order), which `copies` says to copy_pages.  One block, as for
+// trim_pages; the entries of a branch's table are written and counted by all of its threads.
+__global__ void __launch_bounds__(kThreads) fork_pages_kernel(const LsShareArgs a,
+                                                              const int32_t* __restrict__ src,
+                                                              const int32_t* __restrict__ keep,
+                                                              int32_t* copies) {
+  __shared__ int end[kThreads], from_member[kThreads];
+  __shared__ long long wt[32];
+  __shared__ int wp[32];
+  const int tid = threadIdx.x;
+  const int used0 = *a.used;
+  int len = -1, of = -1, n = 0, whole = 0, part = 0, source = -1;
+  bool good = true;
+  if (tid < a.members) {
+    len = a.lens[tid];
+    of = src[tid];
+    if (of >= 0) {
+      good = of < a.members && of != tid && len <= 0;
+      if (good) {
+        const int olen = a.lens[of];
+        n = keep ? keep[tid] : olen;
+        good = olen >= 0 && src[of] < 0 && n >= 0 && n <= olen &&
+               olen <= ((long long)a.max_blocks << a.ps_log2);
+      }
+      if (good) {
+        whole = n >> a.ps_log2;
+        part = n & ((1 << a.ps_log2) - 1);
+        if (part) {
+          source = a.table[(int64_t)of * a.max_blocks + whole];
+          good = (uint32_t)source < (uint32_t)a.num_pages;
+        }
+      } else {
+        n = 0;
+      }
+    }
+  }
+  const bool fresh = good && part > 0;
+  long long entries = good ? whole : 0;
+  int taken = fresh;
+  block_scan(&entries, &taken, wt, wp);
+  end[tid] = (int)entries;
+  from_member[tid] = of;
+  good = __syncthreads_and(good) && used0 >= 0 && wp[31] <= a.num_free - used0;
+  const int total = end[kThreads - 1], pages = wp[31];
+  auto entry = [&](int j, int* member) {  // block of the branch that entry j is
+    int lo = 0, hi = a.members - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (end[mid] > j) hi = mid; else lo = mid + 1;
+    }
+    *member = lo;
+    return j - (lo ? end[lo - 1] : 0);
+  };
+  int page = -1;
+  bool fine = true;
+  if (good) {
+    if (fresh) {
+      page = a.free_list[used0 + taken - 1];
+      fine = (uint32_t)page < (uint32_t)a.num_pages;
+    }
+    for (int j = tid; j < total; j += kThreads) {
+      int m;
+      const int b = entry(j, &m);
+      const int32_t x = a.table[(int64_t)from_member[m] * a.max_blocks + b];
+      if ((uint32_t)x >= (uint32_t)a.num_pages) fine = false;
+    }
+  }
+  good = __syncthreads_and(fine) && good;
+  if (good) {
+    for (int j = tid; j < total; j += kThreads) {
+      int m;
+      const int b = entry(j, &m);
+      const int32_t x = a.table[(int64_t)from_member[m] * a.max_blocks + b];
+      a.table[(int64_t)m * a.max_blocks + b] = x;
+      atomicAdd(a.shared + x, 1);
+    }
+    if (fresh) a.table[(int64_t)tid * a.max_blocks + whole] = page;
+  }
+  if (tid < a.members) {
+    const bool copy = good && fresh;
+    copies[tid] = copy ? source : -1;
+    copies[a.members + tid] = copy ? page : -1;
+    copies[2 * a.members + tid] = copy ? part : 0;
+    a.lens_out[tid] = good && of >= 0 ? n : len;
+  }
+  if (tid == 0) {
+    *a.used_out = good ? used0 + pages : used0;
+    if (!good) ls_report(a.err, LS_DEVERR_CHECK);
+  }
+}
+
 }  // namespace
+
+cudaError_t ls_launch_trim_pages(const LsShareArgs& a, const int32_t* new_lens, cudaStream_t st) {
+  trim_pages_kernel<<<1, kThreads, 0, st>>>(a, new_lens);
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) ls_note_launch();
+  return e;
+}
+
+cudaError_t ls_launch_fork_pages(const LsShareArgs& a, const int32_t* src, const int32_t* keep,
+                                 int32_t* copies, cudaStream_t st) {
+  fork_pages_kernel<<<1, kThreads, 0, st>>>(a, src, keep, copies);
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) ls_note_launch();
+  return e;
+}
 
 cudaError_t ls_launch_extend_pages(const LsExtendArgs& a, int sms, cudaStream_t st) {
   int64_t blocks = (a.capacity + kChunk - 1) / kChunk;

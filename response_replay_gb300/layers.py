@@ -81,28 +81,36 @@ class LayeredResponses:
     adds nothing moves the later ones up, or, with member_rows, every member has that many rows
     and its new tokens are the last of them.  A loop whose members end at different times
     takes member_rows and sets an ended member's add to 0: its rows of ``attend`` hold nothing
-    of use then, and the others' stay where they are."""
+    of use then, and the others' stay where they are.
+
+    A step over drafted trees (member_rows) is ``draft`` in the place of ``extend``, ``append``
+    and ``attend`` with what ``draft`` returned, and, when the policy has chosen behind every row,
+    ``settle``.  ``trim`` cuts responses or ends them and gives their pages back; with sharing,
+    ``fork`` branches them."""
 
     def __init__(self, prompt, num_kv_heads: int, members: int, max_tokens: int,
                  num_pages: int, page_size: int, device, capacity: int | None = None,
-                 axes: int = 1, member_rows: int | None = None):
+                 axes: int = 1, member_rows: int | None = None, sharing: bool = False):
         """prompt: the captured prompt's layers (LayeredKVCache, or anything whose [l] is a
         PagedKVCache); max_tokens: longest response; capacity: most new tokens of a step
         (default: one a member); axes: rows of positions, one an axis of the rotary;
         member_rows: rows of every member in a step (capacity is then members *
-        member_rows)."""
+        member_rows); sharing: members may be branches of one another (``fork``)."""
         if member_rows is not None:
             if member_rows < 1 or capacity not in (None, members * member_rows):
                 raise ValueError("member_rows is at least 1, and capacity members * member_rows")
             capacity = members * member_rows
         self.member_rows = member_rows
+        self._whole = None  # drafts of every row
         self.prompt = prompt
         blocks = (max_tokens + page_size - 1) // page_size
-        self.alloc = api.PageAllocator.empty(members, blocks, num_pages, page_size, device)
+        self.alloc = api.PageAllocator.empty(members, blocks, num_pages, page_size, device,
+                                             sharing=sharing)
         shape = (len(prompt), num_pages, num_kv_heads, page_size, api.HEAD_DIM)
         self.k_pools = torch.empty(shape, dtype=torch.bfloat16, device=device)
         self.v_pools = torch.empty(shape, dtype=torch.bfloat16, device=device)
         self.pools = [api.PagePool(k, v) for k, v in zip(self.k_pools, self.v_pools)]
+        self.all_pools = api.LayerPools(self.k_pools, self.v_pools)
         self.layers = [api.ResponseCache.of(pool, self.alloc) for pool in self.pools]
         n = members if capacity is None else capacity
         self.slots = torch.empty(n, dtype=torch.int32, device=device)
@@ -124,10 +132,65 @@ class LayeredResponses:
                                        rotary, wq, wk, stream=stream, **kw)
 
     def attend(self, layer: int, q: torch.Tensor, softmax_scale: float, o=None, lse=None,
-               stream=None):
-        """q [members][n][Hq][128]: the n newest tokens of every member; returns (o, lse)."""
+               stream=None, visible=None, drafted=None):
+        """q [members][n][Hq][128]: the n newest tokens of every member, in a line or, with
+        visible (``draft``'s) and drafted, as trees; returns (o, lse)."""
+        if visible is not None:
+            return api.decode_attn_tree(self.prompt[layer], self.layers[layer], q, visible,
+                                        softmax_scale, drafted, o, lse, stream)
+        if drafted is not None:
+            raise ValueError("drafted without visible")
         return api.decode_attn(self.prompt[layer], self.layers[layer], q, softmax_scale, o, lse,
                                stream)
+
+
+    def draft(self, parents: torch.Tensor, drafted: torch.Tensor | None = None, stream=None):
+        """Room for every member's drafted tree (parents int32 [members][member_rows], drafted
+        int32 [members], see ls_draft_tree), its slots, and the positions that its depths give;
+        returns the rows that each row sees."""
+        if self.member_rows is None:
+            raise ValueError("drafts need member_rows")
+        if stream is not None:
+            with api._as_current(stream):
+                return self.draft(parents, drafted)
+        M, n = self.alloc.members, self.member_rows
+        if tuple(parents.shape) != (M, n):
+            raise ValueError(f"parents must be [{M} members][{n} member_rows]")
+        if drafted is None:
+            if self._whole is None:
+                self._whole = torch.full((M,), n, dtype=torch.int32, device=parents.device)
+            self.extend(self._whole)
+        else:
+            self.extend(drafted)
+        axes = self.positions.shape[0]
+        return api.draft_tree(parents, self.alloc.lens, self.prompt[0].num_tokens, drafted,
+                              positions=self.positions.view(axes, M, n))[0]
+
+    def settle(self, parents: torch.Tensor, tokens: torch.Tensor, chosen: torch.Tensor,
+               drafted: torch.Tensor | None = None, stream=None):
+        """What the policy keeps of a draft: tokens int32 [members][member_rows] drafted, chosen
+        the policy's token behind each row.  The kept rows' keys and values follow the context
+        in every layer, the others' room is given back.  Returns (rows, count, follow) as
+        accept_draft."""
+        if stream is not None:
+            with api._as_current(stream):
+                return self.settle(parents, tokens, chosen, drafted)
+        rows, count, follow, ends = api.accept_draft(parents, tokens, chosen, self.alloc.lens, drafted)
+        api.compact_rows(self.alloc, self.all_pools, rows, count, drafted)
+        api.trim_pages(self.alloc, ends)
+        return rows, count, follow
+
+    def trim(self, new_lens: torch.Tensor, stream=None) -> None:
+        """Member m keeps its first new_lens[m] tokens (negative: out of use)."""
+        api.trim_pages(self.alloc, new_lens, stream=stream)
+
+    def fork(self, src: torch.Tensor, keep: torch.Tensor | None = None, stream=None) -> None:
+        """Member m with src[m] >= 0 becomes a branch of that member's first keep[m] tokens, in
+        every layer."""
+        if stream is not None:
+            with api._as_current(stream):
+                return self.fork(src, keep)
+        api.copy_pages(self.all_pools, api.fork_pages(self.alloc, src, keep))
 
 
 class KVGradPages:

@@ -776,11 +776,13 @@ def qk_norm_rope_append(pool: PagePool, q: torch.Tensor, k: torch.Tensor, v: tor
 class PageAllocator:
     """Pages of a group's growing responses (ls_extend_pages): block_table int32
     [members][max_blocks], lens int32 [members] (negative: out of use), free_list int32
-    [num_free] and used int32 [1], all on the GPU.  One allocator serves every layer's
-    pools: the token -> page map is the same in each."""
+    [num_free] and used int32 [1], all on the GPU; for branching responses also shared int32
+    [num_pages], the owners of each page besides the first (zeros at the start).  One
+    allocator serves every layer's pools: the token -> page map is the same in each."""
 
     def __init__(self, block_table: torch.Tensor, lens: torch.Tensor, free_list: torch.Tensor,
-                 used: torch.Tensor, page_size: int, num_pages: int | None = None):
+                 used: torch.Tensor, page_size: int, num_pages: int | None = None,
+                 shared: torch.Tensor | None = None):
         _check(block_table, "block_table", torch.int32)
         if block_table.dim() != 2:
             raise ValueError("block_table must be [members][max_blocks]")
@@ -795,15 +797,22 @@ class PageAllocator:
         self.members, self.max_blocks = block_table.shape
         self.num_free = free_list.numel()
         self.num_pages = self.num_free if num_pages is None else num_pages
+        if shared is not None:
+            _check(shared, "shared", torch.int32, (self.num_pages,))
+            if shared.device != block_table.device:
+                raise ValueError("the allocator's tensors must be on one device")
+        self.shared = shared
         self.device_index = block_table.get_device()
 
     @classmethod
     def empty(cls, members: int, max_blocks: int, num_pages: int, page_size: int,
-              device) -> "PageAllocator":
-        """No tokens yet, every page of the pool free."""
+              device, sharing: bool = False) -> "PageAllocator":
+        """No tokens yet, every page of the pool free; sharing: pages may have several owners
+        (fork_pages)."""
         z = dict(dtype=torch.int32, device=device)
         return cls(torch.zeros((members, max_blocks), **z), torch.zeros(members, **z),
-                   torch.arange(num_pages, **z), torch.zeros(1, **z), page_size)
+                   torch.arange(num_pages, **z), torch.zeros(1, **z), page_size,
+                   shared=torch.zeros(num_pages, **z) if sharing else None)
 
 
 def extend_pages(alloc: PageAllocator, add: torch.Tensor, pos0: int, slots: torch.Tensor,
@@ -870,14 +879,9 @@ class ResponseCache:
         return cls(pool, alloc.block_table, alloc.lens)
 
 
-def decode_attn(cache: PagedKVCache, resp: ResponseCache, q: torch.Tensor, softmax_scale: float,
-                o: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None):
-    """Attention of a decode step: q [members][n][Hq][128], the n newest tokens of every
-    member (already appended to its pages), over the shared prompt and the member's own
-    response.  Returns (o, lse)."""
-    if stream is not None:
-        with _as_current(stream):
-            return decode_attn(cache, resp, q, softmax_scale, o, lse)
+def _decode_args(cache: PagedKVCache, resp: ResponseCache, q: torch.Tensor, o, lse):
+    """Checks shared by the decode calls; returns (members, n, Hq, device, stream, q's address, o,
+    lse, their addresses)."""
     if q.dim() != 4:
         raise ValueError("q must be [members][n][Hq][128]")
     _, n, hq, _ = shape = q.shape
@@ -893,7 +897,299 @@ def decode_attn(cache: PagedKVCache, resp: ResponseCache, q: torch.Tensor, softm
         lse = torch.empty((M, n, hq), dtype=torch.float32, device=q.device)
     op = _dense(o, "o", torch.bfloat16, shape, dev)
     lp = _dense(lse, "lse", torch.float32, (M, n, hq), dev)
+    return M, n, hq, dev, st, qp, o, lse, op, lp
+
+
+def decode_attn(cache: PagedKVCache, resp: ResponseCache, q: torch.Tensor, softmax_scale: float,
+                o: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None):
+    """Attention of a decode step: q [members][n][Hq][128], the n newest tokens of every
+    member (already appended to its pages), over the shared prompt and the member's own
+    response.  Returns (o, lse)."""
+    if stream is not None:
+        with _as_current(stream):
+            return decode_attn(cache, resp, q, softmax_scale, o, lse)
+    M, n, hq, dev, st, qp, o, lse, op, lp = _decode_args(cache, resp, q, o, lse)
     _with_workspace(B.ls_decode_attn, (cache.struct, resp.struct, qp, n, hq, softmax_scale, op, lp),
                     lambda: B.ls_decode_attn_workspace(cache.struct, resp.struct, n, hq), q,
                     "decode", st)
     return o, lse
+
+
+# ---------------------------------------------------------------- drafted trees
+
+def _draft_args(parents, lens, drafted):
+    """(members, n, device, parents' address, lens', drafted's) of a step's draft."""
+    if parents.dim() != 2:
+        raise ValueError("parents must be [members][n]")
+    M, n = parents.shape
+    dev = parents.get_device()
+    return (M, n, dev, _dense(parents, "parents", torch.int32, (M, n), dev),
+            _dense(lens, "lens", torch.int32, (M,), dev),
+            None if drafted is None else _dense(drafted, "drafted", torch.int32, (M,), dev))
+
+
+def draft_tree(parents: torch.Tensor, lens: torch.Tensor, pos0: int,
+               drafted: torch.Tensor | None = None, axes: int = 1,
+               visible: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+               stream=None):
+    """The plan of a step over drafted trees (ls_draft_tree): parents int32 [members][n] (the row
+    that a row's node continues, -1: the context), lens int32 [members] with the drafts in them,
+    drafted int32 [members] (default: n of each; the last rows).  Returns (visible int32
+    [members][n][ceil(n / 32)], the rows that a row sees, and positions int32
+    [axes][members][n], pos0 + context + depth)."""
+    if stream is not None:
+        with _as_current(stream):
+            return draft_tree(parents, lens, pos0, drafted, axes, visible, positions)
+    M, n, dev, pp, lp, dp = _draft_args(parents, lens, drafted)
+    st = _dev_stream(dev)
+    if not 0 <= pos0 < 2 ** 31:
+        raise ValueError(f"pos0 must be a position, got {pos0}")
+    if visible is None:
+        visible = torch.empty((M, n, (n + 31) // 32), dtype=torch.int32, device=parents.device)
+    if positions is None:
+        positions = torch.empty((axes, M, n), dtype=torch.int32, device=parents.device)
+    elif positions.dim() == 3:
+        axes = positions.shape[0]
+    B.ls_draft_tree(pp, lp, dp, M, n, pos0, axes,
+                    _dense(visible, "visible", torch.int32, (M, n, (n + 31) // 32), dev),
+                    _dense(positions, "positions", torch.int32, (axes, M, n), dev), st)
+    return visible, positions
+
+
+def decode_attn_tree(cache: PagedKVCache, resp: ResponseCache, q: torch.Tensor,
+                     visible: torch.Tensor, softmax_scale: float,
+                     drafted: torch.Tensor | None = None, o: torch.Tensor | None = None,
+                     lse: torch.Tensor | None = None, stream=None):
+    """decode_attn of drafted trees: q [members][n][Hq][128], row r of member m over the prompt,
+    the member's context and the drafted rows of visible[m][r] (draft_tree's).  Rows before the
+    last drafted[m] are padding and stay as they are in o and lse.  Returns (o, lse)."""
+    if stream is not None:
+        with _as_current(stream):
+            return decode_attn_tree(cache, resp, q, visible, softmax_scale, drafted, o, lse)
+    M, n, hq, dev, st, qp, o, lse, op, lp = _decode_args(cache, resp, q, o, lse)
+    vp = _dense(visible, "visible", torch.int32, (M, n, (n + 31) // 32), dev)
+    dp = None if drafted is None else _dense(drafted, "drafted", torch.int32, (M,), dev)
+    _with_workspace(B.ls_decode_attn_tree,
+                    (cache.struct, resp.struct, qp, n, hq, vp, dp, softmax_scale, op, lp),
+                    lambda: B.ls_decode_attn_tree_workspace(cache.struct, resp.struct, n, hq), q,
+                    "decode", st)
+    return o, lse
+
+
+def accept_draft(parents: torch.Tensor, tokens: torch.Tensor, chosen: torch.Tensor,
+                 lens: torch.Tensor, drafted: torch.Tensor | None = None, stream=None):
+    """The path of each member's draft that the policy chooses itself (ls_accept_draft): tokens
+    int32 [members][n] drafted, chosen int32 [members][n] the policy's token behind each row.
+    Returns (rows int32 [members][n], the kept rows, -1 behind them; count [members]; follow
+    [members], the token chosen behind the last kept row; ends [members], the members' lengths
+    with the kept rows)."""
+    if stream is not None:
+        with _as_current(stream):
+            return accept_draft(parents, tokens, chosen, lens, drafted)
+    M, n, dev, pp, lp, dp = _draft_args(parents, lens, drafted)
+    st = _dev_stream(dev)
+    tp = _dense(tokens, "tokens", torch.int32, (M, n), dev)
+    cp = _dense(chosen, "chosen", torch.int32, (M, n), dev)
+    out = torch.empty(M * (n + 3), dtype=torch.int32, device=parents.device)
+    rows, count, follow, ends = out.split((M * n, M, M, M))
+    p, k = out.data_ptr(), 4 * M
+    B.ls_accept_draft(pp, tp, cp, lp, dp, M, n, p, p + k * n, p + k * (n + 1), p + k * (n + 2), st)
+    return rows.view(M, n), count, follow, ends
+
+
+class LayerPools:
+    """The K / V pages of every layer under one block table: bf16
+    [layers][num_pages][Hkv][page_size][128] each, for calls that move rows in all of them."""
+
+    def __init__(self, k_pools: torch.Tensor, v_pools: torch.Tensor):
+        if k_pools.dim() != 5 or k_pools.shape[0] < 1:
+            raise ValueError("k_pools must be [layers][num_pages][Hkv][page_size][128]")
+        L, n, hkv, ps, _ = k_pools.shape
+        _check_pool(k_pools, "k_pools", (L, n, hkv, ps, HEAD_DIM))
+        _check_pool(v_pools, "v_pools", (L, n, hkv, ps, HEAD_DIM))
+        self.k_pools, self.v_pools = k_pools, v_pools
+        self.layers, self.num_pages, self.page_size = L, n, ps
+        self.layer_stride = n * hkv * ps * HEAD_DIM
+        self.device_indices = {k_pools.get_device(), v_pools.get_device()} - {-1}
+        self.struct = B.ls_page_pool(k_pools.data_ptr(), v_pools.data_ptr(), n, ps, hkv, HEAD_DIM)
+
+
+def _of_alloc(pools: LayerPools, alloc: PageAllocator):
+    if (pools.page_size != alloc.page_size or pools.num_pages < alloc.num_pages
+            or pools.device_indices - {alloc.device_index}):
+        raise ValueError("the pools do not hold the allocator's pages")
+
+
+def compact_rows(alloc: PageAllocator, pools: LayerPools, rows: torch.Tensor, count: torch.Tensor,
+                 drafted: torch.Tensor | None = None, stream=None) -> None:
+    """The keys and values of accept_draft's rows follow the members' contexts, one behind the
+    other, in every layer's pages.  alloc.lens still counts the drafts; trim_pages to
+    accept_draft's ends comes next."""
+    if stream is not None:
+        with _as_current(stream):
+            return compact_rows(alloc, pools, rows, count, drafted)
+    M, dev = alloc.members, alloc.device_index
+    st = _dev_stream(dev)
+    _of_alloc(pools, alloc)
+    n = rows.shape[1] if rows.dim() == 2 else -1
+    B.ls_compact_rows(pools.struct, pools.layers, pools.layer_stride, alloc.block_table.data_ptr(),
+                      alloc.max_blocks, alloc.lens.data_ptr(),
+                      None if drafted is None else _dense(drafted, "drafted", torch.int32, (M,), dev),
+                      M, n, _dense(rows, "rows", torch.int32, (M, n), dev),
+                      _dense(count, "count", torch.int32, (M,), dev), st)
+
+
+# ---------------------------------------------------------------- pages given back and shared
+
+def _lens_used(alloc: PageAllocator, lens_out, used_out):
+    M, dev = alloc.members, alloc.device_index
+    return (alloc.lens.data_ptr() if lens_out is None
+            else _dense(lens_out, "lens_out", torch.int32, (M,), dev),
+            alloc.used.data_ptr() if used_out is None
+            else _dense(used_out, "used_out", torch.int32, (1,), dev))
+
+
+def trim_pages(alloc: PageAllocator, new_lens: torch.Tensor, lens_out: torch.Tensor | None = None,
+               used_out: torch.Tensor | None = None, stream=None) -> None:
+    """Every member keeps its first new_lens[m] tokens (negative: out of use); the pages behind
+    them that nobody else holds go back to the free list.  alloc.lens and alloc.used follow (or
+    lens_out / used_out are written).  See ls_trim_pages for what is refused."""
+    if stream is not None:
+        with _as_current(stream):
+            return trim_pages(alloc, new_lens, lens_out, used_out)
+    M, dev = alloc.members, alloc.device_index
+    st = _dev_stream(dev)
+    lo, uo = _lens_used(alloc, lens_out, used_out)
+    B.ls_trim_pages(alloc.block_table.data_ptr(), M, alloc.max_blocks, alloc.page_size,
+                    alloc.num_pages, alloc.lens.data_ptr(),
+                    _dense(new_lens, "new_lens", torch.int32, (M,), dev), alloc.free_list.data_ptr(),
+                    alloc.num_free, alloc.used.data_ptr(),
+                    None if alloc.shared is None else alloc.shared.data_ptr(), lo, uo, st)
+
+
+def fork_pages(alloc: PageAllocator, src: torch.Tensor, keep: torch.Tensor | None = None,
+               copies: torch.Tensor | None = None, lens_out: torch.Tensor | None = None,
+               used_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Member m with src[m] >= 0 becomes a branch of that member's first keep[m] tokens (default:
+    all).  Whole pages are shared; returns copies int32 [3][members], what copy_pages has to
+    copy of the partial ones.  See ls_fork_pages for what is refused."""
+    if stream is not None:
+        with _as_current(stream):
+            return fork_pages(alloc, src, keep, copies, lens_out, used_out)
+    M, dev = alloc.members, alloc.device_index
+    st = _dev_stream(dev)
+    if alloc.shared is None:
+        raise ValueError("the allocator does not share pages (PageAllocator's shared)")
+    if copies is None:
+        copies = torch.empty((3, M), dtype=torch.int32, device=alloc.block_table.device)
+    lo, uo = _lens_used(alloc, lens_out, used_out)
+    B.ls_fork_pages(alloc.block_table.data_ptr(), M, alloc.max_blocks, alloc.page_size,
+                    alloc.num_pages, alloc.lens.data_ptr(), _dense(src, "src", torch.int32, (M,), dev),
+                    None if keep is None else _dense(keep, "keep", torch.int32, (M,), dev),
+                    alloc.free_list.data_ptr(), alloc.num_free, alloc.used.data_ptr(),
+                    alloc.shared.data_ptr(), _dense(copies, "copies", torch.int32, (3, M), dev), lo,
+                    uo, st)
+    return copies
+
+
+def copy_pages(pools: LayerPools, copies: torch.Tensor, stream=None) -> None:
+    """copies int32 [3][count]: the first copies[2][i] rows of page copies[0][i] to page
+    copies[1][i], in every layer; (-1, -1) where there is nothing to copy."""
+    if stream is not None:
+        with _as_current(stream):
+            return copy_pages(pools, copies)
+    dev = copies.get_device()
+    st = _dev_stream(dev)
+    if pools.device_indices - {dev}:
+        raise ValueError("the pools are on another device")
+    n = copies.shape[1] if copies.dim() == 2 else -1
+    p = _dense(copies, "copies", torch.int32, (3, n), dev)
+    B.ls_copy_pages(pools.struct, pools.layers, pools.layer_stride, n, p, p + 4 * n, p + 8 * n, st)
+
+
+# ---------------------------------------------------------------- token statistics
+
+def _logit_rows(t: torch.Tensor, name: str, dtype, shape, dev: int):
+    """(address, row stride) of [T][V] rows, each dense."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _refuse(t, name, dtype, shape, dev)
+    T, V = shape
+    rs, es = t.stride()
+    if T <= 1:
+        rs = V
+    if (V > 1 and es != 1) or rs < V:
+        raise ValueError(f"{name}: rows must be contiguous and may not overlap")
+    return t.data_ptr(), rs
+
+
+def _logits(logits: torch.Tensor):
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T][V]")
+    if logits.dtype is not torch.bfloat16 and logits.dtype is not torch.float32:
+        raise ValueError("logits must be bf16 or fp32")
+    dev = logits.get_device()
+    p, rs = _logit_rows(logits, "logits", logits.dtype, logits.shape, dev)
+    return dev, *logits.shape, B.LS_BF16 if logits.dtype is torch.bfloat16 else B.LS_FP32, p, rs
+
+
+def token_logp_fwd(logits: torch.Tensor, targets: torch.Tensor | None, temperature: float = 1.0,
+                   top: int = 0, stream=None):
+    """Log probabilities of the targets, entropies and the `top` likeliest tokens of the rows:
+    logits [T][V] bf16 or fp32 (rows may be apart, as of a padded vocabulary), targets int32 [T]
+    (-1: a padding row; None: no log probabilities).  Returns (logp, lse, entropy, top_logp
+    [T][top], top_ids [T][top]); None where there is none.  See ls_token_logp_fwd."""
+    if stream is not None:
+        with _as_current(stream):
+            return token_logp_fwd(logits, targets, temperature, top)
+    dev, T, V, dt, p, rs = _logits(logits)
+    st = _dev_stream(dev)
+    tp = None if targets is None else _dense(targets, "targets", torch.int32, (T,), dev)
+    f32 = dict(dtype=torch.float32, device=logits.device)
+    stats = torch.empty((3, T), **f32)
+    sp = stats.data_ptr()
+    logp, lse, entropy = stats.unbind(0)
+    top_logp = top_ids = lp = ip = None
+    if top > 0:
+        top_logp = torch.empty((T, top), **f32)
+        top_ids = torch.empty((T, top), dtype=torch.int32, device=logits.device)
+        lp, ip = top_logp.data_ptr(), top_ids.data_ptr()
+    if T > 0:
+        _with_workspace(B.ls_token_logp_fwd,
+                        (p, dt, T, V, rs, tp, temperature, top, sp if targets is not None else None,
+                         sp + 4 * T, sp + 8 * T, lp, ip),
+                        lambda: B.ls_token_logp_fwd_workspace(dt, T, V, top), logits, "token_logp", st)
+    return (logp if targets is not None else None), lse, entropy, top_logp, top_ids
+
+
+def token_logp_bwd(logits: torch.Tensor, targets: torch.Tensor | None, lse: torch.Tensor,
+                   entropy: torch.Tensor | None, d_logp: torch.Tensor | None,
+                   d_entropy: torch.Tensor | None = None, temperature: float = 1.0,
+                   top_ids: torch.Tensor | None = None, d_top: torch.Tensor | None = None,
+                   dlogits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gradient that an objective of token_logp_fwd's outputs sends to the logits: d_logp,
+    d_entropy fp32 [T] (each or None), d_top fp32 [T][top] with top_ids.  lse and entropy are
+    the forward's.  dlogits may be the logits themselves.  Returns dlogits."""
+    if stream is not None:
+        with _as_current(stream):
+            return token_logp_bwd(logits, targets, lse, entropy, d_logp, d_entropy, temperature,
+                                  top_ids, d_top, dlogits)
+    dev, T, V, dt, p, rs = _logits(logits)
+    st = _dev_stream(dev)
+
+    def row(t, name, dtype=torch.float32):
+        return None if t is None else _dense(t, name, dtype, (T,), dev)
+
+    if dlogits is None:
+        dlogits = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+    dp, drs = _logit_rows(dlogits, "dlogits", logits.dtype, logits.shape, dev)
+    if (top_ids is None) != (d_top is None):
+        raise ValueError("top_ids and d_top go together")
+    top, ip, tp = 0, None, None
+    if d_top is not None:
+        top = d_top.shape[1] if d_top.dim() == 2 else -1
+        ip = _dense(top_ids, "top_ids", torch.int32, (T, top), dev)
+        tp = _dense(d_top, "d_top", torch.float32, (T, top), dev)
+    B.ls_token_logp_bwd(p, dt, T, V, rs, row(targets, "targets", torch.int32), temperature,
+                        row(lse, "lse"), row(entropy, "entropy"), top, ip, row(d_logp, "d_logp"),
+                        row(d_entropy, "d_entropy"), tp, dp, drs, st)
+    return dlogits
