@@ -1349,7 +1349,7 @@ ls_status ls_token_logp_fwd(const void* logits, ls_dtype dtype, int64_t T, int V
   a.top_ids = top_ids;
   a.workspace = workspace;
   a.err = d.err;
-  return from_cuda(ls_launch_token_logp_fwd(a, parts, (cudaStream_t)stream));
+  return from_cuda(ls_launch_token_logp_fwd(a, parts, d.sms, (cudaStream_t)stream));
 }
 
 ls_status ls_token_logp_bwd(const void* logits, ls_dtype dtype, int64_t T, int V, int64_t row_stride,

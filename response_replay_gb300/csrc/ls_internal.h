@@ -333,7 +333,7 @@ struct LsTokenLogpBwdArgs {
 };
 int ls_token_logp_parts(bool is_bf16, int64_t T, int V, int top, int sms);
 size_t ls_token_logp_ws_bytes(int64_t T, int parts);
-cudaError_t ls_launch_token_logp_fwd(const LsTokenLogpArgs& a, int parts, cudaStream_t st);
+cudaError_t ls_launch_token_logp_fwd(const LsTokenLogpArgs& a, int parts, int sms, cudaStream_t st);
 int64_t ls_token_logp_bwd_parts(const LsTokenLogpBwdArgs& a, int sms);
 cudaError_t ls_launch_token_logp_bwd(const LsTokenLogpBwdArgs& a, int sms, cudaStream_t st);
 

@@ -23,13 +23,15 @@
 
 #include "ls_device.cuh"
 #include "ls_internal.h"
+#include "ls_umma.cuh"
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 384;  // consumers of the forward, a group of 64 bytes each a step
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxGroups = 12288;  // group maxima of a part: 48 KB
-constexpr int kCand = 256;         // groups collected before they are read again
+constexpr int kGroupBytes = 64;
+constexpr int kGmaxBytes = 20480;  // group maxima of a part, of the logits' type
+constexpr int kBwdThreads = 512;
 constexpr double kLn2d = 0.69314718055994530942;
 constexpr double kLog2ed = 1.4426950408889634074;
 
@@ -45,10 +47,23 @@ __device__ __forceinline__ float max_nan(float x, float y) {
 __device__ __forceinline__ float floor_exp(float t) { return max_nan(t, -200.f); }
 
 template <typename E>
-struct Row;  // 32-byte groups of a row
+struct Row;  // N: values of 16 bytes
 template <>
 struct Row<float> {
-  static constexpr int G = 8;
+  static constexpr int N = 4;
+  // the largest of 64 bytes (NaN only where all are)
+  __device__ static float max_of(const uint4* u) {
+    float m[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      m[v] = fmaxf(fmax3(__uint_as_float(u[v].x), __uint_as_float(u[v].y), __uint_as_float(u[v].z)),
+                   __uint_as_float(u[v].w));
+    return fmaxf(fmax3(m[0], m[1], m[2]), m[3]);
+  }
+  // 16 bytes of values
+  __device__ static void put(uint4* u, int i, float x) {
+    reinterpret_cast<float*>(u)[i] = x;
+  }
   __device__ static void unpack(const uint4& u, float* x) {
     x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
     x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
@@ -62,7 +77,21 @@ struct Row<float> {
 };
 template <>
 struct Row<__nv_bfloat16> {
-  static constexpr int G = 16;
+  static constexpr int N = 8;
+  __device__ static float max_of(const uint4* u) {
+    auto max2 = [](uint32_t x, uint32_t y) {  // of two pairs
+      uint32_t r;
+      asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+      return r;
+    };
+    uint32_t m = max2(max2(u[0].x, u[0].y), max2(u[0].z, u[0].w));
+#pragma unroll
+    for (int v = 1; v < 4; ++v) m = max2(m, max2(max2(u[v].x, u[v].y), max2(u[v].z, u[v].w)));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+  __device__ static void put(uint4* u, int i, float x) {
+    reinterpret_cast<__nv_bfloat16*>(u)[i] = __float2bfloat16_rn(x);  // of a bf16 number: exact
+  }
   __device__ static void unpack(const uint4& u, float* x) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -79,16 +108,12 @@ struct Row<__nv_bfloat16> {
   __device__ static void store(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 };
 
-// Logits and places as one number that orders them: larger logits first, equal ones (one
-// zero) by the lower place.  NaN: 0, behind all.
+// Logits as whole numbers in their order (one zero; NaN: 0, behind all), and with their places
+// as one number: larger logits first, equal ones by the lower place (the complement below).
 __device__ __forceinline__ uint32_t order_of(float x) {
   const uint32_t b = __float_as_uint(x + 0.f);
   if (x != x) return 0u;
   return (int32_t)b < 0 ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ u64 key_of(float x, uint32_t place) {
-  const uint32_t o = order_of(x);
-  return o ? (u64)o << 32 | (uint32_t)~place : 0ull;
 }
 __device__ __forceinline__ float value_of(u64 key) {
   const uint32_t o = (uint32_t)(key >> 32);
@@ -116,22 +141,111 @@ __device__ __forceinline__ u64 merge32(u64 list, u64 batch, int lane) {
   return x;
 }
 
-// Running maximum m of the logits, s = sum 2^t, e = sum 2^t t with t = (z - m) c.
+// A reference m (one of the logits; none passes it by more than 2^100, or it is moved), s =
+// sum 2^t, e = sum 2^t t with t = z c - r, r = m c rounded: one multiply-add an exponent.  Where m c
+// is too large for that (a row of a type's lowest values), t = (z - m) c.
 struct Stat {
   float m, s, e;
 };
+__device__ __forceinline__ bool plain_ref(float r) { return fabsf(r) < 1e30f; }
+// t of one maximum under another: what moves sums from the one to the other.
+__device__ __forceinline__ float shift(float from, float to, float c) {
+  const float a = from * c, b = to * c;
+  return plain_ref(a) && plain_ref(b) ? a - b : (from - to) * c;
+}
+__device__ __forceinline__ Stat move(Stat x, float m, float c) {
+  if (x.m == -INFINITY || x.m == m) return x;  // no finite logit: nothing to move
+  const float d = shift(x.m, m, c), f = fast_exp2(d);
+  return {m, x.s * f, (x.e + x.s * floor_exp(d)) * f};
+}
 __device__ __forceinline__ Stat merge(Stat a, Stat b, float c) {
   const float m = fmaxf(a.m, b.m);
-  if (m == -INFINITY) return {m, a.s + b.s, a.e + b.e};  // no finite logit (or NaN sums)
-  auto move = [&](Stat x) {
-    if (x.m == -INFINITY) return x;
-    const float d = (x.m - m) * c, f = fast_exp2(d);
-    return Stat{m, x.s * f, (x.e + x.s * floor_exp(d)) * f};
-  };
-  a = move(a);
-  b = move(b);
+  a = move(a, m, c);
+  b = move(b, m, c);
   return {m, a.s + b.s, a.e + b.e};
 }
+// Over a warp's lanes, in every lane: the maximum first, so that each moves once.
+__device__ __forceinline__ Stat warp_stat(Stat x, float c) {
+  float m = x.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  x = move(x, m, c);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    x.s += __shfl_xor_sync(0xffffffffu, x.s, o);
+    x.e += __shfl_xor_sync(0xffffffffu, x.e, o);
+  }
+  return {m, x.s, x.e};
+}
+
+// A thread's sums over its groups.
+template <typename E>
+struct Sums {
+  static constexpr int H = Row<E>::N;
+  float m, nr, c;                          // nr = -m c
+  float2 s, e;
+  __device__ __forceinline__ explicit Sums(float c_)
+      : m(-INFINITY), nr(INFINITY), c(c_), s(make_float2(0.f, 0.f)), e(make_float2(0.f, 0.f)) {}
+
+  // N vectors of 16 bytes.  The reference stays as it is as long as the sums are numbers of a
+  // usual size: of 32 threads one would find a new maximum in most groups, and the warp would
+  // move its sums with each.  Otherwise (the first group, a logit that passes the reference by
+  // far, an exponent of -inf, NaN) the vectors are taken once more, carefully.
+  template <int N>
+  __device__ __forceinline__ void add(const uint4* u) {
+    const float2 s0 = s, e0 = e, b = make_float2(nr, nr), c2 = make_float2(c, c);
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+      float x[H];
+      Row<E>::unpack(u[v], x);
+#pragma unroll
+      for (int i = 0; i < H; i += 2) {
+        const float2 t = __ffma2_rn(make_float2(x[i], x[i + 1]), c2, b);
+        const float2 p = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+        s = __fadd2_rn(s, p);
+        e = __ffma2_rn(p, t, e);
+      }
+    }
+    if (!(fabsf(e.x + e.y) < 1e30f)) {
+      s = s0;
+      e = e0;
+      carefully<N>(u);
+    }
+  }
+
+  template <int N>
+  __device__ __forceinline__ void carefully(const uint4* u) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+      float x[H];
+      Row<E>::unpack(u[v], x);
+#pragma unroll
+      for (int i = 0; i < H; ++i) mx = fmaxf(mx, x[i]);
+    }
+    if (mx > m) {
+      const Stat x = move(stat(), mx, c);
+      s = make_float2(x.s, 0.f);
+      e = make_float2(x.e, 0.f);
+      m = mx;
+      nr = -(m * c);
+    }
+    const bool fine = plain_ref(nr);
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+      float x[H];
+      Row<E>::unpack(u[v], x);
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        const float t = floor_exp(fine ? fmaf(x[i], c, nr) : m == -INFINITY ? x[i] : (x[i] - m) * c);
+        const float p = fast_exp2(t);
+        s.x += p;
+        e.x = fmaf(p, t, e.x);
+      }
+    }
+  }
+  __device__ __forceinline__ Stat stat() const { return {m, s.x + s.y, e.x + e.y}; }
+};
 
 struct Out {
   float* logp;
@@ -141,46 +255,50 @@ struct Out {
   int32_t* top_ids;
 };
 
-// The row's numbers from its statistics; returns lse.
-__device__ __forceinline__ double finish_row(const Stat& a, double inv_tau, const Out& out,
-                                             int64_t row, bool has_y, float zy) {
-  const double log2s = (double)log2f(a.s);
-  const double lse = a.m == -INFINITY && a.s == 0.f ? -INFINITY
-                                                    : (double)a.m * inv_tau + kLn2d * log2s;
-  if (out.lse) out.lse[row] = (float)lse;
-  if (out.entropy) out.entropy[row] = (float)(kLn2d * (log2s - (double)a.e / (double)a.s));
-  if (out.logp) out.logp[row] = has_y ? (float)((double)zy * inv_tau - lse) : NAN;
-  return lse;
-}
-
 struct FwdArgs {
   const void* logits;
   int64_t T, ld;
   int32_t V, top, parts;
   const int32_t* targets;
-  float c;          // log2(e) / tau
+  float c;          // log2(e) / tau, rounded
   double inv_tau;
+  double c_off;     // by how much, relative
   Out out;
   float* part_stat;  // [T][parts][4]
   u64* part_top;     // [T][parts][32]
   uint32_t* err;
 };
 
+// The row's numbers from its statistics; returns lse.  The rounding of c moves log2 of the sum by
+// c_off times the mean exponent, which is r + e / s.
+__device__ __forceinline__ double finish_row(const FwdArgs& a, const Stat& x, int64_t row, bool has_y,
+                                             float zy) {
+  const float mean = x.e / x.s, r = x.m * a.c;
+  const double log2s = (double)log2f(x.s);
+  double lse;
+  if (x.m == -INFINITY && x.s == 0.f)
+    lse = -INFINITY;
+  else if (plain_ref(r))
+    lse = kLn2d * ((double)r + log2s - a.c_off * ((double)r + (double)mean));
+  else
+    lse = (double)x.m * a.inv_tau + kLn2d * log2s;
+  if (a.out.lse) a.out.lse[row] = (float)lse;
+  if (a.out.entropy) a.out.entropy[row] = (float)(kLn2d * (log2s - (double)mean));
+  if (a.out.logp) a.out.logp[row] = has_y ? (float)((double)zy * a.inv_tau - lse) : NAN;
+  return lse;
+}
+
 // Rows whose target is -1 are padding: their outputs are zeros and ids -1.
-__device__ __forceinline__ bool padding_row(const FwdArgs& a, int64_t row, bool first, int lane) {
-  if (!a.targets || a.targets[row] != -1) return false;
-  if (first) {
-    if (lane == 0) {
-      if (a.out.logp) a.out.logp[row] = 0.f;
-      if (a.out.lse) a.out.lse[row] = 0.f;
-      if (a.out.entropy) a.out.entropy[row] = 0.f;
-    }
-    if (lane < a.top) {
-      a.out.top_logp[row * a.top + lane] = 0.f;
-      a.out.top_ids[row * a.top + lane] = -1;
-    }
+__device__ __forceinline__ void padding_row(const FwdArgs& a, int64_t row, int lane) {
+  if (lane == 0) {
+    if (a.out.logp) a.out.logp[row] = 0.f;
+    if (a.out.lse) a.out.lse[row] = 0.f;
+    if (a.out.entropy) a.out.entropy[row] = 0.f;
   }
-  return true;
+  if (lane < a.top) {
+    a.out.top_logp[row * a.top + lane] = 0.f;
+    a.out.top_ids[row * a.top + lane] = -1;
+  }
 }
 template <typename E>
 __device__ __forceinline__ bool target_logit(const FwdArgs& a, int64_t row, float* zy) {
@@ -194,217 +312,467 @@ __device__ __forceinline__ bool target_logit(const FwdArgs& a, int64_t row, floa
   return true;
 }
 
-// What warp 0 needs besides to pick a part's largest logits.
-struct TopSmem {
-  u64 best[kThreads];  // each thread's largest group
-  u64 found[64];       // logits that passed, on their way into the sorted list
-  int32_t cand[kCand];
-  float gmax[kMaxGroups];
+__device__ __forceinline__ void write_top(const FwdArgs& a, int64_t row, u64 key, double lse, int lane) {
+  if (lane >= a.top) return;
+  a.out.top_logp[row * a.top + lane] = key ? (float)((double)value_of(key) * a.inv_tau - lse) : NAN;
+  a.out.top_ids[row * a.top + lane] = key ? (int32_t)~(uint32_t)key : -1;
+}
+
+// ---------------------------------------------------------------- forward
+//
+// A persistent CTA takes items (a part of a row) by turns: a producer warp streams an item's
+// whole groups through a ring of 24 KB chunks by bulk copies, a group a consumer thread and
+// chunk, and runs ahead into the next item while the consumers end one; a last warp takes the
+// consumers' results and candidates, reads those groups again and writes the row's outputs
+// while the consumers are at the next item.  Groups that stick out of the row are read with
+// plain loads.
+constexpr int kChunkBytes = kThreads * kGroupBytes;
+constexpr int kCtaThreads = kThreads + 64;
+constexpr int kHand = kThreads + 32;  // the consumers and the last warp
+template <bool kTop>
+struct Cfg {
+  static constexpr int kStages = kTop ? 3 : 4;
+};
+constexpr int kFewTops = 12;  // alternatives for which 32 maxima make the threshold
+constexpr int kRanked = 128;  // logits that are put in order by counting
+constexpr int kCand = 512;  // groups that reach the threshold, before the slow way is taken
+
+constexpr int kFound = 32 * 16 + kRanked;
+
+struct FwdSmem {  // behind the ring; [2]: by parity of the item
+  uint64_t full[6], empty[6], free[2];
+  int abort;
+  int cands[2];
+  float m[2][kThreads], s[2][kThreads], e[2][kThreads];
+  uint32_t floor_o[2];  // the threshold: a maximum, and the last place among equal ones
+  int floor_g[2];
+  alignas(16) uint32_t tops[2][64];
+  int topg[2][64];
+  alignas(16) u64 found[kFound];  // logits that reach the threshold, on their way into the list
+  uint16_t cand[2][kCand];
+  uint8_t gmax[kGmaxBytes];  // the groups' maxima, of the logits' type
 };
 
-// The 32 largest logits of groups [g0, g0 + ng), sorted, one a lane of the calling warp.
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+}
+__device__ __forceinline__ void hand_over(int par) {
+  if (par)
+    asm volatile("bar.arrive 3, %0;" ::"n"(kHand) : "memory");
+  else
+    asm volatile("bar.arrive 2, %0;" ::"n"(kHand) : "memory");
+}
+__device__ __forceinline__ void take_over(int par) {
+  if (par)
+    asm volatile("bar.sync 3, %0;" ::"n"(kHand) : "memory");
+  else
+    asm volatile("bar.sync 2, %0;" ::"n"(kHand) : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst), "l"(src), "r"(bytes), "r"(mbar)
+      : "memory");
+}
+
+// An item: groups [g0, g0 + ng) of a row, of which [in0, in1) lie wholly inside it.
 template <typename E>
-__device__ u64 pick(TopSmem& sm, const E* zr, int V, int lead, int g0, int ng, int k, int lane) {
-  constexpr int G = Row<E>::G;
-  u64 mine = 0;
+struct Item {
+  static constexpr int G = kGroupBytes / sizeof(E);
+  const E* zr;
+  int64_t row;
+  int part, lead, g0, ng, in0, in1;
+  bool pad;
+  static __device__ __forceinline__ int64_t row_of(const FwdArgs& a, int64_t item) {
+    return a.parts == 1 ? item : item / a.parts;
+  }
+  // y: the row's target, asked for one item ahead
+  static __device__ __forceinline__ int32_t target(const FwdArgs& a, int64_t item) {
+    return a.targets && item < a.T * a.parts ? __ldg(a.targets + row_of(a, item)) : 0;
+  }
+  __device__ __forceinline__ Item(const FwdArgs& a, int64_t item, int32_t y) {
+    row = row_of(a, item);
+    part = (int)(item - row * a.parts);
+    pad = y == -1;
+    zr = static_cast<const E*>(a.logits) + row * a.ld;
+    lead = (int)((reinterpret_cast<uintptr_t>(zr) & (kGroupBytes - 1)) / sizeof(E));
+    const int64_t all = ((int64_t)lead + a.V + G - 1) / G;
+    g0 = a.parts == 1 ? 0 : (int)(all * part / a.parts);
+    ng = (a.parts == 1 ? (int)all : (int)(all * (part + 1) / a.parts)) - g0;
+    in0 = g0 == 0 && lead > 0 ? 1 : 0;
+    in1 = ng - (part == a.parts - 1 && (lead + a.V) % G != 0 ? 1 : 0);
+    if (in1 < in0) in1 = in0;  // one group that sticks out at both ends
+  }
+  __device__ __forceinline__ int chunks() const { return pad ? 0 : (in1 - in0 + kThreads - 1) / kThreads; }
+  __device__ __forceinline__ const E* at(int g) const { return zr - lead + (int64_t)(g0 + g) * G; }
+  // the place in the row of a group's first value (negative: it sticks out)
+  __device__ __forceinline__ int place(int g) const { return (g0 + g) * G - lead; }
+  // vectors [v0, v0 + n) of a group's 64 bytes; -inf outside the row
+  template <int n>
+  __device__ __forceinline__ void load(int V, int g, int v0, uint4* u) const {
+    if (g >= in0 && g < in1) {
+      const uint4* p = reinterpret_cast<const uint4*>(at(g)) + v0;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) mine = max64(mine, sm.best[lane + 32 * i]);
-  const u64 floor = __shfl_sync(0xffffffffu, sort32(mine, lane), k - 1);
-  u64 list = 0;
-  int found = 0, cands = 0;
-  auto flush = [&] {
-    __syncwarp();
-    constexpr int kPer = 32 / G, kBatch = 8;  // groups a step; steps whose loads go together
-    for (int j0 = 0; j0 < cands; j0 += kPer * kBatch) {
-      u64 key[kBatch];
-      bool pass[kBatch];
+      for (int v = 0; v < n; ++v) u[v] = p[v];
+    } else {
+      const int64_t p = (int64_t)(g0 + g) * G - lead + v0 * Row<E>::N;
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int j = j0 + b * kPer + lane / G;
-        key[b] = 0;
-        pass[b] = false;
-        if (j < cands) {
-          const int g = sm.cand[j], at = (g0 + g) * G + lane % G - lead;
-          if (at >= 0 && at < V) {
-            const float x = Row<E>::load(zr + at);
-            key[b] = key_of(x, at);
-            pass[b] = key_of(x, g) >= floor;
-          }
-        }
-      }
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const u64 kth = __shfl_sync(0xffffffffu, list, k - 1);  // by all lanes
-        const bool in = pass[b] && key[b] > kth;
-        const uint32_t mask = __ballot_sync(0xffffffffu, in);
-        if (mask == 0) continue;
-        if (in) sm.found[found + __popc(mask & ((1u << lane) - 1))] = key[b];
-        found += __popc(mask);
-        __syncwarp();
-        if (found >= 32) {
-          list = merge32(list, sort32(sm.found[found - 32 + lane], lane), lane);
-          found -= 32;
-          __syncwarp();
-        }
-      }
-    }
-    cands = 0;
-  };
-  for (int i = 0; i < kWarps; ++i) {
-    const u64 b = sm.best[lane + 32 * i];
-    uint32_t threads = __ballot_sync(0xffffffffu, b != 0 && b >= floor);
-    while (threads) {
-      const int t = 32 * i + __ffs(threads) - 1;
-      threads &= threads - 1;
-      for (int c0 = 0; t + c0 * kThreads < ng; c0 += 32) {
-        const int g = t + (c0 + lane) * kThreads;
-        const bool in = g < ng && key_of(sm.gmax[g], g) >= floor;
-        const uint32_t mask = __ballot_sync(0xffffffffu, in);
-        if (in) sm.cand[cands + __popc(mask & ((1u << lane) - 1))] = g;
-        cands += __popc(mask);
-        if (cands > kCand - 32) flush();
-      }
+      for (int i = 0; i < n * Row<E>::N; ++i)
+        Row<E>::put(u + i / Row<E>::N, i % Row<E>::N,
+                    p + i >= 0 && p + i < V ? Row<E>::load(zr + p + i) : -INFINITY);
     }
   }
-  flush();
-  if (found) list = merge32(list, sort32(lane < found ? sm.found[lane] : 0ull, lane), lane);
+};
+
+template <typename E>
+__device__ __forceinline__ float group_max(const FwdSmem& sm, int g);
+template <>
+__device__ __forceinline__ float group_max<float>(const FwdSmem& sm, int g) {
+  return reinterpret_cast<const float*>(sm.gmax)[g];
+}
+template <>
+__device__ __forceinline__ float group_max<__nv_bfloat16>(const FwdSmem& sm, int g) {
+  return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(sm.gmax)[g] << 16);
+}
+template <typename E>
+__device__ __forceinline__ void put_max(FwdSmem& sm, int g, float x);
+template <>
+__device__ __forceinline__ void put_max<float>(FwdSmem& sm, int g, float x) {
+  reinterpret_cast<float*>(sm.gmax)[g] = x;
+}
+template <>
+__device__ __forceinline__ void put_max<__nv_bfloat16>(FwdSmem& sm, int g, float x) {
+  reinterpret_cast<uint16_t*>(sm.gmax)[g] = (uint16_t)(__float_as_uint(x) >> 16);
+}
+
+// The 32 largest logits of an item, sorted, one a lane, by one warp: of the groups that reach the
+// threshold, or (more of them than the list holds: rows whose largest logits all lie with the
+// same threads) of all groups.
+template <typename E>
+__device__ u64 pick(FwdSmem& sm, const Item<E>& it, const FwdArgs& a, int par, int lane) {
+  constexpr int kHalf = Item<E>::G / 2;
+  const int cands = sm.cands[par];
+  const bool all = cands > kCand;
+  const int n = all ? it.ng : cands;
+  const uint32_t floor_o = all ? 0u : sm.floor_o[par];
+  const int floor_g = all ? INT32_MAX : sm.floor_g[par];
+  u64 kth = 0, list = 0;
+  int found = 0;
+  for (int j0 = 0; j0 < n; j0 += 16) {  // half a group a lane
+    const int j = j0 + (lane >> 1), g = all ? j : j < n ? sm.cand[par][j] : 0;
+    float x[kHalf];
+    const int place = it.place(g) + (lane & 1) * kHalf;
+    if (j < n) {
+      uint4 u[2];
+      it.template load<2>(a.V, g, 2 * (lane & 1), u);
+      Row<E>::unpack(u[0], x);
+      Row<E>::unpack(u[1], x + kHalf / 2);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) x[i] = NAN;
+    }
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) {
+      const uint32_t o = order_of(x[i]);
+      bool in = o > floor_o || (o == floor_o && o != 0 && g <= floor_g);
+      const u64 key = (u64)o << 32 | (uint32_t)~(uint32_t)(place + i);
+      in = in && key > kth && place + i >= 0 && place + i < a.V;
+      const uint32_t mask = __ballot_sync(0xffffffffu, in);
+      if (mask == 0) continue;
+      if (in) sm.found[found + __popc(mask & ((1u << lane) - 1))] = key;
+      found += __popc(mask);
+    }
+    __syncwarp();
+    if (found > kRanked) {  // more than are put in order by counting
+      while (found >= 32) {
+        found -= 32;
+        list = merge32(list, sort32(sm.found[found + lane], lane), lane);
+      }
+      kth = __shfl_sync(0xffffffffu, list, a.top - 1);
+      __syncwarp();
+    }
+  }
+  if (found <= kRanked && list == 0) {  // (the list is empty in every lane or in none)
+    // each one's place is the number of larger ones
+    u64 mine[kRanked / 32];
+    int rank[kRanked / 32];
+#pragma unroll
+    for (int i = 0; i < kRanked / 32; ++i) {
+      mine[i] = i * 32 + lane < found ? sm.found[i * 32 + lane] : 0ull;
+      rank[i] = 0;
+    }
+    if (lane == 0) sm.found[found] = 0ull;
+    __syncwarp();
+    for (int j = 0; j < found; j += 2) {
+      const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(sm.found + j);
+#pragma unroll
+      for (int i = 0; i < kRanked / 32; ++i) rank[i] += (y.x > mine[i]) + (y.y > mine[i]);
+    }
+    __syncwarp();
+    sm.found[lane] = 0ull;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kRanked / 32; ++i)
+      if (mine[i] != 0 && rank[i] < 32) sm.found[rank[i]] = mine[i];
+    __syncwarp();
+    list = sm.found[lane];
+  } else {
+    for (int i = 0; i < found; i += 32)
+      list = merge32(list, sort32(i + lane < found ? sm.found[i + lane] : 0ull, lane), lane);
+  }
+  __syncwarp();
   return list;
 }
 
-__device__ __forceinline__ void write_top(const Out& out, int64_t row, int top, u64 key, double lse,
-                                          double inv_tau, int lane) {
-  if (lane >= top) return;
-  out.top_logp[row * top + lane] = key ? (float)((double)value_of(key) * inv_tau - lse) : NAN;
-  out.top_ids[row * top + lane] = key ? (int32_t)~(uint32_t)key : -1;
-}
-
 template <typename E, bool kTop>
-__global__ void __launch_bounds__(kThreads, 3) logp_fwd(const FwdArgs a) {
+__global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
   using R = Row<E>;
-  constexpr int G = R::G, H = G / 2;
-  extern __shared__ __align__(16) uint8_t dyn[];
-  __shared__ Stat red[kWarps];
-  TopSmem& sm = *reinterpret_cast<TopSmem*>(dyn);
+  constexpr int kStages = Cfg<kTop>::kStages;
+  extern __shared__ __align__(1024) uint8_t ring[];
+  FwdSmem& sm = *reinterpret_cast<FwdSmem*>(ring + kStages * kChunkBytes);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t row = blockIdx.x / a.parts;
-  const int part = (int)(blockIdx.x - row * a.parts);
+  const int64_t items = a.T * a.parts;
+  const uint32_t full0 = smem_u32(sm.full), empty0 = smem_u32(sm.empty), ring0 = smem_u32(ring);
+  const uint32_t free0 = smem_u32(sm.free);
+  volatile int* abort = &sm.abort;
+  // a wait that gives up records the error and stops every later wait of the CTA
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (umma::mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (umma::mbar_wait(bar, parity)) return true;
+    ls_report(a.err, LS_DEVERR_TIMEOUT);
+    *abort = 1;
+    return false;
+  };
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      umma::mbar_init(full0 + 8 * s, 1);
+      umma::mbar_init(empty0 + 8 * s, kWarps);
+    }
+    umma::mbar_init(free0, 1);
+    umma::mbar_init(free0 + 8, 1);
+    sm.abort = 0;
+    sm.cands[0] = sm.cands[1] = 0;
+    umma::fence_barrier_init();
+  }
+  __syncthreads();
   // the merge may be launched: its blocks wait for this grid before they read from it
   if (a.parts > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (padding_row(a, row, part == 0 && warp == 0, lane)) return;
-  const E* zr = static_cast<const E*>(a.logits) + row * a.ld;
-  // groups of 32 bytes by address; the first and the last one may stick out of the row
-  const int lead = (int)((reinterpret_cast<uintptr_t>(zr) & 31) / sizeof(E));
-  const int64_t all = ((int64_t)lead + a.V + G - 1) / G;
-  const int g0 = (int)(all * part / a.parts), ng = (int)(all * (part + 1) / a.parts) - g0;
-  const E* base = zr - lead + (int64_t)g0 * G;  // of the part's first group
-  const float c = a.c;
-  float m = -INFINITY, bestv = -INFINITY;
-  int bestg = -1;
-  float2 s = {0.f, 0.f}, e = {0.f, 0.f};
-  auto add = [&](const float* x, int g) {
-    float mx = fmax3(x[0], x[1], x[2]);
+
+  umma::RingPos<kStages> rp;
+  if (warp == kWarps) {
+    // ---- producer
+    if (lane == 0) {
+      int issued = 0;
+      int32_t y = Item<E>::target(a, blockIdx.x);
+      for (int64_t item = blockIdx.x; item < items && !*abort; item += gridDim.x) {
+        const Item<E> it(a, item, y);
+        y = Item<E>::target(a, item + gridDim.x);
+        const int n = it.chunks();
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(it.at(it.in0));
+        for (int k = 0; k < n; ++k) {
+          const int left = (it.in1 - it.in0 - k * kThreads) * kGroupBytes;
+          const uint32_t bytes = left < kChunkBytes ? left : kChunkBytes;
+          if (!wait(empty0 + 8 * rp.stage, rp.phase ^ 1u)) break;
+          umma::mbar_expect_tx(full0 + 8 * rp.stage, bytes);
+          bulk_load(ring0 + rp.stage * kChunkBytes, src + (int64_t)k * kChunkBytes, bytes,
+                    full0 + 8 * rp.stage);
+          ++issued;
+          rp.advance();
+        }
+      }
+      // no copy may still be landing when the CTA exits
+      for (int s = 0; s < kStages && s < issued; ++s) {
+        rp.stage = rp.stage == 0 ? kStages - 1 : rp.stage - 1;
+        if (rp.stage == kStages - 1) rp.phase ^= 1u;
+        umma::mbar_wait(full0 + 8 * rp.stage, rp.phase);
+      }
+    }
+    return;
+  }
+
+  int q = 0;
+  if (warp == kWarps + 1) {
+    // ---- outputs
+    int32_t y = Item<E>::target(a, blockIdx.x);
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+      const Item<E> it(a, item, y);
+      y = Item<E>::target(a, item + gridDim.x);
+      if (it.pad) {
+        if (it.part == 0) padding_row(a, it.row, lane);
+        continue;
+      }
+      float zy = 0.f;
+      bool has_y = false;
+      if (lane == 0 && a.parts == 1) has_y = target_logit<E>(a, it.row, &zy);
+      const int par = q & 1;
+      ++q;
+      take_over(par);
+      Stat st = {sm.m[par][lane], 0.f, 0.f};
 #pragma unroll
-    for (int i = 3; i + 1 < G; i += 2) mx = fmax3(mx, x[i], x[i + 1]);
-    mx = fmaxf(mx, x[G - 1]);
-    if (kTop) {
-      sm.gmax[g] = mx;
+      for (int i = 1; i < kWarps; ++i) st.m = fmaxf(st.m, sm.m[par][lane + 32 * i]);
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        const int t = lane + 32 * i;
+        const Stat x = move(Stat{sm.m[par][t], sm.s[par][t], sm.e[par][t]}, st.m, a.c);
+        st.s += x.s;
+        st.e += x.e;
+      }
+      st = warp_stat(st, a.c);
+      u64 list = 0;
+      if (kTop) {
+        list = pick<E>(sm, it, a, par, lane);
+        if (lane == 0) sm.cands[par] = 0;
+      }
+      __syncwarp();
+      if (lane == 0) umma::mbar_arrive(free0 + 8 * par);
+      if (a.parts > 1) {
+        const int64_t at = it.row * a.parts + it.part;
+        if (lane == 0) *reinterpret_cast<float4*>(a.part_stat + 4 * at) = make_float4(st.m, st.s, st.e, 0.f);
+        if (kTop) a.part_top[at * 32 + lane] = list;
+      } else {
+        double lse = 0.0;
+        if (lane == 0) lse = finish_row(a, st, it.row, has_y, zy);
+        if (kTop) write_top(a, it.row, list, __shfl_sync(0xffffffffu, lse, 0), lane);
+      }
+    }
+    return;
+  }
+
+  // ---- consumers
+  const float c = a.c;
+  const int mine = tid * kGroupBytes + ((tid >> 1) & 3) * 16;  // of a chunk
+  int32_t y = Item<E>::target(a, blockIdx.x);
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const Item<E> it(a, item, y);
+    y = Item<E>::target(a, item + gridDim.x);
+    if (it.pad) continue;
+    Sums<E> sums(c);
+    float bestv = -INFINITY, second = -INFINITY;  // the largest of this thread's groups, the next
+    int bestg = -1;
+    auto best = [&](int g, float mx) {
+      put_max<E>(sm, g, mx);
+      second = fmaxf(second, fminf(mx, bestv));
       if (mx > bestv || bestg < 0) {
         bestv = mx;
         bestg = g;
       }
-    }
-    if (mx > m) {
-      if (m != -INFINITY) {
-        const float d = (m - mx) * c, f = fast_exp2(d), dd = floor_exp(d);
-        e.x = (e.x + s.x * dd) * f;
-        e.y = (e.y + s.y * dd) * f;
-        s.x *= f;
-        s.y *= f;
-      }
-      m = mx;
-    }
-    const float nm = m == -INFINITY ? 0.f : -m;
-    const float2 c2 = make_float2(c, c), b = make_float2(nm, nm);
+    };
+    auto edge = [&](int g) {  // a group that sticks out of the row
+      uint4 u[4];
+      it.template load<4>(a.V, g, 0, u);
+      sums.template add<4>(u);
+      if (kTop) best(g, R::max_of(u));
+    };
+    if (tid == 0 && it.in0 > 0) edge(0);
+    // a thread's 64 bytes of every chunk, in an order that keeps eight threads' loads apart; the
+    // chunk is released as soon as they are in registers
+    const int n = it.chunks();
+#pragma unroll 1
+    for (int k = 0; k < n; ++k) {
+      uint4 u[4];
+      const int g = it.in0 + k * kThreads + tid;
+      const bool has = wait(full0 + 8 * rp.stage, rp.phase) && g < it.in1;
+      const uint8_t* chunk = ring + rp.stage * kChunkBytes;
 #pragma unroll
-    for (int i = 0; i < G; i += 2) {
-      float2 t = __fmul2_rn(__fadd2_rn(make_float2(x[i], x[i + 1]), b), c2);
-      t.x = floor_exp(t.x);
-      t.y = floor_exp(t.y);
-      const float2 p = make_float2(fast_exp2(t.x), fast_exp2(t.y));
-      s = __fadd2_rn(s, p);
-      e = __ffma2_rn(p, t, e);
-    }
-  };
-  auto edge = [&](int g) {  // a group that sticks out of the row
-    float x[G];
-#pragma unroll
-    for (int i = 0; i < G; ++i) {
-      const int64_t at = (int64_t)(g0 + g) * G + i - lead;
-      x[i] = at >= 0 && at < a.V ? R::load(zr + at) : -INFINITY;
-    }
-    add(x, g);
-  };
-  const bool cut0 = g0 == 0 && lead > 0, cut1 = part == a.parts - 1 && (lead + (int64_t)a.V) % G != 0;
-  const int in0 = cut0 ? 1 : 0, in1 = ng - (cut1 ? 1 : 0);
-  constexpr int kUnroll = 2;
-  for (int gg = tid; gg < ng; gg += kUnroll * kThreads) {
-    uint4 u[kUnroll][2];
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const int g = gg + k * kThreads;
-      if (g >= in0 && g < in1) {
-        const uint4* p = reinterpret_cast<const uint4*>(base + (int64_t)g * G);
-        u[k][0] = __ldcs(p);
-        u[k][1] = __ldcs(p + 1);
+      for (int v = 0; v < 4; ++v) u[v] = *reinterpret_cast<const uint4*>(chunk + (mine ^ (16 * v)));
+      __syncwarp();
+      if (lane == 0) umma::mbar_arrive(empty0 + 8 * rp.stage);
+      rp.advance();
+      if (has) {
+        sums.template add<4>(u);
+        if (kTop) best(g, R::max_of(u));
       }
     }
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const int g = gg + k * kThreads;
-      if (g >= in0 && g < in1) {
-        float x[G];
-        R::unpack(u[k][0], x);
-        R::unpack(u[k][1], x + H);
-        add(x, g);
-      } else if (g < ng) {
-        edge(g);
+    if (tid == kThreads - 1 && it.in1 < it.ng) edge(it.ng - 1);
+
+    // ---- the item's results, into buffers that the last warp is done with
+    const int par = q & 1;
+    if (q >= 2) wait(free0 + 8 * par, ((q >> 1) - 1) & 1);
+    ++q;
+    const Stat st = sums.stat();
+    sm.m[par][tid] = st.m;
+    sm.s[par][tid] = st.s;
+    sm.e[par][tid] = st.e;
+    if (!kTop) {
+      hand_over(par);
+      continue;
+    }
+    // Candidates.  The largest groups of every warp's threads, a few of each warp, make 32 or 64
+    // distinct ones, and the top-th of them the threshold: it takes the others of the same
+    // maximum along, down to the last place among them.  (With 32 for any top, 32 alternatives
+    // let three times as many logits through as with 64: one in twelve of the warps has two of
+    // its three largest below the rest.)
+    const int tops = a.top > kFewTops ? 64 : 32;
+    const int with = min((it.ng + 31) >> 5, kWarps);
+    const uint32_t largest = bestg < 0 ? 0u : order_of(bestv);
+    if (warp < with) {
+      uint32_t o = largest;
+      for (int i = warp; i < tops; i += with) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, o);
+        const uint32_t at = __reduce_min_sync(0xffffffffu, o == top ? (uint32_t)bestg : 0xffffffffu);
+        if (lane == 0) {
+          sm.tops[par][i] = top;
+          sm.topg[par][i] = top ? (int)at : -1;
+        }
+        if (o == top && (uint32_t)bestg == at) o = 0u;
       }
     }
-  }
-  Stat st = {m, s.x + s.y, e.x + e.y};
+    consumers_sync();
+    uint32_t floor_o;
+    int floor_g;
+    {
+      const uint32_t x = sm.tops[par][lane], x2 = tops > 32 ? sm.tops[par][lane + 32] : 0u;
+      const uint4* all = reinterpret_cast<const uint4*>(sm.tops[par]);
+      int above = 0, above2 = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    st = merge(st, Stat{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o),
-                        __shfl_xor_sync(0xffffffffu, st.e, o)}, c);
-  if (lane == 0) red[warp] = st;
-  if (kTop) sm.best[tid] = bestg < 0 ? 0ull : key_of(bestv, bestg);
-  __syncthreads();
-  if (warp != 0) return;
-  st = lane < kWarps ? red[lane] : Stat{-INFINITY, 0.f, 0.f};
+      for (int i = 0; i < 8; ++i) {
+        const uint4 y = all[i];
+        above += (y.x > x) + (y.y > x) + (y.z > x) + (y.w > x);
+      }
+      if (tops > 32) {
 #pragma unroll
-  for (int o = kWarps / 2; o > 0; o >>= 1)
-    st = merge(st, Stat{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o),
-                        __shfl_xor_sync(0xffffffffu, st.e, o)}, c);
-  st = Stat{__shfl_sync(0xffffffffu, st.m, 0), __shfl_sync(0xffffffffu, st.s, 0),
-            __shfl_sync(0xffffffffu, st.e, 0)};
-  u64 list = 0;
-  if (kTop) list = pick<E>(sm, zr, a.V, lead, g0, ng, a.top, lane);
-  if (a.parts > 1) {
-    const int64_t at = row * a.parts + part;
-    if (lane == 0) *reinterpret_cast<float4*>(a.part_stat + 4 * at) = make_float4(st.m, st.s, st.e, 0.f);
-    if (kTop) a.part_top[at * 32 + lane] = list;
-    return;
+        for (int i = 0; i < 8; ++i) {
+          const uint4 y = all[i], z = all[i + 8];
+          above2 += (y.x > x2) + (y.y > x2) + (y.z > x2) + (y.w > x2);
+          above2 += (z.x > x2) + (z.y > x2) + (z.z > x2) + (z.w > x2);
+          above += (z.x > x) + (z.y > x) + (z.z > x) + (z.w > x);
+        }
+      }
+      // the lowest of those with fewer than top above them
+      floor_o = __reduce_min_sync(0xffffffffu, min(above < a.top ? x : 0xffffffffu,
+                                                   tops > 32 && above2 < a.top ? x2 : 0xffffffffu));
+      floor_g = __reduce_max_sync(0xffffffffu, max(x == floor_o ? sm.topg[par][lane] : -1,
+                                                   tops > 32 && x2 == floor_o ? sm.topg[par][lane + 32] : -1));
+      if (floor_o == 0) floor_g = INT32_MAX;  // fewer groups than alternatives: all of them
+    }
+    if (tid == 0) {
+      sm.floor_o[par] = floor_o;
+      sm.floor_g[par] = floor_g;
+    }
+    auto reaches = [&](uint32_t o, int g) { return o > floor_o || (o == floor_o && g <= floor_g); };
+    if (bestg >= 0 && reaches(largest, bestg)) {
+      auto put = [&](int g) {
+        const int at = atomicAdd(&sm.cands[par], 1);
+        if (at < kCand) sm.cand[par][at] = (uint16_t)g;
+      };
+      if (order_of(second) < floor_o) {  // most threads that have one
+        put(bestg);
+      } else {
+        auto visit = [&](int g) {
+          if (reaches(order_of(group_max<E>(sm, g)), g)) put(g);
+        };
+        if (tid == 0 && it.in0 > 0) visit(0);
+        for (int g = it.in0 + tid; g < it.in1; g += kThreads) visit(g);
+        if (tid == kThreads - 1 && it.in1 < it.ng) visit(it.ng - 1);
+      }
+    }
+    hand_over(par);
   }
-  double lse = 0.0;
-  if (lane == 0) {
-    float zy = 0.f;
-    const bool has = target_logit<E>(a, row, &zy);
-    lse = finish_row(st, a.inv_tau, a.out, row, has, zy);
-  }
-  if (kTop) write_top(a.out, row, a.top, list, __shfl_sync(0xffffffffu, lse, 0), a.inv_tau, lane);
 }
 
-// Rows that were cut into parts: a block a row, its warps take the parts by turns.
+// Rows that were cut into parts: a block a row, its warps take the parts by turns and their
+// results meet in pairs.
 constexpr int kMergeWarps = 8;
 template <typename E, bool kTop>
 __global__ void __launch_bounds__(kMergeWarps * 32) logp_merge(const FwdArgs a) {
@@ -412,31 +780,49 @@ __global__ void __launch_bounds__(kMergeWarps * 32) logp_merge(const FwdArgs a) 
   __shared__ u64 lists[kMergeWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = blockIdx.x;
+  float zy = 0.f;
+  bool has_y = false;
+  if (threadIdx.x == 0 && !(a.targets && a.targets[row] == -1)) has_y = target_logit<E>(a, row, &zy);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (padding_row(a, row, false, lane)) return;
+  if (a.targets && a.targets[row] == -1) return;  // written by the row's first part
   Stat st = {-INFINITY, 0.f, 0.f};
   u64 list = 0;
-  for (int p = warp; p < a.parts; p += kMergeWarps) {
-    const int64_t at = row * a.parts + p;
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_stat + 4 * at));
-    st = merge(st, Stat{x.x, x.y, x.z}, a.c);
-    if (kTop) list = merge32(list, __ldcg(a.part_top + at * 32 + lane), lane);
+  for (int p0 = warp; p0 < a.parts; p0 += 32 * kMergeWarps) {  // a lane a part
+    const int p = p0 + lane * kMergeWarps;
+    Stat x = {-INFINITY, 0.f, 0.f};
+    if (p < a.parts) {
+      const float4 f = __ldcg(reinterpret_cast<const float4*>(a.part_stat + 4 * (row * a.parts + p)));
+      x = Stat{f.x, f.y, f.z};
+    }
+    st = merge(st, warp_stat(x, a.c), a.c);
+  }
+  if (kTop) {
+    constexpr int kBatch = 4;  // lists that are loaded together
+    for (int p0 = warp; p0 < a.parts; p0 += kBatch * kMergeWarps) {
+      u64 x[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int p = p0 + b * kMergeWarps;
+        x[b] = p < a.parts ? __ldcg(a.part_top + (row * a.parts + p) * 32 + lane) : 0ull;
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        if (p0 + b * kMergeWarps < a.parts) list = merge32(list, x[b], lane);
+    }
   }
   if (lane == 0) red[warp] = st;
-  if (kTop) lists[warp][lane] = list;
-  __syncthreads();
+#pragma unroll
+  for (int half = kMergeWarps / 2; half > 0; half >>= 1) {
+    if (kTop) lists[warp][lane] = list;
+    __syncthreads();
+    if (kTop && warp < half) list = merge32(list, lists[warp + half][lane], lane);
+    __syncthreads();
+  }
   if (warp != 0) return;
-  for (int w = 1; w < kMergeWarps; ++w) {
-    st = merge(st, red[w], a.c);
-    if (kTop) list = merge32(list, lists[w][lane], lane);
-  }
+  st = warp_stat(lane < kMergeWarps ? red[lane] : Stat{-INFINITY, 0.f, 0.f}, a.c);
   double lse = 0.0;
-  if (lane == 0) {
-    float zy = 0.f;
-    const bool has = target_logit<E>(a, row, &zy);
-    lse = finish_row(st, a.inv_tau, a.out, row, has, zy);
-  }
-  if (kTop) write_top(a.out, row, a.top, list, __shfl_sync(0xffffffffu, lse, 0), a.inv_tau, lane);
+  if (lane == 0) lse = finish_row(a, st, row, has_y, zy);
+  if (kTop) write_top(a, row, list, __shfl_sync(0xffffffffu, lse, 0), lane);
 }
 
 // ---------------------------------------------------------------- backward
@@ -480,9 +866,9 @@ struct RowGrad {
 };
 
 template <typename E>
-__global__ void __launch_bounds__(kThreads) logp_bwd(const BwdArgs a) {
+__global__ void __launch_bounds__(kBwdThreads) logp_bwd(const BwdArgs a) {
   using R = Row<E>;
-  constexpr int N = R::G / 2;  // values of 16 bytes
+  constexpr int N = R::N;
   __shared__ float s_total;
   __shared__ int32_t special[33];  // the target and the alternatives
   __shared__ float special_z[33], special_g[33];
@@ -540,16 +926,16 @@ __global__ void __launch_bounds__(kThreads) logp_bwd(const BwdArgs a) {
   const bool zero = pad;
   const bool same = ((reinterpret_cast<uintptr_t>(gr) - reinterpret_cast<uintptr_t>(zr)) & 15) == 0;
   constexpr int kUnroll = 4;
-  for (int64_t i0 = v0 + tid; i0 < v1; i0 += kUnroll * kThreads) {
+  for (int64_t i0 = v0 + tid; i0 < v1; i0 += kUnroll * kBwdThreads) {
     uint4 u[kUnroll];
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
-      const int64_t i = i0 + k * kThreads, at = i * N - lead;
+      const int64_t i = i0 + k * kBwdThreads, at = i * N - lead;
       if (i < v1 && at >= 0 && at + N <= a.V && !zero) u[k] = __ldcs(reinterpret_cast<const uint4*>(zr + at));
     }
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
-      const int64_t i = i0 + k * kThreads, at = i * N - lead;
+      const int64_t i = i0 + k * kBwdThreads, at = i * N - lead;
       if (i >= v1) continue;
       float x[N];
       const bool whole = at >= 0 && at + N <= a.V;
@@ -599,16 +985,16 @@ __global__ void __launch_bounds__(kThreads) logp_bwd(const BwdArgs a) {
 
 namespace {
 int groups_of(bool is_bf16, int V) {  // of a row that begins inside a group
-  const int G = is_bf16 ? 16 : 8;
+  const int G = is_bf16 ? 32 : 16;
   return (int)(((int64_t)V + G - 1 + G - 1) / G);
 }
 }  // namespace
 
 // Parts of a row: as many as its group maxima take blocks of shared memory, and with few rows
-// as many as make a block for every SM, of a group a thread at least.
+// as many as make an item for every SM, of a chunk at least.
 int ls_token_logp_parts(bool is_bf16, int64_t T, int V, int top, int sms) {
-  const int64_t groups = groups_of(is_bf16, V);
-  int64_t parts = top > 0 ? (groups + kMaxGroups - 1) / kMaxGroups : 1;
+  const int64_t groups = groups_of(is_bf16, V), room = kGmaxBytes / (is_bf16 ? 2 : 4);
+  int64_t parts = top > 0 ? (groups + room - 1) / room : 1;
   if (T > 0 && T * parts < sms) {
     int64_t more = sms / T;
     const int64_t most = (groups + kThreads - 1) / kThreads;
@@ -623,15 +1009,15 @@ size_t ls_token_logp_ws_bytes(int64_t T, int parts) {
 
 namespace {
 template <typename E, bool kTop>
-cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t st) {
-  const size_t smem = kTop ? sizeof(TopSmem) : 0;
-  if (kTop) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(logp_fwd<E, kTop>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  logp_fwd<E, kTop><<<(unsigned)(a.T * a.parts), kThreads, smem, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+cudaError_t launch_fwd(const FwdArgs& a, int sms, cudaStream_t st) {
+  // without alternatives nothing behind `red` is used
+  const size_t smem = Cfg<kTop>::kStages * kChunkBytes + (kTop ? sizeof(FwdSmem) : offsetof(FwdSmem, floor_o));
+  cudaError_t e =
+      cudaFuncSetAttribute(logp_fwd<E, kTop>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int64_t items = a.T * a.parts, grid = items < 2 * sms ? items : 2 * sms;
+  logp_fwd<E, kTop><<<(unsigned)grid, kCtaThreads, smem, st>>>(a);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   ls_note_launch();
   if (a.parts == 1) return e;
@@ -650,7 +1036,7 @@ cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t st) {
 }
 }  // namespace
 
-cudaError_t ls_launch_token_logp_fwd(const LsTokenLogpArgs& b, int parts, cudaStream_t st) {
+cudaError_t ls_launch_token_logp_fwd(const LsTokenLogpArgs& b, int parts, int sms, cudaStream_t st) {
   FwdArgs a{};
   a.logits = b.logits;
   a.T = b.T;
@@ -659,15 +1045,16 @@ cudaError_t ls_launch_token_logp_fwd(const LsTokenLogpArgs& b, int parts, cudaSt
   a.top = b.top;
   a.parts = parts;
   a.targets = b.targets;
-  a.c = (float)(kLog2ed / (double)b.temperature);
   a.inv_tau = 1.0 / (double)b.temperature;
+  a.c = (float)(kLog2ed * a.inv_tau);
+  a.c_off = ((double)a.c - kLog2ed * a.inv_tau) / (double)a.c;
   a.out = {b.logp, b.lse, b.entropy, b.top_logp, b.top_ids};
   a.part_top = static_cast<u64*>(b.workspace);
   a.part_stat = reinterpret_cast<float*>(a.part_top + (size_t)b.T * parts * 32);
   a.err = b.err;
   if (b.is_bf16)
-    return b.top > 0 ? launch_fwd<__nv_bfloat16, true>(a, st) : launch_fwd<__nv_bfloat16, false>(a, st);
-  return b.top > 0 ? launch_fwd<float, true>(a, st) : launch_fwd<float, false>(a, st);
+    return b.top > 0 ? launch_fwd<__nv_bfloat16, true>(a, sms, st) : launch_fwd<__nv_bfloat16, false>(a, sms, st);
+  return b.top > 0 ? launch_fwd<float, true>(a, sms, st) : launch_fwd<float, false>(a, sms, st);
 }
 
 // Parts of about 64 KB, smaller ones when there are few rows.
@@ -677,7 +1064,7 @@ int64_t ls_token_logp_bwd_parts(const LsTokenLogpBwdArgs& b, int sms) {
   int64_t parts = (vecs + 4095) / 4096;
   if (b.T * parts < 2 * sms) {
     parts = (2 * sms + b.T - 1) / b.T;
-    const int64_t most = (vecs + kThreads - 1) / kThreads;
+    const int64_t most = (vecs + kBwdThreads - 1) / kBwdThreads;
     if (parts > most) parts = most;
   }
   return parts;
@@ -706,9 +1093,9 @@ cudaError_t ls_launch_token_logp_bwd(const LsTokenLogpBwdArgs& b, int sms, cudaS
   const int64_t parts = ls_token_logp_bwd_parts(b, sms);
   a.parts = (int)parts;
   if (b.is_bf16)
-    logp_bwd<__nv_bfloat16><<<(unsigned)(a.T * parts), kThreads, 0, st>>>(a);
+    logp_bwd<__nv_bfloat16><<<(unsigned)(a.T * parts), kBwdThreads, 0, st>>>(a);
   else
-    logp_bwd<float><<<(unsigned)(a.T * parts), kThreads, 0, st>>>(a);
+    logp_bwd<float><<<(unsigned)(a.T * parts), kBwdThreads, 0, st>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) ls_note_launch();
   return e;

@@ -148,8 +148,13 @@ def test_rows_that_are_no_numbers(cuda, T):
     z[2] = -math.inf
     ref = api.token_logp_fwd(z[3:].clone(), y[3:].clone(), top=9)
     out = api.token_logp_fwd(z, y, top=9)
-    for a, b in zip(out, ref):
-        assert torch.equal(a[3:], b) or torch.allclose(a[3:], b, rtol=1e-6)
+    # The others are what they are without these.  The copy's rows begin at other parts of a
+    # 64-byte group, so their sums are taken in another order: each result is within its bound of
+    # the formula's, and the two within twice that of one another.
+    _, _, _, e_lse, e_h = ro.stat_bounds(f64(z[3:]), 1.0)
+    for k, (a, b) in enumerate(zip(out, ref)):
+        e = (e_h if k == 2 else e_lse).reshape(-1, *[1] * (b.dim() - 1)) + ro.U32 * np.abs(f64(b))
+        assert torch.equal(a[3:], b) if k == 4 else (np.abs(f64(a[3:]) - f64(b)) <= 2 * e).all()
     assert torch.isnan(out[0][:3]).all() and torch.isnan(out[2][:3]).all()
     ids = out[4][:3]
     assert bool(((ids >= -1) & (ids < 5000)).all())
