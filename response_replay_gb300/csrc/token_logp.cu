@@ -31,7 +31,7 @@ constexpr int kThreads = 384;  // consumers of the forward, a group of 64 bytes 
 constexpr int kWarps = kThreads / 32;
 constexpr int kGroupBytes = 64;
 constexpr int kGmaxBytes = 20480;  // group maxima of a part, of the logits' type
-constexpr int kBwdThreads = 512;
+constexpr int kBwdThreads = 256, kBwdCtas = 5;  // of the backward, and blocks an SM
 constexpr double kLn2d = 0.69314718055994530942;
 constexpr double kLog2ed = 1.4426950408889634074;
 
@@ -865,23 +865,44 @@ struct RowGrad {
   __device__ __forceinline__ float one(float z) const { return at(make_float2(z, z)).x; }
 };
 
+// A block takes a part of a row; its first loads go out before the row's scalars are there.
+// Bound by HBM: 4,096 rows of 151,936 bf16 values 368 us, all of the copy's rate.  (Five blocks
+// of 256 threads an SM and parts of 128 KB; with six and 64 KB 378 us, three of 512 422, two of
+// 512, whose scalars nothing hides, 448.)
+constexpr int kBwdVecs = 8192;
 template <typename E>
-__global__ void __launch_bounds__(kBwdThreads) logp_bwd(const BwdArgs a) {
+__global__ void __launch_bounds__(kBwdThreads, kBwdCtas) logp_bwd(const BwdArgs a) {
   using R = Row<E>;
   constexpr int N = R::N;
+  constexpr int kUnroll = 4;
   __shared__ float s_total;
   __shared__ int32_t special[33];  // the target and the alternatives
   __shared__ float special_z[33], special_g[33];
   const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x / a.parts;
+  const int64_t row = a.parts == 1 ? blockIdx.x : blockIdx.x / a.parts;
   const int part = (int)(blockIdx.x - row * a.parts);
   const E* zr = static_cast<const E*>(a.logits) + row * a.ld;
   E* gr = static_cast<E*>(a.dlogits) + row * a.dld;
   const int lead = (int)((reinterpret_cast<uintptr_t>(zr) & 15) / sizeof(E));
-  const int64_t all = ((int64_t)lead + a.V + N - 1) / N;
-  const int64_t v0 = all * part / a.parts, v1 = all * (part + 1) / a.parts;
-  const int32_t y = a.targets ? a.targets[row] : 0;
+  const int all = (int)(((int64_t)lead + a.V + N - 1) / N);
+  const int v0 = (int)((int64_t)all * part / a.parts), v1 = (int)((int64_t)all * (part + 1) / a.parts);
+  // vectors that lie wholly in the row
+  const int in0 = lead > 0 ? 1 : 0, in1 = (lead + a.V) / N;
+  const uint4* zv = reinterpret_cast<const uint4*>(zr - lead);
+  uint4 u[kUnroll];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int i = i0 + k * kBwdThreads;
+      if (i < v1 && i >= in0 && i < in1) u[k] = __ldcs(zv + i);
+    }
+  };
+  load(v0 + tid);
+  const int32_t y = a.targets ? __ldg(a.targets + row) : 0;
   const bool pad = a.targets && y == -1;
+  const float h = a.d_entropy && !pad ? __ldg(a.d_entropy + row) : 0.f;
+  const float lse = pad ? 0.f : __ldg(a.lse + row);
+  const float he = h != 0.f ? h * __ldg(a.entropy + row) : 0.f;
   // ---- the row's upstream: g at the target, a_j at the alternatives, their sum
   if (tid < 32) {
     const bool has = tid < a.top && !pad;
@@ -893,8 +914,10 @@ __global__ void __launch_bounds__(kBwdThreads) logp_bwd(const BwdArgs a) {
       g = NAN;
     }
     float sum = g;
+    if (a.top > 0) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
     special[1 + tid] = id;
     special_g[1 + tid] = g;
     if (id >= 0) special_z[1 + tid] = R::load(zr + id);
@@ -902,7 +925,7 @@ __global__ void __launch_bounds__(kBwdThreads) logp_bwd(const BwdArgs a) {
       float gy = 0.f;
       special[0] = -1;
       if (a.targets && !pad) {
-        gy = a.d_logp[row];
+        gy = a.d_logp ? a.d_logp[row] : 0.f;
         if ((uint32_t)y < (uint32_t)a.V) {
           special[0] = y;
           special_z[0] = R::load(zr + y);
@@ -917,44 +940,31 @@ __global__ void __launch_bounds__(kBwdThreads) logp_bwd(const BwdArgs a) {
   }
   __syncthreads();
   RowGrad<E> rg;
-  const float h = a.d_entropy && !pad ? a.d_entropy[row] : 0.f;
-  rg.lse = pad ? 0.f : a.lse[row];
+  rg.lse = lse;
   rg.hi = a.inv_hi;
   rg.lo = a.inv_lo;
-  rg.a = -(s_total + (h != 0.f ? h * a.entropy[row] : 0.f)) * a.inv_hi;
+  rg.a = -(s_total + he) * a.inv_hi;
   rg.b = -h * a.inv_hi;
-  const bool zero = pad;
   const bool same = ((reinterpret_cast<uintptr_t>(gr) - reinterpret_cast<uintptr_t>(zr)) & 15) == 0;
-  constexpr int kUnroll = 4;
-  for (int64_t i0 = v0 + tid; i0 < v1; i0 += kUnroll * kBwdThreads) {
-    uint4 u[kUnroll];
+  for (int i0 = v0 + tid; i0 < v1; i0 += kUnroll * kBwdThreads) {
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
-      const int64_t i = i0 + k * kBwdThreads, at = i * N - lead;
-      if (i < v1 && at >= 0 && at + N <= a.V && !zero) u[k] = __ldcs(reinterpret_cast<const uint4*>(zr + at));
-    }
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const int64_t i = i0 + k * kBwdThreads, at = i * N - lead;
+      const int i = i0 + k * kBwdThreads;
       if (i >= v1) continue;
       float x[N];
-      const bool whole = at >= 0 && at + N <= a.V;
-      if (zero) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) x[e] = 0.f;
+      const bool whole = i >= in0 && i < in1;
+      const int64_t at = (int64_t)i * N - lead;
+      if (whole) {
+        R::unpack(u[k], x);
       } else {
-        if (whole) {
-          R::unpack(u[k], x);
-        } else {
 #pragma unroll
-          for (int e = 0; e < N; ++e) x[e] = at + e >= 0 && at + e < a.V ? R::load(zr + at + e) : 0.f;
-        }
+        for (int e = 0; e < N; ++e) x[e] = at + e >= 0 && at + e < a.V ? R::load(zr + at + e) : 0.f;
+      }
 #pragma unroll
-        for (int e = 0; e < N; e += 2) {
-          const float2 g = rg.at(make_float2(x[e], x[e + 1]));
-          x[e] = g.x;
-          x[e + 1] = g.y;
-        }
+      for (int e = 0; e < N; e += 2) {
+        const float2 g = pad ? make_float2(0.f, 0.f) : rg.at(make_float2(x[e], x[e + 1]));
+        x[e] = g.x;
+        x[e + 1] = g.y;
       }
       if (whole && same) {
         __stcs(reinterpret_cast<uint4*>(gr + at), R::pack(x));
@@ -964,12 +974,13 @@ __global__ void __launch_bounds__(kBwdThreads) logp_bwd(const BwdArgs a) {
           if (at + e >= 0 && at + e < a.V) R::store(gr + at + e, x[e]);
       }
     }
+    load(i0 + kUnroll * kBwdThreads);
   }
   // ---- the target and the alternatives, over what the pass wrote there
   __syncthreads();
-  if (!zero && tid < 33 && special[tid] >= 0) {
+  if (!pad && tid < 33 && special[tid] >= 0) {
     const int32_t v = special[tid];
-    const int64_t i = ((int64_t)v + lead) / N;
+    const int i = (v + lead) / N;
     bool first = i >= v0 && i < v1;
     float g = 0.f;
     for (int j = 0; j < 33; ++j)
@@ -1057,11 +1068,11 @@ cudaError_t ls_launch_token_logp_fwd(const LsTokenLogpArgs& b, int parts, int sm
   return b.top > 0 ? launch_fwd<float, true>(a, sms, st) : launch_fwd<float, false>(a, sms, st);
 }
 
-// Parts of about 64 KB, smaller ones when there are few rows.
+// Parts of up to 128 KB, smaller ones when there are few rows.
 int64_t ls_token_logp_bwd_parts(const LsTokenLogpBwdArgs& b, int sms) {
   const int N = b.is_bf16 ? 8 : 4;
   const int64_t vecs = ((int64_t)b.V + N - 1) / N + 1;
-  int64_t parts = (vecs + 4095) / 4096;
+  int64_t parts = (vecs + kBwdVecs - 1) / kBwdVecs;
   if (b.T * parts < 2 * sms) {
     parts = (2 * sms + b.T - 1) / b.T;
     const int64_t most = (vecs + kBwdThreads - 1) / kBwdThreads;
