@@ -49,23 +49,16 @@
 // Tensor memory (512 columns): S_0 [0,128) S_1 [128,256) O [256,384) P_0 [384,448) P_1 [448,512).
 #include <math.h>
 
-#include "ls_device.cuh"
-#include "ls_internal.h"
-#include "ls_tmap.h"
-#include "ls_umma.cuh"
+#include "ls_decode.cuh"
 
 namespace {
 
 using namespace umma;
+using namespace decode;
 
-constexpr int kD = 128;
-constexpr int kTile = 128;
-constexpr int kTreeTokens = 128;
 constexpr int kRing = 3;  // K tiles, and V tiles, in shared memory
 constexpr int kThreads = 384;
 constexpr int kSoftmaxThreads = 256;
-constexpr uint32_t kTileBytes = kTile * kD * 2;
-constexpr uint32_t kHalfBytes = kTileBytes / 2;
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffK = kTileBytes;
 constexpr uint32_t kOffV = kOffK + kRing * kTileBytes;
@@ -76,12 +69,9 @@ constexpr int kHalfRows = kTile / 2;
 constexpr uint32_t kOffBar = kOffV + kRing * kTileBytes;
 constexpr uint32_t kOffMax = kOffBar + 512;       // [2][2][128] fp32: buffer, key half, row
 constexpr uint32_t kSmemBytes = kOffMax + 2 * 2 * kTile * 4;
-constexpr int kMaxBoxes = kTile / 16;  // a tile's pages at the smallest page size
 constexpr int kHalfKeys = kTile / 2;
 constexpr uint32_t kColO = 2 * kTile, kColP = 3 * kTile;  // tensor memory behind the S buffers
 constexpr int kSegTiles = 3;  // a segment's beginning and end take a CTA as long as so many tiles
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleLog2 = 8.0f;
 
 enum {
   B_K_FULL = 0,
@@ -102,57 +92,8 @@ enum {
 constexpr uint32_t kOffVars = kOffBar + B_COUNT * 8;
 static_assert(B_COUNT * 8 + 32 <= 512, "barrier area");
 
-struct TmapSet {
-  CUtensorMap kp, vp, kr, vr;
-};
-
-// A bounded wait that asks once without the suspend: most of the issuing warps' waits find
-// their phase complete.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
-  return mbar_try_wait(bar, parity) || mbar_wait(bar, parity);
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
-}
-
 __device__ __forceinline__ uint32_t bar_addr(uint32_t base, int i) { return base + kOffBar + 8 * i; }
 
-// A member's response keys: none for a member out of use (negative length); a length
-// past its row of the block table is cut (and reported by the main kernel).
-__device__ __forceinline__ int32_t clamp_len(const LsDecodeArgs& a, int32_t len) {
-  const long long room = (long long)a.max_blocks << a.r_ps_log2;
-  if (len < 0) return 0;
-  return len < room ? len : (int32_t)room;
-}
-// Row groups of the responses: a member's rows, or with a tree the rows of up to a.tpt of its
-// tokens (as many whole tokens as fit a row tile), group by group; a group walks the member's
-// keys like a member of its own.
-template <bool kTree>
-__device__ __forceinline__ int32_t groups_of(const LsDecodeArgs& a) {
-  return kTree ? a.M * a.rtm : a.M;
-}
-template <bool kTree>
-__device__ __forceinline__ int32_t member_of(const LsDecodeArgs& a, int32_t group) {
-  return kTree ? group / a.rtm : group;
-}
-// Drafted tokens of a member, the last of its n.
-__device__ __forceinline__ int32_t drafted_of(const LsDecodeArgs& a, int32_t m) {
-  return a.drafted ? min(max(__ldg(a.drafted + m), 0), a.n) : a.n;
-}
-// Keys that a row group meets: none when all of its tokens are padding.
-template <bool kTree>
-__device__ __forceinline__ int32_t group_len(const LsDecodeArgs& a, int32_t group) {
-  const int32_t m = member_of<kTree>(a, group);
-  const int32_t len = clamp_len(a, __ldg(a.lens + m));
-  if (!kTree) return len;
-  return (group - m * a.rtm + 1) * a.tpt <= a.n - drafted_of(a, m) ? 0 : len;
-}
-__device__ __forceinline__ int32_t tiles_of(int32_t len) {
-  return (int32_t)(((long long)len + kTile - 1) / kTile);
-}
 // Units of the cut: the keys of one source under one KV head weigh their tiles and, in front
 // of them, kSegTiles more.  (With tiles alone a CTA got up to 85 responses of one tile each
 // at 64 members of a few tokens over 262,139: 317 us, with 1 more 247, with 2 180, with 3
@@ -194,17 +135,16 @@ struct Cut {
 // One segment: `count` tiles from key `key0` of one source; rows of one row tile.
 struct Seg {
   bool resp;
-  int32_t kvh, m;       // KV head; row group (responses)
+  int32_t kvh, m;       // KV head; member (responses)
   int32_t item;         // KV head (prompt) or m * hkv + kvh
   int32_t key0, count;
   int32_t len;          // keys of the source
 };
 
-template <bool kTree>
 struct Walk {
   const LsDecodeArgs& a;
   int32_t p, p_end, r, r_end;
-  int32_t m, off;       // row group and unit within its KV heads' units
+  int32_t m, off;       // member and unit within its KV heads' units
   __device__ __forceinline__ Walk(const LsDecodeArgs& a_, const volatile int32_t* start, int32_t p0,
                                   int32_t p1, int32_t r0, int32_t r1)
       : a(a_), p(p0), p_end(p1), r(r0), r_end(r1), m(start[0]), off(start[1]) {}
@@ -221,13 +161,13 @@ struct Walk {
     }
     while (r < r_end) {
       int32_t len = 0, nt = 0, nu = 0;
-      for (; m < groups_of<kTree>(a); ++m, off = 0) {
-        len = group_len<kTree>(a, m);
+      for (; m < a.M; ++m, off = 0) {
+        len = clamp_len(a, __ldg(a.lens + m));
         nt = tiles_of(len);
         nu = units_of(nt);
         if (off < nu * a.hkv) break;
       }
-      if (m >= groups_of<kTree>(a)) return false;  // only when lengths changed under the kernel
+      if (m >= a.M) return false;  // only when lengths changed under the kernel
       const int32_t h = off / nu, x = off - h * nu, step = min(r_end - r, nu - x);
       r += step;
       off += step;
@@ -253,80 +193,17 @@ struct Walk {
 };
 
 // Query rows of a segment: row r of row tile rt is row rt x 128 + r of all (token, head of
-// the group) pairs against the prompt, row r of the row group's own against a response.
-// seg_token: the first token of a response segment's rows, among its member's.
-template <bool kTree>
-__device__ __forceinline__ int32_t seg_token(const LsDecodeArgs& a, const Seg& s) {
-  return kTree ? (s.m - member_of<kTree>(a, s.m) * a.rtm) * a.tpt : 0;
-}
-template <bool kTree>
+// the group) pairs against the prompt, row r of the member's own against a response.
 __device__ __forceinline__ int32_t seg_rows(const LsDecodeArgs& a, const Seg& s, int32_t rt) {
-  if (!s.resp) return min(a.M * a.n * a.g - rt * kTile, kTile);
-  return kTree ? min(a.n - seg_token<kTree>(a, s), a.tpt) * a.g : a.n * a.g;
+  return s.resp ? a.n * a.g : min(a.M * a.n * a.g - rt * kTile, kTile);
 }
 
-template <bool kTree>
 __device__ __forceinline__ bool whole_q(const LsDecodeArgs& a, const Seg& s, int32_t rt) {
-  return seg_rows<kTree>(a, s, rt) > kHalfRows;
+  return seg_rows(a, s, rt) > kHalfRows;
 }
 __device__ __forceinline__ uint32_t q_offset(bool whole, uint32_t seg) {
   return kOffQ + (whole ? 0u : (seg & 1) * kHalfRows * 128u);
 }
-
-// The loads of one ring (K or V) of a CTA, issued by one thread.  A tile's pages are looked
-// up while the last tile's loads are under way.  Whole-tile boxes (pages of 128 rows and
-// more) come with both 64-dim halves in one copy; smaller pages take two copies a page.
-struct Loader {
-  const void* map;              // of the segment's source
-  const int32_t* table;
-  int32_t len, key0, boxes, box_rows, ps_log2, pages, hkv, kvh, pool_rows;
-  int32_t page[kMaxBoxes];
-
-  template <bool kTree>
-  __device__ __forceinline__ void open(const LsDecodeArgs& a, const Seg& s, const void* prompt_map,
-                                       const void* resp_map) {
-    map = s.resp ? resp_map : prompt_map;
-    table = s.resp ? a.blocks + (int64_t)member_of<kTree>(a, s.m) * a.max_blocks : a.page_table;
-    ps_log2 = s.resp ? a.r_ps_log2 : a.ps_log2;
-    pages = s.resp ? a.r_num_pages : a.num_pages;
-    box_rows = min(1 << ps_log2, kTile);
-    boxes = kTile / box_rows;
-    pool_rows = (pages * a.hkv) << ps_log2;
-    hkv = a.hkv;
-    kvh = s.kvh;
-    len = s.len;
-    key0 = s.key0;
-    look_up();
-  }
-  __device__ __forceinline__ void look_up() {
-#pragma unroll
-    for (int x = 0; x < kMaxBoxes; ++x)
-      if (x < boxes && key0 + x * box_rows < len) page[x] = __ldg(table + ((key0 + x * box_rows) >> ps_log2));
-  }
-  // one tile to `dst`, counted on barrier `bar`; then the next tile's pages
-  __device__ __forceinline__ void load(uint32_t dst, uint32_t bar, bool more, uint32_t* err) {
-    mbar_expect_tx(bar, kTileBytes);
-#pragma unroll
-    for (int x = 0; x < kMaxBoxes; ++x) {
-      if (x >= boxes) break;
-      int32_t y = pool_rows;  // out of bounds: zero fill
-      if (key0 + x * box_rows < len) {
-        if ((uint32_t)page[x] < (uint32_t)pages)
-          y = ((page[x] * hkv + kvh) << ps_log2) + ((key0 + x * box_rows) & ((1 << ps_log2) - 1));
-        else
-          ls_report(err, LS_DEVERR_CHECK);
-      }
-      if (boxes == 1) {
-        tma_load_3d(dst, map, 0, y, 0, bar);
-      } else {
-        tma_load_2d(dst + x * box_rows * 128, map, 0, y, bar);
-        tma_load_2d(dst + kHalfBytes + x * box_rows * 128, map, 64, y, bar);
-      }
-    }
-    key0 += kTile;
-    if (more) look_up();
-  }
-};
 
 // Rows of a partial: prompt partials first, then the responses'.  (item + CTA in walk
 // order) numbers a CTA's segments uniquely: from one segment to the next of the whole
@@ -337,7 +214,7 @@ struct Loader {
 // of up to 8,192 tokens took 123 us where this takes 103.  Transposed by shuffles instead,
 // the group of 64 members below took 259 us for 246.)
 __host__ __device__ __forceinline__ int32_t resp_rows_of(const LsDecodeArgs& a) {
-  return (a.tpt * a.g + 7) & ~7;
+  return (a.n * a.g + 7) & ~7;
 }
 __device__ __forceinline__ int64_t prompt_row0(const LsDecodeArgs& a, int32_t h, int32_t col,
                                                int32_t rt) {
@@ -347,28 +224,8 @@ __device__ __forceinline__ int64_t resp_row0(const LsDecodeArgs& a, int64_t prom
                                              int32_t item, int32_t cta) {
   return prompt_rows + ((int64_t)item + cta) * resp_rows_of(a);
 }
-__device__ __forceinline__ float* part_at(const LsDecodeArgs& a, int64_t row) {
-  return a.part_o + (row >> 3) * (8 * kD) + (row & 7) * 4;  // values 4 c .. 4 c + 3 at 32 c
-}
 __host__ __device__ __forceinline__ int64_t prompt_rows_of(const LsDecodeArgs& a) {
   return a.nt > 0 ? ((int64_t)a.hkv + a.cols) * a.rts * kTile : 0;
-}
-
-// What a row of a tree may see of the 64 keys from key kb on: the member's context (the keys
-// before its drafted ones), and of the drafted ones those of its bits.  d: kb counted from the
-// key of the member's first row; pad: rows before the first drafted one.
-__device__ __forceinline__ uint64_t tree_window(const LsDecodeArgs& a, const uint32_t* bits, int32_t d,
-                                                int32_t pad) {
-  auto words = [&](int32_t at) {  // bits 32 at .. 32 at + 31 of the row
-    const int32_t lo = pad - 32 * at, hi = a.n - 32 * at;
-    uint32_t x = at >= 0 && at < a.words ? __ldg(bits + at) : 0u;
-    if (hi < 32) x &= hi > 0 ? (1u << hi) - 1 : 0u;
-    if (lo > 0) x |= lo < 32 ? (1u << lo) - 1 : 0xffffffffu;
-    return x;
-  };
-  const int32_t at = d >> 5, sh = d & 31;
-  const uint32_t w0 = words(at), w1 = words(at + 1), w2 = words(at + 2);
-  return (uint64_t)__funnelshift_r(w0, w1, sh) | (uint64_t)__funnelshift_r(w1, w2, sh) << 32;
 }
 
 template <bool kTree>
@@ -394,22 +251,15 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
   int32_t p0, p1, r0, r1;
   {
     int32_t* wsum = reinterpret_cast<int32_t*>(smem + kOffK);
-    const int32_t groups = groups_of<kTree>(a);
-    const int per = (groups + kThreads - 1) / kThreads;
+    const int per = (a.M + kThreads - 1) / kThreads;
     int32_t mine = 0;
     for (int i = 0; i < per; ++i) {
       const int m = tid * per + i;
-      if (m < groups) {
-        if (cta == 0) {
-          const int32_t member = member_of<kTree>(a, m), len = __ldg(a.lens + member);
-          bool bad = len > clamp_len(a, len);
-          if (kTree && a.drafted && len >= 0) {
-            const int32_t c = __ldg(a.drafted + member);
-            bad = bad || c < 0 || c > a.n || c > len;
-          }
-          if (bad) ls_report(a.err, LS_DEVERR_CHECK);
-        }
-        mine += units_of(tiles_of(group_len<kTree>(a, m)));
+      if (m < a.M) {
+        const int32_t len = __ldg(a.lens + m);
+        const int32_t cl = clamp_len(a, len);
+        if (cta == 0 && (kTree ? bad_member(a, m) : len > cl)) ls_report(a.err, LS_DEVERR_CHECK);
+        mine += units_of(tiles_of(cl));
       }
     }
     int32_t sum = mine;
@@ -436,7 +286,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     if (r0 < r1 && pre * a.hkv <= r0 && r0 < (pre + mine) * a.hkv) {
       for (int i = 0; i < per; ++i) {
         const int m = tid * per + i;
-        const int32_t nu = units_of(tiles_of(group_len<kTree>(a, m)));
+        const int32_t nu = units_of(tiles_of(clamp_len(a, __ldg(a.lens + m))));
         if (r0 < (pre + nu) * a.hkv) {
           start[0] = m;
           start[1] = r0 - pre * a.hkv;
@@ -478,7 +328,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     ls_report(a.err, LS_DEVERR_TIMEOUT);
     *abort_flag = 1;
   };
-  Walk<kTree> walk(a, start, p0, p1, r0, r1);
+  Walk walk(a, start, p0, p1, r0, r1);
   Seg s;
 
   if (warp == 0) {
@@ -491,7 +341,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
       Loader ld;
       bool ok = true;
       while (ok && walk.next(&s)) {
-        ld.open<kTree>(a, s, &tm.kp, &tm.kr);
+        ld.open(a, s.resp, s.m, s.kvh, s.key0, s.len, &tm.kp, &tm.kr);
         for (int32_t j = 0; j < s.count; ++j) {
           ok = wait_bar(bar_addr(sbase, B_K_EMPTY + ring.stage), ring.phase ^ 1) && !*abort_flag;
           if (!ok) {
@@ -522,10 +372,9 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     uint32_t fills = 0, aux_phase = 0, seg = 0;
     Loader ld;
     auto start_q = [&](uint32_t n_seg) {
-      const int rows = seg_rows<kTree>(a, s, rt);
-      const uint32_t buf = sbase + q_offset(whole_q<kTree>(a, s, rt), n_seg);
-      const int32_t row0 = s.resp ? (member_of<kTree>(a, s.m) * a.n + seg_token<kTree>(a, s)) * a.g
-                                  : rt * kTile;
+      const int rows = seg_rows(a, s, rt);
+      const uint32_t buf = sbase + q_offset(whole_q(a, s, rt), n_seg);
+      const int32_t row0 = s.resp ? s.m * a.n * a.g : rt * kTile;
       int32_t token = (row0 + (lane >> 4)) / a.g, head = (row0 + (lane >> 4)) - token * a.g;
       const int c = lane & 15;
       for (int r = lane >> 4; r < rows; r += 2) {
@@ -544,7 +393,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     bool ok = true, have = walk.next(&s);
     if (have) start_q(0);
     for (; ok && have; ++seg) {
-      if (lane == 0) ld.open<kTree>(a, s, &tm.vp, &tm.vr);
+      if (lane == 0) ld.open(a, s.resp, s.m, s.kvh, s.key0, s.len, &tm.vp, &tm.vr);
       uint32_t st = 0;
       for (int32_t j = 0; j < s.count; ++j) {
         st = ring.stage;
@@ -561,13 +410,13 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
       }
       if (!ok) break;
       const int32_t left = s.len - (s.key0 + (s.count - 1) * kTile);
-      const bool whole = whole_q<kTree>(a, s, rt);
+      const bool whole = whole_q(a, s, rt);
       have = walk.next(&s);
       if (have) {
         // the next segment's Q: its half of the Q tile was the segment before's, and a whole
         // tile also waits for this one's last S
         if (seg > 0) ok = wait_bar(bar_addr(sbase, B_Q_EMPTY + ((seg - 1) & 1)), ((seg - 1) >> 1) & 1);
-        if (ok && (whole || whole_q<kTree>(a, s, rt)))
+        if (ok && (whole || whole_q(a, s, rt)))
           ok = wait_bar(bar_addr(sbase, B_Q_EMPTY + (seg & 1)), (seg >> 1) & 1);
         if (!ok) break;
         start_q(seg + 1);
@@ -601,7 +450,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
       bool ok = true;
       for (; ok && walk.next(&s); ++seg) {
         ok = wait_bar(bar_addr(sbase, B_Q_FULL + (seg & 1)), (seg >> 1) & 1);
-        const uint32_t dq = sdesc_lo(sbase + q_offset(whole_q<kTree>(a, s, rt), seg), 16);
+        const uint32_t dq = sdesc_lo(sbase + q_offset(whole_q(a, s, rt), seg), 16);
         for (int32_t j = 0; ok && j < s.count; ++j, ++n) {
           ok = wait_bar(bar_addr(sbase, B_K_FULL + ring.stage), ring.phase);
           if (ok && n >= 2) ok = wait_bar(bar_addr(sbase, B_S_EMPTY + (n & 1)), ((n - 2) >> 1) & 1);
@@ -676,7 +525,7 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
     };
     bool ok = true;
     while (ok && walk.next(&s)) {
-      const int32_t rows = seg_rows<kTree>(a, s, rt);
+      const int32_t rows = seg_rows(a, s, rt);
       const bool idle = quad * 32 >= rows;  // the whole warp is padding
       // keys of the half tile from its first one on that this row sees
       int32_t lim = (s.resp && !kTree ? min(s.len, s.len - a.n + 1 + row / a.g) : s.len) - s.key0 -
@@ -685,10 +534,9 @@ decode_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ L
       int32_t pad = 0;
       const uint32_t* bits = nullptr;
       if (kTree && s.resp) {
-        const int32_t member = member_of<kTree>(a, s.m);
-        pad = a.n - drafted_of(a, member);
+        pad = a.n - drafted_of(a, s.m);
         lim -= a.n - pad;
-        bits = a.visible + ((int64_t)member * a.n + min(seg_token<kTree>(a, s) + row / a.g, a.n - 1)) * a.words;
+        bits = a.visible + ((int64_t)s.m * a.n + min(row / a.g, a.n - 1)) * a.words;
       }
       float m = -INFINITY, l = 0.f, lcomp = 0.f;
       for (int32_t j = 0; j < s.count; ++j, ++n, lim -= kTile) {
@@ -865,8 +713,8 @@ decode_combine(const __grid_constant__ LsDecodeArgs a) {
   const int32_t octets = (a.g + 7) >> 3, group = (blockIdx.x >> 2) / octets;
   const int32_t head0 = 8 * ((blockIdx.x >> 2) - group * octets), col0 = 32 * (blockIdx.x & 3);
   const int32_t token = group / a.hkv, kvh = group - token * a.hkv, m = token / a.n;
-  const int32_t len = __ldg(a.lens + m), at = token - m * a.n;  // token of the member
-  if (len < 0 || (kTree && at < a.n - drafted_of(a, m))) {
+  const int32_t len = __ldg(a.lens + m);
+  if (len < 0 || (kTree && token - m * a.n < a.n - drafted_of(a, m))) {
     // A member out of use, or a token that is padding: its rows stay as they were.  Its blocks wait all the same: the
     // stream goes on when this grid ends, and with every member out of use nothing else
     // would hold it back until the main kernel has ended.
@@ -874,12 +722,11 @@ decode_combine(const __grid_constant__ LsDecodeArgs a) {
     return;
   }
   const int32_t nt = tiles_of(clamp_len(a, len));
-  const int32_t own = kTree ? m * a.rtm + at / a.tpt : m;  // the token's row group
   int32_t tot = 0, pre = 0;
-  for (int i = tid; i < groups_of<kTree>(a); i += kCombineThreads) {
-    const int32_t x = units_of(tiles_of(group_len<kTree>(a, i)));
+  for (int i = tid; i < a.M; i += kCombineThreads) {
+    const int32_t x = units_of(tiles_of(clamp_len(a, __ldg(a.lens + i))));
     tot += x;
-    if (i < own) pre += x;
+    if (i < m) pre += x;
   }
   tot = __reduce_add_sync(0xffffffffu, tot);
   pre = __reduce_add_sync(0xffffffffu, pre);
@@ -930,10 +777,9 @@ decode_combine(const __grid_constant__ LsDecodeArgs a) {
   const int32_t np = all[0], count = np + all[1];
   // a lane's head (behind the last one: that one again): row of all rows (token, head of the
   // group) against the prompt, row of the member's own
-  const int32_t grow = token * a.g + min(head0 + (lane & 7), a.g - 1);
-  const int32_t mrow = grow - (m * a.n + (kTree ? (own - m * a.rtm) * a.tpt : 0)) * a.g;
+  const int32_t grow = token * a.g + min(head0 + (lane & 7), a.g - 1), mrow = grow - m * a.n * a.g;
   const int64_t prompt0 = prompt_row0(a, kvh, 0, grow / kTile) + grow % kTile;
-  const int64_t resp0 = resp_row0(a, prompt_rows_of(a), own * a.hkv + kvh, 0) + mrow;
+  const int64_t resp0 = resp_row0(a, prompt_rows_of(a), m * a.hkv + kvh, 0) + mrow;
   const int32_t resp_rows = resp_rows_of(a);
   auto part_row = [&](int k) {
     if (k < np) return prompt0 + (int64_t)from[0][k] * a.rts * kTile;
@@ -1011,11 +857,10 @@ decode_combine(const __grid_constant__ LsDecodeArgs a) {
 }  // namespace
 
 int ls_decode_row_tile() { return kTile; }
-int ls_decode_tree_tokens() { return kTreeTokens; }
 int ls_decode_seg_tiles() { return kSegTiles; }
 int64_t ls_decode_prompt_rows(const LsDecodeArgs& a) { return prompt_rows_of(a); }
 int64_t ls_decode_resp_rows(const LsDecodeArgs& a) {
-  return ((int64_t)a.M * a.rtm * a.hkv + (int64_t)a.cols * a.rts) * resp_rows_of(a);
+  return ((int64_t)a.M * a.hkv + (int64_t)a.cols * a.rts) * resp_rows_of(a);
 }
 
 namespace {
@@ -1023,19 +868,7 @@ namespace {
 template <bool kTree>
 cudaError_t launch(const LsDecodeArgs& a, cudaStream_t st) {
   TmapSet tm;
-  for (int src = 0; src < 2; ++src) {
-    // rows of 256 bytes; a whole-tile box takes both halves of its rows, half by half
-    const int ps = 1 << (src ? a.r_ps_log2 : a.ps_log2);
-    const uint64_t rows = (uint64_t)(src ? a.r_num_pages : a.num_pages) * a.hkv * ps;
-    const bool whole = ps >= kTile;
-    const uint64_t dims[3] = {whole ? 64u : (uint64_t)kD, rows, 2};
-    const uint64_t strides[2] = {(uint64_t)kD * 2, (uint64_t)kD};
-    const uint32_t box[3] = {64, (uint32_t)(ps < kTile ? ps : kTile), 2};
-    const int rank = whole ? 3 : 2;
-    if (!ls_make_tmap_bf16(src ? &tm.kr : &tm.kp, src ? a.rk_pool : a.k_pool, rank, dims, strides, box) ||
-        !ls_make_tmap_bf16(src ? &tm.vr : &tm.vp, src ? a.rv_pool : a.v_pool, rank, dims, strides, box))
-      return cudaErrorInvalidValue;
-  }
+  if (!make_tmaps(a, &tm)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(decode_attn_kernel<kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kSmemBytes);
   if (e != cudaSuccess) return e;

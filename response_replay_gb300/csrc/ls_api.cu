@@ -988,11 +988,13 @@ ls_status check_pool(const ls_page_pool* c) {
 }
 
 struct DecodeWs {
-  size_t part_o, part_lse, total;
+  size_t part_o, part_lse, plan, total;
 };
 
-// Geometry and workspace of a decode call (device pointers of q and the outputs aside).  With
-// a tree a member's rows may take several row tiles, of whole tokens each.
+constexpr int kTreeTokens = 128;  // most rows of a member with a tree
+
+// Geometry and workspace of a decode call (device pointers of q and the outputs aside).  Trees of
+// more rows than one tile a KV head go to a kernel of their own (plan is set then).
 ls_status decode_args(const ls_kv_cache* c, const ls_resp_cache* r, int n, int Hq, bool tree,
                       LsDecodeArgs* a, DecodeWs* w) {
   ls_status s = check_cache(c);
@@ -1010,18 +1012,16 @@ ls_status decode_args(const ls_kv_cache* c, const ls_resp_cache* r, int n, int H
     return LS_ERR_INVALID_ARG;
   const int tile = ls_decode_row_tile();
   const int g = Hq / c->num_kv_heads;
-  if (tree ? n > ls_decode_tree_tokens() || g > tile : (int64_t)n * g > tile) return LS_ERR_UNSUPPORTED;
-  const int tpt = tree && n > tile / g ? tile / g : n, rtm = (n + tpt - 1) / tpt;
+  if (tree ? n > kTreeTokens || g > tile : (int64_t)n * g > tile) return LS_ERR_UNSUPPORTED;
+  const int groups = ((int64_t)n * g + tile - 1) / tile;  // of a member's rows
   // tile, unit and key counts are 32-bit numbers
   if (c->num_tokens >= (1ll << 31) - 128 ||
       ((int64_t)r->max_blocks * r->pool.page_size / 128 + 1 + ls_decode_seg_tiles()) * r->members *
-              rtm * c->num_kv_heads >= (1ll << 31) ||
+              groups * c->num_kv_heads >= (1ll << 31) ||
       (c->num_tokens / 128 + 1 + ls_decode_seg_tiles()) * c->num_kv_heads >= (1ll << 31))
     return LS_ERR_UNSUPPORTED;
   *a = LsDecodeArgs{};
   a->g = g;
-  a->tpt = tpt;
-  a->rtm = rtm;
   a->words = (n + 31) / 32;
   DevInfo d;
   if ((s = dev_info(&d)) != LS_OK) return s;
@@ -1049,11 +1049,15 @@ ls_status decode_args(const ls_kv_cache* c, const ls_resp_cache* r, int n, int H
   a->rts = (int32_t)rts;
   a->cols = ctas / a->rts;
   a->err = d.err;
-  const size_t rows = (size_t)(ls_decode_prompt_rows(*a) + ls_decode_resp_rows(*a));
+  const bool large = tree && rts > 1;
+  if (large) a->cols = ctas;
+  const size_t rows = large ? (size_t)ls_tree_part_rows(*a)
+                            : (size_t)(ls_decode_prompt_rows(*a) + ls_decode_resp_rows(*a));
   if (rows >= (1ull << 31)) return LS_ERR_UNSUPPORTED;
   w->part_o = 0;
   w->part_lse = align256(rows * kHeadDim * 4);
-  w->total = align256(w->part_lse + rows * 4);
+  w->plan = align256(w->part_lse + rows * 4);
+  w->total = large ? align256(w->plan + ls_tree_plan_bytes()) : w->plan;
   return LS_OK;
 }
 
@@ -1254,6 +1258,10 @@ ls_status decode_attn(const ls_kv_cache* cache, const ls_resp_cache* resp, const
   a.lse = lse;
   a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.part_o);
   a.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.part_lse);
+  if (w.total > w.plan) {
+    a.plan = static_cast<char*>(workspace) + w.plan;
+    return from_cuda(ls_launch_tree_attn(a, (cudaStream_t)stream));
+  }
   return from_cuda(ls_launch_decode_attn(a, (cudaStream_t)stream));
 }
 
@@ -1402,7 +1410,7 @@ namespace {
 
 ls_status draft_args(const int32_t* lens, const int32_t* drafted, int members, int n, LsDraftArgs* a) {
   if (members < 0 || n < 1) return LS_ERR_INVALID_ARG;
-  if (members > 1024 || n > ls_decode_tree_tokens()) return LS_ERR_UNSUPPORTED;
+  if (members > 1024 || n > kTreeTokens) return LS_ERR_UNSUPPORTED;
   if ((members > 0 && !lens) || !aligned4(lens) || !aligned4(drafted)) return LS_ERR_INVALID_ARG;
   a->parents = nullptr;
   a->lens = lens;

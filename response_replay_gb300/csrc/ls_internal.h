@@ -278,7 +278,7 @@ struct LsDecodeArgs {
   const uint32_t* visible;   // trees: [M][n][words] rows that a row sees, NULL: the newest tokens in a line
   const int32_t* drafted;    // trees: [M] drafted tokens, or NULL (n)
   int32_t words;             // 32-bit words of a row of `visible`
-  int32_t tpt, rtm;          // tokens of a row group and row groups of a member (n and 1 without a tree)
+  void* plan;                // trees of more than a tile of rows: how the work is cut (workspace)
   int32_t rts, cols;         // row tiles of 128 (token, head) rows; columns of rts CTAs each
   int32_t nt;                // prompt tiles of one KV head
   const void* q;             // bf16 [M][n][hq][128]
@@ -290,12 +290,15 @@ struct LsDecodeArgs {
   uint32_t* err;
 };
 int ls_decode_row_tile();
-int ls_decode_tree_tokens();  // most tokens of a member with a tree
 int ls_decode_seg_tiles();  // tiles' worth of time that a segment of a response takes besides
 // Rows of partial results: slots x rows.
 int64_t ls_decode_prompt_rows(const LsDecodeArgs& a);
 int64_t ls_decode_resp_rows(const LsDecodeArgs& a);
 cudaError_t ls_launch_decode_attn(const LsDecodeArgs& a, cudaStream_t st);
+// The same for trees of more rows than one tile a KV head (tree_attn.cu); cols: CTAs.
+size_t ls_tree_plan_bytes();
+int64_t ls_tree_part_rows(const LsDecodeArgs& a);
+cudaError_t ls_launch_tree_attn(const LsDecodeArgs& a, cudaStream_t st);
 
 // Log probabilities of given tokens, entropies, top alternatives (token_logp.cu).
 struct LsTokenLogpArgs {

@@ -1,0 +1,827 @@
+// tree_attn.cu -- decode attention of drafted trees with more rows than one tile a KV head.
+//
+// The last drafted[m] of member m's n rows are its draft.  For such a row, query head h, KV
+// head h / g:
+//   s_j = scale <q, k_j> over the P prompt positions, the member's context (its keys before the
+//         draft) and the drafted keys whose bits are set for the row;
+//   lse = log sum_j exp(s_j);   o = sum_j exp(s_j - lse) v_j
+//
+// Work.  The rows (drafted token, head of the group) of all members that share a KV head, padding
+// left out, lie one behind the other and make pairs of row tiles of 128; a CTA takes a pair
+// through a run of key tiles of 128, so that a K/V tile in shared memory serves 256 rows, and
+// one tile's softmax runs beside the other's products.  A prompt item is a pair and one of S
+// equal strips of a KV head's prompt; items go round the first `cp` CTAs, pairs first, so the
+// CTAs of a round walk the same strips at the same time and a key tile comes from HBM about once.
+// The responses' key tiles (member by member, pair of its rows, KV head) are cut evenly over the
+// other CTAs.  cp and S are what makes the longer of the two shortest; every CTA works them out
+// from the lengths and counts on the device, so a captured graph follows them.  Every segment
+// leaves a partial (o, lse); tree_combine merges a row's partials by log-sum-exp.
+//
+// What bounds it.  256 rows meet a key tile of 64 KB for 4.2 MFLOP of each product: the tensor
+// core, then the softmax that feeds it.
+//
+// CTA (one per SM, 12 warps; the pipeline of replay_fwd_tc.cu):
+//   warp 0      TMA producer: K and V tiles, page by page, into a ring of five.
+//   warps 1, 2  issue S_t = Q_t K^T and O_t += P_t V of tile A and tile B, one thread each; the
+//               tiles stay half a period apart.
+//   warp 3      the segments' Q rows (gathered by token and head); clears V rows behind a
+//               sequence's end (stale page contents, even NaN, would survive a zero weight).
+//   warps 4-7   softmax of tile A, warps 8-11 of tile B: a thread a row.
+// Tensor memory (512 columns): S_A [0,128) S_B [128,256) O_A [256,384) O_B [384,512); P_t
+// overlays the first 64 columns of S_t.
+#include "ls_decode.cuh"
+
+namespace {
+
+using namespace umma;
+using namespace decode;
+
+constexpr int kPair = 2 * kTile;
+constexpr int kStages = 5;
+constexpr int kThreads = 384;
+constexpr int kWarps = kThreads / 32;
+// 384 x 168 registers at launch; 128 x 96 + 256 x 200 = 63,488 of the 64,512
+constexpr int kRegsLaunch = 168, kRegsControl = 96, kRegsSoftmax = 200;
+static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
+constexpr uint32_t kOffQ = 0;  // Q_A, Q_B
+constexpr uint32_t kOffRing = 2 * kTileBytes;
+constexpr uint32_t kOffBar = kOffRing + kStages * kTileBytes;
+constexpr int kMaxMembers = 1024;
+constexpr int kSegTiles = 3;  // a segment's beginning and end take a CTA as long as so many tiles
+constexpr int kRounds = 3;    // of prompt items that are tried
+
+enum {
+  B_KV_FULL = 0,
+  B_KV_EMPTY = B_KV_FULL + kStages,
+  B_AUX = B_KV_EMPTY + kStages,      // a ragged V tile has landed, its tail not yet cleared
+  B_Q_FULL = B_AUX + kStages,
+  B_Q_EMPTY,
+  B_S_FULL,                  // 2
+  B_P_FULL = B_S_FULL + 2,   // 4: tile t, key half hf at 2 t + hf
+  B_O_DONE = B_P_FULL + 4,   // 2
+  B_DONE = B_O_DONE + 2,     // 2
+  B_PV_DONE = B_DONE + 2,    // 2: of segments with two tiles
+  B_COUNT = B_PV_DONE + 2
+};
+
+// How the work is cut, from the members' lengths and drafts.
+struct Plan {
+  int32_t tokens;   // drafted ones of all members
+  int32_t np;       // pairs of row tiles against the prompt
+  int32_t strips, strip;  // of the prompt, and a strip's tiles
+  int32_t cp;       // CTAs of the prompt
+  int32_t units, rcs;  // of the responses, and their CTAs: at least a unit each
+  int32_t m0, off0;  // response CTAs: the member its first unit lies with, and how far in
+};
+struct Vars {
+  uint32_t tmem;
+  int32_t abort;
+  Plan plan;
+  unsigned long long best;
+};
+constexpr uint32_t kOffVars = kOffBar + B_COUNT * 8;
+constexpr uint32_t kOffTok = kOffBar + 512;  // tokens before each member
+constexpr uint32_t kSmemBytes = kOffTok + (kMaxMembers + 2) * 2;
+static_assert(B_COUNT * 8 + sizeof(Vars) <= 512 && kOffVars % 8 == 0, "barrier area");
+static_assert(kSmemBytes <= 232448, "shared memory");
+
+__device__ __forceinline__ uint32_t bar_addr(uint32_t base, int i) { return base + kOffBar + 8 * i; }
+
+__device__ __forceinline__ int32_t drafted_tokens(const LsDecodeArgs& a, int32_t m) {
+  return __ldg(a.lens + m) < 0 ? 0 : drafted_of(a, m);
+}
+__device__ __forceinline__ int32_t pairs_of(const LsDecodeArgs& a, int32_t tokens) {
+  return (tokens * a.g + kPair - 1) / kPair;
+}
+// Units of a member: for every pair of its rows and KV head its key tiles and, in front of them,
+// kSegTiles more.
+__device__ __forceinline__ int32_t item_units(const LsDecodeArgs& a, int32_t m) {
+  return tiles_of(clamp_len(a, __ldg(a.lens + m))) + kSegTiles;
+}
+__device__ __forceinline__ int32_t member_units(const LsDecodeArgs& a, int32_t m) {
+  const int32_t c = drafted_tokens(a, m);
+  if (c == 0 || clamp_len(a, __ldg(a.lens + m)) == 0) return 0;
+  return pairs_of(a, c) * a.hkv * item_units(a, m);
+}
+__host__ __device__ __forceinline__ int32_t max_pairs(const LsDecodeArgs& a) {
+  return (a.n * a.g + kPair - 1) / kPair;
+}
+__host__ __device__ __forceinline__ int32_t resp_rows_of(const LsDecodeArgs& a) {
+  const int32_t r = (a.n * a.g + 7) & ~7;
+  return r < kPair ? r : kPair;
+}
+// Rows of partials: 256 a prompt item, then a row group's a response segment.  (Item + CTA
+// numbers a CTA's response segments uniquely: from one to the next of the whole sequence the
+// item, the CTA or both grow.)
+__host__ __device__ __forceinline__ int64_t prompt_rows_of(const LsDecodeArgs& a) {
+  if (a.nt == 0) return 0;
+  const int64_t np = ((int64_t)a.M * a.n * a.g + kPair - 1) / kPair * a.hkv;
+  const int64_t most = (int64_t)kRounds * a.cols;
+  return (np > most ? np : most) * kPair;
+}
+__device__ __forceinline__ int64_t resp_row0(const LsDecodeArgs& a, int32_t m, int32_t pair, int32_t h,
+                                             int32_t rc) {
+  const int32_t item = (m * max_pairs(a) + pair) * a.hkv + h;
+  return prompt_rows_of(a) + ((int64_t)item + rc) * resp_rows_of(a);
+}
+__device__ __forceinline__ int32_t unit_bound(int32_t units, int32_t rc, int32_t n) {
+  return (int32_t)((long long)units * rc / n);
+}
+
+// One segment: `count` key tiles from key0 on of one source, for `rows` rows of a pair.
+struct Seg {
+  bool resp;
+  int32_t kvh, m;       // KV head; member (responses)
+  int32_t row0, rows;   // the pair's first row (of all, or of the member's drafted ones)
+  int32_t key0, count, len;
+  int64_t part;         // first row of its partial
+  __device__ __forceinline__ bool two() const { return rows > kTile; }
+};
+
+struct Walk {
+  const LsDecodeArgs& a;
+  const volatile Plan& p;
+  int32_t at, end, m, off;
+  bool resp;
+  __device__ __forceinline__ Walk(const LsDecodeArgs& a_, const volatile Plan& p_, int32_t cta)
+      : a(a_), p(p_), m(0), off(0), resp(cta >= p_.cp) {
+    if (resp) {
+      const bool some = cta - p.cp < p.rcs;
+      at = some ? unit_bound(p.units, cta - p.cp, p.rcs) : 0;
+      end = some ? unit_bound(p.units, cta - p.cp + 1, p.rcs) : 0;
+      m = p.m0;
+      off = p.off0;
+    } else {
+      at = cta;
+      end = p.strips * p.np * a.hkv;
+    }
+  }
+  __device__ __forceinline__ bool next(Seg* s, int32_t cta) {
+    s->resp = resp;
+    if (!resp) {
+      if (at >= end) return false;
+      const int32_t q = at / p.np, pair = at - q * p.np, h = q / p.strips, strip = q - h * p.strips;
+      s->kvh = h;
+      s->m = 0;
+      s->row0 = pair * kPair;
+      s->rows = min(p.tokens * a.g - s->row0, kPair);
+      s->key0 = strip * p.strip * kTile;
+      s->count = min(p.strip, a.nt - strip * p.strip);
+      s->len = (int32_t)a.P;
+      s->part = (int64_t)at * kPair;
+      at += p.cp;
+      return true;
+    }
+    while (at < end) {
+      for (; m < a.M; ++m, off = 0)
+        if (off < member_units(a, m)) break;
+      if (m >= a.M) return false;  // only when lengths changed under the kernel
+      const int32_t iu = item_units(a, m), item = off / iu, x = off - item * iu, step = min(end - at, iu - x);
+      at += step;
+      off += step;
+      const int32_t first = max(x - kSegTiles, 0);  // its tiles among units x .. x + step - 1
+      s->count = x + step - kSegTiles - first;
+      if (s->count <= 0) continue;  // they are another CTA's
+      const int32_t pair = item / a.hkv;
+      s->kvh = item - pair * a.hkv;
+      s->m = m;
+      s->row0 = pair * kPair;
+      s->rows = min(drafted_tokens(a, m) * a.g - s->row0, kPair);
+      s->key0 = first * kTile;
+      s->len = clamp_len(a, __ldg(a.lens + m));
+      s->part = resp_row0(a, m, pair, s->kvh, cta - p.cp);
+      return true;
+    }
+    return false;
+  }
+};
+
+// The plan, by all threads of a CTA (scratch: 2 x kWarps ints).
+__device__ void make_plan(const LsDecodeArgs& a, Vars* v, uint16_t* tok, int32_t* scratch, int32_t cta) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (a.M + kThreads - 1) / kThreads;
+  int32_t tokens = 0, units = 0;
+  for (int i = 0; i < per; ++i) {
+    const int m = tid * per + i;
+    if (m >= a.M) break;
+    if (cta == 0 && bad_member(a, m)) ls_report(a.err, LS_DEVERR_CHECK);
+    tokens += drafted_tokens(a, m);
+    units += member_units(a, m);
+  }
+  int32_t ts = tokens, us = units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t x = __shfl_up_sync(0xffffffffu, ts, o), y = __shfl_up_sync(0xffffffffu, us, o);
+    if (lane >= o) {
+      ts += x;
+      us += y;
+    }
+  }
+  if (lane == 31) {
+    scratch[warp] = ts;
+    scratch[kWarps + warp] = us;
+  }
+  if (tid == 0) v->best = ~0ull;
+  __syncthreads();
+  int32_t all_tokens = 0, all_units = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    const int32_t x = scratch[i], y = scratch[kWarps + i];
+    if (i < warp) {
+      ts += x;
+      us += y;
+    }
+    all_tokens += x;
+    all_units += y;
+  }
+  int32_t before = ts - tokens;
+  for (int i = 0; i < per; ++i) {
+    const int m = tid * per + i;
+    if (m >= a.M) break;
+    tok[m] = (uint16_t)before;
+    before += drafted_tokens(a, m);
+  }
+  if (tid == 0) tok[a.M] = (uint16_t)all_tokens;
+  // ---- how many CTAs take the prompt, in how many rounds of how long strips
+  const int32_t np = (all_tokens * a.g + kPair - 1) / kPair, per_strip = np * a.hkv, ctas = a.cols;
+  const bool prompt = np > 0 && a.nt > 0;
+  const int32_t most = all_units > 0 ? ctas - 1 : ctas;
+  auto strip_of = [&](int32_t cp, int32_t rounds) {  // tiles of a strip
+    const int32_t s = min(a.nt, max(1, rounds * cp / per_strip));
+    return (a.nt + s - 1) / s;
+  };
+  if (prompt) {
+    for (int i = tid; i < most * kRounds; i += kThreads) {
+      const int32_t cp = 1 + i / kRounds, strip = strip_of(cp, 1 + i % kRounds);
+      const int32_t strips = (a.nt + strip - 1) / strip;
+      const long long tp = (long long)((strips * per_strip + cp - 1) / cp) * (strip + kSegTiles);
+      const long long tr = all_units > 0 ? (all_units + ctas - cp - 1) / (ctas - cp) : 0;
+      atomicMin(&v->best, (unsigned long long)((tp > tr ? tp : tr) << 16 | i));
+    }
+  }
+  __syncthreads();
+  const int32_t pick = prompt ? (int32_t)(v->best & 0xffff) : 0;
+  const int32_t cp = prompt ? 1 + pick / kRounds : 0;
+  if (tid == 0) {
+    Plan& p = v->plan;
+    p.tokens = all_tokens;
+    p.np = np;
+    p.cp = cp;
+    p.strip = prompt ? strip_of(cp, 1 + pick % kRounds) : 1;
+    p.strips = prompt ? (a.nt + p.strip - 1) / p.strip : 0;
+    p.units = all_units;
+    p.rcs = min(ctas - cp, all_units);
+    p.m0 = p.off0 = 0;
+    if (cta == 0) *static_cast<Plan*>(a.plan) = p;  // for the combine
+  }
+  __syncthreads();
+  const int32_t rcs = min(ctas - cp, all_units);
+  if (cta >= cp && cta - cp < rcs) {  // the member that the first unit lies with
+    const int32_t r0 = unit_bound(all_units, cta - cp, rcs);
+    int32_t pre = us - units;
+    if (pre <= r0 && r0 < us)
+      for (int i = 0; i < per; ++i) {
+        const int32_t m = tid * per + i, x = member_units(a, m);
+        if (r0 < pre + x) {
+          v->plan.m0 = m;
+          v->plan.off0 = r0 - pre;
+          break;
+        }
+        pre += x;
+      }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsDecodeArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023) {  // the swizzled tiles' alignment, which the declaration asks for
+    if (threadIdx.x == 0) ls_report(a.err, LS_DEVERR_CHECK);
+    return;
+  }
+  Vars* vars = reinterpret_cast<Vars*>(smem + kOffVars);
+  uint16_t* tok = reinterpret_cast<uint16_t*>(smem + kOffTok);
+  volatile int* abort_flag = &vars->abort;
+  const volatile Plan& plan = vars->plan;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int32_t cta = blockIdx.x;
+
+  // the combine may be launched: its blocks wait for this grid before they read from it
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  make_plan(a, vars, tok, reinterpret_cast<int32_t*>(smem + kOffRing), cta);
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar_addr(sbase, B_KV_FULL + i), 1);
+      mbar_init(bar_addr(sbase, B_KV_EMPTY + i), 2);  // one commit per issuer
+      mbar_init(bar_addr(sbase, B_AUX + i), 1);
+    }
+    mbar_init(bar_addr(sbase, B_Q_FULL), 1);
+    mbar_init(bar_addr(sbase, B_Q_EMPTY), 2);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar_addr(sbase, B_S_FULL + t), 1);
+      mbar_init(bar_addr(sbase, B_P_FULL + 2 * t), kTile);
+      mbar_init(bar_addr(sbase, B_P_FULL + 2 * t + 1), kTile);
+      mbar_init(bar_addr(sbase, B_O_DONE + t), 1);
+      mbar_init(bar_addr(sbase, B_DONE + t), 1);
+      mbar_init(bar_addr(sbase, B_PV_DONE + t), 1);
+    }
+    vars->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&vars->tmem), 512);
+    tmem_relinquish();
+  }
+  fence_proxy_async_smem();  // the scratch above, before TMA writes the ring
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&vars->tmem);
+
+  auto fail = [&](void) {
+    ls_report(a.err, LS_DEVERR_TIMEOUT);
+    *abort_flag = 1;
+  };
+  Walk walk(a, plan, cta);
+  Seg s;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    if (warp == 0) {
+      // ---------------------------------------------------------- K and V loads
+      if (lane == 0) {
+        tma_prefetch_desc(&tm.kp);
+        tma_prefetch_desc(&tm.vp);
+        tma_prefetch_desc(&tm.kr);
+        tma_prefetch_desc(&tm.vr);
+        RingPos<kStages> ring;
+        uint32_t fills = 0;
+        Loader ld;
+        bool ok = true;
+        while (ok && walk.next(&s, cta)) {
+          ld.open(a, s.resp, s.m, s.kvh, s.key0, s.len, &tm.kp, &tm.kr);
+          for (int32_t j = 0; ok && j < s.count; ++j) {
+            const bool ragged = s.len - (s.key0 + j * kTile) < kTile;
+            for (int kv = 0; kv < 2; ++kv) {
+              ok = wait_bar(bar_addr(sbase, B_KV_EMPTY + ring.stage), ring.phase ^ 1) && !*abort_flag;
+              if (!ok) {
+                fail();
+                break;
+              }
+              ld.map = kv ? (s.resp ? &tm.vr : &tm.vp) : (s.resp ? &tm.kr : &tm.kp);
+              ld.issue(sbase + kOffRing + ring.stage * kTileBytes,
+                       bar_addr(sbase, (kv && ragged ? B_AUX : B_KV_FULL) + ring.stage), a.err);
+              ring.advance();
+              ++fills;
+            }
+            ld.advance(j + 1 < s.count);
+          }
+        }
+        // Do not leave while loads into this CTA's shared memory may still be in flight.
+        for (uint32_t i = fills > kStages ? fills - kStages : 0; i < fills; ++i)
+          mbar_wait(bar_addr(sbase, B_KV_FULL + i % kStages), (i / kStages) & 1);
+      }
+    } else if (warp == 3) {
+      // ---------------------------------------------------------- Q rows, V tails
+      uint32_t ring = 0, aux_phase = 0, segs = 0;
+      // Q goes into the operand layout (128-byte swizzle: chunk c of row r lies at chunk
+      // c ^ (r & 7)), row by row.  Rows behind the pair's keep what was there: a row of S, P and
+      // O depends on its own row of Q only, and theirs are not written out.
+      auto load_q = [&](const Seg& g) {
+        for (int r0 = 0; r0 < g.rows; r0 += 32) {
+          const int32_t row = g.row0 + min(r0 + lane, g.rows - 1), t = row / a.g, head = row - t * a.g;
+          int32_t m = g.m, first = t;  // member, and the token among its drafted ones
+          if (!g.resp) {
+            int32_t lo = 0, hi = a.M - 1;  // the last member whose tokens begin at or before t
+            while (lo < hi) {
+              const int32_t mid = (lo + hi + 1) >> 1;
+              if (tok[mid] <= t) lo = mid; else hi = mid - 1;
+            }
+            m = lo;
+            first = t - tok[lo];
+          }
+          const int32_t at = a.n - (tok[m + 1] - tok[m]) + first;  // its row among the member's n
+          const int32_t src = (m * a.n + at) * a.hq + g.kvh * a.g + head;
+#pragma unroll 4
+          for (int k = 0; k < 16; ++k) {
+            const int r = r0 + 2 * k + (lane >> 4), c = lane & 15;
+            const int32_t from = __shfl_sync(0xffffffffu, src, 2 * k + (lane >> 4));
+            if (r < g.rows)
+              cp_async16(sbase + kOffQ + (r >> 7) * kTileBytes + (c >> 3) * kHalfBytes + (r & 127) * 128 +
+                             (((c & 7) ^ (r & 7)) << 4),
+                         static_cast<const __nv_bfloat16*>(a.q) + (int64_t)from * kD + c * 8);
+          }
+        }
+        cp_async_wait_all();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_addr(sbase, B_Q_FULL));
+      };
+      bool ok = true, have = walk.next(&s, cta);
+      if (have) load_q(s);
+      while (ok && have) {
+        const int32_t left = s.len - (s.key0 + (s.count - 1) * kTile);
+        ring += 2 * s.count;
+        if (left < kTile) {  // the segment's last tile passes its source's end
+          const uint32_t st = (ring - 1) % kStages;
+          ok = wait_bar(bar_addr(sbase, B_AUX + st), (aux_phase >> st) & 1);
+          if (!ok) break;
+          aux_phase ^= 1u << st;
+          uint8_t* vb = smem + kOffRing + st * kTileBytes;
+          for (int i = left * 8 + lane; i < kTile * 8; i += 32) {
+            *reinterpret_cast<uint4*>(vb + i * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(vb + kHalfBytes + i * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_addr(sbase, B_KV_FULL + st));
+        }
+        have = walk.next(&s, cta);
+        if (have) {
+          ok = wait_bar(bar_addr(sbase, B_Q_EMPTY), segs & 1) && !*abort_flag;
+          if (ok) load_q(s);
+        }
+        ++segs;
+      }
+      if (!ok) fail();
+    } else if (lane == 0) {
+      // ---------------------------------------------------------- MMA issuers
+      const int t = warp - 1;
+      const uint32_t idS = idesc_bf16_f32(kTile, kTile, false);
+      const uint32_t idPV = idesc_bf16_f32(kTile, kD, true);
+      const uint32_t dq = sdesc_lo(sbase + kOffQ + t * kTileBytes, 16);
+      const uint32_t dk = sdesc_lo(sbase + kOffRing, 16);
+      const uint32_t dv = sdesc_lo(sbase + kOffRing, kHalfBytes);
+      const uint32_t d_s = tmem + t * kTile, d_o = tmem + 256 + t * kTile;
+      auto issue_s = [&](uint32_t st) {
+        const uint32_t b0 = dk + ((st * kTileBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
+          mma_ss_lo(d_s, dq + off, b0 + off, idS, kk > 0);
+        }
+      };
+      // P_t V over keys [64 hf, 64 hf + 64): K steps 4 hf .. 4 hf + 3
+      auto issue_pv_half = [&](uint32_t st, int hf, bool accumulate) {
+        const uint32_t b0 = dv + ((st * kTileBytes) >> 4);
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4) {
+          const int kk = 4 * hf + k4;
+          mma_ts_lo(d_o, d_s + kk * 8, b0 + ((kk * 2048) >> 4), idPV, (accumulate || kk > 0) ? 1u : 0u);
+        }
+      };
+      auto full = [&](uint32_t i) {
+        return wait_bar(bar_addr(sbase, B_KV_FULL + i % kStages), (i / kStages) & 1);
+      };
+      // kc: this tile's key tiles so far; both: those of segments with two row tiles
+      uint32_t ring = 0, segs = 0, kc = 0, both = 0;
+      bool ok = true;
+      while (ok && walk.next(&s, cta)) {
+        const bool two = s.two();
+        ok = wait_bar(bar_addr(sbase, B_Q_FULL), segs & 1) && !*abort_flag;
+        ++segs;
+        if (!ok) break;
+        if (t == 1 && !two) {  // one tile: this issuer only gives the stages back
+          for (int32_t j = 0; ok && j < 2 * s.count; ++j, ++ring) {
+            ok = full(ring);
+            if (ok) mbar_arrive(bar_addr(sbase, B_KV_EMPTY + ring % kStages));
+          }
+          mbar_arrive(bar_addr(sbase, B_Q_EMPTY));
+          continue;
+        }
+        ok = full(ring);
+        if (!ok) break;
+        tc_fence_after();
+        issue_s(ring % kStages);
+        mma_commit(bar_addr(sbase, B_S_FULL + t));
+        mma_commit(bar_addr(sbase, B_KV_EMPTY + ring % kStages));
+        if (s.count == 1) mma_commit(bar_addr(sbase, B_Q_EMPTY));
+        for (int32_t j = 0; j < s.count; ++j) {
+          // Loads first, then the one real dependency (P_t), then the MMAs back to back.
+          const uint32_t vi = ring + 2 * j + 1, ki = vi + 1;
+          const bool more = j + 1 < s.count;
+          ok = full(vi) && (!more || full(ki)) &&
+               // first half of P_t (keys [0,64)); the softmax still works on the second
+               wait_bar(bar_addr(sbase, B_P_FULL + 2 * t), kc & 1);
+          // Half a period apart: tile B's products of a tile follow tile A's, tile A's follow
+          // tile B's of the tile before, so each tile's softmax runs beside the other's MMAs.
+          // (Neither is ever more than one ahead, so a parity names one tile.)
+          if (ok && two && t == 1) ok = wait_bar(bar_addr(sbase, B_PV_DONE), (both + j) & 1);
+          if (ok && two && t == 0 && both + j > 0)
+            ok = wait_bar(bar_addr(sbase, B_PV_DONE + 1), (both + j - 1) & 1);
+          if (!ok || *abort_flag) break;
+          tc_fence_after();
+          issue_pv_half(vi % kStages, 0, j > 0);
+          ok = wait_bar(bar_addr(sbase, B_P_FULL + 2 * t + 1), kc & 1);
+          if (!ok) break;
+          ++kc;
+          tc_fence_after();
+          issue_pv_half(vi % kStages, 1, true);
+          if (two) mma_commit(bar_addr(sbase, B_PV_DONE + t));
+          if (!more) mma_commit(bar_addr(sbase, B_O_DONE + t));
+          mma_commit(bar_addr(sbase, B_KV_EMPTY + vi % kStages));
+          if (!more) break;
+          // S_t of the next tile (after P_t V in issue order: it overwrites P_t)
+          issue_s(ki % kStages);
+          mma_commit(bar_addr(sbase, B_S_FULL + t));
+          mma_commit(bar_addr(sbase, B_KV_EMPTY + ki % kStages));
+          if (j + 2 == s.count) mma_commit(bar_addr(sbase, B_Q_EMPTY));
+        }
+        if (*abort_flag) break;
+        ring += 2 * s.count;
+        if (two) both += s.count;
+      }
+      if (!ok) fail();
+      // every MMA this thread issued has finished before tensor memory is released
+      mma_commit(bar_addr(sbase, B_DONE + t));
+      mbar_wait(bar_addr(sbase, B_DONE + t), 0);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // ------------------------------------------------------------ softmax warpgroups
+    const int t = (warp - 4) >> 2;  // tile A (0) or B (1)
+    const int quad = warp & 3, row = quad * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t s_col = tmem + lane_off + t * kTile;
+    const uint32_t o_col = tmem + lane_off + 256 + t * kTile;
+    const float c = a.scale_log2;
+    uint32_t kc = 0, oc = 0;
+    bool ok = true;
+    while (ok && walk.next(&s, cta)) {
+      const int32_t rows = s.rows - t * kTile;  // of this tile
+      if (rows <= 0) continue;
+      const bool idle = quad * 32 >= rows;  // the whole warp is padding
+      // keys from the tile's first one on that every row sees: the source's, or the context
+      int32_t lim = s.len - s.key0, pad = 0;
+      const uint32_t* bits = nullptr;
+      if (s.resp) {
+        const int32_t drafted = drafted_tokens(a, s.m);
+        pad = a.n - drafted;
+        lim -= drafted;
+        const int32_t at = min(s.row0 + t * kTile + row, s.row0 + s.rows - 1) / a.g;
+        bits = a.visible + ((int64_t)s.m * a.n + pad + at) * a.words;
+      }
+      float m = -INFINITY, l = 0.f, lcomp = 0.f;
+      for (int32_t j = 0; j < s.count; ++j, ++kc, lim -= kTile) {
+        ok = wait_bar(bar_addr(sbase, B_S_FULL + t), kc & 1);
+        if (!ok) break;
+        if (idle) {  // P keeps what was there: rows of D depend on their own rows of A only
+          mbar_arrive(bar_addr(sbase, B_P_FULL + 2 * t));
+          mbar_arrive(bar_addr(sbase, B_P_FULL + 2 * t + 1));
+          continue;
+        }
+        tc_fence_after();
+        uint32_t sr[128];
+        tmem_ld32(s_col + 0, sr);
+        tmem_ld32(s_col + 32, sr + 32);
+        tmem_ld32(s_col + 64, sr + 64);
+        tmem_ld32(s_col + 96, sr + 96);
+        tmem_wait_ld();
+        reg_fence32(sr);
+        reg_fence32(sr + 32);
+        reg_fence32(sr + 64);
+        reg_fence32(sr + 96);
+        if (lim < kTile) {
+          if (s.resp) {  // drafted keys among these
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const uint64_t see = tree_window(a, bits, pad - lim + 64 * hf, pad);
+#pragma unroll
+              for (int e = 0; e < 64; ++e)
+                if (!((uint32_t)(see >> (e & 32)) & (1u << (e & 31)))) sr[64 * hf + e] = __float_as_uint(-INFINITY);
+            }
+          } else {  // the prompt's ragged end
+#pragma unroll
+            for (int e = 0; e < 128; ++e)
+              if (e >= lim) sr[e] = __float_as_uint(-INFINITY);
+          }
+        }
+        float mx8[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(__uint_as_float(sr[k]), __uint_as_float(sr[k + 8]));
+#pragma unroll
+        for (int e = 16; e < 128; e += 16)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mx8[k] = fmax3(mx8[k], __uint_as_float(sr[e + k]), __uint_as_float(sr[e + 8 + k]));
+        const float mt = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
+                               fmaxf(mx8[6], mx8[7])) * c;
+        bool rescale = false;
+        float alpha = 1.f;
+        if (j == 0) {
+          m = mt;
+        } else if (mt > m + kRescaleLog2) {
+          alpha = fast_exp2(m - mt);
+          m = mt;
+          l *= alpha;
+          lcomp *= alpha;
+          rescale = true;
+        }
+        const float msub = (m == -INFINITY) ? 0.f : m;
+        // rescale O first (rare): P_t V of this tile adds to it as soon as the first half of P
+        // is in tensor memory; that of the tile before is done (S came behind it)
+        if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < kD; c0 += 32) {
+            uint32_t ov[32];
+            tmem_ld32(o_col + c0, ov);
+            tmem_wait_ld();
+            reg_fence32(ov);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+            tmem_st32(o_col + c0, ov);
+          }
+        }
+        const float2 c2 = make_float2(c, c), nm2 = make_float2(-msub, -msub);
+        float2 ls4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                         make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {  // P in two 64-key halves, released one by one
+          uint32_t pk[32];
+#pragma unroll
+          for (int jj = 0; jj < 32; ++jj) {
+            const int e = half * 32 + jj;
+            float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])),
+                                  c2, nm2);
+            x.x = fast_exp2(x.x);
+            x.y = fast_exp2(x.y);
+            ls4[jj & 3] = __fadd2_rn(ls4[jj & 3], x);
+            // weights in [0, 2^8] enter the product as bf16, as in the replay forward: their
+            // roundings are independent, so o's error is that of one bf16 rounding
+            pk[jj] = pack_bf16(x.x, x.y);
+          }
+          tmem_st32(s_col + half * 32, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar_addr(sbase, B_P_FULL + 2 * t + half));
+        }
+        const float2 lsa = __fadd2_rn(__fadd2_rn(ls4[0], ls4[1]), __fadd2_rn(ls4[2], ls4[3]));
+        const float ls = lsa.x + lsa.y;
+        const float tsum = l + ls;
+        lcomp += (l - tsum) + ls;
+        l = tsum;
+      }
+      ok = ok && wait_bar(bar_addr(sbase, B_O_DONE + t), oc & 1);
+      if (!ok) break;
+      ++oc;
+      if (!idle) {
+        tc_fence_after();
+        const float lt = l + lcomp;
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;  // a row that sees no key here
+        const int64_t prow = s.part + t * kTile + row;
+        float* po = part_at(a, prow);
+#pragma unroll 1
+        for (int c0 = 0; c0 < kD; c0 += 32) {
+          uint32_t ov[32];
+          tmem_ld32(o_col + c0, ov);
+          tmem_wait_ld();
+          reg_fence32(ov);
+          if (row < rows) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4*>(po + (c0 + i) * 8) =
+                  make_float4(__uint_as_float(ov[i]) * inv, __uint_as_float(ov[i + 1]) * inv,
+                              __uint_as_float(ov[i + 2]) * inv, __uint_as_float(ov[i + 3]) * inv);
+          }
+        }
+        if (row < rows) a.part_lse[prow] = lt == 0.f ? -INFINITY : m + log2f(lt);
+        tc_fence_before();
+      }
+      if (*abort_flag) break;
+    }
+    if (!ok) fail();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Merge a row's partials: lse = log2 sum 2^lse_k, o = sum 2^(lse_k - lse) o_k, in a fixed
+// order.  A warp a row, a lane four values; a block takes eight rows of one member and KV head,
+// whose partials lie in the same lines.
+constexpr int kCombineWarps = 8;
+
+__global__ void __launch_bounds__(kCombineWarps * 32)
+tree_combine(const __grid_constant__ LsDecodeArgs a) {
+  __shared__ int32_t sums[2][kCombineWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int32_t octets = (a.n * a.g + 7) >> 3, m = blockIdx.x / octets, h = blockIdx.y;
+  // the row among the member's n g, the drafted ones last
+  const int32_t row = 8 * (blockIdx.x - m * octets) + warp, tokens = drafted_tokens(a, m);
+  const int32_t mrow = row - (a.n - tokens) * a.g;  // among the drafted ones
+  int32_t before = 0, units = 0;  // tokens and units of the members before
+  for (int i = tid; i < m; i += kCombineWarps * 32) {
+    before += drafted_tokens(a, i);
+    units += member_units(a, i);
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  units = __reduce_add_sync(0xffffffffu, units);
+  if (lane == 0) {
+    sums[0][warp] = before;
+    sums[1][warp] = units;
+  }
+  __syncthreads();
+  before = units = 0;
+#pragma unroll
+  for (int i = 0; i < kCombineWarps; ++i) {
+    before += sums[0][i];
+    units += sums[1][i];
+  }
+  // Rows that are not written (padding, members out of use) wait all the same: the stream goes
+  // on when this grid ends.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (mrow < 0 || row >= a.n * a.g) return;
+  const Plan* pp = static_cast<const Plan*>(a.plan);
+  const int32_t np = __ldcg(&pp->np), strips = __ldcg(&pp->strips);
+  const int32_t all = __ldcg(&pp->units), rcs = __ldcg(&pp->rcs);
+  const int32_t prow = before * a.g + mrow, pair = prow / kPair;
+  const int64_t prompt0 = (int64_t)(h * strips * np + pair) * kPair + (prow - pair * kPair);
+  // the response's units that are this row's tiles
+  const int32_t rpair = mrow / kPair, iu = item_units(a, m), nt = iu - kSegTiles;
+  const int32_t u0 = units + (rpair * a.hkv + h) * iu + kSegTiles;
+  int32_t rc = 0, rc_end = 0;  // response CTAs that have some of them
+  if (nt > 0) {
+    rc = (int32_t)((long long)u0 * rcs / all);
+    while (rc > 0 && unit_bound(all, rc, rcs) > u0) --rc;
+    while (unit_bound(all, rc + 1, rcs) <= u0) ++rc;
+    rc_end = rc + 1;
+    while (rc_end < rcs && unit_bound(all, rc_end, rcs) < u0 + nt) ++rc_end;
+  }
+  const int32_t count = strips + rc_end - rc;
+  const int64_t resp0 = resp_row0(a, m, rpair, h, rc) + (mrow - rpair * kPair);
+  auto part_row = [&](int32_t k) {
+    return k < strips ? prompt0 + (int64_t)k * np * kPair
+                      : resp0 + (int64_t)(k - strips) * resp_rows_of(a);
+  };
+  float mx = -INFINITY;
+  for (int32_t k = lane; k < count; k += 32) mx = fmaxf(mx, __ldcg(a.part_lse + part_row(k)));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float sub = mx == -INFINITY ? 0.f : mx;
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kBatch = 4;
+  for (int32_t k0 = 0; k0 < count; k0 += kBatch) {
+    float l[kBatch];
+    float4 v[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      l[b] = -INFINITY;
+      if (k0 + b < count) {
+        const int64_t r = part_row(k0 + b);
+        l[b] = __ldcg(a.part_lse + r);
+        v[b] = *reinterpret_cast<const float4*>(part_at(a, r) + lane * 32);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (l[b] == -INFINITY) continue;  // a part that saw no key adds nothing
+      const float w = exp2f(l[b] - sub);
+      sum += w;
+      acc.x = fmaf(w, v[b].x, acc.x);
+      acc.y = fmaf(w, v[b].y, acc.y);
+      acc.z = fmaf(w, v[b].z, acc.z);
+      acc.w = fmaf(w, v[b].w, acc.w);
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key at all: o = 0, lse = -inf
+  const int64_t out = ((int64_t)m * a.n + row / a.g) * a.hq + h * a.g + row % a.g;
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + out * kD + lane * 4) =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (lane == 0) a.lse[out] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+}
+
+}  // namespace
+
+size_t ls_tree_plan_bytes() { return sizeof(Plan); }
+int64_t ls_tree_part_rows(const LsDecodeArgs& a) {
+  const int64_t slots = (int64_t)a.M * max_pairs(a) * a.hkv + a.cols;
+  return prompt_rows_of(a) + slots * resp_rows_of(a);
+}
+
+cudaError_t ls_launch_tree_attn(const LsDecodeArgs& a, cudaStream_t st) {
+  TmapSet tm;
+  if (!make_tmaps(a, &tm)) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kSmemBytes);
+  if (e != cudaSuccess) return e;
+  tree_attn_kernel<<<a.cols, kThreads, kSmemBytes, st>>>(tm, a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  ls_note_launch();
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.M * ((a.n * a.g + 7) / 8)), (unsigned)a.hkv);
+  cfg.blockDim = dim3(kCombineWarps * 32);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, tree_combine, a);
+  if (e == cudaSuccess) ls_note_launch();
+  return e;
+}
