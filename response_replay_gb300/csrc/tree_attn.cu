@@ -22,13 +22,13 @@
 //
 // CTA (one per SM, 12 warps; the pipeline of replay_fwd_tc.cu):
 //   warp 0      TMA producer: K and V tiles, page by page, into a ring of five.
-//   warps 1, 2  issue S_t = Q_t K^T and O_t += P_t V of tile A and tile B, one thread each; the
-//               tiles stay half a period apart.
+//   warps 1, 2  issue S_t = Q_t K^T and O_t += P_t V of tile A and tile B, one thread each.
 //   warp 3      the segments' Q rows (gathered by token and head); clears V rows behind a
 //               sequence's end (stale page contents, even NaN, would survive a zero weight).
 //   warps 4-7   softmax of tile A, warps 8-11 of tile B: a thread a row.
-// Tensor memory (512 columns): S_A [0,128) S_B [128,256) O_A [256,384) O_B [384,512); P_t
-// overlays the first 64 columns of S_t.
+// Tensor memory (512 columns): S [0,128) P_A [128,192) P_B [192,256) O_A [256,384) O_B [384,512).
+// The tiles take the S buffer in turn: it is free as soon as the softmax has S in its registers, so
+// a tile's next S is ready while its softmax still works on the last, and P V follows behind.
 #include "ls_decode.cuh"
 
 namespace {
@@ -46,6 +46,7 @@ static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * kRegsLaunch,
 constexpr uint32_t kOffQ = 0;  // Q_A, Q_B
 constexpr uint32_t kOffRing = 2 * kTileBytes;
 constexpr uint32_t kOffBar = kOffRing + kStages * kTileBytes;
+constexpr uint32_t kColP = kTile, kColO = 2 * kTile;  // tensor memory behind the S buffer
 constexpr int kMaxMembers = 1024;
 constexpr int kSegTiles = 3;  // a segment's beginning and end take a CTA as long as so many tiles
 constexpr int kRounds = 3;    // of prompt items that are tried
@@ -57,10 +58,12 @@ enum {
   B_Q_FULL = B_AUX + kStages,
   B_Q_EMPTY,
   B_S_FULL,                  // 2
-  B_P_FULL = B_S_FULL + 2,   // 4: tile t, key half hf at 2 t + hf
+  B_S_TAKEN = B_S_FULL + 2,  // 2: S is in the softmax's registers (segments of two row tiles)
+  B_S_ALONE = B_S_TAKEN + 2, // the same where tile A is alone
+  B_P_FULL,                  // 4: tile t, key half hf at 2 t + hf
   B_O_DONE = B_P_FULL + 4,   // 2
   B_DONE = B_O_DONE + 2,     // 2
-  B_PV_DONE = B_DONE + 2,    // 2: of segments with two tiles
+  B_PV_DONE = B_DONE + 2,    // 2
   B_COUNT = B_PV_DONE + 2
 };
 
@@ -318,10 +321,12 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
     }
     mbar_init(bar_addr(sbase, B_Q_FULL), 1);
     mbar_init(bar_addr(sbase, B_Q_EMPTY), 2);
+    mbar_init(bar_addr(sbase, B_S_ALONE), 4);
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar_addr(sbase, B_S_FULL + t), 1);
-      mbar_init(bar_addr(sbase, B_P_FULL + 2 * t), kTile);
-      mbar_init(bar_addr(sbase, B_P_FULL + 2 * t + 1), kTile);
+      mbar_init(bar_addr(sbase, B_S_TAKEN + t), 4);  // a warp each
+      mbar_init(bar_addr(sbase, B_P_FULL + 2 * t), 4);
+      mbar_init(bar_addr(sbase, B_P_FULL + 2 * t + 1), 4);
       mbar_init(bar_addr(sbase, B_O_DONE + t), 1);
       mbar_init(bar_addr(sbase, B_DONE + t), 1);
       mbar_init(bar_addr(sbase, B_PV_DONE + t), 1);
@@ -453,7 +458,7 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
       const uint32_t dq = sdesc_lo(sbase + kOffQ + t * kTileBytes, 16);
       const uint32_t dk = sdesc_lo(sbase + kOffRing, 16);
       const uint32_t dv = sdesc_lo(sbase + kOffRing, kHalfBytes);
-      const uint32_t d_s = tmem + t * kTile, d_o = tmem + 256 + t * kTile;
+      const uint32_t d_s = tmem, d_p = tmem + kColP + t * (kTile / 2), d_o = tmem + kColO + t * kTile;
       auto issue_s = [&](uint32_t st) {
         const uint32_t b0 = dk + ((st * kTileBytes) >> 4);
 #pragma unroll
@@ -468,69 +473,79 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4) {
           const int kk = 4 * hf + k4;
-          mma_ts_lo(d_o, d_s + kk * 8, b0 + ((kk * 2048) >> 4), idPV, (accumulate || kk > 0) ? 1u : 0u);
+          mma_ts_lo(d_o, d_p + kk * 8, b0 + ((kk * 2048) >> 4), idPV, (accumulate || kk > 0) ? 1u : 0u);
         }
       };
-      auto full = [&](uint32_t i) {
-        return wait_bar(bar_addr(sbase, B_KV_FULL + i % kStages), (i / kStages) & 1);
-      };
-      // kc: this tile's key tiles so far; both: those of segments with two row tiles
-      uint32_t ring = 0, segs = 0, kc = 0, both = 0;
+      uint32_t seen = 0;
+      RingPos<kStages> sp;
+      // ring: loads before the segment; kc: this tile's key tiles so far; both, alone: those of
+      // segments with two row tiles and with one
+      uint32_t ring = 0, segs = 0, kc = 0, both = 0, alone = 0;
       bool ok = true;
       while (ok && walk.next(&s, cta)) {
-        const bool two = s.two();
+        const bool two = s.two(), mine = two || t == 0;
+        const uint32_t last = ring + 2 * s.count - 1;
+        // Loads are waited for in order and without gaps, and a stage is free after an arrival of
+        // either issuer: behind its products, or, from the issuer of a tile without rows, as soon
+        // as the load was seen.  So a stage's parity always names one fill.
+        auto need = [&](uint32_t i) {
+          for (; seen <= i; ++seen, sp.advance()) {
+            if (!wait_bar(bar_addr(sbase, B_KV_FULL + sp.stage), sp.phase)) return false;
+            if (!mine) mbar_arrive(bar_addr(sbase, B_KV_EMPTY + sp.stage));
+          }
+          return true;
+        };
         ok = wait_bar(bar_addr(sbase, B_Q_FULL), segs & 1) && !*abort_flag;
         ++segs;
-        if (!ok) break;
-        if (t == 1 && !two) {  // one tile: this issuer only gives the stages back
-          for (int32_t j = 0; ok && j < 2 * s.count; ++j, ++ring) {
-            ok = full(ring);
-            if (ok) mbar_arrive(bar_addr(sbase, B_KV_EMPTY + ring % kStages));
-          }
+        if (!mine) {
+          ok = ok && need(last);
           mbar_arrive(bar_addr(sbase, B_Q_EMPTY));
+          ring = last + 1;
+          alone += s.count;
           continue;
         }
-        ok = full(ring);
-        if (!ok) break;
-        tc_fence_after();
-        issue_s(ring % kStages);
-        mma_commit(bar_addr(sbase, B_S_FULL + t));
-        mma_commit(bar_addr(sbase, B_KV_EMPTY + ring % kStages));
-        if (s.count == 1) mma_commit(bar_addr(sbase, B_Q_EMPTY));
-        for (int32_t j = 0; j < s.count; ++j) {
-          // Loads first, then the one real dependency (P_t), then the MMAs back to back.
-          const uint32_t vi = ring + 2 * j + 1, ki = vi + 1;
-          const bool more = j + 1 < s.count;
-          ok = full(vi) && (!more || full(ki)) &&
-               // first half of P_t (keys [0,64)); the softmax still works on the second
-               wait_bar(bar_addr(sbase, B_P_FULL + 2 * t), kc & 1);
-          // Half a period apart: tile B's products of a tile follow tile A's, tile A's follow
-          // tile B's of the tile before, so each tile's softmax runs beside the other's MMAs.
-          // (Neither is ever more than one ahead, so a parity names one tile.)
-          if (ok && two && t == 1) ok = wait_bar(bar_addr(sbase, B_PV_DONE), (both + j) & 1);
-          if (ok && two && t == 0 && both + j > 0)
-            ok = wait_bar(bar_addr(sbase, B_PV_DONE + 1), (both + j - 1) & 1);
-          if (!ok || *abort_flag) break;
-          tc_fence_after();
-          issue_pv_half(vi % kStages, 0, j > 0);
-          ok = wait_bar(bar_addr(sbase, B_P_FULL + 2 * t + 1), kc & 1);
-          if (!ok) break;
-          ++kc;
-          tc_fence_after();
-          issue_pv_half(vi % kStages, 1, true);
-          if (two) mma_commit(bar_addr(sbase, B_PV_DONE + t));
-          if (!more) mma_commit(bar_addr(sbase, B_O_DONE + t));
-          mma_commit(bar_addr(sbase, B_KV_EMPTY + vi % kStages));
-          if (!more) break;
-          // S_t of the next tile (after P_t V in issue order: it overwrites P_t)
-          issue_s(ki % kStages);
-          mma_commit(bar_addr(sbase, B_S_FULL + t));
-          mma_commit(bar_addr(sbase, B_KV_EMPTY + ki % kStages));
-          if (j + 2 == s.count) mma_commit(bar_addr(sbase, B_Q_EMPTY));
+        // The tiles take the one S buffer in turn, A before B.  (Of the barriers below none is
+        // ever more than a phase ahead of the one that is waited for.)
+        auto s_free = [&](int32_t j) {
+          if (t == 1) return wait_bar(bar_addr(sbase, B_S_TAKEN), (both + j) & 1);
+          bool r = true;
+          if (two ? both + j > 0 : both > 0 && j == 0)
+            r = wait_bar(bar_addr(sbase, B_S_TAKEN + 1), (both + (two ? j : 0) - 1) & 1);
+          if (two ? alone > 0 && j == 0 : alone + j > 0)
+            r = r && wait_bar(bar_addr(sbase, B_S_ALONE), (alone + (two ? 0 : j) - 1) & 1);
+          return r;
+        };
+        for (int32_t j = 0; ok && j <= s.count; ++j) {
+          if (j < s.count) {  // S of step j goes before P V of step j - 1
+            const uint32_t ki = ring + 2 * j;
+            ok = need(ki) && s_free(j);
+            if (!ok || *abort_flag) break;
+            tc_fence_after();
+            issue_s(ki % kStages);
+            mma_commit(bar_addr(sbase, B_S_FULL + t));
+            mma_commit(bar_addr(sbase, B_KV_EMPTY + ki % kStages));
+            if (j + 1 == s.count) mma_commit(bar_addr(sbase, B_Q_EMPTY));
+          }
+          if (j > 0) {
+            const uint32_t vi = ring + 2 * j - 1;
+            // first half of P_t (keys [0,64)); the softmax still works on the second
+            ok = need(vi) && wait_bar(bar_addr(sbase, B_P_FULL + 2 * t), kc & 1);
+            if (!ok || *abort_flag) break;
+            tc_fence_after();
+            issue_pv_half(vi % kStages, 0, j > 1);
+            ok = wait_bar(bar_addr(sbase, B_P_FULL + 2 * t + 1), kc & 1);
+            if (!ok) break;
+            ++kc;
+            tc_fence_after();
+            issue_pv_half(vi % kStages, 1, true);
+            mma_commit(bar_addr(sbase, B_PV_DONE + t));
+            if (j == s.count) mma_commit(bar_addr(sbase, B_O_DONE + t));
+            mma_commit(bar_addr(sbase, B_KV_EMPTY + vi % kStages));
+          }
         }
         if (*abort_flag) break;
-        ring += 2 * s.count;
-        if (two) both += s.count;
+        ring = last + 1;
+        (two ? both : alone) += s.count;
       }
       if (!ok) fail();
       // every MMA this thread issued has finished before tensor memory is released
@@ -543,16 +558,22 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
     const int t = (warp - 4) >> 2;  // tile A (0) or B (1)
     const int quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t s_col = tmem + lane_off + t * kTile;
-    const uint32_t o_col = tmem + lane_off + 256 + t * kTile;
+    const uint32_t s_col = tmem + lane_off, p_col = tmem + lane_off + kColP + t * (kTile / 2);
+    const uint32_t o_col = tmem + lane_off + kColO + t * kTile;
     const float c = a.scale_log2;
+    auto signal = [&](int bar) {  // by this warp
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_addr(sbase, bar));
+    };
     uint32_t kc = 0, oc = 0;
     bool ok = true;
     while (ok && walk.next(&s, cta)) {
       const int32_t rows = s.rows - t * kTile;  // of this tile
       if (rows <= 0) continue;
+      const int taken = s.two() ? B_S_TAKEN + t : B_S_ALONE;
       const bool idle = quad * 32 >= rows;  // the whole warp is padding
-      // keys from the tile's first one on that every row sees: the source's, or the context
+      // keys from its first key tile on that every row sees: the source's, or the context
       int32_t lim = s.len - s.key0, pad = 0;
       const uint32_t* bits = nullptr;
       if (s.resp) {
@@ -566,9 +587,14 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
       for (int32_t j = 0; j < s.count; ++j, ++kc, lim -= kTile) {
         ok = wait_bar(bar_addr(sbase, B_S_FULL + t), kc & 1);
         if (!ok) break;
+        // P's columns are free, and O may be changed, after P V of the tile before.
+        auto settled = [&]() { return j == 0 || wait_bar(bar_addr(sbase, B_PV_DONE + t), (kc - 1) & 1); };
         if (idle) {  // P keeps what was there: rows of D depend on their own rows of A only
-          mbar_arrive(bar_addr(sbase, B_P_FULL + 2 * t));
-          mbar_arrive(bar_addr(sbase, B_P_FULL + 2 * t + 1));
+          signal(taken);
+          ok = settled();
+          if (!ok) break;
+          signal(B_P_FULL + 2 * t);
+          signal(B_P_FULL + 2 * t + 1);
           continue;
         }
         tc_fence_after();
@@ -582,6 +608,7 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
         reg_fence32(sr + 32);
         reg_fence32(sr + 64);
         reg_fence32(sr + 96);
+        signal(taken);
         if (lim < kTile) {
           if (s.resp) {  // drafted keys among these
 #pragma unroll
@@ -620,8 +647,11 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
         }
         const float msub = (m == -INFINITY) ? 0.f : m;
         // rescale O first (rare): P_t V of this tile adds to it as soon as the first half of P
-        // is in tensor memory; that of the tile before is done (S came behind it)
+        // is in tensor memory
         if (__any_sync(0xffffffffu, rescale)) {
+          ok = settled();
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll 1
           for (int c0 = 0; c0 < kD; c0 += 32) {
             uint32_t ov[32];
@@ -651,11 +681,16 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
             // roundings are independent, so o's error is that of one bf16 rounding
             pk[jj] = pack_bf16(x.x, x.y);
           }
-          tmem_st32(s_col + half * 32, pk);
+          if (half == 0) {
+            ok = settled();
+            if (!ok) break;
+            tc_fence_after();
+          }
+          tmem_st32(p_col + half * 32, pk);
           tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(bar_addr(sbase, B_P_FULL + 2 * t + half));
+          signal(B_P_FULL + 2 * t + half);
         }
+        if (!ok) break;
         const float2 lsa = __fadd2_rn(__fadd2_rn(ls4[0], ls4[1]), __fadd2_rn(ls4[2], ls4[3]));
         const float ls = lsa.x + lsa.y;
         const float tsum = l + ls;
@@ -666,10 +701,10 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
       if (!ok) break;
       ++oc;
       if (!idle) {
+        const int64_t prow = s.part + t * kTile + row;
         tc_fence_after();
         const float lt = l + lcomp;
         const float inv = lt == 0.f ? 0.f : 1.f / lt;  // a row that sees no key here
-        const int64_t prow = s.part + t * kTile + row;
         float* po = part_at(a, prow);
 #pragma unroll 1
         for (int c0 = 0; c0 < kD; c0 += 32) {
