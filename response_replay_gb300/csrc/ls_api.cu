@@ -1057,7 +1057,7 @@ ls_status decode_args(const ls_kv_cache* c, const ls_resp_cache* r, int n, int H
   w->part_o = 0;
   w->part_lse = align256(rows * kHeadDim * 4);
   w->plan = align256(w->part_lse + rows * 4);
-  w->total = large ? align256(w->plan + ls_tree_plan_bytes()) : w->plan;
+  w->total = large ? align256(w->plan + ls_tree_plan_bytes(*a)) : w->plan;
   return LS_OK;
 }
 

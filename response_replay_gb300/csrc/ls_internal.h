@@ -296,7 +296,7 @@ int64_t ls_decode_prompt_rows(const LsDecodeArgs& a);
 int64_t ls_decode_resp_rows(const LsDecodeArgs& a);
 cudaError_t ls_launch_decode_attn(const LsDecodeArgs& a, cudaStream_t st);
 // The same for trees of more rows than one tile a KV head (tree_attn.cu); cols: CTAs.
-size_t ls_tree_plan_bytes();
+size_t ls_tree_plan_bytes(const LsDecodeArgs& a);
 int64_t ls_tree_part_rows(const LsDecodeArgs& a);
 cudaError_t ls_launch_tree_attn(const LsDecodeArgs& a, cudaStream_t st);
 

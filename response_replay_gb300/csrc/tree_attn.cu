@@ -23,9 +23,10 @@
 // CTA (one per SM, 12 warps; the pipeline of replay_fwd_tc.cu):
 //   warp 0      TMA producer: K and V tiles, page by page, into a ring of five.
 //   warps 1, 2  issue S_t = Q_t K^T and O_t += P_t V of tile A and tile B, one thread each.
-//   warp 3      the segments' Q rows (gathered by token and head); clears V rows behind a
-//               sequence's end (stale page contents, even NaN, would survive a zero weight).
-//   warps 4-7   softmax of tile A, warps 8-11 of tile B: a thread a row.
+//   warp 3      clears V rows behind a sequence's end (stale page contents, even NaN, would
+//               survive a zero weight).
+//   warps 4-7   softmax of tile A, warps 8-11 of tile B: a thread a row; they gather the next
+//               segment's Q rows by token and head while the last P V runs.
 // Tensor memory (512 columns): S [0,128) P_A [128,192) P_B [192,256) O_A [256,384) O_B [384,512).
 // The tiles take the S buffer in turn: it is free as soon as the softmax has S in its registers, so
 // a tile's next S is ready while its softmax still works on the last, and P V follows behind.
@@ -37,6 +38,7 @@ using namespace umma;
 using namespace decode;
 
 constexpr int kPair = 2 * kTile;
+constexpr int kMaxMembers = 1024;
 constexpr int kStages = 5;
 constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
@@ -47,7 +49,6 @@ constexpr uint32_t kOffQ = 0;  // Q_A, Q_B
 constexpr uint32_t kOffRing = 2 * kTileBytes;
 constexpr uint32_t kOffBar = kOffRing + kStages * kTileBytes;
 constexpr uint32_t kColP = kTile, kColO = 2 * kTile;  // tensor memory behind the S buffer
-constexpr int kMaxMembers = 1024;
 constexpr int kSegTiles = 3;  // a segment's beginning and end take a CTA as long as so many tiles
 constexpr int kRounds = 3;    // of prompt items that are tried
 
@@ -55,13 +56,12 @@ enum {
   B_KV_FULL = 0,
   B_KV_EMPTY = B_KV_FULL + kStages,
   B_AUX = B_KV_EMPTY + kStages,      // a ragged V tile has landed, its tail not yet cleared
-  B_Q_FULL = B_AUX + kStages,
-  B_Q_EMPTY,
-  B_S_FULL,                  // 2
+  B_Q_FULL = B_AUX + kStages,  // 2
+  B_S_FULL = B_Q_FULL + 2,   // 2
   B_S_TAKEN = B_S_FULL + 2,  // 2: S is in the softmax's registers (segments of two row tiles)
   B_S_ALONE = B_S_TAKEN + 2, // the same where tile A is alone
-  B_P_FULL,                  // 4: tile t, key half hf at 2 t + hf
-  B_O_DONE = B_P_FULL + 4,   // 2
+  B_P_FULL,                  // 2
+  B_O_DONE = B_P_FULL + 2,   // 2
   B_DONE = B_O_DONE + 2,     // 2
   B_PV_DONE = B_DONE + 2,    // 2
   B_COUNT = B_PV_DONE + 2
@@ -76,6 +76,14 @@ struct Plan {
   int32_t units, rcs;  // of the responses, and their CTAs: at least a unit each
   int32_t m0, off0;  // response CTAs: the member its first unit lies with, and how far in
 };
+// What the combine reads of it (workspace): also the tokens before each member and, for every
+// pair of a member's rows and KV head, the first and the last response CTA that has some of its
+// tiles.
+struct Out {
+  Plan plan;
+  int32_t tok[kMaxMembers];
+};
+__device__ __forceinline__ int32_t* cta_range(const LsDecodeArgs& a, int32_t m, int32_t pair, int32_t h);
 struct Vars {
   uint32_t tmem;
   int32_t abort;
@@ -101,8 +109,7 @@ __device__ __forceinline__ int32_t pairs_of(const LsDecodeArgs& a, int32_t token
 __device__ __forceinline__ int32_t item_units(const LsDecodeArgs& a, int32_t m) {
   return tiles_of(clamp_len(a, __ldg(a.lens + m))) + kSegTiles;
 }
-__device__ __forceinline__ int32_t member_units(const LsDecodeArgs& a, int32_t m) {
-  const int32_t c = drafted_tokens(a, m);
+__device__ __forceinline__ int32_t member_units(const LsDecodeArgs& a, int32_t m, int32_t c) {
   if (c == 0 || clamp_len(a, __ldg(a.lens + m)) == 0) return 0;
   return pairs_of(a, c) * a.hkv * item_units(a, m);
 }
@@ -121,6 +128,9 @@ __host__ __device__ __forceinline__ int64_t prompt_rows_of(const LsDecodeArgs& a
   const int64_t np = ((int64_t)a.M * a.n * a.g + kPair - 1) / kPair * a.hkv;
   const int64_t most = (int64_t)kRounds * a.cols;
   return (np > most ? np : most) * kPair;
+}
+__device__ __forceinline__ int32_t* cta_range(const LsDecodeArgs& a, int32_t m, int32_t pair, int32_t h) {
+  return reinterpret_cast<int32_t*>(static_cast<Out*>(a.plan) + 1) + 2 * ((m * max_pairs(a) + pair) * a.hkv + h);
 }
 __device__ __forceinline__ int64_t resp_row0(const LsDecodeArgs& a, int32_t m, int32_t pair, int32_t h,
                                              int32_t rc) {
@@ -144,10 +154,11 @@ struct Seg {
 struct Walk {
   const LsDecodeArgs& a;
   const volatile Plan& p;
+  const uint16_t* tok;
   int32_t at, end, m, off;
   bool resp;
-  __device__ __forceinline__ Walk(const LsDecodeArgs& a_, const volatile Plan& p_, int32_t cta)
-      : a(a_), p(p_), m(0), off(0), resp(cta >= p_.cp) {
+  __device__ __forceinline__ Walk(const LsDecodeArgs& a_, const volatile Plan& p_, const uint16_t* tok_, int32_t cta)
+      : a(a_), p(p_), tok(tok_), m(0), off(0), resp(cta >= p_.cp) {
     if (resp) {
       const bool some = cta - p.cp < p.rcs;
       at = some ? unit_bound(p.units, cta - p.cp, p.rcs) : 0;
@@ -177,7 +188,7 @@ struct Walk {
     }
     while (at < end) {
       for (; m < a.M; ++m, off = 0)
-        if (off < member_units(a, m)) break;
+        if (off < member_units(a, m, tok[m + 1] - tok[m])) break;
       if (m >= a.M) return false;  // only when lengths changed under the kernel
       const int32_t iu = item_units(a, m), item = off / iu, x = off - item * iu, step = min(end - at, iu - x);
       at += step;
@@ -189,7 +200,7 @@ struct Walk {
       s->kvh = item - pair * a.hkv;
       s->m = m;
       s->row0 = pair * kPair;
-      s->rows = min(drafted_tokens(a, m) * a.g - s->row0, kPair);
+      s->rows = min((tok[m + 1] - tok[m]) * a.g - s->row0, kPair);
       s->key0 = first * kTile;
       s->len = clamp_len(a, __ldg(a.lens + m));
       s->part = resp_row0(a, m, pair, s->kvh, cta - p.cp);
@@ -201,6 +212,7 @@ struct Walk {
 
 // The plan, by all threads of a CTA (scratch: 2 x kWarps ints).
 __device__ void make_plan(const LsDecodeArgs& a, Vars* v, uint16_t* tok, int32_t* scratch, int32_t cta) {
+  Out* out = static_cast<Out*>(a.plan);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (a.M + kThreads - 1) / kThreads;
   int32_t tokens = 0, units = 0;
@@ -208,8 +220,9 @@ __device__ void make_plan(const LsDecodeArgs& a, Vars* v, uint16_t* tok, int32_t
     const int m = tid * per + i;
     if (m >= a.M) break;
     if (cta == 0 && bad_member(a, m)) ls_report(a.err, LS_DEVERR_CHECK);
-    tokens += drafted_tokens(a, m);
-    units += member_units(a, m);
+    const int32_t c = drafted_tokens(a, m);
+    tokens += c;
+    units += member_units(a, m, c);
   }
   int32_t ts = tokens, us = units;
 #pragma unroll
@@ -242,6 +255,7 @@ __device__ void make_plan(const LsDecodeArgs& a, Vars* v, uint16_t* tok, int32_t
     const int m = tid * per + i;
     if (m >= a.M) break;
     tok[m] = (uint16_t)before;
+    if (cta == 0) out->tok[m] = before;
     before += drafted_tokens(a, m);
   }
   if (tid == 0) tok[a.M] = (uint16_t)all_tokens;
@@ -254,13 +268,21 @@ __device__ void make_plan(const LsDecodeArgs& a, Vars* v, uint16_t* tok, int32_t
     return (a.nt + s - 1) / s;
   };
   if (prompt) {
+    unsigned long long best = ~0ull;
     for (int i = tid; i < most * kRounds; i += kThreads) {
       const int32_t cp = 1 + i / kRounds, strip = strip_of(cp, 1 + i % kRounds);
       const int32_t strips = (a.nt + strip - 1) / strip;
       const long long tp = (long long)((strips * per_strip + cp - 1) / cp) * (strip + kSegTiles);
       const long long tr = all_units > 0 ? (all_units + ctas - cp - 1) / (ctas - cp) : 0;
-      atomicMin(&v->best, (unsigned long long)((tp > tr ? tp : tr) << 16 | i));
+      const unsigned long long x = (unsigned long long)((tp > tr ? tp : tr) << 16 | i);
+      best = x < best ? x : best;
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const unsigned long long x = __shfl_xor_sync(0xffffffffu, best, o);
+      best = x < best ? x : best;
+    }
+    if (lane == 0) atomicMin(&v->best, best);
   }
   __syncthreads();
   const int32_t pick = prompt ? (int32_t)(v->best & 0xffff) : 0;
@@ -275,7 +297,7 @@ __device__ void make_plan(const LsDecodeArgs& a, Vars* v, uint16_t* tok, int32_t
     p.units = all_units;
     p.rcs = min(ctas - cp, all_units);
     p.m0 = p.off0 = 0;
-    if (cta == 0) *static_cast<Plan*>(a.plan) = p;  // for the combine
+    if (cta == 0) out->plan = p;
   }
   __syncthreads();
   const int32_t rcs = min(ctas - cp, all_units);
@@ -284,7 +306,7 @@ __device__ void make_plan(const LsDecodeArgs& a, Vars* v, uint16_t* tok, int32_t
     int32_t pre = us - units;
     if (pre <= r0 && r0 < us)
       for (int i = 0; i < per; ++i) {
-        const int32_t m = tid * per + i, x = member_units(a, m);
+        const int32_t m = tid * per + i, x = member_units(a, m, drafted_tokens(a, m));
         if (r0 < pre + x) {
           v->plan.m0 = m;
           v->plan.off0 = r0 - pre;
@@ -319,14 +341,12 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
       mbar_init(bar_addr(sbase, B_KV_EMPTY + i), 2);  // one commit per issuer
       mbar_init(bar_addr(sbase, B_AUX + i), 1);
     }
-    mbar_init(bar_addr(sbase, B_Q_FULL), 1);
-    mbar_init(bar_addr(sbase, B_Q_EMPTY), 2);
     mbar_init(bar_addr(sbase, B_S_ALONE), 4);
     for (int t = 0; t < 2; ++t) {
+      mbar_init(bar_addr(sbase, B_Q_FULL + t), 4);
       mbar_init(bar_addr(sbase, B_S_FULL + t), 1);
       mbar_init(bar_addr(sbase, B_S_TAKEN + t), 4);  // a warp each
-      mbar_init(bar_addr(sbase, B_P_FULL + 2 * t), 4);
-      mbar_init(bar_addr(sbase, B_P_FULL + 2 * t + 1), 4);
+      mbar_init(bar_addr(sbase, B_P_FULL + t), 4);
       mbar_init(bar_addr(sbase, B_O_DONE + t), 1);
       mbar_init(bar_addr(sbase, B_DONE + t), 1);
       mbar_init(bar_addr(sbase, B_PV_DONE + t), 1);
@@ -348,7 +368,7 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
     ls_report(a.err, LS_DEVERR_TIMEOUT);
     *abort_flag = 1;
   };
-  Walk walk(a, plan, cta);
+  Walk walk(a, plan, tok, cta);
   Seg s;
 
   if (warp < 4) {
@@ -388,66 +408,26 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
           mbar_wait(bar_addr(sbase, B_KV_FULL + i % kStages), (i / kStages) & 1);
       }
     } else if (warp == 3) {
-      // ---------------------------------------------------------- Q rows, V tails
-      uint32_t ring = 0, aux_phase = 0, segs = 0;
-      // Q goes into the operand layout (128-byte swizzle: chunk c of row r lies at chunk
-      // c ^ (r & 7)), row by row.  Rows behind the pair's keep what was there: a row of S, P and
-      // O depends on its own row of Q only, and theirs are not written out.
-      auto load_q = [&](const Seg& g) {
-        for (int r0 = 0; r0 < g.rows; r0 += 32) {
-          const int32_t row = g.row0 + min(r0 + lane, g.rows - 1), t = row / a.g, head = row - t * a.g;
-          int32_t m = g.m, first = t;  // member, and the token among its drafted ones
-          if (!g.resp) {
-            int32_t lo = 0, hi = a.M - 1;  // the last member whose tokens begin at or before t
-            while (lo < hi) {
-              const int32_t mid = (lo + hi + 1) >> 1;
-              if (tok[mid] <= t) lo = mid; else hi = mid - 1;
-            }
-            m = lo;
-            first = t - tok[lo];
-          }
-          const int32_t at = a.n - (tok[m + 1] - tok[m]) + first;  // its row among the member's n
-          const int32_t src = (m * a.n + at) * a.hq + g.kvh * a.g + head;
-#pragma unroll 4
-          for (int k = 0; k < 16; ++k) {
-            const int r = r0 + 2 * k + (lane >> 4), c = lane & 15;
-            const int32_t from = __shfl_sync(0xffffffffu, src, 2 * k + (lane >> 4));
-            if (r < g.rows)
-              cp_async16(sbase + kOffQ + (r >> 7) * kTileBytes + (c >> 3) * kHalfBytes + (r & 127) * 128 +
-                             (((c & 7) ^ (r & 7)) << 4),
-                         static_cast<const __nv_bfloat16*>(a.q) + (int64_t)from * kD + c * 8);
-          }
-        }
-        cp_async_wait_all();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_addr(sbase, B_Q_FULL));
-      };
-      bool ok = true, have = walk.next(&s, cta);
-      if (have) load_q(s);
-      while (ok && have) {
+      // ---------------------------------------------------------- V tails
+      uint32_t ring = 0, aux_phase = 0;
+      bool ok = true;
+      while (ok && walk.next(&s, cta)) {
         const int32_t left = s.len - (s.key0 + (s.count - 1) * kTile);
         ring += 2 * s.count;
-        if (left < kTile) {  // the segment's last tile passes its source's end
-          const uint32_t st = (ring - 1) % kStages;
-          ok = wait_bar(bar_addr(sbase, B_AUX + st), (aux_phase >> st) & 1);
-          if (!ok) break;
-          aux_phase ^= 1u << st;
-          uint8_t* vb = smem + kOffRing + st * kTileBytes;
-          for (int i = left * 8 + lane; i < kTile * 8; i += 32) {
-            *reinterpret_cast<uint4*>(vb + i * 16) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(vb + kHalfBytes + i * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_addr(sbase, B_KV_FULL + st));
+        if (left >= kTile) continue;
+        // the segment's last tile passes its source's end
+        const uint32_t st = (ring - 1) % kStages;
+        ok = wait_bar(bar_addr(sbase, B_AUX + st), (aux_phase >> st) & 1);
+        if (!ok) break;
+        aux_phase ^= 1u << st;
+        uint8_t* vb = smem + kOffRing + st * kTileBytes;
+        for (int i = left * 8 + lane; i < kTile * 8; i += 32) {
+          *reinterpret_cast<uint4*>(vb + i * 16) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(vb + kHalfBytes + i * 16) = make_uint4(0, 0, 0, 0);
         }
-        have = walk.next(&s, cta);
-        if (have) {
-          ok = wait_bar(bar_addr(sbase, B_Q_EMPTY), segs & 1) && !*abort_flag;
-          if (ok) load_q(s);
-        }
-        ++segs;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_addr(sbase, B_KV_FULL + st));
       }
       if (!ok) fail();
     } else if (lane == 0) {
@@ -467,19 +447,16 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
           mma_ss_lo(d_s, dq + off, b0 + off, idS, kk > 0);
         }
       };
-      // P_t V over keys [64 hf, 64 hf + 64): K steps 4 hf .. 4 hf + 3
-      auto issue_pv_half = [&](uint32_t st, int hf, bool accumulate) {
+      auto issue_pv = [&](uint32_t st, bool accumulate) {
         const uint32_t b0 = dv + ((st * kTileBytes) >> 4);
 #pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4) {
-          const int kk = 4 * hf + k4;
+        for (int kk = 0; kk < 8; ++kk)
           mma_ts_lo(d_o, d_p + kk * 8, b0 + ((kk * 2048) >> 4), idPV, (accumulate || kk > 0) ? 1u : 0u);
-        }
       };
       uint32_t seen = 0;
       RingPos<kStages> sp;
-      // ring: loads before the segment; kc: this tile's key tiles so far; both, alone: those of
-      // segments with two row tiles and with one
+      // ring: loads before the segment; segs: segments that this tile has rows in; kc: its key tiles
+      // so far; both, alone: those of segments with two row tiles and with one
       uint32_t ring = 0, segs = 0, kc = 0, both = 0, alone = 0;
       bool ok = true;
       while (ok && walk.next(&s, cta)) {
@@ -495,15 +472,14 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
           }
           return true;
         };
-        ok = wait_bar(bar_addr(sbase, B_Q_FULL), segs & 1) && !*abort_flag;
-        ++segs;
         if (!mine) {
-          ok = ok && need(last);
-          mbar_arrive(bar_addr(sbase, B_Q_EMPTY));
+          ok = need(last) && !*abort_flag;
           ring = last + 1;
           alone += s.count;
           continue;
         }
+        ok = wait_bar(bar_addr(sbase, B_Q_FULL + t), segs & 1) && !*abort_flag;
+        ++segs;
         // The tiles take the one S buffer in turn, A before B.  (Of the barriers below none is
         // ever more than a phase ahead of the one that is waited for.)
         auto s_free = [&](int32_t j) {
@@ -524,20 +500,14 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
             issue_s(ki % kStages);
             mma_commit(bar_addr(sbase, B_S_FULL + t));
             mma_commit(bar_addr(sbase, B_KV_EMPTY + ki % kStages));
-            if (j + 1 == s.count) mma_commit(bar_addr(sbase, B_Q_EMPTY));
           }
           if (j > 0) {
             const uint32_t vi = ring + 2 * j - 1;
-            // first half of P_t (keys [0,64)); the softmax still works on the second
-            ok = need(vi) && wait_bar(bar_addr(sbase, B_P_FULL + 2 * t), kc & 1);
+            ok = need(vi) && wait_bar(bar_addr(sbase, B_P_FULL + t), kc & 1);
             if (!ok || *abort_flag) break;
-            tc_fence_after();
-            issue_pv_half(vi % kStages, 0, j > 1);
-            ok = wait_bar(bar_addr(sbase, B_P_FULL + 2 * t + 1), kc & 1);
-            if (!ok) break;
             ++kc;
             tc_fence_after();
-            issue_pv_half(vi % kStages, 1, true);
+            issue_pv(vi % kStages, j > 1);
             mma_commit(bar_addr(sbase, B_PV_DONE + t));
             if (j == s.count) mma_commit(bar_addr(sbase, B_O_DONE + t));
             mma_commit(bar_addr(sbase, B_KV_EMPTY + vi % kStages));
@@ -566,18 +536,61 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_addr(sbase, bar));
     };
+    // The next segment that this tile has rows in.
+    auto next = [&]() {
+      while (walk.next(&s, cta))
+        if (s.rows > t * kTile) return true;
+      return false;
+    };
+    // This warp's Q rows of segment s, into the operand layout (128-byte swizzle: chunk c of row r
+    // lies at chunk c ^ (r & 7)).  Rows behind the segment's keep what was there: a row of S, P and
+    // O depends on its own row of Q only, and theirs are not written out.
+    auto load_q = [&]() {
+      const int r0 = quad * 32, rows = s.rows - t * kTile;
+      if (r0 >= rows) return;
+      const int32_t x = s.row0 + t * kTile + min(r0 + lane, rows - 1), at = x / a.g, head = x - at * a.g;
+      int32_t m = s.m, first = at;  // member, and the token among its drafted ones
+      if (!s.resp) {
+        int32_t lo = 0, hi = a.M - 1;  // the last member whose tokens begin at or before `at`
+        while (lo < hi) {
+          const int32_t mid = (lo + hi + 1) >> 1;
+          if (tok[mid] <= at) lo = mid; else hi = mid - 1;
+        }
+        m = lo;
+        first = at - tok[lo];
+      }
+      const int32_t src = (m * a.n + a.n - (tok[m + 1] - tok[m]) + first) * a.hq + s.kvh * a.g + head;
+      const int c = lane & 15;
+      const uint32_t dst = sbase + kOffQ + t * kTileBytes + (c >> 3) * kHalfBytes;
+#pragma unroll 8
+      for (int k = 0; k < 16; ++k) {
+        const int r = r0 + 2 * k + (lane >> 4);
+        const int32_t from = __shfl_sync(0xffffffffu, src, 2 * k + (lane >> 4));
+        if (r < rows)
+          cp_async16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                     static_cast<const __nv_bfloat16*>(a.q) + (int64_t)from * kD + c * 8);
+      }
+    };
+    auto q_loaded = [&]() {
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      signal(B_Q_FULL + t);
+    };
     uint32_t kc = 0, oc = 0;
-    bool ok = true;
-    while (ok && walk.next(&s, cta)) {
+    bool ok = true, have = next();
+    if (have) {
+      load_q();
+      q_loaded();
+    }
+    while (ok && have) {
       const int32_t rows = s.rows - t * kTile;  // of this tile
-      if (rows <= 0) continue;
       const int taken = s.two() ? B_S_TAKEN + t : B_S_ALONE;
       const bool idle = quad * 32 >= rows;  // the whole warp is padding
       // keys from its first key tile on that every row sees: the source's, or the context
       int32_t lim = s.len - s.key0, pad = 0;
       const uint32_t* bits = nullptr;
       if (s.resp) {
-        const int32_t drafted = drafted_tokens(a, s.m);
+        const int32_t drafted = tok[s.m + 1] - tok[s.m];
         pad = a.n - drafted;
         lim -= drafted;
         const int32_t at = min(s.row0 + t * kTile + row, s.row0 + s.rows - 1) / a.g;
@@ -593,8 +606,7 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
           signal(taken);
           ok = settled();
           if (!ok) break;
-          signal(B_P_FULL + 2 * t);
-          signal(B_P_FULL + 2 * t + 1);
+          signal(B_P_FULL + t);
           continue;
         }
         tc_fence_after();
@@ -667,7 +679,7 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
         float2 ls4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                          make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {  // P in two 64-key halves, released one by one
+        for (int half = 0; half < 2; ++half) {  // P in two halves of 64 keys
           uint32_t pk[32];
 #pragma unroll
           for (int jj = 0; jj < 32; ++jj) {
@@ -687,21 +699,31 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
             tc_fence_after();
           }
           tmem_st32(p_col + half * 32, pk);
-          tmem_wait_st();
-          signal(B_P_FULL + 2 * t + half);
         }
         if (!ok) break;
+        tmem_wait_st();
+        signal(B_P_FULL + t);
         const float2 lsa = __fadd2_rn(__fadd2_rn(ls4[0], ls4[1]), __fadd2_rn(ls4[2], ls4[3]));
         const float ls = lsa.x + lsa.y;
         const float tsum = l + ls;
         lcomp += (l - tsum) + ls;
         l = tsum;
       }
-      ok = ok && wait_bar(bar_addr(sbase, B_O_DONE + t), oc & 1);
+      if (!ok) break;
+      // the next segment's Q rows (this one's last S is done), while P V is
+      const int64_t prow = s.part + t * kTile + row;
+      if (tid == 128 && s.resp) {
+        int32_t* range = cta_range(a, s.m, s.row0 / kPair, s.kvh);
+        if (s.key0 == 0) range[0] = cta - plan.cp;
+        if (s.len - s.key0 <= s.count * kTile) range[1] = cta - plan.cp;
+      }
+      have = next();
+      if (have) load_q();
+      ok = wait_bar(bar_addr(sbase, B_O_DONE + t), oc & 1);
       if (!ok) break;
       ++oc;
+      if (have) q_loaded();
       if (!idle) {
-        const int64_t prow = s.part + t * kTile + row;
         tc_fence_after();
         const float lt = l + lcomp;
         const float inv = lt == 0.f ? 0.f : 1.f / lt;  // a row that sees no key here
@@ -742,62 +764,30 @@ constexpr int kCombineWarps = 8;
 
 __global__ void __launch_bounds__(kCombineWarps * 32)
 tree_combine(const __grid_constant__ LsDecodeArgs a) {
-  __shared__ int32_t sums[2][kCombineWarps];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t octets = (a.n * a.g + 7) >> 3, m = blockIdx.x / octets, h = blockIdx.y;
   // the row among the member's n g, the drafted ones last
   const int32_t row = 8 * (blockIdx.x - m * octets) + warp, tokens = drafted_tokens(a, m);
   const int32_t mrow = row - (a.n - tokens) * a.g;  // among the drafted ones
-  int32_t before = 0, units = 0;  // tokens and units of the members before
-  for (int i = tid; i < m; i += kCombineWarps * 32) {
-    before += drafted_tokens(a, i);
-    units += member_units(a, i);
-  }
-  before = __reduce_add_sync(0xffffffffu, before);
-  units = __reduce_add_sync(0xffffffffu, units);
-  if (lane == 0) {
-    sums[0][warp] = before;
-    sums[1][warp] = units;
-  }
-  __syncthreads();
-  before = units = 0;
-#pragma unroll
-  for (int i = 0; i < kCombineWarps; ++i) {
-    before += sums[0][i];
-    units += sums[1][i];
-  }
+  const bool resp = clamp_len(a, __ldg(a.lens + m)) > 0;
   // Rows that are not written (padding, members out of use) wait all the same: the stream goes
   // on when this grid ends.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (mrow < 0 || row >= a.n * a.g) return;
-  const Plan* pp = static_cast<const Plan*>(a.plan);
-  const int32_t np = __ldcg(&pp->np), strips = __ldcg(&pp->strips);
-  const int32_t all = __ldcg(&pp->units), rcs = __ldcg(&pp->rcs);
-  const int32_t prow = before * a.g + mrow, pair = prow / kPair;
+  const Out* out = static_cast<const Out*>(a.plan);
+  const int32_t rpair = mrow / kPair;
+  const int32_t* range = cta_range(a, m, rpair, h);
+  const int32_t np = __ldcg(&out->plan.np), strips = __ldcg(&out->plan.strips);
+  const int32_t prow = __ldcg(out->tok + m) * a.g + mrow, pair = prow / kPair;
+  const int32_t rc = resp ? __ldcg(range) : 0, segs = resp ? __ldcg(range + 1) + 1 - rc : 0;
   const int64_t prompt0 = (int64_t)(h * strips * np + pair) * kPair + (prow - pair * kPair);
-  // the response's units that are this row's tiles
-  const int32_t rpair = mrow / kPair, iu = item_units(a, m), nt = iu - kSegTiles;
-  const int32_t u0 = units + (rpair * a.hkv + h) * iu + kSegTiles;
-  int32_t rc = 0, rc_end = 0;  // response CTAs that have some of them
-  if (nt > 0) {
-    rc = (int32_t)((long long)u0 * rcs / all);
-    while (rc > 0 && unit_bound(all, rc, rcs) > u0) --rc;
-    while (unit_bound(all, rc + 1, rcs) <= u0) ++rc;
-    rc_end = rc + 1;
-    while (rc_end < rcs && unit_bound(all, rc_end, rcs) < u0 + nt) ++rc_end;
-  }
-  const int32_t count = strips + rc_end - rc;
   const int64_t resp0 = resp_row0(a, m, rpair, h, rc) + (mrow - rpair * kPair);
+  const int32_t count = strips + segs;
   auto part_row = [&](int32_t k) {
     return k < strips ? prompt0 + (int64_t)k * np * kPair
                       : resp0 + (int64_t)(k - strips) * resp_rows_of(a);
   };
-  float mx = -INFINITY;
-  for (int32_t k = lane; k < count; k += 32) mx = fmaxf(mx, __ldcg(a.part_lse + part_row(k)));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  const float sub = mx == -INFINITY ? 0.f : mx;
-  float sum = 0.f;
+  float mx = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int kBatch = 4;
   for (int32_t k0 = 0; k0 < count; k0 += kBatch) {
@@ -812,10 +802,16 @@ tree_combine(const __grid_constant__ LsDecodeArgs a) {
         v[b] = *reinterpret_cast<const float4*>(part_at(a, r) + lane * 32);
       }
     }
+    const float top = fmaxf(mx, fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])));
+    if (top == -INFINITY) continue;
+    const float old = exp2f(mx - top);
+    mx = top;
+    sum *= old;
+    acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       if (l[b] == -INFINITY) continue;  // a part that saw no key adds nothing
-      const float w = exp2f(l[b] - sub);
+      const float w = exp2f(l[b] - mx);
       sum += w;
       acc.x = fmaf(w, v[b].x, acc.x);
       acc.y = fmaf(w, v[b].y, acc.y);
@@ -824,15 +820,17 @@ tree_combine(const __grid_constant__ LsDecodeArgs a) {
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key at all: o = 0, lse = -inf
-  const int64_t out = ((int64_t)m * a.n + row / a.g) * a.hq + h * a.g + row % a.g;
-  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + out * kD + lane * 4) =
+  const int64_t to = ((int64_t)m * a.n + row / a.g) * a.hq + h * a.g + row % a.g;
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + to * kD + lane * 4) =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (lane == 0) a.lse[out] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+  if (lane == 0) a.lse[to] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
 }  // namespace
 
-size_t ls_tree_plan_bytes() { return sizeof(Plan); }
+size_t ls_tree_plan_bytes(const LsDecodeArgs& a) {
+  return sizeof(Out) + (size_t)a.M * max_pairs(a) * a.hkv * 2 * sizeof(int32_t);
+}
 int64_t ls_tree_part_rows(const LsDecodeArgs& a) {
   const int64_t slots = (int64_t)a.M * max_pairs(a) * a.hkv + a.cols;
   return prompt_rows_of(a) + slots * resp_rows_of(a);
