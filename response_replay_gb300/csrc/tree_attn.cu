@@ -758,22 +758,21 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
 }
 
 // Merge a row's partials: lse = log2 sum 2^lse_k, o = sum 2^(lse_k - lse) o_k, in a fixed
-// order.  A warp a row, a lane four values; a block takes eight rows of one member and KV head,
-// whose partials lie in the same lines.
+// order.  A block takes eight drafted rows of one member and KV head, a thread four values of one
+// of them: a warp's loads are whole lines of the partials (eight rows, four values of each in turn).
 constexpr int kCombineWarps = 8;
 
 __global__ void __launch_bounds__(kCombineWarps * 32)
 tree_combine(const __grid_constant__ LsDecodeArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t octets = (a.n * a.g + 7) >> 3, m = blockIdx.x / octets, h = blockIdx.y;
-  // the row among the member's n g, the drafted ones last
-  const int32_t row = 8 * (blockIdx.x - m * octets) + warp, tokens = drafted_tokens(a, m);
-  const int32_t mrow = row - (a.n - tokens) * a.g;  // among the drafted ones
+  const int32_t tokens = drafted_tokens(a, m), chunk = warp * 4 + (lane >> 3);
+  const int32_t mrow = 8 * (blockIdx.x - m * octets) + (lane & 7);  // among the drafted ones
   const bool resp = clamp_len(a, __ldg(a.lens + m)) > 0;
   // Rows that are not written (padding, members out of use) wait all the same: the stream goes
   // on when this grid ends.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (mrow < 0 || row >= a.n * a.g) return;
+  if (mrow >= tokens * a.g) return;
   const Out* out = static_cast<const Out*>(a.plan);
   const int32_t rpair = mrow / kPair;
   const int32_t* range = cta_range(a, m, rpair, h);
@@ -799,7 +798,7 @@ tree_combine(const __grid_constant__ LsDecodeArgs a) {
       if (k0 + b < count) {
         const int64_t r = part_row(k0 + b);
         l[b] = __ldcg(a.part_lse + r);
-        v[b] = *reinterpret_cast<const float4*>(part_at(a, r) + lane * 32);
+        v[b] = *reinterpret_cast<const float4*>(part_at(a, r) + chunk * 32);
       }
     }
     const float top = fmaxf(mx, fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])));
@@ -820,10 +819,11 @@ tree_combine(const __grid_constant__ LsDecodeArgs a) {
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key at all: o = 0, lse = -inf
+  const int32_t row = (a.n - tokens) * a.g + mrow;  // the drafted ones are the member's last
   const int64_t to = ((int64_t)m * a.n + row / a.g) * a.hq + h * a.g + row % a.g;
-  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + to * kD + lane * 4) =
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + to * kD + chunk * 4) =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (lane == 0) a.lse[to] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+  if (chunk == 0) a.lse[to] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
 }  // namespace
