@@ -32,6 +32,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kGroupBytes = 64;
 constexpr int kGmaxBytes = 20480;  // group maxima of a part, of the logits' type
 constexpr int kBwdThreads = 256, kBwdCtas = 5;  // of the backward, and blocks an SM
+constexpr float kLargeSum = 2048.f;  // of 2^t t: t = 8, or many somewhat below
 constexpr double kLn2d = 0.69314718055994530942;
 constexpr double kLog2ed = 1.4426950408889634074;
 
@@ -141,8 +142,8 @@ __device__ __forceinline__ u64 merge32(u64 list, u64 batch, int lane) {
   return x;
 }
 
-// A reference m (one of the logits; none passes it by more than 2^100, or it is moved), s =
-// sum 2^t, e = sum 2^t t with t = z c - r, r = m c rounded: one multiply-add an exponent.  Where m c
+// A reference m (a logit, or a number between logits; none passes it by more than 2^8, or it is
+// moved), s = sum 2^t, e = sum 2^t t with t = z c - r, r = m c rounded: one multiply-add an exponent.  Where m c
 // is too large for that (a row of a type's lowest values), t = (z - m) c.
 struct Stat {
   float m, s, e;
@@ -187,10 +188,12 @@ struct Sums {
   __device__ __forceinline__ explicit Sums(float c_)
       : m(-INFINITY), nr(INFINITY), c(c_), s(make_float2(0.f, 0.f)), e(make_float2(0.f, 0.f)) {}
 
-  // N vectors of 16 bytes.  The reference stays as it is as long as the sums are numbers of a
-  // usual size: of 32 threads one would find a new maximum in most groups, and the warp would
-  // move its sums with each.  Otherwise (the first group, a logit that passes the reference by
-  // far, an exponent of -inf, NaN) the vectors are taken once more, carefully.
+  // N vectors of 16 bytes.  The reference stays as it is as long as no logit passes it by far: of
+  // 32 threads one would find a new maximum in most groups, and the warp would move its sums with
+  // each.  Otherwise (the first group, sums of exponents about 8 and more, an exponent of -inf,
+  // NaN) the vectors are taken once more, carefully.  An exponent of the row's likeliest tokens
+  // is off by half a step of its size, which that limit keeps to 2^-22: entropies of 1 are within
+  // 2e-7 (relative, root mean square); with a limit of 2^100 they were off by 3e-6.
   template <int N>
   __device__ __forceinline__ void add(const uint4* u) {
     const float2 s0 = s, e0 = e, b = make_float2(nr, nr), c2 = make_float2(c, c);
@@ -206,7 +209,7 @@ struct Sums {
         e = __ffma2_rn(p, t, e);
       }
     }
-    if (!(fabsf(e.x + e.y) < 1e30f)) {
+    if (!(e.x + e.y < kLargeSum)) {
       s = s0;
       e = e0;
       carefully<N>(u);
@@ -223,6 +226,8 @@ struct Sums {
 #pragma unroll
       for (int i = 0; i < H; ++i) mx = fmaxf(mx, x[i]);
     }
+    // many exponents below the limit that make a sum near it: the reference goes behind them
+    if (e.x + e.y > kLargeSum / 2) mx = fmaxf(mx, m + log2f(s.x + s.y) / c);
     if (mx > m) {
       const Stat x = move(stat(), mx, c);
       s = make_float2(x.s, 0.f);

@@ -990,11 +990,11 @@ def accept_draft(parents: torch.Tensor, tokens: torch.Tensor, chosen: torch.Tens
     st = _dev_stream(dev)
     tp = _dense(tokens, "tokens", torch.int32, (M, n), dev)
     cp = _dense(chosen, "chosen", torch.int32, (M, n), dev)
-    out = torch.empty(M * (n + 3), dtype=torch.int32, device=parents.device)
-    rows, count, follow, ends = out.split((M * n, M, M, M))
-    p, k = out.data_ptr(), 4 * M
-    B.ls_accept_draft(pp, tp, cp, lp, dp, M, n, p, p + k * n, p + k * (n + 1), p + k * (n + 2), st)
-    return rows.view(M, n), count, follow, ends
+    rows = torch.empty((M, n), dtype=torch.int32, device=parents.device)
+    count, follow, ends = (torch.empty_like(lens) for _ in range(3))
+    B.ls_accept_draft(pp, tp, cp, lp, dp, M, n, rows.data_ptr(), count.data_ptr(),
+                      follow.data_ptr(), ends.data_ptr(), st)
+    return rows, count, follow, ends
 
 
 class LayerPools:
@@ -1144,21 +1144,22 @@ def token_logp_fwd(logits: torch.Tensor, targets: torch.Tensor | None, temperatu
     dev, T, V, dt, p, rs = _logits(logits)
     st = _dev_stream(dev)
     tp = None if targets is None else _dense(targets, "targets", torch.int32, (T,), dev)
-    f32 = dict(dtype=torch.float32, device=logits.device)
-    stats = torch.empty((3, T), **f32)
-    sp = stats.data_ptr()
-    logp, lse, entropy = stats.unbind(0)
-    top_logp = top_ids = lp = ip = None
+    lse = torch.empty(T, dtype=torch.float32, device=logits.device)
+    entropy = torch.empty_like(lse)
+    logp = top_logp = top_ids = gp = lp = ip = None
+    if targets is not None:
+        logp = torch.empty_like(lse)
+        gp = logp.data_ptr()
     if top > 0:
-        top_logp = torch.empty((T, top), **f32)
+        top_logp = torch.empty((T, top), dtype=torch.float32, device=logits.device)
         top_ids = torch.empty((T, top), dtype=torch.int32, device=logits.device)
         lp, ip = top_logp.data_ptr(), top_ids.data_ptr()
     if T > 0:
         _with_workspace(B.ls_token_logp_fwd,
-                        (p, dt, T, V, rs, tp, temperature, top, sp if targets is not None else None,
-                         sp + 4 * T, sp + 8 * T, lp, ip),
+                        (p, dt, T, V, rs, tp, temperature, top, gp, lse.data_ptr(),
+                         entropy.data_ptr(), lp, ip),
                         lambda: B.ls_token_logp_fwd_workspace(dt, T, V, top), logits, "token_logp", st)
-    return (logp if targets is not None else None), lse, entropy, top_logp, top_ids
+    return logp, lse, entropy, top_logp, top_ids
 
 
 def token_logp_bwd(logits: torch.Tensor, targets: torch.Tensor | None, lse: torch.Tensor,
