@@ -97,6 +97,39 @@ def test_equal_logits(cuda, T, V, dt, top):
     check_fwd(z, y, 1.0, top)
 
 
+@pytest.mark.parametrize("T,V,dt,temp", [(300, 50257, F32, 0.7), (300, 50257, F32, 1.0), (200, 100003, BF, 1.4)])
+def test_entropies_of_likely_tokens(cuda, T, V, dt, temp):
+    """Likely tokens far above the logits that a thread meets first.  Their exponents are taken
+    against a number at most 2^8 below (half a step of 8: 2^-22) and moved to the row's maximum
+    (16: 2^-21); a weight is off by as much, relatively, and moves the entropy by its share of
+    |log p + H|.  Root mean square over the rows, so the roundings' largest sizes bound it with
+    room for the sums' own."""
+    z, y, _ = rows(cuda, T, V, dt, seed=3)
+    _, _, ent, _, _ = api.token_logp_fwd(z, y, temperature=temp)
+    x = z.double() / temp
+    lp = x - torch.logsumexp(x, -1, keepdim=True)
+    p = lp.exp()
+    h = -(p * lp).sum(-1)
+    spread = (p * (lp + h[:, None]).abs()).sum(-1)
+    rms = lambda t: float((t ** 2).mean().sqrt())
+    assert rms(ent.double() - h) <= 2.0 ** -21 * rms(1 + spread)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("rise", [2.0, 5.0, 5.5, 6.0, 30.0])
+def test_rows_in_steps(cuda, dt, rise):
+    """Rows that rise by steps about as high as the reference of a sum may lie below a logit, with
+    many equal logits a step, and small rises between."""
+    V = 150000
+    at = torch.arange(V, device=cuda) // 25000
+    z = torch.stack([at * rise, at * rise + (torch.arange(V, device=cuda) // 7000) % 3 * 0.25,
+                     torch.where(torch.arange(V, device=cuda) % 5 == 0, at * rise, at * rise - 9)])
+    z = z.repeat(60, 1).to(dt)
+    y = torch.arange(180, device=cuda, dtype=torch.int32)
+    check_fwd(z, y, 1.0, 0)
+    check_fwd(z[:3], y[:3], 1.0, 4)
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("order", ["up", "down", "columns", "threads"])
 def test_orders_of_a_row(cuda, dt, order):
