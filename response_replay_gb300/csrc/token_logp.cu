@@ -17,7 +17,7 @@
 // only groups whose maximum does can hold one of the k largest.  It reads those groups again
 // (about 40 of 9,500 for k = 20) and sorts the logits that pass.
 // A row too long for the group maxima, or a call with few rows, is cut into parts whose results
-// a second kernel merges.
+// a second kernel merges.  Short rows go to a warp or a few each (logp_rows).
 // Sums are in fp32 (a thread adds V / 512 terms, then a tree), the last steps in fp64.
 #include <math.h>
 
@@ -450,6 +450,39 @@ __device__ __forceinline__ void put_max<__nv_bfloat16>(FwdSmem& sm, int g, float
   reinterpret_cast<uint16_t*>(sm.gmax)[g] = (uint16_t)(__float_as_uint(x) >> 16);
 }
 
+// The 32 largest of a list and `found` more, sorted, one a lane.  (The list is empty in every lane
+// or in none.)
+__device__ __forceinline__ u64 order_found(u64* buf, int found, u64 list, int lane) {
+  if (found > kRanked || list != 0) {
+    for (int i = 0; i < found; i += 32)
+      list = merge32(list, sort32(i + lane < found ? buf[i + lane] : 0ull, lane), lane);
+    return list;
+  }
+  // each one's place is the number of larger ones
+  u64 mine[kRanked / 32];
+  int rank[kRanked / 32];
+#pragma unroll
+  for (int i = 0; i < kRanked / 32; ++i) {
+    mine[i] = i * 32 + lane < found ? buf[i * 32 + lane] : 0ull;
+    rank[i] = 0;
+  }
+  if (lane == 0) buf[found] = 0ull;
+  __syncwarp();
+  for (int j = 0; j < found; j += 2) {
+    const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(buf + j);
+#pragma unroll
+    for (int i = 0; i < kRanked / 32; ++i) rank[i] += (y.x > mine[i]) + (y.y > mine[i]);
+  }
+  __syncwarp();
+  buf[lane] = 0ull;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kRanked / 32; ++i)
+    if (mine[i] != 0 && rank[i] < 32) buf[rank[i]] = mine[i];
+  __syncwarp();
+  return buf[lane];
+}
+
 // The 32 largest logits of an item, sorted, one a lane, by one warp: of the groups that reach the
 // threshold, or (more of them than the list holds: rows whose largest logits all lie with the
 // same threads) of all groups.
@@ -497,34 +530,7 @@ __device__ u64 pick(FwdSmem& sm, const Item<E>& it, const FwdArgs& a, int par, i
       __syncwarp();
     }
   }
-  if (found <= kRanked && list == 0) {  // (the list is empty in every lane or in none)
-    // each one's place is the number of larger ones
-    u64 mine[kRanked / 32];
-    int rank[kRanked / 32];
-#pragma unroll
-    for (int i = 0; i < kRanked / 32; ++i) {
-      mine[i] = i * 32 + lane < found ? sm.found[i * 32 + lane] : 0ull;
-      rank[i] = 0;
-    }
-    if (lane == 0) sm.found[found] = 0ull;
-    __syncwarp();
-    for (int j = 0; j < found; j += 2) {
-      const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(sm.found + j);
-#pragma unroll
-      for (int i = 0; i < kRanked / 32; ++i) rank[i] += (y.x > mine[i]) + (y.y > mine[i]);
-    }
-    __syncwarp();
-    sm.found[lane] = 0ull;
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kRanked / 32; ++i)
-      if (mine[i] != 0 && rank[i] < 32) sm.found[rank[i]] = mine[i];
-    __syncwarp();
-    list = sm.found[lane];
-  } else {
-    for (int i = 0; i < found; i += 32)
-      list = merge32(list, sort32(i + lane < found ? sm.found[i + lane] : 0ull, lane), lane);
-  }
+  list = order_found(sm.found, found, list, lane);
   __syncwarp();
   return list;
 }
@@ -776,6 +782,277 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
   }
 }
 
+// ---------------------------------------------------------------- forward, many rows
+//
+// With many rows a streaming CTA a row would spend its time between rows: its results, threshold
+// and candidates take as long as 100 KB of logits.  Here W warps take a row, 8 / W rows a CTA, and
+// the other rows on the SM cover that time.  A group is a vector of 16 bytes (the values in front of
+// the row's first whole vector are group 0, those behind its last one the last group); the two
+// largest of every lane's groups (of every lane's, where several warps share a row) make the
+// threshold, and the groups that reach it are read again.
+constexpr int kRowsThreads = 256;
+constexpr int kRowsWarps = kRowsThreads / 32;
+constexpr int kRowsCand = 256;                  // groups that reach the threshold
+constexpr int kRowsFound = 32 * 8 + kRanked;    // values that are found before they are ordered
+
+struct RowSmem {
+  Stat red[kRowsWarps];
+  int cands;
+  alignas(16) uint32_t tops[64];
+  int topg[64];
+  alignas(16) u64 found[kRowsFound];
+  uint16_t cand[kRowsCand];
+};
+
+template <int W>
+__device__ __forceinline__ void row_sync(int group) {
+  if (W == 1)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * W) : "memory");
+}
+
+// A row as vectors of 16 bytes.
+template <typename E>
+struct Vecs {
+  static constexpr int N = Row<E>::N;
+  const E* zr;
+  int V, head, nvec, tail;  // values in front, whole vectors, values behind
+  __device__ __forceinline__ Vecs(const E* z, int V_) : zr(z), V(V_) {
+    const int in = (int)((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(E));
+    head = min(in ? N - in : 0, V);
+    nvec = (V - head) / N;
+    tail = V - head - nvec * N;
+  }
+  __device__ __forceinline__ const uint4* vec(int i) const { return reinterpret_cast<const uint4*>(zr + head) + i; }
+  __device__ __forceinline__ int groups() const { return nvec + 2; }
+  // values of group g and the place of the first; what is not in the row is NaN
+  __device__ __forceinline__ int values(int g, float* x) const {
+    if (g > 0 && g <= nvec) {
+      Row<E>::unpack(*vec(g - 1), x);
+      return head + (g - 1) * N;
+    }
+    const int at = g == 0 ? 0 : head + nvec * N, n = g == 0 ? head : tail;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = i < n ? Row<E>::load(zr + at + i) : NAN;
+    return at;
+  }
+};
+
+template <typename E>
+__device__ __forceinline__ float vec_max(const uint4& u);
+template <>
+__device__ __forceinline__ float vec_max<float>(const uint4& u) {
+  return fmaxf(fmax3(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z)), __uint_as_float(u.w));
+}
+template <>
+__device__ __forceinline__ float vec_max<__nv_bfloat16>(const uint4& u) {
+  auto max2 = [](uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+  };
+  const uint32_t m = max2(max2(u.x, u.y), max2(u.z, u.w));
+  return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+}
+
+template <typename E, bool kTop, int W>
+__global__ void __launch_bounds__(kRowsThreads, 4) logp_rows(const FwdArgs a, int cap) {
+  using R = Row<E>;
+  extern __shared__ __align__(16) uint8_t rows_smem[];
+  const int lane = threadIdx.x & 31, group = (threadIdx.x >> 5) / W, wl = (threadIdx.x >> 5) % W;
+  const int l = wl * 32 + lane;
+  constexpr int L = 32 * W;
+  RowSmem& sm = reinterpret_cast<RowSmem*>(rows_smem)[group];
+  // the upper halves of the groups' maxima, as whole numbers in their order
+  uint16_t* gmax = reinterpret_cast<uint16_t*>(rows_smem + (kRowsWarps / W) * sizeof(RowSmem)) + group * cap;
+  const int64_t row = (int64_t)blockIdx.x * (kRowsWarps / W) + group;
+  if (row >= a.T) return;  // (a row's warps leave together)
+  if (a.targets && __ldg(a.targets + row) == -1) {
+    if (wl == 0) padding_row(a, row, lane);
+    return;
+  }
+  const Vecs<E> v(static_cast<const E*>(a.logits) + row * a.ld, a.V);
+  float zy = 0.f;
+  bool has_y = false;
+  if (l == 0) has_y = target_logit<E>(a, row, &zy);
+  if (kTop && l == 0) sm.cands = 0;
+
+  Sums<E> sums(a.c);
+  uint32_t best = 0, second = 0;  // the largest of this lane's groups, the next (0: none)
+  int bestg = -1, secondg = -1;
+  auto take = [&](int g, float mx) {
+    const uint32_t o = order_of(mx);
+    gmax[g] = (uint16_t)(o >> 16);
+    if (o > best) {
+      if (W == 1) {
+        second = best;
+        secondg = bestg;
+      }
+      best = o;
+      bestg = g;
+    } else if (W == 1 && o > second) {
+      second = o;
+      secondg = g;
+    }
+  };
+  // one value outside the vectors a lane: the head's, then the tail's
+  float edge = NAN;
+  const bool in_head = l < v.head, has_edge = l < v.head + v.tail;
+  if (has_edge) edge = R::load(v.zr + (in_head ? l : v.nvec * Vecs<E>::N + l));
+  if (kTop) {  // (their maxima: the first lanes are one warp's)
+    if (wl == 0) {
+      const uint32_t o = has_edge ? order_of(edge) : 0u;
+      const uint32_t oh = __reduce_max_sync(0xffffffffu, in_head ? o : 0u);
+      const uint32_t ot = __reduce_max_sync(0xffffffffu, in_head ? 0u : o);
+      if (lane == 0) {
+        gmax[0] = (uint16_t)(oh >> 16);
+        gmax[v.nvec + 1] = (uint16_t)(ot >> 16);
+      }
+      if (in_head && o) {
+        best = o;
+        bestg = 0;
+      }
+    }
+  }
+  int i = l;
+#pragma unroll 1
+  for (; i + 3 * L < v.nvec; i += 4 * L) {
+    uint4 u[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) u[k] = __ldg(v.vec(i + k * L));
+    sums.template add<4>(u);
+    if (kTop) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) take(i + k * L + 1, vec_max<E>(u[k]));
+    }
+  }
+#pragma unroll 1
+  for (; i < v.nvec; i += L) {
+    const uint4 u = __ldg(v.vec(i));
+    sums.template add<1>(&u);
+    if (kTop) take(i + 1, vec_max<E>(u));
+  }
+  if (kTop && has_edge && !in_head) {
+    const uint32_t o = order_of(edge);
+    if (o > best) {
+      second = best;
+      secondg = bestg;
+      best = o;
+      bestg = v.nvec + 1;
+    } else if (o > second) {
+      second = o;
+      secondg = v.nvec + 1;
+    }
+  }
+  Stat st = sums.stat();
+  if (has_edge) {
+    const float one = edge == -INFINITY ? 0.f : 1.f + (edge - edge);  // NaN of NaN and of +inf
+    st = merge(st, Stat{edge != edge ? -INFINITY : edge, one, one - one}, a.c);
+  }
+  st = warp_stat(st, a.c);
+  if (W > 1 && lane == 0) sm.red[wl] = st;
+
+  uint32_t floor_o = 0;
+  int floor_g = INT32_MAX;
+  if (kTop) {
+    if (W <= 2) {
+      const int at = W == 1 ? 2 * lane : l;
+      sm.tops[at] = best;
+      sm.topg[at] = bestg;
+      if (W == 1) {
+        sm.tops[at + 1] = second;
+        sm.topg[at + 1] = secondg;
+      }
+    } else {  // the largest 64 / W of every warp's lanes
+      uint32_t o = best;
+      for (int k = wl; k < 64; k += W) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, o);
+        const uint32_t at = __reduce_min_sync(0xffffffffu, o == top ? (uint32_t)bestg : 0xffffffffu);
+        if (lane == 0) {
+          sm.tops[k] = top;
+          sm.topg[k] = top ? (int)at : -1;
+        }
+        if (o == top && (uint32_t)bestg == at) o = 0u;
+      }
+    }
+    row_sync<W>(group);
+    // the top-th of them: the lowest of those with fewer than top above them, and the last place
+    // among its equals
+    const uint32_t x = sm.tops[lane], x2 = sm.tops[lane + 32];
+    const uint4* all = reinterpret_cast<const uint4*>(sm.tops);
+    int above = 0, above2 = 0;
+#pragma unroll 4
+    for (int k = 0; k < 16; ++k) {
+      const uint4 y = all[k];
+      above += (y.x > x) + (y.y > x) + (y.z > x) + (y.w > x);
+      above2 += (y.x > x2) + (y.y > x2) + (y.z > x2) + (y.w > x2);
+    }
+    floor_o = __reduce_min_sync(0xffffffffu, min(above < a.top ? x : 0xffffffffu, above2 < a.top ? x2 : 0xffffffffu));
+    floor_g = __reduce_max_sync(0xffffffffu, max(x == floor_o ? sm.topg[lane] : -1, x2 == floor_o ? sm.topg[lane + 32] : -1));
+    if (floor_o == 0) floor_g = INT32_MAX;  // fewer groups than alternatives: all of them
+    const uint32_t floor16 = floor_o >> 16;
+    const int n = v.groups();
+    for (int g0 = l * 8; g0 < n; g0 += L * 8) {
+      const uint4 w = *reinterpret_cast<const uint4*>(gmax + g0);
+      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t o = k & 1 ? ws[k >> 1] >> 16 : ws[k >> 1] & 0xffffu;
+        if (o >= floor16 && g0 + k < n) {
+          const int at = atomicAdd(&sm.cands, 1);
+          if (at < kRowsCand) sm.cand[at] = (uint16_t)(g0 + k);
+        }
+      }
+    }
+  }
+  if (W > 1 || kTop) row_sync<W>(group);
+  if (wl != 0) return;
+  if (W > 1) st = warp_stat(lane < W ? sm.red[lane] : Stat{-INFINITY, 0.f, 0.f}, a.c);
+  double lse = 0.0;
+  if (lane == 0) lse = finish_row(a, st, row, has_y, zy);
+  if (!kTop) return;
+  lse = __shfl_sync(0xffffffffu, lse, 0);
+
+  // ---- the candidates' values, or (more of them than the list holds) all values
+  const bool every = sm.cands > kRowsCand;
+  const int n = every ? v.groups() : sm.cands;
+  u64 kth = 0, list = 0;
+  int found = 0;
+  for (int j0 = 0; j0 < n; j0 += 32) {
+    const int j = j0 + lane;
+    float x[Vecs<E>::N];
+    int place = 0;
+    const int g = j < n ? (every ? j : sm.cand[j]) : -1;
+    if (g >= 0) {
+      place = v.values(g, x);
+    } else {
+#pragma unroll
+      for (int k = 0; k < Vecs<E>::N; ++k) x[k] = NAN;
+    }
+#pragma unroll
+    for (int k = 0; k < Vecs<E>::N; ++k) {
+      const uint32_t o = order_of(x[k]);
+      const u64 key = (u64)o << 32 | (uint32_t)~(uint32_t)(place + k);
+      const bool in = o != 0 && (o > floor_o || (o == floor_o && g <= floor_g)) && key > kth;
+      const uint32_t mask = __ballot_sync(0xffffffffu, in);
+      if (mask == 0) continue;
+      if (in) sm.found[found + __popc(mask & ((1u << lane) - 1))] = key;
+      found += __popc(mask);
+    }
+    __syncwarp();
+    if (found >= kRanked) {  // as many as are put in order by counting
+      while (found >= 32) {
+        found -= 32;
+        list = merge32(list, sort32(sm.found[found + lane], lane), lane);
+      }
+      kth = __shfl_sync(0xffffffffu, list, a.top - 1);
+      __syncwarp();
+    }
+  }
+  write_top(a, row, order_found(sm.found, found, list, lane), lse, lane);
+}
+
 // Rows that were cut into parts: a block a row, its warps take the parts by turns and their
 // results meet in pairs.
 constexpr int kMergeWarps = 8;
@@ -1006,9 +1283,38 @@ int groups_of(bool is_bf16, int V) {  // of a row that begins inside a group
 }
 }  // namespace
 
+namespace {
+size_t rows_smem_bytes(int cap, bool top, int W) {
+  const size_t rows = kRowsWarps / W;
+  if (!top) return W > 1 ? rows * sizeof(RowSmem) : 0;
+  return rows * (sizeof(RowSmem) + cap * sizeof(uint16_t));
+}
+int rows_cap(bool is_bf16, int V) { return (V / (is_bf16 ? 8 : 4) + 2 + 7) & ~7; }
+
+
+// Warps that take a row, 0: rows are streamed (logp_fwd).  Rows go to warps where what follows a row
+// costs more than its logits: up to 160 KB with alternatives, 80 KB without (4,096 bf16 rows of
+// 1,000 values with 20 alternatives: 16 against 196 us streamed, of 32,003: 83 against 241; 2,000 of
+// 64,000: 74 against 100, of 4,096 of 151,936: 273 against 271), but few long rows, which are cut
+// into parts over all SMs.  More warps a row until four CTAs fit an SM and 12 warps an SM have a
+// row, two vectors a lane at least (1,000 rows of 8,000 values with 20 alternatives: 17, 14, 16, 20
+// us with 1, 2, 4, 8 warps; 4,096 of 32,003: 102, 83, 89, 106).
+int rows_warps(bool is_bf16, int64_t T, int V, int top, int sms) {
+  const int64_t bytes = (int64_t)V * (is_bf16 ? 2 : 4);
+  if (bytes > (top > 0 ? 160 : 80) * 1024 || (bytes > 64 * 1024 && T < sms)) return 0;
+  const int cap = rows_cap(is_bf16, V);
+  int W = 1;
+  while (W < kRowsWarps && (rows_smem_bytes(cap, top > 0, W) > 56 * 1024 ||
+                            (T * W < 12 * sms && bytes > 16 * 64 * W)))
+    W *= 2;
+  return W;
+}
+}  // namespace
+
 // Parts of a row: as many as its group maxima take blocks of shared memory, and with few rows
 // as many as make an item for every SM, of a chunk at least.
 int ls_token_logp_parts(bool is_bf16, int64_t T, int V, int top, int sms) {
+  if (rows_warps(is_bf16, T, V, top, sms) > 0) return 1;
   const int64_t groups = groups_of(is_bf16, V), room = kGmaxBytes / (is_bf16 ? 2 : 4);
   int64_t parts = top > 0 ? (groups + room - 1) / room : 1;
   if (T > 0 && T * parts < sms) {
@@ -1024,6 +1330,26 @@ size_t ls_token_logp_ws_bytes(int64_t T, int parts) {
 }
 
 namespace {
+template <typename E, bool kTop, int W>
+cudaError_t launch_rows(const FwdArgs& a, cudaStream_t st) {
+  const int cap = rows_cap(sizeof(E) == 2, a.V);
+  const size_t smem = rows_smem_bytes(cap, kTop, W);
+  if (smem > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(logp_rows<E, kTop, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t rows = kRowsWarps / W;
+  logp_rows<E, kTop, W><<<(unsigned)((a.T + rows - 1) / rows), kRowsThreads, smem, st>>>(a, cap);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) ls_note_launch();
+  return e;
+}
+template <typename E, bool kTop>
+cudaError_t launch_rows(const FwdArgs& a, int W, cudaStream_t st) {
+  return W == 1 ? launch_rows<E, kTop, 1>(a, st) : W == 2 ? launch_rows<E, kTop, 2>(a, st)
+       : W == 4 ? launch_rows<E, kTop, 4>(a, st) : launch_rows<E, kTop, 8>(a, st);
+}
+
 template <typename E, bool kTop>
 cudaError_t launch_fwd(const FwdArgs& a, int sms, cudaStream_t st) {
   // without alternatives nothing behind `red` is used
@@ -1068,6 +1394,12 @@ cudaError_t ls_launch_token_logp_fwd(const LsTokenLogpArgs& b, int parts, int sm
   a.part_top = static_cast<u64*>(b.workspace);
   a.part_stat = reinterpret_cast<float*>(a.part_top + (size_t)b.T * parts * 32);
   a.err = b.err;
+  const int W = rows_warps(b.is_bf16, b.T, b.V, b.top, sms);
+  if (W > 0) {
+    if (b.is_bf16)
+      return b.top > 0 ? launch_rows<__nv_bfloat16, true>(a, W, st) : launch_rows<__nv_bfloat16, false>(a, W, st);
+    return b.top > 0 ? launch_rows<float, true>(a, W, st) : launch_rows<float, false>(a, W, st);
+  }
   if (b.is_bf16)
     return b.top > 0 ? launch_fwd<__nv_bfloat16, true>(a, sms, st) : launch_fwd<__nv_bfloat16, false>(a, sms, st);
   return b.top > 0 ? launch_fwd<float, true>(a, sms, st) : launch_fwd<float, false>(a, sms, st);
