@@ -8,17 +8,18 @@
 // With upstream g (of logp), h (of H) and a_j (of alternative j), G = g + sum_j a_j:
 //   dL/dz_v = (1 / tau) (g 1[v = y] + sum_j a_j 1[v = id_j] - p_v (G + h (log p_v + H))).
 //
-// Forward.  One pass over the row: every thread keeps a running maximum m, s = sum 2^t and
+// Forward.  One pass over the row: every thread keeps a reference m, s = sum 2^t and
 // e = sum 2^t t of t = (z - m) c (c = log2(e) / tau), so H = ln 2 (log2 s - e / s).  The
-// alternatives ride along on the maxima that the pass takes anyway: a row is cut into groups
-// of 32 bytes; each group's maximum goes to shared memory, and a thread keeps the largest of
-// its groups (ties to the lowest group, which holds the lower ids).  Behind the row a warp
-// takes the k-th largest of 32 maxima over disjoint groups, tau: k distinct logits reach it, so
-// only groups whose maximum does can hold one of the k largest.  It reads those groups again
-// (about 40 of 9,500 for k = 20) and sorts the logits that pass.
+// alternatives ride along on maxima of the same registers: a row is cut into groups of 64 bytes;
+// each group's maximum goes to shared memory, and a thread keeps the largest of its groups (ties
+// to the lowest group, which holds the lower ids).  Behind the row the k-th largest of 32 or 64
+// maxima over disjoint groups is a threshold: k logits reach it, so only groups whose maximum does
+// can hold one of the k largest.  A warp reads those groups again (about 40 of 4,750 for k = 20)
+// and orders the logits that pass.
 // A row too long for the group maxima, or a call with few rows, is cut into parts whose results
 // a second kernel merges.  Short rows go to a warp or a few each (logp_rows).
-// Sums are in fp32 (a thread adds V / 512 terms, then a tree), the last steps in fp64.
+// Sums are in fp32: over 64 bytes, then over a thread's groups, then a tree; the last steps are in
+// fp64.
 #include <math.h>
 
 #include "ls_device.cuh"
@@ -165,6 +166,11 @@ __device__ __forceinline__ Stat merge(Stat a, Stat b, float c) {
   b = move(b, m, c);
   return {m, a.s + b.s, a.e + b.e};
 }
+// Of one logit.
+__device__ __forceinline__ Stat stat_of(float x) {
+  const float one = x == -INFINITY ? 0.f : 1.f + (x - x);  // NaN of NaN and of +inf
+  return {x != x ? -INFINITY : x, one, one - one};
+}
 // Over a warp's lanes, in every lane: the maximum first, so that each moves once.
 __device__ __forceinline__ Stat warp_stat(Stat x, float c) {
   float m = x.m;
@@ -196,7 +202,9 @@ struct Sums {
   // 2e-7 (relative, root mean square); with a limit of 2^100 they were off by 3e-6.
   template <int N>
   __device__ __forceinline__ void add(const uint4* u) {
-    const float2 s0 = s, e0 = e, b = make_float2(nr, nr), c2 = make_float2(c, c);
+    // sums of these first: a short chain, then one addition
+    float2 s1 = make_float2(0.f, 0.f), e1 = s1;
+    const float2 b = make_float2(nr, nr), c2 = make_float2(c, c);
 #pragma unroll
     for (int v = 0; v < N; ++v) {
       float x[H];
@@ -205,13 +213,15 @@ struct Sums {
       for (int i = 0; i < H; i += 2) {
         const float2 t = __ffma2_rn(make_float2(x[i], x[i + 1]), c2, b);
         const float2 p = make_float2(fast_exp2(t.x), fast_exp2(t.y));
-        s = __fadd2_rn(s, p);
-        e = __ffma2_rn(p, t, e);
+        s1 = __fadd2_rn(s1, p);
+        e1 = __ffma2_rn(p, t, e1);
       }
     }
-    if (!(e.x + e.y < kLargeSum)) {
-      s = s0;
-      e = e0;
+    e1 = __fadd2_rn(e, e1);
+    if (e1.x + e1.y < kLargeSum) {
+      s = __fadd2_rn(s, s1);
+      e = e1;
+    } else {
       carefully<N>(u);
     }
   }
@@ -664,18 +674,17 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
     auto best = [&](int g, float mx) {
       put_max<E>(sm, g, mx);
       second = fmaxf(second, fminf(mx, bestv));
-      if (mx > bestv || bestg < 0) {
+      if (bestg < 0 || mx > bestv || (mx == bestv && g < bestg)) {
         bestv = mx;
         bestg = g;
       }
     };
-    auto edge = [&](int g) {  // a group that sticks out of the row
-      uint4 u[4];
-      it.template load<4>(a.V, g, 0, u);
-      sums.template add<4>(u);
-      if (kTop) best(g, R::max_of(u));
-    };
-    if (tid == 0 && it.in0 > 0) edge(0);
+    // a group that sticks out of the row: the first and the last warp take theirs, a value a lane
+    const bool sticks = (warp == 0 && it.in0 > 0) || (warp == kWarps - 1 && it.in1 < it.ng);
+    const int edge_g = warp == 0 ? 0 : it.ng - 1, edge_at = it.place(edge_g) + lane;
+    const bool has_edge = sticks && lane < Item<E>::G && edge_at >= 0 && edge_at < a.V;
+    float edge = NAN;
+    if (has_edge) edge = R::load(it.zr + edge_at);
     // a thread's 64 bytes of every chunk, in an order that keeps eight threads' loads apart; the
     // chunk is released as soon as they are in registers
     const int n = it.chunks();
@@ -695,13 +704,18 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
         if (kTop) best(g, R::max_of(u));
       }
     }
-    if (tid == kThreads - 1 && it.in1 < it.ng) edge(it.ng - 1);
-
     // ---- the item's results, into buffers that the last warp is done with
     const int par = q & 1;
     if (q >= 2) wait(free0 + 8 * par, ((q >> 1) - 1) & 1);
     ++q;
-    const Stat st = sums.stat();
+    Stat st = sums.stat();
+    if (sticks) {
+      if (has_edge) st = merge(st, stat_of(edge), c);
+      if (kTop) {
+        const uint32_t o = __reduce_max_sync(0xffffffffu, has_edge ? order_of(edge) : 0u);
+        if (lane == 0) best(edge_g, o ? value_of((u64)o << 32) : NAN);
+      }
+    }
     sm.m[par][tid] = st.m;
     sm.s[par][tid] = st.s;
     sm.e[par][tid] = st.e;
@@ -775,7 +789,7 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
         };
         if (tid == 0 && it.in0 > 0) visit(0);
         for (int g = it.in0 + tid; g < it.in1; g += kThreads) visit(g);
-        if (tid == kThreads - 1 && it.in1 < it.ng) visit(it.ng - 1);
+        if (tid == kThreads - 32 && it.in1 < it.ng) visit(it.ng - 1);
       }
     }
     hand_over(par);
@@ -946,10 +960,7 @@ __global__ void __launch_bounds__(kRowsThreads, 4) logp_rows(const FwdArgs a, in
     }
   }
   Stat st = sums.stat();
-  if (has_edge) {
-    const float one = edge == -INFINITY ? 0.f : 1.f + (edge - edge);  // NaN of NaN and of +inf
-    st = merge(st, Stat{edge != edge ? -INFINITY : edge, one, one - one}, a.c);
-  }
+  if (has_edge) st = merge(st, stat_of(edge), a.c);
   st = warp_stat(st, a.c);
   if (W > 1 && lane == 0) sm.red[wl] = st;
 
@@ -1293,19 +1304,21 @@ int rows_cap(bool is_bf16, int V) { return (V / (is_bf16 ? 8 : 4) + 2 + 7) & ~7;
 
 
 // Warps that take a row, 0: rows are streamed (logp_fwd).  Rows go to warps where what follows a row
-// costs more than its logits: up to 160 KB with alternatives, 80 KB without (4,096 bf16 rows of
-// 1,000 values with 20 alternatives: 16 against 196 us streamed, of 32,003: 83 against 241; 2,000 of
-// 64,000: 74 against 100, of 4,096 of 151,936: 273 against 271), but few long rows, which are cut
-// into parts over all SMs.  More warps a row until four CTAs fit an SM and 12 warps an SM have a
-// row, two vectors a lane at least (1,000 rows of 8,000 values with 20 alternatives: 17, 14, 16, 20
-// us with 1, 2, 4, 8 warps; 4,096 of 32,003: 102, 83, 89, 106).
+// costs more than its logits: up to 80 KB a row (4,096 bf16 rows of 32,003 values: 48 us against 66
+// streamed, 2,000 of 50,257: 51 against 46), with alternatives up to 160 KB of bf16 or 96 KB of fp32
+// (with 20 of them 4,096 bf16 rows of 1,000 values: 16 against 196 us, of 32,003: 82 against 182,
+// 2,000 of 64,000: 73 against 106, 4,096 of 151,936: 272 against 281; 4,096 fp32 rows of 16,000: 63
+// against 110, 2,000 of 50,257: 97 against 82), but few long rows, which are cut into parts over all
+// SMs.  More warps a row until four CTAs fit an SM and 12 warps an SM have a row, two vectors a lane
+// at least, and a lane adds at most 512 pairs (1,000 rows of 8,000 values with 20 alternatives: 17, 14, 16, 20 us with 1, 2, 4, 8 warps;
+// 4,096 of 32,003: 102, 83, 89, 106).
 int rows_warps(bool is_bf16, int64_t T, int V, int top, int sms) {
   const int64_t bytes = (int64_t)V * (is_bf16 ? 2 : 4);
-  if (bytes > (top > 0 ? 160 : 80) * 1024 || (bytes > 64 * 1024 && T < sms)) return 0;
+  if (bytes > (top == 0 ? 80 : is_bf16 ? 160 : 96) * 1024 || (bytes > 64 * 1024 && T < sms)) return 0;
   const int cap = rows_cap(is_bf16, V);
   int W = 1;
   while (W < kRowsWarps && (rows_smem_bytes(cap, top > 0, W) > 56 * 1024 ||
-                            (T * W < 12 * sms && bytes > 16 * 64 * W)))
+                            (T * W < 12 * sms && bytes > 16 * 64 * W) || V > 32768 * W))
     W *= 2;
   return W;
 }

@@ -32,8 +32,9 @@ def stat_bounds(z, temperature):
     """Bounds of lse (and, with their own rounding, of log probabilities) and of the entropy.
 
     A term 2^t of t = (z - m) c carries t's three roundings (3 |t| half steps, times ln 2) and
-    the exponential's 2^-21; a sum over V terms is a chain of V / 512 (one more for each of its
-    rescales, one per 8 terms at most) and a tree.  The last steps are in 64 bits but for a
+    the exponential's 2^-21; a sum over V terms is a chain of V / 512, or, where a warp takes a
+    row, of V / 64, 512 at most (one more for each of its rescales, one per 8 terms at most), and a
+    tree.  The last steps are in 64 bits but for a
     logarithm of 2^-22 and the result's rounding."""
     lp, lse = log_probs(z, temperature)
     V = z.shape[1]
@@ -41,7 +42,7 @@ def stat_bounds(z, temperature):
     with np.errstate(invalid="ignore"):
         u = np.where(p > 0, lp - lp.max(-1, keepdims=True), 0)  # = t ln 2
     a1, a2 = (p * np.abs(u)).sum(-1), (p * u * u).sum(-1)
-    chain = 1.5 * V / 512 + 80
+    chain = 1.5 * max(V / 512, min(V / 64, 512)) + 80
     es = 2.0 ** -21 + chain * U32 + 3 * U32 * a1
     h = entropy(lp)
     e_lse = es + 2.0 ** -21 + U32 * np.abs(lse)

@@ -77,6 +77,10 @@ CASES = [
     (8, 151936, BF, 0, 1.0, 20, 0), (3, 151936, F32, 0, 0.7, 32, 2), (200, 32003, BF, 0, 1.0, 8, 0),
     (170, 50257, F32, 47, 0.6, 0, 0), (1, 400003, F32, 0, 1.0, 32, 1), (161, 250002, BF, 0, 1.0, 3, 7),
     (400, 513, BF, 0, 2.0, 1, 0), (31, 4096, F32, 0, 1.0, 0, 0), (160, 100001, F32, 3, 1.0, 32, 0),
+    # many rows of a warp or a few each
+    (2500, 1000, BF, 24, 1.0, 32, 0), (3001, 333, F32, 1, 0.6, 12, 0), (1900, 63, BF, 0, 1.0, 13, 5),
+    (1000, 8001, BF, 0, 1.0, 20, 3), (2000, 20011, BF, 0, 1.4, 32, 0), (700, 20011, F32, 0, 1.0, 17, 1),
+    (1830, 33007, BF, 0, 1.0, 0, 1), (2000, 5, F32, 0, 1.0, 5, 0), (500, 70001, BF, 0, 1.0, 5, 0),
 ]
 
 
@@ -131,10 +135,10 @@ def test_rows_in_steps(cuda, dt, rise):
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("V", [9600, 96000])
 @pytest.mark.parametrize("order", ["up", "down", "columns", "threads"])
-def test_orders_of_a_row(cuda, dt, order):
+def test_orders_of_a_row(cuda, dt, V, order):
     """Rows whose largest logits all lie with one thread, or come last, or rise all along."""
-    V = 40000
     x = torch.linspace(-20, 20, V, device=cuda)
     if order == "down":
         x = x.flip(0)
@@ -149,11 +153,10 @@ def test_orders_of_a_row(cuda, dt, order):
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
-@pytest.mark.parametrize("T", [3, 190])
-def test_masked_vocabulary(cuda, dt, T):
+@pytest.mark.parametrize("T,V", [(3, 30011), (190, 30011), (3, 150011), (190, 100011)])
+def test_masked_vocabulary(cuda, dt, T, V):
     """Logits of -inf and of the type's lowest value have no probability, and the alternatives
     that are left over take them in the order of their ids."""
-    V = 30011
     z, y, g = rows(cuda, T, V, dt, seed=T)
     low = torch.finfo(dt).min
     z[0, 5:] = -math.inf          # five tokens left
@@ -173,9 +176,9 @@ def test_masked_vocabulary(cuda, dt, T):
     assert abs(float(ent[0]) - math.log(V)) < 1e-4 and ids[0].tolist() == [0, 1, 2, 3]
 
 
-@pytest.mark.parametrize("T", [4, 200])
-def test_rows_that_are_no_numbers(cuda, T):
-    z, y, _ = rows(cuda, T, 5000, F32, seed=2)
+@pytest.mark.parametrize("T,V", [(4, 5000), (200, 5000), (4, 50000), (200, 50000)])
+def test_rows_that_are_no_numbers(cuda, T, V):
+    z, y, _ = rows(cuda, T, V, F32, seed=2)
     z[0, 77] = math.nan
     z[1, 78] = math.inf
     z[2] = -math.inf
@@ -190,7 +193,7 @@ def test_rows_that_are_no_numbers(cuda, T):
         assert torch.equal(a[3:], b) if k == 4 else (np.abs(f64(a[3:]) - f64(b)) <= 2 * e).all()
     assert torch.isnan(out[0][:3]).all() and torch.isnan(out[2][:3]).all()
     ids = out[4][:3]
-    assert bool(((ids >= -1) & (ids < 5000)).all())
+    assert bool(((ids >= -1) & (ids < V)).all())
     assert B.ls_last_device_error(0) == B.LS_OK
 
 
