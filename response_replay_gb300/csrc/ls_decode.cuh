@@ -110,10 +110,6 @@ struct Loader {
   }
   // one tile to `dst`, counted on barrier `bar`; then the next tile's pages
   __device__ __forceinline__ void load(uint32_t dst, uint32_t bar, bool more, uint32_t* err) {
-    issue(dst, bar, err);
-    advance(more);
-  }
-  __device__ __forceinline__ void issue(uint32_t dst, uint32_t bar, uint32_t* err) {
     mbar_expect_tx(bar, kTileBytes);
 #pragma unroll
     for (int x = 0; x < kMaxBoxes; ++x) {
@@ -132,8 +128,6 @@ struct Loader {
         tma_load_2d(dst + kHalfBytes + x * box_rows * 128, map, 64, y, bar);
       }
     }
-  }
-  __device__ __forceinline__ void advance(bool more) {
     key0 += kTile;
     if (more) look_up();
   }
@@ -146,7 +140,9 @@ __device__ __forceinline__ float* part_at(const LsDecodeArgs& a, int64_t row) {
 
 // Tensor maps of the prompt's and the responses' pools: rows of 256 bytes; a whole-tile box
 // takes both halves of its rows, half by half.
-inline bool make_tmaps(const LsDecodeArgs& a, TmapSet* tm) {
+// Grouped: boxes are [eight rows][half][row][64 values], so a box of any height is one copy and a
+// tile's groups of eight rows lie 2 KB apart, their halves 1 KB.
+inline bool make_tmaps(const LsDecodeArgs& a, TmapSet* tm, bool grouped = false) {
   for (int src = 0; src < 2; ++src) {
     const int ps = 1 << (src ? a.r_ps_log2 : a.ps_log2);
     const uint64_t rows = (uint64_t)(src ? a.r_num_pages : a.num_pages) * a.hkv * ps;
@@ -155,6 +151,14 @@ inline bool make_tmaps(const LsDecodeArgs& a, TmapSet* tm) {
     const uint64_t strides[2] = {(uint64_t)kD * 2, (uint64_t)kD};
     const uint32_t box[3] = {64, (uint32_t)(ps < kTile ? ps : kTile), 2};
     const int rank = whole ? 3 : 2;
+    if (grouped) {
+      const uint64_t gdims[4] = {64, 8, 2, rows / 8}, gstrides[3] = {(uint64_t)kD * 2, (uint64_t)kD, (uint64_t)kD * 16};
+      const uint32_t gbox[4] = {64, 8, 2, box[1] / 8};
+      if (!ls_make_tmap_bf16(src ? &tm->kr : &tm->kp, src ? a.rk_pool : a.k_pool, 4, gdims, gstrides, gbox) ||
+          !ls_make_tmap_bf16(src ? &tm->vr : &tm->vp, src ? a.rv_pool : a.v_pool, 4, gdims, gstrides, gbox))
+        return false;
+      continue;
+    }
     if (!ls_make_tmap_bf16(src ? &tm->kr : &tm->kp, src ? a.rk_pool : a.k_pool, rank, dims, strides, box) ||
         !ls_make_tmap_bf16(src ? &tm->vr : &tm->vp, src ? a.rv_pool : a.v_pool, rank, dims, strides, box))
       return false;

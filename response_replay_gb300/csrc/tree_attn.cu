@@ -40,6 +40,8 @@ using namespace decode;
 constexpr int kPair = 2 * kTile;
 constexpr int kMaxMembers = 1024;
 constexpr int kStages = 5;
+// K and V tiles: groups of eight rows, in each both halves (64 values a row)
+constexpr uint32_t kGroup = 2048, kGroupHalf = 1024;
 constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
 // 384 x 168 registers at launch; 128 x 96 + 256 x 200 = 63,488 of the 64,512
@@ -207,6 +209,48 @@ struct Walk {
       return true;
     }
     return false;
+  }
+};
+
+// The loads of a segment's tiles, by a warp: a lane a page (from grouped maps, one copy each), which
+// it looks up while the last tile's loads are under way.
+struct Pages {
+  const int32_t* table;
+  int32_t len, key, box_rows, boxes, ps_log2, pages, head, pool_groups, page;
+
+  // lane's page of the tile at first
+  __device__ __forceinline__ void open(const LsDecodeArgs& a, const Seg& s, int lane) {
+    table = s.resp ? a.blocks + (int64_t)s.m * a.max_blocks : a.page_table;
+    ps_log2 = s.resp ? a.r_ps_log2 : a.ps_log2;
+    pages = s.resp ? a.r_num_pages : a.num_pages;
+    box_rows = min(1 << ps_log2, kTile);
+    boxes = kTile / box_rows;
+    pool_groups = ((pages * a.hkv) << ps_log2) >> 3;
+    head = a.hkv;
+    len = s.len;
+    key = s.key0 + lane * box_rows;
+    if (lane < boxes) look_up();
+  }
+  __device__ __forceinline__ void look_up() {
+    if (key < len) page = __ldg(table + (key >> ps_log2));
+  }
+  __device__ __forceinline__ void issue(const void* map, int32_t kvh, uint32_t dst, uint32_t bar, int lane,
+                                        uint32_t* err) const {
+    if (lane == 0) mbar_expect_tx(bar, kTileBytes);
+    __syncwarp();
+    if (lane >= boxes) return;
+    int32_t y = pool_groups;  // out of bounds: zero fill
+    if (key < len) {
+      if ((uint32_t)page < (uint32_t)pages)
+        y = (((page * head + kvh) << ps_log2) + (key & ((1 << ps_log2) - 1))) >> 3;
+      else
+        ls_report(err, LS_DEVERR_CHECK);
+    }
+    tma_load_4d(dst + lane * box_rows * 256, map, 0, 0, 0, y, bar);
+  }
+  __device__ __forceinline__ void advance(bool more, int lane) {
+    key += kTile;
+    if (more && lane < boxes) look_up();
   }
 };
 
@@ -380,33 +424,33 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
         tma_prefetch_desc(&tm.vp);
         tma_prefetch_desc(&tm.kr);
         tma_prefetch_desc(&tm.vr);
-        RingPos<kStages> ring;
-        uint32_t fills = 0;
-        Loader ld;
-        bool ok = true;
-        while (ok && walk.next(&s, cta)) {
-          ld.open(a, s.resp, s.m, s.kvh, s.key0, s.len, &tm.kp, &tm.kr);
-          for (int32_t j = 0; ok && j < s.count; ++j) {
-            const bool ragged = s.len - (s.key0 + j * kTile) < kTile;
-            for (int kv = 0; kv < 2; ++kv) {
-              ok = wait_bar(bar_addr(sbase, B_KV_EMPTY + ring.stage), ring.phase ^ 1) && !*abort_flag;
-              if (!ok) {
-                fail();
-                break;
-              }
-              ld.map = kv ? (s.resp ? &tm.vr : &tm.vp) : (s.resp ? &tm.kr : &tm.kp);
-              ld.issue(sbase + kOffRing + ring.stage * kTileBytes,
-                       bar_addr(sbase, (kv && ragged ? B_AUX : B_KV_FULL) + ring.stage), a.err);
-              ring.advance();
-              ++fills;
-            }
-            ld.advance(j + 1 < s.count);
-          }
-        }
-        // Do not leave while loads into this CTA's shared memory may still be in flight.
-        for (uint32_t i = fills > kStages ? fills - kStages : 0; i < fills; ++i)
-          mbar_wait(bar_addr(sbase, B_KV_FULL + i % kStages), (i / kStages) & 1);
       }
+      RingPos<kStages> ring;
+      uint32_t fills = 0;
+      Pages ld;
+      bool ok = true;
+      while (ok && walk.next(&s, cta)) {
+        ld.open(a, s, lane);
+        for (int32_t j = 0; ok && j < s.count; ++j) {
+          const bool ragged = s.len - (s.key0 + j * kTile) < kTile;
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = __all_sync(0xffffffffu, wait_bar(bar_addr(sbase, B_KV_EMPTY + ring.stage), ring.phase ^ 1) && !*abort_flag);
+            if (!ok) {
+              fail();
+              break;
+            }
+            ld.issue(kv ? (s.resp ? &tm.vr : &tm.vp) : (s.resp ? &tm.kr : &tm.kp), s.kvh,
+                     sbase + kOffRing + ring.stage * kTileBytes,
+                     bar_addr(sbase, (kv && ragged ? B_AUX : B_KV_FULL) + ring.stage), lane, a.err);
+            ring.advance();
+            ++fills;
+          }
+          ld.advance(j + 1 < s.count, lane);
+        }
+      }
+      // Do not leave while loads into this CTA's shared memory may still be in flight.
+      for (uint32_t i = fills > kStages ? fills - kStages : 0; i < fills; ++i)
+        mbar_wait(bar_addr(sbase, B_KV_FULL + i % kStages), (i / kStages) & 1);
     } else if (warp == 3) {
       // ---------------------------------------------------------- V tails
       uint32_t ring = 0, aux_phase = 0;
@@ -421,9 +465,10 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
         if (!ok) break;
         aux_phase ^= 1u << st;
         uint8_t* vb = smem + kOffRing + st * kTileBytes;
-        for (int i = left * 8 + lane; i < kTile * 8; i += 32) {
-          *reinterpret_cast<uint4*>(vb + i * 16) = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(vb + kHalfBytes + i * 16) = make_uint4(0, 0, 0, 0);
+        for (int i = left * 8 + lane; i < kTile * 8; i += 32) {  // row i / 8
+          uint8_t* at = vb + (i >> 6) * kGroup + (i & 63) * 16;
+          *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(at + kGroupHalf) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -437,21 +482,22 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
       const uint32_t idPV = idesc_bf16_f32(kTile, kD, true);
       const uint32_t dq = sdesc_lo(sbase + kOffQ + t * kTileBytes, 16);
       const uint32_t dk = sdesc_lo(sbase + kOffRing, 16);
-      const uint32_t dv = sdesc_lo(sbase + kOffRing, kHalfBytes);
+      const uint32_t dv = sdesc_lo(sbase + kOffRing, kGroupHalf);
       const uint32_t d_s = tmem, d_p = tmem + kColP + t * (kTile / 2), d_o = tmem + kColO + t * kTile;
       auto issue_s = [&](uint32_t st) {
         const uint32_t b0 = dk + ((st * kTileBytes) >> 4);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
-          mma_ss_lo(d_s, dq + off, b0 + off, idS, kk > 0);
+          const uint32_t off = (kk & 3) * 32;
+          mma_ss_groups(d_s, dq + (((kk >> 2) * kHalfBytes + off) >> 4),
+                        b0 + (((kk >> 2) * kGroupHalf + off) >> 4), idS, kk > 0);
         }
       };
       auto issue_pv = [&](uint32_t st, bool accumulate) {
         const uint32_t b0 = dv + ((st * kTileBytes) >> 4);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_ts_lo(d_o, d_p + kk * 8, b0 + ((kk * 2048) >> 4), idPV, (accumulate || kk > 0) ? 1u : 0u);
+          mma_ts_groups(d_o, d_p + kk * 8, b0 + ((kk * 2 * kGroup) >> 4), idPV, (accumulate || kk > 0) ? 1u : 0u);
       };
       uint32_t seen = 0;
       RingPos<kStages> sp;
@@ -838,7 +884,7 @@ int64_t ls_tree_part_rows(const LsDecodeArgs& a) {
 
 cudaError_t ls_launch_tree_attn(const LsDecodeArgs& a, cudaStream_t st) {
   TmapSet tm;
-  if (!make_tmaps(a, &tm)) return cudaErrorInvalidValue;
+  if (!make_tmaps(a, &tm, true)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kSmemBytes);
   if (e != cudaSuccess) return e;
