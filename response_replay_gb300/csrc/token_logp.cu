@@ -31,7 +31,7 @@ namespace {
 constexpr int kThreads = 384;  // consumers of the forward, a group of 64 bytes each a step
 constexpr int kWarps = kThreads / 32;
 constexpr int kGroupBytes = 64;
-constexpr int kGmaxBytes = 20480;  // group maxima of a part, of the logits' type
+constexpr int kMaxGroups = 4864;  // of a part with alternatives: their maxima lie in shared memory
 constexpr int kBwdThreads = 256, kBwdCtas = 5;  // of the backward, and blocks an SM
 constexpr float kLargeSum = 2048.f;  // of 2^t t: t = 8, or many somewhat below
 constexpr double kLn2d = 0.69314718055994530942;
@@ -338,9 +338,10 @@ __device__ __forceinline__ void write_top(const FwdArgs& a, int64_t row, u64 key
 // A persistent CTA takes items (a part of a row) by turns: a producer warp streams an item's
 // whole groups through a ring of 24 KB chunks by bulk copies, a group a consumer thread and
 // chunk, and runs ahead into the next item while the consumers end one; a last warp takes the
-// consumers' results and candidates, reads those groups again and writes the row's outputs
-// while the consumers are at the next item.  Groups that stick out of the row are read with
-// plain loads.
+// consumers' results and maxima, finds the candidates, reads those groups again and writes the
+// row's outputs while the consumers are at the next item (with the consumers at the candidates
+// 4,096 rows of 151,936 bf16 values took 241 us for 5 alternatives).  Groups that stick out of the
+// row are read with plain loads.
 constexpr int kChunkBytes = kThreads * kGroupBytes;
 constexpr int kCtaThreads = kThreads + 64;
 constexpr int kHand = kThreads + 32;  // the consumers and the last warp
@@ -348,7 +349,6 @@ template <bool kTop>
 struct Cfg {
   static constexpr int kStages = kTop ? 3 : 4;
 };
-constexpr int kFewTops = 12;  // alternatives for which 32 maxima make the threshold
 constexpr int kRanked = 128;  // logits that are put in order by counting
 constexpr int kCand = 512;  // groups that reach the threshold, before the slow way is taken
 
@@ -357,20 +357,17 @@ constexpr int kFound = 32 * 16 + kRanked;
 struct FwdSmem {  // behind the ring; [2]: by parity of the item
   uint64_t full[6], empty[6], free[2];
   int abort;
-  int cands[2];
   float m[2][kThreads], s[2][kThreads], e[2][kThreads];
-  uint32_t floor_o[2];  // the threshold: a maximum, and the last place among equal ones
-  int floor_g[2];
-  alignas(16) uint32_t tops[2][64];
-  int topg[2][64];
+  uint32_t best[2][kThreads];  // the largest of a thread's groups (0: none), and which
+  uint16_t bestg[2][kThreads];
+  alignas(16) uint32_t tops[64];
+  int topg[64];
   alignas(16) u64 found[kFound];  // logits that reach the threshold, on their way into the list
-  uint16_t cand[2][kCand];
-  uint8_t gmax[kGmaxBytes];  // the groups' maxima, of the logits' type
+  uint16_t cand[kCand], owner[kThreads];
+  alignas(16) uint16_t gmax[2][kMaxGroups];  // upper halves of the groups' maxima
 };
+static_assert(3 * kThreads * kGroupBytes + sizeof(FwdSmem) <= (228 * 1024 / 2 - 1024), "two CTAs an SM");
 
-__device__ __forceinline__ void consumers_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
-}
 __device__ __forceinline__ void hand_over(int par) {
   if (par)
     asm volatile("bar.arrive 3, %0;" ::"n"(kHand) : "memory");
@@ -439,27 +436,57 @@ struct Item {
   }
 };
 
-template <typename E>
-__device__ __forceinline__ float group_max(const FwdSmem& sm, int g);
-template <>
-__device__ __forceinline__ float group_max<float>(const FwdSmem& sm, int g) {
-  return reinterpret_cast<const float*>(sm.gmax)[g];
+// Two upper halves of floats as whole numbers in their order.
+__device__ __forceinline__ uint32_t order_halves(uint32_t x) {
+  return x ^ (((x >> 15) & 0x00010001u) * 0xffffu | 0x80008000u);
 }
-template <>
-__device__ __forceinline__ float group_max<__nv_bfloat16>(const FwdSmem& sm, int g) {
-  return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(sm.gmax)[g] << 16);
-}
-template <typename E>
-__device__ __forceinline__ void put_max(FwdSmem& sm, int g, float x);
-template <>
-__device__ __forceinline__ void put_max<float>(FwdSmem& sm, int g, float x) {
-  reinterpret_cast<float*>(sm.gmax)[g] = x;
-}
-template <>
-__device__ __forceinline__ void put_max<__nv_bfloat16>(FwdSmem& sm, int g, float x) {
-  reinterpret_cast<uint16_t*>(sm.gmax)[g] = (uint16_t)(__float_as_uint(x) >> 16);
+// The threshold that the top-th largest of 64 maxima over disjoint groups makes, by a warp: the
+// lowest maximum with fewer than top above it, and the last place among its equals.  (With 32
+// maxima 32 alternatives let three times as many logits through.)
+__device__ __forceinline__ void threshold(const uint32_t* tops, const int* topg, int top, int lane,
+                                          uint32_t* floor_o, int* floor_g) {
+  const uint32_t x = tops[lane], x2 = tops[lane + 32];
+  const uint4* all = reinterpret_cast<const uint4*>(tops);
+  int above = 0, above2 = 0;
+#pragma unroll 4
+  for (int k = 0; k < 16; ++k) {
+    const uint4 y = all[k];
+    above += (y.x > x) + (y.y > x) + (y.z > x) + (y.w > x);
+    above2 += (y.x > x2) + (y.y > x2) + (y.z > x2) + (y.w > x2);
+  }
+  *floor_o = __reduce_min_sync(0xffffffffu, min(above < top ? x : 0xffffffffu, above2 < top ? x2 : 0xffffffffu));
+  *floor_g = __reduce_max_sync(0xffffffffu, max(x == *floor_o ? topg[lane] : -1, x2 == *floor_o ? topg[lane + 32] : -1));
+  if (*floor_o == 0) *floor_g = INT32_MAX;  // fewer groups than alternatives: all of them
 }
 
+// The 32 largest of up to 32 K keys, sorted, one a lane: each one's place is the number of larger
+// ones.
+template <int K>
+__device__ __forceinline__ u64 rank_found(u64* buf, int found, int lane) {
+  u64 mine[K];
+  int rank[K];
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    mine[i] = i * 32 + lane < found ? buf[i * 32 + lane] : 0ull;
+    rank[i] = 0;
+  }
+  if (lane == 0) buf[found] = 0ull;
+  __syncwarp();
+#pragma unroll 4
+  for (int j = 0; j < found; j += 2) {
+    const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(buf + j);
+#pragma unroll
+    for (int i = 0; i < K; ++i) rank[i] += (y.x > mine[i]) + (y.y > mine[i]);
+  }
+  __syncwarp();
+  buf[lane] = 0ull;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < K; ++i)
+    if (mine[i] != 0 && rank[i] < 32) buf[rank[i]] = mine[i];
+  __syncwarp();
+  return buf[lane];
+}
 // The 32 largest of a list and `found` more, sorted, one a lane.  (The list is empty in every lane
 // or in none.)
 __device__ __forceinline__ u64 order_found(u64* buf, int found, u64 list, int lane) {
@@ -468,29 +495,18 @@ __device__ __forceinline__ u64 order_found(u64* buf, int found, u64 list, int la
       list = merge32(list, sort32(i + lane < found ? buf[i + lane] : 0ull, lane), lane);
     return list;
   }
-  // each one's place is the number of larger ones
-  u64 mine[kRanked / 32];
-  int rank[kRanked / 32];
+  return found <= 32 ? rank_found<1>(buf, found, lane)
+       : found <= 64 ? rank_found<2>(buf, found, lane) : rank_found<kRanked / 32>(buf, found, lane);
+}
+__device__ __forceinline__ int prefix_sum(int x, int lane, int* total) {  // of the lanes before
+  int t = x;
 #pragma unroll
-  for (int i = 0; i < kRanked / 32; ++i) {
-    mine[i] = i * 32 + lane < found ? buf[i * 32 + lane] : 0ull;
-    rank[i] = 0;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, t, o);
+    if (lane >= o) t += y;
   }
-  if (lane == 0) buf[found] = 0ull;
-  __syncwarp();
-  for (int j = 0; j < found; j += 2) {
-    const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(buf + j);
-#pragma unroll
-    for (int i = 0; i < kRanked / 32; ++i) rank[i] += (y.x > mine[i]) + (y.y > mine[i]);
-  }
-  __syncwarp();
-  buf[lane] = 0ull;
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < kRanked / 32; ++i)
-    if (mine[i] != 0 && rank[i] < 32) buf[rank[i]] = mine[i];
-  __syncwarp();
-  return buf[lane];
+  *total = __shfl_sync(0xffffffffu, t, 31);
+  return t - x;
 }
 
 // The 32 largest logits of an item, sorted, one a lane, by one warp: of the groups that reach the
@@ -498,16 +514,117 @@ __device__ __forceinline__ u64 order_found(u64* buf, int found, u64 list, int la
 // same threads) of all groups.
 template <typename E>
 __device__ u64 pick(FwdSmem& sm, const Item<E>& it, const FwdArgs& a, int par, int lane) {
-  constexpr int kHalf = Item<E>::G / 2;
-  const int cands = sm.cands[par];
+  constexpr int G = Item<E>::G;
+  // the two largest of every lane's threads
+  uint32_t o[kWarps], o1 = 0, o2 = 0;
+  int i1 = -1, i2 = -1;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) o[i] = sm.best[par][lane + 32 * i];
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    if (o[i] > o1) {
+      o2 = o1;
+      i2 = i1;
+      o1 = o[i];
+      i1 = i;
+    } else if (o[i] > o2) {
+      o2 = o[i];
+      i2 = i;
+    }
+  }
+  sm.tops[2 * lane] = o1;
+  sm.topg[2 * lane] = i1 < 0 ? -1 : sm.bestg[par][lane + 32 * i1];
+  sm.tops[2 * lane + 1] = o2;
+  sm.topg[2 * lane + 1] = i2 < 0 ? -1 : sm.bestg[par][lane + 32 * i2];
+  __syncwarp();
+  uint32_t floor_o;
+  int floor_g;
+  threshold(sm.tops, sm.topg, a.top, lane, &floor_o, &floor_g);
+  // the threads that have a group that reaches it, and their groups (both zeros are one)
+  int threads = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    const uint32_t mask = __ballot_sync(0xffffffffu, o[i] >= floor_o);
+    if (o[i] >= floor_o) sm.owner[threads + __popc(mask & ((1u << lane) - 1))] = (uint16_t)(lane + 32 * i);
+    threads += __popc(mask);
+  }
+  __syncwarp();
+  const uint32_t floor16 = (floor_o >> 16) == 0x8000u ? 0x7fffu : floor_o >> 16;
+  auto reaches = [&](int g) { return (order_halves(sm.gmax[par][g]) & 0xffffu) >= floor16; };
+  constexpr int kSteps = (kMaxGroups + kThreads - 1) / kThreads;
+  static_assert(kSteps <= 30, "a bit a group");
+  int cands = 0;
+  for (int t0 = 0; t0 < threads; t0 += 32) {
+    const bool has = t0 + lane < threads;
+    const int first = it.in0 + (has ? sm.owner[t0 + lane] : 0);
+    uint32_t mask = 0;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k)
+      if (has && first + k * kThreads < it.in1 && reaches(first + k * kThreads)) mask |= 1u << k;
+    // the groups that stick out of the row
+    if (t0 == 0 && lane == 0 && it.in0 > 0 && reaches(0)) mask |= 1u << 30;
+    if (t0 == 0 && lane == 0 && it.in1 < it.ng && reaches(it.ng - 1)) mask |= 1u << 31;
+    int total, at = cands + prefix_sum(__popc(mask), lane, &total);
+    for (; mask; mask &= mask - 1, ++at) {
+      const int k = __ffs(mask) - 1;
+      if (at < kCand) sm.cand[at] = (uint16_t)(k == 30 ? 0 : k == 31 ? it.ng - 1 : first + k * kThreads);
+    }
+    cands += total;
+  }
+  __syncwarp();
+  if (cands <= kCand) {
+    const float floor = floor_o ? value_of((u64)floor_o << 32) : -INFINITY;
+    int found = 0;
+    for (int j0 = 0; j0 < cands && found <= kRanked; j0 += 32) {  // a group a lane
+      const int g = j0 + lane < cands ? sm.cand[j0 + lane] : -1;
+      uint32_t mask = 0;
+      uint4 u[4];
+      int place = 0;
+      if (g >= 0) {
+        place = it.place(g);
+        it.template load<4>(a.V, g, 0, u);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          float x[Row<E>::N];
+          Row<E>::unpack(u[v], x);
+#pragma unroll
+          for (int i = 0; i < Row<E>::N; ++i)
+            if (x[i] > floor || (x[i] == floor && g <= floor_g)) mask |= 1u << (v * Row<E>::N + i);
+        }
+        // what lies in the row
+        if (place < 0) mask &= ~0u << -place;
+        if (a.V - place < G) mask &= (1u << (a.V - place)) - 1;
+      }
+      int total, at = found + prefix_sum(__popc(mask), lane, &total);
+      if (found + total <= kRanked) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          float x[Row<E>::N];
+          Row<E>::unpack(u[v], x);
+#pragma unroll
+          for (int i = 0; i < Row<E>::N; ++i) {
+            const int b = v * Row<E>::N + i;
+            if (mask & (1u << b)) sm.found[at++] = (u64)order_of(x[i]) << 32 | (uint32_t)~(uint32_t)(place + b);
+          }
+        }
+      }
+      found += total;
+    }
+    __syncwarp();
+    if (found <= kRanked) {
+      const u64 list = order_found(sm.found, found, 0, lane);
+      __syncwarp();
+      return list;
+    }
+  }
+  // ---- more groups or logits than that: a value a lane and round, the list kept in order
+  constexpr int kHalf = G / 2;
   const bool all = cands > kCand;
   const int n = all ? it.ng : cands;
-  const uint32_t floor_o = all ? 0u : sm.floor_o[par];
-  const int floor_g = all ? INT32_MAX : sm.floor_g[par];
   u64 kth = 0, list = 0;
   int found = 0;
   for (int j0 = 0; j0 < n; j0 += 16) {  // half a group a lane
-    const int j = j0 + (lane >> 1), g = all ? j : j < n ? sm.cand[par][j] : 0;
+    const int j = j0 + (lane >> 1), g = all ? j : j < n ? sm.cand[j] : 0;
     float x[kHalf];
     const int place = it.place(g) + (lane & 1) * kHalf;
     if (j < n) {
@@ -521,9 +638,9 @@ __device__ u64 pick(FwdSmem& sm, const Item<E>& it, const FwdArgs& a, int par, i
     }
 #pragma unroll
     for (int i = 0; i < kHalf; ++i) {
-      const uint32_t o = order_of(x[i]);
-      bool in = o > floor_o || (o == floor_o && o != 0 && g <= floor_g);
-      const u64 key = (u64)o << 32 | (uint32_t)~(uint32_t)(place + i);
+      const uint32_t ox = order_of(x[i]);
+      bool in = ox > floor_o || (ox == floor_o && ox != 0 && g <= floor_g);
+      const u64 key = (u64)ox << 32 | (uint32_t)~(uint32_t)(place + i);
       in = in && key > kth && place + i >= 0 && place + i < a.V;
       const uint32_t mask = __ballot_sync(0xffffffffu, in);
       if (mask == 0) continue;
@@ -573,7 +690,6 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
     umma::mbar_init(free0, 1);
     umma::mbar_init(free0 + 8, 1);
     sm.abort = 0;
-    sm.cands[0] = sm.cands[1] = 0;
     umma::fence_barrier_init();
   }
   __syncthreads();
@@ -643,7 +759,6 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
       u64 list = 0;
       if (kTop) {
         list = pick<E>(sm, it, a, par, lane);
-        if (lane == 0) sm.cands[par] = 0;
       }
       __syncwarp();
       if (lane == 0) umma::mbar_arrive(free0 + 8 * par);
@@ -669,11 +784,15 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
     y = Item<E>::target(a, item + gridDim.x);
     if (it.pad) continue;
     Sums<E> sums(c);
-    float bestv = -INFINITY, second = -INFINITY;  // the largest of this thread's groups, the next
+    // buffers that the last warp is done with
+    const int par = q & 1;
+    if (q >= 2) wait(free0 + 8 * par, ((q >> 1) - 1) & 1);
+    ++q;
+    float bestv = -INFINITY;  // the largest of this thread's groups
     int bestg = -1;
+    uint16_t* gmax = sm.gmax[par];
     auto best = [&](int g, float mx) {
-      put_max<E>(sm, g, mx);
-      second = fmaxf(second, fminf(mx, bestv));
+      gmax[g] = (uint16_t)(__float_as_uint(mx) >> 16);
       if (bestg < 0 || mx > bestv || (mx == bestv && g < bestg)) {
         bestv = mx;
         bestg = g;
@@ -704,10 +823,7 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
         if (kTop) best(g, R::max_of(u));
       }
     }
-    // ---- the item's results, into buffers that the last warp is done with
-    const int par = q & 1;
-    if (q >= 2) wait(free0 + 8 * par, ((q >> 1) - 1) & 1);
-    ++q;
+    // ---- the item's results
     Stat st = sums.stat();
     if (sticks) {
       if (has_edge) st = merge(st, stat_of(edge), c);
@@ -719,78 +835,9 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
     sm.m[par][tid] = st.m;
     sm.s[par][tid] = st.s;
     sm.e[par][tid] = st.e;
-    if (!kTop) {
-      hand_over(par);
-      continue;
-    }
-    // Candidates.  The largest groups of every warp's threads, a few of each warp, make 32 or 64
-    // distinct ones, and the top-th of them the threshold: it takes the others of the same
-    // maximum along, down to the last place among them.  (With 32 for any top, 32 alternatives
-    // let three times as many logits through as with 64: one in twelve of the warps has two of
-    // its three largest below the rest.)
-    const int tops = a.top > kFewTops ? 64 : 32;
-    const int with = min((it.ng + 31) >> 5, kWarps);
-    const uint32_t largest = bestg < 0 ? 0u : order_of(bestv);
-    if (warp < with) {
-      uint32_t o = largest;
-      for (int i = warp; i < tops; i += with) {
-        const uint32_t top = __reduce_max_sync(0xffffffffu, o);
-        const uint32_t at = __reduce_min_sync(0xffffffffu, o == top ? (uint32_t)bestg : 0xffffffffu);
-        if (lane == 0) {
-          sm.tops[par][i] = top;
-          sm.topg[par][i] = top ? (int)at : -1;
-        }
-        if (o == top && (uint32_t)bestg == at) o = 0u;
-      }
-    }
-    consumers_sync();
-    uint32_t floor_o;
-    int floor_g;
-    {
-      const uint32_t x = sm.tops[par][lane], x2 = tops > 32 ? sm.tops[par][lane + 32] : 0u;
-      const uint4* all = reinterpret_cast<const uint4*>(sm.tops[par]);
-      int above = 0, above2 = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4 y = all[i];
-        above += (y.x > x) + (y.y > x) + (y.z > x) + (y.w > x);
-      }
-      if (tops > 32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 y = all[i], z = all[i + 8];
-          above2 += (y.x > x2) + (y.y > x2) + (y.z > x2) + (y.w > x2);
-          above2 += (z.x > x2) + (z.y > x2) + (z.z > x2) + (z.w > x2);
-          above += (z.x > x) + (z.y > x) + (z.z > x) + (z.w > x);
-        }
-      }
-      // the lowest of those with fewer than top above them
-      floor_o = __reduce_min_sync(0xffffffffu, min(above < a.top ? x : 0xffffffffu,
-                                                   tops > 32 && above2 < a.top ? x2 : 0xffffffffu));
-      floor_g = __reduce_max_sync(0xffffffffu, max(x == floor_o ? sm.topg[par][lane] : -1,
-                                                   tops > 32 && x2 == floor_o ? sm.topg[par][lane + 32] : -1));
-      if (floor_o == 0) floor_g = INT32_MAX;  // fewer groups than alternatives: all of them
-    }
-    if (tid == 0) {
-      sm.floor_o[par] = floor_o;
-      sm.floor_g[par] = floor_g;
-    }
-    auto reaches = [&](uint32_t o, int g) { return o > floor_o || (o == floor_o && g <= floor_g); };
-    if (bestg >= 0 && reaches(largest, bestg)) {
-      auto put = [&](int g) {
-        const int at = atomicAdd(&sm.cands[par], 1);
-        if (at < kCand) sm.cand[par][at] = (uint16_t)g;
-      };
-      if (order_of(second) < floor_o) {  // most threads that have one
-        put(bestg);
-      } else {
-        auto visit = [&](int g) {
-          if (reaches(order_of(group_max<E>(sm, g)), g)) put(g);
-        };
-        if (tid == 0 && it.in0 > 0) visit(0);
-        for (int g = it.in0 + tid; g < it.in1; g += kThreads) visit(g);
-        if (tid == kThreads - 32 && it.in1 < it.ng) visit(it.ng - 1);
-      }
+    if (kTop) {
+      sm.best[par][tid] = bestg < 0 ? 0u : order_of(bestv);
+      sm.bestg[par][tid] = (uint16_t)bestg;
     }
     hand_over(par);
   }
@@ -988,20 +1035,7 @@ __global__ void __launch_bounds__(kRowsThreads, 4) logp_rows(const FwdArgs a, in
       }
     }
     row_sync<W>(group);
-    // the top-th of them: the lowest of those with fewer than top above them, and the last place
-    // among its equals
-    const uint32_t x = sm.tops[lane], x2 = sm.tops[lane + 32];
-    const uint4* all = reinterpret_cast<const uint4*>(sm.tops);
-    int above = 0, above2 = 0;
-#pragma unroll 4
-    for (int k = 0; k < 16; ++k) {
-      const uint4 y = all[k];
-      above += (y.x > x) + (y.y > x) + (y.z > x) + (y.w > x);
-      above2 += (y.x > x2) + (y.y > x2) + (y.z > x2) + (y.w > x2);
-    }
-    floor_o = __reduce_min_sync(0xffffffffu, min(above < a.top ? x : 0xffffffffu, above2 < a.top ? x2 : 0xffffffffu));
-    floor_g = __reduce_max_sync(0xffffffffu, max(x == floor_o ? sm.topg[lane] : -1, x2 == floor_o ? sm.topg[lane + 32] : -1));
-    if (floor_o == 0) floor_g = INT32_MAX;  // fewer groups than alternatives: all of them
+    threshold(sm.tops, sm.topg, a.top, lane, &floor_o, &floor_g);
     const uint32_t floor16 = floor_o >> 16;
     const int n = v.groups();
     for (int g0 = l * 8; g0 < n; g0 += L * 8) {
@@ -1328,7 +1362,7 @@ int rows_warps(bool is_bf16, int64_t T, int V, int top, int sms) {
 // as many as make an item for every SM, of a chunk at least.
 int ls_token_logp_parts(bool is_bf16, int64_t T, int V, int top, int sms) {
   if (rows_warps(is_bf16, T, V, top, sms) > 0) return 1;
-  const int64_t groups = groups_of(is_bf16, V), room = kGmaxBytes / (is_bf16 ? 2 : 4);
+  const int64_t groups = groups_of(is_bf16, V), room = kMaxGroups;
   int64_t parts = top > 0 ? (groups + room - 1) / room : 1;
   if (T > 0 && T * parts < sms) {
     int64_t more = sms / T;
@@ -1366,7 +1400,7 @@ cudaError_t launch_rows(const FwdArgs& a, int W, cudaStream_t st) {
 template <typename E, bool kTop>
 cudaError_t launch_fwd(const FwdArgs& a, int sms, cudaStream_t st) {
   // without alternatives nothing behind `red` is used
-  const size_t smem = Cfg<kTop>::kStages * kChunkBytes + (kTop ? sizeof(FwdSmem) : offsetof(FwdSmem, floor_o));
+  const size_t smem = Cfg<kTop>::kStages * kChunkBytes + (kTop ? sizeof(FwdSmem) : offsetof(FwdSmem, best));
   cudaError_t e =
       cudaFuncSetAttribute(logp_fwd<E, kTop>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
