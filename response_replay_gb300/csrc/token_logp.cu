@@ -340,7 +340,7 @@ __device__ __forceinline__ void write_top(const FwdArgs& a, int64_t row, u64 key
 // chunk, and runs ahead into the next item while the consumers end one; a last warp takes the
 // consumers' results and maxima, finds the candidates, reads those groups again and writes the
 // row's outputs while the consumers are at the next item (with the consumers at the candidates
-// 4,096 rows of 151,936 bf16 values took 241 us for 5 alternatives).  Groups that stick out of the
+// 4,096 rows of 151,936 bf16 values took 241 us for 5 alternatives and 271 for 20; now 232 and 236).  Groups that stick out of the
 // row are read with plain loads.
 constexpr int kChunkBytes = kThreads * kGroupBytes;
 constexpr int kCtaThreads = kThreads + 64;
@@ -788,12 +788,12 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
     const int par = q & 1;
     if (q >= 2) wait(free0 + 8 * par, ((q >> 1) - 1) & 1);
     ++q;
-    float bestv = -INFINITY;  // the largest of this thread's groups
+    float bestv = NAN;  // the largest of this thread's groups (the first of its equals), which
     int bestg = -1;
     uint16_t* gmax = sm.gmax[par];
     auto best = [&](int g, float mx) {
       gmax[g] = (uint16_t)(__float_as_uint(mx) >> 16);
-      if (bestg < 0 || mx > bestv || (mx == bestv && g < bestg)) {
+      if (!(mx <= bestv)) {
         bestv = mx;
         bestg = g;
       }
@@ -829,7 +829,9 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
       if (has_edge) st = merge(st, stat_of(edge), c);
       if (kTop) {
         const uint32_t o = __reduce_max_sync(0xffffffffu, has_edge ? order_of(edge) : 0u);
-        if (lane == 0) best(edge_g, o ? value_of((u64)o << 32) : NAN);
+        const float mx = o ? value_of((u64)o << 32) : NAN;
+        if (lane == 0 && mx == bestv && edge_g < bestg) bestg = edge_g;
+        if (lane == 0) best(edge_g, mx);
       }
     }
     sm.m[par][tid] = st.m;
@@ -1340,9 +1342,9 @@ int rows_cap(bool is_bf16, int V) { return (V / (is_bf16 ? 8 : 4) + 2 + 7) & ~7;
 // Warps that take a row, 0: rows are streamed (logp_fwd).  Rows go to warps where what follows a row
 // costs more than its logits: up to 80 KB a row (4,096 bf16 rows of 32,003 values: 48 us against 66
 // streamed, 2,000 of 50,257: 51 against 46), with alternatives up to 160 KB of bf16 or 96 KB of fp32
-// (with 20 of them 4,096 bf16 rows of 1,000 values: 16 against 196 us, of 32,003: 82 against 182,
-// 2,000 of 64,000: 73 against 106, 4,096 of 151,936: 272 against 281; 4,096 fp32 rows of 16,000: 63
-// against 110, 2,000 of 50,257: 97 against 82), but few long rows, which are cut into parts over all
+// (with 20 of them 4,096 bf16 rows of 1,000 values: 15 against 196 us, of 32,003: 83 against 182,
+// 2,000 of 64,000: 73 against 106, 4,096 of 151,936: 272 against 236; 4,096 fp32 rows of 16,000: 62
+// against 110, 2,000 of 50,257: 97 against 72), but few long rows, which are cut into parts over all
 // SMs.  More warps a row until four CTAs fit an SM and 12 warps an SM have a row, two vectors a lane
 // at least, and a lane adds at most 512 pairs (1,000 rows of 8,000 values with 20 alternatives: 17, 14, 16, 20 us with 1, 2, 4, 8 warps;
 // 4,096 of 32,003: 102, 83, 89, 106).
