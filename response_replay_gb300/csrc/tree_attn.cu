@@ -18,9 +18,13 @@
 // leaves a partial (o, lse); tree_combine merges a row's partials by log-sum-exp.
 //
 // What bounds it.  256 rows meet a key tile of 64 KB for 4.2 MFLOP of each product: the tensor
-// core, then the softmax that feeds it.
+// core, 2,048 clocks a step of two row tiles and 128 keys.  A step takes about 3,150: from one row
+// tile's S to the other's lie the softmax's wake, its load of S and the issuer's wake.  8 members'
+// 16 tokens of 24 / 4 heads over 2,097,152: 2.0 to 2.1 ms, 1,560 to 1,640 TFLOP/s; 64 members of up
+// to 24 over 32,749, with responses of up to 8,192: 420 us.  (S and P over one another, an S buffer a
+// row tile: 2.31 ms.  Slots of 64 keys, two a row tile: 2.96 ms.)
 //
-// CTA (one per SM, 12 warps; the pipeline of replay_fwd_tc.cu):
+// CTA (one per SM, 12 warps):
 //   warp 0      TMA producer: K and V tiles, page by page, into a ring of five.
 //   warps 1, 2  issue S_t = Q_t K^T and O_t += P_t V of tile A and tile B, one thread each.
 //   warp 3      clears V rows behind a sequence's end (stale page contents, even NaN, would
