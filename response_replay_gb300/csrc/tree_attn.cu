@@ -319,10 +319,10 @@ __device__ void make_plan(const LsDecodeArgs& a, Vars* v, uint16_t* tok, int32_t
     unsigned long long best = ~0ull;
     for (int i = tid; i < most * kRounds; i += kThreads) {
       const int32_t cp = 1 + i / kRounds, strip = strip_of(cp, 1 + i % kRounds);
-      const int32_t strips = (a.nt + strip - 1) / strip;
-      const long long tp = (long long)((strips * per_strip + cp - 1) / cp) * (strip + kSegTiles);
-      const long long tr = all_units > 0 ? (all_units + ctas - cp - 1) / (ctas - cp) : 0;
-      const unsigned long long x = (unsigned long long)((tp > tr ? tp : tr) << 16 | i);
+      const uint32_t strips = (uint32_t)(a.nt + strip - 1) / strip;
+      const unsigned long long tp = (unsigned long long)((strips * per_strip + cp - 1) / cp) * (strip + kSegTiles);
+      const unsigned long long tr = all_units > 0 ? (uint32_t)(all_units + ctas - cp - 1) / (ctas - cp) : 0;
+      const unsigned long long x = (tp > tr ? tp : tr) << 16 | i;
       best = x < best ? x : best;
     }
 #pragma unroll
@@ -808,16 +808,24 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
 }
 
 // Merge a row's partials: lse = log2 sum 2^lse_k, o = sum 2^(lse_k - lse) o_k, in a fixed
-// order.  A block takes eight drafted rows of one member and KV head, a thread four values of one
-// of them: a warp's loads are whole lines of the partials (eight rows, four values of each in turn).
+// order.  Eight drafted rows of one member and KV head are a block's, a thread four values of one of
+// them, or (kWide) a warp's, a thread 32 values; a warp's loads are whole lines of the partials (eight
+// rows, four values of each in turn).  With many rows there are few partials of each, and what a
+// thread does besides its values counts (2,784 tokens of 16 / 8 heads over 46 and responses of up to
+// 464: the call takes 87 us with a block, 64 with a warp); with few rows there are many, and the loads
+// under way count.
 constexpr int kCombineWarps = 8;
 
+template <bool kWide>
 __global__ void __launch_bounds__(kCombineWarps * 32)
 tree_combine(const __grid_constant__ LsDecodeArgs a) {
+  constexpr int kChunks = kWide ? 8 : 1, kBatch = kWide ? 2 : 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t octets = (a.n * a.g + 7) >> 3, m = blockIdx.x / octets, h = blockIdx.y;
-  const int32_t tokens = drafted_tokens(a, m), chunk = warp * 4 + (lane >> 3);
-  const int32_t mrow = 8 * (blockIdx.x - m * octets) + (lane & 7);  // among the drafted ones
+  const int32_t octets = (a.n * a.g + 7) >> 3, blocks = kWide ? (octets + 7) >> 3 : octets;
+  const int32_t m = blockIdx.x / blocks, h = blockIdx.y, b = blockIdx.x - m * blocks;
+  const int32_t tokens = drafted_tokens(a, m);
+  const int32_t chunk = (kWide ? 0 : warp * 4) + (lane >> 3);                    // the first; then every fourth
+  const int32_t mrow = 8 * (kWide ? b * 8 + warp : b) + (lane & 7);  // among the drafted ones
   const bool resp = clamp_len(a, __ldg(a.lens + m)) > 0;
   // Rows that are not written (padding, members out of use) wait all the same: the stream goes
   // on when this grid ends.
@@ -837,42 +845,55 @@ tree_combine(const __grid_constant__ LsDecodeArgs a) {
                       : resp0 + (int64_t)(k - strips) * resp_rows_of(a);
   };
   float mx = -INFINITY, sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kBatch = 4;
+  float4 acc[kChunks];
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int32_t k0 = 0; k0 < count; k0 += kBatch) {
     float l[kBatch];
-    float4 v[kBatch];
+    float4 v[kBatch][kChunks];
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      l[b] = -INFINITY;
-      if (k0 + b < count) {
-        const int64_t r = part_row(k0 + b);
-        l[b] = __ldcg(a.part_lse + r);
-        v[b] = *reinterpret_cast<const float4*>(part_at(a, r) + chunk * 32);
+    for (int k = 0; k < kBatch; ++k) {
+      l[k] = -INFINITY;
+      if (k0 + k < count) {
+        const int64_t r = part_row(k0 + k);
+        l[k] = __ldcg(a.part_lse + r);
+        const float* p = part_at(a, r) + chunk * 32;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) v[k][c] = __ldcg(reinterpret_cast<const float4*>(p + c * 128));
       }
     }
-    const float top = fmaxf(mx, fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])));
+    float top = mx;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) top = fmaxf(top, l[k]);
     if (top == -INFINITY) continue;
     const float old = exp2f(mx - top);
     mx = top;
     sum *= old;
-    acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      if (l[b] == -INFINITY) continue;  // a part that saw no key adds nothing
-      const float w = exp2f(l[b] - mx);
+    for (int c = 0; c < kChunks; ++c)
+      acc[c] = make_float4(acc[c].x * old, acc[c].y * old, acc[c].z * old, acc[c].w * old);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (l[k] == -INFINITY) continue;  // a part that saw no key adds nothing
+      const float w = exp2f(l[k] - mx);
       sum += w;
-      acc.x = fmaf(w, v[b].x, acc.x);
-      acc.y = fmaf(w, v[b].y, acc.y);
-      acc.z = fmaf(w, v[b].z, acc.z);
-      acc.w = fmaf(w, v[b].w, acc.w);
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        acc[c].x = fmaf(w, v[k][c].x, acc[c].x);
+        acc[c].y = fmaf(w, v[k][c].y, acc[c].y);
+        acc[c].z = fmaf(w, v[k][c].z, acc[c].z);
+        acc[c].w = fmaf(w, v[k][c].w, acc[c].w);
+      }
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key at all: o = 0, lse = -inf
   const int32_t row = (a.n - tokens) * a.g + mrow;  // the drafted ones are the member's last
   const int64_t to = ((int64_t)m * a.n + row / a.g) * a.hq + h * a.g + row % a.g;
-  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + to * kD + chunk * 4) =
-      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  __nv_bfloat16* po = static_cast<__nv_bfloat16*>(a.o) + to * kD + chunk * 4;
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c)
+    *reinterpret_cast<uint2*>(po + c * 16) = make_uint2(pack_bf16(acc[c].x * inv, acc[c].y * inv),
+                                                        pack_bf16(acc[c].z * inv, acc[c].w * inv));
   if (chunk == 0) a.lse[to] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
@@ -899,12 +920,15 @@ cudaError_t ls_launch_tree_attn(const LsDecodeArgs& a, cudaStream_t st) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.M * ((a.n * a.g + 7) / 8)), (unsigned)a.hkv);
+  // rows enough for a warp an SM and four schedulers
+  const int octets = (a.n * a.g + 7) / 8;
+  const bool wide = (int64_t)a.M * octets * a.hkv >= 8 * a.cols;
+  cfg.gridDim = dim3((unsigned)(a.M * (wide ? (octets + 7) / 8 : octets)), (unsigned)a.hkv);
   cfg.blockDim = dim3(kCombineWarps * 32);
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, tree_combine, a);
+  e = wide ? cudaLaunchKernelEx(&cfg, tree_combine<true>, a) : cudaLaunchKernelEx(&cfg, tree_combine<false>, a);
   if (e == cudaSuccess) ls_note_launch();
   return e;
 }
