@@ -147,72 +147,69 @@ __global__ void __launch_bounds__(kMaxRows) accept_draft_kernel(
 
 constexpr int kMoveWarps = 8;
 
-// A warp moves the kept rows of one member, KV head, pool and layer: row i of `rows` goes to
-// the i-th key behind the context.  Rows ascend, so i <= its row, and a key is written only
-// after every row that could be read from it has been (in this batch's loads or before).
+// A block moves the kept rows of one member and layer: row i of `rows` goes to the i-th key behind
+// the context.  It looks the rows' places up once; then a warp takes a KV head of a pool at a time.
+// Rows ascend, so i <= its row, and a key is written only after every row that could be read from
+// it has been (in this batch's loads or before).  (A warp of its own a head and pool, each with
+// its own look-ups: 43 us for the 202 MB of 256 members in 16 layers, now 36.)
 __global__ void __launch_bounds__(kMoveWarps * 32) compact_rows_kernel(
     const LsLayerPools p, const int32_t* __restrict__ table, int max_blocks, const LsDraftArgs a,
     const int32_t* __restrict__ rows, const int32_t* __restrict__ count) {
-  const int lane = threadIdx.x & 31;
-  int64_t item = (int64_t)blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
-  const int64_t per = (int64_t)p.layers * p.hkv * 2;
-  if (item >= per * a.members) return;
-  const int m = (int)(item / per);
-  item -= m * per;
-  const bool first = item == 0;  // reports
-  const int layer = (int)(item / (2 * p.hkv)), h = (int)(item >> 1) % p.hkv;
-  uint4* pool = reinterpret_cast<uint4*>(
-      static_cast<__nv_bfloat16*>(item & 1 ? p.v_pool : p.k_pool) + layer * p.stride);
+  __shared__ int64_t from[kMaxRows], to[kMaxRows];  // in 16 bytes, under KV head 0; -1: not moved
+  const int tid = threadIdx.x, lane = tid & 31, warps = blockDim.x >> 5;
+  const int m = blockIdx.x, layer = blockIdx.y;
   const Member x = member_of(a, m, false);
-  int n = __ldg(count + m);
+  const int n = __ldg(count + m);
   const int64_t room = (int64_t)max_blocks << p.ps_log2;
   bool bad = n < 0 || n > x.drafted || x.len > room;
-  n = bad ? 0 : n;
   // rows of the draft, ascending: so row i is the i-th drafted one or a later one
   const int32_t* mine = rows + (int64_t)m * a.n;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const int i = i0 + lane, r = i < n ? __ldg(mine + i) : a.n;
-    const int prev = i > 0 && i < n ? __ldg(mine + i - 1) : x.first - 1;
-    if (__any_sync(0xffffffffu, i < n && (r <= prev || r >= a.n))) bad = true;
+  const int32_t* blocks = table + (int64_t)m * max_blocks;
+  const int base = x.len - x.drafted;
+  auto key_at = [&](int key, int* page) {  // of KV head 0
+    *page = __ldg(blocks + (key >> p.ps_log2));
+    return (((int64_t)*page * p.hkv) << p.ps_log2 | (key & ((1 << p.ps_log2) - 1))) * 16;
+  };
+  for (int i = tid; !bad && i < n; i += blockDim.x) {
+    const int r = __ldg(mine + i), prev = i > 0 ? __ldg(mine + i - 1) : x.first - 1;
+    if (r <= prev || r >= a.n) bad = true;
+    if (bad) break;
+    from[i] = -1;
+    if (r - x.first == i) continue;
+    int pf, pt;
+    const int64_t f = key_at(base + r - x.first, &pf), t = key_at(base + i, &pt);
+    if ((uint32_t)pf >= (uint32_t)p.num_pages || (uint32_t)pt >= (uint32_t)p.num_pages) {
+      if (layer == 0) ls_report(a.err, LS_DEVERR_CHECK);
+    } else {
+      from[i] = f;
+      to[i] = t;
+    }
   }
-  if (bad) {
-    if (first && lane == 0) ls_report(a.err, LS_DEVERR_CHECK);
+  if (__syncthreads_or(bad)) {
+    if (layer == 0 && tid == 0) ls_report(a.err, LS_DEVERR_CHECK);
     return;
   }
-  const int ps_mask = (1 << p.ps_log2) - 1;
-  const int32_t* blocks = table + (int64_t)m * max_blocks;
-  auto key_at = [&](int key) {  // the row's first 16 bytes, or -1
-    const int page = __ldg(blocks + (key >> p.ps_log2));
-    if ((uint32_t)page >= (uint32_t)p.num_pages) {
-      ls_report(a.err, LS_DEVERR_CHECK);
-      return (int64_t)-1;
-    }
-    return (((int64_t)page * p.hkv + h) << p.ps_log2 | (key & ps_mask)) * 16;
-  };
   constexpr int kBatch = 4;  // two rows a step
-  const int half = lane >> 4, c = lane & 15, base = x.len - x.drafted;
-  for (int i0 = 0; i0 < n; i0 += 2 * kBatch) {
-    uint4 v[kBatch];
-    int64_t to[kBatch];
+  const int half = lane >> 4, c = lane & 15;
+  for (int item = tid >> 5; item < 2 * p.hkv; item += warps) {
+    uint4* pool = reinterpret_cast<uint4*>(
+        static_cast<__nv_bfloat16*>(item & 1 ? p.v_pool : p.k_pool) + layer * p.stride) +
+        (((int64_t)(item >> 1) << p.ps_log2) * 16 + c);
+    for (int i0 = 0; i0 < n; i0 += 2 * kBatch) {
+      uint4 v[kBatch];
+      bool moves[kBatch];
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int i = i0 + 2 * b + half;
-      to[b] = -1;
-      if (i < n) {
-        const int r = __ldg(mine + i) - x.first;  // of the draft
-        if (r != i) {
-          const int64_t from = key_at(base + r);
-          to[b] = key_at(base + i);
-          if (from < 0) to[b] = -1;
-          if (to[b] >= 0) v[b] = pool[from + c];
-        }
+      for (int b = 0; b < kBatch; ++b) {
+        const int i = i0 + 2 * b + half;
+        moves[b] = i < n && from[i] >= 0;
+        if (moves[b]) v[b] = pool[from[i]];
       }
-    }
-    __syncwarp();
+      __syncwarp();
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b)
-      if (to[b] >= 0) pool[to[b] + c] = v[b];
-    __syncwarp();
+      for (int b = 0; b < kBatch; ++b)
+        if (moves[b]) pool[to[i0 + 2 * b + half]] = v[b];
+      __syncwarp();
+    }
   }
 }
 
@@ -277,8 +274,8 @@ cudaError_t ls_launch_accept_draft(const LsDraftArgs& a, const int32_t* tokens,
 cudaError_t ls_launch_compact_rows(const LsLayerPools& p, const int32_t* table, int32_t max_blocks,
                                    const LsDraftArgs& a, const int32_t* rows, const int32_t* count,
                                    cudaStream_t st) {
-  const int64_t warps = (int64_t)a.members * p.layers * p.hkv * 2;
-  compact_rows_kernel<<<(unsigned)((warps + kMoveWarps - 1) / kMoveWarps), kMoveWarps * 32, 0, st>>>(
+  const int warps = 2 * p.hkv < kMoveWarps ? 2 * p.hkv : kMoveWarps;
+  compact_rows_kernel<<<dim3(a.members, p.layers), warps * 32, 0, st>>>(
       p, table, max_blocks, a, rows, count);
   const cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) ls_note_launch();
