@@ -168,6 +168,42 @@ def test_attention(cuda, P, lens, drafted, n, hq, hkv, ps, rps):
     t.check(*t.run())
 
 
+@pytest.mark.parametrize("P,M,top,n,hq,hkv,ps,rps", [
+    (5003, 40, 3000, 24, 24, 4, 16, 256), (257, 58, 460, 48, 16, 8, 256, 16), (40000, 9, 200, 29, 35, 5, 64, 64),
+    (3, 22, 2900, 64, 24, 4, 64, 64)])
+def test_groups(cuda, P, M, top, n, hq, hkv, ps, rps):
+    """Ragged drafts of many members, a CTA's share of several prompt strips and responses, of one row
+    tile and of two; member by member against 64 bits on the GPU, with qk_oracle.decode's bounds."""
+    rng = np.random.default_rng(P)
+    drafted = rng.integers(0, n + 1, M)
+    lens = drafted + rng.integers(0, top, M)
+    lens[::7] = -1
+    t = Tree(cuda, P, lens.tolist(), drafted.tolist(), n, hq, hkv, ps, rps, seed=P)
+    o, lse = t.run(o=torch.zeros_like(t.q), lse=torch.zeros(M, n, hq, device=cuda))
+    g = hq // hkv
+    kp, vp = t.kp.double(), t.vp.double()
+    for m in range(M):
+        x, c = int(lens[m]), int(drafted[m])
+        if x < 0 or c == 0:
+            continue
+        see = torch.ones(c, P + x, dtype=torch.bool, device=cuda)
+        see[:, P + x - c:] = torch.as_tensor(t.sees[m, n - c:, n - c:], device=cuda)
+        for h in range(hkv):
+            k, v = torch.cat([kp[:, h], t.kr[m][:, h].double()]), torch.cat([vp[:, h], t.vr[m][:, h].double()])
+            q = t.q[m, n - c:, h * g:(h + 1) * g].double()
+            s = (q @ k.T * SCALE).masked_fill(~see[:, None], -torch.inf)
+            mag = (q.abs() @ k.abs().T * SCALE).masked_fill(~see[:, None], 0)
+            z = torch.logsumexp(s, -1, keepdim=True)
+            p = torch.exp(s - z)
+            want = p @ v
+            e = (qo.U16 + 2 * 128 * qo.U32 * mag.amax(-1, keepdim=True) + 2.0 ** -18) * (p @ v.abs())
+            e = e + qo.U16 * (want.abs() + e)
+            ez = 128 * qo.U32 * (p * mag).sum(-1) + 2.0 ** -18 + 2.0 ** -20 * z[..., 0].abs()
+            got = o[m, n - c:, h * g:(h + 1) * g].double()
+            assert bool(((got - want).abs() <= e).all()), (m, h)
+            assert bool(((lse[m, n - c:, h * g:(h + 1) * g].double() - z[..., 0]).abs() <= ez).all()), (m, h)
+
+
 def test_any_bits(cuda):
     """Rows may see any rows of the draft, also later ones, or none of it."""
     def some(rng, M, n):
@@ -335,11 +371,12 @@ def test_moves_refuse_what_is_no_path(cuda):
 
 # ------------------------------------------------------------------------------- together
 
-def test_drafted_rollout_equals_the_plain_one(cuda):
+@pytest.mark.parametrize("hq", [8, 40])  # drafts of a row tile, and of several
+def test_drafted_rollout_equals_the_plain_one(cuda, hq):
     """A rollout with drafts over two layers: extend, plan, append, attend, accept, settle.  Its
     accepted tokens, lengths, pages and keys are those of a rollout one token at a time, whose
     tokens the drafts partly foresee."""
-    dev, L, M, n, hq, hkv, ps, P = cuda, 2, 3, 7, 8, 2, 16, 200
+    dev, L, M, n, hkv, ps, P = cuda, 2, 3, 7, 2, 16, 200
     g = torch.Generator(device=dev)
     g.manual_seed(4)
     rng = np.random.default_rng(4)
