@@ -105,7 +105,8 @@ static_assert(kSmemBytes <= 232448, "shared memory");
 __device__ __forceinline__ uint32_t bar_addr(uint32_t base, int i) { return base + kOffBar + 8 * i; }
 
 __device__ __forceinline__ int32_t drafted_tokens(const LsDecodeArgs& a, int32_t m) {
-  return __ldg(a.lens + m) < 0 ? 0 : drafted_of(a, m);
+  const int32_t len = __ldg(a.lens + m), c = drafted_of(a, m);  // one latency
+  return len < 0 ? 0 : c;
 }
 __device__ __forceinline__ int32_t pairs_of(const LsDecodeArgs& a, int32_t tokens) {
   return (tokens * a.g + kPair - 1) / kPair;
@@ -370,6 +371,7 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023) {  // the swizzled tiles' alignment, which the declaration asks for
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x == 0) ls_report(a.err, LS_DEVERR_CHECK);
     return;
   }
@@ -380,9 +382,6 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int32_t cta = blockIdx.x;
 
-  // the combine may be launched: its blocks wait for this grid before they read from it
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  make_plan(a, vars, tok, reinterpret_cast<int32_t*>(smem + kOffRing), cta);
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bar_addr(sbase, B_KV_FULL + i), 1);
@@ -406,6 +405,11 @@ tree_attn_kernel(const __grid_constant__ TmapSet tm, const __grid_constant__ LsD
     tmem_alloc(smem_u32(&vars->tmem), 512);
     tmem_relinquish();
   }
+  // what the stream did before: lengths, drafts, queries and pages come from it
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the combine may be launched: its blocks wait for this grid before they read from it
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  make_plan(a, vars, tok, reinterpret_cast<int32_t*>(smem + kOffRing), cta);
   fence_proxy_async_smem();  // the scratch above, before TMA writes the ring
   tc_fence_before();
   __syncthreads();
@@ -913,13 +917,19 @@ cudaError_t ls_launch_tree_attn(const LsDecodeArgs& a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kSmemBytes);
   if (e != cudaSuccess) return e;
-  tree_attn_kernel<<<a.cols, kThreads, kSmemBytes, st>>>(tm, a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  ls_note_launch();
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.cols);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, tree_attn_kernel, tm, a)) != cudaSuccess) return e;
+  ls_note_launch();
+  cfg.dynamicSmemBytes = 0;
   // rows enough for a warp an SM and four schedulers
   const int octets = (a.n * a.g + 7) / 8;
   const bool wide = (int64_t)a.M * octets * a.hkv >= 8 * a.cols;
