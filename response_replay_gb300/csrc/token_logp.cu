@@ -357,7 +357,7 @@ constexpr int kFound = 32 * 16 + kRanked;
 struct FwdSmem {  // behind the ring; [2]: by parity of the item
   uint64_t full[6], empty[6], free[2];
   int abort;
-  float m[2][kThreads], s[2][kThreads], e[2][kThreads];
+  float m[2][kWarps], s[2][kWarps], e[2][kWarps];
   uint32_t best[2][kThreads];  // the largest of a thread's groups (0: none), and which
   uint16_t bestg[2][kThreads];
   alignas(16) uint32_t tops[64];
@@ -745,16 +745,8 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
       const int par = q & 1;
       ++q;
       take_over(par);
-      Stat st = {sm.m[par][lane], 0.f, 0.f};
-#pragma unroll
-      for (int i = 1; i < kWarps; ++i) st.m = fmaxf(st.m, sm.m[par][lane + 32 * i]);
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        const int t = lane + 32 * i;
-        const Stat x = move(Stat{sm.m[par][t], sm.s[par][t], sm.e[par][t]}, st.m, a.c);
-        st.s += x.s;
-        st.e += x.e;
-      }
+      Stat st = {-INFINITY, 0.f, 0.f};
+      if (lane < kWarps) st = Stat{sm.m[par][lane], sm.s[par][lane], sm.e[par][lane]};
       st = warp_stat(st, a.c);
       u64 list = 0;
       if (kTop) {
@@ -834,9 +826,12 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
         if (lane == 0) best(edge_g, mx);
       }
     }
-    sm.m[par][tid] = st.m;
-    sm.s[par][tid] = st.s;
-    sm.e[par][tid] = st.e;
+    st = warp_stat(st, c);
+    if (lane == 0) {
+      sm.m[par][warp] = st.m;
+      sm.s[par][warp] = st.s;
+      sm.e[par][warp] = st.e;
+    }
     if (kTop) {
       sm.best[par][tid] = bestg < 0 ? 0u : order_of(bestv);
       sm.bestg[par][tid] = (uint16_t)bestg;
