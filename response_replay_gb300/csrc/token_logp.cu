@@ -271,6 +271,7 @@ struct Out {
 };
 
 struct FwdArgs {
+  bool steal;       // more items than CTAs that fit: the rest of the grid is taken over
   const void* logits;
   int64_t T, ld;
   int32_t V, top, parts;
@@ -335,13 +336,15 @@ __device__ __forceinline__ void write_top(const FwdArgs& a, int64_t row, u64 key
 
 // ---------------------------------------------------------------- forward
 //
-// A persistent CTA takes items (a part of a row) by turns: a producer warp streams an item's
-// whole groups through a ring of 24 KB chunks by bulk copies, a group a consumer thread and
-// chunk, and runs ahead into the next item while the consumers end one; a last warp takes the
-// consumers' results and maxima, finds the candidates, reads those groups again and writes the
-// row's outputs while the consumers are at the next item (with the consumers at the candidates
-// 4,096 rows of 151,936 bf16 values took 241 us for 5 alternatives and 271 for 20; now 232 and 236).  Groups that stick out of the
-// row are read with plain loads.
+// A CTA an item (a part of a row), of which two fit an SM; a CTA that runs takes over others that
+// have not begun (cluster launch control), so all end together whatever the SMs' shares of HBM were:
+// dealt out beforehand they ended between 147 and 179 us (4,096 rows of 151,936 bf16 values; 182 us
+// in all, now 175).  A producer warp streams an item's whole groups through a ring of 24 KB chunks
+// by bulk copies, a group a consumer thread and chunk, and runs ahead into the next item while the
+// consumers end one; a last warp takes the consumers' results and maxima, finds the candidates, reads
+// those groups again and writes the row's outputs while the consumers are at the next item (with the
+// consumers at the candidates 241 us for 5 alternatives and 271 for 20; now 224 and 227).  Groups that
+// stick out of the row are read with plain loads.
 constexpr int kChunkBytes = kThreads * kGroupBytes;
 constexpr int kCtaThreads = kThreads + 64;
 constexpr int kHand = kThreads + 32;  // the consumers and the last warp
@@ -354,8 +357,13 @@ constexpr int kCand = 512;  // groups that reach the threshold, before the slow 
 
 constexpr int kFound = 32 * 16 + kRanked;
 
+constexpr int kQueue = 4;  // items on their way from the producer to the other warps
+
 struct FwdSmem {  // behind the ring; [2]: by parity of the item
-  uint64_t full[6], empty[6], free[2];
+  uint64_t full[6], empty[6], free[2], item_full[kQueue], item_empty[kQueue], taken;
+  alignas(16) uint32_t taken_answer[4];
+  int64_t item[kQueue];
+  int32_t target[kQueue];
   int abort;
   float m[2][kWarps], s[2][kWarps], e[2][kWarps];
   uint32_t best[2][kThreads];  // the largest of a thread's groups (0: none), and which
@@ -368,6 +376,26 @@ struct FwdSmem {  // behind the ring; [2]: by parity of the item
 };
 static_assert(3 * kThreads * kGroupBytes + sizeof(FwdSmem) <= (228 * 1024 / 2 - 1024), "two CTAs an SM");
 
+// Takes a CTA of the grid that has not begun; the answer (16 bytes) lands on `bar`.
+__device__ __forceinline__ void take_cta(uint32_t answer, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   answer),
+               "r"(bar)
+               : "memory");
+}
+// Its index, or -1: none was left.
+__device__ __forceinline__ int64_t taken_cta(uint32_t answer) {
+  uint32_t x = 0, ok;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 r;\n ld.shared.b128 r, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n selp.u32 %1, 1, 0, p;\n"
+      " mov.u32 %0, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n}\n"
+      : "=r"(x), "=r"(ok)
+      : "r"(answer)
+      : "memory");
+  return ok ? (int64_t)x : -1;
+}
 __device__ __forceinline__ void hand_over(int par) {
   if (par)
     asm volatile("bar.arrive 3, %0;" ::"n"(kHand) : "memory");
@@ -398,7 +426,7 @@ struct Item {
   static __device__ __forceinline__ int64_t row_of(const FwdArgs& a, int64_t item) {
     return a.parts == 1 ? item : item / a.parts;
   }
-  // y: the row's target, asked for one item ahead
+  // the row's target
   static __device__ __forceinline__ int32_t target(const FwdArgs& a, int64_t item) {
     return a.targets && item < a.T * a.parts ? __ldg(a.targets + row_of(a, item)) : 0;
   }
@@ -669,9 +697,9 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
   extern __shared__ __align__(1024) uint8_t ring[];
   FwdSmem& sm = *reinterpret_cast<FwdSmem*>(ring + kStages * kChunkBytes);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t items = a.T * a.parts;
   const uint32_t full0 = smem_u32(sm.full), empty0 = smem_u32(sm.empty), ring0 = smem_u32(ring);
-  const uint32_t free0 = smem_u32(sm.free);
+  const uint32_t free0 = smem_u32(sm.free), item_full0 = smem_u32(sm.item_full);
+  const uint32_t item_empty0 = smem_u32(sm.item_empty);
   volatile int* abort = &sm.abort;
   // a wait that gives up records the error and stops every later wait of the CTA
   auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -689,6 +717,11 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
     }
     umma::mbar_init(free0, 1);
     umma::mbar_init(free0 + 8, 1);
+    for (int s = 0; s < kQueue; ++s) {
+      umma::mbar_init(item_full0 + 8 * s, 1);
+      umma::mbar_init(item_empty0 + 8 * s, kWarps + 1);
+    }
+    umma::mbar_init(smem_u32(&sm.taken), 1);
     sm.abort = 0;
     umma::fence_barrier_init();
   }
@@ -701,10 +734,26 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
     // ---- producer
     if (lane == 0) {
       int issued = 0;
-      int32_t y = Item<E>::target(a, blockIdx.x);
-      for (int64_t item = blockIdx.x; item < items && !*abort; item += gridDim.x) {
+      umma::RingPos<kQueue> qp;
+      auto push = [&](int64_t item, int32_t y) {
+        if (!wait(item_empty0 + 8 * qp.stage, qp.phase ^ 1u)) return;
+        sm.item[qp.stage] = item;
+        sm.target[qp.stage] = y;
+        umma::mbar_arrive(item_full0 + 8 * qp.stage);
+        qp.advance();
+      };
+      const uint32_t answer = smem_u32(sm.taken_answer), taken = smem_u32(&sm.taken);
+      uint32_t answers = 0;
+      bool asked = false;
+      for (int64_t item = blockIdx.x; item >= 0 && !*abort;) {
+        if (a.steal) {  // the next item, while this one is streamed
+          umma::mbar_expect_tx(taken, 16);
+          take_cta(answer, taken);
+          asked = true;
+        }
+        const int32_t y = Item<E>::target(a, item);
+        push(item, y);
         const Item<E> it(a, item, y);
-        y = Item<E>::target(a, item + gridDim.x);
         const int n = it.chunks();
         const uint8_t* src = reinterpret_cast<const uint8_t*>(it.at(it.in0));
         for (int k = 0; k < n; ++k) {
@@ -717,7 +766,16 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
           ++issued;
           rp.advance();
         }
+        item = -1;
+        if (asked && wait(taken, answers & 1)) {
+          ++answers;
+          asked = false;
+          item = taken_cta(answer);
+          umma::fence_proxy_async_smem();  // read before the next answer is written
+        }
       }
+      push(-1, 0);
+      if (asked) umma::mbar_wait(taken, answers & 1);
       // no copy may still be landing when the CTA exits
       for (int s = 0; s < kStages && s < issued; ++s) {
         rp.stage = rp.stage == 0 ? kStages - 1 : rp.stage - 1;
@@ -729,12 +787,22 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
   }
 
   int q = 0;
+  umma::RingPos<kQueue> qp;
+  int64_t item = 0;
+  int32_t y = 0;
+  auto next = [&]() {  // the CTA's next item, by a warp
+    if (!wait(item_full0 + 8 * qp.stage, qp.phase)) return false;
+    item = sm.item[qp.stage];
+    y = sm.target[qp.stage];
+    __syncwarp();
+    if (lane == 0) umma::mbar_arrive(item_empty0 + 8 * qp.stage);
+    qp.advance();
+    return item >= 0;
+  };
   if (warp == kWarps + 1) {
     // ---- outputs
-    int32_t y = Item<E>::target(a, blockIdx.x);
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    while (next()) {
       const Item<E> it(a, item, y);
-      y = Item<E>::target(a, item + gridDim.x);
       if (it.pad) {
         if (it.part == 0) padding_row(a, it.row, lane);
         continue;
@@ -770,10 +838,8 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
   // ---- consumers
   const float c = a.c;
   const int mine = tid * kGroupBytes + ((tid >> 1) & 3) * 16;  // of a chunk
-  int32_t y = Item<E>::target(a, blockIdx.x);
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+  while (next()) {
     const Item<E> it(a, item, y);
-    y = Item<E>::target(a, item + gridDim.x);
     if (it.pad) continue;
     Sums<E> sums(c);
     // buffers that the last warp is done with
@@ -1395,14 +1461,13 @@ cudaError_t launch_rows(const FwdArgs& a, int W, cudaStream_t st) {
 }
 
 template <typename E, bool kTop>
-cudaError_t launch_fwd(const FwdArgs& a, int sms, cudaStream_t st) {
+cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t st) {
   // without alternatives nothing behind `red` is used
   const size_t smem = Cfg<kTop>::kStages * kChunkBytes + (kTop ? sizeof(FwdSmem) : offsetof(FwdSmem, best));
   cudaError_t e =
       cudaFuncSetAttribute(logp_fwd<E, kTop>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int64_t items = a.T * a.parts, grid = items < 2 * sms ? items : 2 * sms;
-  logp_fwd<E, kTop><<<(unsigned)grid, kCtaThreads, smem, st>>>(a);
+  logp_fwd<E, kTop><<<(unsigned)(a.T * a.parts), kCtaThreads, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   ls_note_launch();
@@ -1430,6 +1495,7 @@ cudaError_t ls_launch_token_logp_fwd(const LsTokenLogpArgs& b, int parts, int sm
   a.V = b.V;
   a.top = b.top;
   a.parts = parts;
+  a.steal = b.T * parts > 2 * sms;
   a.targets = b.targets;
   a.inv_tau = 1.0 / (double)b.temperature;
   a.c = (float)(kLog2ed * a.inv_tau);
@@ -1445,8 +1511,8 @@ cudaError_t ls_launch_token_logp_fwd(const LsTokenLogpArgs& b, int parts, int sm
     return b.top > 0 ? launch_rows<float, true>(a, W, st) : launch_rows<float, false>(a, W, st);
   }
   if (b.is_bf16)
-    return b.top > 0 ? launch_fwd<__nv_bfloat16, true>(a, sms, st) : launch_fwd<__nv_bfloat16, false>(a, sms, st);
-  return b.top > 0 ? launch_fwd<float, true>(a, sms, st) : launch_fwd<float, false>(a, sms, st);
+    return b.top > 0 ? launch_fwd<__nv_bfloat16, true>(a, st) : launch_fwd<__nv_bfloat16, false>(a, st);
+  return b.top > 0 ? launch_fwd<float, true>(a, st) : launch_fwd<float, false>(a, st);
 }
 
 // Parts of up to 128 KB, smaller ones when there are few rows.
