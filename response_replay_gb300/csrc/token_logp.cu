@@ -343,7 +343,7 @@ __device__ __forceinline__ void write_top(const FwdArgs& a, int64_t row, u64 key
 // by bulk copies, a group a consumer thread and chunk, and runs ahead into the next item while the
 // consumers end one; a last warp takes the consumers' results and maxima, finds the candidates, reads
 // those groups again and writes the row's outputs while the consumers are at the next item (with the
-// consumers at the candidates 241 us for 5 alternatives and 271 for 20; now 224 and 227).  Groups that
+// consumers at the candidates 241 us for 5 alternatives and 271 for 20; now 201 and 202).  Groups that
 // stick out of the row are read with plain loads.
 constexpr int kChunkBytes = kThreads * kGroupBytes;
 constexpr int kCtaThreads = kThreads + 64;
@@ -876,9 +876,9 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
       __syncwarp();
       if (lane == 0) umma::mbar_arrive(empty0 + 8 * rp.stage);
       rp.advance();
-      if (has) {
-        sums.template add<4>(u);
+      if (has) {  // (the maximum first: behind the sums it costs registers, 227 against 201 us)
         if (kTop) best(g, R::max_of(u));
+        sums.template add<4>(u);
       }
     }
     // ---- the item's results
@@ -988,7 +988,7 @@ __global__ void __launch_bounds__(kRowsThreads, 4) logp_rows(const FwdArgs a, in
   const int l = wl * 32 + lane;
   constexpr int L = 32 * W;
   RowSmem& sm = reinterpret_cast<RowSmem*>(rows_smem)[group];
-  // the upper halves of the groups' maxima, as whole numbers in their order
+  // the upper halves of the groups' maxima
   uint16_t* gmax = reinterpret_cast<uint16_t*>(rows_smem + (kRowsWarps / W) * sizeof(RowSmem)) + group * cap;
   const int64_t row = (int64_t)blockIdx.x * (kRowsWarps / W) + group;
   if (row >= a.T) return;  // (a row's warps leave together)
@@ -1003,22 +1003,24 @@ __global__ void __launch_bounds__(kRowsThreads, 4) logp_rows(const FwdArgs a, in
   if (kTop && l == 0) sm.cands = 0;
 
   Sums<E> sums(a.c);
-  uint32_t best = 0, second = 0;  // the largest of this lane's groups, the next (0: none)
+  float bestv = NAN, secondv = NAN;  // the largest of this lane's groups, the next
   int bestg = -1, secondg = -1;
-  auto take = [&](int g, float mx) {
-    const uint32_t o = order_of(mx);
-    gmax[g] = (uint16_t)(o >> 16);
-    if (o > best) {
+  auto largest = [&](int g, float mx) {
+    if (!(mx <= bestv)) {
       if (W == 1) {
-        second = best;
+        secondv = bestv;
         secondg = bestg;
       }
-      best = o;
+      bestv = mx;
       bestg = g;
-    } else if (W == 1 && o > second) {
-      second = o;
+    } else if (W == 1 && !(mx <= secondv)) {
+      secondv = mx;
       secondg = g;
     }
+  };
+  auto take = [&](int g, float mx) {
+    gmax[g] = (uint16_t)(__float_as_uint(mx) >> 16);
+    largest(g, mx);
   };
   // one value outside the vectors a lane: the head's, then the tail's
   float edge = NAN;
@@ -1029,14 +1031,11 @@ __global__ void __launch_bounds__(kRowsThreads, 4) logp_rows(const FwdArgs a, in
       const uint32_t o = has_edge ? order_of(edge) : 0u;
       const uint32_t oh = __reduce_max_sync(0xffffffffu, in_head ? o : 0u);
       const uint32_t ot = __reduce_max_sync(0xffffffffu, in_head ? 0u : o);
-      if (lane == 0) {
-        gmax[0] = (uint16_t)(oh >> 16);
-        gmax[v.nvec + 1] = (uint16_t)(ot >> 16);
+      if (lane == 0) {  // (a negative NaN where there are none: below every threshold)
+        gmax[0] = oh ? (uint16_t)(__float_as_uint(value_of((u64)oh << 32)) >> 16) : 0xffffu;
+        gmax[v.nvec + 1] = ot ? (uint16_t)(__float_as_uint(value_of((u64)ot << 32)) >> 16) : 0xffffu;
       }
-      if (in_head && o) {
-        best = o;
-        bestg = 0;
-      }
+      if (in_head && o) largest(0, edge);
     }
   }
   int i = l;
@@ -1045,30 +1044,20 @@ __global__ void __launch_bounds__(kRowsThreads, 4) logp_rows(const FwdArgs a, in
     uint4 u[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) u[k] = __ldg(v.vec(i + k * L));
-    sums.template add<4>(u);
-    if (kTop) {
+    if (kTop) {  // (before the sums, as above)
 #pragma unroll
       for (int k = 0; k < 4; ++k) take(i + k * L + 1, vec_max<E>(u[k]));
     }
+    sums.template add<4>(u);
   }
 #pragma unroll 1
   for (; i < v.nvec; i += L) {
     const uint4 u = __ldg(v.vec(i));
-    sums.template add<1>(&u);
     if (kTop) take(i + 1, vec_max<E>(u));
+    sums.template add<1>(&u);
   }
-  if (kTop && has_edge && !in_head) {
-    const uint32_t o = order_of(edge);
-    if (o > best) {
-      second = best;
-      secondg = bestg;
-      best = o;
-      bestg = v.nvec + 1;
-    } else if (o > second) {
-      second = o;
-      secondg = v.nvec + 1;
-    }
-  }
+  if (kTop && has_edge && !in_head && edge == edge) largest(v.nvec + 1, edge);
+  const uint32_t best = bestg < 0 ? 0u : order_of(bestv), second = secondg < 0 ? 0u : order_of(secondv);
   Stat st = sums.stat();
   if (has_edge) st = merge(st, stat_of(edge), a.c);
   st = warp_stat(st, a.c);
@@ -1099,11 +1088,11 @@ __global__ void __launch_bounds__(kRowsThreads, 4) logp_rows(const FwdArgs a, in
     }
     row_sync<W>(group);
     threshold(sm.tops, sm.topg, a.top, lane, &floor_o, &floor_g);
-    const uint32_t floor16 = floor_o >> 16;
+    const uint32_t floor16 = (floor_o >> 16) == 0x8000u ? 0x7fffu : floor_o >> 16;  // (both zeros are one)
     const int n = v.groups();
     for (int g0 = l * 8; g0 < n; g0 += L * 8) {
       const uint4 w = *reinterpret_cast<const uint4*>(gmax + g0);
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+      const uint32_t ws[4] = {order_halves(w.x), order_halves(w.y), order_halves(w.z), order_halves(w.w)};
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const uint32_t o = k & 1 ? ws[k >> 1] >> 16 : ws[k >> 1] & 0xffffu;
@@ -1402,13 +1391,13 @@ int rows_cap(bool is_bf16, int V) { return (V / (is_bf16 ? 8 : 4) + 2 + 7) & ~7;
 
 // Warps that take a row, 0: rows are streamed (logp_fwd).  Rows go to warps where what follows a row
 // costs more than its logits: up to 80 KB a row (4,096 bf16 rows of 32,003 values: 48 us against 66
-// streamed, 2,000 of 50,257: 51 against 46), with alternatives up to 160 KB of bf16 or 96 KB of fp32
-// (with 20 of them 4,096 bf16 rows of 1,000 values: 15 against 196 us, of 32,003: 83 against 182,
-// 2,000 of 64,000: 73 against 106, 4,096 of 151,936: 272 against 236; 4,096 fp32 rows of 16,000: 62
-// against 110, 2,000 of 50,257: 97 against 72), but few long rows, which are cut into parts over all
-// SMs.  More warps a row until four CTAs fit an SM and 12 warps an SM have a row, two vectors a lane
-// at least, and a lane adds at most 512 pairs (1,000 rows of 8,000 values with 20 alternatives: 17, 14, 16, 20 us with 1, 2, 4, 8 warps;
-// 4,096 of 32,003: 102, 83, 89, 106).
+// streamed, 2,000 of 50,257: 51 against 44), with alternatives up to 160 KB of bf16 or 96 KB of fp32
+// (with 20 of them 4,096 bf16 rows of 1,000 values: 14 against 196 us, of 32,003: 73 against 182; of
+// 151,936: 272 against 200; 4,096 fp32 rows of 16,000: 60 against 110, 2,000 of 50,257: 97 against 70),
+// but few long rows, which are cut into parts over all SMs.  More warps a row until four CTAs fit an
+// SM and 12 warps an SM have a row, two vectors a lane at least, and a lane adds at most 512 pairs
+// (1,000 rows of 8,000 values with 20 alternatives: 17, 14, 16, 20 us with 1, 2, 4, 8 warps; 4,096 of
+// 32,003: 102, 83, 89, 106; all of these before the maxima went in front of the sums).
 int rows_warps(bool is_bf16, int64_t T, int V, int top, int sms) {
   const int64_t bytes = (int64_t)V * (is_bf16 ? 2 : 4);
   if (bytes > (top == 0 ? 80 : is_bf16 ? 160 : 96) * 1024 || (bytes > 64 * 1024 && T < sms)) return 0;
