@@ -337,6 +337,26 @@ def test_same_bits_on_streams_and_in_graphs(cuda):
     assert torch.equal(d, dref.flip(0))
 
 
+def test_calls_on_several_streams_at_once(cuda):
+    """Rows dealt out while the call runs, parts of a row with a second launch, and rows of a warp
+    each, under way together: the bits of each are what they are alone."""
+    sets = [rows(cuda, T, V, dt, seed=T)[:2] for T, V, dt in
+            [(900, 151936, BF), (9, 151936, F32), (2500, 5001, BF), (700, 60001, F32)]]
+    ref = [api.token_logp_fwd(z, y, top=7) for z, y in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    outs = [[] for _ in sets]
+    for _ in range(10):
+        for (z, y), st, o in zip(sets, streams, outs):
+            with torch.cuda.stream(st):
+                o.append(api.token_logp_fwd(z, y, top=7))
+    torch.cuda.synchronize()
+    assert B.ls_last_device_error(0) == B.LS_OK
+    for o, r in zip(outs, ref):
+        for each in o:
+            assert all(torch.equal(a, b) for a, b in zip(each, r))
+
+
 @pytest.mark.parametrize("T,V", [(15000, 151936), (62000, 40000)])
 def test_long_buffers(cuda, T, V):
     """Rows past 2^32 bytes and 2^31 values of the buffer."""
