@@ -101,7 +101,6 @@ class LayeredResponses:
                 raise ValueError("member_rows is at least 1, and capacity members * member_rows")
             capacity = members * member_rows
         self.member_rows = member_rows
-        self._whole = None  # drafts of every row
         self.prompt = prompt
         blocks = (max_tokens + page_size - 1) // page_size
         self.alloc = api.PageAllocator.empty(members, blocks, num_pages, page_size, device,
@@ -146,8 +145,8 @@ class LayeredResponses:
 
     def draft(self, parents: torch.Tensor, drafted: torch.Tensor | None = None, stream=None):
         """Room for every member's drafted tree (parents int32 [members][member_rows], drafted
-        int32 [members], see ls_draft_tree), its slots, and the positions that its depths give;
-        returns the rows that each row sees."""
+        int32 [members], see ls_draft_tree; without it all rows of every member in use), its slots,
+        and the positions that its depths give; returns the rows that each row sees."""
         if self.member_rows is None:
             raise ValueError("drafts need member_rows")
         if stream is not None:
@@ -156,12 +155,11 @@ class LayeredResponses:
         M, n = self.alloc.members, self.member_rows
         if tuple(parents.shape) != (M, n):
             raise ValueError(f"parents must be [{M} members][{n} member_rows]")
-        if drafted is None:
-            if self._whole is None:
-                self._whole = torch.full((M,), n, dtype=torch.int32, device=parents.device)
-            self.extend(self._whole)
-        else:
-            self.extend(drafted)
+        add = drafted
+        if add is None:  # of this call: a kept tensor's values could be a graph's, not yet replayed
+            add = torch.empty_like(self.alloc.lens)
+            torch.ge(self.alloc.lens, 0, out=add).mul_(n)
+        self.extend(add)
         axes = self.positions.shape[0]
         return api.draft_tree(parents, self.alloc.lens, self.prompt[0].num_tokens, drafted,
                               positions=self.positions.view(axes, M, n))[0]
