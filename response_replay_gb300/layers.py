@@ -85,8 +85,9 @@ class LayeredResponses:
 
     A step over drafted trees (member_rows) is ``draft`` in the place of ``extend``, ``append``
     and ``attend`` with what ``draft`` returned, and, when the policy has chosen behind every row,
-    ``settle``.  ``trim`` cuts responses or ends them and gives their pages back; with sharing,
-    ``fork`` branches them."""
+    ``settle``.  These go by the counts that ``draft`` really added (``drafted``): where it was
+    refused (no page left, say) the step does nothing to any response.  ``trim`` cuts responses or
+    ends them and gives their pages back; with sharing, ``fork`` branches them."""
 
     def __init__(self, prompt, num_kv_heads: int, members: int, max_tokens: int,
                  num_pages: int, page_size: int, device, capacity: int | None = None,
@@ -111,6 +112,8 @@ class LayeredResponses:
         self.pools = [api.PagePool(k, v) for k, v in zip(self.k_pools, self.v_pools)]
         self.all_pools = api.LayerPools(self.k_pools, self.v_pools)
         self.layers = [api.ResponseCache.of(pool, self.alloc) for pool in self.pools]
+        # a member's tokens of the last draft
+        self.drafted = torch.zeros(members, dtype=torch.int32, device=device)
         n = members if capacity is None else capacity
         self.slots = torch.empty(n, dtype=torch.int32, device=device)
         self.positions = torch.empty((axes, n), dtype=torch.int32, device=device)
@@ -133,20 +136,26 @@ class LayeredResponses:
     def attend(self, layer: int, q: torch.Tensor, softmax_scale: float, o=None, lse=None,
                stream=None, visible=None, drafted=None):
         """q [members][n][Hq][128]: the n newest tokens of every member, in a line or, with
-        visible (``draft``'s) and drafted, as trees; returns (o, lse)."""
+        visible (``draft``'s), as trees of as many tokens as ``draft`` added (its counts may be
+        given, and need not be); returns (o, lse)."""
         if visible is not None:
+            self._check_counts(drafted)
             return api.decode_attn_tree(self.prompt[layer], self.layers[layer], q, visible,
-                                        softmax_scale, drafted, o, lse, stream)
+                                        softmax_scale, self.drafted, o, lse, stream)
         if drafted is not None:
             raise ValueError("drafted without visible")
         return api.decode_attn(self.prompt[layer], self.layers[layer], q, softmax_scale, o, lse,
                                stream)
 
+    def _check_counts(self, drafted) -> None:
+        if drafted is not None:
+            api._dense(drafted, "drafted", torch.int32, (self.alloc.members,), self.alloc.device_index)
 
     def draft(self, parents: torch.Tensor, drafted: torch.Tensor | None = None, stream=None):
         """Room for every member's drafted tree (parents int32 [members][member_rows], drafted
         int32 [members], see ls_draft_tree; without it all rows of every member in use), its slots,
-        and the positions that its depths give; returns the rows that each row sees."""
+        and the positions that its depths give; returns the rows that each row sees.  Room for all
+        of them or, as ls_extend_pages, none: then no member drafts anything in this step."""
         if self.member_rows is None:
             raise ValueError("drafts need member_rows")
         if stream is not None:
@@ -155,26 +164,31 @@ class LayeredResponses:
         M, n = self.alloc.members, self.member_rows
         if tuple(parents.shape) != (M, n):
             raise ValueError(f"parents must be [{M} members][{n} member_rows]")
+        api._dense(parents, "parents", torch.int32, (M, n), self.alloc.device_index)
         add = drafted
         if add is None:  # of this call: a kept tensor's values could be a graph's, not yet replayed
             add = torch.empty_like(self.alloc.lens)
             torch.ge(self.alloc.lens, 0, out=add).mul_(n)
+        before = self.alloc.lens.clone()
         self.extend(add)
+        torch.sub(self.alloc.lens, before, out=self.drafted)
         axes = self.positions.shape[0]
-        return api.draft_tree(parents, self.alloc.lens, self.prompt[0].num_tokens, drafted,
+        return api.draft_tree(parents, self.alloc.lens, self.prompt[0].num_tokens, self.drafted,
                               positions=self.positions.view(axes, M, n))[0]
 
     def settle(self, parents: torch.Tensor, tokens: torch.Tensor, chosen: torch.Tensor,
                drafted: torch.Tensor | None = None, stream=None):
         """What the policy keeps of a draft: tokens int32 [members][member_rows] drafted, chosen
         the policy's token behind each row.  The kept rows' keys and values follow the context
-        in every layer, the others' room is given back.  Returns (rows, count, follow) as
+        in every layer, the others' room is given back.  The drafts are those that ``draft`` added
+        (its counts may be given, and need not be).  Returns (rows, count, follow) as
         accept_draft."""
         if stream is not None:
             with api._as_current(stream):
                 return self.settle(parents, tokens, chosen, drafted)
-        rows, count, follow, ends = api.accept_draft(parents, tokens, chosen, self.alloc.lens, drafted)
-        api.compact_rows(self.alloc, self.all_pools, rows, count, drafted)
+        self._check_counts(drafted)
+        rows, count, follow, ends = api.accept_draft(parents, tokens, chosen, self.alloc.lens, self.drafted)
+        api.compact_rows(self.alloc, self.all_pools, rows, count, self.drafted)
         api.trim_pages(self.alloc, ends)
         return rows, count, follow
 
