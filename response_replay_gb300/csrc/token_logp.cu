@@ -22,6 +22,7 @@
 // fp64.
 #include <math.h>
 
+#include "ls_chunks.h"
 #include "ls_device.cuh"
 #include "ls_internal.h"
 #include "ls_umma.cuh"
@@ -757,8 +758,7 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
         const int n = it.chunks();
         const uint8_t* src = reinterpret_cast<const uint8_t*>(it.at(it.in0));
         for (int k = 0; k < n; ++k) {
-          const int left = (it.in1 - it.in0 - k * kThreads) * kGroupBytes;
-          const uint32_t bytes = left < kChunkBytes ? left : kChunkBytes;
+          const uint32_t bytes = ls_chunk_bytes<kGroupBytes, kThreads>(it.in1 - it.in0, k);
           if (!wait(empty0 + 8 * rp.stage, rp.phase ^ 1u)) break;
           umma::mbar_expect_tx(full0 + 8 * rp.stage, bytes);
           bulk_load(ring0 + rp.stage * kChunkBytes, src + (int64_t)k * kChunkBytes, bytes,
