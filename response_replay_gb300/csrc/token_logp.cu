@@ -397,6 +397,10 @@ __device__ __forceinline__ int64_t taken_cta(uint32_t answer) {
       : "memory");
   return ok ? (int64_t)x : -1;
 }
+// The consumers' results of an item.  These two have no limit of their own: a consumer warp that
+// gives up hands over once more, for the item that it leaves, and the last warp looks for that
+// before each take-over.  (As an mbarrier, with the limit of the other waits, 199 against 194 us for
+// 4,096 rows of 151,936 bf16 values with 5 alternatives, 47 against 44 for 2,000 of 50,257.)
 __device__ __forceinline__ void hand_over(int par) {
   if (par)
     asm volatile("bar.arrive 3, %0;" ::"n"(kHand) : "memory");
@@ -790,8 +794,8 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
   umma::RingPos<kQueue> qp;
   int64_t item = 0;
   int32_t y = 0;
-  auto next = [&]() {  // the CTA's next item, by a warp
-    if (!wait(item_full0 + 8 * qp.stage, qp.phase)) return false;
+  auto next = [&]() {  // the CTA's next item, by a warp, whose lanes give up together
+    if (!__all_sync(0xffffffffu, wait(item_full0 + 8 * qp.stage, qp.phase))) return false;
     item = sm.item[qp.stage];
     y = sm.target[qp.stage];
     __syncwarp();
@@ -812,6 +816,7 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
       if (lane == 0 && a.parts == 1) has_y = target_logit<E>(a, it.row, &zy);
       const int par = q & 1;
       ++q;
+      if (__any_sync(0xffffffffu, *abort)) break;
       take_over(par);
       Stat st = {-INFINITY, 0.f, 0.f};
       if (lane < kWarps) st = Stat{sm.m[par][lane], sm.s[par][lane], sm.e[par][lane]};
@@ -904,6 +909,7 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
     }
     hand_over(par);
   }
+  if (__any_sync(0xffffffffu, *abort)) hand_over(q & 1);
 }
 
 // ---------------------------------------------------------------- forward, many rows
