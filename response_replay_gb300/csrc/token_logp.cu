@@ -145,16 +145,19 @@ __device__ __forceinline__ u64 merge32(u64 list, u64 batch, int lane) {
 }
 
 // A reference m (a logit, or a number between logits; none passes it by more than 2^8, or it is
-// moved), s = sum 2^t, e = sum 2^t t with t = z c - r, r = m c rounded: one multiply-add an exponent.  Where m c
-// is too large for that (a row of a type's lowest values), t = (z - m) c.
+// moved), s = sum 2^t, e = sum 2^t t with t = z c - r, r = m c rounded: one multiply-add an exponent.
+// r is off by half a step of its size, the same in every t: where that is more than 2 (masks of
+// -1e9, a temperature of 1e-6), sums would leave fp32's range, and t = (z - m) c.
 struct Stat {
   float m, s, e;
 };
-__device__ __forceinline__ bool plain_ref(float r) { return fabsf(r) < 1e30f; }
-// t of one maximum under another: what moves sums from the one to the other.
+__device__ __forceinline__ bool plain_ref(float r) { return fabsf(r) < 67108864.f; }  // 2^26
+// t of one maximum under another: what moves sums from the one to the other.  Plain references
+// stand for r, others for m c itself.
 __device__ __forceinline__ float shift(float from, float to, float c) {
   const float a = from * c, b = to * c;
-  return plain_ref(a) && plain_ref(b) ? a - b : (from - to) * c;
+  if (plain_ref(a)) return plain_ref(b) ? a - b : -fmaf(to, c, -a);
+  return plain_ref(b) ? fmaf(from, c, -b) : (from - to) * c;
 }
 __device__ __forceinline__ Stat move(Stat x, float m, float c) {
   if (x.m == -INFINITY || x.m == m) return x;  // no finite logit: nothing to move
@@ -168,9 +171,10 @@ __device__ __forceinline__ Stat merge(Stat a, Stat b, float c) {
   return {m, a.s + b.s, a.e + b.e};
 }
 // Of one logit.
-__device__ __forceinline__ Stat stat_of(float x) {
+__device__ __forceinline__ Stat stat_of(float x, float c) {
   const float one = x == -INFINITY ? 0.f : 1.f + (x - x);  // NaN of NaN and of +inf
-  return {x != x ? -INFINITY : x, one, one - one};
+  const float r = x * c, t = plain_ref(r) ? fmaf(x, c, -r) : 0.f, s = one * fast_exp2(t);
+  return {x != x ? -INFINITY : x, s, s * t};
 }
 // Over a warp's lanes, in every lane: the maximum first, so that each moves once.
 __device__ __forceinline__ Stat warp_stat(Stat x, float c) {
@@ -190,7 +194,7 @@ __device__ __forceinline__ Stat warp_stat(Stat x, float c) {
 template <typename E>
 struct Sums {
   static constexpr int H = Row<E>::N;
-  float m, nr, c;                          // nr = -m c
+  float m, nr, c;                          // nr = -m c, or (not plain) infinity
   float2 s, e;
   __device__ __forceinline__ explicit Sums(float c_)
       : m(-INFINITY), nr(INFINITY), c(c_), s(make_float2(0.f, 0.f)), e(make_float2(0.f, 0.f)) {}
@@ -198,7 +202,7 @@ struct Sums {
   // N vectors of 16 bytes.  The reference stays as it is as long as no logit passes it by far: of
   // 32 threads one would find a new maximum in most groups, and the warp would move its sums with
   // each.  Otherwise (the first group, sums of exponents about 8 and more, an exponent of -inf,
-  // NaN) the vectors are taken once more, carefully.  An exponent of the row's likeliest tokens
+  // NaN, a reference that is not plain) the vectors are taken once more, carefully.  An exponent of the row's likeliest tokens
   // is off by half a step of its size, which that limit keeps to 2^-22: entropies of 1 are within
   // 2e-7 (relative, root mean square); with a limit of 2^100 they were off by 3e-6.
   template <int N>
@@ -244,7 +248,7 @@ struct Sums {
       s = make_float2(x.s, 0.f);
       e = make_float2(x.e, 0.f);
       m = mx;
-      nr = -(m * c);
+      nr = plain_ref(m * c) ? -(m * c) : INFINITY;
     }
     const bool fine = plain_ref(nr);
 #pragma unroll
@@ -286,23 +290,25 @@ struct FwdArgs {
   uint32_t* err;
 };
 
-// The row's numbers from its statistics; returns lse.  The rounding of c moves log2 of the sum by
-// c_off times the mean exponent, which is r + e / s.
-__device__ __forceinline__ double finish_row(const FwdArgs& a, const Stat& x, int64_t row, bool has_y,
-                                             float zy) {
+// The row's numbers from its statistics.  What is a difference of logits is counted from the
+// reference, so that it is right whatever the logits' size: a log probability is
+// (z - m) / tau - rest.  The rounding of c moves log2 of the sum by c_off times the mean exponent.
+struct Norm {
+  double m, rest;
+  __device__ __forceinline__ float logp(float z, double inv_tau) const {
+    return (float)(((double)z - m) * inv_tau - rest);
+  }
+};
+__device__ __forceinline__ Norm finish_row(const FwdArgs& a, const Stat& x, int64_t row, bool has_y, float zy) {
   const float mean = x.e / x.s, r = x.m * a.c;
   const double log2s = (double)log2f(x.s);
-  double lse;
-  if (x.m == -INFINITY && x.s == 0.f)
-    lse = -INFINITY;
-  else if (plain_ref(r))
-    lse = kLn2d * ((double)r + log2s - a.c_off * ((double)r + (double)mean));
-  else
-    lse = (double)x.m * a.inv_tau + kLn2d * log2s;
-  if (a.out.lse) a.out.lse[row] = (float)lse;
+  const float off = plain_ref(r) ? -fmaf(x.m, a.c, -r) : 0.f;  // r's rounding, exact
+  const Norm n = {(double)x.m, kLn2d * (log2s + ((double)off - a.c_off * (double)mean))};
+  const bool none = x.m == -INFINITY && x.s == 0.f;
+  if (a.out.lse) a.out.lse[row] = none ? -INFINITY : (float)(n.m * a.inv_tau + n.rest);
   if (a.out.entropy) a.out.entropy[row] = (float)(kLn2d * (log2s - (double)mean));
-  if (a.out.logp) a.out.logp[row] = has_y ? (float)((double)zy * a.inv_tau - lse) : NAN;
-  return lse;
+  if (a.out.logp) a.out.logp[row] = has_y ? n.logp(zy, a.inv_tau) : NAN;
+  return n;
 }
 
 // Rows whose target is -1 are padding: their outputs are zeros and ids -1.
@@ -329,9 +335,12 @@ __device__ __forceinline__ bool target_logit(const FwdArgs& a, int64_t row, floa
   return true;
 }
 
-__device__ __forceinline__ void write_top(const FwdArgs& a, int64_t row, u64 key, double lse, int lane) {
+// (n: lane 0's counts)
+__device__ __forceinline__ void write_top(const FwdArgs& a, int64_t row, u64 key, Norm n, int lane) {
+  n.m = __shfl_sync(0xffffffffu, n.m, 0);
+  n.rest = __shfl_sync(0xffffffffu, n.rest, 0);
   if (lane >= a.top) return;
-  a.out.top_logp[row * a.top + lane] = key ? (float)((double)value_of(key) * a.inv_tau - lse) : NAN;
+  a.out.top_logp[row * a.top + lane] = key ? n.logp(value_of(key), a.inv_tau) : NAN;
   a.out.top_ids[row * a.top + lane] = key ? (int32_t)~(uint32_t)key : -1;
 }
 
@@ -832,9 +841,9 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
         if (lane == 0) *reinterpret_cast<float4*>(a.part_stat + 4 * at) = make_float4(st.m, st.s, st.e, 0.f);
         if (kTop) a.part_top[at * 32 + lane] = list;
       } else {
-        double lse = 0.0;
-        if (lane == 0) lse = finish_row(a, st, it.row, has_y, zy);
-        if (kTop) write_top(a, it.row, list, __shfl_sync(0xffffffffu, lse, 0), lane);
+        Norm norm{};
+        if (lane == 0) norm = finish_row(a, st, it.row, has_y, zy);
+        if (kTop) write_top(a, it.row, list, norm, lane);
       }
     }
     return;
@@ -889,7 +898,7 @@ __global__ void __launch_bounds__(kCtaThreads, 2) logp_fwd(const FwdArgs a) {
     // ---- the item's results
     Stat st = sums.stat();
     if (sticks) {
-      if (has_edge) st = merge(st, stat_of(edge), c);
+      if (has_edge) st = merge(st, stat_of(edge, c), c);
       if (kTop) {
         const uint32_t o = __reduce_max_sync(0xffffffffu, has_edge ? order_of(edge) : 0u);
         const float mx = o ? value_of((u64)o << 32) : NAN;
@@ -1065,7 +1074,7 @@ __global__ void __launch_bounds__(kRowsThreads, 4) logp_rows(const FwdArgs a, in
   if (kTop && has_edge && !in_head && edge == edge) largest(v.nvec + 1, edge);
   const uint32_t best = bestg < 0 ? 0u : order_of(bestv), second = secondg < 0 ? 0u : order_of(secondv);
   Stat st = sums.stat();
-  if (has_edge) st = merge(st, stat_of(edge), a.c);
+  if (has_edge) st = merge(st, stat_of(edge, a.c), a.c);
   st = warp_stat(st, a.c);
   if (W > 1 && lane == 0) sm.red[wl] = st;
 
@@ -1112,10 +1121,9 @@ __global__ void __launch_bounds__(kRowsThreads, 4) logp_rows(const FwdArgs a, in
   if (W > 1 || kTop) row_sync<W>(group);
   if (wl != 0) return;
   if (W > 1) st = warp_stat(lane < W ? sm.red[lane] : Stat{-INFINITY, 0.f, 0.f}, a.c);
-  double lse = 0.0;
-  if (lane == 0) lse = finish_row(a, st, row, has_y, zy);
+  Norm norm{};
+  if (lane == 0) norm = finish_row(a, st, row, has_y, zy);
   if (!kTop) return;
-  lse = __shfl_sync(0xffffffffu, lse, 0);
 
   // ---- the candidates' values, or (more of them than the list holds) all values
   const bool every = sm.cands > kRowsCand;
@@ -1153,7 +1161,7 @@ __global__ void __launch_bounds__(kRowsThreads, 4) logp_rows(const FwdArgs a, in
       __syncwarp();
     }
   }
-  write_top(a, row, order_found(sm.found, found, list, lane), lse, lane);
+  write_top(a, row, order_found(sm.found, found, list, lane), norm, lane);
 }
 
 // Rows that were cut into parts: a block a row, its warps take the parts by turns and their
@@ -1205,9 +1213,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) logp_merge(const FwdArgs a) 
   }
   if (warp != 0) return;
   st = warp_stat(lane < kMergeWarps ? red[lane] : Stat{-INFINITY, 0.f, 0.f}, a.c);
-  double lse = 0.0;
-  if (lane == 0) lse = finish_row(a, st, row, has_y, zy);
-  if (kTop) write_top(a, row, list, __shfl_sync(0xffffffffu, lse, 0), lane);
+  Norm norm{};
+  if (lane == 0) norm = finish_row(a, st, row, has_y, zy);
+  if (kTop) write_top(a, row, list, norm, lane);
 }
 
 // ---------------------------------------------------------------- backward
