@@ -717,9 +717,10 @@ ls_status ls_copy_pages(const ls_page_pool* pool, int layers, int64_t layer_stri
  * [T]: -1 marks a padding row, whose outputs are 0 and ids -1 and whose logits are not read;
  * another one outside [0, V) sets LS_ERR_DEVICE_CHECK and gives logp = NaN.  Outputs fp32 [T],
  * each or NULL: logp (needs targets), lse, entropy; targets NULL: no row is padding.  top_logp
- * fp32 and top_ids int32 [T][top] (4-byte aligned, as every array here).  A logit of -inf (or
- * the type's lowest value) has probability 0; a row with a NaN or +inf, or without a finite
- * logit, has NaN numbers, and its ids are of V or -1.
+ * fp32 and top_ids int32 [T][top] (4-byte aligned, as every array here).  A logit of -inf has
+ * probability 0, as has one of the type's lowest value beside ordinary ones (a row of such values
+ * alone is as probable as their distances say).  A row with a NaN or +inf, or without a finite
+ * logit, has NaN numbers, but for the lse of a row of -inf, which is -inf; its ids are of V or -1.
  *
  * Backward, with upstream d_logp [T], d_entropy [T] (each or NULL) and d_top [T][top] (top 0:
  * none) and G = d_logp + sum_j d_top_j:

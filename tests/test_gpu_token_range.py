@@ -1,5 +1,5 @@
 """GPU parity of the token statistics at the ends of their range: temperatures from 1e-6 to 1e6, rows
-whose logits are all masks."""
+whose logits are all masks, rows without a finite logit."""
 import math
 
 import numpy as np
@@ -109,3 +109,26 @@ def test_rows_of_masks(cuda, dt, T, V, top, level):
     # some rows of masks among others
     z[1:] = torch.randn(T - 1, V, device=cuda).to(dt)
     check(z, z.argmax(-1).to(torch.int32), 1.0, top)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T,V,top", [(300, 1003, 9), (200, 90001, 5), (200, 90001, 0), (3, 150011, 9)])
+def test_rows_without_a_finite_logit(cuda, dt, T, V, top):
+    """lse of a row of -inf is -inf, its other numbers are none; of one with NaN or +inf all are none.
+    Their gradients are none either."""
+    z = torch.randn(T, V, device=cuda).to(dt)
+    z[0, 77], z[1, 78], z[2] = math.nan, math.inf, -math.inf
+    y = torch.randint(0, V, (T,), device=cuda).to(torch.int32)
+    logp, lse, ent, tl, ti = api.token_logp_fwd(z, y, top=top)
+    assert B.ls_last_device_error(0) == B.LS_OK
+    assert bool(torch.isnan(lse[:2]).all()) and float(lse[2]) == -math.inf
+    assert bool(torch.isnan(logp[:3]).all()) and bool(torch.isnan(ent[:3]).all())
+    if top:
+        assert bool(torch.isnan(tl[:3]).all())
+        assert bool(((ti >= -1) & (ti < V)).all())
+    one = torch.ones(T, device=cuda)
+    for de in (None, one):
+        d = api.token_logp_bwd(z, y, lse, ent, one, de)
+        assert B.ls_last_device_error(0) == B.LS_OK
+        assert bool(torch.isnan(d[2]).all()) and bool(torch.isnan(d[:2]).all(-1).all())
+        assert bool(torch.isfinite(d[3:]).all())
