@@ -1368,6 +1368,7 @@ ls_status ls_token_logp_bwd(const void* logits, ls_dtype dtype, int64_t T, int V
   ls_status s = token_logp_args(logits, dtype, T, V, row_stride, top, temperature);
   if (s != LS_OK) return s;
   if (d_row_stride < V) return LS_ERR_INVALID_ARG;
+  if (temperature < 1e-3f) return LS_ERR_UNSUPPORTED;  // p of an fp32 lse of ordinary logits / tau
   if (T == 0) return LS_OK;
   const uintptr_t size = dtype == LS_BF16 ? 2 : 4;
   if (!dlogits || (reinterpret_cast<uintptr_t>(dlogits) & (size - 1))) return LS_ERR_INVALID_ARG;

@@ -20,6 +20,7 @@
 // a second kernel merges.  Short rows go to a warp or a few each (logp_rows).
 // Sums are in fp32: over 64 bytes, then over a thread's groups, then a tree; the last steps are in
 // fp64.
+#include <float.h>
 #include <math.h>
 
 #include "ls_chunks.h"
@@ -1242,10 +1243,10 @@ struct RowGrad {
   __device__ __forceinline__ float2 at(float2 z) const {
     // u = z / tau - lse, rounded once.  The rounding of 1 / tau shows in fp32 gradients only
     // (20 half steps of it at a logit of 20), which take its rest; with it an infinite logit
-    // has to be a finite one.
+    // has to be a finite one (the lowest: lse may be as low).
     if (sizeof(E) == 4) {
-      z.x = max_nan(z.x, -1e30f);
-      z.y = max_nan(z.y, -1e30f);
+      z.x = max_nan(z.x, -FLT_MAX);
+      z.y = max_nan(z.y, -FLT_MAX);
     }
     float2 u = __ffma2_rn(z, make_float2(hi, hi), make_float2(-lse, -lse));
     if (sizeof(E) == 4) u = __ffma2_rn(z, make_float2(lo, lo), u);

@@ -1169,7 +1169,8 @@ def token_logp_bwd(logits: torch.Tensor, targets: torch.Tensor | None, lse: torc
                    dlogits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The gradient that an objective of token_logp_fwd's outputs sends to the logits: d_logp,
     d_entropy fp32 [T] (each or None), d_top fp32 [T][top] with top_ids.  lse and entropy are
-    the forward's.  dlogits may be the logits themselves.  Returns dlogits."""
+    the forward's; temperatures from 1e-3 on.  dlogits may be the logits themselves.  Returns
+    dlogits."""
     if stream is not None:
         with _as_current(stream):
             return token_logp_bwd(logits, targets, lse, entropy, d_logp, d_entropy, temperature,

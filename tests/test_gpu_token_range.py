@@ -1,5 +1,5 @@
 """GPU parity of the token statistics at the ends of their range: temperatures from 1e-6 to 1e6, rows
-whose logits are all masks, rows without a finite logit."""
+whose logits are all masks, rows without a finite logit, and gradients there."""
 import math
 
 import numpy as np
@@ -132,3 +132,55 @@ def test_rows_without_a_finite_logit(cuda, dt, T, V, top):
         assert B.ls_last_device_error(0) == B.LS_OK
         assert bool(torch.isnan(d[2]).all()) and bool(torch.isnan(d[:2]).all(-1).all())
         assert bool(torch.isfinite(d[3:]).all())
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_gradients_of_rows_at_the_lowest_value(cuda, dt):
+    """lse, in fp32, is the logit itself there: the formula gives every token a probability of 1."""
+    T, V = 4, 5003
+    z = torch.full((T, V), torch.finfo(dt).min, dtype=dt, device=cuda)
+    y = torch.arange(T, dtype=torch.int32, device=cuda)
+    _, lse, _, _, _ = api.token_logp_fwd(z, y)
+    g = torch.tensor([1.0, -2.0, 0.5, 0.0], device=cuda)
+    d = api.token_logp_bwd(z, y, lse, None, g)
+    want = -g[:, None].expand(T, V).clone()
+    want[torch.arange(T), y.long()] += g
+    assert torch.equal(d.float(), want)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("temp", [1e-3, 2.0 ** -7, 100.0, 1e6])
+@pytest.mark.parametrize("level", [20.0, -30.0])
+def test_gradients_at_low_and_high_temperatures(cuda, dt, temp, level):
+    """Against the formula with lse in 64 bits: off by what the header says besides the roundings that
+    rollout_oracle counts."""
+    T, V = 40, 3001
+    z, y = near_ties(cuda, T, V, dt, level, 9, 4, 1)
+    g = torch.randn(T, device=cuda)
+    _, lse, _, _, _ = api.token_logp_fwd(z, y, temperature=temp)
+    d = api.token_logp_bwd(z, y, lse, None, g, temperature=temp)
+    assert B.ls_last_device_error(0) == B.LS_OK
+    tau = float(np.float32(temp))
+    lp, l64 = stats(z, tau)[:2]
+    p, gg = lp.exp(), g.double()[:, None]
+    want = -p * gg
+    want.scatter_add_(1, y.long()[:, None], gg)
+    # lse: the forward's own error (within 2^-20: a chain of V / 32 and less) and its rounding
+    rel = torch.expm1(ro.U32 * l64.abs() + 2.0 ** -19)[:, None]
+    # the exponent and, at the logits' size, 1 / tau's rounding
+    rel = rel + 2.0 ** -21 + ro.U32 * (44 + 4 * lp.abs() + 4 * z.double().abs() / tau)
+    err = (p * gg.abs() * rel).scatter_add_(1, y.long()[:, None], 40 * ro.U32 * gg.abs())
+    # exponentials below 2^-126 are zero: p is off by as much, the product by |g| of that
+    err = err + ro.TINY * gg.abs()
+    half = ro.U16 if dt is BF else ro.U32
+    off = (d.double() * tau - want).abs()
+    assert bool((off <= err + half * (want.abs() + err)).all()), float(off.max())
+
+
+@pytest.mark.parametrize("temp", [1e-6, 9e-4])
+def test_no_gradient_where_lse_says_nothing(cuda, temp):
+    z, y = near_ties(cuda, 3, 100, F32, 20.0, 9, 4, 0)
+    _, lse, _, _, _ = api.token_logp_fwd(z, y, temperature=temp)
+    with pytest.raises(B.LongstrawError) as e:
+        api.token_logp_bwd(z, y, lse, None, torch.ones(3, device=cuda), temperature=temp)
+    assert e.value.status == B.LS_ERR_UNSUPPORTED
