@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) compact_rows_kernel(
   __shared__ int64_t from[kMaxRows], to[kMaxRows];  // in 16 bytes, under KV head 0; -1: not moved
   const int tid = threadIdx.x, lane = tid & 31, warps = blockDim.x >> 5;
   const int m = blockIdx.x, layer = blockIdx.y;
-  const Member x = member_of(a, m, false);
+  const Member x = member_of(a, m, layer == 0 && tid == 0);
   const int n = __ldg(count + m);
   const int64_t room = (int64_t)max_blocks << p.ps_log2;
   bool bad = n < 0 || n > x.drafted || x.len > room;

@@ -47,17 +47,18 @@ __device__ __forceinline__ int32_t clamp_len(const LsDecodeArgs& a, int32_t len)
 __device__ __forceinline__ int32_t tiles_of(int32_t len) {
   return (int32_t)(((long long)len + kTile - 1) / kTile);
 }
-// Drafted tokens of a member, the last of its n.
+// Drafted tokens of a member, the last of its n: a count outside 0 .. min(n, its length) is cut (and
+// reported by the main kernel).
 __device__ __forceinline__ int32_t drafted_of(const LsDecodeArgs& a, int32_t m) {
-  return a.drafted ? min(max(__ldg(a.drafted + m), 0), a.n) : a.n;
+  const int32_t len = __ldg(a.lens + m), c = a.drafted ? __ldg(a.drafted + m) : a.n;
+  return max(min(c, min(a.n, len)), 0);
 }
 // Whether a member's length and draft are not what they may be.
 __device__ __forceinline__ bool bad_member(const LsDecodeArgs& a, int32_t m) {
   const int32_t len = __ldg(a.lens + m);
   if (len > clamp_len(a, len)) return true;
-  if (!a.drafted || len < 0) return false;
-  const int32_t c = __ldg(a.drafted + m);
-  return c < 0 || c > a.n || c > len;
+  const int32_t c = a.drafted ? __ldg(a.drafted + m) : a.n;
+  return len >= 0 && (c < 0 || c > a.n || c > len);
 }
 
 // What a row of a tree may see of the 64 keys from key kb on: the member's context (the keys

@@ -104,10 +104,6 @@ static_assert(kSmemBytes <= 232448, "shared memory");
 
 __device__ __forceinline__ uint32_t bar_addr(uint32_t base, int i) { return base + kOffBar + 8 * i; }
 
-__device__ __forceinline__ int32_t drafted_tokens(const LsDecodeArgs& a, int32_t m) {
-  const int32_t len = __ldg(a.lens + m), c = drafted_of(a, m);  // one latency
-  return len < 0 ? 0 : c;
-}
 __device__ __forceinline__ int32_t pairs_of(const LsDecodeArgs& a, int32_t tokens) {
   return (tokens * a.g + kPair - 1) / kPair;
 }
@@ -269,7 +265,7 @@ __device__ void make_plan(const LsDecodeArgs& a, Vars* v, uint16_t* tok, int32_t
     const int m = tid * per + i;
     if (m >= a.M) break;
     if (cta == 0 && bad_member(a, m)) ls_report(a.err, LS_DEVERR_CHECK);
-    const int32_t c = drafted_tokens(a, m);
+    const int32_t c = drafted_of(a, m);
     tokens += c;
     units += member_units(a, m, c);
   }
@@ -305,7 +301,7 @@ __device__ void make_plan(const LsDecodeArgs& a, Vars* v, uint16_t* tok, int32_t
     if (m >= a.M) break;
     tok[m] = (uint16_t)before;
     if (cta == 0) out->tok[m] = before;
-    before += drafted_tokens(a, m);
+    before += drafted_of(a, m);
   }
   if (tid == 0) tok[a.M] = (uint16_t)all_tokens;
   // ---- how many CTAs take the prompt, in how many rounds of how long strips
@@ -355,7 +351,7 @@ __device__ void make_plan(const LsDecodeArgs& a, Vars* v, uint16_t* tok, int32_t
     int32_t pre = us - units;
     if (pre <= r0 && r0 < us)
       for (int i = 0; i < per; ++i) {
-        const int32_t m = tid * per + i, x = member_units(a, m, drafted_tokens(a, m));
+        const int32_t m = tid * per + i, x = member_units(a, m, drafted_of(a, m));
         if (r0 < pre + x) {
           v->plan.m0 = m;
           v->plan.off0 = r0 - pre;
@@ -827,7 +823,7 @@ tree_combine(const __grid_constant__ LsDecodeArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t octets = (a.n * a.g + 7) >> 3, blocks = kWide ? (octets + 7) >> 3 : octets;
   const int32_t m = blockIdx.x / blocks, h = blockIdx.y, b = blockIdx.x - m * blocks;
-  const int32_t tokens = drafted_tokens(a, m);
+  const int32_t tokens = drafted_of(a, m);
   const int32_t chunk = (kWide ? 0 : warp * 4) + (lane >> 3);                    // the first; then every fourth
   const int32_t mrow = 8 * (kWide ? b * 8 + warp : b) + (lane & 7);  // among the drafted ones
   const bool resp = clamp_len(a, __ldg(a.lens + m)) > 0;
