@@ -26,6 +26,7 @@
  *                          and fused with the write into pages
  *   ls_extend_pages        pages and slots of a group's growing responses, packed or
  *                          (_by_member) in every member's own rows
+ *   ls_extend_drafts       the same for drafted tokens: also how many each member got
  *   ls_decode_attn         the rollout's decode step: every member's newest tokens over
  *                          the shared captured prompt and its own paged response
  *   ls_draft_tree, ls_decode_attn_tree, ls_accept_draft, ls_compact_rows
@@ -556,13 +557,24 @@ ls_status ls_extend_pages(int32_t* block_table, int members, int max_blocks, int
  * and member m's add[m] new tokens are the last of its rows; slot -1 and position 0 before
  * them.  So row r of member m is its (rows - r)-th newest token, as ls_decode_attn with
  * n = rows takes it.  An add above rows is refused like the others.  (Packed, a member that
- * adds nothing moves every later member's tokens up.) */
+ * adds nothing moves every later member's tokens up.)
+ *
+ * ls_extend_drafts: the same for a step of drafted tokens (ls_draft_tree below).  add may be NULL:
+ * all rows of every member in use.  added int32 [members], no other array: what member m got,
+ * add[m] or, from a refused call, 0; as the `drafted` of the step's other calls it makes a step
+ * without room one that changes nothing. */
 ls_status ls_extend_pages_by_member(int32_t* block_table, int members, int max_blocks,
                                     int page_size, int num_pages, const int32_t* lens,
                                     const int32_t* add, const int32_t* free_list, int num_free,
                                     const int32_t* used, int pos0, int axes, int rows,
                                     int32_t* slots, int32_t* positions, int32_t* lens_out,
                                     int32_t* used_out, ls_stream_t stream);
+ls_status ls_extend_drafts(int32_t* block_table, int members, int max_blocks, int page_size,
+                           int num_pages, const int32_t* lens, const int32_t* add,
+                           const int32_t* free_list, int num_free, const int32_t* used, int pos0,
+                           int axes, int rows, int32_t* slots, int32_t* positions,
+                           int32_t* lens_out, int32_t* used_out, int32_t* added,
+                           ls_stream_t stream);
 
 /* The responses of a group in their own pages: member m's key j lies in page
  * block_table[m][j / page_size] of `pool`; lens int32 [members] on the device, negative

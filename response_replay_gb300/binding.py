@@ -32,7 +32,8 @@ EXPORTED = (
     "ls_capture_latent", "ls_mla_replay_fwd_workspace", "ls_mla_replay_fwd",
     "ls_mla_replay_bwd_workspace", "ls_mla_replay_bwd",
     "ls_qk_norm_rope_fwd", "ls_qk_norm_rope_append", "ls_qk_norm_rope_bwd_workspace",
-    "ls_qk_norm_rope_bwd", "ls_extend_pages", "ls_extend_pages_by_member", "ls_decode_attn_workspace",
+    "ls_qk_norm_rope_bwd", "ls_extend_pages", "ls_extend_pages_by_member", "ls_extend_drafts",
+    "ls_decode_attn_workspace",
     "ls_decode_attn", "ls_decode_attn_tree_workspace", "ls_decode_attn_tree", "ls_draft_tree",
     "ls_accept_draft", "ls_compact_rows", "ls_copy_pages", "ls_trim_pages", "ls_fork_pages",
     "ls_token_logp_fwd_workspace", "ls_token_logp_fwd", "ls_token_logp_bwd",
@@ -163,6 +164,8 @@ def lib() -> C.CDLL:
                                 P],
             "ls_extend_pages_by_member": [P, i32, i32, i32, i32, P, P, P, i32, P, i32, i32, i32, P, P,
                                           P, P, P],
+            "ls_extend_drafts": [P, i32, i32, i32, i32, P, P, P, i32, P, i32, i32, i32, P, P, P, P, P,
+                                 P],
             "ls_decode_attn_workspace": [cache, rcache, i32, i32, szp],
             "ls_decode_attn": [cache, rcache, P, i32, i32, f32, P, P, P, sz, P],
             "ls_decode_attn_tree_workspace": [cache, rcache, i32, i32, szp],
@@ -450,6 +453,16 @@ def ls_extend_pages_by_member(block_table: int, members: int, max_blocks: int, p
         lib().ls_extend_pages_by_member(block_table, members, max_blocks, page_size, num_pages, lens,
                                         add, free_list, num_free, used, pos0, axes, rows, slots,
                                         positions, lens_out, used_out, stream))
+
+
+def ls_extend_drafts(block_table: int, members: int, max_blocks: int, page_size: int, num_pages: int,
+                     lens: int, add: int | None, free_list: int, num_free: int, used: int, pos0: int,
+                     axes: int, rows: int, slots: int, positions: int | None, lens_out: int,
+                     used_out: int, added: int, stream: int = 0) -> None:
+    _ok("ls_extend_drafts",
+        lib().ls_extend_drafts(block_table, members, max_blocks, page_size, num_pages, lens, add,
+                               free_list, num_free, used, pos0, axes, rows, slots, positions,
+                               lens_out, used_out, added, stream))
 
 
 def ls_decode_attn_workspace(cache: ls_kv_cache, resp: ls_resp_cache, n: int, Hq: int) -> int:

@@ -1151,12 +1151,13 @@ ls_status ls_qk_norm_rope_bwd(const ls_qkv_view* x, int64_t T, int Hq, int Hkv,
 
 namespace {
 
-// rows: 0, or the rows of every member, capacity then members * rows
+// rows: 0, or the rows of every member, capacity then members * rows; added: what each got, and add
+// may be NULL then
 ls_status extend_pages(int32_t* block_table, int members, int max_blocks, int page_size,
                        int num_pages, const int32_t* lens, const int32_t* add,
                        const int32_t* free_list, int num_free, const int32_t* used, int pos0,
                        int axes, int rows, int64_t capacity, int32_t* slots, int32_t* positions,
-                       int32_t* lens_out, int32_t* used_out, ls_stream_t stream) {
+                       int32_t* lens_out, int32_t* used_out, int32_t* added, ls_stream_t stream) {
   if (members < 0 || max_blocks < 0 || num_pages < 0 || num_free < 0 || pos0 < 0 || axes < 1 ||
       capacity < 0)
     return LS_ERR_INVALID_ARG;
@@ -1165,7 +1166,8 @@ ls_status extend_pages(int32_t* block_table, int members, int max_blocks, int pa
   if ((int64_t)members * max_blocks >= (1ll << 31) || (int64_t)num_pages * page_size >= (1ll << 31) ||
       (int64_t)max_blocks * page_size + pos0 >= (1ll << 31) || capacity >= (1ll << 31))
     return LS_ERR_UNSUPPORTED;
-  const void* ptrs[] = {used, used_out, lens, add, lens_out};
+  const void* ptrs[] = {used, used_out, lens, lens_out, added && !add ? lens : add};
+  if (!aligned4(added)) return LS_ERR_INVALID_ARG;
   for (int i = 0; i < 5; ++i)  // without members there are no counts
     if ((!ptrs[i] && (i < 2 || members > 0)) || !aligned4(ptrs[i])) return LS_ERR_INVALID_ARG;
   if ((members > 0 && max_blocks > 0 && (!block_table || !aligned4(block_table))) ||
@@ -1184,6 +1186,7 @@ ls_status extend_pages(int32_t* block_table, int members, int max_blocks, int pa
   a.used = used;
   a.lens_out = lens_out;
   a.used_out = used_out;
+  a.added = added;
   a.slots = slots;
   a.pos = positions;
   a.members = members;
@@ -1208,7 +1211,7 @@ ls_status ls_extend_pages(int32_t* block_table, int members, int max_blocks, int
                           int32_t* lens_out, int32_t* used_out, ls_stream_t stream) {
   return extend_pages(block_table, members, max_blocks, page_size, num_pages, lens, add, free_list,
                       num_free, used, pos0, axes, 0, capacity, slots, positions, lens_out, used_out,
-                      stream);
+                      nullptr, stream);
 }
 
 ls_status ls_extend_pages_by_member(int32_t* block_table, int members, int max_blocks, int page_size,
@@ -1220,7 +1223,20 @@ ls_status ls_extend_pages_by_member(int32_t* block_table, int members, int max_b
   const int64_t capacity = members > 0 ? (int64_t)members * rows : 0;
   return extend_pages(block_table, members, max_blocks, page_size, num_pages, lens, add, free_list,
                       num_free, used, pos0, axes, rows, capacity, slots, positions, lens_out,
-                      used_out, stream);
+                      used_out, nullptr, stream);
+}
+
+ls_status ls_extend_drafts(int32_t* block_table, int members, int max_blocks, int page_size,
+                           int num_pages, const int32_t* lens, const int32_t* add,
+                           const int32_t* free_list, int num_free, const int32_t* used, int pos0,
+                           int axes, int rows, int32_t* slots, int32_t* positions,
+                           int32_t* lens_out, int32_t* used_out, int32_t* added,
+                           ls_stream_t stream) {
+  if (rows < 1 || (members > 0 && !added)) return LS_ERR_INVALID_ARG;
+  const int64_t capacity = members > 0 ? (int64_t)members * rows : 0;
+  return extend_pages(block_table, members, max_blocks, page_size, num_pages, lens, add, free_list,
+                      num_free, used, pos0, axes, rows, capacity, slots, positions, lens_out,
+                      used_out, added, stream);
 }
 
 ls_status ls_decode_attn_workspace(const ls_kv_cache* cache, const ls_resp_cache* resp, int n,

@@ -248,11 +248,12 @@ cudaError_t ls_launch_norm_rope_bwd(const LsNormRopeArgs& a, const LsRows& x, co
 struct LsExtendArgs {
   int32_t* table;            // [members][max_blocks]
   const int32_t* lens;
-  const int32_t* add;
+  const int32_t* add;        // NULL: all rows of every member in use
   const int32_t* free_list;
   const int32_t* used;
   int32_t* lens_out;
   int32_t* used_out;
+  int32_t* added;            // [members] or NULL: what each got
   int32_t* slots;            // [capacity]
   int32_t* pos;              // [axes][capacity] or NULL
   int32_t members, max_blocks, num_free, num_pages, ps_log2, axes, pos0;

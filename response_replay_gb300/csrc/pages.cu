@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kThreads) extend_pages_kernel(const LsExtendAr
   const int used0 = __ldcg(a.used);
   if (tid < a.members) {
     len = __ldcg(a.lens + tid);
-    add = __ldg(a.add + tid);
+    add = !kRows || a.add ? __ldg(a.add + tid) : len < 0 ? 0 : a.rows;
     const long long room = (long long)a.max_blocks << a.ps_log2;
     // a member out of use (negative length) may not grow
     good = add >= 0 && (len >= 0 || add == 0) && (long long)(len < 0 ? 0 : len) + add <= room &&
@@ -200,7 +200,10 @@ __global__ void __launch_bounds__(kThreads) extend_pages_kernel(const LsExtendAr
     }
   }
   if (commit && blockIdx.x == 0) {
-    if (tid < a.members) a.lens_out[tid] = ok ? len + add : len;
+    if (tid < a.members) {
+      a.lens_out[tid] = ok ? len + add : len;
+      if (kRows && a.added) a.added[tid] = ok ? add : 0;
+    }
     if (tid == 0) *a.used_out = ok ? used0 + new_pages : used0;
   }
 }

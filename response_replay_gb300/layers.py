@@ -165,15 +165,9 @@ class LayeredResponses:
         if tuple(parents.shape) != (M, n):
             raise ValueError(f"parents must be [{M} members][{n} member_rows]")
         api._dense(parents, "parents", torch.int32, (M, n), self.alloc.device_index)
-        add = drafted
-        if add is None:  # of this call: a kept tensor's values could be a graph's, not yet replayed
-            add = torch.empty_like(self.alloc.lens)
-            torch.ge(self.alloc.lens, 0, out=add).mul_(n)
-        before = self.alloc.lens.clone()
-        self.extend(add)
-        torch.sub(self.alloc.lens, before, out=self.drafted)
-        axes = self.positions.shape[0]
-        return api.draft_tree(parents, self.alloc.lens, self.prompt[0].num_tokens, self.drafted,
+        pos0, axes = self.prompt[0].num_tokens, self.positions.shape[0]
+        api.extend_pages(self.alloc, drafted, pos0, self.slots, member_rows=n, added=self.drafted)
+        return api.draft_tree(parents, self.alloc.lens, pos0, self.drafted,
                               positions=self.positions.view(axes, M, n))[0]
 
     def settle(self, parents: torch.Tensor, tokens: torch.Tensor, chosen: torch.Tensor,

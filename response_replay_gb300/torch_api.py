@@ -815,10 +815,10 @@ class PageAllocator:
                    shared=torch.zeros(num_pages, **z) if sharing else None)
 
 
-def extend_pages(alloc: PageAllocator, add: torch.Tensor, pos0: int, slots: torch.Tensor,
+def extend_pages(alloc: PageAllocator, add: torch.Tensor | None, pos0: int, slots: torch.Tensor,
                  positions: torch.Tensor | None = None, lens_out: torch.Tensor | None = None,
                  used_out: torch.Tensor | None = None, stream=None,
-                 member_rows: int | None = None) -> None:
+                 member_rows: int | None = None, added: torch.Tensor | None = None) -> None:
     """Room for add[m] more tokens of every member: fills slots int32 [capacity] (-1 behind
     the last token) and positions int32 [axes][capacity] (pos0 + index within the
     response), enters new pages into the table and advances alloc.lens and alloc.used (or
@@ -826,11 +826,14 @@ def extend_pages(alloc: PageAllocator, add: torch.Tensor, pos0: int, slots: torc
 
     The tokens are packed, member after member; with member_rows given, capacity is members *
     member_rows and a member's tokens are the last of its own rows (-1 before them), the order
-    in which decode_attn takes queries [members][member_rows] while some members add none."""
+    in which decode_attn takes queries [members][member_rows] while some members add none.
+
+    With added int32 [members] (and member_rows; see ls_extend_drafts) it says what each member got,
+    0 of a refused call; add None then means all rows of every member in use."""
     if stream is not None:
         with _as_current(stream):
             return extend_pages(alloc, add, pos0, slots, positions, lens_out, used_out,
-                                member_rows=member_rows)
+                                member_rows=member_rows, added=added)
     if not -2 ** 31 <= pos0 < 2 ** 31:  # a C int would take its low bits
         raise ValueError(f"pos0 must be a position, got {pos0}")
     M, dev, i32 = alloc.members, alloc.device_index, torch.int32
@@ -838,6 +841,8 @@ def extend_pages(alloc: PageAllocator, add: torch.Tensor, pos0: int, slots: torc
     cap = slots.shape[0] if slots.dim() == 1 else -1
     if member_rows is not None and (member_rows < 1 or cap != M * member_rows):
         raise ValueError(f"slots must be [{M} members * member_rows], member_rows at least 1")
+    if added is None and add is None or added is not None and member_rows is None:
+        raise ValueError("counts that are left out need added, and added member_rows")
     sp = _dense(slots, "slots", i32, (cap,), dev)
     axes, pp = 1, None
     if positions is not None:
@@ -845,12 +850,14 @@ def extend_pages(alloc: PageAllocator, add: torch.Tensor, pos0: int, slots: torc
         pp = _dense(positions, "positions", i32, (axes, cap), dev)
     lens, used = alloc.lens.data_ptr(), alloc.used.data_ptr()
     call, room = ((B.ls_extend_pages, cap) if member_rows is None
-                  else (B.ls_extend_pages_by_member, member_rows))
+                  else (B.ls_extend_pages_by_member, member_rows) if added is None
+                  else (B.ls_extend_drafts, member_rows))
+    more = () if added is None else (_dense(added, "added", i32, (M,), dev),)
     call(alloc.block_table.data_ptr(), M, alloc.max_blocks, alloc.page_size,
-         alloc.num_pages, lens, _dense(add, "add", i32, (M,), dev),
+         alloc.num_pages, lens, None if add is None else _dense(add, "add", i32, (M,), dev),
          alloc.free_list.data_ptr(), alloc.num_free, used, pos0, axes, room, sp, pp,
          lens if lens_out is None else _dense(lens_out, "lens_out", i32, (M,), dev),
-         used if used_out is None else _dense(used_out, "used_out", i32, (1,), dev), st)
+         used if used_out is None else _dense(used_out, "used_out", i32, (1,), dev), *more, st)
 
 
 class ResponseCache:
