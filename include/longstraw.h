@@ -742,8 +742,8 @@ ls_status ls_copy_pages(const ls_page_pool* pool, int layers, int64_t layer_stri
  * rows.  It may be the logits themselves (same pointer and stride), otherwise the two may not
  * overlap.  lse and entropy (needed with d_entropy) are the forward's, top_ids any ids.  p_v is
  * that of the lse given: the rounding of lse to fp32 (2^-24 |lse| at most) is a relative error of
- * p_v.  Temperatures below 1e-3, at which it would be of p_v's size for ordinary logits:
- * LS_ERR_UNSUPPORTED.  A target or id outside [0, V) sets LS_ERR_DEVICE_CHECK and makes its row
+ * p_v.  That is 1/500 for a logit of 30 at a temperature of 1e-3 and all of p_v at 1e-6:
+ * temperatures below 1e-3 are LS_ERR_UNSUPPORTED.  A target or id outside [0, V) sets LS_ERR_DEVICE_CHECK and makes its row
  * NaN. */
 ls_status ls_token_logp_fwd_workspace(ls_dtype dtype, int64_t T, int V, int top, size_t* bytes);
 ls_status ls_token_logp_fwd(const void* logits, ls_dtype dtype, int64_t T, int V, int64_t row_stride,

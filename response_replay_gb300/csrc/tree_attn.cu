@@ -20,7 +20,8 @@
 // What bounds it.  256 rows meet a key tile of 64 KB for 4.2 MFLOP of each product: the tensor
 // core, 2,048 clocks a step of two row tiles and 128 keys.  A step takes about 3,150: from one row
 // tile's S to the other's lie the softmax's wake, its load of S and the issuer's wake.  8 members'
-// 16 tokens of 24 / 4 heads over 2,097,152: 2.0 to 2.1 ms, 1,560 to 1,640 TFLOP/s; 64 members of up
+// 16 tokens of 24 / 4 heads over 2,097,152: 2.0 to 2.1 ms, 1,560 to 1,640 TFLOP/s (2.2 to 2.3 when
+// repeated for seconds, at the power limit); 64 members of up
 // to 24 over 32,749, with responses of up to 8,192: 410 us.  (S and P over one another, an S buffer a
 // row tile: 2.31 ms.  Slots of 64 keys, two a row tile: 2.96 ms.)
 //
